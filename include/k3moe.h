@@ -624,6 +624,155 @@ int k3moe_shared_forward(float *out, const float *x, int32_t T, const k3moe_bf16
                          int32_t n_shared, int32_t d, int32_t f, int32_t accumulate, void *workspace,
                          size_t workspace_bytes, k3moe_stream s);
 
+/* ------------------------------ MXFP4 operands: quantisation and product */
+
+/*
+ * An operand of the MXFP4 product: a matrix of `rows` rows whose blocks of 32
+ * lie along its `in` columns, the axis that the product sums over.  (The
+ * pages quantise stored weights only; these calls serve a program that makes
+ * such weights, or trains with them.)
+ *   codes  [rows][ceil32(in) / 2] bytes, the packing of k3moe_mat.packed; the
+ *          codes past `in` are zero
+ *   atoms  the E8M0 bytes in the order tensor memory takes them in: 512-byte
+ *          atoms of 128 rows x 4 blocks, byte 16 (r mod 32) + 4 (r / 32 mod 4) +
+ *          (block mod 4) of atom (r / 128) * n + block / 4, with
+ *          n = 2 ceil(in / 256); bytes past the matrix are zero
+ * `rows` and `in` are any sizes >= 1.  The caller owns both buffers, of
+ * k3moe_mx_operand_codes_bytes and k3moe_mx_operand_atoms_bytes bytes (-1 if
+ * invalid), 16-byte aligned.  Byte 255 stands for NaN here: a block that held a
+ * non-finite value makes every product that reads it NaN.
+ */
+typedef struct {
+    uint8_t *codes;
+    uint8_t *atoms;
+    int32_t rows;
+    int32_t in;
+} k3moe_mx_operand;
+
+int64_t k3moe_mx_operand_codes_bytes(int32_t rows, int32_t in);
+int64_t k3moe_mx_operand_atoms_bytes(int32_t rows, int32_t in);
+
+/*
+ * Quantises x [rows][cols] by the conversion of k3moe_mx_quantize into
+ *  host_row  (optional) the operand rows x cols, blocks along the columns
+ *  host_col  (optional) the operand cols x rows: x transposed, blocks along the
+ *            rows of x
+ * from one read of x.  At least one of them.  Operands of a linear layer
+ * y = x w^T and its gradients: x and w along rows for y, dy along rows and w
+ * along columns for dx, dy and x along columns for dw.
+ *  x     x_dtype K3MOE_F32 or K3MOE_BF16, aligned to its element size
+ *  ld    elements from one row of x to the next, >= cols
+ * Errors: K3MOE_EINVAL for null pointers, sizes < 1, ld < cols, operands of
+ * another shape, misaligned buffers.
+ */
+int k3moe_mx_quantize_operand(const k3moe_mx_operand *host_row, const k3moe_mx_operand *host_col, const void *x,
+                              int x_dtype, int32_t rows, int32_t cols, int64_t ld, k3moe_stream s);
+
+/*
+ * Makes a stored matrix (an expert's gate, up or down plane pair) an operand:
+ * writes the atoms from its scale plane; the codes are the matrix's own packed
+ * plane, so host_op->codes must be host_W->packed.  host_op->rows = host_W->rows
+ * and ceil32(host_op->in) = host_W->in.  A scale byte 255 (a dropped group)
+ * becomes 0: the group then adds at most 6 * 2^-127 per unit of the other
+ * operand.
+ */
+int k3moe_mx_operand_from_matrix(const k3moe_mx_operand *host_op, const k3moe_mat *host_W, k3moe_stream s);
+
+/* The values an operand stands for: y [rows][in], y_dtype K3MOE_F32 or
+ * K3MOE_BF16 (exact in both), row stride ld >= in elements. */
+int k3moe_mx_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx_operand *host_op, k3moe_stream s);
+
+/*
+ * C [M][N] = A B^T for operands A (M rows) and B (N rows) with the same `in`,
+ * on the block-scaled tensor cores, fp32 accumulation, rounded once to c_dtype.
+ * Any M >= 1: a single token's projection is M = 1 with the weights as B.
+ *  C           c_dtype K3MOE_F32 or K3MOE_BF16, aligned to its element size, row
+ *              stride ldc >= N elements; must not overlap the operands
+ *  accumulate  != 0 adds into C (K3MOE_F32 only), e.g. for weight gradients
+ *              summed over micro-batches
+ * The result does not depend on timing: every sum has a fixed order.
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, `in` that differ, bad
+ * sizes or types.
+ */
+int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *host_A,
+                    const k3moe_mx_operand *host_B, int32_t accumulate, k3moe_stream s);
+
+/* ------------------------------- SwiGLU with an 8-bit activation checkpoint */
+
+/*
+ * h = silu(g) * u between an expert's products, keeping what the backward pass
+ * needs of g and u in 8 bits: e4m3 codes with one E8M0 scale per 32 values of a
+ * row, the smallest power of two s with max|v| / s <= 448 (byte 0 for a block of
+ * zeros; codes round to nearest, ties to even; magnitudes above 240 * 2^120 keep
+ * that value, so that a finite value reads back finite).  A block holding a
+ * non-finite value gets byte 255 and reads back as NaN, so an overflow shows in
+ * the gradients.  h is computed from g and u themselves; the gradients from the
+ * kept values:
+ *   du = dh * g sigma(g),   dg = dh * u * sigma(g) (1 + g (1 - sigma(g)))
+ *  g, u, h, dh, dg, du  [T][f], all of one type (K3MOE_F32 or K3MOE_BF16) in a
+ *              call, each with its own row stride >= f elements (gate and up may
+ *              be halves of one tensor), aligned to the element size; fp32
+ *              arithmetic, rounded once
+ *  ckpt        device, k3moe_swiglu_ckpt_bytes(T, f) bytes, 16-byte aligned
+ * In the backward call dg or du may be dh itself with the same stride.
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, T or f < 1, short
+ * strides, a ckpt_bytes that is too small.
+ */
+int64_t k3moe_swiglu_ckpt_bytes(int32_t T, int32_t f);
+int k3moe_swiglu_forward(void *h, int64_t ldh, void *ckpt, int64_t ckpt_bytes, const void *g, int64_t ldg,
+                         const void *u, int64_t ldu, int dtype, int32_t T, int32_t f, k3moe_stream s);
+int k3moe_swiglu_backward(void *dg, int64_t lddg, void *du, int64_t lddu, const void *dh, int64_t lddh,
+                          const void *ckpt, int64_t ckpt_bytes, int dtype, int32_t T, int32_t f, k3moe_stream s);
+
+/* --------------------------------------- balance loss of the router */
+
+/*
+ * Load-balancing loss of a router's choice and the gradient of its logits.
+ * With p_t the router's probabilities of token t (rule K3MOE_ROUTER_SOFTMAX:
+ * softmax(logits_t); the two sigmoid rules: sigma(logits_t) over its sum), N the
+ * number of valid tokens and c_e how many of their slots chose expert e,
+ *   loss = alpha sum_e f_e P_e,   f_e = E c_e / (top_k N),   P_e = (1/N) sum_t p_te
+ * (1 times alpha for a perfectly even choice).  The counts are constants to the
+ * gradient:
+ *   dlogits_t = dloss alpha / N * p_t (f - <f, p_t>)              softmax
+ *   the same times (1 - sigma(logits_t))                          sigmoid rules
+ * plus, given the gradient dw of the combine weights w, that of the layer's
+ * weight rule at the chosen experts (K3MOE_OPT_SIGMOID_ROUTER / _NORM):
+ *   softmax       w_j (dw_j - <w, dw>)
+ *   sigmoid       s_j (1 - s_j) dw_j,                 s = sigma(logit)
+ *   sigmoid norm  w_j (1 - s_j) (dw_j - <w, dw>)
+ * A token is valid if its mask byte is nonzero (or mask is NULL) and some logit
+ * is above -inf; the others get zero gradients and their logits are not used.
+ * A slot whose id is outside 0..E-1 (a dropped one, e.g. -1) is not counted and
+ * takes no part in <w, dw>.  No valid token: loss 0, N = 0.
+ *  logits   [T][E], dtype K3MOE_F32 or K3MOE_BF16, row stride ld >= E elements;
+ *           1 <= E <= 1024
+ *  ids      int32 [T][top_k], as k3moe_layer_route returns them; 1 <= top_k <= 32
+ *  mask     uint8 [T] or NULL
+ *  loss     fp32 [1], counts int32 [E], n_valid int32 [1] (out; the backward
+ *           call reads the last two)
+ *  dloss    fp32 [1]: the gradient of the loss, in device memory
+ *  w, dw    fp32 [T][top_k], both or neither NULL
+ *  dlogits  [T][E] of the logits' type, row stride ldd >= E; may be logits
+ *           itself with ldd = ld
+ *  workspace  device, k3moe_balance_workspace(E) bytes, 16-byte aligned,
+ *           zeroed once by the caller before its first use and left zero at the
+ *           places that count; not shared by calls that may overlap
+ * Sums are taken in an order that does not depend on timing.
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, bad sizes, types or rule.
+ */
+#define K3MOE_ROUTER_SOFTMAX      0
+#define K3MOE_ROUTER_SIGMOID      1
+#define K3MOE_ROUTER_SIGMOID_NORM 2
+size_t k3moe_balance_workspace(int32_t E);
+int k3moe_balance_forward(float *loss, int32_t *counts, int32_t *n_valid, const void *logits, int dtype, int64_t ld,
+                          const int32_t *ids, const uint8_t *mask, int32_t T, int32_t E, int32_t top_k, float alpha,
+                          int rule, void *workspace, size_t workspace_bytes, k3moe_stream s);
+int k3moe_balance_backward(void *dlogits, int64_t ldd, const void *logits, int dtype, int64_t ld, const int32_t *ids,
+                           const uint8_t *mask, const int32_t *counts, const int32_t *n_valid, const float *dloss,
+                           const float *w, const float *dw, int32_t T, int32_t E, int32_t top_k, float alpha, int rule,
+                           k3moe_stream s);
+
 /* ------------------------------------------------ dense trunk streaming */
 
 /*

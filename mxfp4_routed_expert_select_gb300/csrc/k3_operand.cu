@@ -1,0 +1,362 @@
+// k3_operand.cu -- MXFP4 product operands: quantisation along the rows and
+// along the columns of a matrix from one read, scale atoms of a stored
+// matrix, and the values an operand stands for.
+//
+// A block of 32 values along the reduction axis gets the E8M0 byte
+// e = clamp(floor(log2 max|x|) - 2 + 127, 0, 254) and each value the nearest
+// E2M1 magnitude of |x| 2^(127-e), ties to the even code, saturating at 6 (the
+// OCP Microscaling v1.0 conversion, as k3moe_mx_quantize).  The scaling is a
+// power of two, so the conversion instruction's rounding is the only one.
+//
+// Bound: HBM.  A 128 x 128 tile is read once, converted along its rows from
+// registers (four lanes hold a block; two shuffles find its maximum) and, for
+// the column form, along its columns from shared memory, where a lane walks
+// the 32 values of a block without bank conflicts.  Both forms' codes leave as
+// 64-byte runs and their scale bytes as whole 512-byte atoms.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "k3_launch.cuh"
+#include "k3_operand.cuh"
+
+namespace k3 {
+namespace {
+
+constexpr int QT = 128;        // tile rows and columns
+constexpr int Q_THREADS = 256;
+
+struct QuantArgs {
+    const void *x;
+    long ld;
+    int rows, cols, tiles_x;
+    bool vec;                      // every row 16-byte aligned
+    uint8_t *rcodes, *ratoms;      // row form, or null
+    uint8_t *ccodes, *catoms;      // column form, or null
+};
+
+// The E8M0 byte of a block whose largest magnitude has bits mb, and the
+// factor 2^(127-e) that its values are converted with (0 for byte 255: the
+// codes are 0).
+K3_DEV uint32_t block_byte(uint32_t mb, float &inv)
+{
+    const uint32_t e = (uint32_t)max((int)(mb >> 23) - 2, 0);
+    if (mb >= 0x7f800000u) {
+        inv = 0.f;
+        return 255u;
+    }
+    inv = __uint_as_float((254u - e) << 23);
+    return e;
+}
+// Eight scaled values to eight codes, value i in nibble i.
+K3_DEV uint32_t codes8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+K3_DEV uint32_t convert8(const float (&v)[8], float inv)
+{
+    float a[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) a[i] = inv == 0.f ? 0.f : v[i] * inv;  // a non-finite block: codes 0
+    return codes8(a);
+}
+
+// Sixteen bytes that this kernel reads once.  Not the read-only (nc) path: as
+// a programmatic dependent the kernel may have started before its input was
+// written.
+K3_DEV uint4 ld_once16(const void *p)
+{
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+// Eight values of a row from column c, zero past the matrix.
+template <typename XT>
+struct Chunk {
+    uint32_t w[2 * sizeof(XT)];
+};
+template <typename XT>
+K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
+{
+    Chunk<XT> o;
+    constexpr int NW = 2 * sizeof(XT);
+#pragma unroll
+    for (int i = 0; i < NW; i++) o.w[i] = 0u;
+    if (r >= a.rows || c >= a.cols) return o;
+    const XT *p = (const XT *)a.x + (long)r * a.ld + c;
+    if (a.vec && c + 8 <= a.cols) {
+#pragma unroll
+        for (int i = 0; i < NW / 4; i++) {
+            const uint4 q = ld_once16((const uint4 *)p + i);
+            o.w[4 * i] = q.x, o.w[4 * i + 1] = q.y, o.w[4 * i + 2] = q.z, o.w[4 * i + 3] = q.w;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (c + i < a.cols) {
+                if constexpr (sizeof(XT) == 2)
+                    o.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
+                else
+                    o.w[i] = p[i];
+            }
+    }
+    return o;
+}
+template <typename XT>
+K3_DEV void chunk_values(const Chunk<XT> &q, float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; i++) {
+        if constexpr (sizeof(XT) == 2)
+            v[i] = __uint_as_float((i & 1) ? (q.w[i >> 1] & 0xffff0000u) : (q.w[i >> 1] << 16));
+        else
+            v[i] = __uint_as_float(q.w[i]);
+    }
+}
+
+// Words per tile row in shared memory.  bf16: 64 words of two columns; fp32:
+// 128 words.  The column pass reads 32 consecutive words of one row per warp,
+// and the 16-byte stores of the first pass fall on distinct banks too.
+template <typename XT>
+constexpr int tile_pitch() { return sizeof(XT) == 2 ? 64 : 128; }
+constexpr int CODE_PITCH = 68;  // bytes of one column's staged codes (64, and 4 to spread the banks)
+template <typename XT>
+constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH; }
+
+// XT: uint16_t (bf16 bits) or uint32_t (fp32 bits).
+template <typename XT>
+__global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantArgs a)
+{
+    extern __shared__ __align__(16) uint32_t tile[];
+    __shared__ __align__(16) uint8_t ratom[512], catom[512];
+    constexpr int PITCH = tile_pitch<XT>();
+    constexpr int NIT = QT * (QT / 8) / Q_THREADS;       // chunks per thread
+    constexpr int NB = sizeof(XT) == 2 ? NIT : NIT / 2;  // of them in flight at a time
+    uint8_t *stage = (uint8_t *)(tile + QT * PITCH);
+    const int tid = threadIdx.x;
+    const int tx = blockIdx.x % a.tiles_x, ty = blockIdx.x / a.tiles_x;
+    const int r0 = ty * QT, c0 = tx * QT;
+    const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
+    griddep_launch_dependents();
+    griddep_wait();
+
+    const long rpitch = op_in_padded(a.cols) / 2;
+#pragma unroll
+    for (int it0 = 0; it0 < NIT; it0 += NB) {
+        Chunk<XT> q[NB];
+#pragma unroll
+        for (int j = 0; j < NB; j++) {
+            const int c = (it0 + j) * Q_THREADS + tid;
+            q[j] = load_chunk<XT>(a, r0 + (c >> 4), c0 + 8 * (c & 15));
+        }
+#pragma unroll
+        for (int j = 0; j < NB; j++) {
+            const int c = (it0 + j) * Q_THREADS + tid, r = c >> 4, cc = c & 15;
+            if (do_col) {
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(XT) / 2; i++)
+                    *(uint4 *)(tile + r * PITCH + cc * 2 * (int)sizeof(XT) + 4 * i) =
+                        make_uint4(q[j].w[4 * i], q[j].w[4 * i + 1], q[j].w[4 * i + 2], q[j].w[4 * i + 3]);
+            }
+            if (do_row) {
+                float v[8];
+                chunk_values<XT>(q[j], v);
+                uint32_t mb = 0u;
+#pragma unroll
+                for (int i = 0; i < 8; i++) mb = max(mb, __float_as_uint(v[i]) & 0x7fffffffu);
+                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+                float inv;
+                const uint32_t e = block_byte(mb, inv);
+                const uint32_t w = convert8(v, inv);
+                const bool in = r0 + r < a.rows && c0 + 8 * cc < op_in_padded(a.cols);
+                if (in) *(uint32_t *)(a.rcodes + (long)(r0 + r) * rpitch + c0 / 2 + 4 * cc) = w;
+                if ((cc & 3) == 0) ratom[op_atom_byte(r, cc >> 2)] = in ? (uint8_t)e : 0u;
+            }
+        }
+    }
+    if (!do_row && !do_col) return;
+    __syncthreads();
+    if (do_row && tid < 128)
+        ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
+    if (!do_col) return;
+
+    // columns: a task is one column's (fp32) or column pair's (bf16) 32 rows
+    const int rpad = op_in_padded(a.rows);
+    constexpr int COLS = sizeof(XT) == 2 ? 2 : 1;   // columns per task
+    constexpr int WPR = QT / COLS;                  // tasks per row block
+#pragma unroll
+    for (int t = tid; t < 4 * WPR; t += Q_THREADS) {
+        const int wc = t % WPR, rb = t / WPR;       // word column, row block
+        uint32_t raw[32];
+#pragma unroll
+        for (int i = 0; i < 32; i++) raw[i] = tile[(32 * rb + i) * PITCH + wc];
+#pragma unroll
+        for (int h = 0; h < COLS; h++) {
+            const int c = COLS * wc + h;
+            float v[32];
+            uint32_t mb = 0u;
+#pragma unroll
+            for (int i = 0; i < 32; i++) {
+                const uint32_t bits = sizeof(XT) == 4 ? raw[i] : h ? (raw[i] & 0xffff0000u) : (raw[i] << 16);
+                v[i] = __uint_as_float(bits);
+                mb = max(mb, bits & 0x7fffffffu);
+            }
+            float inv;
+            const uint32_t e = block_byte(mb, inv);
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                const float *vg = v + 8 * g;
+                const float v8[8] = {vg[0], vg[1], vg[2], vg[3], vg[4], vg[5], vg[6], vg[7]};
+                *(uint32_t *)(stage + c * CODE_PITCH + 16 * rb + 4 * g) = convert8(v8, inv);
+            }
+            catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
+        }
+    }
+    __syncthreads();
+    if (tid < 128)
+        ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid] = ((const uint32_t *)catom)[tid];
+    const long cpitch = rpad / 2;
+#pragma unroll
+    for (int it = 0; it < QT * 16 / Q_THREADS; it++) {
+        const int i = it * Q_THREADS + tid, c = i >> 4, w = i & 15;  // 16 words per column
+        if (c0 + c < a.cols && r0 + 8 * w < rpad)
+            *(uint32_t *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 4 * w) =
+                *(const uint32_t *)(stage + c * CODE_PITCH + 4 * w);
+    }
+}
+
+// Scale atoms of a stored matrix (scales [rows][nb], nb blocks per row): byte
+// 255 (a dropped group) becomes 0, so that the group adds at most 6 * 2^-127
+// of the other operand's block.  One CTA per atom.
+__global__ void __launch_bounds__(128) k3_mx_scale_atoms(const uint8_t *scales, int rows, int nb, int nk, uint8_t *atoms)
+{
+    griddep_wait();
+    const int r = (int)(blockIdx.x / nk) * 128 + threadIdx.x, b0 = 4 * (int)(blockIdx.x % nk);
+    uint32_t w = 0u;
+    if (r < rows)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            if (b0 + i < nb) {
+                const uint32_t e = scales[(long)r * nb + b0 + i];
+                w |= (e == 255u ? 0u : e) << (8 * i);
+            }
+    *(uint32_t *)(atoms + (long)blockIdx.x * 512 + op_atom_byte(threadIdx.x, 0)) = w;
+}
+
+// The values of an operand: eight per thread (one code word).
+template <typename YT>
+__global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, const uint8_t *atoms, int rows, int in,
+                                                        YT *y, long ld, bool vec)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int wpr = op_in_padded(in) / 8, nk = op_k_atoms(in);  // code words per row
+    const long n = (long)rows * wpr;
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
+        const int r = (int)(i / wpr), w = (int)(i % wpr), b = w >> 2;
+        const uint32_t q = *(const uint32_t *)(codes + 4 * i);
+        const float s = op_scale(atoms[((long)(r >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r, b)]);
+        uint32_t h[4];
+        e2m1x8_to_half2x4(q, h[0], h[1], h[2], h[3]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float2 f = h2f2(h[j]);
+            v[2 * j] = f.x * s;
+            v[2 * j + 1] = f.y * s;
+        }
+        YT *o = y + (long)r * ld + 8 * w;
+        if constexpr (sizeof(YT) == 2) {
+            uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                p[j] = *(const uint32_t *)&t;
+            }
+            if (vec && 8 * w + 8 <= in)
+                *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
+            else
+                for (int j = 0; j < 8; j++)
+                    if (8 * w + j < in) ((uint16_t *)o)[j] = (uint16_t)(p[j >> 1] >> (16 * (j & 1)));
+        } else {
+            if (vec && 8 * w + 8 <= in) {
+                ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else
+                for (int j = 0; j < 8; j++)
+                    if (8 * w + j < in) ((float *)o)[j] = v[j];
+        }
+    }
+}
+
+bool rows_aligned16(const void *p, long ld, int es) { return ((uintptr_t)p & 15u) == 0 && (ld * es) % 16 == 0; }
+
+}  // namespace
+
+// x [rows][cols] (row stride ld elements) to the row form (row: rows x cols)
+// and / or the column form (col: cols x rows).
+int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long ld, const k3moe_mx_operand *row,
+                               const k3moe_mx_operand *col, cudaStream_t s)
+{
+    QuantArgs a = {};
+    a.x = x;
+    a.ld = ld;
+    a.rows = rows;
+    a.cols = cols;
+    a.vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
+    if (row) a.rcodes = row->codes, a.ratoms = row->atoms;
+    if (col) a.ccodes = col->codes, a.catoms = col->atoms;
+    // the tiles cover every scale atom, the padding ones included
+    a.tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
+    const long tiles = (long)a.tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
+    if (tiles > 0x7fffffffL) return K3MOE_EINVAL;
+    cudaError_t e;
+    if (xdt == K3MOE_BF16) {
+        const size_t sm = col ? quant_smem<uint16_t>() : 0;
+        if (ensure_smem((const void *)k3_mx_quantize_operand<uint16_t>, sm) != K3MOE_OK) return K3MOE_ECUDA;
+        e = launch_pdl(k3_mx_quantize_operand<uint16_t>, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a);
+    } else {
+        const size_t sm = col ? quant_smem<uint32_t>() : 0;
+        if (ensure_smem((const void *)k3_mx_quantize_operand<uint32_t>, sm) != K3MOE_OK) return K3MOE_ECUDA;
+        e = launch_pdl(k3_mx_quantize_operand<uint32_t>, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a);
+    }
+    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+}
+
+int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atoms, cudaStream_t s)
+{
+    const long n = (long)op_row_tiles(rows) * op_k_atoms(in);
+    if (n > 0x7fffffffL) return K3MOE_EINVAL;
+    const cudaError_t e = launch_pdl(k3_mx_scale_atoms, dim3((unsigned)n), dim3(128), 0, s, scales, rows,
+                                     op_in_padded(in) / 32, op_k_atoms(in), atoms);
+    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+}
+
+int launch_mx_dequantize(const k3moe_mx_operand *op, void *y, int ydt, long ld, cudaStream_t s)
+{
+    const long n = (long)op->rows * (op_in_padded(op->in) / 8);
+    const unsigned grid = (unsigned)std::min<long>((n + 255) / 256, 16L * num_sms());
+    const bool vec = rows_aligned16(y, ld, ydt == K3MOE_BF16 ? 2 : 4);
+    const cudaError_t e =
+        ydt == K3MOE_BF16
+            ? launch_pdl(k3_mx_dequantize<uint16_t>, dim3(grid), dim3(256), 0, s, (const uint8_t *)op->codes,
+                         (const uint8_t *)op->atoms, op->rows, op->in, (uint16_t *)y, ld, vec)
+            : launch_pdl(k3_mx_dequantize<float>, dim3(grid), dim3(256), 0, s, (const uint8_t *)op->codes,
+                         (const uint8_t *)op->atoms, op->rows, op->in, (float *)y, ld, vec);
+    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+}
+
+}  // namespace k3

@@ -1,0 +1,24 @@
+// k3_operand.cuh -- layout of an MXFP4 product operand (k3moe_mx_operand).
+#pragma once
+#include "k3_device.cuh"
+
+namespace k3 {
+
+// Codes: [rows][ceil32(in) / 2] bytes.  Scale bytes: 512-byte atoms of 128
+// rows x 4 blocks (128 of the reduction), atom (row tile, k) at
+// (row tile) * n_k + k, with n_k even so that a 256-long step always has two;
+// byte 16 (r mod 32) + 4 (r / 32 mod 4) + (block mod 4) of its atom, the order
+// in which tcgen05.cp takes scales to tensor memory.
+__host__ __device__ inline int op_in_padded(int in) { return (in + 31) & ~31; }
+__host__ __device__ inline int op_row_tiles(int rows) { return (rows + 127) / 128; }
+__host__ __device__ inline int op_k_atoms(int in) { return 2 * ((in + 255) / 256); }
+K3_DEV int op_atom_byte(int r, int b) { return 16 * (r & 31) + 4 * ((r >> 5) & 3) + (b & 3); }
+
+// 2^(e-127) of a scale byte; NaN for byte 255 (a block that held a non-finite
+// value).
+K3_DEV float op_scale(uint32_t e)
+{
+    return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
+}
+
+}  // namespace k3

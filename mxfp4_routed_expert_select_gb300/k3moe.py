@@ -35,6 +35,9 @@ K3MOE_OPT_SIGMOID_ROUTER = 32
 K3MOE_OPT_SIGMOID_NORM = 64
 K3MOE_OPT_MXQ = 128
 K3MOE_NOALLOC_MAX_F = 2048
+K3MOE_ROUTER_SOFTMAX = 0
+K3MOE_ROUTER_SIGMOID = 1
+K3MOE_ROUTER_SIGMOID_NORM = 2
 
 
 class K3Error(RuntimeError):
@@ -90,6 +93,11 @@ class Bf16Expert(ctypes.Structure):
     _fields_ = [("gate", ctypes.c_void_p), ("up", ctypes.c_void_p), ("down", ctypes.c_void_p)]
 
 
+class MxOperandStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("atoms", ctypes.c_void_p),
+                ("rows", ctypes.c_int32), ("in_", ctypes.c_int32)]
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
                             ctypes.POINTER(ctypes.c_void_p))
 FREE_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
@@ -133,6 +141,19 @@ SIGNATURES = {
     "k3moe_shared_workspace": (_SZ, [_I, _I]),
     "k3moe_shared_forward": (ctypes.c_int, [_P, _P, _I, _P, _I, _I, _I, _I, _P, _SZ, _P]),
     "k3moe_mx_quantize": (ctypes.c_int, [_P, _P, _P, _I, _I, _I, _P]),
+    "k3moe_mx_operand_codes_bytes": (_I64, [_I, _I]),
+    "k3moe_mx_operand_atoms_bytes": (_I64, [_I, _I]),
+    "k3moe_mx_quantize_operand": (ctypes.c_int, [_P, _P, _P, _I, _I, _I, _I64, _P]),
+    "k3moe_mx_operand_from_matrix": (ctypes.c_int, [_P, _P, _P]),
+    "k3moe_mx_dequantize": (ctypes.c_int, [_P, _I, _I64, _P, _P]),
+    "k3moe_mx_matmul": (ctypes.c_int, [_P, _I, _I64, _P, _P, _I, _P]),
+    "k3moe_swiglu_ckpt_bytes": (_I64, [_I, _I]),
+    "k3moe_swiglu_forward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P]),
+    "k3moe_swiglu_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P]),
+    "k3moe_balance_workspace": (_SZ, [_I]),
+    "k3moe_balance_forward": (ctypes.c_int, [_P, _P, _P, _P, _I, _I64, _P, _P, _I, _I, _I, _F, _I, _P, _SZ, _P]),
+    "k3moe_balance_backward": (ctypes.c_int, [_P, _I64, _P, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F,
+                                              _I, _P]),
     "k3moe_rmsnorm": (ctypes.c_int, [_P, _P, _I, _F, _P]),
     "k3moe_residual_add": (ctypes.c_int, [_P, _P, _I, _P]),
     "k3moe_cache_create": (ctypes.c_int, [_P, _SZ, _SZ, _P, _I, _I]),
@@ -275,6 +296,150 @@ def mx_quantize(codes, scales, x, rows, cols, stream=None):
     dt = K3MOE_BF16 if x.dtype == torch.bfloat16 else K3MOE_F32
     check(lib().k3moe_mx_quantize(_ptr(codes), _ptr(scales), _ptr(x), dt, rows, cols, _stream(stream)),
           "k3moe_mx_quantize")
+
+
+def _dtype(*tensors):
+    """The K3MOE_* type that all the tensors share."""
+    import torch
+    dt = {torch.float32: K3MOE_F32, torch.bfloat16: K3MOE_BF16}.get(tensors[0].dtype)
+    if dt is None or any(t.dtype != tensors[0].dtype for t in tensors):
+        raise TypeError("fp32 or bf16 tensors of one type expected, got %s" % [t.dtype for t in tensors])
+    return dt
+
+
+def _ld(t, rows, cols):
+    """Row stride (elements) of a [rows][cols] tensor with unit column stride."""
+    if tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+        raise ValueError("expected [%d][%d] with unit column stride, got shape %s strides %s"
+                         % (rows, cols, tuple(t.shape), t.stride()))
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _flat(t, dtype, *shape):
+    """Raw pointer of a contiguous tensor of that type and shape (or None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("expected a contiguous %s tensor of shape %s, got %s %s" % (dtype, shape, t.dtype,
+                                                                                     tuple(t.shape)))
+    return t.data_ptr()
+
+
+class MxOperand:
+    """An operand of the MXFP4 product (k3moe_mx_operand): `rows` rows, blocks
+    of 32 along the `in_` columns.  Holds the device buffers `codes` and
+    `atoms`; filled by mx_quantize_operand or made of a stored matrix."""
+
+    def __init__(self, rows, in_, device="cuda", codes=None):
+        import torch
+        nc, na = lib().k3moe_mx_operand_codes_bytes(rows, in_), lib().k3moe_mx_operand_atoms_bytes(rows, in_)
+        if nc < 0 or na < 0:
+            raise K3Error(K3MOE_EINVAL, "MxOperand(%d, %d)" % (rows, in_))
+        self.rows, self.in_ = rows, in_
+        self.codes = torch.empty(nc, dtype=torch.uint8, device=device) if codes is None else codes
+        self.atoms = torch.empty(na, dtype=torch.uint8, device=self.codes.device)
+        self.struct = MxOperandStruct(self.codes.data_ptr(), self.atoms.data_ptr(), rows, in_)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def from_matrix(cls, packed, scales, rows, in_, stream=None):
+        """The operand of a stored matrix (packed [rows][ceil32(in_)/2], scales
+        [rows][ceil32(in_)/32], uint8): shares `packed`."""
+        import torch
+        pad = -(-in_ // 32) * 32
+        m = Mat(_flat(packed, torch.uint8, rows, pad // 2), _flat(scales, torch.uint8, rows, pad // 32), rows, pad)
+        op = cls(rows, in_, codes=packed)
+        check(lib().k3moe_mx_operand_from_matrix(op.ref, ctypes.byref(m), _stream(stream)),
+              "k3moe_mx_operand_from_matrix")
+        return op
+
+
+def mx_quantize_operand(x, row=None, col=None, stream=None):
+    """x [rows][cols] (fp32 or bf16) to MXFP4 along its columns' axis (row, an
+    MxOperand rows x cols) and / or along its rows' axis (col, cols x rows)."""
+    rows, cols = x.shape
+    check(lib().k3moe_mx_quantize_operand(row and row.ref, col and col.ref, x.data_ptr(), _dtype(x), rows, cols,
+                                          _ld(x, rows, cols), _stream(stream)), "k3moe_mx_quantize_operand")
+
+
+def mx_dequantize(y, op, stream=None):
+    """The values of an operand into y [op.rows][op.in_] (fp32 or bf16)."""
+    check(lib().k3moe_mx_dequantize(y.data_ptr(), _dtype(y), _ld(y, op.rows, op.in_), op.ref, _stream(stream)),
+          "k3moe_mx_dequantize")
+
+
+def mx_matmul(C, A, B, accumulate=False, stream=None):
+    """C [A.rows][B.rows] (fp32 or bf16) = A B^T of two MxOperands, or += (fp32)."""
+    check(lib().k3moe_mx_matmul(C.data_ptr(), _dtype(C), _ld(C, A.rows, B.rows), A.ref, B.ref, int(accumulate),
+                                _stream(stream)), "k3moe_mx_matmul")
+
+
+class SwigluCheckpoint:
+    """Device buffer for the 8-bit copies of a SwiGLU's gate and up [T][f]."""
+
+    def __init__(self, T, f, device="cuda"):
+        import torch
+        n = lib().k3moe_swiglu_ckpt_bytes(T, f)
+        if n < 0:
+            raise K3Error(K3MOE_EINVAL, "SwigluCheckpoint(%d, %d)" % (T, f))
+        self.T, self.f, self.nbytes = T, f, n
+        self.data = torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def swiglu_forward(h, ckpt, g, u, stream=None):
+    """h = silu(g) * u, keeping g and u in ckpt; [T][f] tensors of one type."""
+    T, f = ckpt.T, ckpt.f
+    check(lib().k3moe_swiglu_forward(h.data_ptr(), _ld(h, T, f), ckpt.data.data_ptr(), ckpt.nbytes, g.data_ptr(),
+                                     _ld(g, T, f), u.data_ptr(), _ld(u, T, f), _dtype(h, g, u), T, f,
+                                     _stream(stream)), "k3moe_swiglu_forward")
+
+
+def swiglu_backward(dg, du, dh, ckpt, stream=None):
+    """The gradients of gate and up from dh and the kept copies."""
+    T, f = ckpt.T, ckpt.f
+    check(lib().k3moe_swiglu_backward(dg.data_ptr(), _ld(dg, T, f), du.data_ptr(), _ld(du, T, f), dh.data_ptr(),
+                                      _ld(dh, T, f), ckpt.data.data_ptr(), ckpt.nbytes, _dtype(dg, du, dh), T, f,
+                                      _stream(stream)), "k3moe_swiglu_backward")
+
+
+class BalanceLoss:
+    """k3moe_balance_*: the router's balance loss, per-expert counts and the
+    gradient of the logits, for E experts, top_k slots, weight alpha and a rule
+    ("softmax", "sigmoid", "sigmoid_norm").  Owns the workspace, so one object
+    serves one stream at a time."""
+    RULES = {"softmax": K3MOE_ROUTER_SOFTMAX, "sigmoid": K3MOE_ROUTER_SIGMOID,
+             "sigmoid_norm": K3MOE_ROUTER_SIGMOID_NORM}
+
+    def __init__(self, E, top_k, alpha, rule="softmax", device="cuda"):
+        import torch
+        n = lib().k3moe_balance_workspace(E)
+        if n == 0:
+            raise K3Error(K3MOE_EINVAL, "BalanceLoss(E=%d)" % E)
+        self.E, self.k, self.alpha, self.rule = E, top_k, alpha, self.RULES[rule]
+        self.workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+
+    def forward(self, loss, counts, n_valid, logits, ids, mask=None, stream=None):
+        """loss fp32 [1], counts int32 [E], n_valid int32 [1] of logits [T][E],
+        ids int32 [T][top_k], mask uint8 [T]."""
+        import torch
+        T, E = logits.shape[0], self.E
+        check(lib().k3moe_balance_forward(
+            _flat(loss, torch.float32, 1), _flat(counts, torch.int32, E), _flat(n_valid, torch.int32, 1),
+            logits.data_ptr(), _dtype(logits), _ld(logits, T, E), _flat(ids, torch.int32, T, self.k),
+            _flat(mask, torch.uint8, T), T, E, self.k, self.alpha, self.rule, self.workspace.data_ptr(),
+            self.workspace.numel(), _stream(stream)), "k3moe_balance_forward")
+
+    def backward(self, dlogits, logits, ids, counts, n_valid, dloss, mask=None, w=None, dw=None, stream=None):
+        """dlogits [T][E] from dloss fp32 [1] and, with the combine weights w and
+        their gradients dw (fp32 [T][top_k]), the weight rule's part."""
+        import torch
+        T, E = logits.shape[0], self.E
+        check(lib().k3moe_balance_backward(
+            dlogits.data_ptr(), _ld(dlogits, T, E), logits.data_ptr(), _dtype(logits, dlogits), _ld(logits, T, E),
+            _flat(ids, torch.int32, T, self.k), _flat(mask, torch.uint8, T), _flat(counts, torch.int32, E),
+            _flat(n_valid, torch.int32, 1), _flat(dloss, torch.float32, 1), _flat(w, torch.float32, T, self.k),
+            _flat(dw, torch.float32, T, self.k), T, E, self.k, self.alpha, self.rule, _stream(stream)),
+            "k3moe_balance_backward")
 
 
 def expert_gemv_noalloc(y, x, expert, d, f, stream=None):
