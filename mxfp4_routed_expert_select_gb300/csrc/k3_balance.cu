@@ -210,9 +210,9 @@ __global__ void __launch_bounds__(BL_THREADS) k3_balance_backward(const BalanceA
     const int n = *a.n_valid;
     const long kn = (long)a.k * n;
     for (int e = threadIdx.x; e < 32 * NC; e += BL_THREADS)
-        f1[e] = e < a.E && n > 0 ? (float)((double)((long)a.E * a.counts[e] - kn) / (double)kn) : 0.f;
+        f1[e] = e < a.E && n > 0 ? (float)((long)a.E * a.counts[e] - kn) / (float)kn : 0.f;
     __syncthreads();
-    const float scale = n > 0 ? (float)((double)a.alpha * *a.dloss / n) : 0.f;
+    const float scale = n > 0 ? a.alpha * *a.dloss / (float)n : 0.f;
 
     for (int t = blockIdx.x * BL_WARPS + warp; t < a.T; t += gridDim.x * BL_WARPS) {
         float v[NC], m = 0.f, inv = 0.f;

@@ -42,6 +42,7 @@ namespace {
 
 constexpr int MG_M = 128;       // B rows per tile
 constexpr int MG_THREADS = 256;
+constexpr int MG_MAX_RANKS = 8;  // CTAs that share a tile
 constexpr int MG_W_PROD = 0, MG_W_MMA = 1, MG_W_EPI = 4;
 
 struct MgArgs {
@@ -370,11 +371,25 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         const int u = first, n = (u / a.tiles_m) * MG_M + (int)(threadIdx.x & 127), m0 = (u % a.tiles_m) * NT;
         const int c0 = NT * rank / ranks, c1 = min(NT * (rank + 1) / ranks, a.M - m0);
         if (n < a.N && !*abort_flag)
-            for (int c = c0 + (int)(threadIdx.x >> 7); c < c1; c += MG_THREADS / 128) {
-                const uint32_t at = sbase + (uint32_t)(c * MG_M + (int)(threadIdx.x & 127)) * 4;
-                float v = 0.f;
-                for (int r = 0; r < ranks; r++) v += ld_peer(at, (uint32_t)r);
-                put((CT *)a.C, (long)(m0 + c) * a.ldc + n, v, a.accumulate);
+            // four columns' partial sums of all ranks in flight at a time (a
+            // remote load takes a few hundred cycles)
+            for (int c = c0 + (int)(threadIdx.x >> 7); c < c1; c += 4 * (MG_THREADS / 128)) {
+                float v[4][MG_MAX_RANKS];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int cj = min(c + j * (MG_THREADS / 128), c1 - 1);
+                    const uint32_t at = sbase + (uint32_t)(cj * MG_M + (int)(threadIdx.x & 127)) * 4;
+#pragma unroll
+                    for (int r = 0; r < MG_MAX_RANKS; r++) v[j][r] = r < ranks ? ld_peer(at, (uint32_t)r) : 0.f;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int cj = c + j * (MG_THREADS / 128);
+                    float t = v[j][0];
+#pragma unroll
+                    for (int r = 1; r < MG_MAX_RANKS; r++) t += v[j][r];
+                    if (cj < c1) put((CT *)a.C, (long)(m0 + cj) * a.ldc + n, t, a.accumulate);
+                }
             }
         cluster_sync();  // no CTA leaves while another reads its sums
     } else {
@@ -472,7 +487,7 @@ void choose_tiles(int M, int N, int nks, int sms, int &nt, int &ranks)
     }
     const long tiles = tn * ((M + nt - 1) / nt);
     ranks = 1;
-    while (ranks < 8 && tiles * ranks * 2 <= 2L * sms && nks >= 4 * ranks) ranks *= 2;
+    while (ranks < MG_MAX_RANKS && tiles * ranks * 2 <= 2L * sms && nks >= 4 * ranks) ranks *= 2;
 }
 
 template <typename CT>

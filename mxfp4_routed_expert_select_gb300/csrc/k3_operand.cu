@@ -30,23 +30,17 @@ struct QuantArgs {
     const void *x;
     long ld;
     int rows, cols, tiles_x;
-    bool vec;                      // every row 16-byte aligned
     uint8_t *rcodes, *ratoms;      // row form, or null
     uint8_t *ccodes, *catoms;      // column form, or null
 };
 
 // The E8M0 byte of a block whose largest magnitude has bits mb, and the
-// factor 2^(127-e) that its values are converted with (0 for byte 255: the
-// codes are 0).
+// factor 2^(127-e) that its values are converted with.
 K3_DEV uint32_t block_byte(uint32_t mb, float &inv)
 {
     const uint32_t e = (uint32_t)max((int)(mb >> 23) - 2, 0);
-    if (mb >= 0x7f800000u) {
-        inv = 0.f;
-        return 255u;
-    }
     inv = __uint_as_float((254u - e) << 23);
-    return e;
+    return mb >= 0x7f800000u ? 255u : e;
 }
 // Eight scaled values to eight codes, value i in nibble i.
 K3_DEV uint32_t codes8(const float (&v)[8])
@@ -62,12 +56,12 @@ K3_DEV uint32_t codes8(const float (&v)[8])
         : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
-K3_DEV uint32_t convert8(const float (&v)[8], float inv)
+K3_DEV uint32_t convert8(const float (&v)[8], float inv, uint32_t e)
 {
     float a[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) a[i] = inv == 0.f ? 0.f : v[i] * inv;  // a non-finite block: codes 0
-    return codes8(a);
+    for (int i = 0; i < 8; i++) a[i] = v[i] * inv;
+    return e == 255u ? 0u : codes8(a);  // a non-finite block: codes 0
 }
 
 // Sixteen bytes that this kernel reads once.  Not the read-only (nc) path: as
@@ -82,11 +76,12 @@ K3_DEV uint4 ld_once16(const void *p)
     return v;
 }
 
-// Eight values of a row from column c, zero past the matrix.
+// Eight values of a row.
 template <typename XT>
-struct Chunk {
+struct alignas(16) Chunk {
     uint32_t w[2 * sizeof(XT)];
 };
+// From global memory at column c (rows 16-byte aligned), zero past the matrix.
 template <typename XT>
 K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
 {
@@ -96,7 +91,7 @@ K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
     for (int i = 0; i < NW; i++) o.w[i] = 0u;
     if (r >= a.rows || c >= a.cols) return o;
     const XT *p = (const XT *)a.x + (long)r * a.ld + c;
-    if (a.vec && c + 8 <= a.cols) {
+    if (c + 8 <= a.cols) {
 #pragma unroll
         for (int i = 0; i < NW / 4; i++) {
             const uint4 q = ld_once16((const uint4 *)p + i);
@@ -113,6 +108,23 @@ K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
             }
     }
     return o;
+}
+// Bits of the largest magnitude of eight values.  Non-negative floats order
+// like their bits, a NaN above infinity; bf16 values two at a time.
+template <typename XT>
+K3_DEV uint32_t chunk_max(const Chunk<XT> &q)
+{
+    if constexpr (sizeof(XT) == 2) {
+        uint32_t m = q.w[0] & 0x7fff7fffu;
+#pragma unroll
+        for (int i = 1; i < 4; i++) m = __vmaxu2(m, q.w[i] & 0x7fff7fffu);
+        return max(m & 0xffff0000u, m << 16);
+    } else {
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = max(m, q.w[i] & 0x7fffffffu);
+        return m;
+    }
 }
 template <typename XT>
 K3_DEV void chunk_values(const Chunk<XT> &q, float (&v)[8])
@@ -135,8 +147,10 @@ constexpr int CODE_PITCH = 68;  // bytes of one column's staged codes (64, and 4
 template <typename XT>
 constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH; }
 
-// XT: uint16_t (bf16 bits) or uint32_t (fp32 bits).
-template <typename XT>
+// XT: uint16_t (bf16 bits) or uint32_t (fp32 bits).  VEC: rows are 16-byte
+// aligned; else the tile comes in by single elements, neighbouring lanes on
+// neighbouring columns, through shared memory.
+template <typename XT, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantArgs a)
 {
     extern __shared__ __align__(16) uint32_t tile[];
@@ -152,6 +166,15 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
     griddep_launch_dependents();
     griddep_wait();
 
+    if constexpr (!VEC) {
+        const int c = tid & 127, rows = min(QT, a.rows - r0);
+        const XT *p = (const XT *)a.x + (long)r0 * a.ld + c0 + c;
+        const bool in = c0 + c < a.cols;
+#pragma unroll 16
+        for (int r = tid >> 7; r < QT; r += Q_THREADS / QT)
+            ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
+        __syncthreads();
+    }
     const long rpitch = op_in_padded(a.cols) / 2;
 #pragma unroll
     for (int it0 = 0; it0 < NIT; it0 += NB) {
@@ -159,12 +182,15 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
 #pragma unroll
         for (int j = 0; j < NB; j++) {
             const int c = (it0 + j) * Q_THREADS + tid;
-            q[j] = load_chunk<XT>(a, r0 + (c >> 4), c0 + 8 * (c & 15));
+            if constexpr (VEC)
+                q[j] = load_chunk<XT>(a, r0 + (c >> 4), c0 + 8 * (c & 15));
+            else if (do_row)
+                q[j] = *(const Chunk<XT> *)(tile + (c >> 4) * PITCH + (c & 15) * 2 * (int)sizeof(XT));
         }
 #pragma unroll
         for (int j = 0; j < NB; j++) {
             const int c = (it0 + j) * Q_THREADS + tid, r = c >> 4, cc = c & 15;
-            if (do_col) {
+            if (VEC && do_col) {
 #pragma unroll
                 for (int i = 0; i < (int)sizeof(XT) / 2; i++)
                     *(uint4 *)(tile + r * PITCH + cc * 2 * (int)sizeof(XT) + 4 * i) =
@@ -173,14 +199,12 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
             if (do_row) {
                 float v[8];
                 chunk_values<XT>(q[j], v);
-                uint32_t mb = 0u;
-#pragma unroll
-                for (int i = 0; i < 8; i++) mb = max(mb, __float_as_uint(v[i]) & 0x7fffffffu);
+                uint32_t mb = chunk_max<XT>(q[j]);
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
                 float inv;
                 const uint32_t e = block_byte(mb, inv);
-                const uint32_t w = convert8(v, inv);
+                const uint32_t w = convert8(v, inv, e);
                 const bool in = r0 + r < a.rows && c0 + 8 * cc < op_in_padded(a.cols);
                 if (in) *(uint32_t *)(a.rcodes + (long)(r0 + r) * rpitch + c0 / 2 + 4 * cc) = w;
                 if ((cc & 3) == 0) ratom[op_atom_byte(r, cc >> 2)] = in ? (uint8_t)e : 0u;
@@ -200,27 +224,30 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
 #pragma unroll
     for (int t = tid; t < 4 * WPR; t += Q_THREADS) {
         const int wc = t % WPR, rb = t / WPR;       // word column, row block
-        uint32_t raw[32];
+        uint32_t raw[32], top = 0u;
 #pragma unroll
-        for (int i = 0; i < 32; i++) raw[i] = tile[(32 * rb + i) * PITCH + wc];
+        for (int i = 0; i < 32; i++) {
+            raw[i] = tile[(32 * rb + i) * PITCH + wc];
+            if constexpr (sizeof(XT) == 2)
+                top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
+            else
+                top = max(top, raw[i] & 0x7fffffffu);
+        }
 #pragma unroll
         for (int h = 0; h < COLS; h++) {
             const int c = COLS * wc + h;
             float v[32];
-            uint32_t mb = 0u;
 #pragma unroll
-            for (int i = 0; i < 32; i++) {
-                const uint32_t bits = sizeof(XT) == 4 ? raw[i] : h ? (raw[i] & 0xffff0000u) : (raw[i] << 16);
-                v[i] = __uint_as_float(bits);
-                mb = max(mb, bits & 0x7fffffffu);
-            }
+            for (int i = 0; i < 32; i++)
+                v[i] = __uint_as_float(sizeof(XT) == 4 ? raw[i] : h ? (raw[i] & 0xffff0000u) : (raw[i] << 16));
+            const uint32_t mb = sizeof(XT) == 4 ? top : h ? (top & 0xffff0000u) : (top << 16);
             float inv;
             const uint32_t e = block_byte(mb, inv);
 #pragma unroll
             for (int g = 0; g < 4; g++) {
                 const float *vg = v + 8 * g;
                 const float v8[8] = {vg[0], vg[1], vg[2], vg[3], vg[4], vg[5], vg[6], vg[7]};
-                *(uint32_t *)(stage + c * CODE_PITCH + 16 * rb + 4 * g) = convert8(v8, inv);
+                *(uint32_t *)(stage + c * CODE_PITCH + 16 * rb + 4 * g) = convert8(v8, inv, e);
             }
             catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
         }
@@ -256,48 +283,64 @@ __global__ void __launch_bounds__(128) k3_mx_scale_atoms(const uint8_t *scales, 
     *(uint32_t *)(atoms + (long)blockIdx.x * 512 + op_atom_byte(threadIdx.x, 0)) = w;
 }
 
-// The values of an operand: eight per thread (one code word).
-template <typename YT>
-__global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, const uint8_t *atoms, int rows, int in,
-                                                        YT *y, long ld, bool vec)
+// The values of an operand: eight per thread (one code word) where the rows of
+// y are 16-byte aligned, else two per thread, so that a warp's stores stay next
+// to each other.
+template <typename YT, bool VEC>
+__global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, const uint8_t *atoms, int r0,
+                                                        uint32_t n, FastDiv upr, int nk, int in, YT *y, long ld)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const int wpr = op_in_padded(in) / 8, nk = op_k_atoms(in);  // code words per row
-    const long n = (long)rows * wpr;
-    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long)gridDim.x * 256) {
-        const int r = (int)(i / wpr), w = (int)(i % wpr), b = w >> 2;
-        const uint32_t q = *(const uint32_t *)(codes + 4 * i);
-        const float s = op_scale(atoms[((long)(r >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r, b)]);
-        uint32_t h[4];
-        e2m1x8_to_half2x4(q, h[0], h[1], h[2], h[3]);
-        float v[8];
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const float2 f = h2f2(h[j]);
-            v[2 * j] = f.x * s;
-            v[2 * j + 1] = f.y * s;
-        }
-        YT *o = y + (long)r * ld + 8 * w;
-        if constexpr (sizeof(YT) == 2) {
-            uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
+    constexpr int UB = VEC ? 4 : 1;  // code bytes of a unit
+    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
+        const uint32_t q = upr.div(i);
+        const int r = r0 + (int)q, c = (int)(i - q * upr.d) * 2 * UB, b = c >> 5;
+        const float s = op_scale(atoms[((size_t)(r >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r, b)]);
+        YT *o = y + (long)r * ld + c;
+        if constexpr (VEC) {
+            uint32_t h[4];
+            e2m1x8_to_half2x4(*(const uint32_t *)(codes + 4 * (size_t)i), h[0], h[1], h[2], h[3]);
+            float v[8];
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                p[j] = *(const uint32_t *)&t;
+                const float2 f = h2f2(h[j]);
+                v[2 * j] = f.x * s;
+                v[2 * j + 1] = f.y * s;
             }
-            if (vec && 8 * w + 8 <= in)
-                *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
-            else
-                for (int j = 0; j < 8; j++)
-                    if (8 * w + j < in) ((uint16_t *)o)[j] = (uint16_t)(p[j >> 1] >> (16 * (j & 1)));
+            if constexpr (sizeof(YT) == 2) {
+                uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    p[j] = *(const uint32_t *)&t;
+                }
+                if (c + 8 <= in)
+                    *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
+                else
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (c + j < in) o[j] = (YT)(p[j >> 1] >> (16 * (j & 1)));
+            } else {
+                if (c + 8 <= in) {
+                    ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                    ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                } else
+#pragma unroll
+                    for (int j = 0; j < 8; j++)
+                        if (c + j < in) o[j] = v[j];
+            }
         } else {
-            if (vec && 8 * w + 8 <= in) {
-                ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-            } else
-                for (int j = 0; j < 8; j++)
-                    if (8 * w + j < in) ((float *)o)[j] = v[j];
+            const float2 f = e2m1x2_to_float2(codes[i]);
+#pragma unroll
+            for (int j = 0; j < 2; j++)
+                if (c + j < in) {
+                    const float v = (j ? f.y : f.x) * s;
+                    if constexpr (sizeof(YT) == 2)
+                        o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                    else
+                        o[j] = v;
+                }
         }
     }
 }
@@ -316,24 +359,21 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
     a.ld = ld;
     a.rows = rows;
     a.cols = cols;
-    a.vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
     if (row) a.rcodes = row->codes, a.ratoms = row->atoms;
     if (col) a.ccodes = col->codes, a.catoms = col->atoms;
     // the tiles cover every scale atom, the padding ones included
     a.tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
     const long tiles = (long)a.tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
     if (tiles > 0x7fffffffL) return K3MOE_EINVAL;
-    cudaError_t e;
-    if (xdt == K3MOE_BF16) {
-        const size_t sm = col ? quant_smem<uint16_t>() : 0;
-        if (ensure_smem((const void *)k3_mx_quantize_operand<uint16_t>, sm) != K3MOE_OK) return K3MOE_ECUDA;
-        e = launch_pdl(k3_mx_quantize_operand<uint16_t>, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a);
-    } else {
-        const size_t sm = col ? quant_smem<uint32_t>() : 0;
-        if (ensure_smem((const void *)k3_mx_quantize_operand<uint32_t>, sm) != K3MOE_OK) return K3MOE_ECUDA;
-        e = launch_pdl(k3_mx_quantize_operand<uint32_t>, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a);
-    }
-    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+    const bool vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
+    const size_t sm = !col && vec ? 0 : xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
+    void (*const kernel)(QuantArgs) =
+        xdt == K3MOE_BF16 ? (vec ? k3_mx_quantize_operand<uint16_t, true> : k3_mx_quantize_operand<uint16_t, false>)
+                          : (vec ? k3_mx_quantize_operand<uint32_t, true> : k3_mx_quantize_operand<uint32_t, false>);
+    if (ensure_smem((const void *)kernel, sm) != K3MOE_OK) return K3MOE_ECUDA;
+    return launch_pdl(kernel, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a) == cudaSuccess
+               ? K3MOE_OK
+               : (cudaGetLastError(), K3MOE_ECUDA);
 }
 
 int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atoms, cudaStream_t s)
@@ -345,18 +385,33 @@ int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atom
     return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
 }
 
+template <typename YT, bool VEC>
+static int launch_dequantize(const k3moe_mx_operand *op, YT *y, long ld, cudaStream_t s)
+{
+    // one launch per block of rows whose units fit 31 bits
+    const uint32_t upr = (uint32_t)op_in_padded(op->in) / (VEC ? 8 : 2);
+    const int rows = (int)std::min<long>(op->rows, std::max<long>(1, (1L << 30) / upr));
+    for (int r = 0; r < op->rows; r += rows) {
+        const uint32_t n = (uint32_t)std::min(rows, op->rows - r) * upr;
+        const unsigned grid = (unsigned)std::min<long>(((long)n + 255) / 256, 32L * num_sms());
+        if (launch_pdl(k3_mx_dequantize<YT, VEC>, dim3(grid), dim3(256), 0, s,
+                       (const uint8_t *)op->codes + (size_t)r * (op_in_padded(op->in) / 2), (const uint8_t *)op->atoms,
+                       r, n, FastDiv(upr), op_k_atoms(op->in), op->in, y, ld) != cudaSuccess) {
+            cudaGetLastError();
+            return K3MOE_ECUDA;
+        }
+    }
+    return K3MOE_OK;
+}
+
 int launch_mx_dequantize(const k3moe_mx_operand *op, void *y, int ydt, long ld, cudaStream_t s)
 {
-    const long n = (long)op->rows * (op_in_padded(op->in) / 8);
-    const unsigned grid = (unsigned)std::min<long>((n + 255) / 256, 16L * num_sms());
     const bool vec = rows_aligned16(y, ld, ydt == K3MOE_BF16 ? 2 : 4);
-    const cudaError_t e =
-        ydt == K3MOE_BF16
-            ? launch_pdl(k3_mx_dequantize<uint16_t>, dim3(grid), dim3(256), 0, s, (const uint8_t *)op->codes,
-                         (const uint8_t *)op->atoms, op->rows, op->in, (uint16_t *)y, ld, vec)
-            : launch_pdl(k3_mx_dequantize<float>, dim3(grid), dim3(256), 0, s, (const uint8_t *)op->codes,
-                         (const uint8_t *)op->atoms, op->rows, op->in, (float *)y, ld, vec);
-    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+    if (ydt == K3MOE_BF16)
+        return vec ? launch_dequantize<uint16_t, true>(op, (uint16_t *)y, ld, s)
+                   : launch_dequantize<uint16_t, false>(op, (uint16_t *)y, ld, s);
+    return vec ? launch_dequantize<float, true>(op, (float *)y, ld, s)
+               : launch_dequantize<float, false>(op, (float *)y, ld, s);
 }
 
 }  // namespace k3

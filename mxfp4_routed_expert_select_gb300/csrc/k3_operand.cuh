@@ -21,4 +21,19 @@ K3_DEV float op_scale(uint32_t e)
     return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
 }
 
+// Division of n < 2^31 by a divisor fixed per launch: floor(n / d) =
+// (n m) >> (32 + s) with m = ceil(2^(32+s) / d), 2^s >= d (m < 2^33: its top bit
+// is the addition of n; Granlund and Montgomery, "Division by invariant
+// integers using multiplication", 1994).
+struct FastDiv {
+    uint32_t d, m, s;
+    FastDiv() = default;
+    explicit FastDiv(uint32_t div) : d(div), m(0), s(0)
+    {
+        while ((1ull << s) < d) s++;
+        m = (uint32_t)(((1ull << 32) * ((1ull << s) - d)) / d + 1);
+    }
+    K3_DEV uint32_t div(uint32_t n) const { return (__umulhi(n, m) + n) >> s; }
+};
+
 }  // namespace k3

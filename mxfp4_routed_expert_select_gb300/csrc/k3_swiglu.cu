@@ -26,9 +26,11 @@ struct SwigluArgs {
     const void *g, *u, *dh;
     void *h, *dg, *du;
     long ldg, ldu, ldh, lddg, lddu, lddh;
-    uint8_t *code;  // [2][T][fp] codes of g, then u; then [2][T][fp / 32] scale bytes
-    int T, f, cpr;  // eight-value chunks per row (fp / 8)
-    bool vec;       // every row of every matrix 16-byte aligned
+    uint8_t *cg, *cu, *sg, *su;  // codes [T][fp] and scale bytes [T][fp / 32] of g and u
+    uint32_t n;                  // eight-value chunks of this launch (rows x fp / 8), below 2^31
+    int f;
+    FastDiv cpr;                 // chunks per row (fp / 8)
+    bool vec;                    // every row of every matrix 16-byte aligned
 };
 
 // Eight values of a row from column c, zero past f.
@@ -140,33 +142,41 @@ K3_DEV void from_e4m3x8(uint2 q, uint32_t e, float (&v)[8])
 }
 K3_DEV float sigmoid(float g) { return __fdividef(1.f, 1.f + expf(-g)); }  // 0 where e^-g overflows
 
+// Two chunks per lane in flight: chunk i and the one a block's threads further.
 template <typename T>
 __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_forward(const SwigluArgs a)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const long n = (long)a.T * a.cpr, step = (long)gridDim.x * SW_THREADS;
-    uint8_t *cu = a.code + 8 * n, *sg = cu + 8 * n, *su = sg + n / 4;
+    const uint32_t step = gridDim.x * 2 * SW_THREADS;
     // n is a multiple of 4, so the four lanes of a block stay together; lanes
     // past the end take part in the shuffles
-    for (long i0 = (long)blockIdx.x * SW_THREADS + (threadIdx.x & ~31); i0 < n; i0 += step) {
-        const long i = i0 + (threadIdx.x & 31);
-        const bool on = i < n;
-        const int t = on ? (int)(i / a.cpr) : 0, c = on ? (int)(i % a.cpr) * 8 : a.f;
-        float g[8], u[8], h[8];
-        load8<T>(a.g, a.ldg, t, c, a.f, a.vec, g);
-        load8<T>(a.u, a.ldu, t, c, a.f, a.vec, u);
+    for (uint32_t i0 = blockIdx.x * 2 * SW_THREADS + (threadIdx.x & ~31u); i0 < a.n; i0 += step) {
+        float g[2][8], u[2][8];
+        uint32_t i[2];
+        int t[2], c[2];
 #pragma unroll
-        for (int j = 0; j < 8; j++) h[j] = g[j] * sigmoid(g[j]) * u[j];
-        uint32_t eg, eu;
-        const uint2 qg = e4m3x8(g, eg), qu = e4m3x8(u, eu);
-        if (!on) continue;
-        store8<T>(a.h, a.ldh, t, c, a.f, a.vec, h);
-        *(uint2 *)(a.code + 8 * i) = qg;
-        *(uint2 *)(cu + 8 * i) = qu;
-        if ((i & 3) == 0) {
-            sg[i >> 2] = (uint8_t)eg;
-            su[i >> 2] = (uint8_t)eu;
+        for (int k = 0; k < 2; k++) {
+            i[k] = i0 + k * SW_THREADS + (threadIdx.x & 31);
+            t[k] = (int)a.cpr.div(i[k]);
+            c[k] = i[k] < a.n ? (int)(i[k] - (uint32_t)t[k] * a.cpr.d) * 8 : a.f;
+            load8<T>(a.g, a.ldg, t[k], c[k], a.f, a.vec, g[k]);
+            load8<T>(a.u, a.ldu, t[k], c[k], a.f, a.vec, u[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            uint32_t eg, eu;
+            const uint2 qg = e4m3x8(g[k], eg), qu = e4m3x8(u[k], eu);
+            if (i[k] >= a.n) continue;
+#pragma unroll
+            for (int j = 0; j < 8; j++) g[k][j] = g[k][j] * sigmoid(g[k][j]) * u[k][j];
+            store8<T>(a.h, a.ldh, t[k], c[k], a.f, a.vec, g[k]);
+            *(uint2 *)(a.cg + 8 * (size_t)i[k]) = qg;
+            *(uint2 *)(a.cu + 8 * (size_t)i[k]) = qu;
+            if ((i[k] & 3) == 0) {
+                a.sg[i[k] >> 2] = (uint8_t)eg;
+                a.su[i[k] >> 2] = (uint8_t)eu;
+            }
         }
     }
 }
@@ -176,35 +186,72 @@ __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_backward(const SwigluArg
 {
     griddep_launch_dependents();
     griddep_wait();
-    const long n = (long)a.T * a.cpr, step = (long)gridDim.x * SW_THREADS;
-    const uint8_t *cu = a.code + 8 * n, *sg = cu + 8 * n, *su = sg + n / 4;
-    for (long i = (long)blockIdx.x * SW_THREADS + threadIdx.x; i < n; i += step) {
-        const int t = (int)(i / a.cpr), c = (int)(i % a.cpr) * 8;
-        float g[8], u[8], dh[8];
-        load8<T>(a.dh, a.lddh, t, c, a.f, a.vec, dh);
-        const uint2 qg = *(const uint2 *)(a.code + 8 * i), qu = *(const uint2 *)(cu + 8 * i);
-        from_e4m3x8(qg, sg[i >> 2], g);
-        from_e4m3x8(qu, su[i >> 2], u);
+    const uint32_t step = gridDim.x * 2 * SW_THREADS;
+    for (uint32_t i0 = blockIdx.x * 2 * SW_THREADS + threadIdx.x; i0 < a.n; i0 += step) {
+        float dh[2][8];
+        uint2 qg[2], qu[2];
+        uint32_t eg[2], eu[2], i[2];
+        int t[2], c[2];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float s = sigmoid(g[j]), d = dh[j] * s;
-            dh[j] = d * g[j];
-            g[j] = d * u[j] * (1.f + g[j] * (1.f - s));
+        for (int k = 0; k < 2; k++) {
+            i[k] = i0 + k * SW_THREADS;
+            t[k] = (int)a.cpr.div(i[k]);
+            c[k] = i[k] < a.n ? (int)(i[k] - (uint32_t)t[k] * a.cpr.d) * 8 : a.f;
+            load8<T>(a.dh, a.lddh, t[k], c[k], a.f, a.vec, dh[k]);
+            if (i[k] < a.n) {
+                qg[k] = *(const uint2 *)(a.cg + 8 * (size_t)i[k]);
+                qu[k] = *(const uint2 *)(a.cu + 8 * (size_t)i[k]);
+                eg[k] = a.sg[i[k] >> 2];
+                eu[k] = a.su[i[k] >> 2];
+            }
         }
-        store8<T>(a.dg, a.lddg, t, c, a.f, a.vec, g);
-        store8<T>(a.du, a.lddu, t, c, a.f, a.vec, dh);
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            if (i[k] >= a.n) continue;
+            float g[8], u[8];
+            from_e4m3x8(qg[k], eg[k], g);
+            from_e4m3x8(qu[k], eu[k], u);
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const float s = sigmoid(g[j]), d = dh[k][j] * s;
+                dh[k][j] = d * g[j];
+                g[j] = d * u[j] * (1.f + g[j] * (1.f - s));
+            }
+            store8<T>(a.dg, a.lddg, t[k], c[k], a.f, a.vec, g);
+            store8<T>(a.du, a.lddu, t[k], c[k], a.f, a.vec, dh[k]);
+        }
     }
 }
 
-int launch(const SwigluArgs &a, int dtype, bool backward, cudaStream_t s)
+// One launch per 2^31 / 8 chunks (32-bit chunk indices), each a block of rows.
+int launch(SwigluArgs a, void *ckpt, int dtype, int T, bool backward, cudaStream_t s)
 {
-    const long n = (long)a.T * a.cpr;
-    const dim3 grid((unsigned)std::min<long>((n + SW_THREADS - 1) / SW_THREADS, 16L * num_sms()));
+    const int fp = op_in_padded(a.f), es = dtype == K3MOE_BF16 ? 2 : 4;
+    const uint32_t cpr = (uint32_t)fp / 8;
+    a.cpr = FastDiv(cpr);
+    a.cg = (uint8_t *)ckpt;
+    a.cu = a.cg + (size_t)T * fp;
+    a.sg = a.cu + (size_t)T * fp;
+    a.su = a.sg + (size_t)T * fp / 32;
     void (*const kernel)(SwigluArgs) = dtype == K3MOE_BF16
                                            ? (backward ? k3_swiglu_backward<uint16_t> : k3_swiglu_forward<uint16_t>)
                                            : (backward ? k3_swiglu_backward<float> : k3_swiglu_forward<float>);
-    return launch_pdl(kernel, grid, dim3(SW_THREADS), 0, s, a) == cudaSuccess ? K3MOE_OK
-                                                                            : (cudaGetLastError(), K3MOE_ECUDA);
+    const int rows = (int)std::min<long>(T, std::max<long>(1, (1L << 28) / cpr));
+    for (int t = 0; t < T; t += rows) {
+        const int r = std::min(rows, T - t);
+        a.n = (uint32_t)r * cpr;
+        const dim3 grid((unsigned)std::min<long>(((long)a.n + 2 * SW_THREADS - 1) / (2 * SW_THREADS), 16L * num_sms()));
+        if (launch_pdl(kernel, grid, dim3(SW_THREADS), 0, s, a) != cudaSuccess) {
+            cudaGetLastError();
+            return K3MOE_ECUDA;
+        }
+        auto skip = [&](auto &p, long ld) { p = (decltype(+p))((const char *)p + (size_t)r * ld * es); };
+        skip(a.g, a.ldg), skip(a.u, a.ldu), skip(a.dh, a.lddh);
+        skip(a.h, a.ldh), skip(a.dg, a.lddg), skip(a.du, a.lddu);
+        a.cg += (size_t)r * fp, a.cu += (size_t)r * fp;
+        a.sg += (size_t)r * fp / 32, a.su += (size_t)r * fp / 32;
+    }
+    return K3MOE_OK;
 }
 bool rows16(const void *p, long ld, int dtype)
 {
@@ -219,10 +266,9 @@ int launch_swiglu_forward(void *h, long ldh, void *ckpt, const void *g, long ldg
     SwigluArgs a = {};
     a.g = g, a.u = u, a.h = h;
     a.ldg = ldg, a.ldu = ldu, a.ldh = ldh;
-    a.code = (uint8_t *)ckpt;
-    a.T = T, a.f = f, a.cpr = op_in_padded(f) / 8;
+    a.f = f;
     a.vec = rows16(g, ldg, dtype) && rows16(u, ldu, dtype) && rows16(h, ldh, dtype);
-    return launch(a, dtype, false, s);
+    return launch(a, ckpt, dtype, T, false, s);
 }
 int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void *dh, long lddh, const void *ckpt,
                            int dtype, int T, int f, cudaStream_t s)
@@ -230,10 +276,9 @@ int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void 
     SwigluArgs a = {};
     a.dg = dg, a.du = du, a.dh = dh;
     a.lddg = lddg, a.lddu = lddu, a.lddh = lddh;
-    a.code = (uint8_t *)ckpt;
-    a.T = T, a.f = f, a.cpr = op_in_padded(f) / 8;
+    a.f = f;
     a.vec = rows16(dg, lddg, dtype) && rows16(du, lddu, dtype) && rows16(dh, lddh, dtype);
-    return launch(a, dtype, true, s);
+    return launch(a, (void *)ckpt, dtype, T, true, s);
 }
 
 }  // namespace k3

@@ -229,10 +229,28 @@ def _ptr(t):
     return t.ctypes.data
 
 
-def _stream(s=None):
+_raw_stream = None
+
+
+def _current_stream():
+    """The raw handle of torch's current stream.  torch.cuda.current_stream()
+    builds a Stream object (about 3 us on a Grace core, as long as a whole call
+    into the library); torch's own raw query takes 0.2 us and is used from the
+    second call on, when CUDA is known to be initialised."""
+    global _raw_stream
+    if _raw_stream is not None:
+        return _raw_stream()
     import torch
+    handle = torch.cuda.current_stream().cuda_stream
+    get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if get is not None and dev is not None:
+        _raw_stream = lambda: get(dev())  # noqa: E731
+    return handle
+
+
+def _stream(s=None):
     if s is None:
-        s = torch.cuda.current_stream()
+        return _current_stream()
     return s.cuda_stream if hasattr(s, "cuda_stream") else s
 
 
@@ -298,28 +316,39 @@ def mx_quantize(codes, scales, x, rows, cols, stream=None):
           "k3moe_mx_quantize")
 
 
-def _dtype(*tensors):
+_DTYPES = {}
+
+
+def _dtype(t, *others):
     """The K3MOE_* type that all the tensors share."""
-    import torch
-    dt = {torch.float32: K3MOE_F32, torch.bfloat16: K3MOE_BF16}.get(tensors[0].dtype)
-    if dt is None or any(t.dtype != tensors[0].dtype for t in tensors):
-        raise TypeError("fp32 or bf16 tensors of one type expected, got %s" % [t.dtype for t in tensors])
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: K3MOE_F32, torch.bfloat16: K3MOE_BF16})
+    d = t.dtype
+    dt = _DTYPES.get(d)
+    if dt is None:
+        raise TypeError("fp32 or bf16 tensors expected, got %s" % d)
+    for o in others:
+        if o.dtype is not d:
+            raise TypeError("tensors of one type expected, got %s and %s" % (d, o.dtype))
     return dt
 
 
 def _ld(t, rows, cols):
     """Row stride (elements) of a [rows][cols] tensor with unit column stride."""
-    if tuple(t.shape) != (rows, cols) or (cols > 1 and t.stride(1) != 1):
-        raise ValueError("expected [%d][%d] with unit column stride, got shape %s strides %s"
-                         % (rows, cols, tuple(t.shape), t.stride()))
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if t.shape != (rows, cols):
+        raise ValueError("expected shape [%d][%d], got %s" % (rows, cols, tuple(t.shape)))
+    ld, cs = t.stride()
+    if cs != 1 and cols > 1:
+        raise ValueError("expected unit column stride, got strides %s" % (t.stride(),))
+    return ld if rows > 1 or ld > cols else cols
 
 
 def _flat(t, dtype, *shape):
     """Raw pointer of a contiguous tensor of that type and shape (or None)."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError("expected a contiguous %s tensor of shape %s, got %s %s" % (dtype, shape, t.dtype,
                                                                                      tuple(t.shape)))
     return t.data_ptr()
