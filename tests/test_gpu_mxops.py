@@ -281,3 +281,41 @@ def test_other_stream_and_graph():
     torch.cuda.synchronize()
     assert torch.equal(C, -2.0 * first)
     assert k.device_error() == 0
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(2048, 1537, 160, 0), (1100, 3333, 512, 3), (4096, 1000, 288, 8), (3000, 2064, 64, 0),
+                                       (257, 12000, 1056, 1), (2500, 1300, 1, 4)])
+def test_matmul_pairs(M, N, K, pad, out):
+    """Products large enough for CTA pairs: rows of C aligned for wide stores or
+    not, ragged row and column tiles of every width, a K of one block and less."""
+    A, B, va, vb = _operands(M, N, K, M + 3 * N)
+    C = torch.full((M, N + pad), 5.0, dtype=DT[out], device="cuda")
+    k.mx_matmul(C[:, :N], A, B)
+    a, b = torch.from_numpy(va).cuda(), torch.from_numpy(vb).cuda()
+    want = a @ b.t()
+    tol = (a.abs() @ b.abs().t()) * (K / 64 + 10) * 2.0 ** -22 + want.abs() * (2.0 ** -8 if out == "bf16" else 2.0 ** -24)
+    assert bool(((C[:, :N].double() - want).abs() <= tol).all())
+    assert bool((C[:, N:] == 5).all())
+    if out == "f32":
+        k.mx_matmul(C[:, :N], A, B, accumulate=True)
+        tol = tol * 2 + 2 * want.abs() * 2.0 ** -24
+        assert bool(((C[:, :N].double() - 2 * want).abs() <= tol).all())
+        assert bool((C[:, N:] == 5).all())
+    torch.cuda.synchronize()
+    assert k.device_error() == 0
+
+
+def test_matmul_nan_stays_in_its_rows_and_columns():
+    """Non-finite blocks in a CTA-pair product reach their own row and column only
+    (tiles reach past the matrices, and the tail of K past the blocks)."""
+    M, N, K = 1030, 5000, 96
+    x, w = _x(M, K, torch.float32, 1), _x(N, K, torch.float32, 2)
+    x[700, 40] = float("nan")
+    w[4999, 95] = float("inf")
+    A, B, C = k.MxOperand(M, K), k.MxOperand(N, K), torch.empty(M, N, device="cuda")
+    k.mx_quantize_operand(x, A)
+    k.mx_quantize_operand(w, B)
+    k.mx_matmul(C, A, B)
+    bad = torch.isnan(C)
+    assert bool(bad[700].all()) and bool(bad[:, 4999].all()) and int(bad.sum()) == M + N - 1
