@@ -254,6 +254,34 @@ K3_DEV void put_column(const MgArgs &a, int n, int m, const uint32_t (&r)[CH])
 
 // -------------------------------------------------------------- single CTAs
 
+// This rank's slice of a split tile's columns: the sums of R ranks, in rank order,
+// to C.  A warp takes a column, a lane four consecutive rows of it; eight remote
+// loads (a few hundred clocks each) are in flight per lane.
+template <int NT, int R, typename CT>
+K3_DEV void join_ranks(const MgArgs &a, uint32_t sbase, int tile, int rank)
+{
+    constexpr int J = 8 / R, NW = MG_THREADS / 32;  // columns in flight, warps
+    const int lane = threadIdx.x & 31;
+    const int n = (tile / a.tiles_t) * MG_M + 4 * lane, m0 = (tile % a.tiles_t) * NT;
+    const int c0 = NT * rank / R, c1 = min(NT * (rank + 1) / R, a.M - m0);
+    for (int c = c0 + (int)(threadIdx.x >> 5); c < c1; c += J * NW) {
+        float4 v[J][R];
+#pragma unroll
+        for (int j = 0; j < J; j++)
+#pragma unroll
+            for (int r = 0; r < R; r++)
+                if (c + j * NW < c1) v[j][r] = ld_peer4(sbase + (uint32_t)((c + j * NW) * MG_M + 4 * lane) * 4, (uint32_t)r);
+#pragma unroll
+        for (int j = 0; j < J; j++)
+            if (c + j * NW < c1) {
+                float t[4] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w};
+#pragma unroll
+                for (int r = 1; r < R; r++) t[0] += v[j][r].x, t[1] += v[j][r].y, t[2] += v[j][r].z, t[3] += v[j][r].w;
+                put4((CT *)a.C + (long)(m0 + c + j * NW) * a.ldc, n, a.N, t, a.accumulate, a.vec);
+            }
+    }
+}
+
 // Shared memory and TMEM of one CTA with NT columns, one tile per cluster
 // (SPLIT) or many per CTA.
 template <int NT, bool SPLIT>
@@ -430,31 +458,14 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     if constexpr (SPLIT) {
         __syncwarp();
         cluster_sync();  // every rank's partial sums are in its shared memory
-        // a warp takes a column, a lane four consecutive rows of it: two columns'
-        // partial sums of all ranks are in flight at a time (a remote load takes a
-        // few hundred clocks)
-        const int u = first, n = (u / a.tiles_t) * MG_M + 4 * lane, m0 = (u % a.tiles_t) * NT;
-        const int c0 = NT * rank / ranks, c1 = min(NT * (rank + 1) / ranks, a.M - m0);
-        if (!*abort_flag)
-            for (int c = c0 + warp; c < c1; c += 2 * MG_THREADS / 32) {
-                float4 v[2][MG_MAX_RANKS];
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const uint32_t at = sbase + (uint32_t)(min(c + j * (MG_THREADS / 32), c1 - 1) * MG_M + 4 * lane) * 4;
-#pragma unroll
-                    for (int r = 0; r < MG_MAX_RANKS; r++)
-                        if (r < ranks) v[j][r] = ld_peer4(at, (uint32_t)r);
-                }
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    const int cj = c + j * (MG_THREADS / 32);
-                    float t[4] = {v[j][0].x, v[j][0].y, v[j][0].z, v[j][0].w};
-#pragma unroll
-                    for (int r = 1; r < MG_MAX_RANKS; r++)
-                        if (r < ranks) t[0] += v[j][r].x, t[1] += v[j][r].y, t[2] += v[j][r].z, t[3] += v[j][r].w;
-                    if (cj < c1) put4((CT *)a.C + (long)(m0 + cj) * a.ldc, n, a.N, t, a.accumulate, a.vec);
-                }
-            }
+        if (!*abort_flag) {
+            if (ranks == 2)
+                join_ranks<NT, 2, CT>(a, sbase, first, rank);
+            else if (ranks == 4)
+                join_ranks<NT, 4, CT>(a, sbase, first, rank);
+            else
+                join_ranks<NT, 8, CT>(a, sbase, first, rank);
+        }
         cluster_sync();  // no CTA leaves while another reads its sums
     } else {
         __syncthreads();
