@@ -60,7 +60,10 @@ K3_DEV uint32_t convert8(const float (&v)[8], float inv, uint32_t e)
 {
     float a[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) a[i] = v[i] * inv;
+    for (int i = 0; i < 8; i += 2) {
+        a[i] = v[i], a[i + 1] = v[i + 1];
+        scale2(a[i], a[i + 1], inv);
+    }
     return e == 255u ? 0u : codes8(a);  // a non-finite block: codes 0
 }
 
@@ -108,23 +111,6 @@ K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
             }
     }
     return o;
-}
-// Bits of the largest magnitude of eight values.  Non-negative floats order
-// like their bits, a NaN above infinity; bf16 values two at a time.
-template <typename XT>
-K3_DEV uint32_t chunk_max(const Chunk<XT> &q)
-{
-    if constexpr (sizeof(XT) == 2) {
-        uint32_t m = q.w[0] & 0x7fff7fffu;
-#pragma unroll
-        for (int i = 1; i < 4; i++) m = __vmaxu2(m, q.w[i] & 0x7fff7fffu);
-        return max(m & 0xffff0000u, m << 16);
-    } else {
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; i++) m = max(m, q.w[i] & 0x7fffffffu);
-        return m;
-    }
 }
 template <typename XT>
 K3_DEV void chunk_values(const Chunk<XT> &q, float (&v)[8])
@@ -199,7 +185,7 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
             if (do_row) {
                 float v[8];
                 chunk_values<XT>(q[j], v);
-                uint32_t mb = chunk_max<XT>(q[j]);
+                uint32_t mb = absmax8(q[j].w);
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
                 mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
                 float inv;
@@ -228,10 +214,7 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
 #pragma unroll
         for (int i = 0; i < 32; i++) {
             raw[i] = tile[(32 * rb + i) * PITCH + wc];
-            if constexpr (sizeof(XT) == 2)
-                top = __vmaxu2(top, raw[i] & 0x7fff7fffu);
-            else
-                top = max(top, raw[i] & 0x7fffffffu);
+            top = sizeof(XT) == 2 ? absmax2(top, raw[i]) : absmax(top, raw[i]);
         }
 #pragma unroll
         for (int h = 0; h < COLS; h++) {
@@ -240,7 +223,7 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
 #pragma unroll
             for (int i = 0; i < 32; i++)
                 v[i] = __uint_as_float(sizeof(XT) == 4 ? raw[i] : h ? (raw[i] & 0xffff0000u) : (raw[i] << 16));
-            const uint32_t mb = sizeof(XT) == 4 ? top : h ? (top & 0xffff0000u) : (top << 16);
+            const uint32_t mb = sizeof(XT) == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16;
             float inv;
             const uint32_t e = block_byte(mb, inv);
 #pragma unroll

@@ -21,6 +21,41 @@ K3_DEV float op_scale(uint32_t e)
     return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
 }
 
+// The larger magnitude (its sign is not meaningful); NaN if either is.
+K3_DEV uint32_t absmax(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+K3_DEV uint32_t absmax2(uint32_t a, uint32_t b)  // two bf16 values
+{
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Bits of the largest magnitude of eight values held as NW words (4: bf16 pairs,
+// 8: fp32); 0x7f800000 and above if one is not finite.
+template <int NW>
+K3_DEV uint32_t absmax8(const uint32_t (&w)[NW])
+{
+    if constexpr (NW == 4) {
+        const uint32_t m = absmax2(absmax2(w[0], w[1]), absmax2(w[2], w[3])) & 0x7fff7fffu;
+        return max(m & 0xffff0000u, m << 16);
+    } else {
+        return absmax(absmax(absmax(w[0], w[1]), absmax(w[2], w[3])), absmax(absmax(w[4], w[5]), absmax(w[6], w[7]))) &
+               0x7fffffffu;
+    }
+}
+// (x, y) * s, one instruction.
+K3_DEV void scale2(float &x, float &y, float s)
+{
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %2};\n\tmul.rn.f32x2 a, a, b;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(s));
+}
+
 // Division of n < 2^31 by a divisor fixed per launch: floor(n / d) =
 // (n m) >> (32 + s) with m = ceil(2^(32+s) / d), 2^s >= d (m < 2^33: its top bit
 // is the addition of n; Granlund and Montgomery, "Division by invariant

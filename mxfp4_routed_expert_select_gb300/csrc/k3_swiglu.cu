@@ -30,46 +30,52 @@ struct SwigluArgs {
     uint32_t n;                  // eight-value chunks of this launch (rows x fp / 8), below 2^31
     int f;
     FastDiv cpr;                 // chunks per row (fp / 8)
-    bool vec;                    // every row of every matrix 16-byte aligned
 };
 
-// Eight values of a row from column c, zero past f.
+// Eight values of a row as loaded.
 template <typename T>
-K3_DEV void load8(const void *base, long ld, int t, int c, int f, bool vec, float (&v)[8])
+struct Raw {
+    uint32_t w[2 * sizeof(T)];
+};
+// The values from column c, zero past f.  VEC: every row of every matrix is
+// 16-byte aligned and f a multiple of 8, so a chunk is whole or not there.
+template <typename T, bool VEC>
+K3_DEV Raw<T> load8(const void *base, long ld, int t, int c, int f)
 {
+    Raw<T> r;
+    constexpr int NW = 2 * sizeof(T);
+#pragma unroll
+    for (int i = 0; i < NW; i++) r.w[i] = 0u;
     const T *p = (const T *)base + (long)t * ld + c;
-    if (vec && c + 8 <= f) {
-        uint32_t w[2 * sizeof(T)];
+    if constexpr (VEC) {
+        if (c < f)
 #pragma unroll
-        for (int i = 0; i < (int)sizeof(T) / 2; i++) {
-            uint4 q;
-            asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                         : "l"((const uint4 *)p + i));
-            w[4 * i] = q.x, w[4 * i + 1] = q.y, w[4 * i + 2] = q.z, w[4 * i + 3] = q.w;
-        }
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            if constexpr (sizeof(T) == 2)
-                v[i] = __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-            else
-                v[i] = __uint_as_float(w[i]);
-        }
+            for (int i = 0; i < NW / 4; i++)
+                asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
+                             : "l"((const uint4 *)p + i));
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            v[i] = 0.f;
+        for (int i = 0; i < 8; i++)
             if (c + i < f) {
                 if constexpr (sizeof(T) == 2)
-                    v[i] = __uint_as_float((uint32_t)p[i] << 16);
+                    r.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
                 else
-                    v[i] = p[i];
+                    r.w[i] = p[i];
             }
-        }
     }
+    return r;
 }
 template <typename T>
-K3_DEV void store8(void *base, long ld, int t, int c, int f, bool vec, const float (&v)[8])
+K3_DEV float value(const Raw<T> &r, int i)
+{
+    if constexpr (sizeof(T) == 2)
+        return __uint_as_float((i & 1) ? (r.w[i >> 1] & 0xffff0000u) : (r.w[i >> 1] << 16));
+    else
+        return __uint_as_float(r.w[i]);
+}
+template <typename T, bool VEC>
+K3_DEV void store8(void *base, long ld, int t, int c, int f, const float (&v)[8])
 {
     T *p = (T *)base + (long)t * ld + c;
     if constexpr (sizeof(T) == 2) {
@@ -79,30 +85,33 @@ K3_DEV void store8(void *base, long ld, int t, int c, int f, bool vec, const flo
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             w[i] = *(const uint32_t *)&b;
         }
-        if (vec && c + 8 <= f)
-            *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
-        else
+        if constexpr (VEC) {
+            if (c < f) *(uint4 *)p = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
                 if (c + i < f) p[i] = (T)(w[i >> 1] >> (16 * (i & 1)));
+        }
     } else {
-        if (vec && c + 8 <= f) {
-            ((float4 *)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            ((float4 *)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else
+        if constexpr (VEC) {
+            if (c < f) {
+                ((float4 *)p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                ((float4 *)p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        } else {
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                if (c + i < f) p[i] = v[i];
+                if (c + i < f) p[i] = __float_as_uint(v[i]);
+        }
     }
 }
 
 // The scale byte of the block whose eight values this lane and the three next
 // to it hold, and the lane's codes.
-K3_DEV uint2 e4m3x8(const float (&v)[8], uint32_t &e)
+template <typename T>
+K3_DEV uint2 e4m3x8(const Raw<T> &v, uint32_t &e)
 {
-    uint32_t mb = 0u;
-#pragma unroll
-    for (int i = 0; i < 8; i++) mb = max(mb, __float_as_uint(v[i]) & 0x7fffffffu);
+    uint32_t mb = absmax8(v.w);
     mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
     mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
     if (mb >= 0x7f800000u) {
@@ -114,7 +123,10 @@ K3_DEV uint2 e4m3x8(const float (&v)[8], uint32_t &e)
     const float inv = __uint_as_float((254u - e) << 23);
     float a[8];
 #pragma unroll
-    for (int i = 0; i < 8; i++) a[i] = v[i] * inv;
+    for (int i = 0; i < 8; i += 2) {
+        a[i] = value(v, i), a[i + 1] = value(v, i + 1);
+        scale2(a[i], a[i + 1], inv);
+    }
     if (e == 247u)  // at 2^120 a code of 256 would read back as infinity
 #pragma unroll
         for (int i = 0; i < 8; i++) a[i] = fminf(fmaxf(a[i], -240.f), 240.f);
@@ -140,91 +152,119 @@ K3_DEV void from_e4m3x8(uint2 q, uint32_t e, float (&v)[8])
         v[2 * i + 1] = f.y * s;
     }
 }
-K3_DEV float sigmoid(float g) { return __fdividef(1.f, 1.f + expf(-g)); }  // 0 where e^-g overflows
-
-// Two chunks per lane in flight: chunk i and the one a block's threads further.
+// sigma(g); 0 where e^-g overflows.  bf16 data (2^-8) takes the fast exponential
+// (2^-19 over the range where sigma matters): with the full one the forward pass
+// was bound by issue.
 template <typename T>
+K3_DEV float sigmoid(float g)
+{
+    return __fdividef(1.f, 1.f + (sizeof(T) == 2 ? __expf(-g) : expf(-g)));
+}
+
+// Chunk i of a launch as (row, column); past the end the column is f.
+struct Place {
+    int t, c;
+};
+K3_DEV Place place(const SwigluArgs &a, uint32_t i)
+{
+    const uint32_t t = a.cpr.div(i);
+    return {(int)t, i < a.n ? (int)(i - t * a.cpr.d) * 8 : a.f};
+}
+
+// A lane works on one chunk while the next one's loads are in flight.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_forward(const SwigluArgs a)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t step = gridDim.x * 2 * SW_THREADS;
+    const uint32_t step = gridDim.x * SW_THREADS;
     // n is a multiple of 4, so the four lanes of a block stay together; lanes
     // past the end take part in the shuffles
-    for (uint32_t i0 = blockIdx.x * 2 * SW_THREADS + (threadIdx.x & ~31u); i0 < a.n; i0 += step) {
-        float g[2][8], u[2][8];
-        uint32_t i[2];
-        int t[2], c[2];
+    uint32_t i = blockIdx.x * SW_THREADS + threadIdx.x;
+    Place pl = place(a, i);
+    Raw<T> g = load8<T, VEC>(a.g, a.ldg, pl.t, pl.c, a.f), u = load8<T, VEC>(a.u, a.ldu, pl.t, pl.c, a.f);
+    while ((i & ~31u) < a.n) {
+        const uint32_t in = i + step;
+        const Place pn = place(a, in);
+        const Raw<T> gn = load8<T, VEC>(a.g, a.ldg, pn.t, pn.c, a.f), un = load8<T, VEC>(a.u, a.ldu, pn.t, pn.c, a.f);
+        uint32_t eg, eu;
+        const uint2 qg = e4m3x8(g, eg), qu = e4m3x8(u, eu);
+        if (i < a.n) {
+            float h[8];
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            i[k] = i0 + k * SW_THREADS + (threadIdx.x & 31);
-            t[k] = (int)a.cpr.div(i[k]);
-            c[k] = i[k] < a.n ? (int)(i[k] - (uint32_t)t[k] * a.cpr.d) * 8 : a.f;
-            load8<T>(a.g, a.ldg, t[k], c[k], a.f, a.vec, g[k]);
-            load8<T>(a.u, a.ldu, t[k], c[k], a.f, a.vec, u[k]);
-        }
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            uint32_t eg, eu;
-            const uint2 qg = e4m3x8(g[k], eg), qu = e4m3x8(u[k], eu);
-            if (i[k] >= a.n) continue;
-#pragma unroll
-            for (int j = 0; j < 8; j++) g[k][j] = g[k][j] * sigmoid(g[k][j]) * u[k][j];
-            store8<T>(a.h, a.ldh, t[k], c[k], a.f, a.vec, g[k]);
-            *(uint2 *)(a.cg + 8 * (size_t)i[k]) = qg;
-            *(uint2 *)(a.cu + 8 * (size_t)i[k]) = qu;
-            if ((i[k] & 3) == 0) {
-                a.sg[i[k] >> 2] = (uint8_t)eg;
-                a.su[i[k] >> 2] = (uint8_t)eu;
+            for (int j = 0; j < 8; j++) h[j] = value(g, j) * sigmoid<T>(value(g, j)) * value(u, j);
+            store8<T, VEC>(a.h, a.ldh, pl.t, pl.c, a.f, h);
+            *(uint2 *)(a.cg + 8 * (size_t)i) = qg;
+            *(uint2 *)(a.cu + 8 * (size_t)i) = qu;
+            if ((i & 3) == 0) {
+                a.sg[i >> 2] = (uint8_t)eg;
+                a.su[i >> 2] = (uint8_t)eu;
             }
         }
+        i = in, pl = pn, g = gn, u = un;
     }
 }
 
+// What the backward pass reads of a chunk.
 template <typename T>
+struct Kept {
+    Raw<T> dh;
+    uint2 qg, qu;
+    uint32_t eg, eu;
+};
+template <typename T, bool VEC>
+K3_DEV Kept<T> load_kept(const SwigluArgs &a, uint32_t i, const Place &p)
+{
+    Kept<T> k;
+    k.dh = load8<T, VEC>(a.dh, a.lddh, p.t, p.c, a.f);
+    if (i < a.n) {
+        k.qg = *(const uint2 *)(a.cg + 8 * (size_t)i);
+        k.qu = *(const uint2 *)(a.cu + 8 * (size_t)i);
+        k.eg = a.sg[i >> 2];
+        k.eu = a.su[i >> 2];
+    } else {
+        k.qg = k.qu = make_uint2(0u, 0u);
+        k.eg = k.eu = 0u;
+    }
+    return k;
+}
+
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_backward(const SwigluArgs a)
 {
     griddep_launch_dependents();
     griddep_wait();
-    const uint32_t step = gridDim.x * 2 * SW_THREADS;
-    for (uint32_t i0 = blockIdx.x * 2 * SW_THREADS + threadIdx.x; i0 < a.n; i0 += step) {
-        float dh[2][8];
-        uint2 qg[2], qu[2];
-        uint32_t eg[2], eu[2], i[2];
-        int t[2], c[2];
+    const uint32_t step = gridDim.x * SW_THREADS;
+    uint32_t i = blockIdx.x * SW_THREADS + threadIdx.x;
+    Place pl = place(a, i);
+    Kept<T> k = load_kept<T, VEC>(a, i, pl);
+    while (i < a.n) {
+        const uint32_t in = i + step;
+        const Place pn = place(a, in);
+        const Kept<T> kn = load_kept<T, VEC>(a, in, pn);
+        float g[8], u[8];
+        from_e4m3x8(k.qg, k.eg, g);
+        from_e4m3x8(k.qu, k.eu, u);
 #pragma unroll
-        for (int k = 0; k < 2; k++) {
-            i[k] = i0 + k * SW_THREADS;
-            t[k] = (int)a.cpr.div(i[k]);
-            c[k] = i[k] < a.n ? (int)(i[k] - (uint32_t)t[k] * a.cpr.d) * 8 : a.f;
-            load8<T>(a.dh, a.lddh, t[k], c[k], a.f, a.vec, dh[k]);
-            if (i[k] < a.n) {
-                qg[k] = *(const uint2 *)(a.cg + 8 * (size_t)i[k]);
-                qu[k] = *(const uint2 *)(a.cu + 8 * (size_t)i[k]);
-                eg[k] = a.sg[i[k] >> 2];
-                eu[k] = a.su[i[k] >> 2];
-            }
+        for (int j = 0; j < 8; j++) {
+            const float s = sigmoid<T>(g[j]), d = value(k.dh, j) * s, gj = g[j];
+            g[j] = d * u[j] * (1.f + gj * (1.f - s));
+            u[j] = d * gj;
         }
-#pragma unroll
-        for (int k = 0; k < 2; k++) {
-            if (i[k] >= a.n) continue;
-            float g[8], u[8];
-            from_e4m3x8(qg[k], eg[k], g);
-            from_e4m3x8(qu[k], eu[k], u);
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const float s = sigmoid(g[j]), d = dh[k][j] * s;
-                dh[k][j] = d * g[j];
-                g[j] = d * u[j] * (1.f + g[j] * (1.f - s));
-            }
-            store8<T>(a.dg, a.lddg, t[k], c[k], a.f, a.vec, g);
-            store8<T>(a.du, a.lddu, t[k], c[k], a.f, a.vec, dh[k]);
-        }
+        store8<T, VEC>(a.dg, a.lddg, pl.t, pl.c, a.f, g);
+        store8<T, VEC>(a.du, a.lddu, pl.t, pl.c, a.f, u);
+        i = in, pl = pn, k = kn;
     }
 }
 
+template <typename T, bool VEC>
+constexpr auto pick(bool backward)
+{
+    return backward ? k3_swiglu_backward<T, VEC> : k3_swiglu_forward<T, VEC>;
+}
+
 // One launch per 2^31 / 8 chunks (32-bit chunk indices), each a block of rows.
-int launch(SwigluArgs a, void *ckpt, int dtype, int T, bool backward, cudaStream_t s)
+int launch(SwigluArgs a, void *ckpt, int dtype, int T, bool vec, bool backward, cudaStream_t s)
 {
     const int fp = op_in_padded(a.f), es = dtype == K3MOE_BF16 ? 2 : 4;
     const uint32_t cpr = (uint32_t)fp / 8;
@@ -233,14 +273,15 @@ int launch(SwigluArgs a, void *ckpt, int dtype, int T, bool backward, cudaStream
     a.cu = a.cg + (size_t)T * fp;
     a.sg = a.cu + (size_t)T * fp;
     a.su = a.sg + (size_t)T * fp / 32;
-    void (*const kernel)(SwigluArgs) = dtype == K3MOE_BF16
-                                           ? (backward ? k3_swiglu_backward<uint16_t> : k3_swiglu_forward<uint16_t>)
-                                           : (backward ? k3_swiglu_backward<float> : k3_swiglu_forward<float>);
+    vec = vec && a.f % 8 == 0;
+    void (*const kernel)(SwigluArgs) =
+        dtype == K3MOE_BF16 ? (vec ? pick<uint16_t, true>(backward) : pick<uint16_t, false>(backward))
+                            : (vec ? pick<uint32_t, true>(backward) : pick<uint32_t, false>(backward));
     const int rows = (int)std::min<long>(T, std::max<long>(1, (1L << 28) / cpr));
     for (int t = 0; t < T; t += rows) {
         const int r = std::min(rows, T - t);
         a.n = (uint32_t)r * cpr;
-        const dim3 grid((unsigned)std::min<long>(((long)a.n + 2 * SW_THREADS - 1) / (2 * SW_THREADS), 16L * num_sms()));
+        const dim3 grid((unsigned)std::min<long>(((long)a.n + SW_THREADS - 1) / SW_THREADS, 8L * num_sms()));
         if (launch_pdl(kernel, grid, dim3(SW_THREADS), 0, s, a) != cudaSuccess) {
             cudaGetLastError();
             return K3MOE_ECUDA;
@@ -267,8 +308,8 @@ int launch_swiglu_forward(void *h, long ldh, void *ckpt, const void *g, long ldg
     a.g = g, a.u = u, a.h = h;
     a.ldg = ldg, a.ldu = ldu, a.ldh = ldh;
     a.f = f;
-    a.vec = rows16(g, ldg, dtype) && rows16(u, ldu, dtype) && rows16(h, ldh, dtype);
-    return launch(a, ckpt, dtype, T, false, s);
+    const bool vec = rows16(g, ldg, dtype) && rows16(u, ldu, dtype) && rows16(h, ldh, dtype);
+    return launch(a, ckpt, dtype, T, vec, false, s);
 }
 int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void *dh, long lddh, const void *ckpt,
                            int dtype, int T, int f, cudaStream_t s)
@@ -277,8 +318,8 @@ int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void 
     a.dg = dg, a.du = du, a.dh = dh;
     a.lddg = lddg, a.lddu = lddu, a.lddh = lddh;
     a.f = f;
-    a.vec = rows16(dg, lddg, dtype) && rows16(du, lddu, dtype) && rows16(dh, lddh, dtype);
-    return launch(a, (void *)ckpt, dtype, T, true, s);
+    const bool vec = rows16(dg, lddg, dtype) && rows16(du, lddu, dtype) && rows16(dh, lddh, dtype);
+    return launch(a, (void *)ckpt, dtype, T, vec, true, s);
 }
 
 }  // namespace k3
