@@ -84,26 +84,26 @@ template <typename XT>
 struct alignas(16) Chunk {
     uint32_t w[2 * sizeof(XT)];
 };
-// From global memory at column c (rows 16-byte aligned), zero past the matrix.
+// From p (16-byte aligned if whole), the first `cols` of them, zero past those.
 template <typename XT>
-K3_DEV Chunk<XT> load_chunk(const QuantArgs &a, int r, int c)
+K3_DEV Chunk<XT> load_chunk(const XT *p, bool whole, int cols)
 {
     Chunk<XT> o;
     constexpr int NW = 2 * sizeof(XT);
-#pragma unroll
-    for (int i = 0; i < NW; i++) o.w[i] = 0u;
-    if (r >= a.rows || c >= a.cols) return o;
-    const XT *p = (const XT *)a.x + (long)r * a.ld + c;
-    if (c + 8 <= a.cols) {
+    if (whole) {
 #pragma unroll
         for (int i = 0; i < NW / 4; i++) {
             const uint4 q = ld_once16((const uint4 *)p + i);
             o.w[4 * i] = q.x, o.w[4 * i + 1] = q.y, o.w[4 * i + 2] = q.z, o.w[4 * i + 3] = q.w;
         }
-    } else {
+        return o;
+    }
+#pragma unroll
+    for (int i = 0; i < NW; i++) o.w[i] = 0u;
+    if (cols > 0) {
 #pragma unroll
         for (int i = 0; i < 8; i++)
-            if (c + i < a.cols) {
+            if (i < cols) {
                 if constexpr (sizeof(XT) == 2)
                     o.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
                 else
@@ -129,7 +129,7 @@ K3_DEV void chunk_values(const Chunk<XT> &q, float (&v)[8])
 // and the 16-byte stores of the first pass fall on distinct banks too.
 template <typename XT>
 constexpr int tile_pitch() { return sizeof(XT) == 2 ? 64 : 128; }
-constexpr int CODE_PITCH = 68;  // bytes of one column's staged codes (64, and 4 to spread the banks)
+constexpr int CODE_PITCH = 80;  // bytes of one column's staged codes (64, and 16 to spread the banks)
 template <typename XT>
 constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH; }
 
@@ -161,25 +161,31 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
             ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
         __syncthreads();
     }
+    // This thread's chunks: eight columns, rows rt, rt + 16, ... of the tile.
+    const int rt = tid >> 4, cc = tid & 15, rows_left = a.rows - r0 - rt, cols_left = a.cols - c0 - 8 * cc;
     const long rpitch = op_in_padded(a.cols) / 2;
+    const XT *px = (const XT *)a.x + (long)(r0 + rt) * a.ld + c0 + 8 * cc;
+    uint8_t *pc = a.rcodes + (long)(r0 + rt) * rpitch + c0 / 2 + 4 * cc;
+    uint32_t *pt = tile + rt * PITCH + cc * 2 * (int)sizeof(XT);
+    const bool code_cols = c0 + 8 * cc < op_in_padded(a.cols);
 #pragma unroll
     for (int it0 = 0; it0 < NIT; it0 += NB) {
         Chunk<XT> q[NB];
 #pragma unroll
-        for (int j = 0; j < NB; j++) {
-            const int c = (it0 + j) * Q_THREADS + tid;
+        for (int j = 0; j < NB; j++, px += 16 * a.ld) {
+            const bool row = 16 * (it0 + j) < rows_left;
             if constexpr (VEC)
-                q[j] = load_chunk<XT>(a, r0 + (c >> 4), c0 + 8 * (c & 15));
+                q[j] = load_chunk<XT>(px, row && cols_left >= 8, row ? cols_left : 0);
             else if (do_row)
-                q[j] = *(const Chunk<XT> *)(tile + (c >> 4) * PITCH + (c & 15) * 2 * (int)sizeof(XT));
+                q[j] = *(const Chunk<XT> *)(pt + 16 * (it0 + j) * PITCH);
         }
 #pragma unroll
-        for (int j = 0; j < NB; j++) {
-            const int c = (it0 + j) * Q_THREADS + tid, r = c >> 4, cc = c & 15;
+        for (int j = 0; j < NB; j++, pc += 16 * rpitch) {
+            const int i16 = it0 + j;  // row rt + 16 i16
             if (VEC && do_col) {
 #pragma unroll
                 for (int i = 0; i < (int)sizeof(XT) / 2; i++)
-                    *(uint4 *)(tile + r * PITCH + cc * 2 * (int)sizeof(XT) + 4 * i) =
+                    *(uint4 *)(pt + 16 * i16 * PITCH + 4 * i) =
                         make_uint4(q[j].w[4 * i], q[j].w[4 * i + 1], q[j].w[4 * i + 2], q[j].w[4 * i + 3]);
             }
             if (do_row) {
@@ -191,9 +197,9 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
                 float inv;
                 const uint32_t e = block_byte(mb, inv);
                 const uint32_t w = convert8(v, inv, e);
-                const bool in = r0 + r < a.rows && c0 + 8 * cc < op_in_padded(a.cols);
-                if (in) *(uint32_t *)(a.rcodes + (long)(r0 + r) * rpitch + c0 / 2 + 4 * cc) = w;
-                if ((cc & 3) == 0) ratom[op_atom_byte(r, cc >> 2)] = in ? (uint8_t)e : 0u;
+                const bool in = 16 * i16 < rows_left && code_cols;
+                if (in) *(uint32_t *)pc = w;
+                if ((cc & 3) == 0) ratom[16 * rt + (cc >> 2) + op_atom_byte(16 * i16, 0)] = in ? (uint8_t)e : 0u;
             }
         }
     }
@@ -226,12 +232,14 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
             const uint32_t mb = sizeof(XT) == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16;
             float inv;
             const uint32_t e = block_byte(mb, inv);
+            uint32_t w[4];
 #pragma unroll
             for (int g = 0; g < 4; g++) {
                 const float *vg = v + 8 * g;
                 const float v8[8] = {vg[0], vg[1], vg[2], vg[3], vg[4], vg[5], vg[6], vg[7]};
-                *(uint32_t *)(stage + c * CODE_PITCH + 16 * rb + 4 * g) = convert8(v8, inv, e);
+                w[g] = convert8(v8, inv, e);
             }
+            *(uint4 *)(stage + c * CODE_PITCH + 16 * rb) = make_uint4(w[0], w[1], w[2], w[3]);
             catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
         }
     }
@@ -240,11 +248,11 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
         ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid] = ((const uint32_t *)catom)[tid];
     const long cpitch = rpad / 2;
 #pragma unroll
-    for (int it = 0; it < QT * 16 / Q_THREADS; it++) {
-        const int i = it * Q_THREADS + tid, c = i >> 4, w = i & 15;  // 16 words per column
-        if (c0 + c < a.cols && r0 + 8 * w < rpad)
-            *(uint32_t *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 4 * w) =
-                *(const uint32_t *)(stage + c * CODE_PITCH + 4 * w);
+    for (int it = 0; it < QT * 4 / Q_THREADS; it++) {
+        const int i = it * Q_THREADS + tid, c = i >> 2, rb = i & 3;  // four blocks of 16 bytes per column
+        if (c0 + c < a.cols && r0 + 32 * rb < rpad)
+            *(uint4 *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 16 * rb) =
+                *(const uint4 *)(stage + c * CODE_PITCH + 16 * rb);
     }
 }
 
