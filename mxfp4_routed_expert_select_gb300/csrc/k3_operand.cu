@@ -29,7 +29,7 @@ constexpr int Q_THREADS = 256;
 struct QuantArgs {
     const void *x;
     long ld;
-    int rows, cols, tiles_x;
+    int rows, cols, tiles_x, tiles;
     uint8_t *rcodes, *ratoms;      // row form, or null
     uint8_t *ccodes, *catoms;      // column form, or null
 };
@@ -137,7 +137,7 @@ constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH;
 // aligned; else the tile comes in by single elements, neighbouring lanes on
 // neighbouring columns, through shared memory.
 template <typename XT, bool VEC>
-__global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantArgs a)
+__global__ void __launch_bounds__(Q_THREADS, 3) k3_mx_quantize_operand(const QuantArgs a)
 {
     extern __shared__ __align__(16) uint32_t tile[];
     __shared__ __align__(16) uint8_t ratom[512], catom[512];
@@ -145,114 +145,127 @@ __global__ void __launch_bounds__(Q_THREADS) k3_mx_quantize_operand(const QuantA
     constexpr int NIT = QT * (QT / 8) / Q_THREADS;       // chunks per thread
     constexpr int NB = sizeof(XT) == 2 ? NIT : NIT / 2;  // of them in flight at a time
     uint8_t *stage = (uint8_t *)(tile + QT * PITCH);
-    const int tid = threadIdx.x;
-    const int tx = blockIdx.x % a.tiles_x, ty = blockIdx.x / a.tiles_x;
-    const int r0 = ty * QT, c0 = tx * QT;
-    const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
+    const int tid = threadIdx.x, rt = tid >> 4, cc = tid & 15;  // chunk j: row rt + 16 j, columns 8 cc ..
+    uint32_t *pt = tile + rt * PITCH + cc * 2 * (int)sizeof(XT);
+    const long rpitch = op_in_padded(a.cols) / 2;
+    const int rpad = op_in_padded(a.rows);
+    Chunk<XT> q[NB];
+    // chunks j0 .. j0 + NB - 1 of tile t
+    auto load = [&](int t, int j0) {
+        const int r = (t / a.tiles_x) * QT + rt + 16 * j0, c = (t % a.tiles_x) * QT + 8 * cc;
+        const int rows_left = a.rows - r, cols_left = a.cols - c;
+        const XT *px = (const XT *)a.x + (long)r * a.ld + c;
+#pragma unroll
+        for (int j = 0; j < NB; j++, px += 16 * a.ld) {
+            const bool row = 16 * j < rows_left;
+            q[j] = load_chunk<XT>(px, row && cols_left >= 8, row ? cols_left : 0);
+        }
+    };
     griddep_launch_dependents();
     griddep_wait();
 
-    if constexpr (!VEC) {
-        const int c = tid & 127, rows = min(QT, a.rows - r0);
-        const XT *p = (const XT *)a.x + (long)r0 * a.ld + c0 + c;
-        const bool in = c0 + c < a.cols;
+    if (VEC) load(blockIdx.x, 0);
+    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
+        const int tx = t % a.tiles_x, ty = t / a.tiles_x, r0 = ty * QT, c0 = tx * QT;
+        const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
+        if constexpr (!VEC) {
+            const int c = tid & 127, rows = min(QT, a.rows - r0);
+            const XT *p = (const XT *)a.x + (long)r0 * a.ld + c0 + c;
+            const bool in = c0 + c < a.cols;
 #pragma unroll 16
-        for (int r = tid >> 7; r < QT; r += Q_THREADS / QT)
-            ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
+            for (int r = tid >> 7; r < QT; r += Q_THREADS / QT)
+                ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
+            __syncthreads();
+        }
+        const int rows_left = a.rows - r0 - rt;
+        const bool code_cols = c0 + 8 * cc < op_in_padded(a.cols);
+        uint8_t *pc = a.rcodes + (long)(r0 + rt) * rpitch + c0 / 2 + 4 * cc;
+#pragma unroll
+        for (int it0 = 0; it0 < NIT; it0 += NB) {
+            if constexpr (VEC) {
+                if (it0) load(t, it0);
+            } else if (do_row) {
+#pragma unroll
+                for (int j = 0; j < NB; j++) q[j] = *(const Chunk<XT> *)(pt + 16 * (it0 + j) * PITCH);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; j++, pc += 16 * rpitch) {
+                const int i16 = it0 + j;  // row rt + 16 i16
+                if (VEC && do_col) {
+#pragma unroll
+                    for (int i = 0; i < (int)sizeof(XT) / 2; i++)
+                        *(uint4 *)(pt + 16 * i16 * PITCH + 4 * i) =
+                            make_uint4(q[j].w[4 * i], q[j].w[4 * i + 1], q[j].w[4 * i + 2], q[j].w[4 * i + 3]);
+                }
+                if (do_row) {
+                    float v[8];
+                    chunk_values<XT>(q[j], v);
+                    uint32_t mb = absmax8(q[j].w);
+                    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
+                    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
+                    float inv;
+                    const uint32_t e = block_byte(mb, inv);
+                    const uint32_t w = convert8(v, inv, e);
+                    const bool in = 16 * i16 < rows_left && code_cols;
+                    if (in) *(uint32_t *)pc = w;
+                    if ((cc & 3) == 0) ratom[16 * rt + (cc >> 2) + op_atom_byte(16 * i16, 0)] = in ? (uint8_t)e : 0u;
+                }
+            }
+        }
+        // the next tile's loads are in flight during this one's column pass
+        if (VEC && t + (int)gridDim.x < a.tiles) load(t + gridDim.x, 0);
         __syncthreads();
-    }
-    // This thread's chunks: eight columns, rows rt, rt + 16, ... of the tile.
-    const int rt = tid >> 4, cc = tid & 15, rows_left = a.rows - r0 - rt, cols_left = a.cols - c0 - 8 * cc;
-    const long rpitch = op_in_padded(a.cols) / 2;
-    const XT *px = (const XT *)a.x + (long)(r0 + rt) * a.ld + c0 + 8 * cc;
-    uint8_t *pc = a.rcodes + (long)(r0 + rt) * rpitch + c0 / 2 + 4 * cc;
-    uint32_t *pt = tile + rt * PITCH + cc * 2 * (int)sizeof(XT);
-    const bool code_cols = c0 + 8 * cc < op_in_padded(a.cols);
+        if (do_row && tid < 128)
+            ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
+        if (do_col) {
+            // a task is one column's (fp32) or column pair's (bf16) 32 rows
+            constexpr int COLS = sizeof(XT) == 2 ? 2 : 1;   // columns per task
+            constexpr int WPR = QT / COLS;                  // tasks per row block
 #pragma unroll
-    for (int it0 = 0; it0 < NIT; it0 += NB) {
-        Chunk<XT> q[NB];
+            for (int i = 0; i < 4 * WPR / Q_THREADS; i++) {
+                const int task = i * Q_THREADS + tid, wc = task % WPR, rb = task / WPR;  // word column, row block
+                uint32_t raw[32], top = 0u;
 #pragma unroll
-        for (int j = 0; j < NB; j++, px += 16 * a.ld) {
-            const bool row = 16 * (it0 + j) < rows_left;
-            if constexpr (VEC)
-                q[j] = load_chunk<XT>(px, row && cols_left >= 8, row ? cols_left : 0);
-            else if (do_row)
-                q[j] = *(const Chunk<XT> *)(pt + 16 * (it0 + j) * PITCH);
-        }
+                for (int k = 0; k < 32; k++) {
+                    raw[k] = tile[(32 * rb + k) * PITCH + wc];
+                    top = sizeof(XT) == 2 ? absmax2(top, raw[k]) : absmax(top, raw[k]);
+                }
 #pragma unroll
-        for (int j = 0; j < NB; j++, pc += 16 * rpitch) {
-            const int i16 = it0 + j;  // row rt + 16 i16
-            if (VEC && do_col) {
+                for (int h = 0; h < COLS; h++) {
+                    const int c = COLS * wc + h;
+                    const uint32_t mb =
+                        sizeof(XT) == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16;
+                    float inv;
+                    const uint32_t e = block_byte(mb, inv);
+                    uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < (int)sizeof(XT) / 2; i++)
-                    *(uint4 *)(pt + 16 * i16 * PITCH + 4 * i) =
-                        make_uint4(q[j].w[4 * i], q[j].w[4 * i + 1], q[j].w[4 * i + 2], q[j].w[4 * i + 3]);
+                    for (int g = 0; g < 4; g++) {
+                        float v[8];
+#pragma unroll
+                        for (int k = 0; k < 8; k++) {
+                            const uint32_t x = raw[8 * g + k];
+                            v[k] = __uint_as_float(sizeof(XT) == 4 ? x : h ? (x & 0xffff0000u) : (x << 16));
+                        }
+                        w[g] = convert8(v, inv, e);
+                    }
+                    *(uint4 *)(stage + c * CODE_PITCH + 16 * rb) = make_uint4(w[0], w[1], w[2], w[3]);
+                    catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
+                }
             }
-            if (do_row) {
-                float v[8];
-                chunk_values<XT>(q[j], v);
-                uint32_t mb = absmax8(q[j].w);
-                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-                mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-                float inv;
-                const uint32_t e = block_byte(mb, inv);
-                const uint32_t w = convert8(v, inv, e);
-                const bool in = 16 * i16 < rows_left && code_cols;
-                if (in) *(uint32_t *)pc = w;
-                if ((cc & 3) == 0) ratom[16 * rt + (cc >> 2) + op_atom_byte(16 * i16, 0)] = in ? (uint8_t)e : 0u;
+            __syncthreads();
+            if (tid < 128)
+                ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid] =
+                    ((const uint32_t *)catom)[tid];
+            const long cpitch = rpad / 2;
+#pragma unroll
+            for (int i = 0; i < QT * 4 / Q_THREADS; i++) {
+                const int k = i * Q_THREADS + tid, c = k >> 2, rb = k & 3;  // four blocks of 16 bytes per column
+                if (c0 + c < a.cols && r0 + 32 * rb < rpad)
+                    *(uint4 *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 16 * rb) =
+                        *(const uint4 *)(stage + c * CODE_PITCH + 16 * rb);
             }
         }
-    }
-    if (!do_row && !do_col) return;
-    __syncthreads();
-    if (do_row && tid < 128)
-        ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
-    if (!do_col) return;
-
-    // columns: a task is one column's (fp32) or column pair's (bf16) 32 rows
-    const int rpad = op_in_padded(a.rows);
-    constexpr int COLS = sizeof(XT) == 2 ? 2 : 1;   // columns per task
-    constexpr int WPR = QT / COLS;                  // tasks per row block
-#pragma unroll
-    for (int t = tid; t < 4 * WPR; t += Q_THREADS) {
-        const int wc = t % WPR, rb = t / WPR;       // word column, row block
-        uint32_t raw[32], top = 0u;
-#pragma unroll
-        for (int i = 0; i < 32; i++) {
-            raw[i] = tile[(32 * rb + i) * PITCH + wc];
-            top = sizeof(XT) == 2 ? absmax2(top, raw[i]) : absmax(top, raw[i]);
-        }
-#pragma unroll
-        for (int h = 0; h < COLS; h++) {
-            const int c = COLS * wc + h;
-            float v[32];
-#pragma unroll
-            for (int i = 0; i < 32; i++)
-                v[i] = __uint_as_float(sizeof(XT) == 4 ? raw[i] : h ? (raw[i] & 0xffff0000u) : (raw[i] << 16));
-            const uint32_t mb = sizeof(XT) == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16;
-            float inv;
-            const uint32_t e = block_byte(mb, inv);
-            uint32_t w[4];
-#pragma unroll
-            for (int g = 0; g < 4; g++) {
-                const float *vg = v + 8 * g;
-                const float v8[8] = {vg[0], vg[1], vg[2], vg[3], vg[4], vg[5], vg[6], vg[7]};
-                w[g] = convert8(v8, inv, e);
-            }
-            *(uint4 *)(stage + c * CODE_PITCH + 16 * rb) = make_uint4(w[0], w[1], w[2], w[3]);
-            catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
-        }
-    }
-    __syncthreads();
-    if (tid < 128)
-        ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid] = ((const uint32_t *)catom)[tid];
-    const long cpitch = rpad / 2;
-#pragma unroll
-    for (int it = 0; it < QT * 4 / Q_THREADS; it++) {
-        const int i = it * Q_THREADS + tid, c = i >> 2, rb = i & 3;  // four blocks of 16 bytes per column
-        if (c0 + c < a.cols && r0 + 32 * rb < rpad)
-            *(uint4 *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 16 * rb) =
-                *(const uint4 *)(stage + c * CODE_PITCH + 16 * rb);
+        __syncthreads();  // the tile, its codes and atoms in shared memory are free
     }
 }
 
@@ -355,14 +368,15 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
     // the tiles cover every scale atom, the padding ones included
     a.tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
     const long tiles = (long)a.tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
-    if (tiles > 0x7fffffffL) return K3MOE_EINVAL;
+    if (tiles > 0x3fffffffL) return K3MOE_EINVAL;
+    a.tiles = (int)tiles;
     const bool vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
     const size_t sm = !col && vec ? 0 : xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
     void (*const kernel)(QuantArgs) =
         xdt == K3MOE_BF16 ? (vec ? k3_mx_quantize_operand<uint16_t, true> : k3_mx_quantize_operand<uint16_t, false>)
                           : (vec ? k3_mx_quantize_operand<uint32_t, true> : k3_mx_quantize_operand<uint32_t, false>);
     if (ensure_smem((const void *)kernel, sm) != K3MOE_OK) return K3MOE_ECUDA;
-    return launch_pdl(kernel, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a) == cudaSuccess
+    return launch_pdl(kernel, dim3((unsigned)std::min<long>(tiles, 3L * num_sms())), dim3(Q_THREADS), sm, s, a) == cudaSuccess
                ? K3MOE_OK
                : (cudaGetLastError(), K3MOE_ECUDA);
 }
