@@ -9,11 +9,14 @@
 // nearly even choice does not lose the gradient to cancellation.
 //
 // Bound: HBM for large batches (the logits are read once per direction),
-// latency for small ones.  A warp holds a row in registers (E <= 1024: at most 32
-// values a lane).  Forward: each warp sums its rows' p per expert in registers,
-// a CTA adds its warps' sums in shared memory in warp order, and the CTAs meet in
-// 64-bit fixed point (integer adds: the same result in any order); the last CTA
-// to arrive forms the loss and clears the workspace.  One launch per direction.
+// latency for small ones.  A warp holds a row in registers, expert
+// 128 i + 4 lane + c (E <= 1024: at most 32 values a lane), while its next row is
+// on the way into shared memory (cp.async; rows that are not made of aligned
+// 16-byte units are loaded directly).  Forward: each warp sums its rows' p per
+// expert in registers, a CTA adds its warps' sums in shared memory in warp order,
+// and the CTAs meet in 64-bit fixed point (integer adds: the same result in any
+// order); the last CTA to arrive forms the loss and clears the workspace.  One
+// launch per direction.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -50,6 +53,7 @@ struct BalanceArgs {
     const uint8_t *mask;
     int T, E, k, rule;
     float alpha;
+    bool vec, vec_out;  // rows of logits, of dlogits made of aligned 16-byte units
     // forward
     float *loss;
     int32_t *counts, *n_valid;
@@ -69,11 +73,12 @@ K3_DEV float load1(const void *p, long i)
         return ((const float *)p)[i];
 }
 
-K3_DEV float warp_max(float v)
+// Largest value, NaN if there is one.
+K3_DEV float max_nan(float a, float b)
 {
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-    return v;
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
 // sigma(l) / e^m without overflow or a row of zeros, for m = min(largest l, 0).
@@ -82,69 +87,133 @@ K3_DEV float scaled_sigmoid(float l, float m)
     return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - m) / (1.f + expf(l));
 }
 
-// Row t of the logits, v[i] = logit of expert lane + 32 i (-inf past E).
-// Returns whether the token is valid.  Afterwards v holds the unnormalised
-// probabilities and inv the factor that makes them sum to 1.
-template <typename T, int NC>
-K3_DEV bool row_probs(const BalanceArgs &a, int t, int lane, float (&v)[NC], float &m, float &inv)
+// Starts the copy of row t into a warp's buffer; one group per call.
+template <typename T>
+K3_DEV void fetch_row(const BalanceArgs &a, int t, bool on, uint8_t *buf, int lane)
 {
-    if (a.mask && !a.mask[t]) return false;
-    float mx = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < NC; i++) {
-        const int e = lane + 32 * i;
-        v[i] = e < a.E ? load1<T>(a.logits, (long)t * a.ld + e) : -INFINITY;
+    if (on) {
+        const uint8_t *src = (const uint8_t *)a.logits + (long)t * a.ld * (int)sizeof(T);
+        const int n16 = a.E * (int)sizeof(T) / 16;
+        for (int i = lane; i < n16; i += 32)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(buf + 16 * i)), "l"(src + 16 * i)
+                         : "memory");
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+// Row t into registers: v[4 i + c] = logit of expert 128 i + 4 lane + c, -inf past
+// E; from the warp's buffer (a.vec) or from global memory.
+template <typename T, int NV>
+K3_DEV void read_row(const BalanceArgs &a, int t, const uint8_t *buf, int lane, float (&v)[4 * NV])
+{
 #pragma unroll
-    for (int i = 0; i < NC; i++) {
-        mx = fmaxf(mx, v[i]);
-        nan |= v[i] != v[i];
+    for (int i = 0; i < NV; i++) {
+        const int e = 128 * i + 4 * lane;
+        if (a.vec) {
+            if (e < a.E) {  // E is a multiple of 4
+                if constexpr (sizeof(T) == 2) {
+                    const uint2 q = *(const uint2 *)(buf + 2 * e);
+                    v[4 * i] = __uint_as_float(q.x << 16);
+                    v[4 * i + 1] = __uint_as_float(q.x & 0xffff0000u);
+                    v[4 * i + 2] = __uint_as_float(q.y << 16);
+                    v[4 * i + 3] = __uint_as_float(q.y & 0xffff0000u);
+                } else {
+                    const float4 q = *(const float4 *)(buf + 4 * e);
+                    v[4 * i] = q.x, v[4 * i + 1] = q.y, v[4 * i + 2] = q.z, v[4 * i + 3] = q.w;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; c++) v[4 * i + c] = -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < 4; c++) v[4 * i + c] = e + c < a.E ? load1<T>(a.logits, (long)t * a.ld + e + c) : -INFINITY;
+        }
     }
-    mx = warp_max(mx);
-    if (mx == -INFINITY && !__any_sync(0xffffffffu, nan)) return false;
-    m = a.rule == K3MOE_ROUTER_SOFTMAX ? mx : fminf(mx, 0.f);
+}
+
+// Logits to unnormalised probabilities; inv makes them sum to 1.  False (and
+// nothing done) for a row of -inf.
+template <int NV>
+K3_DEV bool row_probs(const BalanceArgs &a, float (&v)[4 * NV], float &inv)
+{
+    float m = v[0];
+#pragma unroll
+    for (int i = 1; i < 4 * NV; i++) m = max_nan(m, v[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    if (m == -INFINITY) return false;
     float s = 0.f;
     if (a.rule == K3MOE_ROUTER_SOFTMAX) {
 #pragma unroll
-        for (int i = 0; i < NC; i++) s += v[i] = expf(v[i] - m);
+        for (int i = 0; i < 4 * NV; i++) s += v[i] = expf(v[i] - m);
     } else {
+        m = fminf(m, 0.f);  // a NaN among the logits is still in the sum
 #pragma unroll
-        for (int i = 0; i < NC; i++) s += v[i] = scaled_sigmoid(v[i], m);
+        for (int i = 0; i < 4 * NV; i++) s += v[i] = scaled_sigmoid(v[i], m);
     }
     inv = 1.f / warp_sum(s);
     return true;
 }
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(BL_THREADS) k3_balance_forward(const BalanceArgs a)
+// Bytes of a row's buffer.
+__host__ __device__ inline int row_buf(int E, int es) { return (E * es + 15) / 16 * 16; }
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const BalanceArgs a)
 {
-    __shared__ float part[BL_WARPS][32 * NC];
-    __shared__ unsigned cnt[32 * NC];
+    extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp; afterwards the warps' sums
+    __shared__ unsigned cnt[128 * NV];
     __shared__ unsigned nval, last;
-    __shared__ double red[BL_WARPS];
+    __shared__ float red[BL_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < 32 * NC; e += BL_THREADS) cnt[e] = 0u;
+    const int rb = row_buf(a.E, (int)sizeof(T));
+    uint8_t *buf = dyn + warp * 2 * rb;
+    for (int e = threadIdx.x; e < 128 * NV; e += BL_THREADS) cnt[e] = 0u;
     if (threadIdx.x == 0) nval = 0u;
     __syncthreads();
     griddep_launch_dependents();
     griddep_wait();
 
-    float acc[NC];
+    float acc[4 * NV];
 #pragma unroll
-    for (int i = 0; i < NC; i++) acc[i] = 0.f;
+    for (int i = 0; i < 4 * NV; i++) acc[i] = 0.f;
     unsigned mine = 0u;
-    for (int t = blockIdx.x * BL_WARPS + warp; t < a.T; t += gridDim.x * BL_WARPS) {
-        const int id = lane < a.k ? a.ids[(long)t * a.k + lane] : -1;
-        float v[NC], m, inv;
-        if (!row_probs<T, NC>(a, t, lane, v, m, inv)) continue;
-        mine++;
+    const int step = gridDim.x * BL_WARPS;
+    int t = blockIdx.x * BL_WARPS + warp, b = 0;
+    auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };
+    auto slot = [&](int r) { return lane < a.k && r < a.T ? a.ids[(long)r * a.k + lane] : -1; };
+    bool on = kept(t);
+    int id = slot(t);
+    if (a.vec) fetch_row<T>(a, t, on, buf, lane);
+    for (; t < a.T; t += step) {
+        const bool on_next = kept(t + step);
+        const int id_next = slot(t + step);
+        if (a.vec) {
+            fetch_row<T>(a, t + step, on_next, buf + (b ^ 1) * rb, lane);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+        }
+        if (on) {
+            float v[4 * NV], inv;
+            read_row<T, NV>(a, t, buf + b * rb, lane, v);
+            if (row_probs<NV>(a, v, inv)) {
+                mine++;
 #pragma unroll
-        for (int i = 0; i < NC; i++) acc[i] += v[i] * inv;
-        if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1u);
+                for (int i = 0; i < 4 * NV; i++) acc[i] += v[i] * inv;
+                if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1u);
+            }
+        }
+        __syncwarp();  // the buffer has been read before it is filled again
+        on = on_next, id = id_next, b ^= 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+    float *part = (float *)dyn;  // [warp][128 NV]
 #pragma unroll
-    for (int i = 0; i < NC; i++) part[warp][lane + 32 * i] = acc[i];
+    for (int i = 0; i < NV; i++)
+        *(float4 *)(part + warp * 128 * NV + 128 * i + 4 * lane) =
+            make_float4(acc[4 * i], acc[4 * i + 1], acc[4 * i + 2], acc[4 * i + 3]);
     if (lane == 0 && mine) atomicAdd(&nval, mine);
     __syncthreads();
     const BalanceWs ws = balance_ws(a.ws, a.E);
@@ -152,7 +221,7 @@ __global__ void __launch_bounds__(BL_THREADS) k3_balance_forward(const BalanceAr
     for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < BL_WARPS; w++) s += part[w][e];
+        for (int w = 0; w < BL_WARPS; w++) s += part[w * 128 * NV + e];
         // the sum is at most the CTA's tokens, the scaled one below 2^62
         if (s == s) {
             if (s != 0.f) atomicAdd(ws.sum + e, (unsigned long long)(s * unit));
@@ -167,26 +236,25 @@ __global__ void __launch_bounds__(BL_THREADS) k3_balance_forward(const BalanceAr
     __syncthreads();
     if (!last) return;
 
-    // the last CTA: the loss from the whole batch's sums, the workspace cleared
+    // the last CTA: the loss from the whole batch's sums, the workspace cleared.
+    // f_e P_e = E c_e / (k n) * sum / n in fp32, added in a fixed tree.
     const unsigned n = __ldcg(ws.valid);
-    const double unit2 = 1.0 / (double)unit;
-    double l = 0.0;
+    const float kn = (float)a.k * (float)n, pn = n ? 1.f / (unit * (float)n) : 0.f;
+    float l = 0.f;
     for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
         const unsigned c = __ldcg(ws.count + e);
-        l += (double)c * ((double)__ldcg(ws.sum + e) * unit2);
+        l += (float)c * ((float)__ldcg(ws.sum + e) * pn);
         a.counts[e] = (int32_t)c;
         ws.sum[e] = 0ull;
         ws.count[e] = 0u;
     }
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+    l = warp_sum(l);
     if (lane == 0) red[warp] = l;
     __syncthreads();
     if (threadIdx.x == 0) {
-        double s = 0.0;
+        float s = 0.f;
         for (int w = 0; w < BL_WARPS; w++) s += red[w];
-        const double nn = (double)n;
-        float loss = n ? (float)((double)a.alpha * a.E * s / ((double)a.k * nn * nn)) : 0.f;
+        float loss = n ? a.alpha * ((float)a.E * s / kn) : 0.f;
         if (__ldcg(ws.bad)) loss = __uint_as_float(0x7fc00000u);
         *a.loss = loss;
         *a.n_valid = (int32_t)n;
@@ -196,115 +264,176 @@ __global__ void __launch_bounds__(BL_THREADS) k3_balance_forward(const BalanceAr
     }
 }
 
-template <typename T, int NC>
-__global__ void __launch_bounds__(BL_THREADS) k3_balance_backward(const BalanceArgs a)
+template <typename T, int NV>
+__global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const BalanceArgs a)
 {
-    __shared__ float f1[32 * NC];                    // f_e - 1
-    __shared__ float extra[BL_WARPS][32 * NC];       // combine weights' part of a row
+    extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp, then [warp][128 NV]:
+    __shared__ __align__(16) float f1[128 * NV];    // f_e - 1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    for (int e = threadIdx.x; e < 32 * NC; e += BL_THREADS)
+    const int rb = row_buf(a.E, (int)sizeof(T));
+    uint8_t *buf = dyn + warp * 2 * rb;
+    float *extra = (float *)(dyn + BL_WARPS * 2 * rb) + warp * 128 * NV;  // combine weights' part of a row
 #pragma unroll
-        for (int w = 0; w < BL_WARPS; w++) extra[w][e] = 0.f;
+    for (int i = 0; i < NV; i++) *(float4 *)(extra + 128 * i + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
     griddep_launch_dependents();
     griddep_wait();
+    const int step = gridDim.x * BL_WARPS;
+    int t = blockIdx.x * BL_WARPS + warp, b = 0;
+    auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };
+    bool on = kept(t);
+    if (a.vec) fetch_row<T>(a, t, on, buf, lane);
     const int n = *a.n_valid;
     const long kn = (long)a.k * n;
-    for (int e = threadIdx.x; e < 32 * NC; e += BL_THREADS)
+    for (int e = threadIdx.x; e < 128 * NV; e += BL_THREADS)
         f1[e] = e < a.E && n > 0 ? (float)((long)a.E * a.counts[e] - kn) / (float)kn : 0.f;
     __syncthreads();
     const float scale = n > 0 ? a.alpha * *a.dloss / (float)n : 0.f;
 
-    for (int t = blockIdx.x * BL_WARPS + warp; t < a.T; t += gridDim.x * BL_WARPS) {
-        float v[NC], m = 0.f, inv = 0.f;
+    for (; t < a.T; t += step) {
+        const bool on_next = kept(t + step);
         int id = -1;
-        float w = 0.f, dw = 0.f, lj = 0.f;
-        if (a.dw && lane < a.k) {
+        float w = 0.f, dw = 0.f;
+        if (a.dw && on && lane < a.k) {
             id = a.ids[(long)t * a.k + lane];
             w = a.w[(long)t * a.k + lane];
             dw = a.dw[(long)t * a.k + lane];
             if (id < 0 || id >= a.E) id = -1;
-            if (id >= 0 && a.rule != K3MOE_ROUTER_SOFTMAX) lj = load1<T>(a.logits, (long)t * a.ld + id);
         }
-        const bool on = row_probs<T, NC>(a, t, lane, v, m, inv);
+        if (a.vec) {
+            fetch_row<T>(a, t + step, on_next, buf + (b ^ 1) * rb, lane);
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            __syncwarp();
+        }
+        float v[4 * NV], inv;
+        bool valid = on;
         if (on) {
-            float dot = 0.f;
+            // logits of the chosen experts, before any lane may write the row
+            float lj = 0.f;
+            if (id >= 0 && a.rule != K3MOE_ROUTER_SOFTMAX)
+                lj = a.vec ? load1<T>(buf + b * rb, id) : load1<T>(a.logits, (long)t * a.ld + id);
+            read_row<T, NV>(a, t, buf + b * rb, lane, v);
+            valid = row_probs<NV>(a, v, inv);
+            if (valid) {
+                float dot = 0.f;
 #pragma unroll
-            for (int i = 0; i < NC; i++) {
-                v[i] *= inv;
-                dot += v[i] * f1[lane + 32 * i];
-            }
-            dot = warp_sum(dot);
-#pragma unroll
-            for (int i = 0; i < NC; i++) v[i] = scale * v[i] * (f1[lane + 32 * i] - dot);
-            if (a.rule != K3MOE_ROUTER_SOFTMAX) {
-                // 1 - sigma(l) as sigma(-l), which keeps its digits for large l
-#pragma unroll
-                for (int i = 0; i < NC; i++)
-                    if (lane + 32 * i < a.E)
-                        v[i] *= 1.f / (1.f + expf(load1<T>(a.logits, (long)t * a.ld + lane + 32 * i)));
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < NC; i++) v[i] = 0.f;
-        }
-        if (a.dw && on) {
-            const float inner = warp_sum(id >= 0 ? w * dw : 0.f);
-            float c;
-            if (a.rule == K3MOE_ROUTER_SOFTMAX) {
-                c = w * (dw - inner);
-            } else {
-                const float r = 1.f / (1.f + expf(lj));  // 1 - sigma
-                c = a.rule == K3MOE_ROUTER_SIGMOID ? router_sigmoid(lj) * r * dw : w * r * (dw - inner);
-            }
-            // slots with the same id are added in slot order by the first
-            const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
-            if (__any_sync(0xffffffffu, __popc(same) > 1)) {
-                float s = 0.f;
-                for (int j = 0; j < a.k; j++) {
-                    const float cj = __shfl_sync(0xffffffffu, c, j);
-                    if ((same >> j) & 1u) s += cj;
+                for (int i = 0; i < NV; i++) {
+                    const float4 f = *(const float4 *)(f1 + 128 * i + 4 * lane);
+                    v[4 * i] *= inv, v[4 * i + 1] *= inv, v[4 * i + 2] *= inv, v[4 * i + 3] *= inv;
+                    dot += v[4 * i] * f.x + v[4 * i + 1] * f.y + v[4 * i + 2] * f.z + v[4 * i + 3] * f.w;
                 }
-                c = s;
-            }
-            const bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
-            if (first) extra[warp][id] = c;
-            __syncwarp();
+                dot = warp_sum(dot);
 #pragma unroll
-            for (int i = 0; i < NC; i++) v[i] += extra[warp][lane + 32 * i];
-            __syncwarp();
-            if (first) extra[warp][id] = 0.f;
-        }
+                for (int i = 0; i < NV; i++) {
+                    const float4 f = *(const float4 *)(f1 + 128 * i + 4 * lane);
+                    v[4 * i] *= scale * (f.x - dot), v[4 * i + 1] *= scale * (f.y - dot);
+                    v[4 * i + 2] *= scale * (f.z - dot), v[4 * i + 3] *= scale * (f.w - dot);
+                }
+                if (a.rule != K3MOE_ROUTER_SOFTMAX) {
+                    // 1 - sigma(l) as sigma(-l), which keeps its digits for large l
+                    float l[4 * NV];
+                    read_row<T, NV>(a, t, buf + b * rb, lane, l);
 #pragma unroll
-        for (int i = 0; i < NC; i++) {
-            const int e = lane + 32 * i;
-            if (e < a.E) {
-                if constexpr (sizeof(T) == 2)
-                    ((__nv_bfloat16 *)a.dlogits)[(long)t * a.ldd + e] = __float2bfloat16_rn(v[i]);
-                else
-                    ((float *)a.dlogits)[(long)t * a.ldd + e] = v[i];
+                    for (int i = 0; i < 4 * NV; i++) v[i] *= 1.f / (1.f + expf(l[i]));
+                }
+                if (a.dw) {
+                    const float inner = warp_sum(id >= 0 ? w * dw : 0.f);
+                    float c;
+                    if (a.rule == K3MOE_ROUTER_SOFTMAX) {
+                        c = w * (dw - inner);
+                    } else {
+                        const float r = 1.f / (1.f + expf(lj));  // 1 - sigma
+                        c = a.rule == K3MOE_ROUTER_SIGMOID ? router_sigmoid(lj) * r * dw : w * r * (dw - inner);
+                    }
+                    // slots with the same id are added in slot order by the first
+                    const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
+                    if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+                        float s = 0.f;
+                        for (int j = 0; j < a.k; j++) {
+                            const float cj = __shfl_sync(0xffffffffu, c, j);
+                            if ((same >> j) & 1u) s += cj;
+                        }
+                        c = s;
+                    }
+                    const bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
+                    if (first) extra[id] = c;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < NV; i++) {
+                        const float4 x = *(const float4 *)(extra + 128 * i + 4 * lane);
+                        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
+                    }
+                    __syncwarp();
+                    if (first) extra[id] = 0.f;
+                }
             }
         }
+        if (!valid) {
+#pragma unroll
+            for (int i = 0; i < 4 * NV; i++) v[i] = 0.f;
+        }
+        T *o = (T *)a.dlogits + (long)t * a.ldd;
+#pragma unroll
+        for (int i = 0; i < NV; i++) {
+            const int e = 128 * i + 4 * lane;
+            if (a.vec_out) {
+                if (e < a.E) {
+                    if constexpr (sizeof(T) == 2) {
+                        const __nv_bfloat162 lo = __floats2bfloat162_rn(v[4 * i], v[4 * i + 1]),
+                                             hi = __floats2bfloat162_rn(v[4 * i + 2], v[4 * i + 3]);
+                        *(uint2 *)(o + e) = make_uint2(*(const uint32_t *)&lo, *(const uint32_t *)&hi);
+                    } else {
+                        *(float4 *)(o + e) = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 4; c++)
+                    if (e + c < a.E) {
+                        if constexpr (sizeof(T) == 2)
+                            o[e + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v[4 * i + c]));
+                        else
+                            o[e + c] = v[4 * i + c];
+                    }
+            }
+        }
+        __syncwarp();  // the buffer has been read before it is filled again
+        on = on_next, b ^= 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int NC>
+template <typename T, int NV>
 int launch(const BalanceArgs &a, bool backward, cudaStream_t s)
 {
     const dim3 grid((unsigned)std::max(1, std::min((a.T + BL_WARPS - 1) / BL_WARPS, 2 * num_sms())));
-    const cudaError_t e = backward ? launch_pdl(k3_balance_backward<T, NC>, grid, dim3(BL_THREADS), 0, s, a)
-                                   : launch_pdl(k3_balance_forward<T, NC>, grid, dim3(BL_THREADS), 0, s, a);
-    return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
+    const size_t bufs = (size_t)BL_WARPS * 2 * row_buf(a.E, (int)sizeof(T));
+    const size_t sums = sizeof(float) * BL_WARPS * 128 * NV;
+    const size_t smem = backward ? bufs + sums : std::max(bufs, sums);
+    const auto kernel = backward ? k3_balance_backward<T, NV> : k3_balance_forward<T, NV>;
+    // the static arrays count towards the limit too
+    if (ensure_smem((const void *)kernel, smem + 8192) != K3MOE_OK) return K3MOE_ECUDA;
+    return launch_pdl(kernel, grid, dim3(BL_THREADS), smem, s, a) == cudaSuccess ? K3MOE_OK
+                                                                                 : (cudaGetLastError(), K3MOE_ECUDA);
 }
-// Values a lane holds: the next of 4, 8, 16, 24, 32 (a row of E experts).
+// A lane holds four values per 128 experts.
 template <typename T>
 int launch_e(const BalanceArgs &a, bool backward, cudaStream_t s)
 {
-    const int nc = (a.E + 31) / 32;
-    if (nc <= 4) return launch<T, 4>(a, backward, s);
-    if (nc <= 8) return launch<T, 8>(a, backward, s);
-    if (nc <= 16) return launch<T, 16>(a, backward, s);
-    if (nc <= 24) return launch<T, 24>(a, backward, s);
-    return launch<T, 32>(a, backward, s);
+    switch ((a.E + 127) / 128) {
+    case 1: return launch<T, 1>(a, backward, s);
+    case 2: return launch<T, 2>(a, backward, s);
+    case 3: return launch<T, 3>(a, backward, s);
+    case 4: return launch<T, 4>(a, backward, s);
+    case 5: return launch<T, 5>(a, backward, s);
+    case 6: return launch<T, 6>(a, backward, s);
+    case 7: return launch<T, 7>(a, backward, s);
+    default: return launch<T, 8>(a, backward, s);
+    }
+}
+// Rows made of aligned 16-byte units.
+bool rows16(const void *p, long ld, int E, int es)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld * es % 16 == 0 && E * es % 16 == 0;
 }
 int launch_dt(const BalanceArgs &a, int dtype, bool backward, cudaStream_t s)
 {
@@ -323,6 +452,7 @@ int launch_balance_forward(float *loss, int32_t *counts, int32_t *n_valid, const
     a.logits = logits, a.ld = ld, a.ids = ids, a.mask = mask;
     a.T = T, a.E = E, a.k = k, a.rule = rule, a.alpha = alpha;
     a.loss = loss, a.counts = counts, a.n_valid = n_valid, a.ws = ws;
+    a.vec = rows16(logits, ld, E, dtype == K3MOE_BF16 ? 2 : 4);
     a.shift = 61;  // T 2^shift < 2^62
     while (a.shift > 46 || ((long)T >> (62 - a.shift)) != 0) a.shift--;
     return launch_dt(a, dtype, false, s);
@@ -335,6 +465,8 @@ int launch_balance_backward(void *dlogits, long ldd, const void *logits, int dty
     a.logits = logits, a.ld = ld, a.ldd = ldd, a.ids = ids, a.mask = mask;
     a.T = T, a.E = E, a.k = k, a.rule = rule, a.alpha = alpha;
     a.counts = (int32_t *)counts, a.n_valid = (int32_t *)n_valid;
+    a.vec = rows16(logits, ld, E, dtype == K3MOE_BF16 ? 2 : 4);
+    a.vec_out = rows16(dlogits, ldd, E, dtype == K3MOE_BF16 ? 2 : 4);
     a.dlogits = dlogits, a.dloss = dloss, a.w = w, a.dw = dw;
     return launch_dt(a, dtype, true, s);
 }

@@ -446,29 +446,27 @@ class BalanceLoss:
             raise K3Error(K3MOE_EINVAL, "BalanceLoss(E=%d)" % E)
         self.E, self.k, self.alpha, self.rule = E, top_k, alpha, self.RULES[rule]
         self.workspace = torch.zeros(n, dtype=torch.uint8, device=device)
+        self._ws = self.workspace.data_ptr(), n
+        self._f32, self._i32, self._u8 = torch.float32, torch.int32, torch.uint8
 
     def forward(self, loss, counts, n_valid, logits, ids, mask=None, stream=None):
         """loss fp32 [1], counts int32 [E], n_valid int32 [1] of logits [T][E],
         ids int32 [T][top_k], mask uint8 [T]."""
-        import torch
-        T, E = logits.shape[0], self.E
+        T, E, k, i32 = logits.shape[0], self.E, self.k, self._i32
         check(lib().k3moe_balance_forward(
-            _flat(loss, torch.float32, 1), _flat(counts, torch.int32, E), _flat(n_valid, torch.int32, 1),
-            logits.data_ptr(), _dtype(logits), _ld(logits, T, E), _flat(ids, torch.int32, T, self.k),
-            _flat(mask, torch.uint8, T), T, E, self.k, self.alpha, self.rule, self.workspace.data_ptr(),
-            self.workspace.numel(), _stream(stream)), "k3moe_balance_forward")
+            _flat(loss, self._f32, 1), _flat(counts, i32, E), _flat(n_valid, i32, 1), logits.data_ptr(),
+            _dtype(logits), _ld(logits, T, E), _flat(ids, i32, T, k), _flat(mask, self._u8, T), T, E, k, self.alpha,
+            self.rule, *self._ws, _stream(stream)), "k3moe_balance_forward")
 
     def backward(self, dlogits, logits, ids, counts, n_valid, dloss, mask=None, w=None, dw=None, stream=None):
         """dlogits [T][E] from dloss fp32 [1] and, with the combine weights w and
         their gradients dw (fp32 [T][top_k]), the weight rule's part."""
-        import torch
-        T, E = logits.shape[0], self.E
+        T, E, k, f32, i32 = logits.shape[0], self.E, self.k, self._f32, self._i32
         check(lib().k3moe_balance_backward(
             dlogits.data_ptr(), _ld(dlogits, T, E), logits.data_ptr(), _dtype(logits, dlogits), _ld(logits, T, E),
-            _flat(ids, torch.int32, T, self.k), _flat(mask, torch.uint8, T), _flat(counts, torch.int32, E),
-            _flat(n_valid, torch.int32, 1), _flat(dloss, torch.float32, 1), _flat(w, torch.float32, T, self.k),
-            _flat(dw, torch.float32, T, self.k), T, E, self.k, self.alpha, self.rule, _stream(stream)),
-            "k3moe_balance_backward")
+            _flat(ids, i32, T, k), _flat(mask, self._u8, T), _flat(counts, i32, E), _flat(n_valid, i32, 1),
+            _flat(dloss, f32, 1), _flat(w, f32, T, k), _flat(dw, f32, T, k), T, E, k, self.alpha, self.rule,
+            _stream(stream)), "k3moe_balance_backward")
 
 
 def expert_gemv_noalloc(y, x, expert, d, f, stream=None):
