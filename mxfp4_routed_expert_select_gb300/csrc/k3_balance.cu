@@ -73,6 +73,9 @@ K3_DEV float load1(const void *p, long i)
         return ((const float *)p)[i];
 }
 
+K3_DEV void put1(uint16_t *o, int e, float v) { o[e] = __bfloat16_as_ushort(__float2bfloat16_rn(v)); }
+K3_DEV void put1(float *o, int e, float v) { o[e] = v; }
+
 // Largest value, NaN if there is one.
 K3_DEV float max_nan(float a, float b)
 {
@@ -132,10 +135,27 @@ K3_DEV void read_row(const BalanceArgs &a, int t, const uint8_t *buf, int lane, 
     }
 }
 
+// 2^x, relative error 2^-22.
+K3_DEV float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 // Logits to unnormalised probabilities; inv makes them sum to 1.  False (and
-// nothing done) for a row of -inf.
-template <int NV>
-K3_DEV bool row_probs(const BalanceArgs &a, float (&v)[4 * NV], float &inv)
+// nothing done) for a row of -inf.  SIG: the sigmoid rules.
+// Softmax: e^(l - m) as 2^(l log2 e - m log2 e), the product exact in the fused
+// step: the rounding of m log2 e is one factor of the whole row, and that of the
+// exponent t costs p at most t 2^-24, so at most 2^-24 of the row's largest p.
+constexpr float LOG2E = 1.44269504088896340736f;
+template <bool SIG>
+K3_DEV float unnormalised(float l, float shift)
+{
+    return SIG ? scaled_sigmoid(l, shift) : exp2_fast(__fmaf_rn(l, LOG2E, shift));
+}
+template <int NV, bool SIG>
+K3_DEV bool row_probs(float (&v)[4 * NV], float &inv, float &shift)
 {
     float m = v[0];
 #pragma unroll
@@ -143,15 +163,13 @@ K3_DEV bool row_probs(const BalanceArgs &a, float (&v)[4 * NV], float &inv)
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (m == -INFINITY) return false;
+    if constexpr (SIG)
+        shift = fminf(m, 0.f);  // a NaN among the logits is still in the sum
+    else
+        shift = m == INFINITY ? __uint_as_float(0x7fc00000u) : -m * LOG2E;  // inf - inf
     float s = 0.f;
-    if (a.rule == K3MOE_ROUTER_SOFTMAX) {
 #pragma unroll
-        for (int i = 0; i < 4 * NV; i++) s += v[i] = expf(v[i] - m);
-    } else {
-        m = fminf(m, 0.f);  // a NaN among the logits is still in the sum
-#pragma unroll
-        for (int i = 0; i < 4 * NV; i++) s += v[i] = scaled_sigmoid(v[i], m);
-    }
+    for (int i = 0; i < 4 * NV; i++) s += v[i] = unnormalised<SIG>(v[i], shift);
     inv = 1.f / warp_sum(s);
     return true;
 }
@@ -159,7 +177,7 @@ K3_DEV bool row_probs(const BalanceArgs &a, float (&v)[4 * NV], float &inv)
 // Bytes of a row's buffer.
 __host__ __device__ inline int row_buf(int E, int es) { return (E * es + 15) / 16 * 16; }
 
-template <typename T, int NV>
+template <typename T, int NV, bool SIG>
 __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const BalanceArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp; afterwards the warps' sums
@@ -183,11 +201,12 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
     int t = blockIdx.x * BL_WARPS + warp, b = 0;
     auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };
     auto slot = [&](int r) { return lane < a.k && r < a.T ? a.ids[(long)r * a.k + lane] : -1; };
-    bool on = kept(t);
+    // the mask is read two rows ahead, the row and its ids one
+    bool on = kept(t), on_next = kept(t + step);
     int id = slot(t);
     if (a.vec) fetch_row<T>(a, t, on, buf, lane);
     for (; t < a.T; t += step) {
-        const bool on_next = kept(t + step);
+        const bool on_later = kept(t + 2 * step);
         const int id_next = slot(t + step);
         if (a.vec) {
             fetch_row<T>(a, t + step, on_next, buf + (b ^ 1) * rb, lane);
@@ -195,9 +214,9 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
             __syncwarp();
         }
         if (on) {
-            float v[4 * NV], inv;
+            float v[4 * NV], inv, shift;
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
-            if (row_probs<NV>(a, v, inv)) {
+            if (row_probs<NV, SIG>(v, inv, shift)) {
                 mine++;
 #pragma unroll
                 for (int i = 0; i < 4 * NV; i++) acc[i] += v[i] * inv;
@@ -205,7 +224,7 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
             }
         }
         __syncwarp();  // the buffer has been read before it is filled again
-        on = on_next, id = id_next, b ^= 1;
+        on = on_next, on_next = on_later, id = id_next, b ^= 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
@@ -264,24 +283,37 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
     }
 }
 
-template <typename T, int NV>
-__global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const BalanceArgs a)
+template <typename T, int NV, bool SIG>
+__global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const BalanceArgs a)
 {
-    extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp, then [warp][128 NV]:
+    extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp
     __shared__ __align__(16) float f1[128 * NV];    // f_e - 1
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rb = row_buf(a.E, (int)sizeof(T));
     uint8_t *buf = dyn + warp * 2 * rb;
-    float *extra = (float *)(dyn + BL_WARPS * 2 * rb) + warp * 128 * NV;  // combine weights' part of a row
-#pragma unroll
-    for (int i = 0; i < NV; i++) *(float4 *)(extra + 128 * i + 4 * lane) = make_float4(0.f, 0.f, 0.f, 0.f);
     griddep_launch_dependents();
     griddep_wait();
     const int step = gridDim.x * BL_WARPS;
     int t = blockIdx.x * BL_WARPS + warp, b = 0;
     auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };
-    bool on = kept(t);
+    // a row's chosen experts, one per lane, with their weights and gradients
+    struct Slot {
+        int id;
+        float w, dw;
+    };
+    auto slot = [&](int r) {
+        Slot s = {-1, 0.f, 0.f};
+        if (a.dw && lane < a.k && r < a.T) {
+            const long i = (long)r * a.k + lane;
+            s = {a.ids[i], a.w[i], a.dw[i]};
+            if (s.id < 0 || s.id >= a.E) s.id = -1;
+        }
+        return s;
+    };
+    // the mask is read two rows ahead, the row and its slots one
+    bool on = kept(t), on_next = kept(t + step);
     if (a.vec) fetch_row<T>(a, t, on, buf, lane);
+    Slot sl = slot(t);
     const int n = *a.n_valid;
     const long kn = (long)a.k * n;
     for (int e = threadIdx.x; e < 128 * NV; e += BL_THREADS)
@@ -290,62 +322,46 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const Balan
     const float scale = n > 0 ? a.alpha * *a.dloss / (float)n : 0.f;
 
     for (; t < a.T; t += step) {
-        const bool on_next = kept(t + step);
-        int id = -1;
-        float w = 0.f, dw = 0.f;
-        if (a.dw && on && lane < a.k) {
-            id = a.ids[(long)t * a.k + lane];
-            w = a.w[(long)t * a.k + lane];
-            dw = a.dw[(long)t * a.k + lane];
-            if (id < 0 || id >= a.E) id = -1;
-        }
+        const bool on_later = kept(t + 2 * step);
+        const Slot next = slot(t + step);
         if (a.vec) {
             fetch_row<T>(a, t + step, on_next, buf + (b ^ 1) * rb, lane);
             asm volatile("cp.async.wait_group 1;" ::: "memory");
             __syncwarp();
         }
-        float v[4 * NV], inv;
-        bool valid = on;
+        T *o = (T *)a.dlogits + (long)t * a.ldd;
+        float v[4 * NV], inv, shift;
+        bool valid = on, first = false;
+        float at = 0.f;  // the whole gradient of this lane's chosen expert
         if (on) {
-            // logits of the chosen experts, before any lane may write the row
+            // logit of the chosen expert, before any lane may write the row
             float lj = 0.f;
-            if (id >= 0 && a.rule != K3MOE_ROUTER_SOFTMAX)
-                lj = a.vec ? load1<T>(buf + b * rb, id) : load1<T>(a.logits, (long)t * a.ld + id);
+            if (sl.id >= 0) lj = a.vec ? load1<T>(buf + b * rb, sl.id) : load1<T>(a.logits, (long)t * a.ld + sl.id);
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
-            valid = row_probs<NV>(a, v, inv);
+            valid = row_probs<NV, SIG>(v, inv, shift);
             if (valid) {
-                float dot = 0.f;
+                float dot = 0.f;  // <f - 1, unnormalised p>
 #pragma unroll
                 for (int i = 0; i < NV; i++) {
                     const float4 f = *(const float4 *)(f1 + 128 * i + 4 * lane);
-                    v[4 * i] *= inv, v[4 * i + 1] *= inv, v[4 * i + 2] *= inv, v[4 * i + 3] *= inv;
                     dot += v[4 * i] * f.x + v[4 * i + 1] * f.y + v[4 * i + 2] * f.z + v[4 * i + 3] * f.w;
                 }
-                dot = warp_sum(dot);
-#pragma unroll
-                for (int i = 0; i < NV; i++) {
-                    const float4 f = *(const float4 *)(f1 + 128 * i + 4 * lane);
-                    v[4 * i] *= scale * (f.x - dot), v[4 * i + 1] *= scale * (f.y - dot);
-                    v[4 * i + 2] *= scale * (f.z - dot), v[4 * i + 3] *= scale * (f.w - dot);
-                }
-                if (a.rule != K3MOE_ROUTER_SOFTMAX) {
-                    // 1 - sigma(l) as sigma(-l), which keeps its digits for large l
-                    float l[4 * NV];
-                    read_row<T, NV>(a, t, buf + b * rb, lane, l);
-#pragma unroll
-                    for (int i = 0; i < 4 * NV; i++) v[i] *= 1.f / (1.f + expf(l[i]));
-                }
+                // p scale (f - <f, p>)
+                const float c1 = scale * inv, c0 = -warp_sum(dot) * inv * c1;
                 if (a.dw) {
-                    const float inner = warp_sum(id >= 0 ? w * dw : 0.f);
+                    const float inner = warp_sum(sl.id >= 0 ? sl.w * sl.dw : 0.f);
                     float c;
-                    if (a.rule == K3MOE_ROUTER_SOFTMAX) {
-                        c = w * (dw - inner);
-                    } else {
+                    if constexpr (SIG) {
                         const float r = 1.f / (1.f + expf(lj));  // 1 - sigma
-                        c = a.rule == K3MOE_ROUTER_SIGMOID ? router_sigmoid(lj) * r * dw : w * r * (dw - inner);
+                        c = a.rule == K3MOE_ROUTER_SIGMOID ? router_sigmoid(lj) * r * sl.dw
+                                                           : sl.w * r * (sl.dw - inner);
+                        at = r;
+                    } else {
+                        c = sl.w * (sl.dw - inner);
+                        at = 1.f;
                     }
                     // slots with the same id are added in slot order by the first
-                    const unsigned same = __match_any_sync(0xffffffffu, id >= 0 ? id : -1 - lane);
+                    const unsigned same = __match_any_sync(0xffffffffu, sl.id >= 0 ? sl.id : -1 - lane);
                     if (__any_sync(0xffffffffu, __popc(same) > 1)) {
                         float s = 0.f;
                         for (int j = 0; j < a.k; j++) {
@@ -354,16 +370,21 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const Balan
                         }
                         c = s;
                     }
-                    const bool first = id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
-                    if (first) extra[id] = c;
-                    __syncwarp();
+                    first = sl.id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
+                    at = unnormalised<SIG>(lj, shift) * (f1[max(sl.id, 0)] * c1 + c0) * at + c;
+                }
 #pragma unroll
-                    for (int i = 0; i < NV; i++) {
-                        const float4 x = *(const float4 *)(extra + 128 * i + 4 * lane);
-                        v[4 * i] += x.x, v[4 * i + 1] += x.y, v[4 * i + 2] += x.z, v[4 * i + 3] += x.w;
-                    }
-                    __syncwarp();
-                    if (first) extra[id] = 0.f;
+                for (int i = 0; i < NV; i++) {
+                    const float4 f = *(const float4 *)(f1 + 128 * i + 4 * lane);
+                    v[4 * i] *= f.x * c1 + c0, v[4 * i + 1] *= f.y * c1 + c0;
+                    v[4 * i + 2] *= f.z * c1 + c0, v[4 * i + 3] *= f.w * c1 + c0;
+                }
+                if constexpr (SIG) {
+                    // 1 - sigma(l) as sigma(-l), which keeps its digits for large l
+                    float l[4 * NV];
+                    read_row<T, NV>(a, t, buf + b * rb, lane, l);
+#pragma unroll
+                    for (int i = 0; i < 4 * NV; i++) v[i] *= 1.f / (1.f + expf(l[i]));
                 }
             }
         }
@@ -371,7 +392,6 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const Balan
 #pragma unroll
             for (int i = 0; i < 4 * NV; i++) v[i] = 0.f;
         }
-        T *o = (T *)a.dlogits + (long)t * a.ldd;
 #pragma unroll
         for (int i = 0; i < NV; i++) {
             const int e = 128 * i + 4 * lane;
@@ -388,47 +408,42 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_backward(const Balan
             } else {
 #pragma unroll
                 for (int c = 0; c < 4; c++)
-                    if (e + c < a.E) {
-                        if constexpr (sizeof(T) == 2)
-                            o[e + c] = __bfloat16_as_ushort(__float2bfloat16_rn(v[4 * i + c]));
-                        else
-                            o[e + c] = v[4 * i + c];
-                    }
+                    if (e + c < a.E) put1(o, e + c, v[4 * i + c]);
             }
         }
-        __syncwarp();  // the buffer has been read before it is filled again
-        on = on_next, b ^= 1;
+        // the row is stored (and the buffer read, before it is filled again); the
+        // chosen experts' entries are stored over it
+        __syncwarp();
+        if (first) put1(o, sl.id, at);
+        on = on_next, on_next = on_later, sl = next, b ^= 1;
     }
     asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int NV>
+template <typename T, int NV, bool SIG>
 int launch(const BalanceArgs &a, bool backward, cudaStream_t s)
 {
-    const dim3 grid((unsigned)std::max(1, std::min((a.T + BL_WARPS - 1) / BL_WARPS, 2 * num_sms())));
+    const dim3 grid((unsigned)std::max(1, std::min((a.T + BL_WARPS - 1) / BL_WARPS, (backward ? 3 : 2) * num_sms())));
     const size_t bufs = (size_t)BL_WARPS * 2 * row_buf(a.E, (int)sizeof(T));
-    const size_t sums = sizeof(float) * BL_WARPS * 128 * NV;
-    const size_t smem = backward ? bufs + sums : std::max(bufs, sums);
-    const auto kernel = backward ? k3_balance_backward<T, NV> : k3_balance_forward<T, NV>;
+    const size_t smem = backward ? bufs : std::max(bufs, sizeof(float) * BL_WARPS * 128 * NV);
+    const auto kernel = backward ? k3_balance_backward<T, NV, SIG> : k3_balance_forward<T, NV, SIG>;
     // the static arrays count towards the limit too
     if (ensure_smem((const void *)kernel, smem + 8192) != K3MOE_OK) return K3MOE_ECUDA;
     return launch_pdl(kernel, grid, dim3(BL_THREADS), smem, s, a) == cudaSuccess ? K3MOE_OK
                                                                                  : (cudaGetLastError(), K3MOE_ECUDA);
 }
 // A lane holds four values per 128 experts.
-template <typename T>
+template <typename T, bool SIG, int NV = 1>
 int launch_e(const BalanceArgs &a, bool backward, cudaStream_t s)
 {
-    switch ((a.E + 127) / 128) {
-    case 1: return launch<T, 1>(a, backward, s);
-    case 2: return launch<T, 2>(a, backward, s);
-    case 3: return launch<T, 3>(a, backward, s);
-    case 4: return launch<T, 4>(a, backward, s);
-    case 5: return launch<T, 5>(a, backward, s);
-    case 6: return launch<T, 6>(a, backward, s);
-    case 7: return launch<T, 7>(a, backward, s);
-    default: return launch<T, 8>(a, backward, s);
-    }
+    if constexpr (NV < 8)
+        if (a.E > 128 * NV) return launch_e<T, SIG, NV + 1>(a, backward, s);
+    return launch<T, NV, SIG>(a, backward, s);
+}
+template <typename T>
+int launch_rule(const BalanceArgs &a, bool backward, cudaStream_t s)
+{
+    return a.rule == K3MOE_ROUTER_SOFTMAX ? launch_e<T, false>(a, backward, s) : launch_e<T, true>(a, backward, s);
 }
 // Rows made of aligned 16-byte units.
 bool rows16(const void *p, long ld, int E, int es)
@@ -437,7 +452,7 @@ bool rows16(const void *p, long ld, int E, int es)
 }
 int launch_dt(const BalanceArgs &a, int dtype, bool backward, cudaStream_t s)
 {
-    return dtype == K3MOE_BF16 ? launch_e<uint16_t>(a, backward, s) : launch_e<float>(a, backward, s);
+    return dtype == K3MOE_BF16 ? launch_rule<uint16_t>(a, backward, s) : launch_rule<float>(a, backward, s);
 }
 
 }  // namespace
