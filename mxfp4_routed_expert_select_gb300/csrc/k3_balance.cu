@@ -27,7 +27,10 @@
 namespace k3 {
 namespace {
 
-constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;
+constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;  // backward: three CTAs per SM
+// Forward: one CTA per SM, so that half as many sums meet in global atomics as
+// with two of 256 threads.
+constexpr int BF_THREADS = 512, BF_WARPS = BF_THREADS / 32;
 
 // Workspace: fixed-point sums [E], counts [E], valid tokens, a flag for
 // non-finite sums, the ticket.
@@ -178,16 +181,16 @@ K3_DEV bool row_probs(float (&v)[4 * NV], float &inv, float &shift)
 __host__ __device__ inline int row_buf(int E, int es) { return (E * es + 15) / 16 * 16; }
 
 template <typename T, int NV, bool SIG>
-__global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const BalanceArgs a)
+__global__ void __launch_bounds__(BF_THREADS, 1) k3_balance_forward(const BalanceArgs a)
 {
     extern __shared__ __align__(16) uint8_t dyn[];  // two row buffers per warp; afterwards the warps' sums
     __shared__ unsigned cnt[128 * NV];
     __shared__ unsigned nval, last;
-    __shared__ float red[BL_WARPS];
+    __shared__ float red[BF_WARPS];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rb = row_buf(a.E, (int)sizeof(T));
     uint8_t *buf = dyn + warp * 2 * rb;
-    for (int e = threadIdx.x; e < 128 * NV; e += BL_THREADS) cnt[e] = 0u;
+    for (int e = threadIdx.x; e < 128 * NV; e += BF_THREADS) cnt[e] = 0u;
     if (threadIdx.x == 0) nval = 0u;
     __syncthreads();
     griddep_launch_dependents();
@@ -197,8 +200,8 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
 #pragma unroll
     for (int i = 0; i < 4 * NV; i++) acc[i] = 0.f;
     unsigned mine = 0u;
-    const int step = gridDim.x * BL_WARPS;
-    int t = blockIdx.x * BL_WARPS + warp, b = 0;
+    const int step = gridDim.x * BF_WARPS;
+    int t = blockIdx.x * BF_WARPS + warp, b = 0;
     auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };
     auto slot = [&](int r) { return lane < a.k && r < a.T ? a.ids[(long)r * a.k + lane] : -1; };
     // the mask is read two rows ahead, the row and its ids one
@@ -237,10 +240,10 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
     __syncthreads();
     const BalanceWs ws = balance_ws(a.ws, a.E);
     const float unit = __uint_as_float((uint32_t)(127 + a.shift) << 23);
-    for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
+    for (int e = threadIdx.x; e < a.E; e += BF_THREADS) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < BL_WARPS; w++) s += part[w * 128 * NV + e];
+        for (int w = 0; w < BF_WARPS; w++) s += part[w * 128 * NV + e];
         // the sum is at most the CTA's tokens, the scaled one below 2^62
         if (s == s) {
             if (s != 0.f) atomicAdd(ws.sum + e, (unsigned long long)(s * unit));
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
     const unsigned n = __ldcg(ws.valid);
     const float kn = (float)a.k * (float)n, pn = n ? 1.f / (unit * (float)n) : 0.f;
     float l = 0.f;
-    for (int e = threadIdx.x; e < a.E; e += BL_THREADS) {
+    for (int e = threadIdx.x; e < a.E; e += BF_THREADS) {
         const unsigned c = __ldcg(ws.count + e);
         l += (float)c * ((float)__ldcg(ws.sum + e) * pn);
         a.counts[e] = (int32_t)c;
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(BL_THREADS, 2) k3_balance_forward(const Balanc
     __syncthreads();
     if (threadIdx.x == 0) {
         float s = 0.f;
-        for (int w = 0; w < BL_WARPS; w++) s += red[w];
+        for (int w = 0; w < BF_WARPS; w++) s += red[w];
         float loss = n ? a.alpha * ((float)a.E * s / kn) : 0.f;
         if (__ldcg(ws.bad)) loss = __uint_as_float(0x7fc00000u);
         *a.loss = loss;
@@ -423,13 +426,14 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
 template <typename T, int NV, bool SIG>
 int launch(const BalanceArgs &a, bool backward, cudaStream_t s)
 {
-    const dim3 grid((unsigned)std::max(1, std::min((a.T + BL_WARPS - 1) / BL_WARPS, (backward ? 3 : 2) * num_sms())));
-    const size_t bufs = (size_t)BL_WARPS * 2 * row_buf(a.E, (int)sizeof(T));
-    const size_t smem = backward ? bufs : std::max(bufs, sizeof(float) * BL_WARPS * 128 * NV);
+    const int threads = backward ? BL_THREADS : BF_THREADS, warps = threads / 32;
+    const dim3 grid((unsigned)std::max(1, std::min((a.T - 1) / warps + 1, (backward ? 3 : 1) * num_sms())));
+    const size_t bufs = (size_t)warps * 2 * row_buf(a.E, (int)sizeof(T));
+    const size_t smem = backward ? bufs : std::max(bufs, sizeof(float) * warps * 128 * NV);
     const auto kernel = backward ? k3_balance_backward<T, NV, SIG> : k3_balance_forward<T, NV, SIG>;
     // the static arrays count towards the limit too
     if (ensure_smem((const void *)kernel, smem + 8192) != K3MOE_OK) return K3MOE_ECUDA;
-    return launch_pdl(kernel, grid, dim3(BL_THREADS), smem, s, a) == cudaSuccess ? K3MOE_OK
+    return launch_pdl(kernel, grid, dim3((unsigned)threads), smem, s, a) == cudaSuccess ? K3MOE_OK
                                                                                  : (cudaGetLastError(), K3MOE_ECUDA);
 }
 // A lane holds four values per 128 experts.
