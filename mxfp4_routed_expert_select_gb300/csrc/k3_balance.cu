@@ -22,7 +22,7 @@
 #include <algorithm>
 
 #include "k3_launch.cuh"
-#include "k3_device.cuh"
+#include "k3_operand.cuh"
 
 namespace k3 {
 namespace {
@@ -138,20 +138,11 @@ K3_DEV void read_row(const BalanceArgs &a, int t, const uint8_t *buf, int lane, 
     }
 }
 
-// 2^x, relative error 2^-22.
-K3_DEV float exp2_fast(float x)
-{
-    float r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // Logits to unnormalised probabilities; inv makes them sum to 1.  False (and
 // nothing done) for a row of -inf.  SIG: the sigmoid rules.
 // Softmax: e^(l - m) as 2^(l log2 e - m log2 e), the product exact in the fused
 // step: the rounding of m log2 e is one factor of the whole row, and that of the
 // exponent t costs p at most t 2^-24, so at most 2^-24 of the row's largest p.
-constexpr float LOG2E = 1.44269504088896340736f;
 template <bool SIG>
 K3_DEV float unnormalised(float l, float shift)
 {

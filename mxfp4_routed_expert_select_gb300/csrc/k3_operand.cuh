@@ -21,6 +21,22 @@ K3_DEV float op_scale(uint32_t e)
     return __uint_as_float(e == 255u ? 0x7fc00000u : e == 0u ? 0x00400000u : e << 23);
 }
 
+// 2^x (relative error 2^-22) and 1 / x (2^-23), results below 2^-126 as 0: one
+// instruction each, where the forms that keep such results take four.
+K3_DEV float exp2_fast(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+K3_DEV float rcp_fast(float x)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LOG2E = 1.44269504088896340736f;
+
 // The larger magnitude (its sign is not meaningful); NaN if either is.
 K3_DEV uint32_t absmax(uint32_t a, uint32_t b)
 {

@@ -153,12 +153,12 @@ K3_DEV void from_e4m3x8(uint2 q, uint32_t e, float (&v)[8])
     }
 }
 // sigma(g); 0 where e^-g overflows.  bf16 data (2^-8) takes the fast exponential
-// (2^-19 over the range where sigma matters): with the full one the forward pass
-// was bound by issue.
+// (an argument rounded to 2^-24 of itself: 2^-19 of sigma over the range where it
+// matters): with the full one the forward pass was bound by issue.
 template <typename T>
 K3_DEV float sigmoid(float g)
 {
-    return __fdividef(1.f, 1.f + (sizeof(T) == 2 ? __expf(-g) : expf(-g)));
+    return rcp_fast(1.f + (sizeof(T) == 2 ? exp2_fast(-LOG2E * g) : expf(-g)));
 }
 
 // Chunk i of a launch as (row, column); past the end the column is f.
