@@ -76,8 +76,8 @@ __host__ __device__ constexpr uint32_t mg_idesc(int m, int n, uint32_t sfid)
 //   sf         TMEM column of the stage's scales: the lanes' in 8 columns, the
 //              columns' in 8 per 128 rows, k-atom major
 //   shift      first scale word of the columns' rows within their atoms
-// QT: row tiles of the columns' atoms; GRP: cta_group (2: each CTA of a pair copies
-// its own atoms to its own TMEM).
+// GRP: cta_group.  1: one row tile of column atoms; 2: two, and each CTA of the pair
+// copies its own atoms to its own TMEM.
 #define MG_HEAD                                                                                              \
     "{\n\t.reg .pred p, t, e;\n\t.reg .b64 d, da, db;\n\t.reg .b32 x, y, z;\n\t"                              \
     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %7, %7;\n\tadd.u32 z, %4, %5;\n\t"
@@ -92,19 +92,15 @@ __host__ __device__ constexpr uint32_t mg_idesc(int m, int n, uint32_t sfid)
     ::"r"(tacc), "r"(slo), "r"(tlo), "r"(sal), "r"(sf), "r"(shift), "r"(acc), "r"(mg_idesc(M, NT, 0)), "r"(AHI),     \
         "r"(SW128_HI), "r"(mg_idesc(M, NT, 2))                                                               \
         : "memory"
-template <int GRP, int NT, int QT>
+template <int GRP, int NT>
 K3_DEV void mg_step(uint32_t tacc, uint32_t slo, uint32_t tlo, uint32_t sal, uint32_t sf, uint32_t shift, uint32_t acc)
 {
     constexpr uint32_t AHI = (128u >> 4) | (1u << 14);  // atoms: 8 rows of 16 bytes 128 bytes apart, no swizzle
     constexpr int M = GRP * MG_M;
-    if constexpr (GRP == 2 && QT == 2)
+    if constexpr (GRP == 2)
         asm volatile(MG_HEAD MG_CP(2, 0, 0) MG_CP(2, 4, 32) MG_CP(2, 8, 64) MG_CP(2, 12, 128) MG_CP(2, 16, 96)
                          MG_CP(2, 20, 160) MG_MMA(2, 0, 0, 8, "%7", "p") MG_MMA(2, 2, 0, 8, "%10", "t")
                              MG_MMA(2, 4, 4, 16, "%7", "t") MG_MMA(2, 6, 4, 16, "%10", "t") "}" MG_OPERANDS);
-    else if constexpr (GRP == 2)
-        asm volatile(MG_HEAD MG_CP(2, 0, 0) MG_CP(2, 4, 32) MG_CP(2, 8, 64) MG_CP(2, 12, 96)
-                         MG_MMA(2, 0, 0, 8, "%7", "p") MG_MMA(2, 2, 0, 8, "%10", "t") MG_MMA(2, 4, 4, 12, "%7", "t")
-                             MG_MMA(2, 6, 4, 12, "%10", "t") "}" MG_OPERANDS);
     else
         asm volatile(MG_HEAD MG_CP(1, 0, 0) MG_CP(1, 4, 32) MG_CP(1, 8, 64) MG_CP(1, 12, 96)
                          MG_MMA(1, 0, 0, 8, "%7", "p") MG_MMA(1, 2, 0, 8, "%10", "t") MG_MMA(1, 4, 4, 12, "%7", "t")
@@ -409,7 +405,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // look at the next stage while this one is issued
                 ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
-                mg_step<1, NT, 1>(tmem + (uint32_t)(buf * NT), slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
+                mg_step<1, NT>(tmem + (uint32_t)(buf * NT), slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
                                   slo + C::OFF_SA / 16 + (uint32_t)s * SD, tmem + (uint32_t)(C::SF0 + C::SF * s), 0u,
                                   ks > k0 ? 1u : 0u);
                 mma_commit(bar(B_EMPTY + s));
@@ -503,7 +499,7 @@ constexpr int MP_BOX = 4096;  // bytes of a staged piece of C: 32 rows of 128 by
 
 template <int NT>
 struct MpCfg {
-    static constexpr int QT = NT == 128 ? 1 : 2;      // row tiles of B's scale atoms per tile (192: from a half tile)
+    static constexpr int QT = 2;                      // row tiles of B's scale atoms per tile (192: from a half tile)
     static constexpr int S_BYTES = MG_M * 128, T_BYTES = NT / 2 * 128;
     static constexpr int OFF_T = S_BYTES;
     static constexpr int OFF_SA = OFF_T + T_BYTES;    // this CTA's two A atoms
@@ -730,7 +726,7 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // look at the next stage while this one is issued
                 ready = __all_sync(0xffffffffu, mbar_test_cluster(bar(B_FULL + sn), pn));
-                mg_step<2, NT, C::QT>(tacc, slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
+                mg_step<2, NT>(tacc, slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
                                       slo + C::OFF_SA / 16 + (uint32_t)s * SD, tmem + (uint32_t)(C::SF0 + C::SF * s),
                                       shift, ks ? 1u : 0u);
                 mp_commit(bar(B_EMPTY + s));
@@ -960,29 +956,38 @@ struct MgPlan {
     int nt, ranks;
 };
 
-// Up to 128 rows of A one column tile holds them all, on single CTAs.  Above
-// that, pairs where the tiles fill them: the fewest bytes into an SM over the
-// waves of 128, 192 or 256 columns (a step brings 16 KB of A, 64 bytes per row
-// of B and 2 or 3 KB of scales), ties to the wider tile.  Single tiles that leave
-// SMs idle are split along K while every rank keeps two steps.
+// The form by a model of its time in ns, fitted on one GB300 to products of 1 to
+// 8192 rows, 1000 to 20000 columns and K 256 to 8192 (each predicted within 15%):
+//  - tiles: a wave of one tile per SM takes 223 a k-step and 700 for its epilogue
+//  - pairs: 1000 more to start, 1100 a wave's epilogue, and 335 or 272 a step with
+//    256 or 192 columns (bytes into an SM): ahead from two waves of single tiles on (2048 x 1536 x 7168 13.1 against 16.1 us; but 1536 x 1536 x
+//    7168, one wave, 11.8 against 9.5)
+//  - split (up to 128 rows of A, one column tile): 170 a step of the longest rank
+//    and the joining of the ranks' sums, which grows with the columns (1 x 1536 x
+//    7168 4.0 against 7.3 us whole; 333 x 1000 x 1112 6.8 against 5.4)
 MgPlan choose_plan(int M, int N, int nks, int sms)
 {
-    if (M > 128) {
-        const long tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M), pairs = std::max(1, sms / 2);
-        long best = 0;
-        int nt = 0;
-        for (int w : {256, 192, 128}) {
-            const long tiles = tm * (((long)N + w - 1) / w);
-            const long cost = (tiles + pairs - 1) / pairs * (16 + w / 16 + (w == 128 ? 2 : 3));
-            if (!nt || cost < best) best = cost, nt = w;
+    const long tn = ((long)N + MG_M - 1) / MG_M;
+    if (M <= 128) {
+        MgPlan best = {false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
+        const long join = best.nt == 16 ? 700 : best.nt == 32 ? 900 : best.nt == 64 ? 1500 : 3000;
+        long cost = 170L * nks;
+        for (int r = 2; r <= MG_MAX_RANKS && r <= nks && tn * r <= 2L * sms; r *= 2) {
+            const long c = 170L * ((nks + r - 1) / r) + join;
+            if (c < cost) cost = c, best.ranks = r;
         }
-        const long single = (((long)N + MG_M - 1) / MG_M) * ((M + 127) / 128);
-        if (2 * single > sms) return {true, nt, 1};
+        return best;
     }
-    MgPlan p = {false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
-    const long tiles = (((long)N + MG_M - 1) / MG_M) * ((M + p.nt - 1) / p.nt);
-    while (p.ranks < MG_MAX_RANKS && tiles * p.ranks * 2 <= 2L * sms && nks >= 4 * p.ranks) p.ranks *= 2;
-    return p;
+    const auto waves = [](long tiles, long at_once) { return (tiles + at_once - 1) / at_once; };
+    MgPlan best = {false, 128, 1};
+    long cost = waves(tn * (((long)M + 127) / 128), sms) * (223L * nks + 700);
+    const long tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M);
+    for (int w : {256, 192}) {
+        const long step = w == 256 ? 335 : 272;
+        const long c = 1000 + waves(tm * (((long)N + w - 1) / w), std::max(1, sms / 2)) * (step * nks + 1100);
+        if (c < cost) cost = c, best = {true, w, 1};
+    }
+    return best;
 }
 
 template <typename CT>
@@ -990,9 +995,7 @@ int launch_ct(const k3moe_mx_operand *A, const k3moe_mx_operand *B, const MgArgs
 {
     const MgPlan p = choose_plan(a.M, a.N, a.nks, num_sms());
     if (p.pair)
-        return p.nt == 256   ? launch_pair<256, CT>(A, B, a, s)
-               : p.nt == 192 ? launch_pair<192, CT>(A, B, a, s)
-                             : launch_pair<128, CT>(A, B, a, s);
+        return p.nt == 256 ? launch_pair<256, CT>(A, B, a, s) : launch_pair<192, CT>(A, B, a, s);
     switch (p.nt) {
     case 16: return launch_nt<16, CT>(A, B, a, p.ranks, s);
     case 32: return launch_nt<32, CT>(A, B, a, p.ranks, s);

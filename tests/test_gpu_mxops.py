@@ -285,7 +285,9 @@ def test_other_stream_and_graph():
 
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K,pad", [(2048, 1537, 160, 0), (1100, 3333, 512, 3), (4096, 1000, 288, 8), (3000, 2064, 64, 0),
-                                       (257, 12000, 1056, 1), (2500, 1300, 1, 4)])
+                                       (257, 12000, 1056, 1), (2500, 1300, 1, 4), (4096, 1537, 2100, 0),
+                                       (2300, 3333, 1500, 3), (1500, 7001, 900, 8), (2500, 7168, 260, 0),
+                                       (9000, 5000, 96, 0), (3001, 4600, 1056, 2)])
 def test_matmul_pairs(M, N, K, pad, out):
     """Products large enough for CTA pairs: rows of C aligned for wide stores or
     not, ragged row and column tiles of every width, a K of one block and less."""
@@ -309,10 +311,10 @@ def test_matmul_pairs(M, N, K, pad, out):
 def test_matmul_nan_stays_in_its_rows_and_columns():
     """Non-finite blocks in a CTA-pair product reach their own row and column only
     (tiles reach past the matrices, and the tail of K past the blocks)."""
-    M, N, K = 1030, 5000, 96
+    M, N, K = 2050, 5000, 2000
     x, w = _x(M, K, torch.float32, 1), _x(N, K, torch.float32, 2)
     x[700, 40] = float("nan")
-    w[4999, 95] = float("inf")
+    w[4999, 1999] = float("inf")
     A, B, C = k.MxOperand(M, K), k.MxOperand(N, K), torch.empty(M, N, device="cuda")
     k.mx_quantize_operand(x, A)
     k.mx_quantize_operand(w, B)
