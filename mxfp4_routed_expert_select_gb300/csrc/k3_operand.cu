@@ -8,11 +8,13 @@
 // OCP Microscaling v1.0 conversion, as k3moe_mx_quantize).  The scaling is a
 // power of two, so the conversion instruction's rounding is the only one.
 //
-// Bound: HBM.  A 128 x 128 tile is read once, converted along its rows from
-// registers (four lanes hold a block; two shuffles find its maximum) and, for
-// the column form, along its columns from shared memory, where a lane walks
-// the 32 values of a block without bank conflicts.  Both forms' codes leave as
-// 64-byte runs and their scale bytes as whole 512-byte atoms.
+// Bound: HBM, and close behind it issue (about ten instructions per value for both
+// forms).  A 128 x 128 tile is copied once into shared memory (cp.async, zero past
+// the matrix) and converted from there along its rows and along its columns; a
+// thread holds a whole block of 32, so that its maximum needs no exchange and its
+// codes leave as 16 bytes.  Row pitches and the order of a thread's reads keep the
+// banks apart.  Both forms' codes leave in 64-byte runs and their scale bytes as
+// whole 512-byte atoms.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -29,7 +31,7 @@ constexpr int Q_THREADS = 256;
 struct QuantArgs {
     const void *x;
     long ld;
-    int rows, cols, tiles_x, tiles;
+    int rows, cols, tiles_x;
     uint8_t *rcodes, *ratoms;      // row form, or null
     uint8_t *ccodes, *catoms;      // column form, or null
 };
@@ -67,205 +69,155 @@ K3_DEV uint32_t convert8(const float (&v)[8], float inv, uint32_t e)
     return e == 255u ? 0u : codes8(a);  // a non-finite block: codes 0
 }
 
-// Sixteen bytes that this kernel reads once.  Not the read-only (nc) path: as
-// a programmatic dependent the kernel may have started before its input was
-// written.
-K3_DEV uint4 ld_once16(const void *p)
+// 16 bytes to shared memory, the first n of them from p (zero past those).
+K3_DEV void copy16(uint32_t dst, const void *p, int n)
 {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
 }
 
-// Eight values of a row.
+// Words per tile row in shared memory: 64 words of two bf16 columns or 128 of one
+// fp32 column, and 4 that move each row on by 16 bytes of banks.
 template <typename XT>
-struct alignas(16) Chunk {
-    uint32_t w[2 * sizeof(XT)];
-};
-// From p (16-byte aligned if whole), the first `cols` of them, zero past those.
-template <typename XT>
-K3_DEV Chunk<XT> load_chunk(const XT *p, bool whole, int cols)
-{
-    Chunk<XT> o;
-    constexpr int NW = 2 * sizeof(XT);
-    if (whole) {
-#pragma unroll
-        for (int i = 0; i < NW / 4; i++) {
-            const uint4 q = ld_once16((const uint4 *)p + i);
-            o.w[4 * i] = q.x, o.w[4 * i + 1] = q.y, o.w[4 * i + 2] = q.z, o.w[4 * i + 3] = q.w;
-        }
-        return o;
-    }
-#pragma unroll
-    for (int i = 0; i < NW; i++) o.w[i] = 0u;
-    if (cols > 0) {
-#pragma unroll
-        for (int i = 0; i < 8; i++)
-            if (i < cols) {
-                if constexpr (sizeof(XT) == 2)
-                    o.w[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-                else
-                    o.w[i] = p[i];
-            }
-    }
-    return o;
-}
-template <typename XT>
-K3_DEV void chunk_values(const Chunk<XT> &q, float (&v)[8])
-{
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        if constexpr (sizeof(XT) == 2)
-            v[i] = __uint_as_float((i & 1) ? (q.w[i >> 1] & 0xffff0000u) : (q.w[i >> 1] << 16));
-        else
-            v[i] = __uint_as_float(q.w[i]);
-    }
-}
-
-// Words per tile row in shared memory.  bf16: 64 words of two columns; fp32:
-// 128 words.  The column pass reads 32 consecutive words of one row per warp,
-// and the 16-byte stores of the first pass fall on distinct banks too.
-template <typename XT>
-constexpr int tile_pitch() { return sizeof(XT) == 2 ? 64 : 128; }
+constexpr int tile_pitch() { return QT * (int)sizeof(XT) / 4 + 4; }
 constexpr int CODE_PITCH = 80;  // bytes of one column's staged codes (64, and 16 to spread the banks)
 template <typename XT>
 constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH; }
 
 // XT: uint16_t (bf16 bits) or uint32_t (fp32 bits).  VEC: rows are 16-byte
 // aligned; else the tile comes in by single elements, neighbouring lanes on
-// neighbouring columns, through shared memory.
+// neighbouring columns.
 template <typename XT, bool VEC>
-__global__ void __launch_bounds__(Q_THREADS, 3) k3_mx_quantize_operand(const QuantArgs a)
+__global__ void __launch_bounds__(Q_THREADS, sizeof(XT) == 2 ? 4 : 2) k3_mx_quantize_operand(const QuantArgs a)
 {
     extern __shared__ __align__(16) uint32_t tile[];
     __shared__ __align__(16) uint8_t ratom[512], catom[512];
-    constexpr int PITCH = tile_pitch<XT>();
-    constexpr int NIT = QT * (QT / 8) / Q_THREADS;       // chunks per thread
-    constexpr int NB = sizeof(XT) == 2 ? NIT : NIT / 2;  // of them in flight at a time
+    constexpr int PITCH = tile_pitch<XT>(), ES = (int)sizeof(XT);
     uint8_t *stage = (uint8_t *)(tile + QT * PITCH);
-    const int tid = threadIdx.x, rt = tid >> 4, cc = tid & 15;  // chunk j: row rt + 16 j, columns 8 cc ..
-    uint32_t *pt = tile + rt * PITCH + cc * 2 * (int)sizeof(XT);
-    const long rpitch = op_in_padded(a.cols) / 2;
-    const int rpad = op_in_padded(a.rows);
-    Chunk<XT> q[NB];
-    // chunks j0 .. j0 + NB - 1 of tile t
-    auto load = [&](int t, int j0) {
-        const int r = (t / a.tiles_x) * QT + rt + 16 * j0, c = (t % a.tiles_x) * QT + 8 * cc;
-        const int rows_left = a.rows - r, cols_left = a.cols - c;
-        const XT *px = (const XT *)a.x + (long)r * a.ld + c;
-#pragma unroll
-        for (int j = 0; j < NB; j++, px += 16 * a.ld) {
-            const bool row = 16 * j < rows_left;
-            q[j] = load_chunk<XT>(px, row && cols_left >= 8, row ? cols_left : 0);
-        }
-    };
+    const int tid = threadIdx.x;
+    const int tx = blockIdx.x % a.tiles_x, ty = blockIdx.x / a.tiles_x;
+    const int r0 = ty * QT, c0 = tx * QT;
+    const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
     griddep_launch_dependents();
     griddep_wait();
+    if (!do_row && !do_col) return;
 
-    if (VEC) load(blockIdx.x, 0);
-    for (int t = blockIdx.x; t < a.tiles; t += gridDim.x) {
-        const int tx = t % a.tiles_x, ty = t / a.tiles_x, r0 = ty * QT, c0 = tx * QT;
-        const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
-        if constexpr (!VEC) {
-            const int c = tid & 127, rows = min(QT, a.rows - r0);
-            const XT *p = (const XT *)a.x + (long)r0 * a.ld + c0 + c;
-            const bool in = c0 + c < a.cols;
+    if constexpr (VEC) {
+        constexpr int CPR = QT * ES / 16, RS = Q_THREADS / CPR;  // 16-byte units per row, rows per pass
+        const int u = tid % CPR, r = tid / CPR;
+        const int bytes = min(max((a.cols - c0) * ES - 16 * u, 0), 16);
+        const XT *p = (const XT *)a.x + (long)(r0 + r) * a.ld + c0 + u * (16 / ES);
+        uint32_t dst = smem_u32(tile + r * PITCH + 4 * u);
+#pragma unroll
+        for (int i = 0; i < QT / RS; i++) {
+            const bool in = bytes > 0 && r0 + r + i * RS < a.rows;
+            copy16(dst + (uint32_t)(i * RS * PITCH * 4), in ? p + (long)(i * RS) * a.ld : (const XT *)a.x, in ? bytes : 0);
+        }
+        asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
+    } else {
+        const int c = tid & 127, rows = min(QT, a.rows - r0);
+        const XT *p = (const XT *)a.x + (long)r0 * a.ld + c0 + c;
+        const bool in = c0 + c < a.cols;
 #pragma unroll 16
-            for (int r = tid >> 7; r < QT; r += Q_THREADS / QT)
-                ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
-            __syncthreads();
+        for (int r = tid >> 7; r < QT; r += Q_THREADS / QT)
+            ((XT *)(tile + r * PITCH))[c] = in && r < rows ? p[(long)r * a.ld] : (XT)0;
+    }
+    __syncthreads();
+
+    if (do_row) {
+        // a task is a row's block; four lanes take a row's four.  Their reads go
+        // round the block from a quarter that differs between them (ROT words of
+        // codes on), so that eight lanes' 16-byte reads fall on distinct banks.
+        const long rpitch = op_in_padded(a.cols) / 2;
+        const int b = tid & 3, rot = ES == 2 ? 2 * (b >> 1) : b;
+        const bool block = c0 + 32 * b < op_in_padded(a.cols);
+#pragma unroll
+        for (int i = 0; i < QT * 4 / Q_THREADS; i++) {
+            const int r = i * (Q_THREADS / 4) + (tid >> 2);
+            constexpr int NW = 32 * ES / 4;  // words of a block
+            uint32_t q[NW];
+            const uint32_t *p = tile + r * PITCH + NW * b;
+#pragma unroll
+            for (int k = 0; k < NW / 4; k++) {
+                // quarters of the block (8 values: ES / 2 reads each), rotated
+                const uint4 v = *(const uint4 *)(p + 4 * ((k + rot * (ES / 2)) & (NW / 4 - 1)));
+                q[4 * k] = v.x, q[4 * k + 1] = v.y, q[4 * k + 2] = v.z, q[4 * k + 3] = v.w;
+            }
+            uint32_t top = q[0];
+#pragma unroll
+            for (int k = 1; k < NW; k++) top = ES == 2 ? absmax2(top, q[k]) : absmax(top, q[k]);
+            top = ES == 2 ? max(top & 0x7fff0000u, (top & 0x7fffu) << 16) : top & 0x7fffffffu;
+            float inv;
+            const uint32_t e = block_byte(top, inv);
+            uint32_t w[4];
+#pragma unroll
+            for (int g = 0; g < 4; g++) {
+                float v[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    v[k] = __uint_as_float(ES == 4            ? q[8 * g + k]
+                                           : (k & 1) ? (q[4 * g + (k >> 1)] & 0xffff0000u)
+                                                     : (q[4 * g + (k >> 1)] << 16));
+                w[g] = convert8(v, inv, e);
+            }
+            // back to the block's order: word g holds quarter (g + rot) mod 4
+            const uint4 out = rot == 0   ? make_uint4(w[0], w[1], w[2], w[3])
+                              : rot == 1 ? make_uint4(w[3], w[0], w[1], w[2])
+                              : rot == 2 ? make_uint4(w[2], w[3], w[0], w[1])
+                                         : make_uint4(w[1], w[2], w[3], w[0]);
+            const bool in = block && r0 + r < a.rows;
+            if (in) *(uint4 *)(a.rcodes + (long)(r0 + r) * rpitch + c0 / 2 + 16 * b) = out;
+            ratom[op_atom_byte(r, b)] = in ? (uint8_t)e : 0u;
         }
-        const int rows_left = a.rows - r0 - rt;
-        const bool code_cols = c0 + 8 * cc < op_in_padded(a.cols);
-        uint8_t *pc = a.rcodes + (long)(r0 + rt) * rpitch + c0 / 2 + 4 * cc;
+    }
+    if (do_col) {
+        // a task is one column's (fp32) or column pair's (bf16) 32 rows
+        const int rpad = op_in_padded(a.rows);
+        constexpr int COLS = 4 / ES, WPR = QT / COLS;  // columns per task, tasks per row block
+#pragma unroll 1
+        for (int i = 0; i < 4 * WPR / Q_THREADS; i++) {
+            const int task = i * Q_THREADS + tid, wc = task % WPR, rb = task / WPR;  // word column, row block
+            uint32_t raw[32], top = 0u;
 #pragma unroll
-        for (int it0 = 0; it0 < NIT; it0 += NB) {
-            if constexpr (VEC) {
-                if (it0) load(t, it0);
-            } else if (do_row) {
-#pragma unroll
-                for (int j = 0; j < NB; j++) q[j] = *(const Chunk<XT> *)(pt + 16 * (it0 + j) * PITCH);
+            for (int k = 0; k < 32; k++) {
+                raw[k] = tile[(32 * rb + k) * PITCH + wc];
+                top = ES == 2 ? absmax2(top, raw[k]) : absmax(top, raw[k]);
             }
 #pragma unroll
-            for (int j = 0; j < NB; j++, pc += 16 * rpitch) {
-                const int i16 = it0 + j;  // row rt + 16 i16
-                if (VEC && do_col) {
+            for (int h = 0; h < COLS; h++) {
+                const int c = COLS * wc + h;
+                float inv;
+                const uint32_t e = block_byte(
+                    ES == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16, inv);
+                uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < (int)sizeof(XT) / 2; i++)
-                        *(uint4 *)(pt + 16 * i16 * PITCH + 4 * i) =
-                            make_uint4(q[j].w[4 * i], q[j].w[4 * i + 1], q[j].w[4 * i + 2], q[j].w[4 * i + 3]);
-                }
-                if (do_row) {
+                for (int g = 0; g < 4; g++) {
                     float v[8];
-                    chunk_values<XT>(q[j], v);
-                    uint32_t mb = absmax8(q[j].w);
-                    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 1));
-                    mb = max(mb, __shfl_xor_sync(0xffffffffu, mb, 2));
-                    float inv;
-                    const uint32_t e = block_byte(mb, inv);
-                    const uint32_t w = convert8(v, inv, e);
-                    const bool in = 16 * i16 < rows_left && code_cols;
-                    if (in) *(uint32_t *)pc = w;
-                    if ((cc & 3) == 0) ratom[16 * rt + (cc >> 2) + op_atom_byte(16 * i16, 0)] = in ? (uint8_t)e : 0u;
-                }
-            }
-        }
-        // the next tile's loads are in flight during this one's column pass
-        if (VEC && t + (int)gridDim.x < a.tiles) load(t + gridDim.x, 0);
-        __syncthreads();
-        if (do_row && tid < 128)
-            ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
-        if (do_col) {
-            // a task is one column's (fp32) or column pair's (bf16) 32 rows
-            constexpr int COLS = sizeof(XT) == 2 ? 2 : 1;   // columns per task
-            constexpr int WPR = QT / COLS;                  // tasks per row block
 #pragma unroll
-            for (int i = 0; i < 4 * WPR / Q_THREADS; i++) {
-                const int task = i * Q_THREADS + tid, wc = task % WPR, rb = task / WPR;  // word column, row block
-                uint32_t raw[32], top = 0u;
-#pragma unroll
-                for (int k = 0; k < 32; k++) {
-                    raw[k] = tile[(32 * rb + k) * PITCH + wc];
-                    top = sizeof(XT) == 2 ? absmax2(top, raw[k]) : absmax(top, raw[k]);
-                }
-#pragma unroll
-                for (int h = 0; h < COLS; h++) {
-                    const int c = COLS * wc + h;
-                    const uint32_t mb =
-                        sizeof(XT) == 4 ? top & 0x7fffffffu : h ? top & 0x7fff0000u : (top & 0x7fffu) << 16;
-                    float inv;
-                    const uint32_t e = block_byte(mb, inv);
-                    uint32_t w[4];
-#pragma unroll
-                    for (int g = 0; g < 4; g++) {
-                        float v[8];
-#pragma unroll
-                        for (int k = 0; k < 8; k++) {
-                            const uint32_t x = raw[8 * g + k];
-                            v[k] = __uint_as_float(sizeof(XT) == 4 ? x : h ? (x & 0xffff0000u) : (x << 16));
-                        }
-                        w[g] = convert8(v, inv, e);
+                    for (int k = 0; k < 8; k++) {
+                        const uint32_t x = raw[8 * g + k];
+                        v[k] = __uint_as_float(ES == 4 ? x : h ? (x & 0xffff0000u) : (x << 16));
                     }
-                    *(uint4 *)(stage + c * CODE_PITCH + 16 * rb) = make_uint4(w[0], w[1], w[2], w[3]);
-                    catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
+                    w[g] = convert8(v, inv, e);
                 }
-            }
-            __syncthreads();
-            if (tid < 128)
-                ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid] =
-                    ((const uint32_t *)catom)[tid];
-            const long cpitch = rpad / 2;
-#pragma unroll
-            for (int i = 0; i < QT * 4 / Q_THREADS; i++) {
-                const int k = i * Q_THREADS + tid, c = k >> 2, rb = k & 3;  // four blocks of 16 bytes per column
-                if (c0 + c < a.cols && r0 + 32 * rb < rpad)
-                    *(uint4 *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 16 * rb) =
-                        *(const uint4 *)(stage + c * CODE_PITCH + 16 * rb);
+                *(uint4 *)(stage + c * CODE_PITCH + 16 * rb) = make_uint4(w[0], w[1], w[2], w[3]);
+                catom[op_atom_byte(c, rb)] = c0 + c < a.cols && r0 + 32 * rb < rpad ? (uint8_t)e : 0u;
             }
         }
-        __syncthreads();  // the tile, its codes and atoms in shared memory are free
+    }
+    __syncthreads();
+    if (do_row && tid < 128)
+        ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
+    if (!do_col) return;
+    if (tid >= 128)
+        ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid - 128] =
+            ((const uint32_t *)catom)[tid - 128];
+    const long cpitch = op_in_padded(a.rows) / 2;
+#pragma unroll
+    for (int i = 0; i < QT * 4 / Q_THREADS; i++) {
+        const int k = i * Q_THREADS + tid, c = k >> 2, rb = k & 3;  // four blocks of 16 bytes per column
+        if (c0 + c < a.cols && r0 + 32 * rb < op_in_padded(a.rows))
+            *(uint4 *)(a.ccodes + (long)(c0 + c) * cpitch + r0 / 2 + 16 * rb) =
+                *(const uint4 *)(stage + c * CODE_PITCH + 16 * rb);
     }
 }
 
@@ -369,14 +321,13 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
     a.tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
     const long tiles = (long)a.tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
     if (tiles > 0x3fffffffL) return K3MOE_EINVAL;
-    a.tiles = (int)tiles;
     const bool vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
-    const size_t sm = !col && vec ? 0 : xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
+    const size_t sm = xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
     void (*const kernel)(QuantArgs) =
         xdt == K3MOE_BF16 ? (vec ? k3_mx_quantize_operand<uint16_t, true> : k3_mx_quantize_operand<uint16_t, false>)
                           : (vec ? k3_mx_quantize_operand<uint32_t, true> : k3_mx_quantize_operand<uint32_t, false>);
     if (ensure_smem((const void *)kernel, sm) != K3MOE_OK) return K3MOE_ECUDA;
-    return launch_pdl(kernel, dim3((unsigned)std::min<long>(tiles, 3L * num_sms())), dim3(Q_THREADS), sm, s, a) == cudaSuccess
+    return launch_pdl(kernel, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a) == cudaSuccess
                ? K3MOE_OK
                : (cudaGetLastError(), K3MOE_ECUDA);
 }
