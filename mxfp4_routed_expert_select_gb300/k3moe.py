@@ -229,28 +229,26 @@ def _ptr(t):
     return t.ctypes.data
 
 
-_raw_stream = None
+_raw_stream = _raw_device = None
 
 
-def _current_stream():
-    """The raw handle of torch's current stream.  torch.cuda.current_stream()
-    builds a Stream object (about 3 us on a Grace core, as long as a whole call
-    into the library); torch's own raw query takes 0.2 us and is used from the
-    second call on, when CUDA is known to be initialised."""
-    global _raw_stream
-    if _raw_stream is not None:
-        return _raw_stream()
+def _first_stream():
+    """torch's current stream by its public call, and from the second call on by
+    its raw queries: torch.cuda.current_stream() builds a Stream object (about
+    3 us on a Grace core, as long as a whole call into the library), the raw
+    handle takes 0.2 us.  CUDA is initialised by then."""
+    global _raw_stream, _raw_device
     import torch
     handle = torch.cuda.current_stream().cuda_stream
     get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
     if get is not None and dev is not None:
-        _raw_stream = lambda: get(dev())  # noqa: E731
+        _raw_stream, _raw_device = get, dev
     return handle
 
 
 def _stream(s=None):
     if s is None:
-        return _current_stream()
+        return _raw_stream(_raw_device()) if _raw_stream is not None else _first_stream()
     return s.cuda_stream if hasattr(s, "cuda_stream") else s
 
 
@@ -387,20 +385,26 @@ def mx_quantize_operand(x, row=None, col=None, stream=None):
     """x [rows][cols] (fp32 or bf16) to MXFP4 along its columns' axis (row, an
     MxOperand rows x cols) and / or along its rows' axis (col, cols x rows)."""
     rows, cols = x.shape
-    check(lib().k3moe_mx_quantize_operand(row and row.ref, col and col.ref, x.data_ptr(), _dtype(x), rows, cols,
-                                          _ld(x, rows, cols), _stream(stream)), "k3moe_mx_quantize_operand")
+    st = (_lib or lib()).k3moe_mx_quantize_operand(row and row.ref, col and col.ref, x.data_ptr(), _dtype(x), rows,
+                                                   cols, _ld(x, rows, cols), _stream(stream))
+    if st:
+        check(st, "k3moe_mx_quantize_operand")
 
 
 def mx_dequantize(y, op, stream=None):
     """The values of an operand into y [op.rows][op.in_] (fp32 or bf16)."""
-    check(lib().k3moe_mx_dequantize(y.data_ptr(), _dtype(y), _ld(y, op.rows, op.in_), op.ref, _stream(stream)),
-          "k3moe_mx_dequantize")
+    st = (_lib or lib()).k3moe_mx_dequantize(y.data_ptr(), _dtype(y), _ld(y, op.rows, op.in_), op.ref,
+                                             _stream(stream))
+    if st:
+        check(st, "k3moe_mx_dequantize")
 
 
 def mx_matmul(C, A, B, accumulate=False, stream=None):
     """C [A.rows][B.rows] (fp32 or bf16) = A B^T of two MxOperands, or += (fp32)."""
-    check(lib().k3moe_mx_matmul(C.data_ptr(), _dtype(C), _ld(C, A.rows, B.rows), A.ref, B.ref, int(accumulate),
-                                _stream(stream)), "k3moe_mx_matmul")
+    st = (_lib or lib()).k3moe_mx_matmul(C.data_ptr(), _dtype(C), _ld(C, A.rows, B.rows), A.ref, B.ref,
+                                         1 if accumulate else 0, _stream(stream))
+    if st:
+        check(st, "k3moe_mx_matmul")
 
 
 class SwigluCheckpoint:
@@ -413,22 +417,27 @@ class SwigluCheckpoint:
             raise K3Error(K3MOE_EINVAL, "SwigluCheckpoint(%d, %d)" % (T, f))
         self.T, self.f, self.nbytes = T, f, n
         self.data = torch.empty(n, dtype=torch.uint8, device=device)
+        self.ptr = self.data.data_ptr()
 
 
 def swiglu_forward(h, ckpt, g, u, stream=None):
     """h = silu(g) * u, keeping g and u in ckpt; [T][f] tensors of one type."""
     T, f = ckpt.T, ckpt.f
-    check(lib().k3moe_swiglu_forward(h.data_ptr(), _ld(h, T, f), ckpt.data.data_ptr(), ckpt.nbytes, g.data_ptr(),
-                                     _ld(g, T, f), u.data_ptr(), _ld(u, T, f), _dtype(h, g, u), T, f,
-                                     _stream(stream)), "k3moe_swiglu_forward")
+    st = (_lib or lib()).k3moe_swiglu_forward(h.data_ptr(), _ld(h, T, f), ckpt.ptr, ckpt.nbytes, g.data_ptr(),
+                                              _ld(g, T, f), u.data_ptr(), _ld(u, T, f), _dtype(h, g, u), T, f,
+                                              _stream(stream))
+    if st:
+        check(st, "k3moe_swiglu_forward")
 
 
 def swiglu_backward(dg, du, dh, ckpt, stream=None):
     """The gradients of gate and up from dh and the kept copies."""
     T, f = ckpt.T, ckpt.f
-    check(lib().k3moe_swiglu_backward(dg.data_ptr(), _ld(dg, T, f), du.data_ptr(), _ld(du, T, f), dh.data_ptr(),
-                                      _ld(dh, T, f), ckpt.data.data_ptr(), ckpt.nbytes, _dtype(dg, du, dh), T, f,
-                                      _stream(stream)), "k3moe_swiglu_backward")
+    st = (_lib or lib()).k3moe_swiglu_backward(dg.data_ptr(), _ld(dg, T, f), du.data_ptr(), _ld(du, T, f),
+                                               dh.data_ptr(), _ld(dh, T, f), ckpt.ptr, ckpt.nbytes,
+                                               _dtype(dg, du, dh), T, f, _stream(stream))
+    if st:
+        check(st, "k3moe_swiglu_backward")
 
 
 class BalanceLoss:
@@ -453,20 +462,24 @@ class BalanceLoss:
         """loss fp32 [1], counts int32 [E], n_valid int32 [1] of logits [T][E],
         ids int32 [T][top_k], mask uint8 [T]."""
         T, E, k, i32 = logits.shape[0], self.E, self.k, self._i32
-        check(lib().k3moe_balance_forward(
+        st = (_lib or lib()).k3moe_balance_forward(
             _flat(loss, self._f32, 1), _flat(counts, i32, E), _flat(n_valid, i32, 1), logits.data_ptr(),
             _dtype(logits), _ld(logits, T, E), _flat(ids, i32, T, k), _flat(mask, self._u8, T), T, E, k, self.alpha,
-            self.rule, *self._ws, _stream(stream)), "k3moe_balance_forward")
+            self.rule, *self._ws, _stream(stream))
+        if st:
+            check(st, "k3moe_balance_forward")
 
     def backward(self, dlogits, logits, ids, counts, n_valid, dloss, mask=None, w=None, dw=None, stream=None):
         """dlogits [T][E] from dloss fp32 [1] and, with the combine weights w and
         their gradients dw (fp32 [T][top_k]), the weight rule's part."""
         T, E, k, f32, i32 = logits.shape[0], self.E, self.k, self._f32, self._i32
-        check(lib().k3moe_balance_backward(
+        st = (_lib or lib()).k3moe_balance_backward(
             dlogits.data_ptr(), _ld(dlogits, T, E), logits.data_ptr(), _dtype(logits, dlogits), _ld(logits, T, E),
             _flat(ids, i32, T, k), _flat(mask, self._u8, T), _flat(counts, i32, E), _flat(n_valid, i32, 1),
             _flat(dloss, f32, 1), _flat(w, f32, T, k), _flat(dw, f32, T, k), T, E, k, self.alpha, self.rule,
-            _stream(stream)), "k3moe_balance_backward")
+            _stream(stream))
+        if st:
+            check(st, "k3moe_balance_backward")
 
 
 def expert_gemv_noalloc(y, x, expert, d, f, stream=None):
