@@ -521,10 +521,14 @@ struct MpCfg {
     static_assert(STAGE % 1024 == 0 && OFF_SA % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 };
 
-// Arrival at the barrier of the same offset in the pair's CTA `rank`.
+// Arrival at the barrier of the same offset in the pair's CTA `rank`, for a
+// hand-over of tensor memory alone: the accumulator's loads are ordered by their
+// wait and the tcgen05 fence before this, and no ordinary memory is handed over, so
+// the arrival is relaxed (a release at cluster scope took 1200 clocks, on the path
+// of the next tile's first MMA).
 K3_DEV void mbar_arrive_rank(uint32_t bar, uint32_t rank)
 {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr_of_rank(bar, rank)) : "memory");
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr_of_rank(bar, rank)) : "memory");
 }
 // The waits for barriers that the other CTA's threads, copies or commits arrive
 // at: cluster scope, bounded as mbar_wait.
