@@ -960,16 +960,17 @@ struct MgPlan {
     int nt, ranks;
 };
 
-// The form by a model of its time in ns, fitted on one GB300 to products of 1 to
-// 8192 rows, 1000 to 20000 columns and K 256 to 8192 (each predicted within 15%):
-//  - tiles: a wave of one tile per SM takes 223 a k-step and 700 for its epilogue
-//  - pairs: 1000 more to start, 1100 a wave's epilogue, and 335 or 272 a step with
-//    256 or 192 columns (bytes into an SM): ahead from two waves of single tiles on (2048 x 1536 x 7168 13.1 against 16.1 us; but 1536 x 1536 x
-//    7168, one wave, 11.8 against 9.5)
-//  - split (up to 128 rows of A, one column tile): 170 a step of the longest rank
-//    and the joining of the ranks' sums, which grows with the columns (1 x 1536 x
-//    7168 4.0 against 7.3 us whole; 333 x 1000 x 1112 6.8 against 5.4)
-MgPlan choose_plan(int M, int N, int nks, int sms)
+// The form by a model of its time, fitted on one GB300.
+//  - above 128 rows of A, tiles or pairs: a start, and for every wave of tiles over
+//    the SMs a time per k-step and one per tile (more in fp32).  Fitted by least
+//    squares to 21 products of 200 to 8192 rows, 1024 to 20000 columns and K 256 to
+//    7168, each run in all three forms: the choice was the fastest form or within
+//    2% of it in every one (2048 x 1536 x 7168: pairs 11.5, tiles 15.6 us; 1536 x
+//    1536 x 7168, one wave of tiles: 11.1 against 9.4).
+//  - up to 128 rows, one column tile, split or not: 170 ns a step of the longest
+//    rank and the joining of the ranks' sums, which grows with the columns (1 x 1536
+//    x 7168: 4.0 split, 7.3 us whole; 128 x 1000 x 1112: 6.4 against 5.3).
+MgPlan choose_plan(int M, int N, int nks, int sms, bool bf16)
 {
     const long tn = ((long)N + MG_M - 1) / MG_M;
     if (M <= 128) {
@@ -982,22 +983,27 @@ MgPlan choose_plan(int M, int N, int nks, int sms)
         }
         return best;
     }
-    const auto waves = [](long tiles, long at_once) { return (tiles + at_once - 1) / at_once; };
-    MgPlan best = {false, 128, 1};
-    long cost = waves(tn * (((long)M + 127) / 128), sms) * (223L * nks + 700);
-    const long tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M);
-    for (int w : {256, 192}) {
-        const long step = w == 256 ? 335 : 272;
-        const long c = 1000 + waves(tm * (((long)N + w - 1) / w), std::max(1, sms / 2)) * (step * nks + 1100);
-        if (c < cost) cost = c, best = {true, w, 1};
+    const long tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M), pairs = std::max(1, sms / 2);
+    const struct {
+        MgPlan plan;
+        long tiles, at_once, start, step, tile;  // ns
+    } forms[3] = {{{false, 128, 1}, tn * (((long)M + 127) / 128), sms, 2610, 199, bf16 ? 840 : 1280},
+                  {{true, 192, 1}, tm * (((long)N + 191) / 192), pairs, 3430, 252, bf16 ? 680 : 1600},
+                  {{true, 256, 1}, tm * (((long)N + 255) / 256), pairs, 3570, 284, bf16 ? 880 : 2130}};
+    int best = 0;
+    long cost = 0;
+    for (int i = 0; i < 3; i++) {
+        const auto &f = forms[i];
+        const long c = f.start + (f.tiles + f.at_once - 1) / f.at_once * (f.step * nks + f.tile);
+        if (!i || c < cost) cost = c, best = i;
     }
-    return best;
+    return forms[best].plan;
 }
 
 template <typename CT>
 int launch_ct(const k3moe_mx_operand *A, const k3moe_mx_operand *B, const MgArgs &a, cudaStream_t s)
 {
-    const MgPlan p = choose_plan(a.M, a.N, a.nks, num_sms());
+    const MgPlan p = choose_plan(a.M, a.N, a.nks, num_sms(), sizeof(CT) == 2);
     if (p.pair)
         return p.nt == 256 ? launch_pair<256, CT>(A, B, a, s) : launch_pair<192, CT>(A, B, a, s);
     switch (p.nt) {

@@ -244,59 +244,76 @@ __global__ void __launch_bounds__(128) k3_mx_scale_atoms(const uint8_t *scales, 
 // to each other.
 template <typename YT, bool VEC>
 __global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, const uint8_t *atoms, int r0,
-                                                        uint32_t n, FastDiv upr, int nk, int in, YT *y, long ld)
+                                                        uint32_t n, FastDiv upr, int nk, int in, YT *y, long ld,
+                                                        bool spread)
 {
     griddep_launch_dependents();
     griddep_wait();
-    constexpr int UB = VEC ? 4 : 1;  // code bytes of a unit
-    for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < n; i += gridDim.x * 256) {
-        const uint32_t q = upr.div(i);
-        const int r = r0 + (int)q, c = (int)(i - q * upr.d) * 2 * UB, b = c >> 5;
-        const float s = op_scale(atoms[((size_t)(r >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r, b)]);
-        YT *o = y + (long)r * ld + c;
-        if constexpr (VEC) {
-            uint32_t h[4];
-            e2m1x8_to_half2x4(*(const uint32_t *)(codes + 4 * (size_t)i), h[0], h[1], h[2], h[3]);
-            float v[8];
+    constexpr int UB = VEC ? 4 : 1, U = 4;  // code bytes of a unit, units of a thread in flight
+    // a thread's units lie 256 apart (a CTA's are then one run), or, when that would
+    // leave SMs idle, a grid apart
+    const uint32_t gap = spread ? gridDim.x * 256 : 256;
+    for (uint32_t i0 = blockIdx.x * (spread ? 256 : U * 256) + threadIdx.x; i0 < n; i0 += gridDim.x * U * 256) {
+        uint32_t word[U], scale[U];
+        int r[U], c[U];
 #pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const float2 f = h2f2(h[j]);
-                v[2 * j] = f.x * s;
-                v[2 * j + 1] = f.y * s;
-            }
-            if constexpr (sizeof(YT) == 2) {
-                uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
+        for (int u = 0; u < U; u++) {
+            const uint32_t i = min(i0 + u * gap, n - 1), q = upr.div(i);
+            r[u] = r0 + (int)q, c[u] = (int)(i - q * upr.d) * 2 * UB;
+            const int b = c[u] >> 5;
+            word[u] = VEC ? *(const uint32_t *)(codes + 4 * (size_t)i) : (uint32_t)codes[i];
+            scale[u] = atoms[((size_t)(r[u] >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r[u], b)];
+        }
+#pragma unroll
+        for (int u = 0; u < U; u++) {
+            if (i0 + u * gap >= n) break;
+            const float s = op_scale(scale[u]);
+            YT *o = y + (long)r[u] * ld + c[u];
+            const int left = in - c[u];
+            if constexpr (VEC) {
+                uint32_t h[4];
+                e2m1x8_to_half2x4(word[u], h[0], h[1], h[2], h[3]);
+                float v[8];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
-                    const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                    p[j] = *(const uint32_t *)&t;
+                    const float2 f = h2f2(h[j]);
+                    v[2 * j] = f.x * s;
+                    v[2 * j + 1] = f.y * s;
                 }
-                if (c + 8 <= in)
-                    *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
-                else
+                if constexpr (sizeof(YT) == 2) {
+                    uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
 #pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (c + j < in) o[j] = (YT)(p[j >> 1] >> (16 * (j & 1)));
-            } else {
-                if (c + 8 <= in) {
-                    ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                    ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                } else
-#pragma unroll
-                    for (int j = 0; j < 8; j++)
-                        if (c + j < in) o[j] = v[j];
-            }
-        } else {
-            const float2 f = e2m1x2_to_float2(codes[i]);
-#pragma unroll
-            for (int j = 0; j < 2; j++)
-                if (c + j < in) {
-                    const float v = (j ? f.y : f.x) * s;
-                    if constexpr (sizeof(YT) == 2)
-                        o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                    for (int j = 0; j < 4; j++) {
+                        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                        p[j] = *(const uint32_t *)&t;
+                    }
+                    if (left >= 8)
+                        *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
                     else
-                        o[j] = v;
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            if (j < left) o[j] = (YT)(p[j >> 1] >> (16 * (j & 1)));
+                } else {
+                    if (left >= 8) {
+                        ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    } else
+#pragma unroll
+                        for (int j = 0; j < 8; j++)
+                            if (j < left) o[j] = v[j];
                 }
+            } else {
+                const float2 f = e2m1x2_to_float2(word[u]);
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    if (j < left) {
+                        const float v = (j ? f.y : f.x) * s;
+                        if constexpr (sizeof(YT) == 2)
+                            o[j] = __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                        else
+                            o[j] = v;
+                    }
+            }
         }
     }
 }
@@ -349,10 +366,11 @@ static int launch_dequantize(const k3moe_mx_operand *op, YT *y, long ld, cudaStr
     const int rows = (int)std::min<long>(op->rows, std::max<long>(1, (1L << 30) / upr));
     for (int r = 0; r < op->rows; r += rows) {
         const uint32_t n = (uint32_t)std::min(rows, op->rows - r) * upr;
-        const unsigned grid = (unsigned)std::min<long>(((long)n + 255) / 256, 32L * num_sms());
+        const bool spread = n < 1024u * (unsigned)num_sms();
+        const unsigned grid = (unsigned)std::min<long>(spread ? (n + 255) / 256 : (n + 1023) / 1024, 16L * num_sms());
         if (launch_pdl(k3_mx_dequantize<YT, VEC>, dim3(grid), dim3(256), 0, s,
                        (const uint8_t *)op->codes + (size_t)r * (op_in_padded(op->in) / 2), (const uint8_t *)op->atoms,
-                       r, n, FastDiv(upr), op_k_atoms(op->in), op->in, y, ld) != cudaSuccess) {
+                       r, n, FastDiv(upr), op_k_atoms(op->in), op->in, y, ld, spread) != cudaSuccess) {
             cudaGetLastError();
             return K3MOE_ECUDA;
         }
