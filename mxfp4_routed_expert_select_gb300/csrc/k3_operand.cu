@@ -26,7 +26,10 @@ namespace k3 {
 namespace {
 
 constexpr int QT = 128;        // tile rows and columns
-constexpr int Q_THREADS = 256;
+// Threads of a CTA: four CTAs of 256 share an SM on bf16 tiles, two of 512 on fp32
+// tiles, whose shared memory is twice as large.
+template <typename XT>
+constexpr int q_threads() { return sizeof(XT) == 2 ? 256 : 512; }
 
 struct QuantArgs {
     const void *x;
@@ -87,8 +90,9 @@ constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH;
 // aligned; else the tile comes in by single elements, neighbouring lanes on
 // neighbouring columns.
 template <typename XT, bool VEC>
-__global__ void __launch_bounds__(Q_THREADS, sizeof(XT) == 2 ? 4 : 2) k3_mx_quantize_operand(const QuantArgs a)
+__global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_mx_quantize_operand(const QuantArgs a)
 {
+    constexpr int Q_THREADS = q_threads<XT>();
     extern __shared__ __align__(16) uint32_t tile[];
     __shared__ __align__(16) uint8_t ratom[512], catom[512];
     constexpr int PITCH = tile_pitch<XT>(), ES = (int)sizeof(XT);
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(Q_THREADS, sizeof(XT) == 2 ? 4 : 2) k3_mx_quan
     if (do_row && tid < 128)
         ((uint32_t *)(a.ratoms + ((long)ty * op_k_atoms(a.cols) + tx) * 512))[tid] = ((const uint32_t *)ratom)[tid];
     if (!do_col) return;
-    if (tid >= 128)
+    if (tid >= 128 && tid < 256)
         ((uint32_t *)(a.catoms + ((long)tx * op_k_atoms(a.rows) + ty) * 512))[tid - 128] =
             ((const uint32_t *)catom)[tid - 128];
     const long cpitch = op_in_padded(a.rows) / 2;
@@ -344,7 +348,7 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
         xdt == K3MOE_BF16 ? (vec ? k3_mx_quantize_operand<uint16_t, true> : k3_mx_quantize_operand<uint16_t, false>)
                           : (vec ? k3_mx_quantize_operand<uint32_t, true> : k3_mx_quantize_operand<uint32_t, false>);
     if (ensure_smem((const void *)kernel, sm) != K3MOE_OK) return K3MOE_ECUDA;
-    return launch_pdl(kernel, dim3((unsigned)tiles), dim3(Q_THREADS), sm, s, a) == cudaSuccess
+    return launch_pdl(kernel, dim3((unsigned)tiles), dim3((unsigned)(xdt == K3MOE_BF16 ? q_threads<uint16_t>() : q_threads<uint32_t>())), sm, s, a) == cudaSuccess
                ? K3MOE_OK
                : (cudaGetLastError(), K3MOE_ECUDA);
 }
