@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(BF_THREADS, 1) k3_balance_forward(const Balanc
     for (int e = threadIdx.x; e < 128 * NV; e += BF_THREADS) cnt[e] = 0u;
     if (threadIdx.x == 0) nval = 0u;
     __syncthreads();
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
 
     float acc[4 * NV];
 #pragma unroll
@@ -285,8 +285,8 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int rb = row_buf(a.E, (int)sizeof(T));
     uint8_t *buf = dyn + warp * 2 * rb;
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const int step = gridDim.x * BL_WARPS;
     int t = blockIdx.x * BL_WARPS + warp, b = 0;
     auto kept = [&](int r) { return r < a.T && (!a.mask || a.mask[r]); };

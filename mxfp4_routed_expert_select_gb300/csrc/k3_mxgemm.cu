@@ -349,7 +349,6 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
-    griddep_launch_dependents();
     griddep_wait();
 
     if (warp == MG_W_PROD || warp == MG_W_PROD2) {
@@ -655,7 +654,6 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
     cluster_sync();  // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
-    griddep_launch_dependents();
     griddep_wait();
 
     if (warp == MG_W_PROD || warp == MG_W_PROD2) {

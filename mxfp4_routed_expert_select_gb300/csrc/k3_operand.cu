@@ -101,7 +101,6 @@ __global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_m
     const int tx = blockIdx.x % a.tiles_x, ty = blockIdx.x / a.tiles_x;
     const int r0 = ty * QT, c0 = tx * QT;
     const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
-    griddep_launch_dependents();
     griddep_wait();
     if (!do_row && !do_col) return;
 
@@ -251,7 +250,6 @@ __global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, co
                                                         uint32_t n, FastDiv upr, int nk, int in, YT *y, long ld,
                                                         bool spread)
 {
-    griddep_launch_dependents();
     griddep_wait();
     constexpr int UB = VEC ? 4 : 1, U = 4;  // code bytes of a unit, units of a thread in flight
     // a thread's units lie 256 apart (a CTA's are then one run), or, when that would

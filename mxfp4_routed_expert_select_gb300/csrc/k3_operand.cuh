@@ -4,6 +4,13 @@
 
 namespace k3 {
 
+// Programmatic dependent launches of the kernels that use this header: all start
+// as dependents and wait (griddep_wait) before they touch global memory.  Those
+// that may write what a later kernel reads before its own wait (the GEMV and
+// shared-expert kernels load weights there: codes, values, products) do not let
+// their dependents start early; the others do so only after their wait, when
+// everything before them is complete.
+
 // Codes: [rows][ceil32(in) / 2] bytes.  Scale bytes: 512-byte atoms of 128
 // rows x 4 blocks (128 of the reduction), atom (row tile, k) at
 // (row tile) * n_k + k, with n_k even so that a 256-long step always has two;

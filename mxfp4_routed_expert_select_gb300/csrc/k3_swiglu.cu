@@ -180,8 +180,8 @@ K3_DEV Place place(const SwigluArgs &a, uint32_t i, uint32_t end)
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_forward(const SwigluArgs a)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     // each CTA takes one run of chunks, in steps of its threads
     const uint32_t end = min(a.n, (blockIdx.x + 1) * a.run), step = SW_THREADS;
     // n is a multiple of 4, so the four lanes of a block stay together; lanes
@@ -238,8 +238,8 @@ K3_DEV Kept<T> load_kept(const SwigluArgs &a, uint32_t i, uint32_t end, const Pl
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_backward(const SwigluArgs a)
 {
-    griddep_launch_dependents();
     griddep_wait();
+    griddep_launch_dependents();
     const uint32_t end = min(a.n, (blockIdx.x + 1) * a.run), step = SW_THREADS;
     uint32_t i = blockIdx.x * a.run + threadIdx.x;
     Place pl = place(a, i, end);
