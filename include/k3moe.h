@@ -637,7 +637,7 @@ int k3moe_shared_forward(float *out, const float *x, int32_t T, const k3moe_bf16
  *          atoms of 128 rows x 4 blocks, byte 16 (r mod 32) + 4 (r / 32 mod 4) +
  *          (block mod 4) of atom (r / 128) * n + block / 4, with
  *          n = 2 ceil(in / 256); bytes past the matrix are zero
- * `rows` and `in` are any sizes >= 1.  The caller owns both buffers, of
+ * `rows` and `in` are any sizes from 1 to 2^30.  The caller owns both buffers, of
  * k3moe_mx_operand_codes_bytes and k3moe_mx_operand_atoms_bytes bytes (-1 if
  * invalid), 16-byte aligned.  Byte 255 stands for NaN here: a block that held a
  * non-finite value makes every product that reads it NaN.
@@ -715,8 +715,8 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *h
  *              arithmetic, rounded once
  *  ckpt        device, k3moe_swiglu_ckpt_bytes(T, f) bytes, 16-byte aligned
  * In the backward call dg or du may be dh itself with the same stride.
- * Errors: K3MOE_EINVAL for null or misaligned pointers, T or f < 1, short
- * strides, a ckpt_bytes that is too small.
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, T or f outside 1 .. 2^30,
+ * short strides, a ckpt_bytes that is too small.
  */
 int64_t k3moe_swiglu_ckpt_bytes(int32_t T, int32_t f);
 int k3moe_swiglu_forward(void *h, int64_t ldh, void *ckpt, int64_t ckpt_bytes, const void *g, int64_t ldg,
@@ -746,7 +746,7 @@ int k3moe_swiglu_backward(void *dg, int64_t lddg, void *du, int64_t lddu, const 
  * A slot whose id is outside 0..E-1 (a dropped one, e.g. -1) is not counted and
  * takes no part in <w, dw>.  No valid token: loss 0, N = 0.
  *  logits   [T][E], dtype K3MOE_F32 or K3MOE_BF16, row stride ld >= E elements;
- *           1 <= E <= 1024
+ *           1 <= E <= 1024, 1 <= T <= 2^30
  *  ids      int32 [T][top_k], as k3moe_layer_route returns them; 1 <= top_k <= 32
  *  mask     uint8 [T] or NULL
  *  loss     fp32 [1], counts int32 [E], n_valid int32 [1] (out; the backward

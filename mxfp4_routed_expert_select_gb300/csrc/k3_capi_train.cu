@@ -115,7 +115,7 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *A
 
 int64_t k3moe_swiglu_ckpt_bytes(int32_t T, int32_t f)
 {
-    if (T < 1 || f < 1 || f > kMaxDim) return -1;
+    if (T < 1 || T > kMaxDim || f < 1 || f > kMaxDim) return -1;
     return 2 * (int64_t)T * (k3::op_in_padded(f) + k3::op_in_padded(f) / 32);
 }
 
@@ -148,7 +148,7 @@ size_t k3moe_balance_workspace(int32_t E) { return E < 1 || E > 1024 ? 0 : k3::b
 static bool valid_balance(const void *logits, int dtype, int64_t ld, const int32_t *ids, int32_t T, int32_t E,
                           int32_t k, int rule)
 {
-    return T >= 1 && E >= 1 && E <= 1024 && k >= 1 && k <= 32 && valid_dtype(dtype) &&
+    return T >= 1 && T <= kMaxDim && E >= 1 && E <= 1024 && k >= 1 && k <= 32 && valid_dtype(dtype) &&
            valid_rows(logits, dtype, ld, E) && ids && aligned(ids, 4) && rule >= K3MOE_ROUTER_SOFTMAX &&
            rule <= K3MOE_ROUTER_SIGMOID_NORM;
 }

@@ -45,7 +45,7 @@ def _filled(rows, n):
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 31, 0), (1, 7168, 0), (33, 32, 0), (128, 256, 8), (129, 257, 3),
-                                           (300, 100, 4), (31, 1000, 1), (1000, 127, 0), (512, 640, 0)])
+                                           (300, 100, 4), (31, 1000, 1), (1000, 127, 0), (512, 640, 0), (70, 33, 7), (300, 391, 9)])
 def test_quantize_both_ways(rows, cols, pad, dt):
     x = _x(rows, cols, DT[dt], rows * 1000 + cols, pad)
     row, col = _filled(rows, cols), _filled(cols, rows)
@@ -321,3 +321,51 @@ def test_matmul_nan_stays_in_its_rows_and_columns():
     k.mx_matmul(C, A, B)
     bad = torch.isnan(C)
     assert bool(bad[700].all()) and bool(bad[:, 4999].all()) and int(bad.sum()) == M + N - 1
+
+
+def test_weights_written_by_a_call_are_seen_by_the_next():
+    """Calls that load weights before their predecessor on the stream has finished
+    see what a dequantisation, a product or a quantisation wrote just before."""
+    d, f = 1024, 512
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    blob = torch.empty(k.shared_expert_bytes(d, f) // 2, dtype=torch.bfloat16, device="cuda")
+    view = [k.shared_expert_view(blob.data_ptr(), d, f)]
+    x, ws = torch.randn(1, d, generator=gen, device="cuda"), torch.empty(1 << 16, dtype=torch.uint8, device="cuda")
+    got, want = torch.empty(1, d, device="cuda"), torch.empty(1, d, device="cuda")
+    ops = [k.MxOperand(f, d), k.MxOperand(f, d), k.MxOperand(d, f)]
+    planes = [blob[:f * d].view(f, d), blob[f * d:2 * f * d].view(f, d), blob[2 * f * d:].view(d, f)]
+    ident = k.MxOperand(f, f)
+    k.mx_quantize_operand(torch.eye(f, device="cuda"), ident)
+    down_t = k.MxOperand(d, f)
+    for it in range(20):
+        ws_ = [torch.randn(o.rows, o.in_, generator=gen, device="cuda") * 0.05 for o in ops]
+        for o, w in zip(ops, ws_):
+            k.mx_quantize_operand(w, o)
+        k.mx_quantize_operand(ws_[2], down_t)
+        torch.cuda.synchronize()
+        # the last plane by a dequantisation, or by a product with the identity
+        order = (2, 1, 0) if it % 2 else (0, 1, 2)
+        for i in order:
+            if it % 4 == 2 and i == 2:
+                k.mx_matmul(planes[2], down_t, ident)
+            else:
+                k.mx_dequantize(planes[i], ops[i])
+        k.shared_forward(got, x, 1, view, d, f, ws)
+        torch.cuda.synchronize()
+        k.shared_forward(want, x, 1, view, d, f, ws)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    # an expert's packed gate plane written by the quantiser, then its GEMV
+    packed, scales = torch.empty(f, d // 2, dtype=torch.uint8, device="cuda"), torch.full((f, d // 32), 124, device="cuda",
+                                                                                          dtype=torch.uint8)
+    y, y2 = torch.empty(f, device="cuda"), torch.empty(f, device="cuda")
+    op = k.MxOperand(f, d, codes=packed.view(-1))
+    for _ in range(20):
+        w = torch.randn(f, d, generator=gen, device="cuda")
+        torch.cuda.synchronize()
+        k.mx_quantize_operand(w, op)
+        k.matmul_mxfp4(y, x, packed, scales, f, d)
+        torch.cuda.synchronize()
+        k.matmul_mxfp4(y2, x, packed, scales, f, d)
+        torch.cuda.synchronize()
+        assert torch.equal(y, y2)

@@ -114,6 +114,16 @@ def test_balance_refusals():
                                         a["rule"], None) == EINVAL, bad
 
 
+def test_more_tokens_than_indices_hold():
+    L = k.lib()
+    T = (1 << 30) + 1
+    assert L.k3moe_swiglu_ckpt_bytes(T, 32) == -1
+    assert L.k3moe_swiglu_forward(P, 32, P, 1 << 60, P, 32, P, 32, 0, T, 32, None) == EINVAL
+    ws = L.k3moe_balance_workspace(32)
+    assert L.k3moe_balance_forward(P, P, P, P, 0, 32, P, None, T, 32, 2, 0.1, 0, P, ws, None) == EINVAL
+    assert L.k3moe_balance_backward(2 * P, 32, P, 0, 32, P, None, P, P, P, None, None, T, 32, 2, 0.1, 0, None) == EINVAL
+
+
 def test_binding_refuses_other_tensors():
     import torch
     x = torch.zeros(4, 8)
