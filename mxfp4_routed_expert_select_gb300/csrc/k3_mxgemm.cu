@@ -766,13 +766,19 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
 #pragma unroll 1
             for (int i = half; i < NP; i += 2) {
                 const int j = C::OVER < NT && !buf ? (i + C::OVER / PC) % NP : i, n = n0 + j * PC;
+                uint32_t r[PC / 32][32];
+#pragma unroll
+                for (int h = 0; h < PC / 32; h++) tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r[h]);
+                if (i + 2 >= SP && i < SP) {  // this warp's last shared piece
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_rank(bar(B_ACCE + buf), 0);
+                }
                 // the piece staged before has been read
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < PC / 32; h++) {
-                    uint32_t r[32];
-                    tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r);
                     constexpr int W = 32 * (int)sizeof(CT) / 16;  // 16-byte chunks of 32 columns
 #pragma unroll
                     for (int c = 0; c < W; c++) {
@@ -781,21 +787,16 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
                             uint32_t w[4];
 #pragma unroll
                             for (int x = 0; x < 4; x++) {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[8 * c + 2 * x]),
-                                                                               __uint_as_float(r[8 * c + 2 * x + 1]));
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[h][8 * c + 2 * x]),
+                                                                               __uint_as_float(r[h][8 * c + 2 * x + 1]));
                                 w[x] = *(const uint32_t *)&p;
                             }
                             v = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
-                            v = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
+                            v = make_uint4(r[h][4 * c], r[h][4 * c + 1], r[h][4 * c + 2], r[h][4 * c + 3]);
                         }
                         *(uint4 *)(box + lane * 128 + (((h * W + c) ^ (lane & 7)) << 4)) = v;
                     }
-                }
-                if (i + 2 >= SP && i < SP) {  // this warp's last shared piece
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive_rank(bar(B_ACCE + buf), 0);
                 }
                 if (a.tma) {
                     fence_async_smem();
