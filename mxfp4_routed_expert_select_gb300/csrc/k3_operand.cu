@@ -34,7 +34,8 @@ constexpr int q_threads() { return sizeof(XT) == 2 ? 256 : 512; }
 struct QuantArgs {
     const void *x;
     long ld;
-    int rows, cols, tiles_x;
+    int rows, cols;
+    FastDiv tiles_x;
     uint8_t *rcodes, *ratoms;      // row form, or null
     uint8_t *ccodes, *catoms;      // column form, or null
 };
@@ -72,7 +73,12 @@ K3_DEV uint32_t convert8(const float (&v)[8], float inv, uint32_t e)
     return e == 255u ? 0u : codes8(a);  // a non-finite block: codes 0
 }
 
-// 16 bytes to shared memory, the first n of them from p (zero past those).
+// 16 bytes to shared memory.
+K3_DEV void copy16(uint32_t dst, const void *p)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(p) : "memory");
+}
+// The first n of them from p, zero past those.
 K3_DEV void copy16(uint32_t dst, const void *p, int n)
 {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(p), "r"(n) : "memory");
@@ -98,7 +104,7 @@ __global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_m
     constexpr int PITCH = tile_pitch<XT>(), ES = (int)sizeof(XT);
     uint8_t *stage = (uint8_t *)(tile + QT * PITCH);
     const int tid = threadIdx.x;
-    const int tx = blockIdx.x % a.tiles_x, ty = blockIdx.x / a.tiles_x;
+    const int ty = (int)a.tiles_x.div(blockIdx.x), tx = (int)blockIdx.x - ty * (int)a.tiles_x.d;
     const int r0 = ty * QT, c0 = tx * QT;
     const bool do_row = a.rcodes && ty < op_row_tiles(a.rows), do_col = a.ccodes && tx < op_row_tiles(a.cols);
     griddep_wait();
@@ -107,13 +113,19 @@ __global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_m
     if constexpr (VEC) {
         constexpr int CPR = QT * ES / 16, RS = Q_THREADS / CPR;  // 16-byte units per row, rows per pass
         const int u = tid % CPR, r = tid / CPR;
-        const int bytes = min(max((a.cols - c0) * ES - 16 * u, 0), 16);
         const XT *p = (const XT *)a.x + (long)(r0 + r) * a.ld + c0 + u * (16 / ES);
-        uint32_t dst = smem_u32(tile + r * PITCH + 4 * u);
+        const uint32_t dst = smem_u32(tile + r * PITCH + 4 * u);
+        const long pass = RS * a.ld;
+        if (r0 + QT <= a.rows && c0 + QT <= a.cols) {
 #pragma unroll
-        for (int i = 0; i < QT / RS; i++) {
-            const bool in = bytes > 0 && r0 + r + i * RS < a.rows;
-            copy16(dst + (uint32_t)(i * RS * PITCH * 4), in ? p + (long)(i * RS) * a.ld : (const XT *)a.x, in ? bytes : 0);
+            for (int i = 0; i < QT / RS; i++, p += pass) copy16(dst + (uint32_t)(i * RS * PITCH * 4), p);
+        } else {
+            const int bytes = min(max((a.cols - c0) * ES - 16 * u, 0), 16);
+#pragma unroll
+            for (int i = 0; i < QT / RS; i++, p += pass) {
+                const bool in = bytes > 0 && r0 + r + i * RS < a.rows;
+                copy16(dst + (uint32_t)(i * RS * PITCH * 4), in ? p : (const XT *)a.x, in ? bytes : 0);
+            }
         }
         asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory");
     } else {
@@ -337,8 +349,9 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
     if (row) a.rcodes = row->codes, a.ratoms = row->atoms;
     if (col) a.ccodes = col->codes, a.catoms = col->atoms;
     // the tiles cover every scale atom, the padding ones included
-    a.tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
-    const long tiles = (long)a.tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
+    const int tiles_x = row ? op_k_atoms(cols) : op_row_tiles(cols);
+    a.tiles_x = FastDiv((uint32_t)tiles_x);
+    const long tiles = (long)tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
     if (tiles > 0x3fffffffL) return K3MOE_EINVAL;
     const bool vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
     const size_t sm = xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
