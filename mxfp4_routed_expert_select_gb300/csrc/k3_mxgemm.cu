@@ -77,34 +77,43 @@ __host__ __device__ constexpr uint32_t mg_idesc(int m, int n, uint32_t sfid)
 //              columns' in 8 per 128 rows, k-atom major
 //   shift      first scale word of the columns' rows within their atoms
 // GRP: cta_group.  1: one row tile of column atoms; 2: two, and each CTA of the pair
-// copies its own atoms to its own TMEM.
+// copies its own atoms to its own TMEM.  384 columns are two MMAs of 192, their code
+// rows 96 apart in the stage and their scales in three row tiles.
 #define MG_HEAD                                                                                              \
-    "{\n\t.reg .pred p, t, e;\n\t.reg .b64 d, da, db;\n\t.reg .b32 x, y, z;\n\t"                              \
+    "{\n\t.reg .pred p, t, e;\n\t.reg .b64 d, da, db;\n\t.reg .b32 x, y, z, w;\n\tadd.u32 w, %0, 192;\n\t"       \
     "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, %7, %7;\n\tadd.u32 z, %4, %5;\n\t"
 #define MG_CP(grp, col, off)                                                                                 \
     "add.u32 x, %3, " #off ";\n\tadd.u32 y, %4, " #col ";\n\tmov.b64 d, {x, %8};\n\t"                          \
     "@e tcgen05.cp.cta_group::" #grp ".32x128b.warpx4 [y], d;\n\t"
-#define MG_MMA(grp, k2, sfa, sfb, id, pred)                                                                  \
-    "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %9};\n\tmov.b64 db, {y, %9};\n\t"   \
+#define MG_MMA(grp, acc, k2, t2, sfa, sfb, id, pred)                                                                \
+    "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #t2 ";\n\tmov.b64 da, {x, %9};\n\tmov.b64 db, {y, %9};\n\t"   \
     "add.u32 x, %4, " #sfa ";\n\tadd.u32 y, z, " #sfb ";\n\t"                                                \
-    "@e tcgen05.mma.cta_group::" #grp ".kind::mxf4.block_scale.scale_vec::2X [%0], da, db, " id ", [x], [y], " pred ";\n\t"
+    "@e tcgen05.mma.cta_group::" #grp ".kind::mxf4.block_scale.scale_vec::2X [" acc "], da, db, " id ", [x], [y], " pred ";\n\t"
 #define MG_OPERANDS                                                                                          \
-    ::"r"(tacc), "r"(slo), "r"(tlo), "r"(sal), "r"(sf), "r"(shift), "r"(acc), "r"(mg_idesc(M, NT, 0)), "r"(AHI),     \
-        "r"(SW128_HI), "r"(mg_idesc(M, NT, 2))                                                               \
+    ::"r"(tacc), "r"(slo), "r"(tlo), "r"(sal), "r"(sf), "r"(shift), "r"(acc), "r"(mg_idesc(M, MN, 0)), "r"(AHI),     \
+        "r"(SW128_HI), "r"(mg_idesc(M, MN, 2))                                                               \
         : "memory"
 template <int GRP, int NT>
 K3_DEV void mg_step(uint32_t tacc, uint32_t slo, uint32_t tlo, uint32_t sal, uint32_t sf, uint32_t shift, uint32_t acc)
 {
     constexpr uint32_t AHI = (128u >> 4) | (1u << 14);  // atoms: 8 rows of 16 bytes 128 bytes apart, no swizzle
-    constexpr int M = GRP * MG_M;
-    if constexpr (GRP == 2)
+    constexpr int M = GRP * MG_M, MN = NT > 256 ? NT / 2 : NT;
+    if constexpr (NT == 384)
+        asm volatile(MG_HEAD MG_CP(2, 0, 0) MG_CP(2, 4, 32) MG_CP(2, 8, 64) MG_CP(2, 12, 128) MG_CP(2, 16, 192)
+                         MG_CP(2, 20, 96) MG_CP(2, 24, 160) MG_CP(2, 28, 224)
+                             MG_MMA(2, "%0", 0, 0, 0, 8, "%7", "p") MG_MMA(2, "w", 0, 768, 0, 14, "%7", "p")
+                                 MG_MMA(2, "%0", 2, 2, 0, 8, "%10", "t") MG_MMA(2, "w", 2, 770, 0, 14, "%10", "t")
+                                     MG_MMA(2, "%0", 4, 4, 4, 20, "%7", "t") MG_MMA(2, "w", 4, 772, 4, 26, "%7", "t")
+                                         MG_MMA(2, "%0", 6, 6, 4, 20, "%10", "t")
+                                             MG_MMA(2, "w", 6, 774, 4, 26, "%10", "t") "}" MG_OPERANDS);
+    else if constexpr (GRP == 2)
         asm volatile(MG_HEAD MG_CP(2, 0, 0) MG_CP(2, 4, 32) MG_CP(2, 8, 64) MG_CP(2, 12, 128) MG_CP(2, 16, 96)
-                         MG_CP(2, 20, 160) MG_MMA(2, 0, 0, 8, "%7", "p") MG_MMA(2, 2, 0, 8, "%10", "t")
-                             MG_MMA(2, 4, 4, 16, "%7", "t") MG_MMA(2, 6, 4, 16, "%10", "t") "}" MG_OPERANDS);
+                         MG_CP(2, 20, 160) MG_MMA(2, "%0", 0, 0, 0, 8, "%7", "p") MG_MMA(2, "%0", 2, 2, 0, 8, "%10", "t")
+                             MG_MMA(2, "%0", 4, 4, 4, 16, "%7", "t") MG_MMA(2, "%0", 6, 6, 4, 16, "%10", "t") "}" MG_OPERANDS);
     else
         asm volatile(MG_HEAD MG_CP(1, 0, 0) MG_CP(1, 4, 32) MG_CP(1, 8, 64) MG_CP(1, 12, 96)
-                         MG_MMA(1, 0, 0, 8, "%7", "p") MG_MMA(1, 2, 0, 8, "%10", "t") MG_MMA(1, 4, 4, 12, "%7", "t")
-                             MG_MMA(1, 6, 4, 12, "%10", "t") "}" MG_OPERANDS);
+                         MG_MMA(1, "%0", 0, 0, 0, 8, "%7", "p") MG_MMA(1, "%0", 2, 2, 0, 8, "%10", "t")
+                             MG_MMA(1, "%0", 4, 4, 4, 12, "%7", "t") MG_MMA(1, "%0", 6, 6, 4, 12, "%10", "t") "}" MG_OPERANDS);
 }
 #undef MG_HEAD
 #undef MG_CP
@@ -479,8 +488,11 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
 // clocks of MMAs (measured 880 a step, 5.3 PFLOP/s at 8192^3).  A pair of CTAs
 // (cta_group::2) works on 256 rows of A x NT rows of B together: each loads its own
 // 128 rows of A and half of B's, and the MMA reads both halves, so a step brings
-// and reads 35 KB per SM: shared memory and the tensor cores are both near full
-// (7.2 PFLOP/s at 8192^3).
+// and reads 35 KB per SM: shared memory's 64 bytes a clock (553 clocks a step) and
+// the tensor cores (512) are both near full (7.5 PFLOP/s at 8192^3).  192 columns
+// leave the MMAs 384 of 490 clocks but split some products into fuller waves; 384,
+// for products that are then one wave, are bound by the MMAs (790 of 768 clocks),
+// but with one accumulator the epilogue of a tile is not hidden.
 //
 // A's rows take the lanes here, so that a lane of the epilogue holds consecutive n
 // and stages them with 16-byte stores (with B's rows in the lanes its 2-byte ones
@@ -498,21 +510,22 @@ constexpr int MP_BOX = 4096;  // bytes of a staged piece of C: 32 rows of 128 by
 
 template <int NT>
 struct MpCfg {
-    static constexpr int QT = 2;                      // row tiles of B's scale atoms per tile (192: from a half tile)
+    static constexpr int MN = NT > 256 ? NT / 2 : NT;  // columns of an MMA
+    static constexpr int QT = NT > 256 ? 3 : 2;       // row tiles of B's scale atoms per tile (192: from a half tile)
     static constexpr int S_BYTES = MG_M * 128, T_BYTES = NT / 2 * 128;
     static constexpr int OFF_T = S_BYTES;
     static constexpr int OFF_SA = OFF_T + T_BYTES;    // this CTA's two A atoms
     static constexpr int OFF_TA = OFF_SA + 1024;      // all of B's atoms of the tile (each CTA needs them)
     static constexpr int STAGE = OFF_TA + QT * 1024;
-    static constexpr int NS = 5;
+    static constexpr int NS = NT > 256 ? 4 : 5;
     static constexpr int OFF_C = NS * STAGE;          // a staged piece per epilogue warp
     static constexpr int OFF_BAR = OFF_C + MP_EPI * MP_BOX;
     static constexpr int SMEM = 1024 + OFF_BAR + 256;
     // TMEM: two accumulators, then each stage's scales.  Two accumulators of 256
     // columns do not fit beside the scales: the second starts at OVER, and the
-    // columns they share are read first.
+    // columns they share are read first.  Of 384 there is one.
     static constexpr int SF = 8 + 8 * QT;
-    static constexpr int OVER = NT == 256 ? 128 : NT;
+    static constexpr int OVER = NT > 256 ? 0 : NT == 256 ? 128 : NT;
     static constexpr int SF0 = OVER + NT;
     static constexpr int BARS = 2 * NS + 2 * 2 + 1;
     static_assert(SMEM <= 232448, "shared memory");
@@ -582,6 +595,14 @@ K3_DEV void mp_load(uint32_t dst, const CUtensorMap *map, uint32_t adst, const C
                  "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], "
                  "[%3, {0, %6, %7}], [%8];\n\t}" ::"r"(dst),
                  "l"((uint64_t)map), "r"(adst), "l"((uint64_t)amap), "r"(x), "r"(row), "r"(ka), "r"(rt), "r"(bar)
+                 : "memory");
+}
+K3_DEV void mp_load_codes(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
                  : "memory");
 }
 // Arrival at the barrier of this offset in both CTAs once everything issued
@@ -668,7 +689,7 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
         for (int u = first; u < a.n_tiles && ok; u += step) {
             // rows and atoms past the matrices read as zero
             const int m0 = (u / a.tiles_t) * 2 * MG_M + rank * MG_M, n0 = (u % a.tiles_t) * NT;
-            const int row = is_s ? m0 : n0 + rank * (NT / 2), rt = (is_s ? m0 : n0) / 128;
+            const int row = is_s ? m0 : n0 + rank * (C::MN / 2), rt = (is_s ? m0 : n0) / 128;
             for (int ks = 0; ks < a.nks; ks++, it++) {
                 if (!ready && !__all_sync(0xffffffffu, tc_wait_cluster(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
                     ok = false;
@@ -680,6 +701,9 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
                 if (is_s && rank == 0) mbar_expect_elected(bar(B_FULL + s), 2 * C::STAGE);
                 mp_load(dst0 + (uint32_t)(s * C::STAGE), map, adst0 + (uint32_t)(s * C::STAGE), amap, ks * 128, row,
                         2 * ks, rt, full0 + 8 * s);
+                if (C::MN < NT && !is_s)  // the second MMA's columns
+                    mp_load_codes(dst0 + (uint32_t)(s * C::STAGE + C::T_BYTES / 2), map, ks * 128, row + C::MN,
+                                  full0 + 8 * s);
                 s = sn;
                 phase = pn;
             }
@@ -938,7 +962,7 @@ int launch_pair(const k3moe_mx_operand *A, const k3moe_mx_operand *B, MgArgs a, 
 {
     CUtensorMap smap, tmap, samap, tamap, cmap;
     int st = code_map(&smap, A, MG_M);
-    if (st == K3MOE_OK) st = code_map(&tmap, B, NT / 2);
+    if (st == K3MOE_OK) st = code_map(&tmap, B, MpCfg<NT>::MN / 2);
     if (st == K3MOE_OK) st = atom_map(&samap, A, 1);
     if (st == K3MOE_OK) st = atom_map(&tamap, B, MpCfg<NT>::QT);
     if (st != K3MOE_OK) return st;
@@ -961,11 +985,12 @@ struct MgPlan {
 
 // The form by a model of its time, fitted on one GB300.
 //  - above 128 rows of A, tiles or pairs: a start, and for every wave of tiles over
-//    the SMs a time per k-step and one per tile (more in fp32).  Fitted by least
-//    squares to 21 products of 200 to 8192 rows, 1024 to 20000 columns and K 256 to
-//    7168, each run in all three forms: the choice was the fastest form or within
-//    2% of it in every one (2048 x 1536 x 7168: pairs 11.5, tiles 15.6 us; 1536 x
-//    1536 x 7168, one wave of tiles: 11.1 against 9.4).
+//    the SMs a time per k-step and one per tile (more in fp32).  Fitted to 27
+//    products of 200 to 8192 rows, 1024 to 20000 columns and K 256 to 8192, each run
+//    in all four forms: the choice was the fastest form or within 4% of it in every
+//    one (us: 2048 x 1536 x 7168 bf16, 192 columns 12.0, one wave of 256 13.3, tiles
+//    15.6; 4096 x 1536 x 7168, one wave of 384 17.9, two of 192 19.4; 4096 x 7168 x
+//    1536, 256 20.2, 192 21.6, 384 23.0; 1536 x 1536 x 7168, tiles 9.5, 192 11.8).
 //  - up to 128 rows, one column tile, split or not: 170 ns a step of the longest
 //    rank and the joining of the ranks' sums, which grows with the columns (1 x 1536
 //    x 7168: 4.0 split, 7.3 us whole; 128 x 1000 x 1112: 6.4 against 5.3).
@@ -986,12 +1011,13 @@ MgPlan choose_plan(int M, int N, int nks, int sms, bool bf16)
     const struct {
         MgPlan plan;
         long tiles, at_once, start, step, tile;  // ns
-    } forms[3] = {{{false, 128, 1}, tn * (((long)M + 127) / 128), sms, 2610, 199, bf16 ? 840 : 1280},
-                  {{true, 192, 1}, tm * (((long)N + 191) / 192), pairs, 3430, 252, bf16 ? 680 : 1600},
-                  {{true, 256, 1}, tm * (((long)N + 255) / 256), pairs, 3570, 284, bf16 ? 880 : 2130}};
+    } forms[4] = {{{false, 128, 1}, tn * (((long)M + 127) / 128), sms, 2610, 199, bf16 ? 840 : 1280},
+                  {{true, 192, 1}, tm * (((long)N + 191) / 192), pairs, 4400, 252, bf16 ? 640 : 1250},
+                  {{true, 256, 1}, tm * (((long)N + 255) / 256), pairs, 4400, 284, bf16 ? 950 : 2000},
+                  {{true, 384, 1}, tm * (((long)N + 383) / 384), pairs, 4400, 410, bf16 ? 2000 : 3300}};
     int best = 0;
     long cost = 0;
-    for (int i = 0; i < 3; i++) {
+    for (int i = 0; i < 4; i++) {
         const auto &f = forms[i];
         const long c = f.start + (f.tiles + f.at_once - 1) / f.at_once * (f.step * nks + f.tile);
         if (!i || c < cost) cost = c, best = i;
@@ -1004,7 +1030,9 @@ int launch_ct(const k3moe_mx_operand *A, const k3moe_mx_operand *B, const MgArgs
 {
     const MgPlan p = choose_plan(a.M, a.N, a.nks, num_sms(), sizeof(CT) == 2);
     if (p.pair)
-        return p.nt == 256 ? launch_pair<256, CT>(A, B, a, s) : launch_pair<192, CT>(A, B, a, s);
+        return p.nt == 384   ? launch_pair<384, CT>(A, B, a, s)
+               : p.nt == 256 ? launch_pair<256, CT>(A, B, a, s)
+                             : launch_pair<192, CT>(A, B, a, s);
     switch (p.nt) {
     case 16: return launch_nt<16, CT>(A, B, a, p.ranks, s);
     case 32: return launch_nt<32, CT>(A, B, a, p.ranks, s);

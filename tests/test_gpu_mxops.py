@@ -287,7 +287,9 @@ def test_other_stream_and_graph():
 @pytest.mark.parametrize("M,N,K,pad", [(2048, 1537, 160, 0), (1100, 3333, 512, 3), (4096, 1000, 288, 8), (3000, 2064, 64, 0),
                                        (257, 12000, 1056, 1), (2500, 1300, 1, 4), (4096, 1537, 2100, 0),
                                        (2300, 3333, 1500, 3), (1500, 7001, 900, 8), (2500, 7168, 260, 0),
-                                       (9000, 5000, 96, 0), (3001, 4600, 1056, 2)])
+                                       (9000, 5000, 96, 0), (3001, 4600, 1056, 2),
+                                       (2304, 2901, 2500, 3), (2200, 2950, 4000, 2), (4095, 1536, 7168, 8),
+                                       (2100, 5400, 10000, 0)])
 def test_matmul_pairs(M, N, K, pad, out):
     """Products large enough for CTA pairs: rows of C aligned for wide stores or
     not, ragged row and column tiles of every width, a K of one block and less."""
