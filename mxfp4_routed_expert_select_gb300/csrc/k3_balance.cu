@@ -29,8 +29,11 @@ namespace {
 
 constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;  // backward: three CTAs per SM
 // Forward: one CTA per SM, so that half as many sums meet in global atomics as
-// with two of 256 threads.
-constexpr int BF_THREADS = 512, BF_WARPS = BF_THREADS / 32;
+// with two of 256 threads.  Its rows cost latency (two reductions each), so more
+// warps help until the joining of their sums costs as much: 16384 x 896 fp32 takes
+// 14.8 us with 16 warps, 13.2 with 20, 14.0 with 24 (a third row in flight per warp
+// changed nothing).
+constexpr int BF_THREADS = 640, BF_WARPS = BF_THREADS / 32;
 
 // Workspace: fixed-point sums [E], counts [E], valid tokens, a flag for
 // non-finite sums, the ticket.
@@ -355,8 +358,8 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
                         at = 1.f;
                     }
                     // slots with the same id are added in slot order by the first
-                    const unsigned same = __match_any_sync(0xffffffffu, sl.id >= 0 ? sl.id : -1 - lane);
-                    if (__any_sync(0xffffffffu, __popc(same) > 1)) {
+                    const unsigned same = __match_any_sync(0xffffffffu, sl.id);
+                    if (__any_sync(0xffffffffu, sl.id >= 0 && __popc(same) > 1)) {
                         float s = 0.f;
                         for (int j = 0; j < a.k; j++) {
                             const float cj = __shfl_sync(0xffffffffu, c, j);
