@@ -362,6 +362,8 @@ class MxOperand:
         nc, na = lib().k3moe_mx_operand_codes_bytes(rows, in_), lib().k3moe_mx_operand_atoms_bytes(rows, in_)
         if nc < 0 or na < 0:
             raise K3Error(K3MOE_EINVAL, "MxOperand(%d, %d)" % (rows, in_))
+        if codes is not None and (codes.dtype is not torch.uint8 or codes.numel() != nc or not codes.is_contiguous()):
+            raise ValueError("expected %d contiguous bytes of codes, got %s %s" % (nc, codes.dtype, tuple(codes.shape)))
         self.rows, self.in_ = rows, in_
         self.codes = torch.empty(nc, dtype=torch.uint8, device=device) if codes is None else codes
         self.atoms = torch.empty(na, dtype=torch.uint8, device=self.codes.device)

@@ -140,3 +140,14 @@ def test_binding_refuses_other_tensors():
     with pytest.raises(ValueError):
         k._flat(x, torch.int32, 4, 8)
     assert k._ld(x[:1, :3], 1, 3) == 8 and k._ld(x[:, :1], 4, 1) == 8
+
+
+def test_operand_codes_of_the_wrong_size():
+    """Codes given by the caller are the operand's bytes, all of them."""
+    torch = pytest.importorskip("torch")
+    ok = k.MxOperand(3, 33, codes=torch.empty(3, 32, dtype=torch.uint8))
+    assert ok.atoms.numel() == k.lib().k3moe_mx_operand_atoms_bytes(3, 33)
+    for bad in (torch.empty(3, 31, dtype=torch.uint8), torch.empty(3, 32, dtype=torch.int8),
+                torch.empty(32, 3, dtype=torch.uint8).t(), torch.empty(0, dtype=torch.uint8)):
+        with pytest.raises(ValueError):
+            k.MxOperand(3, 33, codes=bad)
