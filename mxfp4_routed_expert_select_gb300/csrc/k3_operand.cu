@@ -88,6 +88,7 @@ K3_DEV void copy16(uint32_t dst, const void *p, int n)
 // fp32 column, and 4 that move each row on by 16 bytes of banks.
 template <typename XT>
 constexpr int tile_pitch() { return QT * (int)sizeof(XT) / 4 + 4; }
+constexpr int DQ_U = 2;       // dequantise: 16-value units of a thread in flight
 constexpr int CODE_PITCH = 80;  // bytes of one column's staged codes (64, and 16 to spread the banks)
 template <typename XT>
 constexpr int quant_smem() { return QT * tile_pitch<XT>() * 4 + QT * CODE_PITCH; }
@@ -254,28 +255,43 @@ __global__ void __launch_bounds__(128) k3_mx_scale_atoms(const uint8_t *scales, 
     *(uint32_t *)(atoms + (long)blockIdx.x * 512 + op_atom_byte(threadIdx.x, 0)) = w;
 }
 
-// The values of an operand: eight per thread (one code word) where the rows of
-// y are 16-byte aligned, else two per thread, so that a warp's stores stay next
-// to each other.
+// 32 bytes to an address of that alignment.
+K3_DEV void st32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// The values of an operand: units of 16 per thread (two code words, half a block)
+// where the rows of y are 16-byte aligned, stored 32 bytes at a time where they are
+// 32-byte aligned (wide), else two values per thread, so that a warp's stores stay
+// next to each other.  HBM writes bound it, and with units of eight values the
+// addresses' instructions did: 4096 x 7168 to bf16 took 10.6 us, 9.2 so (9.7 and 9.5
+// with four and one units in flight).
 template <typename YT, bool VEC>
 __global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, const uint8_t *atoms, int r0,
                                                         uint32_t n, FastDiv upr, int nk, int in, YT *y, long ld,
-                                                        bool spread)
+                                                        bool spread, bool wide)
 {
     griddep_wait();
-    constexpr int UB = VEC ? 4 : 1, U = 4;  // code bytes of a unit, units of a thread in flight
+    constexpr int UV = VEC ? 16 : 2, U = VEC ? DQ_U : 4;  // values of a unit, units of a thread in flight
     // a thread's units lie 256 apart (a CTA's are then one run), or, when that would
     // leave SMs idle, a grid apart
     const uint32_t gap = spread ? gridDim.x * 256 : 256;
     for (uint32_t i0 = blockIdx.x * (spread ? 256 : U * 256) + threadIdx.x; i0 < n; i0 += gridDim.x * U * 256) {
-        uint32_t word[U], scale[U];
+        uint2 word[U];
+        uint32_t scale[U];
         int r[U], c[U];
 #pragma unroll
         for (int u = 0; u < U; u++) {
             const uint32_t i = min(i0 + u * gap, n - 1), q = upr.div(i);
-            r[u] = r0 + (int)q, c[u] = (int)(i - q * upr.d) * 2 * UB;
+            r[u] = r0 + (int)q, c[u] = (int)(i - q * upr.d) * UV;
             const int b = c[u] >> 5;
-            word[u] = VEC ? *(const uint32_t *)(codes + 4 * (size_t)i) : (uint32_t)codes[i];
+            if constexpr (VEC)
+                word[u] = ((const uint2 *)codes)[i];
+            else
+                word[u].x = codes[i];
             scale[u] = atoms[((size_t)(r[u] >> 7) * nk + (b >> 2)) * 512 + op_atom_byte(r[u], b)];
         }
 #pragma unroll
@@ -285,39 +301,39 @@ __global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, co
             YT *o = y + (long)r[u] * ld + c[u];
             const int left = in - c[u];
             if constexpr (VEC) {
-                uint32_t h[4];
-                e2m1x8_to_half2x4(word[u], h[0], h[1], h[2], h[3]);
-                float v[8];
+                uint32_t h[8], w[16 * sizeof(YT) / 4];
+                e2m1x8_to_half2x4(word[u].x, h[0], h[1], h[2], h[3]);
+                e2m1x8_to_half2x4(word[u].y, h[4], h[5], h[6], h[7]);
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const float2 f = h2f2(h[j]);
-                    v[2 * j] = f.x * s;
-                    v[2 * j + 1] = f.y * s;
-                }
-                if constexpr (sizeof(YT) == 2) {
-                    uint32_t p[4];  // an E2M1 value times a power of two is exact in bf16
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const __nv_bfloat162 t = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
-                        p[j] = *(const uint32_t *)&t;
+                for (int j = 0; j < 8; j++) {
+                    float2 f = h2f2(h[j]);
+                    scale2(f.x, f.y, s);
+                    if constexpr (sizeof(YT) == 2) {  // an E2M1 value times a power of two is exact in bf16
+                        const __nv_bfloat162 t = __floats2bfloat162_rn(f.x, f.y);
+                        w[j] = *(const uint32_t *)&t;
+                    } else {
+                        w[2 * j] = __float_as_uint(f.x), w[2 * j + 1] = __float_as_uint(f.y);
                     }
-                    if (left >= 8)
-                        *(uint4 *)o = make_uint4(p[0], p[1], p[2], p[3]);
-                    else
+                }
+                constexpr int NW = sizeof(w) / 4;
+                if (left >= 16 && wide) {
 #pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            if (j < left) o[j] = (YT)(p[j >> 1] >> (16 * (j & 1)));
+                    for (int j = 0; j < NW; j += 8) st32((uint32_t *)o + j, w + j);
+                } else if (left >= 16) {
+#pragma unroll
+                    for (int j = 0; j < NW; j += 4) ((uint4 *)o)[j / 4] = make_uint4(w[j], w[j + 1], w[j + 2], w[j + 3]);
                 } else {
-                    if (left >= 8) {
-                        ((float4 *)o)[0] = make_float4(v[0], v[1], v[2], v[3]);
-                        ((float4 *)o)[1] = make_float4(v[4], v[5], v[6], v[7]);
-                    } else
 #pragma unroll
-                        for (int j = 0; j < 8; j++)
-                            if (j < left) o[j] = v[j];
+                    for (int j = 0; j < 15; j++)
+                        if (j < left) {
+                            if constexpr (sizeof(YT) == 2)
+                                o[j] = (YT)(w[j >> 1] >> (16 * (j & 1)));
+                            else
+                                o[j] = __uint_as_float(w[j]);
+                        }
                 }
             } else {
-                const float2 f = e2m1x2_to_float2(word[u]);
+                const float2 f = e2m1x2_to_float2(word[u].x);
 #pragma unroll
                 for (int j = 0; j < 2; j++)
                     if (j < left) {
@@ -332,7 +348,7 @@ __global__ void __launch_bounds__(256) k3_mx_dequantize(const uint8_t *codes, co
     }
 }
 
-bool rows_aligned16(const void *p, long ld, int es) { return ((uintptr_t)p & 15u) == 0 && (ld * es) % 16 == 0; }
+bool rows_aligned(const void *p, long ld, int es, int n) { return (uintptr_t)p % n == 0 && (ld * es) % n == 0; }
 
 }  // namespace
 
@@ -353,7 +369,7 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
     a.tiles_x = FastDiv((uint32_t)tiles_x);
     const long tiles = (long)tiles_x * (col ? op_k_atoms(rows) : op_row_tiles(rows));
     if (tiles > 0x3fffffffL) return K3MOE_EINVAL;
-    const bool vec = rows_aligned16(x, ld, xdt == K3MOE_BF16 ? 2 : 4);
+    const bool vec = rows_aligned(x, ld, xdt == K3MOE_BF16 ? 2 : 4, 16);
     const size_t sm = xdt == K3MOE_BF16 ? quant_smem<uint16_t>() : quant_smem<uint32_t>();
     void (*const kernel)(QuantArgs) =
         xdt == K3MOE_BF16 ? (vec ? k3_mx_quantize_operand<uint16_t, true> : k3_mx_quantize_operand<uint16_t, false>)
@@ -377,15 +393,17 @@ template <typename YT, bool VEC>
 static int launch_dequantize(const k3moe_mx_operand *op, YT *y, long ld, cudaStream_t s)
 {
     // one launch per block of rows whose units fit 31 bits
-    const uint32_t upr = (uint32_t)op_in_padded(op->in) / (VEC ? 8 : 2);
+    const uint32_t upr = (uint32_t)op_in_padded(op->in) / (VEC ? 16 : 2);
     const int rows = (int)std::min<long>(op->rows, std::max<long>(1, (1L << 30) / upr));
     for (int r = 0; r < op->rows; r += rows) {
         const uint32_t n = (uint32_t)std::min(rows, op->rows - r) * upr;
-        const bool spread = n < 1024u * (unsigned)num_sms();
-        const unsigned grid = (unsigned)std::min<long>(spread ? (n + 255) / 256 : (n + 1023) / 1024, 16L * num_sms());
+        constexpr uint32_t CTA = 256 * (VEC ? DQ_U : 4);
+        const bool spread = n < CTA * (unsigned)num_sms();
+        const unsigned grid = (unsigned)std::min<long>(spread ? (n + 255) / 256 : (n + CTA - 1) / CTA, 16L * num_sms());
         if (launch_pdl(k3_mx_dequantize<YT, VEC>, dim3(grid), dim3(256), 0, s,
                        (const uint8_t *)op->codes + (size_t)r * (op_in_padded(op->in) / 2), (const uint8_t *)op->atoms,
-                       r, n, FastDiv(upr), op_k_atoms(op->in), op->in, y, ld, spread) != cudaSuccess) {
+                       r, n, FastDiv(upr), op_k_atoms(op->in), op->in, y, ld, spread,
+                       rows_aligned(y, ld, (int)sizeof(YT), 32)) != cudaSuccess) {
             cudaGetLastError();
             return K3MOE_ECUDA;
         }
@@ -395,7 +413,7 @@ static int launch_dequantize(const k3moe_mx_operand *op, YT *y, long ld, cudaStr
 
 int launch_mx_dequantize(const k3moe_mx_operand *op, void *y, int ydt, long ld, cudaStream_t s)
 {
-    const bool vec = rows_aligned16(y, ld, ydt == K3MOE_BF16 ? 2 : 4);
+    const bool vec = rows_aligned(y, ld, ydt == K3MOE_BF16 ? 2 : 4, 16);
     if (ydt == K3MOE_BF16)
         return vec ? launch_dequantize<uint16_t, true>(op, (uint16_t *)y, ld, s)
                    : launch_dequantize<uint16_t, false>(op, (uint16_t *)y, ld, s);

@@ -114,7 +114,8 @@ def test_nonfinite_block_reads_back_as_nan_and_spreads_to_its_products(bad):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("rows,n,pad", [(1, 1, 0), (3, 33, 0), (130, 300, 5), (256, 512, 8)])
+@pytest.mark.parametrize("rows,n,pad", [(1, 1, 0), (3, 33, 0), (130, 300, 5), (256, 512, 8), (40, 300, 4),
+                                        (133, 1000, 0), (70, 49, 7), (9, 47, 9), (5, 290, 6)])
 def test_dequantize(rows, n, pad, dt):
     op = k.MxOperand(rows, n)
     k.mx_quantize_operand(_x(rows, n, torch.float32, 11), op)
@@ -123,6 +124,23 @@ def test_dequantize(rows, n, pad, dt):
     codes, scales = ref.quantize(_np(_x(rows, n, torch.float32, 11)))
     assert np.array_equal(_np(y[:, :n]).astype(np.float64), ref.values(codes, scales)[:, :n])
     assert bool((y[:, n:] == 77).all())
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_dequantize_many_units_per_thread(dt):
+    """A matrix of more units than the grid has threads, against its row blocks."""
+    rows, n = 4100, 5216
+    x = _x(rows, n, torch.float32, 12)
+    op = k.MxOperand(rows, n)
+    k.mx_quantize_operand(x, op)
+    y = torch.empty(rows, n, dtype=DT[dt], device="cuda")
+    k.mx_dequantize(y, op)
+    for r in range(0, rows, 1000):
+        part = x[r:r + 1000]
+        op, want = k.MxOperand(part.shape[0], n), torch.empty_like(y[r:r + 1000])
+        k.mx_quantize_operand(part, op)
+        k.mx_dequantize(want, op)
+        assert torch.equal(y[r:r + 1000], want)
 
 
 def _bound(a, b, out):
