@@ -400,6 +400,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         constexpr uint32_t SD = C::STAGE / 16;  // descriptor words between stages
         for (int u = first; u < a.n_tiles && ok; u += step, ut++) {
             const int buf = (int)(ut & 1);
+            // a 64-column tile starts at a half of a scale atom's rows every other time
+            const uint32_t shift = NT < 64 ? 0u : (uint32_t)(((u % a.tiles_t) * NT % 128) / 32);
             if (ut >= 2 && !__all_sync(0xffffffffu, tc_wait(bar(B_ACCE + buf), (ut / 2 - 1) & 1, a.err, abort_flag)))
                 break;
             tc_fence_after();
@@ -414,7 +416,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 // look at the next stage while this one is issued
                 ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
                 mg_step<1, NT>(tmem + (uint32_t)(buf * NT), slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
-                                  slo + C::OFF_SA / 16 + (uint32_t)s * SD, tmem + (uint32_t)(C::SF0 + C::SF * s), 0u,
+                                  slo + C::OFF_SA / 16 + (uint32_t)s * SD, tmem + (uint32_t)(C::SF0 + C::SF * s), shift,
                                   ks > k0 ? 1u : 0u);
                 mma_commit(bar(B_EMPTY + s));
                 s = sn;
@@ -991,6 +993,10 @@ struct MgPlan {
 //    one (us: 2048 x 1536 x 7168 bf16, 192 columns 12.0, one wave of 256 13.3, tiles
 //    15.6; 4096 x 1536 x 7168, one wave of 384 17.9, two of 192 19.4; 4096 x 7168 x
 //    1536, 256 20.2, 192 21.6, 384 23.0; 1536 x 1536 x 7168, tiles 9.5, 192 11.8).
+//    A long K over few tiles is split (fitted to 5 shapes of 160 to 333 rows, 64 or
+//    128 columns, 2 or 4 ranks, no more CTAs than SMs: 160 x 1536 x 7168 bf16, 64
+//    columns over 4 ranks 7.3, whole tiles 9.3; 333 rows, 128 over 4, 8.6 and 9.4;
+//    512 rows, 128 over 2, 10.0 and 9.2).
 //  - up to 128 rows, one column tile, split or not: 170 ns a step of the longest
 //    rank and the joining of the ranks' sums, which grows with the columns (1 x 1536
 //    x 7168: 4.0 split, 7.3 us whole; 128 x 1000 x 1112: 6.4 against 5.3).
@@ -1022,7 +1028,13 @@ MgPlan choose_plan(int M, int N, int nks, int sms, bool bf16)
         const long c = f.start + (f.tiles + f.at_once - 1) / f.at_once * (f.step * nks + f.tile);
         if (!i || c < cost) cost = c, best = i;
     }
-    return forms[best].plan;
+    MgPlan plan = forms[best].plan;
+    for (int nt = 64; nt <= 128; nt += 64)
+        for (int r = 2; r <= 4 && r <= nks && tn * ((M + nt - 1) / nt) * r <= sms; r *= 2) {
+            const long c = (nt == 64 ? 4400 + 200 * r : 4800 + 300 * r) + (nt == 64 ? 270 : 320) * (long)((nks + r - 1) / r);
+            if (c < cost) cost = c, plan = {false, nt, r};
+        }
+    return plan;
 }
 
 template <typename CT>

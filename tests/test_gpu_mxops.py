@@ -328,6 +328,27 @@ def test_matmul_pairs(M, N, K, pad, out):
     assert k.device_error() == 0
 
 
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K,pad", [(129, 1536, 7168, 0), (160, 1001, 7000, 3), (192, 1536, 5000, 4), (255, 1400, 7168, 0),
+                                       (333, 1500, 8200, 1), (160, 128, 4000, 0), (300, 37, 9000, 2), (1000, 130, 9000, 0)])
+def test_matmul_split_beyond_one_row_tile(M, N, K, pad, out):
+    """A long K split over CTAs, several tiles of 64 and 128 rows of A."""
+    A, B, va, vb = _operands(M, N, K, M + N)
+    C = torch.full((M, N + pad), 5.0, dtype=DT[out], device="cuda")
+    k.mx_matmul(C[:, :N], A, B)
+    want = va @ vb.T
+    tol = _bound(va, vb, out)
+    assert bool((np.abs(_np(C[:, :N]).astype(np.float64) - want) <= tol).all())
+    assert bool((C[:, N:] == 5).all())
+    again = torch.empty_like(C)
+    k.mx_matmul(again[:, :N], A, B)
+    assert torch.equal(again[:, :N], C[:, :N])
+    if out == "f32":
+        k.mx_matmul(C[:, :N], A, B, accumulate=True)
+        assert bool((np.abs(_np(C[:, :N]).astype(np.float64) - 2 * want) <= 2 * tol + np.abs(want) * 2.0 ** -23).all())
+    assert k.device_error() == 0
+
+
 def test_matmul_nan_stays_in_its_rows_and_columns():
     """Non-finite blocks in a CTA-pair product reach their own row and column only
     (tiles reach past the matrices, and the tail of K past the blocks)."""
