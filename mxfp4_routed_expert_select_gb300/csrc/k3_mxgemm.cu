@@ -298,7 +298,7 @@ struct MgCfg {
     static constexpr int TX = OFF_TA + 1024;                 // bytes copied per stage
     static constexpr int STAGE = (TX + 1023) / 1024 * 1024;
     // Split CTAs share an SM in pairs where the stages allow it.
-    static constexpr int NS = !SPLIT ? 6 : NT == 128 ? 3 : NT <= 16 ? 5 : 4;
+    static constexpr int NS = !SPLIT ? 6 : NT <= 16 ? 5 : 4;
     // TMEM: the accumulators (two of NT columns, one when split), then each
     // stage's scales.
     static constexpr int SF = 16;
@@ -956,7 +956,9 @@ int launch_tiles(const k3moe_mx_operand *A, const k3moe_mx_operand *B, MgArgs a,
 template <int NT, typename CT>
 int launch_nt(const k3moe_mx_operand *A, const k3moe_mx_operand *B, const MgArgs &a, int ranks, cudaStream_t s)
 {
-    return ranks > 1 ? launch_tiles<NT, true, CT>(A, B, a, ranks, s) : launch_tiles<NT, false, CT>(A, B, a, 1, s);
+    if constexpr (NT <= 64)
+        if (ranks > 1) return launch_tiles<NT, true, CT>(A, B, a, ranks, s);
+    return launch_tiles<NT, false, CT>(A, B, a, 1, s);
 }
 
 template <int NT, typename CT>
@@ -985,56 +987,48 @@ struct MgPlan {
     int nt, ranks;
 };
 
-// The form by a model of its time, fitted on one GB300.
-//  - above 128 rows of A, tiles or pairs: a start, and for every wave of tiles over
-//    the SMs a time per k-step and one per tile (more in fp32).  Fitted to 27
-//    products of 200 to 8192 rows, 1024 to 20000 columns and K 256 to 8192, each run
-//    in all four forms: the choice was the fastest form or within 4% of it in every
-//    one (us: 2048 x 1536 x 7168 bf16, 192 columns 12.0, one wave of 256 13.3, tiles
-//    15.6; 4096 x 1536 x 7168, one wave of 384 17.9, two of 192 19.4; 4096 x 7168 x
-//    1536, 256 20.2, 192 21.6, 384 23.0; 1536 x 1536 x 7168, tiles 9.5, 192 11.8).
-//    A long K over few tiles is split (fitted to 5 shapes of 160 to 333 rows, 64 or
-//    128 columns, 2 or 4 ranks, no more CTAs than SMs: 160 x 1536 x 7168 bf16, 64
-//    columns over 4 ranks 7.3, whole tiles 9.3; 333 rows, 128 over 4, 8.6 and 9.4;
-//    512 rows, 128 over 2, 10.0 and 9.2).
-//  - up to 128 rows, one column tile, split or not: 170 ns a step of the longest
-//    rank and the joining of the ranks' sums, which grows with the columns (1 x 1536
-//    x 7168: 4.0 split, 7.3 us whole; 128 x 1000 x 1112: 6.4 against 5.3).
+// The form by a model of its time, fitted on one GB300: a start, and for every wave of
+// tiles over the SMs a time per k-step and one per tile.  Forms: narrow tiles (as
+// many columns as there are rows of A, 64 at most), tiles of 128 columns, pairs of
+// 192, 256 and 384.  Few narrow tiles with a long K are split over 2 to 8 CTAs, no
+// more than there are SMs (two per SM lost: 32 x 4096 x 4096 over 8 took 7.1 us, over
+// 4 5.1, whole 5.6); the join grows with the ranks and columns.
+// Fitted to 27 products of 200 to 8192 rows, 1024 to 20000 columns and K 256 to 8192,
+// 54 of 65 to 1024 rows and 48 of 1 to 128, in bf16 and fp32, each run in every form:
+// the choice was the fastest form or within 5% of it in nearly all.  Some, in us:
+//   1 x 1536 x 7168      narrow over 8 4.6, whole 7.5
+//   128 x 1536 x 7168    narrow over 4 6.7, whole 8.2, 128 columns over 8 7.8
+//   512 x 2048 x 2048    narrow 4.5, 128 columns 5.4
+//   1536 x 1536 x 7168   128 columns 9.5, pairs of 192 11.8
+//   2048 x 1536 x 7168   pairs of 192 12.0, one wave of 256 13.3, 128 columns 15.6
+//   4096 x 1536 x 7168   pairs of 384, one wave, 17.9, 192, two waves, 19.4
+//   4096 x 7168 x 1536   pairs of 256 20.2, 192 21.6, 384 23.0
 MgPlan choose_plan(int M, int N, int nks, int sms, bool bf16)
 {
-    const long tn = ((long)N + MG_M - 1) / MG_M;
-    if (M <= 128) {
-        MgPlan best = {false, M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128, 1};
-        const long join = best.nt == 16 ? 700 : best.nt == 32 ? 900 : best.nt == 64 ? 1500 : 3000;
-        long cost = 170L * nks;
-        for (int r = 2; r <= MG_MAX_RANKS && r <= nks && tn * r <= 2L * sms; r *= 2) {
-            const long c = 170L * ((nks + r - 1) / r) + join;
-            if (c < cost) cost = c, best.ranks = r;
-        }
-        return best;
-    }
-    const long tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M), pairs = std::max(1, sms / 2);
+    const int nt = M <= 16 ? 16 : M <= 32 ? 32 : 64;
+    const long tn = ((long)N + MG_M - 1) / MG_M, tm = ((long)M + 2 * MG_M - 1) / (2 * MG_M);
+    const long pairs = std::max(1, sms / 2);
     const struct {
         MgPlan plan;
         long tiles, at_once, start, step, tile;  // ns
-    } forms[4] = {{{false, 128, 1}, tn * (((long)M + 127) / 128), sms, 2610, 199, bf16 ? 840 : 1280},
+    } forms[5] = {{{false, nt, 1}, tn * ((M + nt - 1L) / nt), sms, nt == 64 ? 2650 : 2400, nt == 64 ? 185 : 170,
+                   nt < 64 ? 350 : bf16 ? 400 : 450},
+                  {{false, 128, 1}, tn * (((long)M + 127) / 128), sms, 2610, 199, bf16 ? 840 : 1000},
                   {{true, 192, 1}, tm * (((long)N + 191) / 192), pairs, 4400, 252, bf16 ? 640 : 1250},
                   {{true, 256, 1}, tm * (((long)N + 255) / 256), pairs, 4400, 284, bf16 ? 950 : 2000},
                   {{true, 384, 1}, tm * (((long)N + 383) / 384), pairs, 4400, 410, bf16 ? 2000 : 3300}};
-    int best = 0;
+    MgPlan best = forms[0].plan;
     long cost = 0;
-    for (int i = 0; i < 4; i++) {
-        const auto &f = forms[i];
+    for (const auto &f : forms) {
         const long c = f.start + (f.tiles + f.at_once - 1) / f.at_once * (f.step * nks + f.tile);
-        if (!i || c < cost) cost = c, best = i;
+        if (!cost || c < cost) cost = c, best = f.plan;
     }
-    MgPlan plan = forms[best].plan;
-    for (int nt = 64; nt <= 128; nt += 64)
-        for (int r = 2; r <= 4 && r <= nks && tn * ((M + nt - 1) / nt) * r <= sms; r *= 2) {
-            const long c = (nt == 64 ? 4400 + 200 * r : 4800 + 300 * r) + (nt == 64 ? 270 : 320) * (long)((nks + r - 1) / r);
-            if (c < cost) cost = c, plan = {false, nt, r};
-        }
-    return plan;
+    const long start = nt == 16 ? 3900 : nt == 32 ? 4300 : 4600, rank = nt == 16 ? 40 : nt == 32 ? 60 : 100;
+    for (int r = 2; r <= MG_MAX_RANKS && r <= nks && forms[0].tiles * r <= sms; r *= 2) {
+        const long c = start + rank * r + (nt == 64 ? 225L : 170L) * ((nks + r - 1) / r);
+        if (c < cost) cost = c, best = {false, nt, r};
+    }
+    return best;
 }
 
 template <typename CT>
