@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_m
 #pragma unroll
             for (int i = 0; i < QT / RS; i++, p += pass) copy16(dst + (uint32_t)(i * RS * PITCH * 4), p);
         } else {
-            const int bytes = min(max((a.cols - c0) * ES - 16 * u, 0), 16);
+            // counted in elements up to a unit's: the bytes of a row do not fit 32 bits
+            const int bytes = min(max(a.cols - c0 - u * (16 / ES), 0), 16 / ES) * ES;
 #pragma unroll
             for (int i = 0; i < QT / RS; i++, p += pass) {
                 const bool in = bytes > 0 && r0 + r + i * RS < a.rows;
