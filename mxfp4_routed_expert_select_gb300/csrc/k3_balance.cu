@@ -145,30 +145,29 @@ K3_DEV void read_row(const BalanceArgs &a, int t, const uint8_t *buf, int lane, 
 
 // Logits to unnormalised probabilities; inv makes them sum to 1.  False (and
 // nothing done) for a row of -inf.  SIG: the sigmoid rules.
-// Softmax: e^(l - m) as 2^(l log2 e - m log2 e), the product exact in the fused
-// step: the rounding of m log2 e is one factor of the whole row, and that of the
-// exponent t costs p at most t 2^-24, so at most 2^-24 of the row's largest p.
+// Softmax: e^(l - m) as 2^((l - m) log2 e) by the one-instruction exponential
+// (2^-22).  The difference comes first: the product of a large m alone is off by
+// more than an exponent can hold (from about 2^31 on) or infinite.  The roundings
+// of the difference t, of the constant and of the product cost p at most 3 t 2^-24
+// of itself, so about 2^-24 of the row's largest p.
 template <bool SIG>
-K3_DEV float unnormalised(float l, float shift)
+K3_DEV float unnormalised(float l, float m)
 {
-    return SIG ? scaled_sigmoid(l, shift) : exp2_fast(__fmaf_rn(l, LOG2E, shift));
+    return SIG ? scaled_sigmoid(l, m) : exp2_fast((l - m) * LOG2E);
 }
 template <int NV, bool SIG>
-K3_DEV bool row_probs(float (&v)[4 * NV], float &inv, float &shift)
+K3_DEV bool row_probs(float (&v)[4 * NV], float &inv, float &m)
 {
-    float m = v[0];
+    m = v[0];
 #pragma unroll
     for (int i = 1; i < 4 * NV; i++) m = max_nan(m, v[i]);
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
     if (m == -INFINITY) return false;
-    if constexpr (SIG)
-        shift = fminf(m, 0.f);  // a NaN among the logits is still in the sum
-    else
-        shift = m == INFINITY ? __uint_as_float(0x7fc00000u) : -m * LOG2E;  // inf - inf
+    if constexpr (SIG) m = fminf(m, 0.f);  // a NaN among the logits is still in the sum
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4 * NV; i++) s += v[i] = unnormalised<SIG>(v[i], shift);
+    for (int i = 0; i < 4 * NV; i++) s += v[i] = unnormalised<SIG>(v[i], m);
     inv = 1.f / warp_sum(s);
     return true;
 }
@@ -213,9 +212,9 @@ __global__ void __launch_bounds__(BF_THREADS, 1) k3_balance_forward(const Balanc
             __syncwarp();
         }
         if (on) {
-            float v[4 * NV], inv, shift;
+            float v[4 * NV], inv, m;
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
-            if (row_probs<NV, SIG>(v, inv, shift)) {
+            if (row_probs<NV, SIG>(v, inv, m)) {
                 mine++;
 #pragma unroll
                 for (int i = 0; i < 4 * NV; i++) acc[i] += v[i] * inv;
@@ -329,7 +328,7 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
             __syncwarp();
         }
         T *o = (T *)a.dlogits + (long)t * a.ldd;
-        float v[4 * NV], inv, shift;
+        float v[4 * NV], inv, m;
         bool valid = on, first = false;
         float at = 0.f;  // the whole gradient of this lane's chosen expert
         if (on) {
@@ -337,7 +336,7 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
             float lj = 0.f;
             if (sl.id >= 0) lj = a.vec ? load1<T>(buf + b * rb, sl.id) : load1<T>(a.logits, (long)t * a.ld + sl.id);
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
-            valid = row_probs<NV, SIG>(v, inv, shift);
+            valid = row_probs<NV, SIG>(v, inv, m);
             if (valid) {
                 float dot = 0.f;  // <f - 1, unnormalised p>
 #pragma unroll
@@ -370,7 +369,7 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
                         c = s;
                     }
                     first = sl.id >= 0 && (same & ((1u << lane) - 1u)) == 0u;
-                    at = unnormalised<SIG>(lj, shift) * (f1[max(sl.id, 0)] * c1 + c0) * at + c;
+                    at = unnormalised<SIG>(lj, m) * (f1[max(sl.id, 0)] * c1 + c0) * at + c;
                 }
 #pragma unroll
                 for (int i = 0; i < NV; i++) {
