@@ -712,7 +712,9 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *h
  *  g, u, h, dh, dg, du  [T][f], all of one type (K3MOE_F32 or K3MOE_BF16) in a
  *              call, each with its own row stride >= f elements (gate and up may
  *              be halves of one tensor), aligned to the element size; fp32
- *              arithmetic, rounded once
+ *              arithmetic (sigma to 2^-21 of itself for fp32 data, 2^-18 for bf16),
+ *              rounded once; sigma below the smallest normal fp32 number keeps its
+ *              products with g, u and dh
  *  ckpt        device, k3moe_swiglu_ckpt_bytes(T, f) bytes, 16-byte aligned
  * In the backward call dg or du may be dh itself with the same stride.
  * Errors: K3MOE_EINVAL for null or misaligned pointers, T or f outside 1 .. 2^30,

@@ -157,13 +157,28 @@ K3_DEV void from_e4m3x8(uint2 q, uint32_t e, float (&v)[8])
         v[2 * i + 1] = f.y * s;
     }
 }
-// sigma(g); 0 where e^-g overflows.  bf16 data (2^-8) takes the fast exponential
-// (an argument rounded to 2^-24 of itself: 2^-19 of sigma over the range where it
-// matters): with the full one the forward pass was bound by issue.
+// sigma(g) for |g| <= 56 (near() below).  bf16 data (2^-8) takes the fast
+// exponential: its argument is rounded to 2^-24 of itself, 2^-18 of sigma at -56 and
+// 2^-21 at -8; with the full one the forward pass was bound by issue.
 template <typename T>
 K3_DEV float sigmoid(float g)
 {
     return rcp_fast(1.f + (sizeof(T) == 2 ? exp2_fast(-LOG2E * g) : expf(-g)));
+}
+// Does a block's scale byte say that its gates are at most 448 * 2^-3 = 56?
+K3_DEV bool near(uint32_t eg) { return eg <= 124u; }
+// Any gate: sigma = q f^2 and 1 - sigma = r with f = e^(-|g|/2) for g < 0 and 1 for
+// g >= 0, q = 1 / (1 + e^-|g|).  sigma leaves the normal fp32 numbers below -87 while
+// its products with g, u and dh need not, so each factor f goes to one of them.
+// Blocks of such gates are rare, and one branch on their scale byte leaves the
+// others their time.
+struct Sigma {
+    float f, q, r;
+};
+K3_DEV Sigma sigma_far(float g)
+{
+    const float e = expf(-0.5f * fabsf(g)), q = rcp_fast(1.f + e * e);
+    return g < 0.f ? Sigma{e, q, q} : Sigma{1.f, q, e * e * q};
 }
 
 // Chunk i of a launch as (row, column); from `end` on the column is f.
@@ -197,8 +212,16 @@ __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_forward(const SwigluArgs
         const uint2 qg = e4m3x8(g, eg), qu = e4m3x8(u, eu);
         if (i < end) {
             float h[8];
+            if (near(eg)) {
 #pragma unroll
-            for (int j = 0; j < 8; j++) h[j] = value(g, j) * sigmoid<T>(value(g, j)) * value(u, j);
+                for (int j = 0; j < 8; j++) h[j] = value(g, j) * sigmoid<T>(value(g, j)) * value(u, j);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; j++) {
+                    const Sigma s = sigma_far(value(g, j));
+                    h[j] = value(g, j) * s.f * s.q * (value(u, j) * s.f);
+                }
+            }
             store8<T, VEC>(a.h, a.ldh, pl.t, pl.c, a.f, h);
             *(uint2 *)(a.cg + 8 * (size_t)i) = qg;
             *(uint2 *)(a.cu + 8 * (size_t)i) = qu;
@@ -251,11 +274,21 @@ __global__ void __launch_bounds__(SW_THREADS) k3_swiglu_backward(const SwigluArg
         float g[8], u[8];
         from_e4m3x8(k.qg, k.eg, g);
         from_e4m3x8(k.qu, k.eu, u);
+        if (near(k.eg)) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const float s = sigmoid<T>(g[j]), d = value(k.dh, j) * s, gj = g[j];
-            g[j] = d * u[j] * (1.f + gj * (1.f - s));
-            u[j] = d * gj;
+            for (int j = 0; j < 8; j++) {
+                const float s = sigmoid<T>(g[j]), d = value(k.dh, j) * s, gj = g[j];
+                g[j] = d * u[j] * (1.f + gj * (1.f - s));
+                u[j] = d * gj;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const Sigma s = sigma_far(g[j]);
+                const float d = value(k.dh, j) * s.f * s.q, gj = g[j];
+                g[j] = d * (u[j] * s.f) * (1.f + gj * s.r);
+                u[j] = d * (gj * s.f);
+            }
         }
         store8<T, VEC>(a.dg, a.lddg, pl.t, pl.c, a.f, g);
         store8<T, VEC>(a.du, a.lddu, pl.t, pl.c, a.f, u);
