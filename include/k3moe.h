@@ -718,7 +718,8 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *h
  *  ckpt        device, k3moe_swiglu_ckpt_bytes(T, f) bytes, 16-byte aligned
  * In the backward call dg or du may be dh itself with the same stride.
  * Errors: K3MOE_EINVAL for null or misaligned pointers, T or f outside 1 .. 2^30,
- * short strides, a ckpt_bytes that is too small.
+ * short strides, a ckpt_bytes that is too small, dg or du at dh with another
+ * stride.
  */
 int64_t k3moe_swiglu_ckpt_bytes(int32_t T, int32_t f);
 int k3moe_swiglu_forward(void *h, int64_t ldh, void *ckpt, int64_t ckpt_bytes, const void *g, int64_t ldg,

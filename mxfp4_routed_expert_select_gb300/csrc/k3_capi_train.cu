@@ -138,6 +138,8 @@ int k3moe_swiglu_backward(void *dg, int64_t lddg, void *du, int64_t lddu, const 
         ckpt_bytes < k3moe_swiglu_ckpt_bytes(T, f) || !valid_rows(dg, dtype, lddg, f) ||
         !valid_rows(du, dtype, lddu, f) || !valid_rows(dh, dtype, lddh, f) || dg == du)
         return K3MOE_EINVAL;
+    // on top of dh with another stride a row would be written before it is read
+    if (T > 1 && ((dg == dh && lddg != lddh) || (du == dh && lddu != lddh))) return K3MOE_EINVAL;
     return guarded([&] {
         return k3::launch_swiglu_backward(dg, (long)lddg, du, (long)lddu, dh, (long)lddh, ckpt, dtype, T, f, cs(s));
     });
