@@ -332,10 +332,11 @@ __global__ void __launch_bounds__(BL_THREADS, 3) k3_balance_backward(const Balan
         bool valid = on, first = false;
         float at = 0.f;  // the whole gradient of this lane's chosen expert
         if (on) {
-            // logit of the chosen expert, before any lane may write the row
+            // logit of the chosen expert, before another lane may write it (in place)
             float lj = 0.f;
             if (sl.id >= 0) lj = a.vec ? load1<T>(buf + b * rb, sl.id) : load1<T>(a.logits, (long)t * a.ld + sl.id);
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
+            __syncwarp();
             valid = row_probs<NV, SIG>(v, inv, m);
             if (valid) {
                 float dot = 0.f;  // <f - 1, unnormalised p>

@@ -1,11 +1,13 @@
-"""The balance loss over logits of any finite size."""
+"""The balance loss over logits of any finite size, and in place on rows that are
+not made of aligned 16-byte units."""
 import pytest
 import torch
 
 import test_gpu_balance as base
+from mxfp4_routed_expert_select_gb300 import k3moe as k
 
 pytestmark = pytest.mark.gpu
-DT, RULES = base.DT, base.RULES
+DT, RULES, ALPHA = base.DT, base.RULES, base.ALPHA
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -35,3 +37,18 @@ def test_only_rows_at_the_lowest_value(rule, dt):
     got = base.call(l, ids, None, rule, 1.0, w, dw)
     base.compare(l, ids, None, rule, 1.0, w, dw, got)
     assert int(got[2]) == 9 and bool(torch.isfinite(got[3]).all())
+
+
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("T,E,K", [(40, 33, 6), (5000, 33, 4), (5000, 64, 4)])
+def test_in_place(T, E, K, rule):
+    """dlogits on top of logits gives what separate ones give, rows loaded directly
+    (33 experts) or copied ahead (64), with repeated ids."""
+    l, ids, mask, w, dw = base.make(T, E, K, rule, "f32", 15, masked=0.2)
+    ids[:, 3] = ids[:, 1]
+    want = base.call(l, ids, mask, rule, 1.0, w, dw)
+    bal, d = k.BalanceLoss(E, K, ALPHA, rule), torch.ones(1, device="cuda")
+    for _ in range(3):
+        x = l.clone()
+        bal.backward(x, x, ids, want[1], want[2], d, mask, w, dw)
+        assert torch.equal(x, want[3])
