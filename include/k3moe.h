@@ -31,6 +31,12 @@
  *    Invalid arguments are refused with K3MOE_EINVAL before anything is
  *    enqueued; nothing is guessed or defaulted (a zero or inconsistent size is
  *    an error).  No call exits the process or throws.
+ *  - Weights may be written by earlier work on the same stream.  The kernels of
+ *    k3moe_expert_gemv, k3moe_matmul_mxfp4, k3moe_shared_forward and the batch-1
+ *    layer request weights before the kernel in front of them has completed, but
+ *    not behind a call of this library that may have written some.  A kernel from
+ *    elsewhere that writes weights must not release its dependents early
+ *    (griddepcontrol.launch_dependents) when such a call follows it.
  *  - A NaN E8M0 scale (byte 255) is not an error: its 32-group contributes 0
  *    [ENG, "What byte-identical actually costs"].
  *  - Device kernels never trap.  Errors detected on the device (a bounded

@@ -684,6 +684,7 @@ int k3moe_mx_quantize(uint8_t *codes, uint8_t *scales, const void *x, int x_dtyp
     if (!codes || !scales || !x || rows <= 0 || cols <= 0 || cols % 32 ||
         (x_dtype != K3MOE_F32 && x_dtype != K3MOE_BF16))
         return K3MOE_EINVAL;
+    k3::note_weight_writes(cs(s));
     return k3::launch_mx_quantize(x, x_dtype, rows, cols, codes, scales, cs(s));
 }
 

@@ -48,13 +48,15 @@ bool valid_operand(const k3moe_mx_operand *o, int32_t rows, int32_t in)
 {
     return valid_operand(o) && o->rows == rows && o->in == in;
 }
-// The launches allocate no memory of their own, but the library's table of
-// raised shared-memory limits may grow: no exception leaves an entry point.
+// A launch that writes what a later call may read as weights.  The launches allocate
+// no memory of their own, but the library's table of raised shared-memory limits may
+// grow: no exception leaves an entry point.
 template <typename F>
-int guarded(F f)
+int writing(k3moe_stream s, F launch)
 {
     try {
-        return f();
+        k3::note_weight_writes(cs(s));
+        return launch();
     } catch (...) {
         return K3MOE_ENOMEM;
     }
@@ -83,7 +85,7 @@ int k3moe_mx_quantize_operand(const k3moe_mx_operand *row, const k3moe_mx_operan
         !valid_rows(x, x_dtype, ld, cols) || (row && !valid_operand(row, rows, cols)) ||
         (col && !valid_operand(col, cols, rows)))
         return K3MOE_EINVAL;
-    return guarded([&] { return k3::launch_mx_quantize_operand(x, x_dtype, rows, cols, (long)ld, row, col, cs(s)); });
+    return writing(s, [&] { return k3::launch_mx_quantize_operand(x, x_dtype, rows, cols, (long)ld, row, col, cs(s)); });
 }
 
 int k3moe_mx_operand_from_matrix(const k3moe_mx_operand *op, const k3moe_mat *W, k3moe_stream s)
@@ -91,13 +93,13 @@ int k3moe_mx_operand_from_matrix(const k3moe_mx_operand *op, const k3moe_mat *W,
     if (!valid_operand(op) || !W || !W->packed || !W->scales || op->codes != W->packed || op->rows != W->rows ||
         W->in % 32 || k3::op_in_padded(op->in) != W->in || !aligned(W->scales, 16))
         return K3MOE_EINVAL;
-    return guarded([&] { return k3::launch_mx_scale_atoms(W->scales, op->rows, op->in, op->atoms, cs(s)); });
+    return writing(s, [&] { return k3::launch_mx_scale_atoms(W->scales, op->rows, op->in, op->atoms, cs(s)); });
 }
 
 int k3moe_mx_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx_operand *op, k3moe_stream s)
 {
     if (!valid_operand(op) || !valid_dtype(y_dtype) || !valid_rows(y, y_dtype, ld, op->in)) return K3MOE_EINVAL;
-    return guarded([&] { return k3::launch_mx_dequantize(op, y, y_dtype, (long)ld, cs(s)); });
+    return writing(s, [&] { return k3::launch_mx_dequantize(op, y, y_dtype, (long)ld, cs(s)); });
 }
 
 int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *A, const k3moe_mx_operand *B,
@@ -106,7 +108,7 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *A
     if (!valid_operand(A) || !valid_operand(B) || A->in != B->in || !valid_dtype(c_dtype) ||
         !valid_rows(C, c_dtype, ldc, B->rows) || (accumulate && c_dtype != K3MOE_F32))
         return K3MOE_EINVAL;
-    return guarded([&] {
+    return writing(s, [&] {
         int *err = k3::device_error_word();
         if (!err) return (int)K3MOE_ECUDA;
         return k3::launch_mx_matmul(C, c_dtype, (long)ldc, A, B, accumulate ? 1 : 0, err, cs(s));
@@ -126,7 +128,7 @@ int k3moe_swiglu_forward(void *h, int64_t ldh, void *ckpt, int64_t ckpt_bytes, c
         ckpt_bytes < k3moe_swiglu_ckpt_bytes(T, f) || !valid_rows(h, dtype, ldh, f) || !valid_rows(g, dtype, ldg, f) ||
         !valid_rows(u, dtype, ldu, f))
         return K3MOE_EINVAL;
-    return guarded([&] {
+    return writing(s, [&] {
         return k3::launch_swiglu_forward(h, (long)ldh, ckpt, g, (long)ldg, u, (long)ldu, dtype, T, f, cs(s));
     });
 }
@@ -140,7 +142,7 @@ int k3moe_swiglu_backward(void *dg, int64_t lddg, void *du, int64_t lddu, const 
         return K3MOE_EINVAL;
     // on top of dh with another stride a row would be written before it is read
     if (T > 1 && ((dg == dh && lddg != lddh) || (du == dh && lddu != lddh))) return K3MOE_EINVAL;
-    return guarded([&] {
+    return writing(s, [&] {
         return k3::launch_swiglu_backward(dg, (long)lddg, du, (long)lddu, dh, (long)lddh, ckpt, dtype, T, f, cs(s));
     });
 }
@@ -163,7 +165,7 @@ int k3moe_balance_forward(float *loss, int32_t *counts, int32_t *n_valid, const 
         !aligned(counts, 4) || !aligned(n_valid, 4) || !ws || !aligned(ws, 16) ||
         ws_bytes < k3moe_balance_workspace(E))
         return K3MOE_EINVAL;
-    return guarded([&] {
+    return writing(s, [&] {
         return k3::launch_balance_forward(loss, counts, n_valid, logits, dtype, (long)ld, ids, mask, T, E, k, alpha,
                                           rule, ws, cs(s));
     });
@@ -178,7 +180,7 @@ int k3moe_balance_backward(void *dlogits, int64_t ldd, const void *logits, int d
         !n_valid || !dloss || !aligned(counts, 4) || !aligned(n_valid, 4) || !aligned(dloss, 4) || (!w != !dw) ||
         !aligned(w, 4) || !aligned(dw, 4) || (dlogits == logits && ldd != ld))
         return K3MOE_EINVAL;
-    return guarded([&] {
+    return writing(s, [&] {
         return k3::launch_balance_backward(dlogits, (long)ldd, logits, dtype, (long)ld, ids, mask, counts, n_valid,
                                            dloss, w, dw, T, E, k, alpha, rule, cs(s));
     });

@@ -32,6 +32,15 @@ int ensure_smem(const void *fn, size_t bytes);
 K3_DEV void griddep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 K3_DEV void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Some kernels load weights (never their inputs or outputs) before that wait.
+// That is sound after any kernel that leaves weights alone; after one that may have
+// written them, such a kernel is launched without the attribute.  A call that writes
+// device memory a caller may use as weights says so (note_weight_writes, before its
+// launch), and the launchers of the kernels that load weights early ask first
+// (weights_settled).  Both keep to the order of calls on a stream (k3_runtime.cu).
+void note_weight_writes(cudaStream_t s);
+bool weights_settled(cudaStream_t s);
+
 // Device error word (bounded waits that ran out write K3MOE_ETIMEOUT here):
 // one int per device, a file-scope device variable (k3::device_error_word()).
 K3_DEV void set_device_error(int *err, int code)

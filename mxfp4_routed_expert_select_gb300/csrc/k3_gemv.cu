@@ -447,7 +447,7 @@ static int launch_rows_pipe(const float *x, const ExpertSrc &src, int k, int in,
     const int nstage = (int)((total + kPipeR - 1) / kPipeR);
     int grid = num_sms();
     if (grid > nstage) grid = nstage;
-    if (launch_pdl(kern, dim3(grid), dim3(threads), smem, s, x, src, k, in, rows, out, nstage, S, err) !=
+    if (launch_pdl_weights(kern, dim3(grid), dim3(threads), smem, s, x, src, k, in, rows, out, nstage, S, err) !=
         cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
@@ -513,7 +513,7 @@ static int launch_down_hpl(const float *h, const ExpertSrc &src, const float *w,
     const size_t smem = (size_t)k * rpc * sizeof(float);
     if (ensure_smem((const void *)k3_down_t1<HPL, kUdown>, smem) != K3MOE_OK) return K3MOE_ECUDA;
     const int grid = (d + rpc - 1) / rpc;
-    if (launch_pdl(k3_down_t1<HPL, kUdown>, dim3(grid), dim3(threads), smem, s, h, src, w, k, d, f, out, rpc,
+    if (launch_pdl_weights(k3_down_t1<HPL, kUdown>, dim3(grid), dim3(threads), smem, s, h, src, w, k, d, f, out, rpc,
                    acc ? 1 : 0) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;

@@ -6,13 +6,15 @@
 
 namespace k3 {
 
+bool weights_settled(cudaStream_t s);
+
 // Launches kernel<<<grid, block, smem, s>>>(args...) as a programmatic
-// dependent of the previous kernel on s where the driver takes it (the
-// kernel then overlaps its prologue, and the weight loads it issues before
+// dependent of the previous kernel on s where that is wanted and the driver takes
+// it (the kernel then overlaps its prologue, and the weight loads it issues before
 // griddep_wait, with that kernel's tail), else as a plain launch.
 template <typename... KArgs, typename... Args>
-static cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
-                              Args... args)
+static cudaError_t launch_dependent(bool wanted, void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                    cudaStream_t s, Args... args)
 {
     static std::atomic<int> refused{0};
     cudaLaunchAttribute attr[1];
@@ -24,7 +26,7 @@ static cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = refused.load(std::memory_order_relaxed) ? 0 : 1;
+    cfg.numAttrs = wanted && !refused.load(std::memory_order_relaxed) ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
     if (e != cudaSuccess && cfg.numAttrs == 1) {
         cudaGetLastError();
@@ -33,6 +35,21 @@ static cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
         e = cudaLaunchKernelEx(&cfg, kernel, args...);
     }
     return e;
+}
+
+// For kernels that touch nothing before griddep_wait.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              Args... args)
+{
+    return launch_dependent(true, kernel, grid, block, smem, s, args...);
+}
+// For kernels that load weights before griddep_wait.
+template <typename... KArgs, typename... Args>
+static cudaError_t launch_pdl_weights(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                                      Args... args)
+{
+    return launch_dependent(weights_settled(s), kernel, grid, block, smem, s, args...);
 }
 
 }  // namespace k3

@@ -734,9 +734,9 @@ K3_DEV bool mx_route(const MxRoute &r, const MxArgs &a0, float *out, uint8_t *sm
         }
     }
     // Launched as a programmatic dependent of the previous kernel on the
-    // stream: only the router rows (weights, never written by a kernel) are
-    // requested before it has completed; x, out and the workspace are touched
-    // after this wait.
+    // stream: only the router rows (weights; after a call that may have written
+    // them the launch is a plain one) are requested before it has completed; x,
+    // out and the workspace are touched after this wait.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const XT *x = reinterpret_cast<const XT *>(r.x);
     const long NW = (long)G * (MX_THREADS / 32), gw = (long)blockIdx.x * (MX_THREADS / 32) + warp;
@@ -1068,7 +1068,7 @@ static int launch_layer(const MxRoute &r, const MxArgs &a0, const MxArgs &a1, un
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = pdl_refused.load(std::memory_order_relaxed) ? 0 : 1;
+    cfg.numAttrs = weights_settled(s) && !pdl_refused.load(std::memory_order_relaxed) ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k3_mx_layer<XT>, r, a0, a1, hready, exit_cnt, bar_off);
     if (e != cudaSuccess && cfg.numAttrs == 1) {
         cudaGetLastError();

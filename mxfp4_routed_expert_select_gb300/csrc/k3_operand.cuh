@@ -5,11 +5,10 @@
 namespace k3 {
 
 // Programmatic dependent launches of the kernels that use this header: all start
-// as dependents and wait (griddep_wait) before they touch global memory.  Those
-// that may write what a later kernel reads before its own wait (the GEMV and
-// shared-expert kernels load weights there: codes, values, products) do not let
-// their dependents start early; the others do so only after their wait, when
-// everything before them is complete.
+// as dependents and wait (griddep_wait) before they touch global memory.  Kernels
+// that load weights before their own wait (GEMV, shared experts, the batch-1 layer)
+// are ordered behind them on the host: each entry point here notes its writes
+// (note_weight_writes), and such a kernel is then launched without the attribute.
 
 // Codes: [rows][ceil32(in) / 2] bytes.  Scale bytes: 512-byte atoms of 128
 // rows x 4 blocks (128 of the reduction), atom (row tile, k) at

@@ -1,8 +1,8 @@
-// k3_runtime.cu -- per-device host state shared by every launch of the
-// library: the device error word, the SM count, and the dynamic shared-memory
-// limits raised for each kernel.
+// k3_runtime.cu -- host state shared by every launch of the library: the device
+// error word, the SM count, the dynamic shared-memory limits raised for each
+// kernel, and the streams whose last weights may not be complete.
 //
-// All three are kept per device (the current device at the call), since a
+// The first three are kept per device (the current device at the call), since a
 // CUDA context holds its own copy of each, and their first-time set-up is
 // guarded so that concurrent first calls from several host threads are safe.
 #include <cuda_runtime.h>
@@ -31,6 +31,35 @@ struct SmemLimit {
     size_t bytes;
 };
 std::vector<SmemLimit> g_smem;
+
+
+// Streams on which a call has written what may be weights and no kernel that loads
+// weights early has followed yet; the mark goes with the first one, which waits for
+// everything before it.  In a capture the mark is the capture's and stays: its
+// streams may depend on one another, and a graph is recorded once.  When the table
+// is full every stream counts as marked, and captures up to the newest id that left
+// the ring do.
+std::mutex g_written_mu;
+constexpr int kMaxWritten = 256, kMaxCaptures = 64;
+std::atomic<int> g_n_written{0};      // marked streams; kMaxWritten + 1: all
+std::atomic<int> g_n_captures{0};     // captures marked so far
+uintptr_t g_written[kMaxWritten];
+unsigned long long g_capture[kMaxCaptures], g_capture_floor;
+
+// One more than the id of the capture that s takes part in, 0 for none.  (The legacy
+// stream beside another's capture gives an error and takes part in none.)
+unsigned long long capture_of(cudaStream_t s)
+{
+    cudaStreamCaptureStatus st = cudaStreamCaptureStatusNone;
+    unsigned long long id = 0;
+    if (cudaStreamGetCaptureInfo(s, &st, &id) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return st == cudaStreamCaptureStatusNone ? 0 : id + 1;
+}
+// One key for the two names of the legacy default stream.
+uintptr_t stream_key(cudaStream_t s) { return s == cudaStreamLegacy ? 0 : (uintptr_t)s; }
 
 int current_device()
 {
@@ -98,6 +127,59 @@ int ensure_smem(const void *fn, size_t bytes)
     }
     g_smem.push_back({dev, fn, bytes});
     return K3MOE_OK;
+}
+
+// The table alone, by key and capture id.
+void written_note(uintptr_t stream, unsigned long long capture)
+{
+    std::lock_guard<std::mutex> lock(g_written_mu);
+    if (capture) {
+        const int n = g_n_captures.load(std::memory_order_relaxed);
+        for (int i = 0; i < n && i < kMaxCaptures; i++)
+            if (g_capture[i] == capture) return;
+        unsigned long long &slot = g_capture[n % kMaxCaptures];
+        if (n >= kMaxCaptures && slot > g_capture_floor) g_capture_floor = slot;
+        slot = capture;
+        g_n_captures.store(n < 2 * kMaxCaptures ? n + 1 : n + 1 - kMaxCaptures, std::memory_order_relaxed);
+        return;
+    }
+    const int n = g_n_written.load(std::memory_order_relaxed);
+    if (n > kMaxWritten) return;
+    for (int i = 0; i < n; i++)
+        if (g_written[i] == stream) return;
+    if (n < kMaxWritten) g_written[n] = stream;
+    g_n_written.store(n + 1, std::memory_order_relaxed);
+}
+bool written_take(uintptr_t stream, unsigned long long capture)
+{
+    std::lock_guard<std::mutex> lock(g_written_mu);
+    if (capture) {
+        const int n = g_n_captures.load(std::memory_order_relaxed);
+        for (int i = 0; i < n && i < kMaxCaptures; i++)
+            if (g_capture[i] == capture) return true;
+        return capture <= g_capture_floor;
+    }
+    const int n = g_n_written.load(std::memory_order_relaxed);
+    if (n > kMaxWritten) return true;
+    for (int i = 0; i < n; i++)
+        if (g_written[i] == stream) {
+            // one handle names the per-thread default streams of all threads: kept
+            if (stream != (uintptr_t)cudaStreamPerThread) {
+                g_written[i] = g_written[n - 1];
+                g_n_written.store(n - 1, std::memory_order_relaxed);
+            }
+            return true;
+        }
+    return false;
+}
+
+void note_weight_writes(cudaStream_t s) { written_note(stream_key(s), capture_of(s)); }
+bool weights_settled(cudaStream_t s)
+{
+    // nothing marked anywhere: no question to the driver
+    if (g_n_written.load(std::memory_order_relaxed) == 0 && g_n_captures.load(std::memory_order_relaxed) == 0)
+        return true;
+    return !written_take(stream_key(s), capture_of(s));
 }
 
 }  // namespace k3

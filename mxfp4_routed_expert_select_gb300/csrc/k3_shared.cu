@@ -288,16 +288,16 @@ int launch_shared(const uint16_t *const *gate, const uint16_t *const *up, const 
             ensure_smem(two ? (const void *)k3_shared_down2 : (const void *)k3_shared_down, sh) != K3MOE_OK)
             return K3MOE_ECUDA;
         const int g1 = resident_grid(k3_shared_gateup, sx, (long)n * f / SH_RG);
-        cudaError_t e = launch_pdl(k3_shared_gateup, dim3(g1), dim3(SH_WARPS * 32), sx, s, src, n,
+        cudaError_t e = launch_pdl_weights(k3_shared_gateup, dim3(g1), dim3(SH_WARPS * 32), sx, s, src, n,
                                    x + (size_t)t0 * d, tt, d, f, h);
         if (e == cudaSuccess) {
             if (two) {
                 const int g2 = resident_grid(k3_shared_down2, sh, ((long)d + SH2_WARPS - 1) / SH2_WARPS, SH2_WARPS * 32);
-                e = launch_pdl(k3_shared_down2, dim3(g2), dim3(SH2_WARPS * 32), sh, s, src, n, (const float *)h, tt, d,
+                e = launch_pdl_weights(k3_shared_down2, dim3(g2), dim3(SH2_WARPS * 32), sh, s, src, n, (const float *)h, tt, d,
                                f, out + (size_t)t0 * d, accumulate);
             } else {
                 const int g2 = resident_grid(k3_shared_down, sh, ((long)d + SH_WARPS - 1) / SH_WARPS);
-                e = launch_pdl(k3_shared_down, dim3(g2), dim3(SH_WARPS * 32), sh, s, src, n, (const float *)h, tt, d,
+                e = launch_pdl_weights(k3_shared_down, dim3(g2), dim3(SH_WARPS * 32), sh, s, src, n, (const float *)h, tt, d,
                                f, out + (size_t)t0 * d, accumulate);
             }
         }
