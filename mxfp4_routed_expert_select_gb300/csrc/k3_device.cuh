@@ -38,8 +38,8 @@ K3_DEV void griddep_launch_dependents() { asm volatile("griddepcontrol.launch_de
 // device memory a caller may use as weights says so (note_weight_writes, before its
 // launch), and the launchers of the kernels that load weights early ask first
 // (weights_settled).  Both keep to the order of calls on a stream (k3_runtime.cu).
-void note_weight_writes(cudaStream_t s);
-bool weights_settled(cudaStream_t s);
+void note_weight_writes(cudaStream_t s) noexcept;
+bool weights_settled(cudaStream_t s) noexcept;
 
 // Device error word (bounded waits that ran out write K3MOE_ETIMEOUT here):
 // one int per device, a file-scope device variable (k3::device_error_word()).

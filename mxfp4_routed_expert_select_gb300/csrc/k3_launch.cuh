@@ -6,7 +6,7 @@
 
 namespace k3 {
 
-bool weights_settled(cudaStream_t s);
+bool weights_settled(cudaStream_t s) noexcept;
 
 // Launches kernel<<<grid, block, smem, s>>>(args...) as a programmatic
 // dependent of the previous kernel on s where that is wanted and the driver takes

@@ -173,13 +173,25 @@ bool written_take(uintptr_t stream, unsigned long long capture)
     return false;
 }
 
-void note_weight_writes(cudaStream_t s) { written_note(stream_key(s), capture_of(s)); }
-bool weights_settled(cudaStream_t s)
+// A lock that fails counts as marked; no exception reaches an entry point.
+void note_weight_writes(cudaStream_t s) noexcept
+{
+    try {
+        written_note(stream_key(s), capture_of(s));
+    } catch (...) {
+        g_n_written.store(kMaxWritten + 1, std::memory_order_relaxed);
+    }
+}
+bool weights_settled(cudaStream_t s) noexcept
 {
     // nothing marked anywhere: no question to the driver
     if (g_n_written.load(std::memory_order_relaxed) == 0 && g_n_captures.load(std::memory_order_relaxed) == 0)
         return true;
-    return !written_take(stream_key(s), capture_of(s));
+    try {
+        return !written_take(stream_key(s), capture_of(s));
+    } catch (...) {
+        return false;
+    }
 }
 
 }  // namespace k3
