@@ -920,20 +920,8 @@ int launch_clusters(void (*kernel)(KArgs...), int grid, int cluster, int threads
                     const Args &...args)
 {
     if (ensure_smem((const void *)kernel, smem) != K3MOE_OK) return K3MOE_ECUDA;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)cluster;
-    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = cluster > 1 ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    if (launch_dependent(true, cluster, kernel, dim3((unsigned)grid), dim3((unsigned)threads), smem, s, args...) !=
+        cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
