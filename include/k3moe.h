@@ -757,7 +757,7 @@ int k3moe_swiglu_backward(void *dg, int64_t lddg, void *du, int64_t lddu, const 
  *  logits   [T][E], dtype K3MOE_F32 or K3MOE_BF16, row stride ld >= E elements;
  *           1 <= E <= 1024, 1 <= T <= 2^30
  *  ids      int32 [T][top_k], as k3moe_layer_route returns them; 1 <= top_k <= 32
- *  mask     uint8 [T] or NULL
+ *  mask     uint8 [T] (a C bool array is one) or NULL
  *  loss     fp32 [1], counts int32 [E], n_valid int32 [1] (out; the backward
  *           call reads the last two)
  *  dloss    fp32 [1]: the gradient of the loss, in device memory

@@ -352,6 +352,20 @@ def _flat(t, dtype, *shape):
     return t.data_ptr()
 
 
+def _gpu(t):
+    """Number of the GPU that a tensor is on, None (no tensor's number) on the CPU."""
+    n = t.get_device()
+    return n if n >= 0 else None
+
+
+def _elsewhere(gpu, *tensors):
+    """Raises for tensors that are not on GPU number `gpu`: the kernels would follow
+    their pointers.  (Called after a check in line, 40 ns a tensor; in a loop of a
+    call of its own the checks took 0.3 to 1 us.)"""
+    raise ValueError("expected tensors on %s, got %s" % (
+        "a GPU" if gpu is None else "GPU %d" % gpu, ", ".join(str(t.device) for t in tensors if t is not None)))
+
+
 class MxOperand:
     """An operand of the MXFP4 product (k3moe_mx_operand): `rows` rows, blocks
     of 32 along the `in_` columns.  Holds the device buffers `codes` and
@@ -367,6 +381,7 @@ class MxOperand:
         self.rows, self.in_ = rows, in_
         self.codes = torch.empty(nc, dtype=torch.uint8, device=device) if codes is None else codes
         self.atoms = torch.empty(na, dtype=torch.uint8, device=self.codes.device)
+        self.gpu = _gpu(self.codes)
         self.struct = MxOperandStruct(self.codes.data_ptr(), self.atoms.data_ptr(), rows, in_)
         self.ref = ctypes.byref(self.struct)
 
@@ -377,6 +392,8 @@ class MxOperand:
         import torch
         pad = -(-in_ // 32) * 32
         m = Mat(_flat(packed, torch.uint8, rows, pad // 2), _flat(scales, torch.uint8, rows, pad // 32), rows, pad)
+        if _gpu(packed) is None or scales.get_device() != packed.get_device():
+            _elsewhere(_gpu(packed), packed, scales)
         op = cls(rows, in_, codes=packed)
         check(lib().k3moe_mx_operand_from_matrix(op.ref, ctypes.byref(m), _stream(stream)),
               "k3moe_mx_operand_from_matrix")
@@ -387,6 +404,9 @@ def mx_quantize_operand(x, row=None, col=None, stream=None):
     """x [rows][cols] (fp32 or bf16) to MXFP4 along its columns' axis (row, an
     MxOperand rows x cols) and / or along its rows' axis (col, cols x rows)."""
     rows, cols = x.shape
+    gpu = x.get_device()
+    if (row is not None and row.gpu != gpu) or (col is not None and col.gpu != gpu):
+        _elsewhere(row.gpu if row is not None else col.gpu, x)
     st = (_lib or lib()).k3moe_mx_quantize_operand(row and row.ref, col and col.ref, x.data_ptr(), _dtype(x), rows,
                                                    cols, _ld(x, rows, cols), _stream(stream))
     if st:
@@ -395,6 +415,8 @@ def mx_quantize_operand(x, row=None, col=None, stream=None):
 
 def mx_dequantize(y, op, stream=None):
     """The values of an operand into y [op.rows][op.in_] (fp32 or bf16)."""
+    if y.get_device() != op.gpu:
+        _elsewhere(op.gpu, y)
     st = (_lib or lib()).k3moe_mx_dequantize(y.data_ptr(), _dtype(y), _ld(y, op.rows, op.in_), op.ref,
                                              _stream(stream))
     if st:
@@ -403,6 +425,8 @@ def mx_dequantize(y, op, stream=None):
 
 def mx_matmul(C, A, B, accumulate=False, stream=None):
     """C [A.rows][B.rows] (fp32 or bf16) = A B^T of two MxOperands, or += (fp32)."""
+    if C.get_device() != A.gpu or B.gpu != A.gpu:
+        _elsewhere(A.gpu, C, B.codes)
     st = (_lib or lib()).k3moe_mx_matmul(C.data_ptr(), _dtype(C), _ld(C, A.rows, B.rows), A.ref, B.ref,
                                          1 if accumulate else 0, _stream(stream))
     if st:
@@ -420,10 +444,14 @@ class SwigluCheckpoint:
         self.T, self.f, self.nbytes = T, f, n
         self.data = torch.empty(n, dtype=torch.uint8, device=device)
         self.ptr = self.data.data_ptr()
+        self.gpu = _gpu(self.data)
 
 
 def swiglu_forward(h, ckpt, g, u, stream=None):
     """h = silu(g) * u, keeping g and u in ckpt; [T][f] tensors of one type."""
+    gpu = ckpt.gpu
+    if h.get_device() != gpu or g.get_device() != gpu or u.get_device() != gpu:
+        _elsewhere(gpu, h, g, u)
     T, f = ckpt.T, ckpt.f
     st = (_lib or lib()).k3moe_swiglu_forward(h.data_ptr(), _ld(h, T, f), ckpt.ptr, ckpt.nbytes, g.data_ptr(),
                                               _ld(g, T, f), u.data_ptr(), _ld(u, T, f), _dtype(h, g, u), T, f,
@@ -434,6 +462,9 @@ def swiglu_forward(h, ckpt, g, u, stream=None):
 
 def swiglu_backward(dg, du, dh, ckpt, stream=None):
     """The gradients of gate and up from dh and the kept copies."""
+    gpu = ckpt.gpu
+    if dg.get_device() != gpu or du.get_device() != gpu or dh.get_device() != gpu:
+        _elsewhere(gpu, dg, du, dh)
     T, f = ckpt.T, ckpt.f
     st = (_lib or lib()).k3moe_swiglu_backward(dg.data_ptr(), _ld(dg, T, f), du.data_ptr(), _ld(du, T, f),
                                                dh.data_ptr(), _ld(dh, T, f), ckpt.ptr, ckpt.nbytes,
@@ -458,15 +489,26 @@ class BalanceLoss:
         self.E, self.k, self.alpha, self.rule = E, top_k, alpha, self.RULES[rule]
         self.workspace = torch.zeros(n, dtype=torch.uint8, device=device)
         self._ws = self.workspace.data_ptr(), n
-        self._f32, self._i32, self._u8 = torch.float32, torch.int32, torch.uint8
+        self._f32, self._i32, self._u8, self._bool = torch.float32, torch.int32, torch.uint8, torch.bool
+        self.gpu = _gpu(self.workspace)
+
+    def _mask(self, mask, T):
+        if mask is None:
+            return None
+        return _flat(mask, self._bool if mask.dtype is self._bool else self._u8, T)  # a bool is a byte, 0 or 1
 
     def forward(self, loss, counts, n_valid, logits, ids, mask=None, stream=None):
         """loss fp32 [1], counts int32 [E], n_valid int32 [1] of logits [T][E],
-        ids int32 [T][top_k], mask uint8 [T]."""
+        ids int32 [T][top_k], mask uint8 or bool [T]."""
         T, E, k, i32 = logits.shape[0], self.E, self.k, self._i32
+        gpu = self.gpu
+        if (loss.get_device() != gpu or counts.get_device() != gpu or n_valid.get_device() != gpu or
+                logits.get_device() != gpu or ids.get_device() != gpu or
+                (mask is not None and mask.get_device() != gpu)):
+            _elsewhere(gpu, loss, counts, n_valid, logits, ids, mask)
         st = (_lib or lib()).k3moe_balance_forward(
             _flat(loss, self._f32, 1), _flat(counts, i32, E), _flat(n_valid, i32, 1), logits.data_ptr(),
-            _dtype(logits), _ld(logits, T, E), _flat(ids, i32, T, k), _flat(mask, self._u8, T), T, E, k, self.alpha,
+            _dtype(logits), _ld(logits, T, E), _flat(ids, i32, T, k), self._mask(mask, T), T, E, k, self.alpha,
             self.rule, *self._ws, _stream(stream))
         if st:
             check(st, "k3moe_balance_forward")
@@ -475,9 +517,15 @@ class BalanceLoss:
         """dlogits [T][E] from dloss fp32 [1] and, with the combine weights w and
         their gradients dw (fp32 [T][top_k]), the weight rule's part."""
         T, E, k, f32, i32 = logits.shape[0], self.E, self.k, self._f32, self._i32
+        gpu = self.gpu
+        if (dlogits.get_device() != gpu or logits.get_device() != gpu or ids.get_device() != gpu or
+                counts.get_device() != gpu or n_valid.get_device() != gpu or dloss.get_device() != gpu or
+                (mask is not None and mask.get_device() != gpu) or (w is not None and w.get_device() != gpu) or
+                (dw is not None and dw.get_device() != gpu)):
+            _elsewhere(gpu, dlogits, logits, ids, counts, n_valid, dloss, mask, w, dw)
         st = (_lib or lib()).k3moe_balance_backward(
             dlogits.data_ptr(), _ld(dlogits, T, E), logits.data_ptr(), _dtype(logits, dlogits), _ld(logits, T, E),
-            _flat(ids, i32, T, k), _flat(mask, self._u8, T), _flat(counts, i32, E), _flat(n_valid, i32, 1),
+            _flat(ids, i32, T, k), self._mask(mask, T), _flat(counts, i32, E), _flat(n_valid, i32, 1),
             _flat(dloss, f32, 1), _flat(w, f32, T, k), _flat(dw, f32, T, k), T, E, k, self.alpha, self.rule,
             _stream(stream))
         if st:

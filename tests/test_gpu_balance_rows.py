@@ -52,3 +52,9 @@ def test_in_place(T, E, K, rule):
         x = l.clone()
         bal.backward(x, x, ids, want[1], want[2], d, mask, w, dw)
         assert torch.equal(x, want[3])
+
+
+def test_mask_of_bools():
+    l, ids, mask, w, dw = base.make(70, 48, 4, "softmax", "f32", 8, masked=0.4)
+    for a, b in zip(base.call(l, ids, mask, "softmax", 1.0, w, dw), base.call(l, ids, mask.bool(), "softmax", 1.0, w, dw)):
+        assert torch.equal(a, b)
