@@ -703,6 +703,14 @@ int k3moe_mx_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx_operand
 int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *host_A,
                     const k3moe_mx_operand *host_B, int32_t accumulate, k3moe_stream s);
 
+/*
+ * How k3moe_mx_matmul runs a product of these sizes on the current device (for
+ * profiles and tests): on CTA pairs (*host_pair 1) or single CTAs, columns per
+ * tile, and the CTAs that share one tile along `in`.  Errors: K3MOE_EINVAL.
+ */
+int k3moe_mx_matmul_form(int32_t M, int32_t N, int32_t in, int c_dtype, int32_t *host_pair, int32_t *host_columns,
+                         int32_t *host_ranks);
+
 /* ------------------------------- SwiGLU with an 8-bit activation checkpoint */
 
 /*

@@ -12,6 +12,7 @@ int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atom
 int launch_mx_dequantize(const k3moe_mx_operand *op, void *y, int ydt, long ld, cudaStream_t s);
 int launch_mx_matmul(void *C, int cdt, long ldc, const k3moe_mx_operand *A, const k3moe_mx_operand *B, int accumulate,
                      int *err, cudaStream_t s);
+void mx_matmul_form(int M, int N, int in, int cdt, int *pair, int *columns, int *ranks);
 int launch_swiglu_forward(void *h, long ldh, void *ckpt, const void *g, long ldg, const void *u, long ldu, int dtype,
                           int T, int f, cudaStream_t s);
 int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void *dh, long lddh, const void *ckpt,
@@ -113,6 +114,16 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *A
         if (!err) return (int)K3MOE_ECUDA;
         return k3::launch_mx_matmul(C, c_dtype, (long)ldc, A, B, accumulate ? 1 : 0, err, cs(s));
     });
+}
+
+int k3moe_mx_matmul_form(int32_t M, int32_t N, int32_t in, int c_dtype, int32_t *pair, int32_t *columns,
+                         int32_t *ranks)
+{
+    if (M < 1 || N < 1 || in < 1 || M > kMaxDim || N > kMaxDim || in > kMaxDim || !valid_dtype(c_dtype) || !pair ||
+        !columns || !ranks)
+        return K3MOE_EINVAL;
+    k3::mx_matmul_form(M, N, in, c_dtype, pair, columns, ranks);
+    return K3MOE_OK;
 }
 
 int64_t k3moe_swiglu_ckpt_bytes(int32_t T, int32_t f)

@@ -1037,6 +1037,12 @@ int launch_ct(const k3moe_mx_operand *A, const k3moe_mx_operand *B, const MgArgs
 
 }  // namespace
 
+void mx_matmul_form(int M, int N, int in, int cdt, int *pair, int *columns, int *ranks)
+{
+    const MgPlan p = choose_plan(M, N, (in + 255) / 256, num_sms(), cdt == K3MOE_BF16);
+    *pair = p.pair, *columns = p.nt, *ranks = p.ranks;
+}
+
 int launch_mx_matmul(void *C, int cdt, long ldc, const k3moe_mx_operand *A, const k3moe_mx_operand *B, int accumulate,
                      int *err, cudaStream_t s)
 {

@@ -147,6 +147,7 @@ SIGNATURES = {
     "k3moe_mx_operand_from_matrix": (ctypes.c_int, [_P, _P, _P]),
     "k3moe_mx_dequantize": (ctypes.c_int, [_P, _I, _I64, _P, _P]),
     "k3moe_mx_matmul": (ctypes.c_int, [_P, _I, _I64, _P, _P, _I, _P]),
+    "k3moe_mx_matmul_form": (ctypes.c_int, [_I, _I, _I, ctypes.c_int, _P, _P, _P]),
     "k3moe_swiglu_ckpt_bytes": (_I64, [_I, _I]),
     "k3moe_swiglu_forward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P]),
     "k3moe_swiglu_backward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _I, _I, _I, _P]),
@@ -431,6 +432,16 @@ def mx_matmul(C, A, B, accumulate=False, stream=None):
                                          1 if accumulate else 0, _stream(stream))
     if st:
         check(st, "k3moe_mx_matmul")
+
+
+def mx_matmul_form(M, N, in_, dtype):
+    """How mx_matmul runs a product of these sizes into a tensor of that type on
+    the current device: (CTA pairs, columns per tile, CTAs per tile)."""
+    import torch
+    out = [ctypes.c_int32() for _ in range(3)]
+    check(lib().k3moe_mx_matmul_form(M, N, in_, K3MOE_BF16 if dtype is torch.bfloat16 else K3MOE_F32,
+                                     *(ctypes.byref(o) for o in out)), "k3moe_mx_matmul_form")
+    return bool(out[0].value), out[1].value, out[2].value
 
 
 class SwigluCheckpoint:
