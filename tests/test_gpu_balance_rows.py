@@ -1,5 +1,5 @@
-"""The balance loss over logits of any finite size, and in place on rows that are
-not made of aligned 16-byte units."""
+"""The balance loss over logits of any finite size, in place on rows that are not made
+of aligned 16-byte units, and over more rows than the grids hold at once."""
 import pytest
 import torch
 
@@ -57,4 +57,23 @@ def test_in_place(T, E, K, rule):
 def test_mask_of_bools():
     l, ids, mask, w, dw = base.make(70, 48, 4, "softmax", "f32", 8, masked=0.4)
     for a, b in zip(base.call(l, ids, mask, "softmax", 1.0, w, dw), base.call(l, ids, mask.bool(), "softmax", 1.0, w, dw)):
+        assert torch.equal(a, b)
+
+
+# A pass of the forward grid covers 20 rows on each of 152 SMs (3040), one of the
+# backward grid 3 x 8 (3648): these go round both loops, up to seven times, with
+# rows in aligned 16-byte units (copied ahead) and without (loaded directly).
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rule", RULES)
+@pytest.mark.parametrize("T,E,K,pad", [(3041, 8, 2, 0), (3649, 33, 4, 2), (7000, 256, 6, 0), (7000, 257, 6, 0),
+                                       (20000, 64, 4, 0), (20011, 50, 3, 1), (8000, 896, 8, 0)])
+def test_many_rows_a_warp(T, E, K, pad, rule, dt):
+    l, ids, mask, w, dw = base.make(T, E, K, rule, dt, T + E, 0.3, 0.1, True, 0.02, pad)
+    # whole runs of rows off, across the passes of both grids
+    mask[3000:3700] = 0
+    mask[6000:6200] = 0
+    mask[-1] = 1
+    got = base.call(l, ids, mask, rule, 1.5, w, dw)
+    base.compare(l, ids, mask, rule, 1.5, w, dw, got)
+    for a, b in zip(got, base.call(l, ids, mask, rule, 1.5, w, dw)):
         assert torch.equal(a, b)

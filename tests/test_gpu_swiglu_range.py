@@ -1,5 +1,6 @@
 """SwiGLU and its gradients at gates far from zero, where sigma is below the
-smallest normal fp32 number but the product is not."""
+smallest normal fp32 number but the product is not, and over more chunks than the
+grid takes in one step."""
 import numpy as np
 import pytest
 import torch
@@ -48,3 +49,29 @@ def test_gates_far_out(dt):
         # 1 - sigma and the sum with 1 lose 2^-24 of their own size before they cancel
         slack = np.abs(D * U * s) * (1 + 2 * np.abs(G)) * REL
         assert (np.abs(base._f64(dg) - want_g) <= slack + np.abs(want_g) * HALF[dt] + tiny).all()
+
+
+# 152 SMs x 48 runs x 256 threads take 1.87 million chunks of eight values a step
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("T,f", [(4001, 4096), (12001, 4096), (4001, 4001), (9001, 4001), (70001, 250)])
+def test_many_chunks_a_thread(T, f, dt):
+    """Against the same rows in small calls, bit for bit, for whole aligned chunks
+    and for rows that are not made of them."""
+    gen = torch.Generator(device="cuda").manual_seed(T + f)
+    g, u, dh = (torch.randn(T, f, generator=gen, device="cuda").to(DT[dt]) for _ in range(3))
+    ck, h, dg, du = k.SwigluCheckpoint(T, f), torch.empty_like(g), torch.empty_like(g), torch.empty_like(g)
+    k.swiglu_forward(h, ck, g, u)
+    k.swiglu_backward(dg, du, dh, ck)
+    pad = -(-f // 32) * 32
+    codes = ck.data[:2 * T * pad].view(2, T, pad)
+    scales = ck.data[2 * T * pad:].view(2, T, pad // 32)
+    step = 997
+    for a in range(0, T, step):
+        b = min(T, a + step)
+        n = b - a
+        c, hh, dgg, duu = k.SwigluCheckpoint(n, f), torch.empty_like(g[a:b]), torch.empty_like(g[a:b]), torch.empty_like(g[a:b])
+        k.swiglu_forward(hh, c, g[a:b], u[a:b])
+        k.swiglu_backward(dgg, duu, dh[a:b], c)
+        assert torch.equal(h[a:b], hh) and torch.equal(dg[a:b], dgg) and torch.equal(du[a:b], duu), a
+        assert torch.equal(codes[:, a:b], c.data[:2 * n * pad].view(2, n, pad))
+        assert torch.equal(scales[:, a:b], c.data[2 * n * pad:].view(2, n, pad // 32))
