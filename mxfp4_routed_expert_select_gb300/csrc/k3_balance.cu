@@ -27,14 +27,16 @@
 namespace k3 {
 namespace {
 
-// Backward: three CTAs per SM (16384 x 896 fp32 with combine weights 21.7 us, 5.6 TB/s
-// read and written).
+// Backward: three CTAs per SM (16384 x 896 fp32, softmax, with combine weights 22.9 us,
+// 5.3 TB/s read and written; the sigmoid rules 59 us, bound by the issue of their
+// exponentials and divisions).
 constexpr int BL_THREADS = 256, BL_WARPS = BL_THREADS / 32;
 // Forward: one CTA per SM, so that half as many sums meet in global atomics as
 // with two of 256 threads.  Its rows cost latency (two reductions each), so more
 // warps help until the joining of their sums costs as much: 16384 x 896 fp32 takes
 // 14.8 us with 16 warps, 13.2 with 20, 14.0 with 24 (a third row in flight per warp
-// changed nothing).
+// changed nothing); 13.6 since the row's maximum is subtracted first; the sigmoid rules
+// 33.6.
 constexpr int BF_THREADS = 640, BF_WARPS = BF_THREADS / 32;
 
 // Workspace: fixed-point sums [E], counts [E], valid tokens, a flag for
@@ -216,6 +218,7 @@ __global__ void __launch_bounds__(BF_THREADS, 1) k3_balance_forward(const Balanc
             read_row<T, NV>(a, t, buf + b * rb, lane, v);
             if (row_probs<NV, SIG>(v, inv, m)) {
                 mine++;
+                // a warp has at most T / 3040 + 1 rows: fp32 loses 2^-24 of the sum a row
 #pragma unroll
                 for (int i = 0; i < 4 * NV; i++) acc[i] += v[i] * inv;
                 if (id >= 0 && id < a.E) atomicAdd(&cnt[id], 1u);
@@ -254,7 +257,8 @@ __global__ void __launch_bounds__(BF_THREADS, 1) k3_balance_forward(const Balanc
     if (!last) return;
 
     // the last CTA: the loss from the whole batch's sums, the workspace cleared.
-    // f_e P_e = E c_e / (k n) * sum / n in fp32, added in a fixed tree.
+    // f_e P_e = E c_e / (k n) * sum / n in fp32, added in a fixed tree: a few 2^-24 of
+    // the loss, which is of one sign throughout.
     const unsigned n = __ldcg(ws.valid);
     const float kn = (float)a.k * (float)n, pn = n ? 1.f / (unit * (float)n) : 0.f;
     float l = 0.f;

@@ -297,7 +297,8 @@ struct MgCfg {
     static constexpr int OFF_TA = OFF_SA + 1024;             // A's two atoms
     static constexpr int TX = OFF_TA + 1024;                 // bytes copied per stage
     static constexpr int STAGE = (TX + 1023) / 1024 * 1024;
-    // Split CTAs share an SM in pairs where the stages allow it.
+    // Split: few enough stages that two CTAs fit an SM, although choose_plan gives
+    // each one of its own (two per SM lost).
     static constexpr int NS = !SPLIT ? 6 : NT <= 16 ? 5 : 4;
     // TMEM: the accumulators (two of NT columns, one when split), then each
     // stage's scales.
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
 // (cta_group::2) works on 256 rows of A x NT rows of B together: each loads its own
 // 128 rows of A and half of B's, and the MMA reads both halves, so a step brings
 // and reads 35 KB per SM: shared memory's 64 bytes a clock (553 clocks a step) and
-// the tensor cores (512) are both near full (7.5 PFLOP/s at 8192^3).  192 columns
+// the tensor cores (512) are both near full (7.4 PFLOP/s at 8192^3).  192 columns
 // leave the MMAs 384 of 490 clocks but split some products into fuller waves; 384,
 // for products that are then one wave, are bound by the MMAs (790 of 768 clocks),
 // but with one accumulator the epilogue of a tile is not hidden.
