@@ -6,6 +6,7 @@
 
 namespace k3 {
 
+void note_weight_writes(cudaStream_t s) noexcept;
 bool weights_settled(cudaStream_t s) noexcept;
 
 // Launches kernel<<<grid, block, smem, s>>>(args...), in clusters of `cluster` CTAs,
@@ -60,7 +61,10 @@ template <typename... KArgs, typename... Args>
 static cudaError_t launch_pdl_weights(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                                       const Args &...args)
 {
-    return launch_dependent(weights_settled(s), 1, kernel, grid, block, smem, s, args...);
+    const bool settled = weights_settled(s);
+    const cudaError_t e = launch_dependent(settled, 1, kernel, grid, block, smem, s, args...);
+    if (e != cudaSuccess && !settled) note_weight_writes(s);  // nothing has waited for them
+    return e;
 }
 
 }  // namespace k3

@@ -1068,7 +1068,8 @@ static int launch_layer(const MxRoute &r, const MxArgs &a0, const MxArgs &a1, un
     cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cfg.attrs = attr;
-    cfg.numAttrs = weights_settled(s) && !pdl_refused.load(std::memory_order_relaxed) ? 1 : 0;
+    const bool settled = weights_settled(s);
+    cfg.numAttrs = settled && !pdl_refused.load(std::memory_order_relaxed) ? 1 : 0;
     cudaError_t e = cudaLaunchKernelEx(&cfg, k3_mx_layer<XT>, r, a0, a1, hready, exit_cnt, bar_off);
     if (e != cudaSuccess && cfg.numAttrs == 1) {
         cudaGetLastError();
@@ -1078,6 +1079,7 @@ static int launch_layer(const MxRoute &r, const MxArgs &a0, const MxArgs &a1, un
     }
     if (e != cudaSuccess) {
         cudaGetLastError();
+        if (!settled) note_weight_writes(s);  // nothing has waited for them
         return K3MOE_ECUDA;
     }
     return K3MOE_OK;

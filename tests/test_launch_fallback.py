@@ -24,6 +24,8 @@ extern "C" cudaError_t cudaLaunchKernelExC(const cudaLaunchConfig_t *c, const vo
 }
 extern "C" cudaError_t cudaGetLastError() { return cudaSuccess; }
 namespace k3 {
+static int noted;
+void note_weight_writes(cudaStream_t) noexcept { noted++; }
 bool weights_settled(cudaStream_t s) noexcept { return s == nullptr; }
 }
 static void one(int) {}
@@ -47,7 +49,11 @@ int main()
     refuse = 0;
     CHECK(launch_pdl_weights(three, g, b, 0, nullptr, 1.f) == cudaSuccess && dependent && cluster == 1);
     CHECK(launch_pdl_weights(three, g, b, 0, (cudaStream_t)8, 1.f) == cudaSuccess && !dependent);
-    CHECK(launch_pdl(three, g, b, 0, (cudaStream_t)8, 1.f) == cudaSuccess && dependent);
+    CHECK(launch_pdl(three, g, b, 0, (cudaStream_t)8, 1.f) == cudaSuccess && dependent && noted == 0);
+    // a launch that failed behind a writer leaves its note for the next
+    broken = 1;
+    CHECK(launch_pdl_weights(three, g, b, 0, nullptr, 1.f) != cudaSuccess && noted == 0);
+    CHECK(launch_pdl_weights(three, g, b, 0, (cudaStream_t)8, 1.f) != cudaSuccess && noted == 1);
     puts("ok");
     return 0;
 }
