@@ -711,6 +711,175 @@ int k3moe_mx_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx_operand *h
 int k3moe_mx_matmul_form(int32_t M, int32_t N, int32_t in, int c_dtype, int32_t *host_pair, int32_t *host_columns,
                          int32_t *host_ranks);
 
+/* ------------------------------------------------- 8-bit rows and the norm */
+
+/*
+ * A matrix of activations in 8 bits: e4m3 codes with one E8M0 scale per 32 values of
+ * a row, by the rule of the SwiGLU checkpoint below (the smallest power of two s with
+ * max|v| / s <= 448, round to nearest, ties to even; byte 0 for a block of zeros;
+ * magnitudes above 240 * 2^120 keep that value; byte 255, NaN, for a block that holds
+ * a non-finite value).  (The pages quantise stored weights only; these rows are what
+ * the grouped product below multiplies with them.)
+ *   codes   [rows][ceil32(in)] bytes, zero past `in`
+ *   scales  [rows][4 ceil(in / 128)] bytes, byte b of a row for its values 32 b ..
+ *           32 b + 31, zero past `in`
+ * 1 <= rows <= 2^30, 1 <= in <= 2^20.  The caller owns both buffers, of
+ * k3moe_mx8_codes_bytes and k3moe_mx8_scales_bytes bytes (-1 if invalid), 16-byte
+ * aligned.
+ */
+typedef struct {
+    uint8_t *codes;
+    uint8_t *scales;
+    int32_t rows;
+    int32_t in;
+} k3moe_mx8_rows;
+
+int64_t k3moe_mx8_codes_bytes(int32_t rows, int32_t in);
+int64_t k3moe_mx8_scales_bytes(int32_t rows, int32_t in);
+
+/* Quantises x [rows][in] (x_dtype K3MOE_F32 or K3MOE_BF16, row stride ld >= in
+ * elements, aligned to its element size), and the values such rows stand for: y
+ * [rows][in], rounded once to y_dtype (exact in both but below 2^-126).
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, bad sizes, types, strides. */
+int k3moe_mx8_quantize(const k3moe_mx8_rows *host_out, const void *x, int x_dtype, int64_t ld, k3moe_stream s);
+int k3moe_mx8_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx8_rows *host_rows, k3moe_stream s);
+
+/*
+ * The norm in front of a layer for a batch, with the residual's addition (the
+ * batched, trainable form of k3moe_residual_add and k3moe_rmsnorm):
+ *   r = x + delta, rounded to the rows' type;   y = r / sqrt(mean(r^2) + eps) * gain
+ * and its gradients, with s = 1 / sqrt(mean(r^2) + eps), g = dy * gain, xhat = r s:
+ *   dx = dr + s (g - xhat mean(g xhat)),   dgain = sum over rows of dy xhat
+ * dx is the gradient of x and of delta.  fp32 arithmetic; a mean of squares beyond
+ * fp32 (values above 10^19) or below its normal numbers is formed in a scaled range.
+ *  x, delta, r, y, dy, dr, dx  [T][n], all of one type (K3MOE_F32 or K3MOE_BF16) in a
+ *              call, each with its own row stride >= n elements, aligned to the
+ *              element size.  1 <= T <= 2^30, 1 <= n <= 32768
+ *  delta       NULL for none; r is then x itself and the parameter r must be NULL.
+ *              With delta, r may be NULL where it is not kept
+ *  y, y8       at least one of them: y in the rows' type, y8 in 8 bits (T rows of n),
+ *              quantised from the unrounded values
+ *  rstd        fp32 [T] or NULL: s, which the backward call reads
+ *  gain        fp32 [n], or NULL for ones
+ *  dr          gradient that reaches r past the norm, or NULL
+ *  dgain       fp32 [n], or NULL; needs gain.  accumulate != 0 adds into it
+ *  workspace   backward with dgain: device, k3moe_norm_workspace(n) bytes (0 for an
+ *              invalid n), 16-byte aligned; not shared by calls that may overlap
+ * y and r may be x or delta with the same stride (not both the same); dx may be dy, dr
+ * or r with the same stride.  Sums are taken in an order that does not depend on
+ * timing.  Errors: K3MOE_EINVAL for null or misaligned pointers, bad sizes, types or
+ * strides, an eps that is negative or not finite.
+ */
+size_t k3moe_norm_workspace(int32_t n);
+int k3moe_norm_forward(void *y, int64_t ldy, void *r, int64_t ldr, float *rstd, const k3moe_mx8_rows *host_y8,
+                       const void *x, int64_t ldx, const void *delta, int64_t ldd, const float *gain, int dtype, int32_t T,
+                       int32_t n, float eps, k3moe_stream s);
+int k3moe_norm_backward(void *dx, int64_t lddx, float *dgain, int32_t accumulate, const void *dy, int64_t lddy,
+                        const void *dr, int64_t lddr, const void *r, int64_t ldr, const float *rstd, const float *gain,
+                        int dtype, int32_t T, int32_t n, void *workspace, size_t workspace_bytes, k3moe_stream s);
+
+/* --------------------------------------------- products grouped by expert */
+
+/*
+ * The (token, slot) pairs of a routed batch grouped by expert: slot t * top_k + j of
+ * ids[t][j] (as k3moe_layer_route returns them), by rising expert and, within one,
+ * by rising slot.
+ *   offsets  int32 [E + 1]: the places offsets[e] .. offsets[e + 1] - 1 are expert e's
+ *   order    int32 [tokens * top_k]: the slot at each place, -1 from offsets[E] on
+ *   pos      int32 [tokens * top_k]: the place of each slot, -1 for a dropped one (an
+ *            id outside 0 .. E - 1)
+ * "Rows in group order" below are rows whose index is a place.  1 <= E <= 1024,
+ * 1 <= top_k <= 32, 1 <= tokens, tokens * top_k <= 2^30.  An expert may be named twice
+ * by a token.  The caller owns the three arrays.
+ */
+typedef struct {
+    int32_t *offsets;
+    int32_t *order;
+    int32_t *pos;
+    int32_t E;
+    int32_t top_k;
+    int32_t tokens;
+} k3moe_groups;
+
+/* Fills a plan from ids int32 [tokens][top_k].  workspace: device,
+ * k3moe_groups_workspace(E, tokens * top_k) bytes (0 if invalid), 16-byte aligned, not
+ * shared by calls that may overlap.  Errors: K3MOE_EINVAL. */
+size_t k3moe_groups_workspace(int32_t E, int64_t slots);
+int k3moe_groups_plan(const k3moe_groups *host_g, const int32_t *ids, void *workspace, size_t workspace_bytes,
+                      k3moe_stream s);
+
+/*
+ * The matrices [rows][in] of E experts as operands of the grouped product: expert e's
+ * codes and atoms (as in k3moe_mx_operand, with `in` a multiple of 128) at codes + e *
+ * codes_stride and atoms + e * atoms_stride, so that stacked operands and the planes of
+ * equally spaced expert blobs both serve.  codes 32-byte aligned and codes_stride a
+ * multiple of 32 (of at least the plane's bytes), atoms 16-byte aligned and
+ * atoms_stride a multiple of 16.
+ */
+typedef struct {
+    const uint8_t *codes;
+    const uint8_t *atoms;
+    int64_t codes_stride;
+    int64_t atoms_stride;
+    int32_t E;
+    int32_t rows;
+    int32_t in;
+} k3moe_mx_experts;
+
+/*
+ * C[i] = W_e a(i) for every place i of a plan, e the expert it belongs to: 8-bit rows
+ * times MXFP4 matrices on the block-scaled tensor cores, fp32 accumulation, rounded
+ * once to c_dtype.  One call for all experts, from a single token to whole batches;
+ * with the transposed matrices and the 8-bit rows of dC it is the input gradient.
+ *  A           the rows, `in` = W's.  gather != 0: a row per token, a(i) is that of the
+ *              token of slot order[i] (A->rows >= tokens).  gather = 0: rows in group
+ *              order (A->rows >= tokens * top_k)
+ *  C           [tokens * top_k][W->rows] rows in group order, c_dtype K3MOE_F32 or
+ *              K3MOE_BF16, aligned to its element size, row stride ldc >= W->rows;
+ *              rows from offsets[E] on are left as they are
+ *  accumulate  != 0 adds into C (K3MOE_F32 only)
+ * The result does not depend on timing.
+ * Errors: K3MOE_EINVAL for null or misaligned pointers, E or `in` that differ, too few
+ * rows, bad sizes or types.
+ */
+int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *host_A, const k3moe_mx_experts *host_W,
+                         const k3moe_groups *host_g, int32_t gather, int32_t accumulate, k3moe_stream s);
+
+/*
+ * The gradients of the experts' matrices, dW_e = sum over e's places i of dY[i] x(i)^T,
+ * from bf16 rows on the tensor cores, fp32 accumulation, rounded once to dw_dtype.  An
+ * expert without places gets zeros (nothing is added to it with accumulate).
+ *  dY          bf16 [tokens * top_k][N] in group order, row stride lddy >= N
+ *  X           bf16 [xrows][K], row stride ldx >= K.  gather != 0: a row per token
+ *              (xrows >= tokens); gather = 0: rows in group order (xrows >= tokens * top_k)
+ *  dW          [E][N][K], dw_dtype K3MOE_F32 or K3MOE_BF16
+ *  accumulate  != 0 adds into dW (K3MOE_F32 only)
+ * N and K are multiples of 8; dY, X and dW 16-byte aligned, lddy and ldx multiples of 8.
+ * The result does not depend on timing.  Errors: K3MOE_EINVAL.
+ */
+int k3moe_grouped_wgrad(void *dW, int dw_dtype, const void *dY, int64_t lddy, const void *X, int64_t ldx, int32_t xrows,
+                        int32_t N, int32_t K, const k3moe_groups *host_g, int32_t gather, int32_t accumulate,
+                        k3moe_stream s);
+
+/*
+ * The end of the layer, out[t] (+)= sum_j w[t][j] y[pos[t][j]], and its gradients
+ *   dy[pos[t][j]] = w[t][j] dout[t],   dw[t][j] = <dout[t], y[pos[t][j]]>
+ * (dw is what k3moe_balance_backward takes).  Dropped slots add nothing and get dw = 0.
+ * fp32 arithmetic, rounded once.  With w NULL all weights are 1: the sum of the rows
+ * that belong to a token, e.g. of its input gradients.
+ *  y, dy       [tokens * top_k][n] rows in group order; rows of dy from offsets[E] on are
+ *              left as they are
+ *  out, dout   [tokens][n]; accumulate != 0 adds into out
+ *  w, dw       fp32 [tokens][top_k]; dw NULL where it is not wanted (y may then be NULL)
+ * y, dy, out and dout of one type (K3MOE_F32 or K3MOE_BF16) in a call, row strides >= n,
+ * aligned to the element size; 1 <= n <= 2^20.  dy may be y with the same stride.
+ * Sums are taken in rising j.  Errors: K3MOE_EINVAL.
+ */
+int k3moe_combine(void *out, int64_t ldo, const void *y, int64_t ldy, int dtype, int32_t n, const k3moe_groups *host_g,
+                  const float *w, int32_t accumulate, k3moe_stream s);
+int k3moe_combine_backward(void *dy, int64_t lddy, float *dw, const void *dout, int64_t lddo, const void *y, int64_t ldy,
+                           int dtype, int32_t n, const k3moe_groups *host_g, const float *w, k3moe_stream s);
+
 /* ------------------------------- SwiGLU with an 8-bit activation checkpoint */
 
 /*

@@ -1,9 +1,12 @@
 // k3_capi_train.cu -- the extern "C" entry points around training and making
 // MXFP4 layers: operands and their product, the SwiGLU checkpoint, the balance
-// loss.  Argument checks and one launch each.
+// loss, the norm, 8-bit rows and what is grouped by expert.  Argument checks and the
+// launches.
 #include <cuda_runtime.h>
 
-#include "k3_operand.cuh"
+#include <cmath>
+
+#include "k3_e4m3.cuh"
 
 namespace k3 {
 int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long ld, const k3moe_mx_operand *row,
@@ -25,6 +28,25 @@ int launch_balance_backward(void *dlogits, long ldd, const void *logits, int dty
                             const uint8_t *mask, const int32_t *counts, const int32_t *n_valid, const float *dloss,
                             const float *w, const float *dw, int T, int E, int k, float alpha, int rule,
                             cudaStream_t s);
+int launch_mx8_quantize(const k3moe_mx8_rows *o, const void *x, int dtype, long ld, cudaStream_t s);
+int launch_mx8_dequantize(void *y, int dtype, long ld, const k3moe_mx8_rows *o, cudaStream_t s);
+size_t norm_workspace_bytes(int n);
+int launch_norm_forward(void *y, long ldy, void *r, long ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
+                        long ldx, const void *delta, long ldd, const float *gain, int dtype, int T, int n, float eps,
+                        cudaStream_t s);
+int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, const void *dy, long lddy, const void *dr,
+                         long lddr, const void *r, long ldr, const float *rstd, const float *gain, int dtype, int T,
+                         int n, void *ws, cudaStream_t s);
+size_t groups_workspace_bytes(int E, long slots);
+int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, cudaStream_t s);
+int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
+                          const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s);
+int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const void *X, long ldx, int xrows, int N, int K,
+                         const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s);
+int launch_combine(void *out, long ldo, const void *y, long ldy, int dtype, int n, const k3moe_groups *g, const float *w,
+                   int accumulate, cudaStream_t s);
+int launch_combine_backward(void *dy, long lddy, float *dw, const void *dout, long lddo, const void *y, long ldy, int dtype,
+                            int n, const k3moe_groups *g, const float *w, cudaStream_t s);
 }  // namespace k3
 
 namespace {
@@ -49,6 +71,20 @@ bool valid_operand(const k3moe_mx_operand *o, int32_t rows, int32_t in)
 {
     return valid_operand(o) && o->rows == rows && o->in == in;
 }
+constexpr int32_t kMaxIn = 1 << 20;  // columns of 8-bit rows and combined rows
+bool valid_mx8(const k3moe_mx8_rows *o)
+{
+    return o && o->codes && o->scales && aligned(o->codes, 16) && aligned(o->scales, 16) &&
+           k3moe_mx8_codes_bytes(o->rows, o->in) > 0;
+}
+bool valid_groups(const k3moe_groups *g)
+{
+    return g && g->offsets && g->order && g->pos && aligned(g->offsets, 4) && aligned(g->order, 4) && aligned(g->pos, 4) &&
+           g->E >= 1 && g->E <= 1024 && g->top_k >= 1 && g->top_k <= 32 && g->tokens >= 1 &&
+           (int64_t)g->tokens * g->top_k <= kMaxDim;
+}
+// Two row matrices of a call that may be one: the same rows then.
+bool apart_or_same(const void *p, int64_t ldp, const void *q, int64_t ldq, int32_t T) { return p != q || T == 1 || ldp == ldq; }
 // A launch that writes what a later call may read as weights.  The launches allocate
 // no memory of their own, but the library's table of raised shared-memory limits may
 // grow: no exception leaves an entry point.
@@ -194,6 +230,150 @@ int k3moe_balance_backward(void *dlogits, int64_t ldd, const void *logits, int d
     return writing(s, [&] {
         return k3::launch_balance_backward(dlogits, (long)ldd, logits, dtype, (long)ld, ids, mask, counts, n_valid,
                                            dloss, w, dw, T, E, k, alpha, rule, cs(s));
+    });
+}
+
+// ------------------------------------------------------- 8-bit rows and the norm
+
+int64_t k3moe_mx8_codes_bytes(int32_t rows, int32_t in)
+{
+    if (rows < 1 || in < 1 || rows > kMaxDim || in > kMaxIn) return -1;
+    return (int64_t)rows * k3::op_in_padded(in);
+}
+
+int64_t k3moe_mx8_scales_bytes(int32_t rows, int32_t in)
+{
+    if (rows < 1 || in < 1 || rows > kMaxDim || in > kMaxIn) return -1;
+    return (int64_t)rows * k3::mx8_scale_stride(in);
+}
+
+int k3moe_mx8_quantize(const k3moe_mx8_rows *o, const void *x, int x_dtype, int64_t ld, k3moe_stream s)
+{
+    if (!valid_mx8(o) || !valid_dtype(x_dtype) || !valid_rows(x, x_dtype, ld, o->in)) return K3MOE_EINVAL;
+    return writing(s, [&] { return k3::launch_mx8_quantize(o, x, x_dtype, (long)ld, cs(s)); });
+}
+
+int k3moe_mx8_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx8_rows *o, k3moe_stream s)
+{
+    if (!valid_mx8(o) || !valid_dtype(y_dtype) || !valid_rows(y, y_dtype, ld, o->in)) return K3MOE_EINVAL;
+    return writing(s, [&] { return k3::launch_mx8_dequantize(y, y_dtype, (long)ld, o, cs(s)); });
+}
+
+static bool valid_norm(int32_t T, int32_t n) { return T >= 1 && T <= kMaxDim && n >= 1 && n <= 32768; }
+
+size_t k3moe_norm_workspace(int32_t n) { return valid_norm(1, n) ? k3::norm_workspace_bytes(n) : 0; }
+
+int k3moe_norm_forward(void *y, int64_t ldy, void *r, int64_t ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
+                       int64_t ldx, const void *delta, int64_t ldd, const float *gain, int dtype, int32_t T, int32_t n,
+                       float eps, k3moe_stream s)
+{
+    if (!valid_norm(T, n) || !valid_dtype(dtype) || !valid_rows(x, dtype, ldx, n) ||
+        (delta && !valid_rows(delta, dtype, ldd, n)) || (y && !valid_rows(y, dtype, ldy, n)) ||
+        (r && (!delta || !valid_rows(r, dtype, ldr, n))) || (!y && !y8) ||
+        (y8 && (!valid_mx8(y8) || y8->rows != T || y8->in != n)) || !aligned(rstd, 4) || !aligned(gain, 4) ||
+        !(eps >= 0.f) || std::isinf(eps) || (y && y == r) || (y && !apart_or_same(y, ldy, x, ldx, T)) ||
+        (y && delta && !apart_or_same(y, ldy, delta, ldd, T)) || (r && !apart_or_same(r, ldr, x, ldx, T)) ||
+        (r && !apart_or_same(r, ldr, delta, ldd, T)))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        return k3::launch_norm_forward(y, (long)ldy, r, (long)ldr, rstd, y8, x, (long)ldx, delta, (long)ldd, gain, dtype, T,
+                                       n, eps, cs(s));
+    });
+}
+
+int k3moe_norm_backward(void *dx, int64_t lddx, float *dgain, int32_t accumulate, const void *dy, int64_t lddy,
+                        const void *dr, int64_t lddr, const void *r, int64_t ldr, const float *rstd, const float *gain,
+                        int dtype, int32_t T, int32_t n, void *ws, size_t ws_bytes, k3moe_stream s)
+{
+    if (!valid_norm(T, n) || !valid_dtype(dtype) || !valid_rows(dx, dtype, lddx, n) || !valid_rows(dy, dtype, lddy, n) ||
+        !valid_rows(r, dtype, ldr, n) || (dr && !valid_rows(dr, dtype, lddr, n)) || !rstd || !aligned(rstd, 4) ||
+        !aligned(gain, 4) || (dgain && (!gain || !aligned(dgain, 4) || !ws || !aligned(ws, 16) ||
+                                        ws_bytes < k3moe_norm_workspace(n))) ||
+        !apart_or_same(dx, lddx, dy, lddy, T) || !apart_or_same(dx, lddx, r, ldr, T) ||
+        (dr && !apart_or_same(dx, lddx, dr, lddr, T)))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        return k3::launch_norm_backward(dx, (long)lddx, dgain, accumulate ? 1 : 0, dy, (long)lddy, dr, (long)lddr, r,
+                                        (long)ldr, rstd, gain, dtype, T, n, ws, cs(s));
+    });
+}
+
+// ------------------------------------------------------------ grouped by expert
+
+size_t k3moe_groups_workspace(int32_t E, int64_t slots)
+{
+    return E < 1 || E > 1024 || slots < 1 || slots > kMaxDim ? 0 : k3::groups_workspace_bytes(E, (long)slots);
+}
+
+int k3moe_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, size_t ws_bytes, k3moe_stream s)
+{
+    if (!valid_groups(g) || !ids || !aligned(ids, 4) || !ws || !aligned(ws, 16) ||
+        ws_bytes < k3moe_groups_workspace(g->E, (int64_t)g->tokens * g->top_k))
+        return K3MOE_EINVAL;
+    return writing(s, [&] { return k3::launch_groups_plan(g, ids, ws, cs(s)); });
+}
+
+int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
+                         const k3moe_groups *g, int32_t gather, int32_t accumulate, k3moe_stream s)
+{
+    if (!valid_groups(g) || !valid_mx8(A) || !W || !W->codes || !W->atoms || !aligned(W->codes, 32) || !aligned(W->atoms, 16) ||
+        W->E != g->E || W->rows < 1 || W->rows > kMaxDim || W->in != A->in || W->in % 128 ||
+        W->codes_stride % 32 || W->codes_stride < (int64_t)W->rows * (W->in / 2) || W->codes_stride >= ((int64_t)1 << 40) ||
+        W->atoms_stride % 16 || W->atoms_stride < k3moe_mx_operand_atoms_bytes(W->rows, W->in) ||
+        W->atoms_stride > ((int64_t)1 << 40) || A->rows < (gather ? g->tokens : g->tokens * g->top_k) ||
+        !valid_dtype(c_dtype) || !valid_rows(C, c_dtype, ldc, W->rows) || (accumulate && c_dtype != K3MOE_F32))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        int *err = k3::device_error_word();
+        if (!err) return (int)K3MOE_ECUDA;
+        return k3::launch_grouped_matmul(C, c_dtype, (long)ldc, A, W, g, gather ? 1 : 0, accumulate ? 1 : 0, err, cs(s));
+    });
+}
+
+int k3moe_grouped_wgrad(void *dW, int dw_dtype, const void *dY, int64_t lddy, const void *X, int64_t ldx, int32_t xrows,
+                        int32_t N, int32_t K, const k3moe_groups *g, int32_t gather, int32_t accumulate, k3moe_stream s)
+{
+    if (!valid_groups(g) || N < 8 || K < 8 || N > kMaxIn || K > kMaxIn || N % 8 || K % 8 || !valid_dtype(dw_dtype) || !dW ||
+        !aligned(dW, 16) || !valid_rows(dY, K3MOE_BF16, lddy, N) || !valid_rows(X, K3MOE_BF16, ldx, K) || !aligned(dY, 16) ||
+        !aligned(X, 16) || lddy % 8 || ldx % 8 || lddy >= ((int64_t)1 << 39) || ldx >= ((int64_t)1 << 39) ||
+        (int64_t)N * K >= ((int64_t)1 << 38) || xrows < (gather ? g->tokens : g->tokens * g->top_k) || xrows > kMaxDim ||
+        (accumulate && dw_dtype != K3MOE_F32))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        int *err = k3::device_error_word();
+        if (!err) return (int)K3MOE_ECUDA;
+        return k3::launch_grouped_wgrad(dW, dw_dtype, dY, (long)lddy, X, (long)ldx, xrows, N, K, g, gather ? 1 : 0,
+                                        accumulate ? 1 : 0, err, cs(s));
+    });
+}
+
+// The grids take a token's columns by the thousand: 2^31 blocks at most.
+static bool valid_combine(const k3moe_groups *g, int dtype, int32_t n)
+{
+    return valid_groups(g) && valid_dtype(dtype) && n >= 1 && n <= kMaxIn &&
+           (int64_t)g->tokens * ((n + 1023) / 1024) <= 0x7fffffff;
+}
+
+int k3moe_combine(void *out, int64_t ldo, const void *y, int64_t ldy, int dtype, int32_t n, const k3moe_groups *g,
+                  const float *w, int32_t accumulate, k3moe_stream s)
+{
+    if (!valid_combine(g, dtype, n) || !valid_rows(out, dtype, ldo, n) || !valid_rows(y, dtype, ldy, n) || !aligned(w, 4) ||
+        out == y)
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        return k3::launch_combine(out, (long)ldo, y, (long)ldy, dtype, n, g, w, accumulate ? 1 : 0, cs(s));
+    });
+}
+
+int k3moe_combine_backward(void *dy, int64_t lddy, float *dw, const void *dout, int64_t lddo, const void *y, int64_t ldy,
+                           int dtype, int32_t n, const k3moe_groups *g, const float *w, k3moe_stream s)
+{
+    if (!valid_combine(g, dtype, n) || !valid_rows(dy, dtype, lddy, n) || !valid_rows(dout, dtype, lddo, n) || dy == dout ||
+        (dw && (!w || !valid_rows(y, dtype, ldy, n) || !aligned(dw, 4))) || !aligned(w, 4) ||
+        (dw && !apart_or_same(dy, lddy, y, ldy, 2)))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        return k3::launch_combine_backward(dy, (long)lddy, dw, dout, (long)lddo, y, (long)ldy, dtype, n, g, w, cs(s));
     });
 }
 

@@ -1,0 +1,375 @@
+// k3_grouped_wgrad.cu -- weight gradients grouped by expert, dW_e = dY_e^T X_e, on the
+// tensor cores (tcgen05.mma kind::f16, bf16 operands, fp32 sums).
+//
+// dW_e[n][k] = sum over the rows i of expert e's group of dY[i][n] X[i][k].  The sum
+// runs over rows, the slow axis of both matrices, so both operands are read as they
+// lie in memory (M- and N-major tiles, the 128-byte swizzle over 64 columns of a row)
+// and nothing is transposed.
+//
+// A persistent CTA walks (expert, 128 n, 256 k) tiles; a step is 64 rows of the group.
+// The last step's rows past the group come as zeros: they are gathered with a row index
+// outside the matrix.  Roles: warp 0 copies dY's columns, warp 2 X's (by index where X
+// has a row per token), warp 1 issues MMAs, warps 4 and up read one accumulator out
+// by TMA stores while the other one's products run.
+//
+// Every wait is bounded (2 s); a timeout sets the device error word and the CTA
+// drains its copies and MMAs, frees TMEM and exits.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "k3_launch.cuh"
+#include "k3_operand.cuh"
+#include "k3_tcgen05.cuh"
+#include "k3_tmem.cuh"
+
+namespace k3 {
+namespace {
+
+constexpr int GW_M = 128, GW_N = 256, GW_K = 64;  // n and k of a tile, rows of a step
+constexpr int GW_W_Y = 0, GW_W_MMA = 1, GW_W_X = 2, GW_W_EPI = 4;
+constexpr int GW_EPI = 8;  // epilogue warps: two per TMEM lane quadrant, on alternate pieces
+constexpr int GW_THREADS = (GW_W_EPI + GW_EPI) * 32;
+
+struct GwArgs {
+    const int32_t *offsets, *order;
+    int E, top_k, slots, gather, xrows;
+    int tiles_k, tiles_e;  // k tiles of a row of tiles, tiles of an expert
+    int N, accumulate;
+    int *err;
+};
+
+constexpr int GW_PANEL = GW_K * 128;  // 64 rows of 64 columns
+constexpr int GW_OFF_X = GW_M / 64 * GW_PANEL, GW_STAGE = GW_OFF_X + GW_N / 64 * GW_PANEL;
+constexpr int GW_NS = 4;
+constexpr int GW_BOX = 4096;  // a staged piece of dW: 32 rows of 128 bytes
+constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * GW_BOX;
+constexpr int GW_BARS = 2 * GW_NS + 2 * 2 + 1;
+constexpr int GW_SMEM = 1024 + GW_OFF_BAR + 256;
+static_assert(GW_SMEM <= 232448, "shared memory");
+
+// Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both M/N-major.
+constexpr uint32_t GW_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(GW_N >> 3) << 17) |
+                              ((uint32_t)(GW_M >> 4) << 24);
+
+// A step: four MMAs of 16 rows.  Descriptors of M/N-major tiles: panels of 64 columns
+// GW_PANEL bytes apart (leading offset), groups of eight rows 1024 bytes (stride).
+K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc)
+{
+#define GW_MMA(k2, pred)                                                                                     \
+    "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %4};\n\tmov.b64 db, {y, %4};\n\t" \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, " pred ";\n\t"
+    asm volatile("{\n\t.reg .pred p, t, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t" GW_MMA(0, "p") GW_MMA(128, "t") GW_MMA(256, "t")
+                     GW_MMA(384, "t") "}" ::"r"(tacc),
+                 "r"(ylo), "r"(xlo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC)
+                 : "memory");
+#undef GW_MMA
+}
+K3_DEV uint32_t mn_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(GW_PANEL >> 4) << 16); }
+
+K3_DEV void gw_gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&r)[4], uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
+                 : "memory");
+}
+K3_DEV void gw_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
+                 "r"(bytes)
+                 : "memory");
+}
+// A staged piece to (k, n) of expert e: stored, or added in fp32.
+K3_DEV void gw_store(const CUtensorMap *map, uint32_t src, int k, int n, int e, int accumulate)
+{
+    if (accumulate)
+        asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         (uint64_t)map),
+                     "r"(k), "r"(n), "r"(e), "r"(src)
+                     : "memory");
+    else
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                         (uint64_t)map),
+                     "r"(k), "r"(n), "r"(e), "r"(src)
+                     : "memory");
+}
+
+// Tile u: its expert, n, k, and the group's rows.
+struct GwTile {
+    int e, n0, k0, row, rows;
+};
+K3_DEV GwTile gw_tile(const GwArgs &a, int u)
+{
+    GwTile t;
+    t.e = u / a.tiles_e;
+    const int r = u - t.e * a.tiles_e;
+    t.n0 = r / a.tiles_k * GW_M;
+    t.k0 = r % a.tiles_k * GW_N;
+    t.row = max(a.offsets[t.e], 0);
+    t.rows = max(min(a.offsets[t.e + 1], a.slots) - t.row, 0);
+    return t;
+}
+
+// ymap, xmap: 64 columns x 64 rows; yrow, xrow: single rows for gathers.
+template <typename CT>
+__global__ void __launch_bounds__(GW_THREADS, 1)
+    k3_grouped_wgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap yrow,
+                     const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xrow,
+                     const __grid_constant__ CUtensorMap cmap, const GwArgs a)
+{
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_addr(sm);
+    uint64_t *bars = (uint64_t *)(sm + GW_OFF_BAR);
+    constexpr int NS = GW_NS;
+    constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2;
+    uint32_t *tmem_slot = (uint32_t *)(bars + GW_BARS);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    auto bar = [&](int i) { return smem_addr(bars + i); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NS; i++) {
+            mbar_init(bar(B_FULL + i), 2);
+            mbar_init(bar(B_EMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_ACCF + i), 1);
+            mbar_init(bar(B_ACCE + i), GW_EPI);
+        }
+        mbar_init(bar(B_FIN), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == GW_W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
+    griddep_wait();
+    const int n_tiles = a.E * a.tiles_e, first = (int)blockIdx.x, step = (int)gridDim.x;
+
+    if (warp == GW_W_Y || warp == GW_W_X) {
+        // ------------------------------------------------------- producers
+        const bool is_y = warp == GW_W_Y;
+        const CUtensorMap *map = is_y ? &ymap : &xmap, *rmap = is_y ? &yrow : &xrow;
+        const int panels = is_y ? GW_M / 64 : GW_N / 64, limit = is_y ? a.slots : a.xrows;
+        const bool by_index = !is_y && a.gather;
+        uint32_t it = 0, phase = 1;  // before its first completion an EMPTY barrier's odd phase counts as passed
+        int s = 0;
+        bool ok = true;
+        for (int u = first; u < n_tiles && ok; u += step) {
+            const GwTile t = gw_tile(a, u);
+            const int col = is_y ? t.n0 : t.k0, quad = 4 * (lane & 15);
+            for (int r0 = 0; r0 < t.rows; r0 += GW_K, it++) {
+                const bool gather = by_index || r0 + GW_K > t.rows;
+                int src[4];
+                if (gather)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int r = r0 + quad + i;
+                        int x = limit;  // past the group: a row outside the matrix, zeros
+                        if (r < t.rows) {
+                            x = t.row + r;
+                            if (by_index) x = a.order[x] / a.top_k;
+                            if (x < 0 || x > limit) x = limit;
+                        }
+                        src[i] = x;
+                    }
+                if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t dst = sbase + (uint32_t)(s * GW_STAGE + (is_y ? 0 : GW_OFF_X)), full = bar(B_FULL + s);
+                gw_expect(full, (uint32_t)(panels * GW_PANEL));
+                __syncwarp();
+                if (gather) {
+                    for (int p = lane >> 4; p < panels; p += 2)
+                        gw_gather4(dst + (uint32_t)(p * GW_PANEL + quad * 128), rmap, col + 64 * p, src, full);
+                } else if (lane < panels) {
+                    tma_load_2d(dst + (uint32_t)(lane * GW_PANEL), map, col + 64 * lane, t.row + r0, full);
+                }
+                __syncwarp();
+                if (++s == NS) s = 0, phase ^= 1u;
+            }
+        }
+        // drain: every copy issued here has landed before the CTA exits (the last
+        // NS of them; earlier ones were waited for before their reuse)
+        for (uint32_t i = it > (uint32_t)NS ? it - NS : 0; i < it; i++)
+            mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
+        __syncwarp();
+    } else if (warp == GW_W_MMA) {
+        // -------------------------------------------------------------- MMA
+        uint32_t ut = 0, phase = 0;  // ut: tiles with rows
+        int s = 0;
+        bool ok = true;
+        const uint32_t lo = mn_lo(sbase);
+        for (int u = first; u < n_tiles && ok; u += step) {
+            const GwTile t = gw_tile(a, u);
+            if (!t.rows) continue;
+            const int buf = (int)(ut & 1);
+            if (ut >= 2 && !__all_sync(0xffffffffu, tc_wait(bar(B_ACCE + buf), (ut / 2 - 1) & 1, a.err, abort_flag)))
+                break;
+            tc_fence_after();
+            for (int r0 = 0; r0 < t.rows; r0 += GW_K) {
+                if (!__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
+                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_X / 16, r0 ? 1u : 0u);
+                mma_commit(bar(B_EMPTY + s));
+                if (++s == NS) s = 0, phase ^= 1u;
+            }
+            if (!ok) break;
+            mma_commit(bar(B_ACCF + buf));
+            ut++;
+        }
+        // every MMA issued above has completed before TMEM is freed
+        mma_commit(bar(B_FIN));
+        mbar_wait(bar(B_FIN), 0, a.err);
+        __syncwarp();
+    } else if (warp >= GW_W_EPI) {
+        // --------------------------------------------------------- epilogue
+        // A lane holds one row n.  A warp stages 32 rows of 128 bytes (16-byte chunk c
+        // of row r at chunk c ^ (r mod 8), as the 128-byte swizzle has it) and they
+        // leave by TMA, clipped at the expert's matrix.
+        const int q = warp & 3, half = (warp - GW_W_EPI) >> 2;
+        constexpr int PC = 128 / (int)sizeof(CT), NP = GW_N / PC;  // columns of a piece, pieces of a tile
+        uint8_t *box = sm + GW_OFF_C + (warp - GW_W_EPI) * GW_BOX;
+        uint32_t ut = 0;
+        for (int u = first; u < n_tiles; u += step) {
+            const GwTile t = gw_tile(a, u);
+            if (!t.rows && a.accumulate) continue;
+            const int buf = (int)(ut & 1);
+            if (t.rows) {
+                if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
+                tc_fence_after();
+            }
+            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * GW_N);
+            const int n = t.n0 + q * 32;
+#pragma unroll 1
+            for (int j = half; j < NP; j += 2) {
+                uint32_t r[PC / 32][32];
+                if (t.rows) {
+#pragma unroll
+                    for (int h = 0; h < PC / 32; h++) tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r[h]);
+                    if (j + 2 >= NP) {  // this warp's last piece
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
+                    }
+                } else {
+#pragma unroll
+                    for (int h = 0; h < PC / 32; h++)
+#pragma unroll
+                        for (int c = 0; c < 32; c++) r[h][c] = 0u;
+                }
+                // the piece staged before has been read
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int h = 0; h < PC / 32; h++) {
+                    constexpr int W = 32 * (int)sizeof(CT) / 16;  // 16-byte chunks of 32 columns
+#pragma unroll
+                    for (int c = 0; c < W; c++) {
+                        uint4 v;
+                        if constexpr (sizeof(CT) == 2) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int x = 0; x < 4; x++) {
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[h][8 * c + 2 * x]),
+                                                                               __uint_as_float(r[h][8 * c + 2 * x + 1]));
+                                w[x] = *(const uint32_t *)&p;
+                            }
+                            v = make_uint4(w[0], w[1], w[2], w[3]);
+                        } else {
+                            v = make_uint4(r[h][4 * c], r[h][4 * c + 1], r[h][4 * c + 2], r[h][4 * c + 3]);
+                        }
+                        *(uint4 *)(box + lane * 128 + (((h * W + c) ^ (lane & 7)) << 4)) = v;
+                    }
+                }
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0 && n < a.N) {
+                    gw_store(&cmap, smem_addr(box), t.k0 + j * PC, n, t.e, a.accumulate);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+            if (t.rows) ut++;
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == GW_W_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------- launchers
+
+// A bf16 matrix in boxes of 64 columns x `rows`, 128-byte swizzle.
+int row_map(CUtensorMap *map, const void *p, int cols, int n_rows, long ld, int rows)
+{
+    const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)n_rows}, strides[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+template <typename CT>
+int launch_gw(void *dW, const void *dY, long lddy, const void *X, long ldx, int K, const GwArgs &a, cudaStream_t s)
+{
+    CUtensorMap ymap, yrow, xmap, xrow, cmap;
+    int st = row_map(&ymap, dY, a.N, a.slots, lddy, GW_K);
+    if (st == K3MOE_OK) st = row_map(&yrow, dY, a.N, a.slots, lddy, 1);
+    if (st == K3MOE_OK) st = row_map(&xmap, X, K, a.xrows, ldx, GW_K);
+    if (st == K3MOE_OK) st = row_map(&xrow, X, K, a.xrows, ldx, 1);
+    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)a.N, (cuuint64_t)a.E},
+                     strides[2] = {(cuuint64_t)K * sizeof(CT), (cuuint64_t)K * a.N * sizeof(CT)};
+    const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(CT)), 32, 1};
+    if (st == K3MOE_OK)
+        st = encode_map(&cmap, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dW,
+                        dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (st != K3MOE_OK) return st;
+    if (ensure_smem((const void *)k3_grouped_wgrad<CT>, GW_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
+    const int grid = std::min(a.E * a.tiles_e, num_sms());
+    if (launch_pdl(k3_grouped_wgrad<CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, yrow, xmap, xrow, cmap,
+                   a) != cudaSuccess) {
+        cudaGetLastError();
+        return K3MOE_ECUDA;
+    }
+    return K3MOE_OK;
+}
+
+}  // namespace
+
+int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const void *X, long ldx, int xrows, int N, int K,
+                         const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s)
+{
+    GwArgs a = {};
+    a.offsets = g->offsets, a.order = g->order;
+    a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = xrows;
+    a.tiles_k = (K + GW_N - 1) / GW_N;
+    const long tiles = (long)a.tiles_k * ((N + GW_M - 1) / GW_M);
+    if (tiles * a.E > 0x7fffffffL) return K3MOE_EINVAL;
+    a.tiles_e = (int)tiles;
+    a.N = N, a.accumulate = accumulate, a.err = err;
+    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(dW, dY, lddy, X, ldx, K, a, s)
+                              : launch_gw<float>(dW, dY, lddy, X, ldx, K, a, s);
+}
+
+}  // namespace k3

@@ -1,0 +1,329 @@
+// k3_groups.cu -- the slots of a routed batch grouped by expert, and the weighted
+// sum of each token's expert rows with its gradients.
+//
+// Grouping is a stable counting sort of ids[T][k] (slot t k + j): offsets[e] counts
+// the slots of lower experts, order lists the slots expert by expert in rising
+// order, pos is its inverse.  One CTA sorts up to GR_CHUNK slots: each warp counts
+// its own run of slots per expert, the counts are scanned over the warps and the
+// experts, and the warps place their slots 32 at a time (the lanes that hold one
+// expert rank themselves by a match).  More slots are cut in chunks: every chunk's
+// counts, one CTA's scan over them, and the placing.  Ranks come from positions,
+// never from the order of atomics, so the result is one and the same.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "k3_e4m3.cuh"
+#include "k3_launch.cuh"
+
+namespace k3 {
+namespace {
+
+constexpr int GR_THREADS = 1024, GR_WARPS = GR_THREADS / 32;
+constexpr int GR_CHUNK = 8192;  // slots of a CTA; a warp's run fits the 16-bit counts
+
+struct GroupArgs {
+    const int32_t *ids;
+    int32_t *offsets, *order, *pos, *counts;  // counts [chunks][E]: of a chunk, then where its slots start
+    int S, E, chunks;
+};
+
+// Exclusive sum over the block's threads; *total receives the whole sum.
+K3_DEV int block_scan(int v, int *warp_sums, int *total)
+{
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[w] = x;
+    __syncthreads();
+    if (w == 0) {
+        int s = warp_sums[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o) s += y;
+        }
+        warp_sums[lane] = s;
+    }
+    __syncthreads();
+    *total = warp_sums[31];
+    return x - v + (w ? warp_sums[w - 1] : 0);
+}
+
+// The expert of a slot, -1 for a dropped one.
+K3_DEV int expert_of(const GroupArgs &a, int slot, int end)
+{
+    if (slot >= end) return -1;
+    const int e = a.ids[slot];
+    return e >= 0 && e < a.E ? e : -1;
+}
+
+// WHOLE: one chunk is the batch.  Otherwise COUNT leaves the chunk's counts and the
+// placing pass reads where each expert's slots of this chunk start.
+template <bool WHOLE, bool COUNT>
+__global__ void __launch_bounds__(GR_THREADS) k3_groups(const GroupArgs a)
+{
+    extern __shared__ uint16_t cnt[];  // [GR_WARPS][E]: of a warp, then of the warps before it
+    __shared__ int warp_sums[32];
+    __shared__ int starts[1024];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    for (int i = threadIdx.x; i < GR_WARPS * a.E; i += GR_THREADS) cnt[i] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    const int first = (int)blockIdx.x * GR_CHUNK, n = min(GR_CHUNK, a.S - first), run = (n + GR_THREADS - 1) / GR_THREADS * 32;
+    const int s0 = first + w * run, s1 = min(first + n, s0 + run);
+    uint16_t *mine = cnt + w * a.E;
+    for (int s = s0; s < s1; s += 32) {
+        const int e = expert_of(a, s + lane, s1);
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        if (e >= 0 && (same & ((1u << lane) - 1)) == 0) mine[e] += (uint16_t)__popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    const int e = threadIdx.x;
+    int total = 0;
+    if (e < a.E)
+        for (int i = 0; i < GR_WARPS; i++) {
+            const int c = cnt[i * a.E + e];
+            cnt[i * a.E + e] = (uint16_t)total;
+            total += c;
+        }
+    if constexpr (COUNT) {
+        if (e < a.E) a.counts[(long)blockIdx.x * a.E + e] = total;
+        return;
+    }
+    int kept;
+    if constexpr (WHOLE) {
+        const int at = block_scan(total, warp_sums, &kept);
+        if (e < a.E) starts[e] = at, a.offsets[e] = at;
+        if (e == 0) a.offsets[a.E] = kept;
+    } else {
+        if (e < a.E) starts[e] = a.counts[(long)blockIdx.x * a.E + e];
+        kept = a.offsets[a.E];
+    }
+    __syncthreads();
+    for (int s = s0; s < s1; s += 32) {
+        const int x = expert_of(a, s + lane, s1);
+        const uint32_t same = __match_any_sync(0xffffffffu, x), before = same & ((1u << lane) - 1);
+        const int p = x >= 0 ? starts[x] + mine[x] + __popc(before) : -1;
+        __syncwarp();
+        if (x >= 0 && before == 0) mine[x] += (uint16_t)__popc(same);
+        __syncwarp();
+        if (s + lane < s1) {
+            a.pos[s + lane] = p;
+            if (p >= 0) a.order[p] = s + lane;
+        }
+    }
+    // the places behind the last group
+    for (int i = first + threadIdx.x; i < first + n; i += GR_THREADS)
+        if (i >= kept) a.order[i] = -1;
+}
+
+// Counts of the chunks to where their slots start, and the offsets.
+__global__ void __launch_bounds__(GR_THREADS) k3_groups_scan(const GroupArgs a)
+{
+    __shared__ int warp_sums[32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int e = threadIdx.x;
+    int total = 0, kept;
+    if (e < a.E)
+#pragma unroll 8
+        for (int c = 0; c < a.chunks; c++) total += a.counts[(long)c * a.E + e];
+    int at = block_scan(total, warp_sums, &kept);
+    if (e < a.E) {
+        a.offsets[e] = at;
+#pragma unroll 8
+        for (int c = 0; c < a.chunks; c++) {
+            const int v = a.counts[(long)c * a.E + e];
+            a.counts[(long)c * a.E + e] = at;
+            at += v;
+        }
+    }
+    if (e == 0) a.offsets[a.E] = kept;
+}
+
+// ------------------------------------------------------------- the combine
+//
+// out[t] (+)= sum_j w[t][j] y[pos[t][j]] over a token's slots, in rising j.
+// Bound: HBM, each row of y read once.  A thread takes eight columns of a token and
+// has up to CB_DEEP slots' loads in flight.
+
+constexpr int CB_DEEP = 8;
+
+struct CombineArgs {
+    const void *y, *dout;
+    void *out, *dy;
+    long ldy, ldo, lddy;  // ldo: of out, or of dout
+    const float *w;
+    float *dw;
+    const int32_t *pos;
+    int T, k, n, rows, accumulate;  // rows: slots, what pos stays below
+    int blocks;                     // forward: CTAs of a token
+};
+
+// Where slot j of a token's row is, -1 for a dropped one; its weight.
+K3_DEV int place_of(const CombineArgs &a, long slot)
+{
+    const int p = a.pos[slot];
+    return p >= 0 && p < a.rows ? p : -1;
+}
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(128) k3_combine(const CombineArgs a)
+{
+    griddep_wait();
+    griddep_launch_dependents();
+    const int t = (int)(blockIdx.x / (uint32_t)a.blocks), c = ((int)(blockIdx.x % (uint32_t)a.blocks) * 128 + (int)threadIdx.x) * 8;
+    if (c >= a.n) return;
+    float v[8] = {};
+    if (a.accumulate) {
+        const Raw<T> o = load8<T, VEC>(a.out, a.ldo, t, c, a.n);
+#pragma unroll
+        for (int i = 0; i < 8; i++) v[i] = value(o, i);
+    }
+    for (int j0 = 0; j0 < a.k; j0 += CB_DEEP) {
+        Raw<T> r[CB_DEEP];
+        float w[CB_DEEP];
+#pragma unroll
+        for (int j = 0; j < CB_DEEP; j++) {
+            const long slot = (long)t * a.k + j0 + j;
+            const int p = j0 + j < a.k ? place_of(a, slot) : -1;
+            w[j] = p < 0 ? 0.f : a.w ? a.w[slot] : 1.f;
+            r[j] = load8<T, VEC>(a.y, a.ldy, max(p, 0), p < 0 ? a.n : c, a.n);
+        }
+#pragma unroll
+        for (int j = 0; j < CB_DEEP; j++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] += w[j] * value(r[j], i);
+    }
+    store8<T, VEC>(a.out, a.ldo, t, c, a.n, v);
+}
+
+// dy[pos[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[pos[t][j]]>.  A CTA takes a
+// token, its threads eight columns at a time; the dot products of up to CB_DEEP slots
+// are joined together.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) k3_combine_backward(const CombineArgs a)
+{
+    __shared__ float sh[2][CB_DEEP][8];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int t = (int)blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    uint32_t turn = 0;
+    for (int j0 = 0; j0 < a.k; j0 += CB_DEEP, turn ^= 1) {
+        int p[CB_DEEP];
+        float w[CB_DEEP], dot[CB_DEEP];
+#pragma unroll
+        for (int j = 0; j < CB_DEEP; j++) {
+            const long slot = (long)t * a.k + j0 + j;
+            p[j] = j0 + j < a.k ? place_of(a, slot) : -1;
+            w[j] = p[j] < 0 ? 0.f : a.w ? a.w[slot] : 1.f;
+            dot[j] = 0.f;
+        }
+        for (int c = (int)threadIdx.x * 8; c < a.n; c += (int)blockDim.x * 8) {
+            const Raw<T> g = load8<T, VEC>(a.dout, a.ldo, t, c, a.n);
+            Raw<T> r[CB_DEEP];
+            if (a.dw)
+#pragma unroll
+                for (int j = 0; j < CB_DEEP; j++) r[j] = load8<T, VEC>(a.y, a.ldy, max(p[j], 0), p[j] < 0 ? a.n : c, a.n);
+            float d[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) d[i] = value(g, i);
+            if (a.dw)
+#pragma unroll
+                for (int j = 0; j < CB_DEEP; j++)
+                    if (p[j] >= 0)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) dot[j] += d[i] * value(r[j], i);
+#pragma unroll
+            for (int j = 0; j < CB_DEEP; j++)
+                if (p[j] >= 0) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) v[i] = w[j] * d[i];
+                    store8<T, VEC>(a.dy, a.lddy, p[j], c, a.n, v);
+                }
+        }
+        if (!a.dw) continue;
+#pragma unroll
+        for (int j = 0; j < CB_DEEP; j++) {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) dot[j] += __shfl_xor_sync(0xffffffffu, dot[j], o);
+            if (lane == 0) sh[turn][j][warp] = dot[j];
+        }
+        __syncthreads();
+        if ((int)threadIdx.x < CB_DEEP && j0 + (int)threadIdx.x < a.k) {
+            float v = 0.f;
+            for (int i = 0; i < nw; i++) v += sh[turn][threadIdx.x][i];
+            a.dw[(long)t * a.k + j0 + threadIdx.x] = v;
+        }
+    }
+}
+
+bool rows16(const void *p, long ld, int dtype)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
+}
+template <typename... KArgs, typename... Args>
+int launch(void (*kernel)(KArgs...), long grid, int threads, size_t smem, cudaStream_t s, const Args &...args)
+{
+    if (ensure_smem((const void *)kernel, smem) != K3MOE_OK) return K3MOE_ECUDA;
+    if (launch_pdl(kernel, dim3((unsigned)grid), dim3((unsigned)threads), smem, s, args...) != cudaSuccess) {
+        cudaGetLastError();
+        return K3MOE_ECUDA;
+    }
+    return K3MOE_OK;
+}
+
+}  // namespace
+
+size_t groups_workspace_bytes(int E, long slots)
+{
+    return slots <= GR_CHUNK ? 16 : (size_t)((slots + GR_CHUNK - 1) / GR_CHUNK) * E * sizeof(int32_t);
+}
+
+int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, cudaStream_t s)
+{
+    GroupArgs a = {ids, g->offsets, g->order, g->pos, (int32_t *)ws, g->tokens * g->top_k, g->E, 0};
+    a.chunks = (a.S + GR_CHUNK - 1) / GR_CHUNK;
+    const size_t smem = (size_t)GR_WARPS * a.E * sizeof(uint16_t);
+    if (a.chunks == 1) return launch(k3_groups<true, false>, 1, GR_THREADS, smem, s, a);
+    int st = launch(k3_groups<false, true>, a.chunks, GR_THREADS, smem, s, a);
+    if (st == K3MOE_OK) st = launch(k3_groups_scan, 1, GR_THREADS, 0, s, a);
+    if (st == K3MOE_OK) st = launch(k3_groups<false, false>, a.chunks, GR_THREADS, smem, s, a);
+    return st;
+}
+
+int launch_combine(void *out, long ldo, const void *y, long ldy, int dtype, int n, const k3moe_groups *g, const float *w,
+                   int accumulate, cudaStream_t s)
+{
+    CombineArgs a = {};
+    a.y = y, a.out = out, a.ldy = ldy, a.ldo = ldo, a.w = w, a.pos = g->pos;
+    a.T = g->tokens, a.k = g->top_k, a.n = n, a.rows = a.T * a.k, a.accumulate = accumulate;
+    a.blocks = (n + 1023) / 1024;
+    const bool vec = n % 8 == 0 && rows16(y, ldy, dtype) && rows16(out, ldo, dtype);
+    void (*const kernel)(CombineArgs) = dtype == K3MOE_BF16 ? (vec ? k3_combine<uint16_t, true> : k3_combine<uint16_t, false>)
+                                                            : (vec ? k3_combine<uint32_t, true> : k3_combine<uint32_t, false>);
+    return launch(kernel, (long)a.T * a.blocks, 128, 0, s, a);
+}
+
+int launch_combine_backward(void *dy, long lddy, float *dw, const void *dout, long lddo, const void *y, long ldy, int dtype,
+                            int n, const k3moe_groups *g, const float *w, cudaStream_t s)
+{
+    CombineArgs a = {};
+    a.y = y, a.dout = dout, a.dy = dy, a.dw = dw, a.ldy = ldy, a.ldo = lddo, a.lddy = lddy, a.w = w, a.pos = g->pos;
+    a.T = g->tokens, a.k = g->top_k, a.n = n, a.rows = a.T * a.k;
+    const bool vec = n % 8 == 0 && rows16(dout, lddo, dtype) && rows16(dy, lddy, dtype) && (!dw || rows16(y, ldy, dtype));
+    void (*const kernel)(CombineArgs) = dtype == K3MOE_BF16
+                                            ? (vec ? k3_combine_backward<uint16_t, true> : k3_combine_backward<uint16_t, false>)
+                                            : (vec ? k3_combine_backward<uint32_t, true> : k3_combine_backward<uint32_t, false>);
+    return launch(kernel, a.T, std::min(256, (n + 255) / 256 * 32), 0, s, a);
+}
+
+}  // namespace k3

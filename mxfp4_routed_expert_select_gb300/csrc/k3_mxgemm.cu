@@ -36,6 +36,7 @@
 #include "k3_launch.cuh"
 #include "k3_operand.cuh"
 #include "k3_tcgen05.cuh"
+#include "k3_tmem.cuh"
 
 namespace k3 {
 namespace {
@@ -119,41 +120,6 @@ K3_DEV void mg_step(uint32_t tacc, uint32_t slo, uint32_t tlo, uint32_t sal, uin
 #undef MG_CP
 #undef MG_MMA
 #undef MG_OPERANDS
-
-// 16 or 32 columns of the accumulator, one row per lane.  The wait names the
-// registers, so that nothing made from them can move above it.
-K3_DEV void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[16])
-{
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-                 "%14, %15}, [%16];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-                   "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-                 : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
-                 :
-                 : "memory");
-}
-K3_DEV void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                   "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                   "+r"(r[30]), "+r"(r[31])
-                 :
-                 : "memory");
-}
 
 K3_DEV uint32_t cluster_rank()
 {
@@ -861,32 +827,6 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
 
 // ---------------------------------------------------------------- launchers
 
-PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) !=
-                cudaSuccess ||
-            q != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            fn = nullptr;
-        }
-        return (PFN_cuTensorMapEncodeTiled_v12000)fn;
-    }();
-    return encode;
-}
-int make_map(CUtensorMap *map, CUtensorMapDataType type, int nd, const void *p, const cuuint64_t *dims,
-             const cuuint64_t *strides, const cuuint32_t *box, CUtensorMapSwizzle swizzle)
-{
-    const auto encode = map_encoder();
-    if (!encode) return K3MOE_ECUDA;
-    const cuuint32_t estr[3] = {1, 1, 1};
-    return encode(map, type, (cuuint32_t)nd, (void *)p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
-                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-               ? K3MOE_OK
-               : K3MOE_EINVAL;
-}
 // Codes plane of an operand in boxes of box_rows x 128 bytes (256 codes),
 // 128-byte swizzle; rows and bytes past the plane read as zero.
 int code_map(CUtensorMap *map, const k3moe_mx_operand *op, int box_rows)
@@ -894,7 +834,7 @@ int code_map(CUtensorMap *map, const k3moe_mx_operand *op, int box_rows)
     const cuuint64_t width = (cuuint64_t)(op_in_padded(op->in) / 2);
     const cuuint64_t dims[2] = {width, (cuuint64_t)op->rows}, strides[1] = {width};
     const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, op->codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, op->codes, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 // The scale atoms of an operand, [row tile][k][512 bytes], in boxes of two k of
 // `tiles` row tiles.
@@ -903,7 +843,7 @@ int atom_map(CUtensorMap *map, const k3moe_mx_operand *op, int tiles)
     const cuuint64_t nk = (cuuint64_t)op_k_atoms(op->in);
     const cuuint64_t dims[3] = {128, nk, (cuuint64_t)op_row_tiles(op->rows)}, strides[2] = {512, nk * 512};
     const cuuint32_t box[3] = {128, 2, (cuuint32_t)tiles};
-    return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, op->atoms, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, op->atoms, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 // C in boxes of a staged piece: 32 rows of 128 bytes, 128-byte swizzle.
 template <typename CT>
@@ -911,7 +851,7 @@ int c_map(CUtensorMap *map, const MgArgs &a)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)a.N, (cuuint64_t)a.M}, strides[1] = {(cuuint64_t)a.ldc * sizeof(CT)};
     const cuuint32_t box[2] = {(cuuint32_t)(128 / sizeof(CT)), 32};
-    return make_map(map, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.C, dims,
+    return encode_map(map, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, a.C, dims,
                     strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 

@@ -1,0 +1,448 @@
+// k3_norm.cu -- root-mean-square norm of a residual stream's rows, forward and
+// backward, and the 8-bit rows (k3moe_mx8_rows) by themselves.
+//
+// r = x + delta, rounded to its type (the stream that the next layer adds to);
+// s = 1 / sqrt(mean r^2 + eps);  y = r s gain.  With g = dy gain and xhat = r s
+//   dx = dr + s (g - xhat mean(g xhat)),   dgain = sum over rows of dy xhat.
+//
+// Bound: HBM, one pass each way.  A team of warps holds a row, C chunks of eight
+// values a thread, and takes one row after the other, so that its gains (and the
+// sums of dgain) stay in registers and the next row's loads are in flight while
+// this one's sum is joined.  The column sums of the teams meet in a second small
+// kernel, in an order that does not depend on timing.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <climits>
+
+#include "k3_e4m3.cuh"
+#include "k3_launch.cuh"
+
+namespace k3 {
+namespace {
+
+constexpr int NORM_PARTS = 512;    // rows of column sums in the workspace
+constexpr int NORM_THREADS = 512;  // of a CTA at most
+
+struct NormArgs {
+    const void *x, *delta, *dy, *dr;  // backward: x is r
+    void *y, *r, *dx;
+    long ldx, ldd, lddy, lddr, ldy, ldr, lddx;
+    const float *gain;
+    float *rstd, *parts;
+    uint8_t *codes, *scales;
+    int T, n, warps;  // warps of a team
+    float eps, inv_n;
+};
+
+// Eight values as the bits of fp32.
+template <typename T>
+K3_DEV Raw<uint32_t> widened(const float (&v)[8])
+{
+    Raw<uint32_t> r;
+#pragma unroll
+    for (int i = 0; i < 8; i++) r.w[i] = __float_as_uint(v[i]);
+    return r;
+}
+// v rounded to the rows' type.
+template <typename T>
+K3_DEV float rounded(float v)
+{
+    return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v;
+}
+K3_DEV float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+K3_DEV float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// A team's warps, its barrier and its slots for partial results.  Two sets of
+// slots in turn: a warp that has passed one barrier cannot reach the second next
+// one's writes before the others have read.
+struct Team {
+    int warps, warp, lane, bar;
+    float *slots;  // [2][32]
+    uint32_t turn;
+
+    template <bool MAX>
+    K3_DEV float all(float v)
+    {
+        v = MAX ? warp_max(v) : warp_sum(v);
+        if (warps == 1) return v;
+        float *s = slots + (turn++ & 1) * 32;
+        if (lane == 0) s[warp] = v;
+        asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(warps * 32) : "memory");
+        v = lane < warps ? s[lane] : 0.f;
+        return MAX ? warp_max(v) : warp_sum(v);
+    }
+    K3_DEV float sum(float v) { return all<false>(v); }
+    K3_DEV float max(float v) { return all<true>(v); }  // of magnitudes
+};
+
+// 1 / sqrt(mean v^2 + eps) where the sum of squares left fp32's range or its normal
+// numbers while its root need not: the values scaled by a power of two.
+template <int C>
+__device__ __noinline__ float far_rstd(Team &team, const float (&v)[C][8], float ss, float inv_n, float eps)
+{
+    float m = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[c][i]));
+    m = team.max(m);
+    if (!(m > 0.f) || m > 3.4028235e38f || ss != ss) return rsqrtf(ss * inv_n + eps);
+    const int e = max(-126, min(126, 126 - (int)(__float_as_uint(m) >> 23)));
+    const float s = __uint_as_float((uint32_t)(127 + e) << 23);
+    float t = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) t += v[c][i] * s * (v[c][i] * s);
+    t = team.sum(t);
+    const float es = eps * s * s;
+    return es > 1e37f ? rsqrtf(eps) : rsqrtf(t * inv_n + es) * s;
+}
+
+// Where this thread's row team stands: first row, rows to the next.
+K3_DEV Team make_team(int warps, float (*slots)[64], int &first, int &step)
+{
+    const int teams = (int)(blockDim.x >> 5) / warps, w = threadIdx.x >> 5, id = w / warps;
+    first = (int)blockIdx.x * teams + id;
+    step = (int)gridDim.x * teams;
+    return Team{warps, w - id * warps, (int)threadIdx.x & 31, 1 + id, slots[id], 0};
+}
+template <int C>
+K3_DEV void load_gain(float (&gn)[C][8], const float *gain, int col0, int stride, int n)
+{
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const int col = col0 + c * stride + i;
+            gn[c][i] = gain && col < n ? gain[col] : 1.f;
+        }
+}
+
+template <typename T, bool VEC, int C>
+__global__ void __launch_bounds__(NORM_THREADS) k3_norm_forward(const NormArgs a)
+{
+    __shared__ float slots[8][64];
+    griddep_wait();
+    griddep_launch_dependents();
+    int t, step;
+    Team team = make_team(a.warps, slots, t, step);
+    const int tid = team.warp * 32 + team.lane, stride = a.warps * 256, col0 = tid * 8;
+    float gn[C][8];
+    load_gain(gn, a.gain, col0, stride, a.n);
+    Raw<T> x[C], d[C];
+    auto load = [&](int row) {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const int col = row < a.T ? col0 + c * stride : a.n;
+            x[c] = load8<T, VEC>(a.x, a.ldx, row, col, a.n);
+            if (a.delta) d[c] = load8<T, VEC>(a.delta, a.ldd, row, col, a.n);
+        }
+    };
+    load(t);
+    for (; t < a.T; t += step) {
+        float v[C][8], ss = 0.f;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                v[c][i] = value(x[c], i);
+                if (a.delta) v[c][i] = rounded<T>(v[c][i] + value(d[c], i));
+                ss += v[c][i] * v[c][i];
+            }
+        load(t + step);
+        if (a.r)
+#pragma unroll
+            for (int c = 0; c < C; c++) store8<T, VEC>(a.r, a.ldr, t, col0 + c * stride, a.n, v[c]);
+        ss = team.sum(ss);
+        // the sum is exact enough unless it left the normal range, or fell below
+        // where eps outweighs what it lost
+        float s = rsqrtf(ss * a.inv_n + a.eps);
+        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f)) s = far_rstd<C>(team, v, ss, a.inv_n, a.eps);
+        if (a.rstd && tid == 0) a.rstd[t] = s;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[c][i] = v[c][i] * s * gn[c][i];
+        if (a.y)
+#pragma unroll
+            for (int c = 0; c < C; c++) store8<T, VEC>(a.y, a.ldy, t, col0 + c * stride, a.n, v[c]);
+        if (a.codes)
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+                const int col = col0 + c * stride;
+                float q[8];
+#pragma unroll
+                for (int i = 0; i < 8; i++) q[i] = col + i < a.n ? v[c][i] : 0.f;
+                store_mx8(a.codes, a.scales, a.n, t, col, widened<T>(q));
+            }
+    }
+}
+
+template <typename T, bool VEC, int C>
+__global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs a)
+{
+    __shared__ float slots[8][64];
+    griddep_wait();
+    griddep_launch_dependents();
+    int t, step;
+    Team team = make_team(a.warps, slots, t, step);
+    const int part = t, tid = team.warp * 32 + team.lane, stride = a.warps * 256, col0 = tid * 8;
+    float gn[C][8], sum[C][8];
+    load_gain(gn, a.gain, col0, stride, a.n);
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum[c][i] = 0.f;
+    Raw<T> x[C], dy[C], dr[C];
+    float s = 0.f;
+    auto load = [&](int row) {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            const int col = row < a.T ? col0 + c * stride : a.n;
+            x[c] = load8<T, VEC>(a.x, a.ldx, row, col, a.n);
+            dy[c] = load8<T, VEC>(a.dy, a.lddy, row, col, a.n);
+            if (a.dr) dr[c] = load8<T, VEC>(a.dr, a.lddr, row, col, a.n);
+        }
+        s = row < a.T ? a.rstd[row] : 0.f;
+    };
+    load(t);
+    for (; t < a.T; t += step) {
+        float xh[C][8], g[C][8], res[C][8], dot = 0.f;
+        const float sc = s;
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                xh[c][i] = value(x[c], i) * sc;
+                const float dv = value(dy[c], i);
+                sum[c][i] += dv * xh[c][i];
+                g[c][i] = dv * gn[c][i];
+                dot += g[c][i] * xh[c][i];
+                res[c][i] = a.dr ? value(dr[c], i) : 0.f;
+            }
+        load(t + step);
+        dot = team.sum(dot) * a.inv_n;
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) g[c][i] = res[c][i] + sc * (g[c][i] - xh[c][i] * dot);
+            store8<T, VEC>(a.dx, a.lddx, t, col0 + c * stride, a.n, g[c]);
+        }
+    }
+    if (a.parts)
+#pragma unroll
+        for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (col0 + c * stride + i < a.n) a.parts[(long)part * a.n + col0 + c * stride + i] = sum[c][i];
+}
+
+// dgain[c] (+)= the sum of its column over the parts.  A block takes 32 columns, its
+// eight warps a share of the parts each.
+__global__ void __launch_bounds__(256) k3_norm_columns(float *dgain, const float *parts, int n, int n_parts, int accumulate)
+{
+    __shared__ float sh[8][32];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = (int)blockIdx.x * 32 + lane;
+    float v = 0.f;
+    if (col < n)
+#pragma unroll 8
+        for (int p = w; p < n_parts; p += 8) v += parts[(long)p * n + col];
+    sh[w][lane] = v;
+    __syncthreads();
+    if (w == 0 && col < n) {
+#pragma unroll
+        for (int i = 1; i < 8; i++) v += sh[i][lane];
+        dgain[col] = accumulate ? dgain[col] + v : v;
+    }
+}
+
+// ------------------------------------------------------------- 8-bit rows
+
+constexpr int M8_THREADS = 256;
+
+struct Mx8Args {
+    const void *x;
+    void *y;
+    long ld;
+    uint8_t *codes, *scales;
+    uint32_t n;   // eight-value chunks of this launch, rows x cpr, below 2^31
+    int in;
+    FastDiv cpr;  // chunks per row, ceil128(in) / 8
+};
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(M8_THREADS) k3_mx8_quantize(const Mx8Args a)
+{
+    griddep_wait();
+    const uint32_t i = blockIdx.x * M8_THREADS + threadIdx.x;
+    const uint32_t t = a.cpr.div(i);
+    const int c = i < a.n ? (int)(i - t * a.cpr.d) * 8 : INT_MAX - 8;
+    const Raw<T> v = load8<T, VEC>(a.x, a.ld, (int)t, c, a.in);
+    store_mx8(a.codes, a.scales, a.in, (int)t, c, v);
+}
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(M8_THREADS) k3_mx8_dequantize(const Mx8Args a)
+{
+    griddep_wait();
+    const uint32_t i = blockIdx.x * M8_THREADS + threadIdx.x;
+    if (i >= a.n) return;
+    const uint32_t t = a.cpr.div(i);
+    const int c = (int)(i - t * a.cpr.d) * 8;
+    if (c >= a.in) return;
+    const uint2 q = *(const uint2 *)(a.codes + (long)t * op_in_padded(a.in) + c);
+    const uint32_t e = a.scales[(long)t * mx8_scale_stride(a.in) + c / 32];
+    float v[8];
+    from_e4m3x8(q, e, v);
+    store8<T, VEC>(a.y, a.ld, (int)t, c, a.in, v);
+}
+
+bool rows16(const void *p, long ld, int dtype)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
+}
+
+// Chunks a thread, by the row's length: few, so that the next row's chunks fit in
+// registers beside this one's.
+template <typename T, bool VEC>
+auto pick(int c, bool backward) -> void (*)(NormArgs)
+{
+    if (backward)
+        return c == 1 ? k3_norm_backward<T, VEC, 1> : c == 2 ? k3_norm_backward<T, VEC, 2>
+               : c == 4 ? k3_norm_backward<T, VEC, 4> : k3_norm_backward<T, VEC, 8>;
+    return c == 1 ? k3_norm_forward<T, VEC, 1> : c == 2 ? k3_norm_forward<T, VEC, 2>
+           : c == 4 ? k3_norm_forward<T, VEC, 4> : k3_norm_forward<T, VEC, 8>;
+}
+struct NormPlan {
+    int c, warps, teams, grid;
+};
+NormPlan norm_plan(int T, int n)
+{
+    NormPlan p;
+    const int chunks = (n + 7) / 8;
+    p.c = chunks <= 128 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+    p.warps = (chunks + 32 * p.c - 1) / (32 * p.c);
+    p.teams = std::max(1, 8 / p.warps);
+    const int threads = p.warps * p.teams * 32;
+    p.grid = (int)std::min<long>((T + p.teams - 1L) / p.teams, (long)num_sms() * std::max(1, 1024 / threads));
+    return p;
+}
+int launch_norm(NormArgs a, int dtype, bool vec, bool backward, const NormPlan &p, cudaStream_t s)
+{
+    a.warps = p.warps;
+    a.inv_n = 1.f / (float)a.n;
+    vec = vec && a.n % 8 == 0;
+    void (*const kernel)(NormArgs) = dtype == K3MOE_BF16
+                                         ? (vec ? pick<uint16_t, true>(p.c, backward) : pick<uint16_t, false>(p.c, backward))
+                                         : (vec ? pick<uint32_t, true>(p.c, backward) : pick<uint32_t, false>(p.c, backward));
+    if (launch_pdl(kernel, dim3((unsigned)p.grid), dim3((unsigned)(p.warps * p.teams * 32)), 0, s, a) != cudaSuccess) {
+        cudaGetLastError();
+        return K3MOE_ECUDA;
+    }
+    return K3MOE_OK;
+}
+
+template <typename K>
+int launch_mx8(K pick_kernel, Mx8Args a, int dtype, int rows, bool vec, cudaStream_t s)
+{
+    const int es = dtype == K3MOE_BF16 ? 2 : 4;
+    const uint32_t cpr = (uint32_t)mx8_scale_stride(a.in) * 4;
+    a.cpr = FastDiv(cpr);
+    vec = vec && a.in % 8 == 0;
+    void (*const kernel)(Mx8Args) = pick_kernel(dtype == K3MOE_BF16, vec);
+    const int step = (int)std::min<long>(rows, std::max<long>(1, (1L << 28) / cpr));
+    for (int t = 0; t < rows; t += step) {
+        const int r = std::min(step, rows - t);
+        a.n = (uint32_t)r * cpr;
+        if (launch_pdl(kernel, dim3((a.n + M8_THREADS - 1) / M8_THREADS), dim3(M8_THREADS), 0, s, a) != cudaSuccess) {
+            cudaGetLastError();
+            return K3MOE_ECUDA;
+        }
+        if (a.x) a.x = (const char *)a.x + (size_t)r * a.ld * es;
+        if (a.y) a.y = (char *)a.y + (size_t)r * a.ld * es;
+        a.codes += (size_t)r * op_in_padded(a.in);
+        a.scales += (size_t)r * mx8_scale_stride(a.in);
+    }
+    return K3MOE_OK;
+}
+
+}  // namespace
+
+size_t norm_workspace_bytes(int n) { return (size_t)NORM_PARTS * (size_t)n * sizeof(float); }
+
+int launch_norm_forward(void *y, long ldy, void *r, long ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
+                        long ldx, const void *delta, long ldd, const float *gain, int dtype, int T, int n, float eps,
+                        cudaStream_t s)
+{
+    NormArgs a = {};
+    a.x = x, a.delta = delta, a.y = y, a.r = r;
+    a.ldx = ldx, a.ldd = ldd, a.ldy = ldy, a.ldr = ldr;
+    a.gain = gain, a.rstd = rstd;
+    if (y8) a.codes = y8->codes, a.scales = y8->scales;
+    a.T = T, a.n = n, a.eps = eps;
+    const bool vec = rows16(x, ldx, dtype) && (!delta || rows16(delta, ldd, dtype)) && (!y || rows16(y, ldy, dtype)) &&
+                     (!r || rows16(r, ldr, dtype));
+    return launch_norm(a, dtype, vec, false, norm_plan(T, n), s);
+}
+
+int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, const void *dy, long lddy, const void *dr,
+                         long lddr, const void *r, long ldr, const float *rstd, const float *gain, int dtype, int T,
+                         int n, void *ws, cudaStream_t s)
+{
+    NormArgs a = {};
+    a.x = r, a.dy = dy, a.dr = dr, a.dx = dx;
+    a.ldx = ldr, a.lddy = lddy, a.lddr = lddr, a.lddx = lddx;
+    a.gain = gain, a.rstd = (float *)rstd;
+    a.parts = dgain ? (float *)ws : nullptr;
+    a.T = T, a.n = n;
+    const bool vec = rows16(r, ldr, dtype) && rows16(dy, lddy, dtype) && (!dr || rows16(dr, lddr, dtype)) &&
+                     rows16(dx, lddx, dtype);
+    NormPlan p = norm_plan(T, n);
+    p.grid = std::min(p.grid, NORM_PARTS / p.teams);
+    const int st = launch_norm(a, dtype, vec, true, p, s);
+    if (st != K3MOE_OK || !dgain) return st;
+    if (launch_pdl(k3_norm_columns, dim3((unsigned)((n + 31) / 32)), dim3(256), 0, s, dgain, (const float *)ws, n,
+                   p.grid * p.teams, accumulate) != cudaSuccess) {
+        cudaGetLastError();
+        return K3MOE_ECUDA;
+    }
+    return K3MOE_OK;
+}
+
+int launch_mx8_quantize(const k3moe_mx8_rows *o, const void *x, int dtype, long ld, cudaStream_t s)
+{
+    Mx8Args a = {};
+    a.x = x, a.ld = ld, a.codes = o->codes, a.scales = o->scales, a.in = o->in;
+    return launch_mx8(
+        [](bool bf16, bool vec) {
+            return bf16 ? (vec ? k3_mx8_quantize<uint16_t, true> : k3_mx8_quantize<uint16_t, false>)
+                        : (vec ? k3_mx8_quantize<uint32_t, true> : k3_mx8_quantize<uint32_t, false>);
+        },
+        a, dtype, o->rows, rows16(x, ld, dtype), s);
+}
+int launch_mx8_dequantize(void *y, int dtype, long ld, const k3moe_mx8_rows *o, cudaStream_t s)
+{
+    Mx8Args a = {};
+    a.y = y, a.ld = ld, a.codes = o->codes, a.scales = o->scales, a.in = o->in;
+    return launch_mx8(
+        [](bool bf16, bool vec) {
+            return bf16 ? (vec ? k3_mx8_dequantize<uint16_t, true> : k3_mx8_dequantize<uint16_t, false>)
+                        : (vec ? k3_mx8_dequantize<uint32_t, true> : k3_mx8_dequantize<uint32_t, false>);
+        },
+        a, dtype, o->rows, rows16(y, ld, dtype), s);
+}
+
+}  // namespace k3

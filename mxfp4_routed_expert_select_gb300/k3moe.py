@@ -98,6 +98,22 @@ class MxOperandStruct(ctypes.Structure):
                 ("rows", ctypes.c_int32), ("in_", ctypes.c_int32)]
 
 
+class Mx8RowsStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int32), ("in_", ctypes.c_int32)]
+
+
+class GroupsStruct(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("order", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("tokens", ctypes.c_int32)]
+
+
+class MxExpertsStruct(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("atoms", ctypes.c_void_p), ("codes_stride", ctypes.c_int64),
+                ("atoms_stride", ctypes.c_int64), ("E", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("in_", ctypes.c_int32)]
+
+
 ALLOC_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t,
                             ctypes.POINTER(ctypes.c_void_p))
 FREE_FN = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p)
@@ -155,6 +171,20 @@ SIGNATURES = {
     "k3moe_balance_forward": (ctypes.c_int, [_P, _P, _P, _P, _I, _I64, _P, _P, _I, _I, _I, _F, _I, _P, _SZ, _P]),
     "k3moe_balance_backward": (ctypes.c_int, [_P, _I64, _P, _I, _I64, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _F,
                                               _I, _P]),
+    "k3moe_mx8_codes_bytes": (_I64, [_I, _I]),
+    "k3moe_mx8_scales_bytes": (_I64, [_I, _I]),
+    "k3moe_mx8_quantize": (ctypes.c_int, [_P, _P, _I, _I64, _P]),
+    "k3moe_mx8_dequantize": (ctypes.c_int, [_P, _I, _I64, _P, _P]),
+    "k3moe_norm_workspace": (_SZ, [_I]),
+    "k3moe_norm_forward": (ctypes.c_int, [_P, _I64, _P, _I64, _P, _P, _P, _I64, _P, _I64, _P, _I, _I, _I, _F, _P]),
+    "k3moe_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _P, _SZ,
+                                           _P]),
+    "k3moe_groups_workspace": (_SZ, [_I, _I64]),
+    "k3moe_groups_plan": (ctypes.c_int, [_P, _P, _P, _SZ, _P]),
+    "k3moe_grouped_matmul": (ctypes.c_int, [_P, _I, _I64, _P, _P, _P, _I, _I, _P]),
+    "k3moe_grouped_wgrad": (ctypes.c_int, [_P, _I, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _I, _P]),
+    "k3moe_combine": (ctypes.c_int, [_P, _I64, _P, _I64, _I, _I, _P, _P, _I, _P]),
+    "k3moe_combine_backward": (ctypes.c_int, [_P, _I64, _P, _P, _I64, _P, _I64, _I, _I, _P, _P, _P]),
     "k3moe_rmsnorm": (ctypes.c_int, [_P, _P, _I, _F, _P]),
     "k3moe_residual_add": (ctypes.c_int, [_P, _P, _I, _P]),
     "k3moe_cache_create": (ctypes.c_int, [_P, _SZ, _SZ, _P, _I, _I]),
@@ -482,6 +512,266 @@ def swiglu_backward(dg, du, dh, ckpt, stream=None):
                                                _dtype(dg, du, dh), T, f, _stream(stream))
     if st:
         check(st, "k3moe_swiglu_backward")
+
+
+class Mx8Rows:
+    """Activations in 8 bits (k3moe_mx8_rows): `rows` rows of `in_` values, e4m3 codes
+    with a scale per 32.  Holds the device buffers `codes` and `scales`; filled by
+    mx8_quantize or RmsNorm.forward."""
+
+    def __init__(self, rows, in_, device="cuda"):
+        import torch
+        nc, ns = lib().k3moe_mx8_codes_bytes(rows, in_), lib().k3moe_mx8_scales_bytes(rows, in_)
+        if nc < 0 or ns < 0:
+            raise K3Error(K3MOE_EINVAL, "Mx8Rows(%d, %d)" % (rows, in_))
+        self.rows, self.in_ = rows, in_
+        self.codes = torch.empty(nc, dtype=torch.uint8, device=device)
+        self.scales = torch.empty(ns, dtype=torch.uint8, device=self.codes.device)
+        self.gpu = _gpu(self.codes)
+        self.struct = Mx8RowsStruct(self.codes.data_ptr(), self.scales.data_ptr(), rows, in_)
+        self.ref = ctypes.byref(self.struct)
+
+
+def mx8_quantize(rows8, x, stream=None):
+    """x [rows8.rows][rows8.in_] (fp32 or bf16) to 8 bits."""
+    if x.get_device() != rows8.gpu:
+        _elsewhere(rows8.gpu, x)
+    st = (_lib or lib()).k3moe_mx8_quantize(rows8.ref, x.data_ptr(), _dtype(x), _ld(x, rows8.rows, rows8.in_),
+                                            _stream(stream))
+    if st:
+        check(st, "k3moe_mx8_quantize")
+
+
+def mx8_dequantize(y, rows8, stream=None):
+    """The values of 8-bit rows into y [rows8.rows][rows8.in_] (fp32 or bf16)."""
+    if y.get_device() != rows8.gpu:
+        _elsewhere(rows8.gpu, y)
+    st = (_lib or lib()).k3moe_mx8_dequantize(y.data_ptr(), _dtype(y), _ld(y, rows8.rows, rows8.in_), rows8.ref,
+                                              _stream(stream))
+    if st:
+        check(st, "k3moe_mx8_dequantize")
+
+
+class RmsNorm:
+    """k3moe_norm_*: the norm of rows of n values with the residual's addition, and
+    its gradients.  Owns the backward call's workspace, so one object's backward calls
+    serve one stream at a time."""
+
+    def __init__(self, n, eps, device="cuda"):
+        import torch
+        nb = lib().k3moe_norm_workspace(n)
+        if nb == 0:
+            raise K3Error(K3MOE_EINVAL, "RmsNorm(n=%d)" % n)
+        self.n, self.eps = n, eps
+        self.workspace = torch.empty(nb, dtype=torch.uint8, device=device)
+        self._ws = self.workspace.data_ptr(), nb
+        self._f32 = torch.float32
+        self.gpu = _gpu(self.workspace)
+
+    def _rows(self, t, T, dtype):
+        if t is None:
+            return None, 0
+        if t.dtype is not dtype:
+            raise TypeError("tensors of one type expected, got %s and %s" % (dtype, t.dtype))
+        return t.data_ptr(), _ld(t, T, self.n)
+
+    def forward(self, y, x, delta=None, r=None, rstd=None, gain=None, y8=None, stream=None):
+        """r = x + delta; y (rows' type) and / or y8 (Mx8Rows) = r / sqrt(mean r^2 +
+        eps) * gain; rstd fp32 [T].  x, delta, r, y [T][n] of one type, gain fp32 [n]."""
+        T, dt, gpu = x.shape[0], x.dtype, self.gpu
+        if (x.get_device() != gpu or (y is not None and y.get_device() != gpu) or
+                (delta is not None and delta.get_device() != gpu) or (r is not None and r.get_device() != gpu) or
+                (rstd is not None and rstd.get_device() != gpu) or (gain is not None and gain.get_device() != gpu) or
+                (y8 is not None and y8.gpu != gpu)):
+            _elsewhere(gpu, x, y, delta, r, rstd, gain, None if y8 is None else y8.codes)
+        st = (_lib or lib()).k3moe_norm_forward(
+            *self._rows(y, T, dt), *self._rows(r, T, dt), _flat(rstd, self._f32, T), y8 and y8.ref,
+            *self._rows(x, T, dt), *self._rows(delta, T, dt), _flat(gain, self._f32, self.n), _dtype(x), T, self.n,
+            self.eps, _stream(stream))
+        if st:
+            check(st, "k3moe_norm_forward")
+
+    def backward(self, dx, dgain, dy, r, rstd, gain=None, dr=None, accumulate=False, stream=None):
+        """dx [T][n] and dgain fp32 [n] (or None; accumulate adds into it) from dy, the
+        forward call's r (x where there was no delta) and rstd, and the gradient dr that
+        reaches r past the norm."""
+        T, dt, gpu = dy.shape[0], dy.dtype, self.gpu
+        if (dx.get_device() != gpu or dy.get_device() != gpu or r.get_device() != gpu or rstd.get_device() != gpu or
+                (dgain is not None and dgain.get_device() != gpu) or (gain is not None and gain.get_device() != gpu) or
+                (dr is not None and dr.get_device() != gpu)):
+            _elsewhere(gpu, dx, dgain, dy, r, rstd, gain, dr)
+        st = (_lib or lib()).k3moe_norm_backward(
+            *self._rows(dx, T, dt), _flat(dgain, self._f32, self.n), 1 if accumulate else 0, *self._rows(dy, T, dt),
+            *self._rows(dr, T, dt), *self._rows(r, T, dt), _flat(rstd, self._f32, T), _flat(gain, self._f32, self.n),
+            _dtype(dy), T, self.n, *self._ws, _stream(stream))
+        if st:
+            check(st, "k3moe_norm_backward")
+
+
+class ExpertGroups:
+    """k3moe_groups: the slots of a routed batch of up to max_tokens tokens grouped by
+    expert.  plan(ids) fills the device tensors offsets [E + 1], order and pos
+    [tokens * top_k]; the grouped calls after it on the same stream use that plan.
+    Owns them and the workspace, so one object serves one stream at a time."""
+
+    def __init__(self, E, top_k, max_tokens, device="cuda"):
+        import torch
+        nb = lib().k3moe_groups_workspace(E, max_tokens * top_k) if 1 <= top_k <= 32 else 0
+        if nb == 0:
+            raise K3Error(K3MOE_EINVAL, "ExpertGroups(%d, %d, %d)" % (E, top_k, max_tokens))
+        self.E, self.k, self.max_tokens = E, top_k, max_tokens
+        self.offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
+        self._order = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
+        self._pos = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
+        self.workspace = torch.empty(nb, dtype=torch.uint8, device=device)
+        self._ws = self.workspace.data_ptr(), nb
+        self._i32 = torch.int32
+        self.gpu = _gpu(self.offsets)
+        self.struct = GroupsStruct(self.offsets.data_ptr(), self._order.data_ptr(), self._pos.data_ptr(), E, top_k, 0)
+        self.ref = ctypes.byref(self.struct)
+        self.tokens = self.slots = 0
+
+    @property
+    def order(self):
+        return self._order[:self.slots]
+
+    @property
+    def pos(self):
+        return self._pos[:self.slots]
+
+    def plan(self, ids, stream=None):
+        """Groups ids int32 [tokens][top_k]; an id outside 0 .. E - 1 drops its slot."""
+        T = ids.shape[0]
+        if ids.get_device() != self.gpu:
+            _elsewhere(self.gpu, ids)
+        if not 1 <= T <= self.max_tokens:
+            raise ValueError("expected 1 to %d tokens, got %d" % (self.max_tokens, T))
+        p = _flat(ids, self._i32, T, self.k)
+        self.struct.tokens = T
+        st = (_lib or lib()).k3moe_groups_plan(self.ref, p, *self._ws, _stream(stream))
+        if st:
+            self.struct.tokens = self.tokens
+            check(st, "k3moe_groups_plan")
+        self.tokens, self.slots = T, T * self.k
+
+
+class MxExperts:
+    """The matrices [rows][in_] of E experts for the grouped product
+    (k3moe_mx_experts); in_ a multiple of 128.  operand(e) is expert e's MxOperand, to
+    be filled by mx_quantize_operand; from_matrices takes stored planes."""
+
+    def __init__(self, E, rows, in_, device="cuda", codes=None):
+        import torch
+        nc, na = lib().k3moe_mx_operand_codes_bytes(rows, in_), lib().k3moe_mx_operand_atoms_bytes(rows, in_)
+        if nc < 0 or na < 0 or not 1 <= E <= 1024 or in_ % 128:
+            raise K3Error(K3MOE_EINVAL, "MxExperts(%d, %d, %d)" % (E, rows, in_))
+        self.E, self.rows, self.in_ = E, rows, in_
+        self.codes = torch.empty(E, rows, in_ // 2, dtype=torch.uint8, device=device) if codes is None else codes
+        self.atoms = torch.empty(E, na, dtype=torch.uint8, device=self.codes.device)
+        self.gpu = _gpu(self.codes)
+        # one expert has no next: any stride that its plane fits in
+        stride = self.codes.stride(0) if E > 1 else -(-nc // 32) * 32
+        self.struct = MxExpertsStruct(self.codes.data_ptr(), self.atoms.data_ptr(), stride, na, E, rows, in_)
+        self.ref = ctypes.byref(self.struct)
+
+    def operand(self, e):
+        """Expert e's matrix as an MxOperand that shares its buffers."""
+        op = MxOperand.__new__(MxOperand)
+        op.rows, op.in_, op.codes, op.atoms, op.gpu = self.rows, self.in_, self.codes[e].view(-1), self.atoms[e], self.gpu
+        op.struct = MxOperandStruct(op.codes.data_ptr(), op.atoms.data_ptr(), self.rows, self.in_)
+        op.ref = ctypes.byref(op.struct)
+        return op
+
+    @classmethod
+    def from_matrices(cls, packed, scales, stream=None):
+        """Of stored matrices: packed [E][rows][in_/2] and scales [E][rows][in_/32],
+        uint8, each expert's plane contiguous (the planes of equally spaced blobs are
+        such tensors).  Shares `packed`."""
+        import torch
+        E, rows, half = packed.shape
+        if (packed.dtype is not torch.uint8 or scales.dtype is not torch.uint8 or scales.shape != (E, rows, half // 16) or
+                not packed[0].is_contiguous() or not scales[0].is_contiguous()):
+            raise ValueError("expected byte planes [E][rows][in/2] and [E][rows][in/32], got %s and %s" % (
+                tuple(packed.shape), tuple(scales.shape)))
+        if _gpu(packed) is None or scales.get_device() != packed.get_device():
+            _elsewhere(_gpu(packed), packed, scales)
+        W = cls(E, rows, 2 * half, codes=packed)
+        if scales.data_ptr() % 16 or (E > 1 and scales.stride(0) % 16):  # the library reads aligned planes
+            n, handle = rows * half // 16, _stream(stream)
+            with torch.cuda.device(packed.device), torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+                aligned = torch.empty(E, -(-n // 16) * 16, dtype=torch.uint8, device=packed.device)
+                aligned[:, :n].copy_(scales.reshape(E, n))
+            scales = W._planes = aligned
+        for e in range(E):
+            m = Mat(packed[e].data_ptr(), scales[e].data_ptr(), rows, 2 * half)
+            check(lib().k3moe_mx_operand_from_matrix(W.operand(e).ref, ctypes.byref(m), _stream(stream)),
+                  "k3moe_mx_operand_from_matrix")
+        return W
+
+
+def grouped_matmul(C, A, W, groups, gather=False, accumulate=False, stream=None):
+    """C [slots][W.rows] (fp32 or bf16), rows in group order, = the Mx8Rows A (a row
+    per token with gather, else rows in group order) times each expert's matrix of the
+    MxExperts W, or += (fp32)."""
+    gpu = groups.gpu
+    if C.get_device() != gpu or A.gpu != gpu or W.gpu != gpu:
+        _elsewhere(gpu, C, A.codes, W.codes)
+    st = (_lib or lib()).k3moe_grouped_matmul(C.data_ptr(), _dtype(C), _ld(C, groups.slots, W.rows), A.ref, W.ref,
+                                              groups.ref, 1 if gather else 0, 1 if accumulate else 0, _stream(stream))
+    if st:
+        check(st, "k3moe_grouped_matmul")
+
+
+def grouped_wgrad(dW, dY, X, groups, gather=False, accumulate=False, stream=None):
+    """dW [E][N][K] (fp32 or bf16) = dY_e^T X_e of every expert's group, or += (fp32):
+    dY bf16 [slots][N] in group order, X bf16 [tokens][K] with gather, else [slots][K]
+    in group order."""
+    gpu = groups.gpu
+    if dW.get_device() != gpu or dY.get_device() != gpu or X.get_device() != gpu:
+        _elsewhere(gpu, dW, dY, X)
+    E, N, K = dW.shape
+    if E != groups.E or not dW.is_contiguous():
+        raise ValueError("expected a contiguous [%d][N][K] gradient, got %s" % (groups.E, tuple(dW.shape)))
+    if _dtype(dY, X) != K3MOE_BF16:
+        raise TypeError("bf16 rows expected, got %s" % dY.dtype)
+    xrows = X.shape[0]
+    st = (_lib or lib()).k3moe_grouped_wgrad(dW.data_ptr(), _dtype(dW), dY.data_ptr(), _ld(dY, groups.slots, N),
+                                             X.data_ptr(), _ld(X, xrows, K), xrows, N, K, groups.ref, 1 if gather else 0,
+                                             1 if accumulate else 0, _stream(stream))
+    if st:
+        check(st, "k3moe_grouped_wgrad")
+
+
+def combine(out, y, groups, w=None, accumulate=False, stream=None):
+    """out [tokens][n] (+)= the sum of each token's rows of y [slots][n] (group order),
+    weighted by w fp32 [tokens][top_k] (ones without)."""
+    import torch
+    gpu = groups.gpu
+    if out.get_device() != gpu or y.get_device() != gpu or (w is not None and w.get_device() != gpu):
+        _elsewhere(gpu, out, y, w)
+    n = out.shape[1]
+    st = (_lib or lib()).k3moe_combine(out.data_ptr(), _ld(out, groups.tokens, n), y.data_ptr(), _ld(y, groups.slots, n),
+                                       _dtype(out, y), n, groups.ref, _flat(w, torch.float32, groups.tokens, groups.k),
+                                       1 if accumulate else 0, _stream(stream))
+    if st:
+        check(st, "k3moe_combine")
+
+
+def combine_backward(dy, dw, dout, y, groups, w=None, stream=None):
+    """dy [slots][n] (group order) and dw fp32 [tokens][top_k] (or None; y is then not
+    needed) from dout [tokens][n]."""
+    import torch
+    gpu = groups.gpu
+    if (dy.get_device() != gpu or dout.get_device() != gpu or (dw is not None and dw.get_device() != gpu) or
+            (y is not None and y.get_device() != gpu) or (w is not None and w.get_device() != gpu)):
+        _elsewhere(gpu, dy, dout, dw, y, w)
+    n, T, k, f32 = dout.shape[1], groups.tokens, groups.k, torch.float32
+    st = (_lib or lib()).k3moe_combine_backward(
+        dy.data_ptr(), _ld(dy, groups.slots, n), _flat(dw, f32, T, k), dout.data_ptr(), _ld(dout, T, n),
+        None if y is None else y.data_ptr(), 0 if y is None else _ld(y, groups.slots, n),
+        _dtype(dout, dy) if y is None else _dtype(dout, dy, y), n, groups.ref, _flat(w, f32, T, k), _stream(stream))
+    if st:
+        check(st, "k3moe_combine_backward")
 
 
 class BalanceLoss:
