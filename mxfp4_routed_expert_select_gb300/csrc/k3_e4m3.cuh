@@ -80,6 +80,13 @@ K3_DEV void store8(void *base, long ld, int t, int c, int f, const float (&v)[8]
     }
 }
 
+// The scale byte of a block by its largest magnitude (finite), and 1 / scale.
+K3_DEV float scale_of_block(uint32_t mb, uint32_t &e)
+{
+    // max = 1.m * 2^(E-127): 2^(E-8-127) holds it up to 1.75 * 2^8 = 448
+    e = (uint32_t)max((int)(mb >> 23) - 8 + ((mb & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
+    return __uint_as_float((254u - e) << 23);
+}
 // The scale byte of the block whose eight values this lane and the three next
 // to it hold, and the lane's codes.
 template <typename T>
@@ -92,9 +99,7 @@ K3_DEV uint2 e4m3x8(const Raw<T> &v, uint32_t &e)
         e = 255u;
         return make_uint2(0u, 0u);
     }
-    // max = 1.m * 2^(E-127): 2^(E-8-127) holds it up to 1.75 * 2^8 = 448
-    e = (uint32_t)max((int)(mb >> 23) - 8 + ((mb & 0x7fffffu) > 0x600000u ? 1 : 0), 0);
-    const float inv = __uint_as_float((254u - e) << 23);
+    const float inv = scale_of_block(mb, e);
     float a[8];
 #pragma unroll
     for (int i = 0; i < 8; i += 2) {
@@ -147,6 +152,22 @@ K3_DEV void store_mx8(uint8_t *codes, uint8_t *scales, int in, int t, int c, con
     w |= __shfl_xor_sync(0xffffffffu, w, 4);
     w |= __shfl_xor_sync(0xffffffffu, w, 8);
     if ((lane & 15) == 0 && c / 32 < ss) *(uint32_t *)(scales + (long)t * ss + c / 32) = w;
+}
+
+// One value a lane, a whole warp on one block of 32: lane 0's column is a multiple of 32.
+K3_DEV void store_mx8_block(uint8_t *codes, uint8_t *scales, int in, int t, int c, float v)
+{
+    const uint32_t mb = __reduce_max_sync(0xffffffffu, __float_as_uint(v) & 0x7fffffffu);
+    const int fp = op_in_padded(in), ss = mx8_scale_stride(in);
+    uint32_t e = 255u;
+    uint16_t q = 0;
+    if (mb < 0x7f800000u) {
+        float a = scale_of_block(mb, e) * v;
+        if (e == 247u) a = fminf(fmaxf(a, -240.f), 240.f);
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(0.f), "f"(a));
+    }
+    if (c < fp) codes[(long)t * fp + c] = (uint8_t)q;
+    if ((c & 31) == 0 && c / 32 < ss) scales[(long)t * ss + c / 32] = (uint8_t)e;
 }
 
 }  // namespace k3

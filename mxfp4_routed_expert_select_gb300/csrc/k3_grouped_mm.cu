@@ -38,6 +38,7 @@ constexpr int GM_M = 128;  // weight rows of a tile
 constexpr int GM_THREADS = 256;
 constexpr int GM_W_W = 0, GM_W_MMA = 1, GM_W_X = 2, GM_W_SF = 3, GM_W_EPI = 4;
 constexpr int GM_MAX_E = 1024;
+constexpr int GM_AHEAD = 8;  // steps of row scales in flight
 
 struct GmArgs {
     const uint8_t *atoms;      // scale atoms of the weights, atoms_stride bytes from expert to expert
@@ -97,8 +98,9 @@ K3_DEV void gm_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
 // Four rows of 128 bytes by index; a row outside the matrix reads as zero.
 K3_DEV void gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&r)[4], uint32_t bar)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
                  "l"((uint64_t)map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
                  : "memory");
 }
@@ -245,32 +247,20 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     gm_table<NT>(tab, sums, a);
     const int n_tiles = tab[a.E] * a.tiles_n, first = (int)blockIdx.x, step = (int)gridDim.x;
 
-    if (warp == GM_W_W || warp == GM_W_X || warp == GM_W_SF) {
-        // ------------------------------------------------------- producers
+    if (warp == GM_W_W || warp == GM_W_X) {
+        // ----------------------------------- producers of the code tiles
         uint32_t it = 0, phase = 1;  // before its first completion an EMPTY barrier's odd phase counts as passed
         int s = 0;
         bool ok = true;
         for (int u = first; u < n_tiles && ok; u += step) {
             const GmTile t = gm_tile<NT>(tab, a, u);
             const uint8_t *atoms = a.atoms + (long)t.e * a.atoms_stride + (long)(t.n0 / 128) * a.nka * 512;
-            // rows of the tile: the gathering warp's lane has four in a row, the scale
-            // warp's every 32nd from its own on.  Columns past the group repeat its last
-            // row (they are not stored).
+            // the gathering warp's lane has four rows of the tile; columns past the group
+            // repeat its last row (they are not stored)
             int src[4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int r = warp == GM_W_X ? 4 * lane + i : lane + 32 * i;
-                src[i] = warp == GM_W_W ? 0 : gm_source(a, t.row + min(r, t.rows - 1));
-            }
-            const uint8_t *sp[4];
-#pragma unroll
-            for (int i = 0; i < 4; i++) sp[i] = a.scales + (long)src[i] * a.sstride;
+            for (int i = 0; i < 4; i++) src[i] = warp == GM_W_W ? 0 : gm_source(a, t.row + min(4 * lane + i, t.rows - 1));
             for (int ks = 0; ks < a.nks; ks++, it++) {
-                uint32_t w[4] = {};
-                if (warp == GM_W_SF)
-#pragma unroll
-                    for (int i = 0; i < (NT + 31) / 32; i++)
-                        w[i] = *(const uint32_t *)(sp[i] + 4 * ks);
                 if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
@@ -279,25 +269,69 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
                 if (warp == GM_W_W) {
                     expect_elected(full, C::TX_W);
                     gm_load_w(st, &wmap, ks * 128, t.n0, t.e, st + C::OFF_WA, atoms + (long)ks * 512, full);
-                } else if (warp == GM_W_X) {
-                    expect_elected(full, C::TX_X);
-                    __syncwarp();
-                    if (4 * lane < NT) gather4(st + C::OFF_X + (uint32_t)lane * 512, &xmap, ks * 128, src, full);
-                    __syncwarp();
                 } else {
-                    *(uint4 *)(sm + s * C::STAGE + C::OFF_XA + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(full);
+                    expect_elected(full, C::TX_X);
+#pragma unroll
+                    for (int q = 0; q < NT / 4; q++) {
+                        int r[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) r[i] = __shfl_sync(0xffffffffu, src[i], q);
+                        gather4(st + C::OFF_X + (uint32_t)q * 512, &xmap, ks * 128, r, full);
+                    }
                 }
                 if (++s == NS) s = 0, phase ^= 1u;
             }
         }
         // drain: every copy issued here has landed before the CTA exits (the last
         // NS of them; earlier ones were waited for before their reuse)
-        if (warp != GM_W_SF)
-            for (uint32_t i = it > (uint32_t)NS ? it - NS : 0; i < it; i++)
-                mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
+        for (uint32_t i = it > (uint32_t)NS ? it - NS : 0; i < it; i++)
+            mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
+        __syncwarp();
+    } else if (warp == GM_W_SF) {
+        // ------------------------------------- producer of the rows' scales
+        // A lane has the words of every 32nd row from its own on: a 16-byte store puts
+        // them where tensor memory takes them from.  GM_AHEAD steps' words are loaded
+        // before they are needed.
+        constexpr int J = (NT + 31) / 32;
+        uint32_t phase = 1;
+        int s = 0;
+        bool ok = true;
+        for (int u = first; u < n_tiles && ok; u += step) {
+            const GmTile t = gm_tile<NT>(tab, a, u);
+            const uint8_t *sp[J];
+#pragma unroll
+            for (int j = 0; j < J; j++)
+                sp[j] = a.scales + (long)gm_source(a, t.row + min(lane + 32 * j, t.rows - 1)) * a.sstride;
+            uint32_t w[GM_AHEAD][J], wn[GM_AHEAD][J];
+            auto load = [&](uint32_t (&d)[GM_AHEAD][J], int k0) {
+#pragma unroll
+                for (int i = 0; i < GM_AHEAD; i++)
+#pragma unroll
+                    for (int j = 0; j < J; j++) d[i][j] = k0 + i < a.nks ? *(const uint32_t *)(sp[j] + 4 * (k0 + i)) : 0u;
+            };
+            load(w, 0);
+            for (int k0 = 0; k0 < a.nks && ok; k0 += GM_AHEAD) {
+                load(wn, k0 + GM_AHEAD);
+#pragma unroll
+                for (int i = 0; i < GM_AHEAD; i++) {
+                    if (k0 + i >= a.nks || !ok) break;
+                    if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    *(uint4 *)(sm + s * C::STAGE + C::OFF_XA + lane * 16) =
+                        make_uint4(w[i][0], w[i][J > 1 ? 1 : 0], w[i][J > 2 ? 2 : 0], w[i][J > 3 ? 3 : 0]);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_FULL + s));
+                    if (++s == NS) s = 0, phase ^= 1u;
+                }
+#pragma unroll
+                for (int i = 0; i < GM_AHEAD; i++)
+#pragma unroll
+                    for (int j = 0; j < J; j++) w[i][j] = wn[i][j];
+            }
+        }
         __syncwarp();
     } else if (warp == GM_W_MMA) {
         // -------------------------------------------------------------- MMA

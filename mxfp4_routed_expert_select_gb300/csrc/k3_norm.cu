@@ -35,15 +35,6 @@ struct NormArgs {
     float eps, inv_n;
 };
 
-// Eight values as the bits of fp32.
-template <typename T>
-K3_DEV Raw<uint32_t> widened(const float (&v)[8])
-{
-    Raw<uint32_t> r;
-#pragma unroll
-    for (int i = 0; i < 8; i++) r.w[i] = __float_as_uint(v[i]);
-    return r;
-}
 // v rounded to the rows' type.
 template <typename T>
 K3_DEV float rounded(float v)
@@ -89,7 +80,7 @@ struct Team {
 // 1 / sqrt(mean v^2 + eps) where the sum of squares left fp32's range or its normal
 // numbers while its root need not: the values scaled by a power of two.
 template <int C>
-__device__ __noinline__ float far_rstd(Team &team, const float (&v)[C][8], float ss, float inv_n, float eps)
+K3_DEV float far_rstd(Team &team, const float (&v)[C][8], float ss, float inv_n, float eps)
 {
     float m = 0.f;
 #pragma unroll
@@ -118,39 +109,107 @@ K3_DEV Team make_team(int warps, float (*slots)[64], int &first, int &step)
     step = (int)gridDim.x * teams;
     return Team{warps, w - id * warps, (int)threadIdx.x & 31, 1 + id, slots[id], 0};
 }
-template <int C>
-K3_DEV void load_gain(float (&gn)[C][8], const float *gain, int col0, int stride, int n)
-{
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const int col = col0 + c * stride + i;
-            gn[c][i] = gain && col < n ? gain[col] : 1.f;
-        }
-}
+// A thread's columns.  WIDE (every row 16-byte aligned, n a multiple of 8): C chunks of
+// eight, 16-byte accesses.  Otherwise 8 C single values, 32 neighbours to a warp, so
+// that rows of any alignment are read and written whole sectors at a time.
+template <bool WIDE, int C>
+struct Cols {
+    int first, step, n;  // of chunk 0 or value 0; to the next chunk or value
 
-template <typename T, bool VEC, int C>
-__global__ void __launch_bounds__(NORM_THREADS) k3_norm_forward(const NormArgs a)
+    K3_DEV Cols(const Team &team, int n_) : n(n_)
+    {
+        first = WIDE ? (team.warp * 32 + team.lane) * 8 : team.warp * 32 + team.lane;
+        step = WIDE ? team.warps * 256 : team.warps * 32;
+    }
+    K3_DEV int at(int c, int i) const { return WIDE ? first + c * step + i : first + (c * 8 + i) * step; }
+    template <typename T>
+    K3_DEV Raw<T> load(const void *base, long ld, int t, int c, bool on) const
+    {
+        if constexpr (WIDE) return load8<T, true>(base, ld, t, on ? first + c * step : n, n);
+        Raw<T> r;
+        const T *p = (const T *)base + (long)t * ld;
+#pragma unroll
+        for (int i = 0; i < (int)(2 * sizeof(T)); i++) r.w[i] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (on && at(c, i) < n) {
+                if constexpr (sizeof(T) == 2)
+                    r.w[i >> 1] |= (uint32_t)p[at(c, i)] << (16 * (i & 1));
+                else
+                    r.w[i] = p[at(c, i)];
+            }
+        return r;
+    }
+    template <typename T>
+    K3_DEV void store(void *base, long ld, int t, int c, const float (&v)[8]) const
+    {
+        if constexpr (WIDE) {
+            store8<T, true>(base, ld, t, first + c * step, n, v);
+            return;
+        }
+        T *p = (T *)base + (long)t * ld;
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+            if (at(c, i) < n) {
+                if constexpr (sizeof(T) == 2)
+                    p[at(c, i)] = __bfloat16_as_ushort(__float2bfloat16_rn(v[i]));
+                else
+                    p[at(c, i)] = __float_as_uint(v[i]);
+            }
+    }
+    K3_DEV void load_gain(float (&g)[C][8], const float *gain) const
+    {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if (WIDE && gain && ((uintptr_t)gain & 15u) == 0) {
+                const int col = min(first + c * step, n - 8);
+                const float4 a = *(const float4 *)(gain + col), b = *(const float4 *)(gain + col + 4);
+                g[c][0] = a.x, g[c][1] = a.y, g[c][2] = a.z, g[c][3] = a.w;
+                g[c][4] = b.x, g[c][5] = b.y, g[c][6] = b.z, g[c][7] = b.w;
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) g[c][i] = gain && at(c, i) < n ? gain[at(c, i)] : 1.f;
+            }
+        }
+    }
+    // Row t in 8 bits; called by whole warps.
+    K3_DEV void store_8bit(uint8_t *codes, uint8_t *scales, int t, const float (&v)[C][8]) const
+    {
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+            if constexpr (WIDE) {
+                Raw<uint32_t> q;
+#pragma unroll
+                for (int i = 0; i < 8; i++) q.w[i] = first + c * step < n ? __float_as_uint(v[c][i]) : 0u;
+                store_mx8(codes, scales, n, t, first + c * step, q);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; i++) store_mx8_block(codes, scales, n, t, at(c, i), at(c, i) < n ? v[c][i] : 0.f);
+            }
+        }
+    }
+};
+
+template <typename T, bool WIDE, int C>
+__global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1) k3_norm_forward(const NormArgs a)
 {
     __shared__ float slots[8][64];
     griddep_wait();
     griddep_launch_dependents();
     int t, step;
     Team team = make_team(a.warps, slots, t, step);
-    const int tid = team.warp * 32 + team.lane, stride = a.warps * 256, col0 = tid * 8;
-    float gn[C][8];
-    load_gain(gn, a.gain, col0, stride, a.n);
+    const Cols<WIDE, C> cols(team, a.n);
     Raw<T> x[C], d[C];
     auto load = [&](int row) {
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            const int col = row < a.T ? col0 + c * stride : a.n;
-            x[c] = load8<T, VEC>(a.x, a.ldx, row, col, a.n);
-            if (a.delta) d[c] = load8<T, VEC>(a.delta, a.ldd, row, col, a.n);
+            x[c] = cols.template load<T>(a.x, a.ldx, row, c, row < a.T);
+            if (a.delta) d[c] = cols.template load<T>(a.delta, a.ldd, row, c, row < a.T);
         }
     };
     load(t);
+    float gn[C][8];
+    cols.load_gain(gn, a.gain);
     for (; t < a.T; t += step) {
         float v[C][8], ss = 0.f;
 #pragma unroll
@@ -164,33 +223,25 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_forward(const NormArgs a
         load(t + step);
         if (a.r)
 #pragma unroll
-            for (int c = 0; c < C; c++) store8<T, VEC>(a.r, a.ldr, t, col0 + c * stride, a.n, v[c]);
+            for (int c = 0; c < C; c++) cols.template store<T>(a.r, a.ldr, t, c, v[c]);
         ss = team.sum(ss);
         // the sum is exact enough unless it left the normal range, or fell below
         // where eps outweighs what it lost
         float s = rsqrtf(ss * a.inv_n + a.eps);
         if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f)) s = far_rstd<C>(team, v, ss, a.inv_n, a.eps);
-        if (a.rstd && tid == 0) a.rstd[t] = s;
+        if (a.rstd && team.warp == 0 && team.lane == 0) a.rstd[t] = s;
 #pragma unroll
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 8; i++) v[c][i] = v[c][i] * s * gn[c][i];
         if (a.y)
 #pragma unroll
-            for (int c = 0; c < C; c++) store8<T, VEC>(a.y, a.ldy, t, col0 + c * stride, a.n, v[c]);
-        if (a.codes)
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-                const int col = col0 + c * stride;
-                float q[8];
-#pragma unroll
-                for (int i = 0; i < 8; i++) q[i] = col + i < a.n ? v[c][i] : 0.f;
-                store_mx8(a.codes, a.scales, a.n, t, col, widened<T>(q));
-            }
+            for (int c = 0; c < C; c++) cols.template store<T>(a.y, a.ldy, t, c, v[c]);
+        if (a.codes) cols.store_8bit(a.codes, a.scales, t, v);
     }
 }
 
-template <typename T, bool VEC, int C>
+template <typename T, bool WIDE, int C>
 __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs a)
 {
     __shared__ float slots[8][64];
@@ -198,26 +249,26 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
     griddep_launch_dependents();
     int t, step;
     Team team = make_team(a.warps, slots, t, step);
-    const int part = t, tid = team.warp * 32 + team.lane, stride = a.warps * 256, col0 = tid * 8;
-    float gn[C][8], sum[C][8];
-    load_gain(gn, a.gain, col0, stride, a.n);
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) sum[c][i] = 0.f;
+    const int part = t;
+    const Cols<WIDE, C> cols(team, a.n);
     Raw<T> x[C], dy[C], dr[C];
     float s = 0.f;
     auto load = [&](int row) {
 #pragma unroll
         for (int c = 0; c < C; c++) {
-            const int col = row < a.T ? col0 + c * stride : a.n;
-            x[c] = load8<T, VEC>(a.x, a.ldx, row, col, a.n);
-            dy[c] = load8<T, VEC>(a.dy, a.lddy, row, col, a.n);
-            if (a.dr) dr[c] = load8<T, VEC>(a.dr, a.lddr, row, col, a.n);
+            x[c] = cols.template load<T>(a.x, a.ldx, row, c, row < a.T);
+            dy[c] = cols.template load<T>(a.dy, a.lddy, row, c, row < a.T);
+            if (a.dr) dr[c] = cols.template load<T>(a.dr, a.lddr, row, c, row < a.T);
         }
         s = row < a.T ? a.rstd[row] : 0.f;
     };
     load(t);
+    float gn[C][8], sum[C][8];
+    cols.load_gain(gn, a.gain);
+#pragma unroll
+    for (int c = 0; c < C; c++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum[c][i] = 0.f;
     for (; t < a.T; t += step) {
         float xh[C][8], g[C][8], res[C][8], dot = 0.f;
         const float sc = s;
@@ -238,7 +289,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
         for (int c = 0; c < C; c++) {
 #pragma unroll
             for (int i = 0; i < 8; i++) g[c][i] = res[c][i] + sc * (g[c][i] - xh[c][i] * dot);
-            store8<T, VEC>(a.dx, a.lddx, t, col0 + c * stride, a.n, g[c]);
+            cols.template store<T>(a.dx, a.lddx, t, c, g[c]);
         }
     }
     if (a.parts)
@@ -246,26 +297,27 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
         for (int c = 0; c < C; c++)
 #pragma unroll
             for (int i = 0; i < 8; i++)
-                if (col0 + c * stride + i < a.n) a.parts[(long)part * a.n + col0 + c * stride + i] = sum[c][i];
+                if (cols.at(c, i) < a.n) a.parts[(long)part * a.n + cols.at(c, i)] = sum[c][i];
 }
 
 // dgain[c] (+)= the sum of its column over the parts.  A block takes 32 columns, its
-// eight warps a share of the parts each.
-__global__ void __launch_bounds__(256) k3_norm_columns(float *dgain, const float *parts, int n, int n_parts, int accumulate)
+// warps a share of the parts each.
+constexpr int NC_WARPS = 32;
+__global__ void __launch_bounds__(NC_WARPS * 32) k3_norm_columns(float *dgain, const float *parts, int n, int n_parts, int accumulate)
 {
-    __shared__ float sh[8][32];
+    __shared__ float sh[NC_WARPS][32];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = (int)blockIdx.x * 32 + lane;
     float v = 0.f;
     if (col < n)
 #pragma unroll 8
-        for (int p = w; p < n_parts; p += 8) v += parts[(long)p * n + col];
+        for (int p = w; p < n_parts; p += NC_WARPS) v += parts[(long)p * n + col];
     sh[w][lane] = v;
     __syncthreads();
     if (w == 0 && col < n) {
 #pragma unroll
-        for (int i = 1; i < 8; i++) v += sh[i][lane];
+        for (int i = 1; i < NC_WARPS; i++) v += sh[i][lane];
         dgain[col] = accumulate ? dgain[col] + v : v;
     }
 }
@@ -414,7 +466,7 @@ int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, cons
     p.grid = std::min(p.grid, NORM_PARTS / p.teams);
     const int st = launch_norm(a, dtype, vec, true, p, s);
     if (st != K3MOE_OK || !dgain) return st;
-    if (launch_pdl(k3_norm_columns, dim3((unsigned)((n + 31) / 32)), dim3(256), 0, s, dgain, (const float *)ws, n,
+    if (launch_pdl(k3_norm_columns, dim3((unsigned)((n + 31) / 32)), dim3(NC_WARPS * 32), 0, s, dgain, (const float *)ws, n,
                    p.grid * p.teams, accumulate) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
