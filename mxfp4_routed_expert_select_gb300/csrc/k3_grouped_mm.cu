@@ -12,11 +12,13 @@
 // walks (expert, NT rows, 128 n) tiles; which exist follows from the group borders in
 // device memory, which each CTA turns into a table of tile numbers.
 //
-// Roles: warp 0 copies the weights (TMA, 128 of K per stage; the copy spreads 16
-// four-bit codes over 16 bytes, the form this kind of MMA reads, so HBM and L2 move
-// packed bytes) and their scale atoms, warp 2 gathers the rows' codes (TMA gather of
-// four rows by index), warp 3 their scale bytes, warp 1 issues scale copies and MMAs,
-// warps 4 and up read the accumulators while the next tile's products run.
+// Roles: warp 0 issues scale copies and MMAs, warps 4 to 7 read the accumulators while
+// the next tile's products run, and each further warp fills one stage of 128 of K: the
+// weights and their scale atom by TMA (the copy spreads 16 four-bit codes over 16 bytes,
+// the form this kind of MMA reads, so HBM and L2 move packed bytes), the rows' codes by
+// TMA where they lie in group order, else row by row with asynchronous copies into the
+// same swizzled form, and the rows' scale bytes.  (Gathered by TMA, four rows a copy of
+// 72 clocks, 65536 rows x 1536 x 7168 took 2.94 ms; the same rows as tiles 0.76.)
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -35,16 +37,14 @@ namespace k3 {
 namespace {
 
 constexpr int GM_M = 128;  // weight rows of a tile
-constexpr int GM_THREADS = 256;
-constexpr int GM_W_W = 0, GM_W_MMA = 1, GM_W_X = 2, GM_W_SF = 3, GM_W_EPI = 4;
+constexpr int GM_W_MMA = 0, GM_W_EPI = 4, GM_W_FILL = 8;
 constexpr int GM_MAX_E = 1024;
-constexpr int GM_AHEAD = 8;  // steps of row scales in flight
 
 struct GmArgs {
     const uint8_t *atoms;      // scale atoms of the weights, atoms_stride bytes from expert to expert
     long atoms_stride;
-    const uint8_t *scales;     // scale bytes of the rows
-    int sstride;
+    const uint8_t *codes, *scales;  // of the rows
+    int cstride, sstride;
     const int32_t *offsets, *order;
     int E, top_k, slots, gather, xrows;  // xrows: rows of the 8-bit matrix
     int N, nks, nka, tiles_n;  // nks: steps of 128 along K; nka: atoms per row tile
@@ -95,75 +95,75 @@ K3_DEV void gm_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
                  "l"((uint64_t)map), "r"(adst), "l"(atom), "r"(x), "r"(row), "r"(e), "r"(bar)
                  : "memory");
 }
-// Four rows of 128 bytes by index; a row outside the matrix reads as zero.
-K3_DEV void gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&r)[4], uint32_t bar)
+// 16 bytes from global to shared memory, asynchronously.
+K3_DEV void copy16(uint32_t dst, const void *src)
 {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
-                 "l"((uint64_t)map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-                 : "memory");
-}
-K3_DEV void expect_elected(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// The tiles of the batch: tab[e] row tiles lie before expert e's.
+// The tiles of the batch, made by every CTA in shared memory: before[e] row tiles lie
+// before expert e's, off[e] is its first place.
+struct GmTable {
+    int before[GM_MAX_E + 1], off[GM_MAX_E + 1], sums[32];
+};
 struct GmTile {
     int e, row, rows, n0;  // first row of C, rows of the group from there on (> 0), first weight row
 };
-template <int NT>
-K3_DEV void gm_table(int *tab, int *sums, const GmArgs &a)
+template <int NT, int THREADS>
+K3_DEV void gm_table(GmTable &tab, const GmArgs &a)
 {
-    // four experts a thread
-    int v[4], mine = 0;
+    constexpr int PER = (GM_MAX_E + 256 - 1) / 256;  // experts of each of the first 256 threads
+    static_assert(THREADS >= 256, "threads of the table");
+    int v[PER], mine = 0;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, e0 = PER * (int)threadIdx.x;
+    if (threadIdx.x < 256) {
+        int lo = e0 <= a.E ? min(max(a.offsets[e0], 0), a.slots) : 0;
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int e = 4 * (int)threadIdx.x + i;
-        const int lo = e < a.E ? min(max(a.offsets[e], 0), a.slots) : 0, hi = e < a.E ? min(a.offsets[e + 1], a.slots) : 0;
-        v[i] = hi > lo ? (hi - lo + NT - 1) / NT : 0;
-        mine += v[i];
+        for (int i = 0; i < PER; i++) {
+            const int e = e0 + i, hi = e < a.E ? min(max(a.offsets[e + 1], lo), a.slots) : lo;
+            if (e <= a.E) tab.off[e] = lo;
+            v[i] = (hi - lo + NT - 1) / NT;
+            mine += v[i];
+            lo = hi;
+        }
+        if (e0 + PER == a.E) tab.off[a.E] = lo;
     }
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     int x = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, x, o);
         if (lane >= o) x += y;
     }
-    if (lane == 31) sums[w] = x;
+    if (lane == 31) tab.sums[w] = x;
     __syncthreads();
-    int at = x - mine;
-    for (int i = 0; i < w; i++) at += sums[i];
+    if (threadIdx.x < 256) {
+        int at = x - mine;
+        for (int i = 0; i < w; i++) at += tab.sums[i];
 #pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int e = 4 * (int)threadIdx.x + i;
-        if (e <= a.E) tab[e] = at;
-        at += v[i];
+        for (int i = 0; i < PER; i++) {
+            if (e0 + i <= a.E) tab.before[e0 + i] = at;
+            at += v[i];
+        }
+        if (e0 + PER == a.E) tab.before[a.E] = at;
     }
-    if (threadIdx.x == GM_THREADS - 1 && a.E == GM_MAX_E) tab[a.E] = at;
     __syncthreads();
 }
 template <int NT>
-K3_DEV GmTile gm_tile(const int *tab, const GmArgs &a, int u)
+K3_DEV GmTile gm_tile(const GmTable &tab, const GmArgs &a, int u)
 {
     const int r = u / a.tiles_n;
-    int lo = 0, hi = a.E;  // tab[lo] <= r < tab[hi]
+    int lo = 0, hi = a.E;  // before[lo] <= r < before[hi]
     while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
-        if (tab[m] <= r)
+        if (tab.before[m] <= r)
             lo = m;
         else
             hi = m;
     }
     GmTile t;
     t.e = lo;
-    t.row = max(a.offsets[lo], 0) + (r - tab[lo]) * NT;
-    t.rows = min(a.offsets[lo + 1], a.slots) - t.row;
+    t.row = tab.off[lo] + (r - tab.before[lo]) * NT;
+    t.rows = tab.off[lo + 1] - t.row;
     t.n0 = (u - r * a.tiles_n) * GM_M;
     return t;
 }
@@ -179,14 +179,16 @@ struct GmCfg {
     static constexpr int W_BYTES = GM_M * 128, X_BYTES = NT * 128;
     static constexpr int OFF_X = W_BYTES, OFF_WA = OFF_X + X_BYTES, OFF_XA = OFF_WA + 512;
     static constexpr int STAGE = (OFF_XA + 512 + 1023) / 1024 * 1024;
-    static constexpr int NS = (227 * 1024 - 8192) / STAGE < 10 ? (227 * 1024 - 8192) / STAGE : 10;
+    static constexpr int ROOM = 227 * 1024 - 1024 - 512 - (int)sizeof(GmTable);
+    static constexpr int NS = ROOM / STAGE < 10 ? ROOM / STAGE : 10;
+    static constexpr int THREADS = 32 * (GM_W_FILL + NS);  // a warp fills one stage
     static constexpr int TX_W = W_BYTES / 2 + 512, TX_X = X_BYTES;  // bytes as they lie in memory: the weights packed
     static constexpr int SF0 = 2 * NT, SF = 8;
     static constexpr int COLS_USED = SF0 + SF * NS;
     static constexpr int TMEM_COLS = COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
     static constexpr int BARS = 2 * NS + 2 * 2 + 1;
     static constexpr int OFF_TAB = NS * STAGE + 256;
-    static constexpr int SMEM = 1024 + OFF_TAB + (GM_MAX_E + 1 + 8) * 4;
+    static constexpr int SMEM = 1024 + OFF_TAB + (int)sizeof(GmTable);
     static_assert(SMEM <= 232448, "shared memory");
     static_assert(COLS_USED <= 512, "TMEM layout");
     static_assert(BARS * 8 + 8 <= 256, "barriers");
@@ -202,7 +204,7 @@ K3_DEV void gm_put(CT *p, float v, int accumulate)
 }
 
 template <int NT, typename CT>
-__global__ void __launch_bounds__(GM_THREADS, 1)
+__global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
     k3_grouped_matmul(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap, const GmArgs a)
 {
     using C = GmCfg<NT>;
@@ -214,7 +216,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2;
     uint32_t *tmem_slot = (uint32_t *)(bars + C::BARS);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
-    int *tab = (int *)(sm + C::OFF_TAB), *sums = tab + GM_MAX_E + 1;
+    GmTable &tab = *(GmTable *)(sm + C::OFF_TAB);
     auto bar = [&](int i) { return smem_addr(bars + i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -222,7 +224,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&wmap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&xmap) : "memory");
         for (int i = 0; i < NS; i++) {
-            mbar_init(bar(B_FULL + i), 3);  // weights, rows, the rows' scales
+            mbar_init(bar(B_FULL + i), 2);  // the copies' bytes announced; the rows' part done
             mbar_init(bar(B_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -244,94 +246,69 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
     griddep_wait();
-    gm_table<NT>(tab, sums, a);
-    const int n_tiles = tab[a.E] * a.tiles_n, first = (int)blockIdx.x, step = (int)gridDim.x;
+    gm_table<NT, C::THREADS>(tab, a);
+    const int n_tiles = tab.before[a.E] * a.tiles_n, first = (int)blockIdx.x, step = (int)gridDim.x;
 
-    if (warp == GM_W_W || warp == GM_W_X) {
-        // ----------------------------------- producers of the code tiles
-        uint32_t it = 0, phase = 1;  // before its first completion an EMPTY barrier's odd phase counts as passed
-        int s = 0;
-        bool ok = true;
-        for (int u = first; u < n_tiles && ok; u += step) {
-            const GmTile t = gm_tile<NT>(tab, a, u);
-            const uint8_t *atoms = a.atoms + (long)t.e * a.atoms_stride + (long)(t.n0 / 128) * a.nka * 512;
-            // the gathering warp's lane has four rows of the tile; columns past the group
-            // repeat its last row (they are not stored)
-            int src[4];
+    if (warp >= GM_W_FILL) {
+        // -------------------------------------------------- a stage's filler
+        // Every NS-th step of this CTA's tiles.  Lanes 8 q .. 8 q + 7 copy the 16-byte
+        // chunks of rows q, q + 4, ..; a lane has the scale words of rows lane, lane +
+        // 32, ... of the tile, loaded a turn ahead.  Columns past the group keep what
+        // the stage held (they are not stored).
+        constexpr int J = (NT + 31) / 32, R = NT / 4;
+        const int s = warp - GM_W_FILL;
+        const uint32_t st = sbase + (uint32_t)(s * C::STAGE), full = bar(B_FULL + s);
+        uint32_t turn = 0;
+        int u = first, ks = s, tile = -1;
+        GmTile t = {};
+        const uint8_t *atoms = nullptr, *sp[J];
+        int src[R];
+        uint32_t w[J];
+        for (;; ks += NS, turn++) {
+            while (ks >= a.nks) ks -= a.nks, u += step;
+            if (u >= n_tiles) break;
+            if (u != tile) {
+                tile = u;
+                t = gm_tile<NT>(tab, a, u);
+                atoms = a.atoms + (long)t.e * a.atoms_stride + (long)(t.n0 / 128) * a.nka * 512;
 #pragma unroll
-            for (int i = 0; i < 4; i++) src[i] = warp == GM_W_W ? 0 : gm_source(a, t.row + min(4 * lane + i, t.rows - 1));
-            for (int ks = 0; ks < a.nks; ks++, it++) {
-                if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t st = sbase + (uint32_t)(s * C::STAGE), full = bar(B_FULL + s);
-                if (warp == GM_W_W) {
-                    expect_elected(full, C::TX_W);
-                    gm_load_w(st, &wmap, ks * 128, t.n0, t.e, st + C::OFF_WA, atoms + (long)ks * 512, full);
-                } else {
-                    expect_elected(full, C::TX_X);
+                for (int j = 0; j < J; j++)
+                    sp[j] = lane + 32 * j < t.rows ? a.scales + (long)gm_source(a, t.row + lane + 32 * j) * a.sstride : nullptr;
+                if (a.gather)
 #pragma unroll
-                    for (int q = 0; q < NT / 4; q++) {
-                        int r[4];
-#pragma unroll
-                        for (int i = 0; i < 4; i++) r[i] = __shfl_sync(0xffffffffu, src[i], q);
-                        gather4(st + C::OFF_X + (uint32_t)q * 512, &xmap, ks * 128, r, full);
+                    for (int i = 0; i < R; i++) {
+                        const int r = 4 * i + (lane >> 3);
+                        src[i] = r < t.rows ? gm_source(a, t.row + r) : -1;
                     }
-                }
-                if (++s == NS) s = 0, phase ^= 1u;
             }
-        }
-        // drain: every copy issued here has landed before the CTA exits (the last
-        // NS of them; earlier ones were waited for before their reuse)
-        for (uint32_t i = it > (uint32_t)NS ? it - NS : 0; i < it; i++)
-            mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
-        __syncwarp();
-    } else if (warp == GM_W_SF) {
-        // ------------------------------------- producer of the rows' scales
-        // A lane has the words of every 32nd row from its own on: a 16-byte store puts
-        // them where tensor memory takes them from.  GM_AHEAD steps' words are loaded
-        // before they are needed.
-        constexpr int J = (NT + 31) / 32;
-        uint32_t phase = 1;
-        int s = 0;
-        bool ok = true;
-        for (int u = first; u < n_tiles && ok; u += step) {
-            const GmTile t = gm_tile<NT>(tab, a, u);
-            const uint8_t *sp[J];
 #pragma unroll
-            for (int j = 0; j < J; j++)
-                sp[j] = a.scales + (long)gm_source(a, t.row + min(lane + 32 * j, t.rows - 1)) * a.sstride;
-            uint32_t w[GM_AHEAD][J], wn[GM_AHEAD][J];
-            auto load = [&](uint32_t (&d)[GM_AHEAD][J], int k0) {
+            for (int j = 0; j < J; j++) w[j] = sp[j] ? *(const uint32_t *)(sp[j] + 4 * ks) : 0u;
+            // before its first completion an EMPTY barrier's odd phase counts as passed
+            if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
+            if (lane == 0) mbar_arrive_expect_tx(full, C::TX_W + (a.gather ? 0 : C::TX_X));
+            __syncwarp();
+            gm_load_w(st, &wmap, ks * 128, t.n0, t.e, st + C::OFF_WA, atoms + (long)ks * 512, full);
+            if (a.gather) {
+                const uint8_t *base = a.codes + (long)ks * 128 + (lane & 7) * 16;
 #pragma unroll
-                for (int i = 0; i < GM_AHEAD; i++)
-#pragma unroll
-                    for (int j = 0; j < J; j++) d[i][j] = k0 + i < a.nks ? *(const uint32_t *)(sp[j] + 4 * (k0 + i)) : 0u;
-            };
-            load(w, 0);
-            for (int k0 = 0; k0 < a.nks && ok; k0 += GM_AHEAD) {
-                load(wn, k0 + GM_AHEAD);
-#pragma unroll
-                for (int i = 0; i < GM_AHEAD; i++) {
-                    if (k0 + i >= a.nks || !ok) break;
-                    if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
-                        ok = false;
-                        break;
-                    }
-                    *(uint4 *)(sm + s * C::STAGE + C::OFF_XA + lane * 16) =
-                        make_uint4(w[i][0], w[i][J > 1 ? 1 : 0], w[i][J > 2 ? 2 : 0], w[i][J > 3 ? 3 : 0]);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(B_FULL + s));
-                    if (++s == NS) s = 0, phase ^= 1u;
+                for (int i = 0; i < R; i++) {
+                    const int r = 4 * i + (lane >> 3);
+                    if (src[i] >= 0)
+                        copy16(st + C::OFF_X + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)), base + (long)src[i] * a.cstride);
                 }
-#pragma unroll
-                for (int i = 0; i < GM_AHEAD; i++)
-#pragma unroll
-                    for (int j = 0; j < J; j++) w[i][j] = wn[i][j];
+            } else if (lane == 0) {
+                tma_load_2d(st + C::OFF_X, &xmap, ks * 128, t.row, full);
             }
+#pragma unroll
+            for (int j = 0; j < J; j++) *(uint32_t *)(sm + s * C::STAGE + C::OFF_XA + lane * 16 + j * 4) = w[j];
+            if (a.gather) asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(full);
         }
+        // drain: every copy issued here has landed before the CTA exits (the last turn's;
+        // earlier ones were waited for before their stage's reuse)
+        if (turn) mbar_wait(full, (turn - 1) & 1, a.err);
         __syncwarp();
     } else if (warp == GM_W_MMA) {
         // -------------------------------------------------------------- MMA
@@ -364,7 +341,7 @@ __global__ void __launch_bounds__(GM_THREADS, 1)
         mma_commit(bar(B_FIN));
         mbar_wait(bar(B_FIN), 0, a.err);
         __syncwarp();
-    } else {
+    } else if (warp >= GM_W_EPI) {
         // --------------------------------------------------------- epilogue
         const int q = warp - GM_W_EPI;  // TMEM lane quadrant: weight rows 32 q .. 32 q + 31 of the tile
         constexpr int CH = NT < 32 ? 16 : 32, NCH = NT / CH;
@@ -414,13 +391,13 @@ int launch_gm(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &
     const cuuint32_t wb[3] = {128, GM_M, 1};
     int st = encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, W->codes, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
     const cuuint64_t xd[2] = {(cuuint64_t)A->in, (cuuint64_t)A->rows}, xs[1] = {(cuuint64_t)op_in_padded(A->in)};
-    const cuuint32_t xb[2] = {128, 1};
+    const cuuint32_t xb[2] = {128, NT};
     if (st == K3MOE_OK)
         st = encode_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A->codes, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
     if (st != K3MOE_OK) return st;
     if (ensure_smem((const void *)k3_grouped_matmul<NT, CT>, C::SMEM) != K3MOE_OK) return K3MOE_ECUDA;
     const long most = std::min<long>(a.slots, (long)a.E + a.slots / NT) * a.tiles_n;  // tiles there can be
-    if (launch_pdl(k3_grouped_matmul<NT, CT>, dim3((unsigned)std::min<long>(most, num_sms())), dim3(GM_THREADS), C::SMEM, s,
+    if (launch_pdl(k3_grouped_matmul<NT, CT>, dim3((unsigned)std::min<long>(most, num_sms())), dim3(C::THREADS), C::SMEM, s,
                    wmap, xmap, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
@@ -444,7 +421,7 @@ int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, c
 {
     GmArgs a = {};
     a.atoms = W->atoms, a.atoms_stride = W->atoms_stride;
-    a.scales = A->scales, a.sstride = mx8_scale_stride(A->in);
+    a.codes = A->codes, a.scales = A->scales, a.cstride = op_in_padded(A->in), a.sstride = mx8_scale_stride(A->in);
     a.offsets = g->offsets, a.order = g->order;
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = A->rows;
     a.N = W->rows, a.nks = W->in / 128, a.nka = op_k_atoms(W->in), a.tiles_n = (W->rows + GM_M - 1) / GM_M;
