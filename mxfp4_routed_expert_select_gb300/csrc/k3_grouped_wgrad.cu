@@ -7,10 +7,12 @@
 // and nothing is transposed.
 //
 // A persistent CTA walks (expert, 128 n, 256 k) tiles; a step is 64 rows of the group.
-// The last step's rows past the group come as zeros: they are gathered with a row index
-// outside the matrix.  Roles: warp 0 copies dY's columns, warp 2 X's (by index where X
-// has a row per token), warp 1 issues MMAs, warps 4 and up read one accumulator out
-// by TMA stores while the other one's products run.
+// Roles: warp 0 issues MMAs, warps 4 to 11 read one accumulator out by TMA stores while
+// the other one's products run, and each further warp fills one stage of 64 rows: dY's
+// columns by TMA, X's by TMA too where it lies in group order, else row by row with
+// asynchronous copies into the same swizzled form; in a group's last step the rows past
+// it are made zeros in both.  (TMA gathers of four rows take 72 clocks each: 64 experts x
+// 1536 x 7168 from 16384 rows took 2.06 ms with them.)
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -29,21 +31,25 @@ namespace k3 {
 namespace {
 
 constexpr int GW_M = 128, GW_N = 256, GW_K = 64;  // n and k of a tile, rows of a step
-constexpr int GW_W_Y = 0, GW_W_MMA = 1, GW_W_X = 2, GW_W_EPI = 4;
+constexpr int GW_NS = 4;
+constexpr int GW_W_MMA = 0, GW_W_EPI = 4;
 constexpr int GW_EPI = 8;  // epilogue warps: two per TMEM lane quadrant, on alternate pieces
-constexpr int GW_THREADS = (GW_W_EPI + GW_EPI) * 32;
+constexpr int GW_W_FILL = GW_W_EPI + GW_EPI;
+constexpr int GW_FILL = 2;  // warps that fill a stage, half of its rows each
+constexpr int GW_THREADS = (GW_W_FILL + GW_FILL * GW_NS) * 32;
 
 struct GwArgs {
     const int32_t *offsets, *order;
     int E, top_k, slots, gather, xrows;
     int tiles_k, tiles_e;  // k tiles of a row of tiles, tiles of an expert
-    int N, accumulate;
+    int N, K, accumulate;
+    const __nv_bfloat16 *dy, *x;
+    long lddy, ldx;
     int *err;
 };
 
 constexpr int GW_PANEL = GW_K * 128;  // 64 rows of 64 columns
 constexpr int GW_OFF_X = GW_M / 64 * GW_PANEL, GW_STAGE = GW_OFF_X + GW_N / 64 * GW_PANEL;
-constexpr int GW_NS = 4;
 constexpr int GW_BOX = 4096;  // a staged piece of dW: 32 rows of 128 bytes
 constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * GW_BOX;
 constexpr int GW_BARS = 2 * GW_NS + 2 * 2 + 1;
@@ -70,19 +76,25 @@ K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc)
 }
 K3_DEV uint32_t mn_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(GW_PANEL >> 4) << 16); }
 
-K3_DEV void gw_gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&r)[4], uint32_t bar)
+// 16 bytes from global to shared memory, asynchronously.
+K3_DEV void gw_copy16(uint32_t dst, const void *src)
 {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-                 "l"((uint64_t)map), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(bar)
-                 : "memory");
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-K3_DEV void gw_expect(uint32_t bar, uint32_t bytes)
+// Chunk c of row r of a panel: eight columns of a row, zeros where `on` is false or the
+// columns lie past the matrix.
+K3_DEV void gw_chunk(uint32_t panel, int r, int c, const __nv_bfloat16 *row, int col, int cols, bool on)
 {
-    asm volatile("{\n\t.reg .pred e;\n\t.reg .b64 st;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 st, [%0], %1;\n\t}" ::"r"(bar),
-                 "r"(bytes)
-                 : "memory");
+    const uint32_t dst = panel + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
+    if (on && col < cols)
+        gw_copy16(dst, row + col);
+    else
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
+}
+// Announces copied bytes, without an arrival.
+K3_DEV void mbar_expect(uint32_t bar, uint32_t bytes)
+{
+    asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
 // A staged piece to (k, n) of expert e: stored, or added in fp32.
 K3_DEV void gw_store(const CUtensorMap *map, uint32_t src, int k, int n, int e, int accumulate)
@@ -115,11 +127,9 @@ K3_DEV GwTile gw_tile(const GwArgs &a, int u)
     return t;
 }
 
-// ymap, xmap: 64 columns x 64 rows; yrow, xrow: single rows for gathers.
 template <typename CT>
 __global__ void __launch_bounds__(GW_THREADS, 1)
-    k3_grouped_wgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap yrow,
-                     const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap xrow,
+    k3_grouped_wgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ CUtensorMap cmap, const GwArgs a)
 {
     extern __shared__ uint8_t smem_raw[];
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; i++) {
-            mbar_init(bar(B_FULL + i), 2);
+            mbar_init(bar(B_FULL + i), GW_FILL);
             mbar_init(bar(B_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -159,54 +169,68 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
     griddep_wait();
     const int n_tiles = a.E * a.tiles_e, first = (int)blockIdx.x, step = (int)gridDim.x;
 
-    if (warp == GW_W_Y || warp == GW_W_X) {
-        // ------------------------------------------------------- producers
-        const bool is_y = warp == GW_W_Y;
-        const CUtensorMap *map = is_y ? &ymap : &xmap, *rmap = is_y ? &yrow : &xrow;
-        const int panels = is_y ? GW_M / 64 : GW_N / 64, limit = is_y ? a.slots : a.xrows;
-        const bool by_index = !is_y && a.gather;
-        uint32_t it = 0, phase = 1;  // before its first completion an EMPTY barrier's odd phase counts as passed
-        int s = 0;
-        bool ok = true;
-        for (int u = first; u < n_tiles && ok; u += step) {
-            const GwTile t = gw_tile(a, u);
-            const int col = is_y ? t.n0 : t.k0, quad = 4 * (lane & 15);
-            for (int r0 = 0; r0 < t.rows; r0 += GW_K, it++) {
-                const bool gather = by_index || r0 + GW_K > t.rows;
-                int src[4];
-                if (gather)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const int r = r0 + quad + i;
-                        int x = limit;  // past the group: a row outside the matrix, zeros
-                        if (r < t.rows) {
-                            x = t.row + r;
-                            if (by_index) x = a.order[x] / a.top_k;
-                            if (x < 0 || x > limit) x = limit;
-                        }
-                        src[i] = x;
-                    }
-                if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
-                    ok = false;
-                    break;
-                }
-                const uint32_t dst = sbase + (uint32_t)(s * GW_STAGE + (is_y ? 0 : GW_OFF_X)), full = bar(B_FULL + s);
-                gw_expect(full, (uint32_t)(panels * GW_PANEL));
-                __syncwarp();
-                if (gather) {
-                    for (int p = lane >> 4; p < panels; p += 2)
-                        gw_gather4(dst + (uint32_t)(p * GW_PANEL + quad * 128), rmap, col + 64 * p, src, full);
-                } else if (lane < panels) {
-                    tma_load_2d(dst + (uint32_t)(lane * GW_PANEL), map, col + 64 * lane, t.row + r0, full);
-                }
-                __syncwarp();
-                if (++s == NS) s = 0, phase ^= 1u;
+    if (warp >= GW_W_FILL) {
+        // -------------------------------------------------- a stage's fillers
+        // Every NS-th step of this CTA's tiles; the GW_FILL warps of a stage have
+        // half of its rows each, the first one issues the TMA copies.
+        const int s = (warp - GW_W_FILL) / GW_FILL, half = (warp - GW_W_FILL) % GW_FILL;
+        constexpr int ROWS = GW_K / GW_FILL;
+        const uint32_t st = sbase + (uint32_t)(s * GW_STAGE), full = bar(B_FULL + s);
+        uint32_t turn = 0;
+        int u = first, r0 = s * GW_K, tile = -1;
+        GwTile t = {};
+        for (;; r0 += NS * GW_K, turn++) {
+            for (; u < n_tiles; u += step) {
+                if (u != tile) tile = u, t = gw_tile(a, u);
+                if (r0 < t.rows) break;
+                r0 -= (t.rows + GW_K - 1) / GW_K * GW_K;
             }
+            if (u >= n_tiles) break;
+            const int n = min(GW_K, t.rows - r0);  // rows of the group in this step
+            // lane l: X's row of the half's row l
+            int src = 0;
+            if (a.gather && half * ROWS + lane < n) {
+                src = a.order[t.row + r0 + half * ROWS + lane] / a.top_k;
+                if (src < 0 || src >= a.xrows) src = 0;
+            }
+            // before its first completion an EMPTY barrier's odd phase counts as passed
+            if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
+            const bool whole = n == GW_K;
+            // whole steps: dY (and X in group order) by TMA
+            if (half == 0 && whole && lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_OFF_X : GW_STAGE));
+            __syncwarp();
+            if (half == 0 && whole) {
+                if (lane < GW_M / 64)
+                    tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &ymap, t.n0 + 64 * lane, t.row + r0, full);
+                else if (!a.gather && lane < GW_M / 64 + GW_N / 64)
+                    tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &xmap, t.k0 + 64 * (lane - GW_M / 64), t.row + r0, full);
+            }
+            __syncwarp();
+            if (a.gather || !whole) {
+                // A row of 128 + 256 columns is 16 + 32 chunks of 16 bytes: dY's by half a
+                // warp, two rows at a time, X's by a warp
+                if (!whole)
+                    for (int i = 0; i < ROWS; i += 2) {
+                        const int r = half * ROWS + i + (lane >> 4), c = lane & 15;
+                        gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy,
+                                 t.n0 + 8 * c, a.N, r < n);
+                    }
+#pragma unroll 8
+                for (int i = 0; i < ROWS; i++) {
+                    const int r = half * ROWS + i;
+                    const long x = a.gather ? __shfl_sync(0xffffffffu, src, i) : t.row + r0 + min(r, n - 1);
+                    gw_chunk(st + (uint32_t)(GW_OFF_X + (lane >> 3) * GW_PANEL), r, lane & 7, a.x + x * a.ldx, t.k0 + 8 * lane,
+                             a.K, r < n);
+                }
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+                __syncwarp();
+            }
+            if (lane == 0) mbar_arrive(full);
         }
-        // drain: every copy issued here has landed before the CTA exits (the last
-        // NS of them; earlier ones were waited for before their reuse)
-        for (uint32_t i = it > (uint32_t)NS ? it - NS : 0; i < it; i++)
-            mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
+        // drain: every copy issued here has landed before the CTA exits (the last turn's;
+        // earlier ones were waited for before their stage's reuse)
+        if (turn) mbar_wait(full, (turn - 1) & 1, a.err);
         __syncwarp();
     } else if (warp == GW_W_MMA) {
         // -------------------------------------------------------------- MMA
@@ -322,22 +346,21 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
 
 // ---------------------------------------------------------------- launchers
 
-// A bf16 matrix in boxes of 64 columns x `rows`, 128-byte swizzle.
-int row_map(CUtensorMap *map, const void *p, int cols, int n_rows, long ld, int rows)
+// A bf16 matrix in boxes of a panel: 64 columns x 64 rows, 128-byte swizzle.
+int row_map(CUtensorMap *map, const void *p, int cols, int n_rows, long ld)
 {
     const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)n_rows}, strides[1] = {(cuuint64_t)ld * 2};
-    const cuuint32_t box[2] = {64, (cuuint32_t)rows};
+    const cuuint32_t box[2] = {64, GW_K};
     return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 template <typename CT>
-int launch_gw(void *dW, const void *dY, long lddy, const void *X, long ldx, int K, const GwArgs &a, cudaStream_t s)
+int launch_gw(void *dW, const GwArgs &a, cudaStream_t s)
 {
-    CUtensorMap ymap, yrow, xmap, xrow, cmap;
-    int st = row_map(&ymap, dY, a.N, a.slots, lddy, GW_K);
-    if (st == K3MOE_OK) st = row_map(&yrow, dY, a.N, a.slots, lddy, 1);
-    if (st == K3MOE_OK) st = row_map(&xmap, X, K, a.xrows, ldx, GW_K);
-    if (st == K3MOE_OK) st = row_map(&xrow, X, K, a.xrows, ldx, 1);
+    CUtensorMap ymap, xmap, cmap;
+    int st = row_map(&ymap, a.dy, a.N, a.slots, a.lddy);
+    if (st == K3MOE_OK) st = row_map(&xmap, a.x, a.K, a.xrows, a.ldx);
+    const int K = a.K;
     const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)a.N, (cuuint64_t)a.E},
                      strides[2] = {(cuuint64_t)K * sizeof(CT), (cuuint64_t)K * a.N * sizeof(CT)};
     const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(CT)), 32, 1};
@@ -347,8 +370,7 @@ int launch_gw(void *dW, const void *dY, long lddy, const void *X, long ldx, int 
     if (st != K3MOE_OK) return st;
     if (ensure_smem((const void *)k3_grouped_wgrad<CT>, GW_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
     const int grid = std::min(a.E * a.tiles_e, num_sms());
-    if (launch_pdl(k3_grouped_wgrad<CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, yrow, xmap, xrow, cmap,
-                   a) != cudaSuccess) {
+    if (launch_pdl(k3_grouped_wgrad<CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, xmap, cmap, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
@@ -367,9 +389,10 @@ int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const vo
     const long tiles = (long)a.tiles_k * ((N + GW_M - 1) / GW_M);
     if (tiles * a.E > 0x7fffffffL) return K3MOE_EINVAL;
     a.tiles_e = (int)tiles;
-    a.N = N, a.accumulate = accumulate, a.err = err;
-    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(dW, dY, lddy, X, ldx, K, a, s)
-                              : launch_gw<float>(dW, dY, lddy, X, ldx, K, a, s);
+    a.N = N, a.K = K, a.accumulate = accumulate, a.err = err;
+    a.dy = (const __nv_bfloat16 *)dY, a.x = (const __nv_bfloat16 *)X, a.lddy = lddy, a.ldx = ldx;
+    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(dW, a, s)
+                              : launch_gw<float>(dW, a, s);
 }
 
 }  // namespace k3
