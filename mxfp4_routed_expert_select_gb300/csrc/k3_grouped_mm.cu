@@ -50,7 +50,7 @@ struct GmArgs {
     int N, nks, nka, tiles_n;  // nks: steps of 128 along K; nka: atoms per row tile
     void *C;
     long ldc;
-    int accumulate;
+    int accumulate, pairs;     // pairs: two columns of a bf16 C form an aligned word
     int *err;
 };
 
@@ -109,11 +109,9 @@ struct GmTable {
 struct GmTile {
     int e, row, rows, n0;  // first row of C, rows of the group from there on (> 0), first weight row
 };
-template <int NT, int THREADS>
-K3_DEV void gm_table(GmTable &tab, const GmArgs &a)
+K3_DEV void gm_table(GmTable &tab, const GmArgs &a, int tile_rows)
 {
-    constexpr int PER = (GM_MAX_E + 256 - 1) / 256;  // experts of each of the first 256 threads
-    static_assert(THREADS >= 256, "threads of the table");
+    constexpr int PER = (GM_MAX_E + 256 - 1) / 256;  // experts of each of the first 256 threads (a CTA has more)
     int v[PER], mine = 0;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, e0 = PER * (int)threadIdx.x;
     if (threadIdx.x < 256) {
@@ -122,7 +120,7 @@ K3_DEV void gm_table(GmTable &tab, const GmArgs &a)
         for (int i = 0; i < PER; i++) {
             const int e = e0 + i, hi = e < a.E ? min(max(a.offsets[e + 1], lo), a.slots) : lo;
             if (e <= a.E) tab.off[e] = lo;
-            v[i] = (hi - lo + NT - 1) / NT;
+            v[i] = (hi - lo + tile_rows - 1) / tile_rows;
             mine += v[i];
             lo = hi;
         }
@@ -194,13 +192,37 @@ struct GmCfg {
     static_assert(BARS * 8 + 8 <= 256, "barriers");
 };
 
-template <typename CT>
-K3_DEV void gm_put(CT *p, float v, int accumulate)
+// A lane's column n of C, rows 0 .. rows - 1 of the CH from o on.  pairs (bf16, N even,
+// rows of C aligned for it): lanes swap every other value with their neighbour and store
+// two columns of every other row, half as many stores (which bounded products of a
+// short K: 65536 rows x 7168 x 1536 took 794 us with single ones, 572 with half of them).
+template <typename CT, int CH>
+K3_DEV void gm_put(const GmArgs &a, CT *o, int n, int rows, const uint32_t (&r)[CH])
 {
-    if constexpr (sizeof(CT) == 2)
-        *p = __float2bfloat16_rn(v);
-    else
-        *p = accumulate ? *p + v : v;
+    if constexpr (sizeof(CT) == 2) {
+        if (a.pairs) {
+            const int odd = threadIdx.x & 1;
+            CT *p = o + (long)odd * a.ldc - odd;
+#pragma unroll
+            for (int c = 0; c < CH; c += 2) {
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? r[c] : r[c + 1], 1);
+                const __nv_bfloat162 v = odd ? __floats2bfloat162_rn(__uint_as_float(got), __uint_as_float(r[c + 1]))
+                                             : __floats2bfloat162_rn(__uint_as_float(r[c]), __uint_as_float(got));
+                if (c + odd < rows && n < a.N) *(__nv_bfloat162 *)(p + (long)c * a.ldc) = v;
+            }
+            return;
+        }
+    }
+    if (n >= a.N) return;
+#pragma unroll
+    for (int c = 0; c < CH; c++)
+        if (c < rows) {
+            CT *p = o + (long)c * a.ldc;
+            if constexpr (sizeof(CT) == 2)
+                *p = __float2bfloat16_rn(__uint_as_float(r[c]));
+            else
+                *p = a.accumulate ? *p + __uint_as_float(r[c]) : __uint_as_float(r[c]);
+        }
 }
 
 template <int NT, typename CT>
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
     griddep_wait();
-    gm_table<NT, C::THREADS>(tab, a);
+    gm_table(tab, a, NT);
     const int n_tiles = tab.before[a.E] * a.tiles_n, first = (int)blockIdx.x, step = (int)gridDim.x;
 
     if (warp >= GM_W_FILL) {
@@ -362,11 +384,7 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
                 }
-                if (n >= a.N) continue;
-                CT *o = (CT *)a.C + (long)(t.row + j * CH) * a.ldc + n;
-#pragma unroll
-                for (int c = 0; c < CH; c++)
-                    if (j * CH + c < t.rows) gm_put(o + (long)c * a.ldc, __uint_as_float(r[c]), a.accumulate);
+                gm_put<CT, CH>(a, (CT *)a.C + (long)(t.row + j * CH) * a.ldc + n, n, t.rows - j * CH, r);
             }
         }
     }
@@ -379,26 +397,371 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
     }
 }
 
+// ---------------------------------------------------------------- CTA pairs
+//
+// Large groups.  A lone CTA's 128 x 128 tile brings 32 KB per 128 of K into its shared
+// memory and reads as much, 512 clocks of its bandwidth for 256 clocks of MMAs.  A pair
+// (cta_group::2) works on 256 weight rows x up to 256 rows of the group together: each
+// CTA loads its own 128 weight rows and half of the group's rows, and the MMA reads both
+// halves, so that shared memory and tensor cores are both busy for 512 clocks a step.
+//
+// The MMA's columns are the rows of the group, so their number follows the tile: a
+// group is cut into equal tiles of whole 32 rows, and a short tile costs a short MMA.
+//
+// The even CTA issues for both.  Every stage has two filling warps in each CTA; the
+// copies of both CTAs are counted on the even CTA's barrier, and each warp arrives there
+// when its rows' codes and scale bytes are in place.
+
+constexpr int GP_EPI = 8, GP_FILL = 2, GP_NT = 256;
+constexpr int GP_W_FILL = GM_W_EPI + GP_EPI;
+constexpr int GP_OFF_X = GM_M * 128, GP_OFF_WA = 2 * GM_M * 128, GP_OFF_XA = GP_OFF_WA + 512;
+constexpr int GP_STAGE = GP_OFF_XA + 1024 + 512, GP_NS = 6;
+constexpr int GP_THREADS = 32 * (GP_W_FILL + GP_FILL * GP_NS);
+constexpr int GP_BOX = 32;  // rows of a TMA copy of the group's rows
+// TMEM: two accumulators of up to 256 columns, the second from column 128 on (the
+// columns they share are read first), then each stage's scales.  (Tiles of up to 192 rows
+// with accumulators of their own lost: 65536 rows x 1536 x 7168 545 against 508 us, x 7168
+// x 1536 691 against 671.)
+constexpr int GP_OVER = 128, GP_SF0 = GP_OVER + GP_NT, GP_SF = 12;
+constexpr int GP_BARS = 2 * GP_NS + 2 * 2 + 1;
+constexpr int GP_OFF_TAB = GP_NS * GP_STAGE + 256;
+constexpr int GP_SMEM = 1024 + GP_OFF_TAB + (int)sizeof(GmTable);
+static_assert(GP_STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
+static_assert(GP_SMEM <= 232448 && GP_SF0 + GP_SF * GP_NS <= 512 && GP_BARS * 8 + 8 <= 256, "shared memory, TMEM");
+
+// One step for the pair: each CTA's atoms to its own TMEM, four MMAs of K = 32.
+K3_DEV void gp_step(uint32_t tacc, uint32_t wlo, uint32_t xlo, uint32_t sal, uint32_t sf, uint32_t acc, uint32_t id)
+{
+    constexpr uint32_t AHI = (128u >> 4) | (1u << 14);
+    constexpr uint32_t ID1 = (1u << 4) | (1u << 29);  // the next scale byte of both
+#define GP_CP(col, off) \
+    "add.u32 x, %3, " #off ";\n\tadd.u32 y, %4, " #col ";\n\tmov.b64 d, {x, %7};\n\t@e tcgen05.cp.cta_group::2.32x128b.warpx4 [y], d;\n\t"
+#define GP_MMA(k2, pred)                                                                                      \
+    "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %8};\n\tmov.b64 db, {y, %8};\n\t"  \
+    "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], da, db, i, [%4], [z], " pred ";\n\t" \
+    "add.u32 i, i, %9;\n\t"
+    asm volatile("{\n\t.reg .pred p, t, e;\n\t.reg .b64 d, da, db;\n\t.reg .b32 x, y, z, i;\n\t"
+                 "elect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.eq.b32 t, %6, %6;\n\tadd.u32 z, %4, 4;\n\t"
+                 "mov.b32 i, %6;\n\t" GP_CP(0, 0) GP_CP(4, 32) GP_CP(8, 64) GP_MMA(0, "p") GP_MMA(2, "t") GP_MMA(4, "t")
+                     GP_MMA(6, "t") "}" ::"r"(tacc),
+                 "r"(wlo), "r"(xlo), "r"(sal), "r"(sf), "r"(acc), "r"(id), "r"(AHI), "r"(SW128_HI), "r"(ID1)
+                 : "memory");
+#undef GP_CP
+#undef GP_MMA
+}
+// gm_load_w with its bytes counted on barrier `bar`, a shared::cluster address (the
+// even CTA's); the atom by a tensor copy, which can name it.
+K3_DEV void gp_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int e, uint32_t adst, const CUtensorMap *amap,
+                      int ak, int art, uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%4, %5, %6}], [%9];\n\t"
+                 "@e cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%2], "
+                 "[%3, {0, %7, %8, %6}], [%9];\n\t}" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(adst), "l"((uint64_t)amap), "r"(x), "r"(row), "r"(e), "r"(ak), "r"(art), "r"(bar)
+                 : "memory");
+}
+K3_DEV void gp_load_x(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
+                 : "memory");
+}
+// Arrival at the even CTA's barrier behind what this thread (and, after a warp barrier,
+// its warp) has written to its own CTA's shared memory.  Those bytes never leave that
+// shared memory: the tensor core beside it reads them, behind the proxy fence that each
+// writer has passed.  So no wider fence than the CTA's own goes with the arrival; one at
+// cluster scope takes 1000 clocks or more, and with it in each stage's path 65536 rows x
+// 1536 x 7168 took 648 us instead of 520.
+K3_DEV void gp_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+// The waits are of the CTA's scope too, those for the other CTA's arrivals among them: what
+// they hand over is tensor memory and staged tiles, which only the tensor core and copies
+// touch.  (An acquire at cluster scope makes a warp wait for its own stores.)
+
+// A pair's tile: tiles of a group are equal but for the last.  half: columns of each CTA.
+struct GpTile {
+    int e, row, rows, n0, half;
+};
+K3_DEV GpTile gp_tile(const GmTable &tab, const GmArgs &a, int u)
+{
+    const int r = u / a.tiles_n;
+    int lo = 0, hi = a.E;  // before[lo] <= r < before[hi]
+    while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (tab.before[m] <= r)
+            lo = m;
+        else
+            hi = m;
+    }
+    const int n = tab.off[lo + 1] - tab.off[lo], tiles = tab.before[lo + 1] - tab.before[lo];
+    const int h = ((n + tiles - 1) / tiles + 31) & ~31, i = r - tab.before[lo];
+    GpTile t;
+    t.e = lo;
+    t.row = tab.off[lo] + i * h;
+    t.rows = min(h, n - i * h);
+    t.half = ((t.rows + 31) & ~31) / 2;
+    t.n0 = (u - r * a.tiles_n) * 2 * GM_M;
+    return t;
+}
+
+template <typename CT>
+__global__ void __launch_bounds__(GP_THREADS, 1)
+    k3_grouped_matmul_pair(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap amap,
+                           const __grid_constant__ CUtensorMap xmap, const GmArgs a)
+{
+    constexpr int NS = GP_NS;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const uint32_t sbase = smem_addr(sm);
+    uint64_t *bars = (uint64_t *)(sm + NS * GP_STAGE);
+    constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2;
+    uint32_t *tmem_slot = (uint32_t *)(bars + GP_BARS);
+    volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
+    GmTable &tab = *(GmTable *)(sm + GP_OFF_TAB);
+    auto bar = [&](int i) { return smem_addr(bars + i); };
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();  // 0: the CTA that issues
+    const int first = (int)blockIdx.x >> 1, step = (int)gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&wmap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&amap) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&xmap) : "memory");
+        for (int i = 0; i < NS; i++) {
+            mbar_init(bar(B_FULL + i), 1 + 2 * GP_FILL);  // the bytes announced; each filler's part done
+            mbar_init(bar(B_EMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            mbar_init(bar(B_ACCF + i), 1);
+            mbar_init(bar(B_ACCE + i), 2 * GP_EPI);  // the epilogue warps of both CTAs
+        }
+        mbar_init(bar(B_FIN), 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == GM_W_MMA) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                     "r"(512)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // the other CTA's barriers are initialised
+    tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
+    griddep_wait();
+    gm_table(tab, a, GP_NT);
+    const int n_tiles = tab.before[a.E] * a.tiles_n;
+
+    if (warp >= GP_W_FILL) {
+        // -------------------------------------------------- a stage's fillers
+        // Every NS-th step of this pair's tiles.  Of this CTA's rows (half the tile's)
+        // each warp copies 64, lanes 8 q .. 8 q + 7 the 16-byte chunks of rows q, q + 4,
+        // ..; of all the tile's rows it brings the scale words of 128, a lane every 32nd.
+        constexpr int R = 64 / 4;
+        const int s = (warp - GP_W_FILL) / GP_FILL, f = (warp - GP_W_FILL) % GP_FILL;
+        const uint32_t st = sbase + (uint32_t)(s * GP_STAGE), full0 = addr_of_rank(bar(B_FULL + s), 0);
+        uint32_t turn = 0;
+        int u = first, ks = s, tile = -1;
+        GpTile t = {};
+        const uint8_t *sp[4];
+        int src[R];
+        for (;; ks += NS, turn++) {
+            while (ks >= a.nks) ks -= a.nks, u += step;
+            if (u >= n_tiles) break;
+            if (u != tile) {
+                tile = u;
+                t = gp_tile(tab, a, u);
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int r = 128 * f + 32 * j + lane;
+                    sp[j] = r < t.rows ? a.scales + (long)gm_source(a, t.row + r) * a.sstride : nullptr;
+                }
+                if (a.gather)
+#pragma unroll
+                    for (int i = 0; i < R; i++) {
+                        const int r = 64 * f + 4 * i + (lane >> 3), c = rank * t.half + r;
+                        src[i] = r < t.half && c < t.rows ? gm_source(a, t.row + c) : -1;
+                    }
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) w[j] = sp[j] ? *(const uint32_t *)(sp[j] + 4 * ks) : 0u;
+            // before its first completion an EMPTY barrier's odd phase counts as passed
+            if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
+            const int boxes = (t.half + GP_BOX - 1) / GP_BOX;
+            if (f == 0) {
+                if (rank == 0 && lane == 0)
+                    mbar_arrive_expect_tx(bar(B_FULL + s), 2u * (GM_M * 64 + 512 + (a.gather ? 0 : boxes * GP_BOX * 128)));
+                __syncwarp();
+                gp_load_w(st, &wmap, ks * 128, t.n0 + rank * GM_M, t.e, st + GP_OFF_WA, &amap, ks, t.n0 / 128 + rank, full0);
+            }
+            if (a.gather) {
+                const uint8_t *base = a.codes + (long)ks * 128 + (lane & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < R; i++) {
+                    const int r = 64 * f + 4 * i + (lane >> 3);
+                    if (src[i] >= 0)
+                        copy16(st + GP_OFF_X + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)), base + (long)src[i] * a.cstride);
+                }
+            } else if (f == 1 && lane < boxes) {
+                gp_load_x(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t.row + rank * t.half + lane * GP_BOX,
+                          full0);
+            }
+            *(uint4 *)(sm + s * GP_STAGE + GP_OFF_XA + f * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (a.gather) asm volatile("cp.async.wait_all;" ::: "memory");
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) gp_arrive(full0);
+        }
+        // drain: the last turn's copies of both CTAs have landed before the even CTA
+        // exits; the odd one waits in the closing cluster barrier
+        if (rank == 0 && turn) mbar_wait(bar(B_FULL + s), (turn - 1) & 1, a.err);
+        __syncwarp();
+    } else if (warp == GM_W_MMA && rank == 1) {
+        // the even CTA's last commits have arrived here before this CTA may exit
+        volatile int ignore = 0;  // after an abort too
+        if (lane == 0) tc_wait(bar(B_FIN), 0, a.err, &ignore);
+        __syncwarp();
+    } else if (warp == GM_W_MMA) {
+        // -------------------------------------------------------------- MMA
+        uint32_t ut = 0, phase = 0;
+        int s = 0;
+        bool ok = true, ready = false;
+        const uint32_t lo = sw128_lo(sbase);
+        constexpr uint32_t SD = GP_STAGE / 16;  // descriptor words between stages
+        for (int u = first; u < n_tiles && ok; u += step, ut++) {
+            const int buf = (int)(ut & 1);
+            const uint32_t id = gm_idesc(2 * GM_M, 2 * gp_tile(tab, a, u).half, 0);
+            // the epilogue frees the columns that a tile's accumulator shares with the next
+            if (ut >= 1) {
+                const uint32_t p = ut - 1;
+                if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCE + (int)(p & 1)), (p / 2) & 1, a.err, abort_flag)))
+                    break;
+            }
+            tc_fence_after();
+            for (int ks = 0; ks < a.nks; ks++) {
+                if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const int sn = s + 1 == NS ? 0 : s + 1;
+                const uint32_t pn = sn ? phase : phase ^ 1u;
+                // look at the next stage while this one is issued
+                ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
+                const uint32_t d = lo + (uint32_t)s * SD;
+                gp_step(tmem + (uint32_t)(buf * GP_OVER), d, d + GP_OFF_X / 16, d + GP_OFF_WA / 16,
+                        tmem + (uint32_t)(GP_SF0 + GP_SF * s), ks ? 1u : 0u, id);
+                pair_commit(bar(B_EMPTY + s));
+                s = sn;
+                phase = pn;
+            }
+            if (!ok) break;
+            pair_commit(bar(B_ACCF + buf));
+        }
+        // every MMA and copy issued above has completed before TMEM is freed
+        pair_commit(bar(B_FIN));
+        mbar_wait(bar(B_FIN), 0, a.err);
+        __syncwarp();
+    } else if (warp >= GM_W_EPI) {
+        // --------------------------------------------------------- epilogue
+        // A lane holds one weight row n, 32 columns (rows of C) at a time; the two warps
+        // of a quadrant take alternate pieces, those in the columns shared with the
+        // other accumulator first.
+        const int q = warp & 3, other = (warp - GM_W_EPI) >> 2;
+        constexpr int PIECES = GP_NT / 32, OVER = GP_OVER / 32, SHARED = PIECES - OVER;
+        uint32_t ut = 0;
+        for (int u = first; u < n_tiles; u += step, ut++) {
+            const int buf = (int)(ut & 1);
+            const GpTile t = gp_tile(tab, a, u);
+            if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
+            tc_fence_after();
+            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * GP_OVER);
+            const int n = t.n0 + rank * GM_M + q * 32 + lane;
+#pragma unroll 1
+            for (int i = other; i < PIECES; i += 2) {
+                const int j = buf ? i : (i + OVER) % PIECES;
+                const bool on = j * 32 < t.rows;
+                uint32_t r[32];
+                if (on) tmem_ld_chunk(tacc + (uint32_t)(j * 32), r);
+                if (i + 2 >= SHARED && i < SHARED) {  // this warp's last shared piece
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_rank(bar(B_ACCE + buf), 0);
+                }
+                if (on) gm_put<CT, 32>(a, (CT *)a.C + (long)(t.row + j * 32) * a.ldc + n, n, t.rows - j * 32, r);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();  // neither CTA leaves, or frees TMEM, while the other's work may reach it
+    if (warp == GM_W_MMA) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
 // ---------------------------------------------------------------- launchers
+
+int weight_map(CUtensorMap *map, const k3moe_mx_experts *W)
+{
+    const cuuint64_t wd[3] = {(cuuint64_t)W->in, (cuuint64_t)W->rows, (cuuint64_t)W->E},
+                     ws[2] = {(cuuint64_t)W->in / 2, (cuuint64_t)W->codes_stride};
+    const cuuint32_t wb[3] = {128, GM_M, 1};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, W->codes, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+// The rows' codes in boxes of 128 bytes x `rows`.
+int row8_map(CUtensorMap *map, const k3moe_mx8_rows *A, int rows)
+{
+    const cuuint64_t xd[2] = {(cuuint64_t)A->in, (cuuint64_t)A->rows}, xs[1] = {(cuuint64_t)op_in_padded(A->in)};
+    const cuuint32_t xb[2] = {128, (cuuint32_t)rows};
+    return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A->codes, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+}
 
 template <int NT, typename CT>
 int launch_gm(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &a, cudaStream_t s)
 {
     using C = GmCfg<NT>;
     CUtensorMap wmap, xmap;
-    const cuuint64_t wd[3] = {(cuuint64_t)W->in, (cuuint64_t)W->rows, (cuuint64_t)W->E},
-                     ws[2] = {(cuuint64_t)W->in / 2, (cuuint64_t)W->codes_stride};
-    const cuuint32_t wb[3] = {128, GM_M, 1};
-    int st = encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 3, W->codes, wd, ws, wb, CU_TENSOR_MAP_SWIZZLE_128B);
-    const cuuint64_t xd[2] = {(cuuint64_t)A->in, (cuuint64_t)A->rows}, xs[1] = {(cuuint64_t)op_in_padded(A->in)};
-    const cuuint32_t xb[2] = {128, NT};
-    if (st == K3MOE_OK)
-        st = encode_map(&xmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, A->codes, xd, xs, xb, CU_TENSOR_MAP_SWIZZLE_128B);
+    int st = weight_map(&wmap, W);
+    if (st == K3MOE_OK) st = row8_map(&xmap, A, NT);
     if (st != K3MOE_OK) return st;
     if (ensure_smem((const void *)k3_grouped_matmul<NT, CT>, C::SMEM) != K3MOE_OK) return K3MOE_ECUDA;
     const long most = std::min<long>(a.slots, (long)a.E + a.slots / NT) * a.tiles_n;  // tiles there can be
     if (launch_pdl(k3_grouped_matmul<NT, CT>, dim3((unsigned)std::min<long>(most, num_sms())), dim3(C::THREADS), C::SMEM, s,
                    wmap, xmap, a) != cudaSuccess) {
+        cudaGetLastError();
+        return K3MOE_ECUDA;
+    }
+    return K3MOE_OK;
+}
+template <typename CT>
+int launch_gp(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, GmArgs a, cudaStream_t s)
+{
+    CUtensorMap wmap, amap, xmap;
+    int st = weight_map(&wmap, W);
+    if (st == K3MOE_OK) st = row8_map(&xmap, A, GP_BOX);
+    // the scale atoms, [expert][row tile][k][512 bytes], one at a time
+    const cuuint64_t nk = (cuuint64_t)a.nka, ad[4] = {128, nk, (cuuint64_t)op_row_tiles(W->rows), (cuuint64_t)W->E},
+                     as[3] = {512, nk * 512, (cuuint64_t)W->atoms_stride};
+    const cuuint32_t ab[4] = {128, 1, 1, 1};
+    if (st == K3MOE_OK)
+        st = encode_map(&amap, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, W->atoms, ad, as, ab, CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (st != K3MOE_OK) return st;
+    if (ensure_smem((const void *)k3_grouped_matmul_pair<CT>, GP_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
+    a.tiles_n = (a.N + 2 * GM_M - 1) / (2 * GM_M);
+    const long most = std::min<long>(a.slots, (long)a.E + a.slots / GP_NT) * a.tiles_n;  // tiles there can be
+    if (launch_dependent(true, 2, k3_grouped_matmul_pair<CT>, dim3((unsigned)(2 * std::min<long>(most, num_sms() / 2))),
+                         dim3(GP_THREADS), GP_SMEM, s, wmap, amap, xmap, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
@@ -411,7 +774,8 @@ int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArg
     return avg <= 12   ? launch_gm<16, CT>(A, W, a, s)
            : avg <= 24 ? launch_gm<32, CT>(A, W, a, s)
            : avg <= 48 ? launch_gm<64, CT>(A, W, a, s)
-                       : launch_gm<128, CT>(A, W, a, s);
+           : avg <= 96 ? launch_gm<128, CT>(A, W, a, s)
+                       : launch_gp<CT>(A, W, a, s);
 }
 
 }  // namespace
@@ -426,6 +790,7 @@ int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, c
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = A->rows;
     a.N = W->rows, a.nks = W->in / 128, a.nka = op_k_atoms(W->in), a.tiles_n = (W->rows + GM_M - 1) / GM_M;
     a.C = C, a.ldc = ldc, a.accumulate = accumulate, a.err = err;
+    a.pairs = cdt == K3MOE_BF16 && a.N % 2 == 0 && ldc % 2 == 0 && ((uintptr_t)C & 3u) == 0;
     if (((long)a.E + a.slots) * a.tiles_n > 0x7fffffffL) return K3MOE_EINVAL;
     return cdt == K3MOE_BF16 ? launch_gm_ct<__nv_bfloat16>(A, W, a, s) : launch_gm_ct<float>(A, W, a, s);
 }

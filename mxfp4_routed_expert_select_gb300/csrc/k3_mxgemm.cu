@@ -121,27 +121,11 @@ K3_DEV void mg_step(uint32_t tacc, uint32_t slo, uint32_t tlo, uint32_t sal, uin
 #undef MG_MMA
 #undef MG_OPERANDS
 
-K3_DEV uint32_t cluster_rank()
-{
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
 K3_DEV uint32_t cluster_size()
 {
     uint32_t r;
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
     return r;
-}
-K3_DEV void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-K3_DEV uint32_t addr_of_rank(uint32_t addr, uint32_t rank)
-{
-    uint32_t a;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-    return a;
 }
 K3_DEV float4 ld_peer4(uint32_t addr, uint32_t rank)
 {
@@ -502,57 +486,6 @@ struct MpCfg {
     static_assert(STAGE % 1024 == 0 && OFF_SA % 1024 == 0, "swizzled tiles are 1024-byte aligned");
 };
 
-// Arrival at the barrier of the same offset in the pair's CTA `rank`, for a
-// hand-over of tensor memory alone: the accumulator's loads are ordered by their
-// wait and the tcgen05 fence before this, and no ordinary memory is handed over, so
-// the arrival is relaxed (a release at cluster scope took 1200 clocks, on the path
-// of the next tile's first MMA).
-K3_DEV void mbar_arrive_rank(uint32_t bar, uint32_t rank)
-{
-    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr_of_rank(bar, rank)) : "memory");
-}
-// The waits for barriers that the other CTA's threads, copies or commits arrive
-// at: cluster scope, bounded as mbar_wait.
-K3_DEV uint32_t mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity), "r"(20000u)
-                 : "memory");
-    return ok;
-}
-static __device__ __noinline__ bool mbar_wait_cluster_slow(uint32_t bar, uint32_t parity, int *err)
-{
-    const uint64_t t0 = global_ns();
-    for (uint32_t n = 1;; n++) {
-        if (mbar_try_wait_cluster(bar, parity)) return true;
-        if ((n & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
-            set_device_error(err, K3MOE_ETIMEOUT);
-            return false;
-        }
-    }
-}
-K3_DEV bool tc_wait_cluster(uint32_t bar, uint32_t parity, int *err, volatile int *abort_flag)
-{
-    if (*abort_flag) return false;
-    if (mbar_try_wait_cluster(bar, parity) || mbar_wait_cluster_slow(bar, parity, err)) return true;
-    *abort_flag = 1;
-    return false;
-}
-// Non-blocking: has the phase completed?
-K3_DEV bool mbar_test_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return ok != 0;
-}
 // mg_load with all bytes counted on barrier `bar` (a shared::cluster address: the
 // even CTA's), the atoms as boxes [row tile][2][512] at (ka, rt).
 K3_DEV void mp_load(uint32_t dst, const CUtensorMap *map, uint32_t adst, const CUtensorMap *amap, int x, int row,
@@ -572,16 +505,6 @@ K3_DEV void mp_load_codes(uint32_t dst, const CUtensorMap *map, int x, int row, 
                  "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
                  "[%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
                  "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
-                 : "memory");
-}
-// Arrival at the barrier of this offset in both CTAs once everything issued
-// before has completed.
-K3_DEV void mp_commit(uint32_t bar)
-{
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
-                 "%1;\n\t}" ::"r"(bar),
-                 "h"((uint16_t)3)
                  : "memory");
 }
 // A staged piece of C from shared memory: stored, or added in fp32.
@@ -724,15 +647,15 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
                 mg_step<2, NT>(tacc, slo + (uint32_t)s * SD, slo + C::OFF_T / 16 + (uint32_t)s * SD,
                                       slo + C::OFF_SA / 16 + (uint32_t)s * SD, tmem + (uint32_t)(C::SF0 + C::SF * s),
                                       shift, ks ? 1u : 0u);
-                mp_commit(bar(B_EMPTY + s));
+                pair_commit(bar(B_EMPTY + s));
                 s = sn;
                 phase = pn;
             }
             if (!ok) break;
-            mp_commit(bar(B_ACCF + buf));
+            pair_commit(bar(B_ACCF + buf));
         }
         // every MMA and copy issued above has completed before TMEM is freed
-        mp_commit(bar(B_FIN));
+        pair_commit(bar(B_FIN));
         mbar_wait(bar(B_FIN), 0, a.err);
         __syncwarp();
     } else if (warp >= MG_W_EPI) {

@@ -1,5 +1,5 @@
-// k3_tmem.cuh -- accumulator reads and tensor-map making shared by the operand
-// product and the grouped products.
+// k3_tmem.cuh -- accumulator reads, the barriers of CTA pairs, and tensor-map making,
+// shared by the operand product and the grouped products.
 #pragma once
 #include "k3_tcgen05.cuh"
 
@@ -40,6 +40,84 @@ K3_DEV void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32])
                  : "memory");
 }
 
+K3_DEV uint32_t cluster_rank()
+{
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+K3_DEV void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+K3_DEV uint32_t addr_of_rank(uint32_t addr, uint32_t rank)
+{
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+    return a;
+}
+// Arrival at the barrier of the same offset in the pair's CTA `rank`, for a
+// hand-over of tensor memory alone: the accumulator's loads are ordered by their
+// wait and the tcgen05 fence before this, and no ordinary memory is handed over, so
+// the arrival is relaxed (a release at cluster scope took 1200 clocks, on the path
+// of the next tile's first MMA).
+K3_DEV void mbar_arrive_rank(uint32_t bar, uint32_t rank)
+{
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr_of_rank(bar, rank)) : "memory");
+}
+// The waits for barriers that the other CTA's threads, copies or commits arrive
+// at: cluster scope, bounded as mbar_wait.
+K3_DEV uint32_t mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "memory");
+    return ok;
+}
+static __device__ __noinline__ bool mbar_wait_cluster_slow(uint32_t bar, uint32_t parity, int *err)
+{
+    const uint64_t t0 = global_ns();
+    for (uint32_t n = 1;; n++) {
+        if (mbar_try_wait_cluster(bar, parity)) return true;
+        if ((n & 63u) == 0 && global_ns() - t0 > kWaitLimitNs) {
+            set_device_error(err, K3MOE_ETIMEOUT);
+            return false;
+        }
+    }
+}
+K3_DEV bool tc_wait_cluster(uint32_t bar, uint32_t parity, int *err, volatile int *abort_flag)
+{
+    if (*abort_flag) return false;
+    if (mbar_try_wait_cluster(bar, parity) || mbar_wait_cluster_slow(bar, parity, err)) return true;
+    *abort_flag = 1;
+    return false;
+}
+// Non-blocking: has the phase completed?
+K3_DEV bool mbar_test_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+// Arrival at the barrier of this offset in both CTAs once everything issued
+// before has completed.
+K3_DEV void pair_commit(uint32_t bar)
+{
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], "
+                 "%1;\n\t}" ::"r"(bar),
+                 "h"((uint16_t)3)
+                 : "memory");
+}
+
 inline PFN_cuTensorMapEncodeTiled_v12000 map_encoder()
 {
     static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
@@ -60,7 +138,7 @@ inline int encode_map(CUtensorMap *map, CUtensorMapDataType type, int nd, const 
 {
     const auto encode = map_encoder();
     if (!encode) return K3MOE_ECUDA;
-    const cuuint32_t estr[3] = {1, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
     return encode(map, type, (cuuint32_t)nd, (void *)p, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
                ? K3MOE_OK
