@@ -410,24 +410,33 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
 //
 // The even CTA issues for both.  Every stage has two filling warps in each CTA; the
 // copies of both CTAs are counted on the even CTA's barrier, and each warp arrives there
-// when its rows' codes and scale bytes are in place.
+// when its rows' codes and scale bytes are in place.  Warp 1 finds out each tile (its
+// expert, its rows, which rows of the 8-bit matrix they are) ahead of the others and
+// leaves it in a ring: a search takes 1000 clocks, a sixth of a tile with K = 1536.
 
-constexpr int GP_EPI = 8, GP_FILL = 2, GP_NT = 256;
-constexpr int GP_W_FILL = GM_W_EPI + GP_EPI;
+constexpr int GP_EPI = 8, GP_FILL = 2, GP_NT = 256, GP_RING = 4;
+constexpr int GP_W_PLAN = 1, GP_W_FILL = GM_W_EPI + GP_EPI;
 constexpr int GP_OFF_X = GM_M * 128, GP_OFF_WA = 2 * GM_M * 128, GP_OFF_XA = GP_OFF_WA + 512;
 constexpr int GP_STAGE = GP_OFF_XA + 1024 + 512, GP_NS = 6;
 constexpr int GP_THREADS = 32 * (GP_W_FILL + GP_FILL * GP_NS);
 constexpr int GP_BOX = 32;  // rows of a TMA copy of the group's rows
-// TMEM: two accumulators of up to 256 columns, the second from column 128 on (the
-// columns they share are read first), then each stage's scales.  (Tiles of up to 192 rows
-// with accumulators of their own lost: 65536 rows x 1536 x 7168 545 against 508 us, x 7168
-// x 1536 691 against 671.)
-constexpr int GP_OVER = 128, GP_SF0 = GP_OVER + GP_NT, GP_SF = 12;
-constexpr int GP_BARS = 2 * GP_NS + 2 * 2 + 1;
+// TMEM: two accumulators of up to 256 columns, the second from column 192 on, then five
+// slots of scales.  The columns that the accumulators share are read first: the next
+// tile's products wait for that.  (Tiles of up to 192 rows with accumulators of their
+// own lost: 65536 rows x 1536 x 7168 545 against 508 us, x 7168 x 1536 691 against 671.)
+constexpr int GP_OVER = 192, GP_SF0 = GP_OVER + GP_NT, GP_SF = 12, GP_SLOTS = 5;
+constexpr int GP_BARS = 2 * GP_NS + 2 * 2 + 1 + 2 * GP_RING;
 constexpr int GP_OFF_TAB = GP_NS * GP_STAGE + 256;
-constexpr int GP_SMEM = 1024 + GP_OFF_TAB + (int)sizeof(GmTable);
+// A tile: tiles of a group are equal but for the last.
+struct GpTile {
+    int e, row, rows, n0, half;  // expert (-1: no more tiles); half: columns of each CTA
+    int src[GP_NT];              // rows of the 8-bit matrix behind its rows
+};
+constexpr int GP_OFF_RING = GP_OFF_TAB + (int)sizeof(GmTable);
+constexpr int GP_SMEM = 1024 + GP_OFF_RING + GP_RING * (int)sizeof(GpTile);
 static_assert(GP_STAGE % 1024 == 0, "swizzled tiles are 1024-byte aligned");
-static_assert(GP_SMEM <= 232448 && GP_SF0 + GP_SF * GP_NS <= 512 && GP_BARS * 8 + 8 <= 256, "shared memory, TMEM");
+static_assert(GP_SLOTS == GP_NS - 1, "a slot of scales is free when the next stage is full");
+static_assert(GP_SMEM <= 232448 && GP_SF0 + GP_SF * GP_SLOTS <= 512 && GP_BARS * 8 + 8 <= 256, "shared memory, TMEM");
 
 // One step for the pair: each CTA's atoms to its own TMEM, four MMAs of K = 32.
 K3_DEV void gp_step(uint32_t tacc, uint32_t wlo, uint32_t xlo, uint32_t sal, uint32_t sf, uint32_t acc, uint32_t id)
@@ -484,13 +493,10 @@ K3_DEV void gp_arrive(uint32_t bar)
 // they hand over is tensor memory and staged tiles, which only the tensor core and copies
 // touch.  (An acquire at cluster scope makes a warp wait for its own stores.)
 
-// A pair's tile: tiles of a group are equal but for the last.  half: columns of each CTA.
-struct GpTile {
-    int e, row, rows, n0, half;
-};
-K3_DEV GpTile gp_tile(const GmTable &tab, const GmArgs &a, int u)
+// Tile u into the ring, by a whole warp.
+K3_DEV void gp_plan(GpTile &t, const GmTable &tab, const GmArgs &a, int u)
 {
-    const int r = u / a.tiles_n;
+    const int lane = threadIdx.x & 31, r = u / a.tiles_n;
     int lo = 0, hi = a.E;  // before[lo] <= r < before[hi]
     while (hi - lo > 1) {
         const int m = (lo + hi) >> 1;
@@ -501,13 +507,15 @@ K3_DEV GpTile gp_tile(const GmTable &tab, const GmArgs &a, int u)
     }
     const int n = tab.off[lo + 1] - tab.off[lo], tiles = tab.before[lo + 1] - tab.before[lo];
     const int h = ((n + tiles - 1) / tiles + 31) & ~31, i = r - tab.before[lo];
-    GpTile t;
-    t.e = lo;
-    t.row = tab.off[lo] + i * h;
-    t.rows = min(h, n - i * h);
-    t.half = ((t.rows + 31) & ~31) / 2;
-    t.n0 = (u - r * a.tiles_n) * 2 * GM_M;
-    return t;
+    const int row = tab.off[lo] + i * h, rows = min(h, n - i * h);
+    if (lane == 0) {
+        t.e = lo, t.row = row, t.rows = rows;
+        t.half = ((rows + 31) & ~31) / 2;
+        t.n0 = (u - r * a.tiles_n) * 2 * GM_M;
+    }
+#pragma unroll
+    for (int j = 0; j < GP_NT / 32; j++)
+        if (32 * j < rows) t.src[32 * j + lane] = gm_source(a, row + min(32 * j + lane, rows - 1));
 }
 
 template <typename CT>
@@ -520,10 +528,12 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_addr(sm);
     uint64_t *bars = (uint64_t *)(sm + NS * GP_STAGE);
-    constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2;
+    constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2, B_TILEF = B_FIN + 1,
+                  B_TILEE = B_TILEF + GP_RING;
     uint32_t *tmem_slot = (uint32_t *)(bars + GP_BARS);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     GmTable &tab = *(GmTable *)(sm + GP_OFF_TAB);
+    GpTile *ring = (GpTile *)(sm + GP_OFF_RING);
     auto bar = [&](int i) { return smem_addr(bars + i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)cluster_rank();  // 0: the CTA that issues
@@ -540,6 +550,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_ACCF + i), 1);
             mbar_init(bar(B_ACCE + i), 2 * GP_EPI);  // the epilogue warps of both CTAs
+        }
+        for (int i = 0; i < GP_RING; i++) {
+            mbar_init(bar(B_TILEF + i), 1);
+            mbar_init(bar(B_TILEE + i), GP_FILL * NS + GP_EPI + (rank == 0));  // the warps that read it
         }
         mbar_init(bar(B_FIN), 1);
         *abort_flag = 0;
@@ -560,7 +574,34 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     gm_table(tab, a, GP_NT);
     const int n_tiles = tab.before[a.E] * a.tiles_n;
 
-    if (warp >= GP_W_FILL) {
+    // The ring as a reader sees it: tile i of this pair; a warp that has what it needs of
+    // it lets it go.
+    auto tile_in = [&](uint32_t i) {
+        return __all_sync(0xffffffffu, tc_wait(bar(B_TILEF + (int)(i % GP_RING)), (i / GP_RING) & 1, a.err, abort_flag));
+    };
+    auto tile_out = [&](uint32_t i) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_TILEE + (int)(i % GP_RING)));
+    };
+
+    if (warp == GP_W_PLAN) {
+        // ------------------------------------------------------------ tiles
+        uint32_t i = 0;
+        for (int u = first;; u += step, i++) {
+            // before its first completion a barrier's odd phase counts as passed
+            if (!__all_sync(0xffffffffu,
+                            tc_wait(bar(B_TILEE + (int)(i % GP_RING)), ((i / GP_RING) & 1) ^ 1u, a.err, abort_flag)))
+                break;
+            GpTile &t = ring[i % GP_RING];
+            if (u < n_tiles)
+                gp_plan(t, tab, a, u);
+            else if (lane == 0)
+                t.e = -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_TILEF + (int)(i % GP_RING)));
+            if (u >= n_tiles) break;
+        }
+    } else if (warp >= GP_W_FILL) {
         // -------------------------------------------------- a stage's fillers
         // Every NS-th step of this pair's tiles.  Of this CTA's rows (half the tile's)
         // each warp copies 64, lanes 8 q .. 8 q + 7 the 16-byte chunks of rows q, q + 4,
@@ -568,51 +609,43 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         constexpr int R = 64 / 4;
         const int s = (warp - GP_W_FILL) / GP_FILL, f = (warp - GP_W_FILL) % GP_FILL;
         const uint32_t st = sbase + (uint32_t)(s * GP_STAGE), full0 = addr_of_rank(bar(B_FULL + s), 0);
-        uint32_t turn = 0;
-        int u = first, ks = s, tile = -1;
-        GpTile t = {};
-        const uint8_t *sp[4];
-        int src[R];
-        for (;; ks += NS, turn++) {
-            while (ks >= a.nks) ks -= a.nks, u += step;
-            if (u >= n_tiles) break;
-            if (u != tile) {
-                tile = u;
-                t = gp_tile(tab, a, u);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int r = 128 * f + 32 * j + lane;
-                    sp[j] = r < t.rows ? a.scales + (long)gm_source(a, t.row + r) * a.sstride : nullptr;
-                }
-                if (a.gather)
-#pragma unroll
-                    for (int i = 0; i < R; i++) {
-                        const int r = 64 * f + 4 * i + (lane >> 3), c = rank * t.half + r;
-                        src[i] = r < t.half && c < t.rows ? gm_source(a, t.row + c) : -1;
-                    }
+        uint32_t turn = 0, tiles = 0;
+        int ks = s;
+        bool ok = tile_in(0);
+        const GpTile *t = ring;
+        for (; ok && t->e >= 0; ks += NS, turn++) {
+            while (ks >= a.nks && ok && t->e >= 0) {
+                ks -= a.nks;
+                tile_out(tiles++);
+                ok = tile_in(tiles);
+                t = ring + tiles % GP_RING;
             }
+            if (!ok || t->e < 0) break;
+            const int rows = t->rows, half = t->half;
             uint32_t w[4];
 #pragma unroll
-            for (int j = 0; j < 4; j++) w[j] = sp[j] ? *(const uint32_t *)(sp[j] + 4 * ks) : 0u;
-            // before its first completion an EMPTY barrier's odd phase counts as passed
+            for (int j = 0; j < 4; j++) {
+                const int r = 128 * f + 32 * j + lane;
+                w[j] = r < rows ? *(const uint32_t *)(a.scales + (long)t->src[r] * a.sstride + 4 * ks) : 0u;
+            }
             if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
-            const int boxes = (t.half + GP_BOX - 1) / GP_BOX;
+            const int boxes = (half + GP_BOX - 1) / GP_BOX;
             if (f == 0) {
                 if (rank == 0 && lane == 0)
                     mbar_arrive_expect_tx(bar(B_FULL + s), 2u * (GM_M * 64 + 512 + (a.gather ? 0 : boxes * GP_BOX * 128)));
                 __syncwarp();
-                gp_load_w(st, &wmap, ks * 128, t.n0 + rank * GM_M, t.e, st + GP_OFF_WA, &amap, ks, t.n0 / 128 + rank, full0);
+                gp_load_w(st, &wmap, ks * 128, t->n0 + rank * GM_M, t->e, st + GP_OFF_WA, &amap, ks, t->n0 / 128 + rank, full0);
             }
             if (a.gather) {
                 const uint8_t *base = a.codes + (long)ks * 128 + (lane & 7) * 16;
 #pragma unroll
                 for (int i = 0; i < R; i++) {
-                    const int r = 64 * f + 4 * i + (lane >> 3);
-                    if (src[i] >= 0)
-                        copy16(st + GP_OFF_X + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)), base + (long)src[i] * a.cstride);
+                    const int r = 64 * f + 4 * i + (lane >> 3), c = rank * half + r;
+                    if (r < half && c < rows)
+                        copy16(st + GP_OFF_X + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)), base + (long)t->src[c] * a.cstride);
                 }
             } else if (f == 1 && lane < boxes) {
-                gp_load_x(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t.row + rank * t.half + lane * GP_BOX,
+                gp_load_x(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t->row + rank * half + lane * GP_BOX,
                           full0);
             }
             *(uint4 *)(sm + s * GP_STAGE + GP_OFF_XA + f * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -632,14 +665,18 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         __syncwarp();
     } else if (warp == GM_W_MMA) {
         // -------------------------------------------------------------- MMA
-        uint32_t ut = 0, phase = 0;
+        uint32_t phase = 0, slot = 0, it = 0;
         int s = 0;
-        bool ok = true, ready = false;
+        bool ready = false;
         const uint32_t lo = sw128_lo(sbase);
         constexpr uint32_t SD = GP_STAGE / 16;  // descriptor words between stages
-        for (int u = first; u < n_tiles && ok; u += step, ut++) {
+        for (uint32_t ut = 0;; ut++) {
             const int buf = (int)(ut & 1);
-            const uint32_t id = gm_idesc(2 * GM_M, 2 * gp_tile(tab, a, u).half, 0);
+            bool ok = tile_in(ut);
+            const GpTile *t = ring + ut % GP_RING;
+            if (!ok || t->e < 0) break;
+            const uint32_t id = gm_idesc(2 * GM_M, 2 * t->half, 0);
+            tile_out(ut);
             // the epilogue frees the columns that a tile's accumulator shares with the next
             if (ut >= 1) {
                 const uint32_t p = ut - 1;
@@ -647,7 +684,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                     break;
             }
             tc_fence_after();
-            for (int ks = 0; ks < a.nks; ks++) {
+            for (int ks = 0; ks < a.nks; ks++, it++) {
                 if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
@@ -657,12 +694,20 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // look at the next stage while this one is issued
                 ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
+                // The products that read this slot of scales before have completed: the
+                // next stage could only be filled behind them.  Where it is not yet, wait.
+                if (!ready && it >= (uint32_t)GP_SLOTS &&
+                    !__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + sn), ((it - GP_SLOTS) / NS) & 1, a.err, abort_flag))) {
+                    ok = false;
+                    break;
+                }
                 const uint32_t d = lo + (uint32_t)s * SD;
                 gp_step(tmem + (uint32_t)(buf * GP_OVER), d, d + GP_OFF_X / 16, d + GP_OFF_WA / 16,
-                        tmem + (uint32_t)(GP_SF0 + GP_SF * s), ks ? 1u : 0u, id);
+                        tmem + (uint32_t)GP_SF0 + slot, ks ? 1u : 0u, id);
                 pair_commit(bar(B_EMPTY + s));
                 s = sn;
                 phase = pn;
+                slot = slot + GP_SF == GP_SF * GP_SLOTS ? 0 : slot + GP_SF;
             }
             if (!ok) break;
             pair_commit(bar(B_ACCF + buf));
@@ -674,30 +719,33 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     } else if (warp >= GM_W_EPI) {
         // --------------------------------------------------------- epilogue
         // A lane holds one weight row n, 32 columns (rows of C) at a time; the two warps
-        // of a quadrant take alternate pieces, those in the columns shared with the
-        // other accumulator first.
+        // of a quadrant take alternate pieces, first the one each in the columns shared
+        // with the other accumulator (the first one's last, the second one's first).
         const int q = warp & 3, other = (warp - GM_W_EPI) >> 2;
-        constexpr int PIECES = GP_NT / 32, OVER = GP_OVER / 32, SHARED = PIECES - OVER;
-        uint32_t ut = 0;
-        for (int u = first; u < n_tiles; u += step, ut++) {
+        constexpr int PIECES = GP_NT / 32, OVER = GP_OVER / 32;
+        static_assert(PIECES - OVER == 2, "a shared piece for each warp of a quadrant");
+        for (uint32_t ut = 0;; ut++) {
             const int buf = (int)(ut & 1);
-            const GpTile t = gp_tile(tab, a, u);
+            if (!tile_in(ut)) break;
+            const GpTile *t = ring + ut % GP_RING;
+            const int e = t->e, row = t->row, rows = t->rows, n = t->n0 + rank * GM_M + q * 32 + lane;
+            if (e < 0) break;
+            tile_out(ut);
             if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * GP_OVER);
-            const int n = t.n0 + rank * GM_M + q * 32 + lane;
 #pragma unroll 1
             for (int i = other; i < PIECES; i += 2) {
                 const int j = buf ? i : (i + OVER) % PIECES;
-                const bool on = j * 32 < t.rows;
+                const bool on = j * 32 < rows;
                 uint32_t r[32];
                 if (on) tmem_ld_chunk(tacc + (uint32_t)(j * 32), r);
-                if (i + 2 >= SHARED && i < SHARED) {  // this warp's last shared piece
+                if (i == other) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_rank(bar(B_ACCE + buf), 0);
                 }
-                if (on) gm_put<CT, 32>(a, (CT *)a.C + (long)(t.row + j * 32) * a.ldc + n, n, t.rows - j * 32, r);
+                if (on) gm_put<CT, 32>(a, (CT *)a.C + (long)(row + j * 32) * a.ldc + n, n, rows - j * 32, r);
             }
         }
     }
