@@ -815,14 +815,36 @@ int launch_gp(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, GmArgs a, cuda
     }
     return K3MOE_OK;
 }
+// The form by the time it would take: for every wave of tiles over the SMs (or pairs of
+// them) a time per step and one per tile.  An expert with `avg` rows makes about avg /
+// height + 1/2 tiles.  Measured on 64 experts, in us, with 16, 32 and 64 rows and pairs:
+//   1536 x 7168, 8 rows an expert 80 82 86 104, 16 rows 104 83 86 105, 32 rows 163 107 90
+//   107, 64 rows 285 170 120 110, 192 rows 771 420 266 152;
+//   7168 x 1536, 8 rows 82 80 83 101, 32 rows 175 113 98 103, 64 rows 317 187 145 109.
+// (Single tiles of 128 rows never won: 114, 203 and 164 us at the last three sizes but
+// one, and 16 to 35% behind pairs from 128 rows on.)
 template <typename CT>
 int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &a, cudaStream_t s)
 {
-    const int avg = (a.slots + a.E - 1) / a.E;
-    return avg <= 12   ? launch_gm<16, CT>(A, W, a, s)
-           : avg <= 24 ? launch_gm<32, CT>(A, W, a, s)
-           : avg <= 48 ? launch_gm<64, CT>(A, W, a, s)
-           : avg <= 96 ? launch_gm<128, CT>(A, W, a, s)
+    const long hit = std::min(a.E, a.slots), sms = num_sms();
+    const struct {
+        int rows, step, tile;  // of a tile; ns
+        long columns, at_once;
+    } forms[4] = {{16, 236, 500, a.tiles_n, sms},
+                  {32, 240, 600, a.tiles_n, sms},
+                  {64, 255, 1300, a.tiles_n, sms},
+                  {GP_NT, 290, 1500, (a.N + 2L * GM_M - 1) / (2 * GM_M), std::max(1L, sms / 2)}};
+    int best = 0;
+    long cost = 0;
+    for (int i = 0; i < 4; i++) {
+        const long half_tiles = std::max(2 * hit, 2 * (long)a.slots / forms[i].rows + hit);
+        const long waves = (half_tiles * forms[i].columns + 2 * forms[i].at_once - 1) / (2 * forms[i].at_once);
+        const long c = waves * ((long)forms[i].step * a.nks + forms[i].tile);
+        if (!cost || c < cost) cost = c, best = i;
+    }
+    return best == 0   ? launch_gm<16, CT>(A, W, a, s)
+           : best == 1 ? launch_gm<32, CT>(A, W, a, s)
+           : best == 2 ? launch_gm<64, CT>(A, W, a, s)
                        : launch_gp<CT>(A, W, a, s);
 }
 
