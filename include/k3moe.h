@@ -790,23 +790,27 @@ int k3moe_norm_backward(void *dx, int64_t lddx, float *dgain, int32_t accumulate
  *            id outside 0 .. E - 1)
  * "Rows in group order" below are rows whose index is a place.  1 <= E <= 1024,
  * 1 <= top_k <= 32, 1 <= tokens, tokens * top_k <= 2^30.  An expert may be named twice
- * by a token.  The caller owns the three arrays.
+ * by a token.  The caller owns the three arrays and
+ *   workspace  device, workspace_bytes >= k3moe_groups_workspace(E, tokens * top_k) (0 if
+ *            invalid), 16-byte aligned, zeroed once by the caller before its first use and
+ *            left zero at the places that count; the plan and the grouped product use it,
+ *            so it is not shared by calls that may overlap.  One for the most tokens
+ *            serves plans of fewer
  */
 typedef struct {
     int32_t *offsets;
     int32_t *order;
     int32_t *pos;
+    void *workspace;
+    size_t workspace_bytes;
     int32_t E;
     int32_t top_k;
     int32_t tokens;
 } k3moe_groups;
 
-/* Fills a plan from ids int32 [tokens][top_k].  workspace: device,
- * k3moe_groups_workspace(E, tokens * top_k) bytes (0 if invalid), 16-byte aligned, not
- * shared by calls that may overlap.  Errors: K3MOE_EINVAL. */
+/* Fills a plan from ids int32 [tokens][top_k].  Errors: K3MOE_EINVAL. */
 size_t k3moe_groups_workspace(int32_t E, int64_t slots);
-int k3moe_groups_plan(const k3moe_groups *host_g, const int32_t *ids, void *workspace, size_t workspace_bytes,
-                      k3moe_stream s);
+int k3moe_groups_plan(const k3moe_groups *host_g, const int32_t *ids, k3moe_stream s);
 
 /*
  * The matrices [rows][in] of E experts as operands of the grouped product: expert e's

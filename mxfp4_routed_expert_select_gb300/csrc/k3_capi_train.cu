@@ -38,7 +38,7 @@ int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, cons
                          long lddr, const void *r, long ldr, const float *rstd, const float *gain, int dtype, int T,
                          int n, void *ws, cudaStream_t s);
 size_t groups_workspace_bytes(int E, long slots);
-int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, cudaStream_t s);
+int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, cudaStream_t s);
 int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
                           const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s);
 int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const void *X, long ldx, int xrows, int N, int K,
@@ -81,7 +81,8 @@ bool valid_groups(const k3moe_groups *g)
 {
     return g && g->offsets && g->order && g->pos && aligned(g->offsets, 4) && aligned(g->order, 4) && aligned(g->pos, 4) &&
            g->E >= 1 && g->E <= 1024 && g->top_k >= 1 && g->top_k <= 32 && g->tokens >= 1 &&
-           (int64_t)g->tokens * g->top_k <= kMaxDim;
+           (int64_t)g->tokens * g->top_k <= kMaxDim && g->workspace && aligned(g->workspace, 16) &&
+           g->workspace_bytes >= k3moe_groups_workspace(g->E, (int64_t)g->tokens * g->top_k);
 }
 // Two row matrices of a call that may be one: the same rows then.
 bool apart_or_same(const void *p, int64_t ldp, const void *q, int64_t ldq, int32_t T) { return p != q || T == 1 || ldp == ldq; }
@@ -305,12 +306,10 @@ size_t k3moe_groups_workspace(int32_t E, int64_t slots)
     return E < 1 || E > 1024 || slots < 1 || slots > kMaxDim ? 0 : k3::groups_workspace_bytes(E, (long)slots);
 }
 
-int k3moe_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, size_t ws_bytes, k3moe_stream s)
+int k3moe_groups_plan(const k3moe_groups *g, const int32_t *ids, k3moe_stream s)
 {
-    if (!valid_groups(g) || !ids || !aligned(ids, 4) || !ws || !aligned(ws, 16) ||
-        ws_bytes < k3moe_groups_workspace(g->E, (int64_t)g->tokens * g->top_k))
-        return K3MOE_EINVAL;
-    return writing(s, [&] { return k3::launch_groups_plan(g, ids, ws, cs(s)); });
+    if (!valid_groups(g) || !ids || !aligned(ids, 4)) return K3MOE_EINVAL;
+    return writing(s, [&] { return k3::launch_groups_plan(g, ids, cs(s)); });
 }
 
 int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,

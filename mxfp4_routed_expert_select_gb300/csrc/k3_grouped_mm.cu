@@ -39,6 +39,7 @@ namespace {
 constexpr int GM_M = 128;  // weight rows of a tile
 constexpr int GM_W_MMA = 0, GM_W_EPI = 4, GM_W_FILL = 8;
 constexpr int GM_MAX_E = 1024;
+constexpr int GM_CTAS = 192, GM_MAX_NT = 64;  // the workspace has sums of that many CTAs' columns
 
 struct GmArgs {
     const uint8_t *atoms;      // scale atoms of the weights, atoms_stride bytes from expert to expert
@@ -48,6 +49,8 @@ struct GmArgs {
     const int32_t *offsets, *order;
     int E, top_k, slots, gather, xrows;  // xrows: rows of the 8-bit matrix
     int N, nks, nka, tiles_n;  // nks: steps of 128 along K; nka: atoms per row tile
+    float *parts;              // sums of parts of tiles, [CTA][columns][128]
+    int32_t *counts;           // parts of a tile that are done
     void *C;
     long ldc;
     int accumulate, pairs;     // pairs: two columns of a bf16 C form an aligned word
@@ -165,6 +168,24 @@ K3_DEV GmTile gm_tile(const GmTable &tab, const GmArgs &a, int u)
     t.n0 = (u - r * a.tiles_n) * GM_M;
     return t;
 }
+// What a CTA works on as its i-th piece: whole tiles in turn over the CTAs, as many as
+// make full waves, and of the tiles that are left a part along K, several CTAs to a tile
+// where there are enough (1 token x 16 experts x 1536 x 7168, 192 tiles on 152 SMs: %s
+// us against %s).  slot: where a part leaves its sums; u < 0: nothing more.
+struct GmPart {
+    int u, k0, k1, of, slot;
+};
+constexpr int GM_MAX_PARTS = 8, GM_JOIN_STEPS = 16;  // joining parts takes as long as so many steps
+K3_DEV GmPart gm_part(const GmArgs &a, int n_tiles, int i)
+{
+    const int ctas = (int)gridDim.x, me = (int)blockIdx.x, whole = n_tiles / ctas, left = n_tiles - whole * ctas;
+    if (i < whole) return {i * ctas + me, 0, a.nks, 1, 0};
+    int of = left ? min(ctas / left, GM_MAX_PARTS) : 1;
+    if (a.nks - a.nks / of < GM_JOIN_STEPS) of = 1;
+    if (i > whole || me >= left * of) return {-1, 0, 0, 1, 0};
+    const int p = me % of;
+    return {whole * ctas + me / of, a.nks * p / of, a.nks * (p + 1) / of, of, me};
+}
 // Row of the 8-bit matrix behind row i of C (0 should the order name none).
 K3_DEV int gm_source(const GmArgs &a, int i)
 {
@@ -269,30 +290,45 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
     griddep_wait();
     gm_table(tab, a, NT);
-    const int n_tiles = tab.before[a.E] * a.tiles_n, first = (int)blockIdx.x, step = (int)gridDim.x;
+    const int n_tiles = tab.before[a.E] * a.tiles_n;
 
     if (warp >= GM_W_FILL) {
         // -------------------------------------------------- a stage's filler
-        // Every NS-th step of this CTA's tiles.  Lanes 8 q .. 8 q + 7 copy the 16-byte
+        // Every NS-th step of this CTA's parts.  Lanes 8 q .. 8 q + 7 copy the 16-byte
         // chunks of rows q, q + 4, ..; a lane has the scale words of rows lane, lane +
-        // 32, ... of the tile, loaded a turn ahead.  Columns past the group keep what
-        // the stage held (they are not stored).
+        // 32, ... of the tile.  Columns past the group keep what the stage held (they are
+        // not stored).
         constexpr int J = (NT + 31) / 32, R = NT / 4;
         const int s = warp - GM_W_FILL;
         const uint32_t st = sbase + (uint32_t)(s * C::STAGE), full = bar(B_FULL + s);
         uint32_t turn = 0;
-        int u = first, ks = s, tile = -1;
+        int i = 0, tile = -1;
+        GmPart part = gm_part(a, n_tiles, 0);
+        int ks = part.k0 + s;
         GmTile t = {};
         const uint8_t *atoms = nullptr, *sp[J];
         int src[R];
         uint32_t w[J];
         for (;; ks += NS, turn++) {
-            while (ks >= a.nks) ks -= a.nks, u += step;
-            if (u >= n_tiles) break;
-            if (u != tile) {
-                tile = u;
-                t = gm_tile<NT>(tab, a, u);
+            while (part.u >= 0 && ks >= part.k1) {
+                const int over = ks - part.k1;
+                part = gm_part(a, n_tiles, ++i);
+                ks = part.k0 + over;
+            }
+            if (part.u < 0) break;
+            const bool entered = i != tile;
+            if (entered) {
+                tile = i;
+                t = gm_tile<NT>(tab, a, part.u);
                 atoms = a.atoms + (long)t.e * a.atoms_stride + (long)(t.n0 / 128) * a.nka * 512;
+            }
+            // before its first completion an EMPTY barrier's odd phase counts as passed
+            if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
+            // the weights first: they have the longest way
+            if (lane == 0) mbar_arrive_expect_tx(full, C::TX_W + (a.gather ? 0 : C::TX_X));
+            __syncwarp();
+            gm_load_w(st, &wmap, ks * 128, t.n0, t.e, st + C::OFF_WA, atoms + (long)ks * 512, full);
+            if (entered) {
 #pragma unroll
                 for (int j = 0; j < J; j++)
                     sp[j] = lane + 32 * j < t.rows ? a.scales + (long)gm_source(a, t.row + lane + 32 * j) * a.sstride : nullptr;
@@ -305,11 +341,6 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
             }
 #pragma unroll
             for (int j = 0; j < J; j++) w[j] = sp[j] ? *(const uint32_t *)(sp[j] + 4 * ks) : 0u;
-            // before its first completion an EMPTY barrier's odd phase counts as passed
-            if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, C::TX_W + (a.gather ? 0 : C::TX_X));
-            __syncwarp();
-            gm_load_w(st, &wmap, ks * 128, t.n0, t.e, st + C::OFF_WA, atoms + (long)ks * 512, full);
             if (a.gather) {
                 const uint8_t *base = a.codes + (long)ks * 128 + (lane & 7) * 16;
 #pragma unroll
@@ -339,12 +370,14 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
         bool ok = true;
         const uint32_t lo = sw128_lo(sbase);
         constexpr uint32_t SD = C::STAGE / 16;  // descriptor words between stages
-        for (int u = first; u < n_tiles && ok; u += step, ut++) {
+        for (;; ut++) {
+            const GmPart part = gm_part(a, n_tiles, (int)ut);
+            if (part.u < 0) break;
             const int buf = (int)(ut & 1);
             if (ut >= 2 && !__all_sync(0xffffffffu, tc_wait(bar(B_ACCE + buf), (ut / 2 - 1) & 1, a.err, abort_flag)))
                 break;
             tc_fence_after();
-            for (int ks = 0; ks < a.nks; ks++) {
+            for (int ks = part.k0; ks < part.k1; ks++) {
                 if (!__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
@@ -352,7 +385,7 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
                 tc_fence_after();
                 const uint32_t d = lo + (uint32_t)s * SD;
                 gm_step<NT>(tmem + (uint32_t)(buf * NT), d, d + C::OFF_X / 16, d + C::OFF_WA / 16,
-                            tmem + (uint32_t)(C::SF0 + C::SF * s), ks ? 1u : 0u);
+                            tmem + (uint32_t)(C::SF0 + C::SF * s), ks > part.k0 ? 1u : 0u);
                 mma_commit(bar(B_EMPTY + s));
                 if (++s == NS) s = 0, phase ^= 1u;
             }
@@ -367,14 +400,16 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
         // --------------------------------------------------------- epilogue
         const int q = warp - GM_W_EPI;  // TMEM lane quadrant: weight rows 32 q .. 32 q + 31 of the tile
         constexpr int CH = NT < 32 ? 16 : 32, NCH = NT / CH;
-        uint32_t ut = 0;
-        for (int u = first; u < n_tiles; u += step, ut++) {
+        for (uint32_t ut = 0;; ut++) {
+            const GmPart part = gm_part(a, n_tiles, (int)ut);
+            if (part.u < 0) break;
             const int buf = (int)(ut & 1);
-            const GmTile t = gm_tile<NT>(tab, a, u);
+            const GmTile t = gm_tile<NT>(tab, a, part.u);
             if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
             tc_fence_after();
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT);
-            const int n = t.n0 + q * 32 + lane;
+            const int n = t.n0 + q * 32 + lane, cols = min(t.rows, NT);
+            float *const mine = a.parts + ((long)part.slot * NT) * GM_M + q * 32 + lane;  // [column][128]
 #pragma unroll 1
             for (int j = 0; j < NCH; j++) {
                 uint32_t r[CH];
@@ -384,8 +419,38 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
                 }
+                if (part.of == 1) {
+                    gm_put<CT, CH>(a, (CT *)a.C + (long)(t.row + j * CH) * a.ldc + n, n, t.rows - j * CH, r);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CH; c++)
+                        if (j * CH + c < cols) __stcg(mine + (long)(j * CH + c) * GM_M, __uint_as_float(r[c]));
+                }
+            }
+            if (part.of == 1) continue;
+            // A part of a tile: the CTA that is last to leave its sums adds all parts up,
+            // in their order, and leaves the count at zero.
+            __threadfence();
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (threadIdx.x == GM_W_EPI * 32) tab.sums[0] = atomicAdd(a.counts + part.slot / part.of, 1) == part.of - 1;
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if (!tab.sums[0]) continue;
+            __threadfence();
+            const float *all = a.parts + ((long)(part.slot - part.slot % part.of) * NT) * GM_M + q * 32 + lane;
+#pragma unroll 1
+            for (int j = 0; j < NCH && j * CH < cols; j++) {
+                uint32_t r[CH];
+#pragma unroll
+                for (int c = 0; c < CH; c++) r[c] = 0u;
+#pragma unroll 1
+                for (int p = 0; p < part.of; p++)
+#pragma unroll
+                    for (int c = 0; c < CH; c++)
+                        if (j * CH + c < cols)
+                            r[c] = __float_as_uint(__uint_as_float(r[c]) + __ldcg(all + ((long)p * NT + j * CH + c) * GM_M));
                 gm_put<CT, CH>(a, (CT *)a.C + (long)(t.row + j * CH) * a.ldc + n, n, t.rows - j * CH, r);
             }
+            if (threadIdx.x == GM_W_EPI * 32) a.counts[part.slot / part.of] = 0;
         }
     }
     tc_fence_before();
@@ -784,8 +849,8 @@ int launch_gm(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &
     if (st == K3MOE_OK) st = row8_map(&xmap, A, NT);
     if (st != K3MOE_OK) return st;
     if (ensure_smem((const void *)k3_grouped_matmul<NT, CT>, C::SMEM) != K3MOE_OK) return K3MOE_ECUDA;
-    const long most = std::min<long>(a.slots, (long)a.E + a.slots / NT) * a.tiles_n;  // tiles there can be
-    if (launch_pdl(k3_grouped_matmul<NT, CT>, dim3((unsigned)std::min<long>(most, num_sms())), dim3(C::THREADS), C::SMEM, s,
+    // as many CTAs as there are SMs and places for parts of tiles
+    if (launch_pdl(k3_grouped_matmul<NT, CT>, dim3((unsigned)std::min(num_sms(), GM_CTAS)), dim3(C::THREADS), C::SMEM, s,
                    wmap, xmap, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
@@ -850,6 +915,10 @@ int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArg
 
 }  // namespace
 
+// The workspace: a count for each tile that has parts (zero between calls), and the sums
+// of parts of tiles.
+size_t grouped_matmul_workspace_bytes() { return GM_CTAS * (sizeof(float) * GM_M * GM_MAX_NT + sizeof(int32_t)); }
+
 int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
                           const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s)
 {
@@ -859,6 +928,8 @@ int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, c
     a.offsets = g->offsets, a.order = g->order;
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = A->rows;
     a.N = W->rows, a.nks = W->in / 128, a.nka = op_k_atoms(W->in), a.tiles_n = (W->rows + GM_M - 1) / GM_M;
+    a.counts = (int32_t *)g->workspace;
+    a.parts = (float *)(a.counts + GM_CTAS);
     a.C = C, a.ldc = ldc, a.accumulate = accumulate, a.err = err;
     a.pairs = cdt == K3MOE_BF16 && a.N % 2 == 0 && ldc % 2 == 0 && ((uintptr_t)C & 3u) == 0;
     if (((long)a.E + a.slots) * a.tiles_n > 0x7fffffffL) return K3MOE_EINVAL;

@@ -17,6 +17,7 @@
 #include "k3_launch.cuh"
 
 namespace k3 {
+size_t grouped_matmul_workspace_bytes();
 namespace {
 
 constexpr int GR_THREADS = 1024, GR_WARPS = GR_THREADS / 32;
@@ -294,14 +295,16 @@ int launch(void (*kernel)(KArgs...), long grid, int threads, size_t smem, cudaSt
 
 }  // namespace
 
+// The workspace: the grouped product's part, then the counts of the chunks.
 size_t groups_workspace_bytes(int E, long slots)
 {
-    return slots <= GR_WHOLE ? 16 : (size_t)((slots + GR_CHUNK - 1) / GR_CHUNK) * E * sizeof(int32_t);
+    const size_t chunks = slots <= GR_WHOLE ? 0 : (size_t)((slots + GR_CHUNK - 1) / GR_CHUNK);
+    return grouped_matmul_workspace_bytes() + chunks * (size_t)E * sizeof(int32_t);
 }
 
-int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, void *ws, cudaStream_t s)
+int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, cudaStream_t s)
 {
-    GroupArgs a = {ids, g->offsets, g->order, g->pos, (int32_t *)ws, g->tokens * g->top_k, g->E, 0};
+    GroupArgs a = {ids, g->offsets, g->order, g->pos, (int32_t *)((char *)g->workspace + grouped_matmul_workspace_bytes()), g->tokens * g->top_k, g->E, 0};
     a.chunks = (a.S + GR_CHUNK - 1) / GR_CHUNK;
     const size_t smem = (size_t)GR_WARPS * a.E * sizeof(uint16_t);
     if (a.S <= GR_WHOLE) return launch(k3_groups<true, false>, 1, GR_THREADS, smem, s, a);

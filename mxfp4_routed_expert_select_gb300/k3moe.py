@@ -105,6 +105,7 @@ class Mx8RowsStruct(ctypes.Structure):
 
 class GroupsStruct(ctypes.Structure):
     _fields_ = [("offsets", ctypes.c_void_p), ("order", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("E", ctypes.c_int32), ("top_k", ctypes.c_int32), ("tokens", ctypes.c_int32)]
 
 
@@ -180,7 +181,7 @@ SIGNATURES = {
     "k3moe_norm_backward": (ctypes.c_int, [_P, _I64, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I, _I, _I, _P, _SZ,
                                            _P]),
     "k3moe_groups_workspace": (_SZ, [_I, _I64]),
-    "k3moe_groups_plan": (ctypes.c_int, [_P, _P, _P, _SZ, _P]),
+    "k3moe_groups_plan": (ctypes.c_int, [_P, _P, _P]),
     "k3moe_grouped_matmul": (ctypes.c_int, [_P, _I, _I64, _P, _P, _P, _I, _I, _P]),
     "k3moe_grouped_wgrad": (ctypes.c_int, [_P, _I, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _I, _P]),
     "k3moe_combine": (ctypes.c_int, [_P, _I64, _P, _I64, _I, _I, _P, _P, _I, _P]),
@@ -623,11 +624,11 @@ class ExpertGroups:
         self.offsets = torch.empty(E + 1, dtype=torch.int32, device=device)
         self._order = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
         self._pos = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
-        self.workspace = torch.empty(nb, dtype=torch.uint8, device=device)
-        self._ws = self.workspace.data_ptr(), nb
+        self.workspace = torch.zeros(nb, dtype=torch.uint8, device=device)
         self._i32 = torch.int32
         self.gpu = _gpu(self.offsets)
-        self.struct = GroupsStruct(self.offsets.data_ptr(), self._order.data_ptr(), self._pos.data_ptr(), E, top_k, 0)
+        self.struct = GroupsStruct(self.offsets.data_ptr(), self._order.data_ptr(), self._pos.data_ptr(),
+                                   self.workspace.data_ptr(), nb, E, top_k, 0)
         self.ref = ctypes.byref(self.struct)
         self.tokens = self.slots = 0
 
@@ -648,7 +649,7 @@ class ExpertGroups:
             raise ValueError("expected 1 to %d tokens, got %d" % (self.max_tokens, T))
         p = _flat(ids, self._i32, T, self.k)
         self.struct.tokens = T
-        st = (_lib or lib()).k3moe_groups_plan(self.ref, p, *self._ws, _stream(stream))
+        st = (_lib or lib()).k3moe_groups_plan(self.ref, p, _stream(stream))
         if st:
             self.struct.tokens = self.tokens
             check(st, "k3moe_groups_plan")
