@@ -35,7 +35,7 @@ constexpr int GW_NS = 4;
 constexpr int GW_W_MMA = 0, GW_W_EPI = 4;
 constexpr int GW_EPI = 8;  // epilogue warps: two per TMEM lane quadrant, on alternate pieces
 constexpr int GW_W_FILL = GW_W_EPI + GW_EPI;
-constexpr int GW_FILL = 2;  // warps that fill a stage, half of its rows each
+constexpr int GW_FILL = 4;  // warps that fill a stage, a quarter of its rows each
 constexpr int GW_THREADS = (GW_W_FILL + GW_FILL * GW_NS) * 32;
 
 struct GwArgs {
@@ -55,22 +55,25 @@ constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * GW_B
 constexpr int GW_BARS = 2 * GW_NS + 2 * 2 + 1;
 constexpr int GW_SMEM = 1024 + GW_OFF_BAR + 256;
 static_assert(GW_SMEM <= 232448, "shared memory");
+static_assert(GW_K / GW_FILL == 16, "a share is the rows of an MMA");
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both M/N-major.
 constexpr uint32_t GW_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(GW_N >> 3) << 17) |
                               ((uint32_t)(GW_M >> 4) << 24);
 
-// A step: four MMAs of 16 rows.  Descriptors of M/N-major tiles: panels of 64 columns
-// GW_PANEL bytes apart (leading offset), groups of eight rows 1024 bytes (stride).
-K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc)
+// A step: an MMA for each 16 rows, one to four.  Descriptors of M/N-major tiles: panels
+// of 64 columns GW_PANEL bytes apart (leading offset), groups of eight rows 1024 bytes
+// (stride).
+K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc, int mmas)
 {
-#define GW_MMA(k2, pred)                                                                                     \
+#define GW_MMA(k2, pred, on)                                                                                 \
     "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %4};\n\tmov.b64 db, {y, %4};\n\t" \
-    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, " pred ";\n\t"
-    asm volatile("{\n\t.reg .pred p, t, e;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\t" GW_MMA(0, "p") GW_MMA(128, "t") GW_MMA(256, "t")
-                     GW_MMA(384, "t") "}" ::"r"(tacc),
-                 "r"(ylo), "r"(xlo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC)
+    "@" on " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, " pred ";\n\t"
+    asm volatile("{\n\t.reg .pred p, t, e, f, g, h;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\tsetp.gt.and.s32 f, %6, 1, e;\n\t"
+                 "setp.gt.and.s32 g, %6, 2, e;\n\tsetp.gt.and.s32 h, %6, 3, e;\n\t" GW_MMA(0, "p", "e") GW_MMA(128, "t", "f")
+                     GW_MMA(256, "t", "g") GW_MMA(384, "t", "h") "}" ::"r"(tacc),
+                 "r"(ylo), "r"(xlo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC), "r"(mmas)
                  : "memory");
 #undef GW_MMA
 }
@@ -171,9 +174,9 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
 
     if (warp >= GW_W_FILL) {
         // -------------------------------------------------- a stage's fillers
-        // Every NS-th step of this CTA's tiles; the GW_FILL warps of a stage have
-        // half of its rows each, the first one issues the TMA copies.
-        const int s = (warp - GW_W_FILL) / GW_FILL, half = (warp - GW_W_FILL) % GW_FILL;
+        // Every NS-th step of this CTA's tiles; the GW_FILL warps of a stage have a
+        // share of its rows each, the first one issues the TMA copies.
+        const int s = (warp - GW_W_FILL) / GW_FILL, share = (warp - GW_W_FILL) % GW_FILL;
         constexpr int ROWS = GW_K / GW_FILL;
         const uint32_t st = sbase + (uint32_t)(s * GW_STAGE), full = bar(B_FULL + s);
         uint32_t turn = 0;
@@ -187,37 +190,39 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
             }
             if (u >= n_tiles) break;
             const int n = min(GW_K, t.rows - r0);  // rows of the group in this step
-            // lane l: X's row of the half's row l
+            const int n16 = (n + 15) & ~15;        // rows that its MMAs read
+            // lane l: X's row of the share's row l
             int src = 0;
-            if (a.gather && half * ROWS + lane < n) {
-                src = a.order[t.row + r0 + half * ROWS + lane] / a.top_k;
+            if (a.gather && lane < ROWS && share * ROWS + lane < n) {
+                src = a.order[t.row + r0 + share * ROWS + lane] / a.top_k;
                 if (src < 0 || src >= a.xrows) src = 0;
             }
             // before its first completion an EMPTY barrier's odd phase counts as passed
             if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
-            const bool whole = n == GW_K;
-            // whole steps: dY (and X in group order) by TMA
-            if (half == 0 && whole && lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_OFF_X : GW_STAGE));
-            __syncwarp();
-            if (half == 0 && whole) {
+            const bool whole = n == n16;
+            // where no row past the group is read: dY (and X in group order) by TMA
+            if (share == 0 && whole) {
+                if (lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_OFF_X : GW_STAGE));
+                __syncwarp();
                 if (lane < GW_M / 64)
                     tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &ymap, t.n0 + 64 * lane, t.row + r0, full);
                 else if (!a.gather && lane < GW_M / 64 + GW_N / 64)
                     tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &xmap, t.k0 + 64 * (lane - GW_M / 64), t.row + r0, full);
+                __syncwarp();
             }
-            __syncwarp();
-            if (a.gather || !whole) {
+            if ((a.gather || !whole) && share * ROWS < n16) {
                 // A row of 128 + 256 columns is 16 + 32 chunks of 16 bytes: dY's by half a
                 // warp, two rows at a time, X's by a warp
                 if (!whole)
+#pragma unroll
                     for (int i = 0; i < ROWS; i += 2) {
-                        const int r = half * ROWS + i + (lane >> 4), c = lane & 15;
+                        const int r = share * ROWS + i + (lane >> 4), c = lane & 15;
                         gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy,
                                  t.n0 + 8 * c, a.N, r < n);
                     }
-#pragma unroll 8
+#pragma unroll
                 for (int i = 0; i < ROWS; i++) {
-                    const int r = half * ROWS + i;
+                    const int r = share * ROWS + i;
                     const long x = a.gather ? __shfl_sync(0xffffffffu, src, i) : t.row + r0 + min(r, n - 1);
                     gw_chunk(st + (uint32_t)(GW_OFF_X + (lane >> 3) * GW_PANEL), r, lane & 7, a.x + x * a.ldx, t.k0 + 8 * lane,
                              a.K, r < n);
@@ -236,7 +241,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
         // -------------------------------------------------------------- MMA
         uint32_t ut = 0, phase = 0;  // ut: tiles with rows
         int s = 0;
-        bool ok = true;
+        bool ok = true, ready = false;
         const uint32_t lo = mn_lo(sbase);
         for (int u = first; u < n_tiles && ok; u += step) {
             const GwTile t = gw_tile(a, u);
@@ -246,15 +251,20 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 break;
             tc_fence_after();
             for (int r0 = 0; r0 < t.rows; r0 += GW_K) {
-                if (!__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const int sn = s + 1 == NS ? 0 : s + 1;
+                const uint32_t pn = sn ? phase : phase ^ 1u;
+                // look at the next stage while this one is issued
+                ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
                 const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
-                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_X / 16, r0 ? 1u : 0u);
+                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_X / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
                 mma_commit(bar(B_EMPTY + s));
-                if (++s == NS) s = 0, phase ^= 1u;
+                s = sn;
+                phase = pn;
             }
             if (!ok) break;
             mma_commit(bar(B_ACCF + buf));
@@ -285,26 +295,23 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
             const int n = t.n0 + q * 32;
 #pragma unroll 1
             for (int j = half; j < NP; j += 2) {
-                uint32_t r[PC / 32][32];
-                if (t.rows) {
-#pragma unroll
-                    for (int h = 0; h < PC / 32; h++) tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r[h]);
-                    if (j + 2 >= NP) {  // this warp's last piece
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
-                    }
-                } else {
-#pragma unroll
-                    for (int h = 0; h < PC / 32; h++)
-#pragma unroll
-                        for (int c = 0; c < 32; c++) r[h][c] = 0u;
-                }
                 // the piece staged before has been read
                 if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
                 __syncwarp();
 #pragma unroll
                 for (int h = 0; h < PC / 32; h++) {
+                    uint32_t r[32];
+                    if (t.rows) {
+                        tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r);
+                        if (j + 2 >= NP && h == PC / 32 - 1) {  // this warp's last columns
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
+                        }
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c++) r[c] = 0u;
+                    }
                     constexpr int W = 32 * (int)sizeof(CT) / 16;  // 16-byte chunks of 32 columns
 #pragma unroll
                     for (int c = 0; c < W; c++) {
@@ -313,13 +320,13 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                             uint32_t w[4];
 #pragma unroll
                             for (int x = 0; x < 4; x++) {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[h][8 * c + 2 * x]),
-                                                                               __uint_as_float(r[h][8 * c + 2 * x + 1]));
+                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[8 * c + 2 * x]),
+                                                                               __uint_as_float(r[8 * c + 2 * x + 1]));
                                 w[x] = *(const uint32_t *)&p;
                             }
                             v = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
-                            v = make_uint4(r[h][4 * c], r[h][4 * c + 1], r[h][4 * c + 2], r[h][4 * c + 3]);
+                            v = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
                         }
                         *(uint4 *)(box + lane * 128 + (((h * W + c) ^ (lane & 7)) << 4)) = v;
                     }
