@@ -6,13 +6,16 @@
 // lie in memory (M- and N-major tiles, the 128-byte swizzle over 64 columns of a row)
 // and nothing is transposed.
 //
-// A persistent CTA walks (expert, 128 n, 256 k) tiles; a step is 64 rows of the group.
-// Roles: warp 0 issues MMAs, warps 4 to 11 read one accumulator out by TMA stores while
-// the other one's products run, and each further warp fills one stage of 64 rows: dY's
-// columns by TMA, X's by TMA too where it lies in group order, else row by row with
-// asynchronous copies into the same swizzled form; in a group's last step the rows past
-// it are made zeros in both.  (TMA gathers of four rows take 72 clocks each: 64 experts x
-// 1536 x 7168 from 16384 rows took 2.06 ms with them.)
+// X's columns k take the MMA's 128 lanes and dY's columns n its 256 columns, so that the
+// matrix whose rows may have to be gathered is the smaller part of a step (with n in the
+// lanes 16 x 2048 x 2048 from 131072 gathered rows took 1029 us instead of 765).
+//
+// A persistent CTA walks (expert, 128 k, 256 n) tiles; a step is 64 rows of the group.
+// Roles: warp 0 issues MMAs, warps 4 to 11 read one accumulator out while the other one's
+// products run, and each further warp fills a share of a stage of 64 rows: dY's columns by
+// TMA, X's by TMA too where it lies in group order, else row by row with asynchronous
+// copies into the same swizzled form; in a group's last step rows past it are made zeros
+// in both.  (TMA gathers of four rows take 72 clocks each: 2.06 ms with them.)
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -30,7 +33,7 @@
 namespace k3 {
 namespace {
 
-constexpr int GW_M = 128, GW_N = 256, GW_K = 64;  // n and k of a tile, rows of a step
+constexpr int GW_M = 128, GW_N = 256, GW_K = 64;  // k and n of a tile, rows of a step
 constexpr int GW_NS = 4;
 constexpr int GW_W_MMA = 0, GW_W_EPI = 4;
 constexpr int GW_EPI = 8;  // epilogue warps: two per TMEM lane quadrant, on alternate pieces
@@ -41,17 +44,18 @@ constexpr int GW_THREADS = (GW_W_FILL + GW_FILL * GW_NS) * 32;
 struct GwArgs {
     const int32_t *offsets, *order;
     int E, top_k, slots, gather, xrows;
-    int tiles_k, tiles_e;  // k tiles of a row of tiles, tiles of an expert
+    FastDiv tiles_k, tiles_e;  // k tiles of a row of tiles, tiles of an expert
     int N, K, accumulate;
     const __nv_bfloat16 *dy, *x;
+    void *dw;
     long lddy, ldx;
     int *err;
 };
 
 constexpr int GW_PANEL = GW_K * 128;  // 64 rows of 64 columns
-constexpr int GW_OFF_X = GW_M / 64 * GW_PANEL, GW_STAGE = GW_OFF_X + GW_N / 64 * GW_PANEL;
-constexpr int GW_BOX = 4096;  // a staged piece of dW: 32 rows of 128 bytes
-constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * GW_BOX;
+constexpr int GW_OFF_Y = GW_M / 64 * GW_PANEL, GW_STAGE = GW_OFF_Y + GW_N / 64 * GW_PANEL;
+constexpr int GW_BOX = 16;  // rows n of a staged box of dW, 32 columns k wide; two boxes a warp
+constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * 2 * GW_BOX * 128;
 constexpr int GW_BARS = 2 * GW_NS + 2 * 2 + 1;
 constexpr int GW_SMEM = 1024 + GW_OFF_BAR + 256;
 static_assert(GW_SMEM <= 232448, "shared memory");
@@ -64,7 +68,7 @@ constexpr uint32_t GW_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | 
 // A step: an MMA for each 16 rows, one to four.  Descriptors of M/N-major tiles: panels
 // of 64 columns GW_PANEL bytes apart (leading offset), groups of eight rows 1024 bytes
 // (stride).
-K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc, int mmas)
+K3_DEV void gw_step(uint32_t tacc, uint32_t xlo, uint32_t ylo, uint32_t acc, int mmas)
 {
 #define GW_MMA(k2, pred, on)                                                                                 \
     "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %4};\n\tmov.b64 db, {y, %4};\n\t" \
@@ -73,7 +77,7 @@ K3_DEV void gw_step(uint32_t tacc, uint32_t ylo, uint32_t xlo, uint32_t acc, int
                  "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\tsetp.gt.and.s32 f, %6, 1, e;\n\t"
                  "setp.gt.and.s32 g, %6, 2, e;\n\tsetp.gt.and.s32 h, %6, 3, e;\n\t" GW_MMA(0, "p", "e") GW_MMA(128, "t", "f")
                      GW_MMA(256, "t", "g") GW_MMA(384, "t", "h") "}" ::"r"(tacc),
-                 "r"(ylo), "r"(xlo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC), "r"(mmas)
+                 "r"(xlo), "r"(ylo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC), "r"(mmas)
                  : "memory");
 #undef GW_MMA
 }
@@ -99,7 +103,23 @@ K3_DEV void mbar_expect(uint32_t bar, uint32_t bytes)
 {
     asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
-// A staged piece to (k, n) of expert e: stored, or added in fp32.
+// Tile u: its expert, n, k, and the group's rows.
+struct GwTile {
+    int e, n0, k0, row, rows;
+};
+K3_DEV GwTile gw_tile(const GwArgs &a, int u)
+{
+    GwTile t;
+    t.e = (int)a.tiles_e.div((uint32_t)u);
+    const int r = u - t.e * (int)a.tiles_e.d, rn = (int)a.tiles_k.div((uint32_t)r);
+    t.n0 = rn * GW_N;
+    t.k0 = (r - rn * (int)a.tiles_k.d) * GW_M;
+    t.row = max(a.offsets[t.e], 0);
+    t.rows = max(min(a.offsets[t.e + 1], a.slots) - t.row, 0);
+    return t;
+}
+
+// A staged box to (k, n) of expert e: stored, or added in fp32.
 K3_DEV void gw_store(const CUtensorMap *map, uint32_t src, int k, int n, int e, int accumulate)
 {
     if (accumulate)
@@ -112,22 +132,6 @@ K3_DEV void gw_store(const CUtensorMap *map, uint32_t src, int k, int n, int e, 
                          (uint64_t)map),
                      "r"(k), "r"(n), "r"(e), "r"(src)
                      : "memory");
-}
-
-// Tile u: its expert, n, k, and the group's rows.
-struct GwTile {
-    int e, n0, k0, row, rows;
-};
-K3_DEV GwTile gw_tile(const GwArgs &a, int u)
-{
-    GwTile t;
-    t.e = u / a.tiles_e;
-    const int r = u - t.e * a.tiles_e;
-    t.n0 = r / a.tiles_k * GW_M;
-    t.k0 = r % a.tiles_k * GW_N;
-    t.row = max(a.offsets[t.e], 0);
-    t.rows = max(min(a.offsets[t.e + 1], a.slots) - t.row, 0);
-    return t;
 }
 
 template <typename CT>
@@ -170,7 +174,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
     tc_fence_after();
     const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
     griddep_wait();
-    const int n_tiles = a.E * a.tiles_e, first = (int)blockIdx.x, step = (int)gridDim.x;
+    const int n_tiles = a.E * (int)a.tiles_e.d, first = (int)blockIdx.x, step = (int)gridDim.x;
 
     if (warp >= GW_W_FILL) {
         // -------------------------------------------------- a stage's fillers
@@ -202,31 +206,32 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
             const bool whole = n == n16;
             // where no row past the group is read: dY (and X in group order) by TMA
             if (share == 0 && whole) {
-                if (lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_OFF_X : GW_STAGE));
+                if (lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_STAGE - GW_OFF_Y : GW_STAGE));
                 __syncwarp();
-                if (lane < GW_M / 64)
-                    tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &ymap, t.n0 + 64 * lane, t.row + r0, full);
-                else if (!a.gather && lane < GW_M / 64 + GW_N / 64)
-                    tma_load_2d(st + (uint32_t)(lane * GW_PANEL), &xmap, t.k0 + 64 * (lane - GW_M / 64), t.row + r0, full);
+                if (lane < GW_N / 64)
+                    tma_load_2d(st + (uint32_t)(GW_OFF_Y + lane * GW_PANEL), &ymap, t.n0 + 64 * lane, t.row + r0, full);
+                else if (!a.gather && lane < GW_N / 64 + GW_M / 64)
+                    tma_load_2d(st + (uint32_t)((lane - GW_N / 64) * GW_PANEL), &xmap, t.k0 + 64 * (lane - GW_N / 64), t.row + r0,
+                                full);
                 __syncwarp();
             }
             if ((a.gather || !whole) && share * ROWS < n16) {
-                // A row of 128 + 256 columns is 16 + 32 chunks of 16 bytes: dY's by half a
-                // warp, two rows at a time, X's by a warp
+                // A row of 128 + 256 columns is 16 + 32 chunks of 16 bytes: X's by half a
+                // warp, two rows at a time, dY's by a warp
+#pragma unroll
+                for (int i = 0; i < ROWS; i += 2) {
+                    const int r = share * ROWS + i + (lane >> 4), c = lane & 15;
+                    const int g = __shfl_sync(0xffffffffu, src, i + (lane >> 4));
+                    const long x = a.gather ? g : t.row + r0 + min(r, n - 1);
+                    gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.x + x * a.ldx, t.k0 + 8 * c, a.K, r < n);
+                }
                 if (!whole)
 #pragma unroll
-                    for (int i = 0; i < ROWS; i += 2) {
-                        const int r = share * ROWS + i + (lane >> 4), c = lane & 15;
-                        gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy,
-                                 t.n0 + 8 * c, a.N, r < n);
+                    for (int i = 0; i < ROWS; i++) {
+                        const int r = share * ROWS + i;
+                        gw_chunk(st + (uint32_t)(GW_OFF_Y + (lane >> 3) * GW_PANEL), r, lane & 7,
+                                 a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy, t.n0 + 8 * lane, a.N, r < n);
                     }
-#pragma unroll
-                for (int i = 0; i < ROWS; i++) {
-                    const int r = share * ROWS + i;
-                    const long x = a.gather ? __shfl_sync(0xffffffffu, src, i) : t.row + r0 + min(r, n - 1);
-                    gw_chunk(st + (uint32_t)(GW_OFF_X + (lane >> 3) * GW_PANEL), r, lane & 7, a.x + x * a.ldx, t.k0 + 8 * lane,
-                             a.K, r < n);
-                }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_async_smem();
                 __syncwarp();
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 // look at the next stage while this one is issued
                 ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
                 const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
-                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_X / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
+                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_Y / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
                 mma_commit(bar(B_EMPTY + s));
                 s = sn;
                 phase = pn;
@@ -276,12 +281,16 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
         __syncwarp();
     } else if (warp >= GW_W_EPI) {
         // --------------------------------------------------------- epilogue
-        // A lane holds one row n.  A warp stages 32 rows of 128 bytes (16-byte chunk c
-        // of row r at chunk c ^ (r mod 8), as the 128-byte swizzle has it) and they
-        // leave by TMA, clipped at the expert's matrix.
+        // A lane holds one column k of dW, 32 rows n at a time; the two warps of a
+        // quadrant take alternate pieces.  Boxes of 16 rows leave by TMA, clipped at the
+        // expert's matrix, one being filled while the other is read.  (Stored from
+        // registers, 128 bytes of a row at a time, an SM's stores left at 18 bytes a clock:
+        // 64 x 1536 x 7168 from 16384 gathered rows took 664 us; with one box of 32 rows,
+        // waited for, 558.)
         const int q = warp & 3, half = (warp - GW_W_EPI) >> 2;
-        constexpr int PC = 128 / (int)sizeof(CT), NP = GW_N / PC;  // columns of a piece, pieces of a tile
-        uint8_t *box = sm + GW_OFF_C + (warp - GW_W_EPI) * GW_BOX;
+        constexpr int NP = GW_N / 32;
+        CT *const boxes = (CT *)(sm + GW_OFF_C + (warp - GW_W_EPI) * 2 * GW_BOX * 128);
+        uint32_t box = 0;
         uint32_t ut = 0;
         for (int u = first; u < n_tiles; u += step) {
             const GwTile t = gw_tile(a, u);
@@ -292,50 +301,41 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 tc_fence_after();
             }
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * GW_N);
-            const int n = t.n0 + q * 32;
+            const int k = t.k0 + q * 32 + lane;
 #pragma unroll 1
             for (int j = half; j < NP; j += 2) {
-                // the piece staged before has been read
-                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                __syncwarp();
-#pragma unroll
-                for (int h = 0; h < PC / 32; h++) {
-                    uint32_t r[32];
-                    if (t.rows) {
-                        tmem_ld_chunk(tacc + (uint32_t)(j * PC + 32 * h), r);
-                        if (j + 2 >= NP && h == PC / 32 - 1) {  // this warp's last columns
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
-                        }
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < 32; c++) r[c] = 0u;
+                uint32_t r[32];
+                if (t.rows) {
+                    tmem_ld_chunk(tacc + (uint32_t)(j * 32), r);
+                    if (j + 2 >= NP) {  // this warp's last piece
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
                     }
-                    constexpr int W = 32 * (int)sizeof(CT) / 16;  // 16-byte chunks of 32 columns
+                } else {
 #pragma unroll
-                    for (int c = 0; c < W; c++) {
-                        uint4 v;
-                        if constexpr (sizeof(CT) == 2) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int x = 0; x < 4; x++) {
-                                const __nv_bfloat162 p = __floats2bfloat162_rn(__uint_as_float(r[8 * c + 2 * x]),
-                                                                               __uint_as_float(r[8 * c + 2 * x + 1]));
-                                w[x] = *(const uint32_t *)&p;
-                            }
-                            v = make_uint4(w[0], w[1], w[2], w[3]);
-                        } else {
-                            v = make_uint4(r[4 * c], r[4 * c + 1], r[4 * c + 2], r[4 * c + 3]);
-                        }
-                        *(uint4 *)(box + lane * 128 + (((h * W + c) ^ (lane & 7)) << 4)) = v;
-                    }
+                    for (int c = 0; c < 32; c++) r[c] = 0u;
                 }
-                fence_async_smem();
-                __syncwarp();
-                if (lane == 0 && n < a.N) {
-                    gw_store(&cmap, smem_addr(box), t.k0 + j * PC, n, t.e, a.accumulate);
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+#pragma unroll
+                for (int h = 0; h < 2; h++, box ^= 1) {
+                    CT *const o = boxes + box * (GW_BOX * 32) + lane;
+                    // the box's last copy, the one before the newest, has been read
+                    if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int c = 0; c < GW_BOX; c++) {
+                        if constexpr (sizeof(CT) == 2)
+                            o[c * 32] = __float2bfloat16_rn(__uint_as_float(r[h * GW_BOX + c]));
+                        else
+                            o[c * 32] = __uint_as_float(r[h * GW_BOX + c]);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        const int n = t.n0 + j * 32 + h * GW_BOX;
+                        if (n < a.N && k < a.K) gw_store(&cmap, smem_addr(o), k, n, t.e, a.accumulate);
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
                 }
             }
             if (t.rows) ut++;
@@ -362,21 +362,21 @@ int row_map(CUtensorMap *map, const void *p, int cols, int n_rows, long ld)
 }
 
 template <typename CT>
-int launch_gw(void *dW, const GwArgs &a, cudaStream_t s)
+int launch_gw(const GwArgs &a, cudaStream_t s)
 {
-    CUtensorMap ymap, xmap, cmap;
+    CUtensorMap ymap, xmap;
     int st = row_map(&ymap, a.dy, a.N, a.slots, a.lddy);
     if (st == K3MOE_OK) st = row_map(&xmap, a.x, a.K, a.xrows, a.ldx);
-    const int K = a.K;
-    const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)a.N, (cuuint64_t)a.E},
-                     strides[2] = {(cuuint64_t)K * sizeof(CT), (cuuint64_t)K * a.N * sizeof(CT)};
-    const cuuint32_t box[3] = {(cuuint32_t)(128 / sizeof(CT)), 32, 1};
+    CUtensorMap cmap;
+    const cuuint64_t dims[3] = {(cuuint64_t)a.K, (cuuint64_t)a.N, (cuuint64_t)a.E},
+                     strides[2] = {(cuuint64_t)a.K * sizeof(CT), (cuuint64_t)a.K * a.N * sizeof(CT)};
+    const cuuint32_t box[3] = {32, GW_BOX, 1};
     if (st == K3MOE_OK)
-        st = encode_map(&cmap, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, dW,
-                        dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        st = encode_map(&cmap, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.dw,
+                        dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != K3MOE_OK) return st;
     if (ensure_smem((const void *)k3_grouped_wgrad<CT>, GW_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
-    const int grid = std::min(a.E * a.tiles_e, num_sms());
+    const int grid = std::min(a.E * (int)a.tiles_e.d, num_sms());
     if (launch_pdl(k3_grouped_wgrad<CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, xmap, cmap, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
@@ -392,14 +392,14 @@ int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const vo
     GwArgs a = {};
     a.offsets = g->offsets, a.order = g->order;
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = xrows;
-    a.tiles_k = (K + GW_N - 1) / GW_N;
-    const long tiles = (long)a.tiles_k * ((N + GW_M - 1) / GW_M);
+    const int tiles_k = (K + GW_M - 1) / GW_M;
+    const long tiles = (long)tiles_k * ((N + GW_N - 1) / GW_N);
     if (tiles * a.E > 0x7fffffffL) return K3MOE_EINVAL;
-    a.tiles_e = (int)tiles;
+    a.tiles_k = FastDiv((uint32_t)tiles_k), a.tiles_e = FastDiv((uint32_t)tiles);
     a.N = N, a.K = K, a.accumulate = accumulate, a.err = err;
-    a.dy = (const __nv_bfloat16 *)dY, a.x = (const __nv_bfloat16 *)X, a.lddy = lddy, a.ldx = ldx;
-    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(dW, a, s)
-                              : launch_gw<float>(dW, a, s);
+    a.dy = (const __nv_bfloat16 *)dY, a.x = (const __nv_bfloat16 *)X, a.dw = dW, a.lddy = lddy, a.ldx = ldx;
+    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(a, s)
+                              : launch_gw<float>(a, s);
 }
 
 }  // namespace k3
