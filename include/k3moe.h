@@ -822,13 +822,20 @@ int k3moe_groups_plan(const k3moe_groups *host_g, const int32_t *ids, k3moe_stre
  */
 typedef struct {
     const uint8_t *codes;
-    const uint8_t *atoms;
+    uint8_t *atoms;
     int64_t codes_stride;
     int64_t atoms_stride;
     int32_t E;
     int32_t rows;
     int32_t in;
 } k3moe_mx_experts;
+
+/* Makes stored matrices operands: writes every expert's atoms from its scale plane
+ * [rows][in / 32] (row-major bytes, any alignment) at scales + e * scales_stride, by the
+ * rule of k3moe_mx_operand_from_matrix; the codes are the matrices' own packed planes.
+ * Errors: K3MOE_EINVAL. */
+int k3moe_mx_experts_from_matrices(const k3moe_mx_experts *host_W, const uint8_t *scales, int64_t scales_stride,
+                                   k3moe_stream s);
 
 /*
  * C[i] = W_e a(i) for every place i of a plan, e the expert it belongs to: 8-bit rows
@@ -842,12 +849,19 @@ typedef struct {
  *              K3MOE_BF16, aligned to its element size, row stride ldc >= W->rows;
  *              rows from offsets[E] on are left as they are
  *  accumulate  != 0 adds into C (K3MOE_F32 only)
- * The result does not depend on timing.
+ * The result does not depend on timing.  After a device-side timeout
+ * (k3moe_device_error() == K3MOE_ETIMEOUT) the plan's workspace is zeroed again before it
+ * is used.
  * Errors: K3MOE_EINVAL for null or misaligned pointers, E or `in` that differ, too few
  * rows, bad sizes or types.
  */
 int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *host_A, const k3moe_mx_experts *host_W,
                          const k3moe_groups *host_g, int32_t gather, int32_t accumulate, k3moe_stream s);
+
+/* How a grouped product of `slots` rows with E matrices [N][in] runs on the current device
+ * (for profiles and tests): *host_rows is the most rows of a tile, 256 on CTA pairs, else
+ * 16, 32 or 64.  Errors: K3MOE_EINVAL. */
+int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, int32_t *host_rows);
 
 /*
  * The gradients of the experts' matrices, dW_e = sum over e's places i of dY[i] x(i)^T,

@@ -11,7 +11,8 @@
 namespace k3 {
 int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long ld, const k3moe_mx_operand *row,
                                const k3moe_mx_operand *col, cudaStream_t s);
-int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atoms, cudaStream_t s);
+int launch_mx_scale_atoms(const uint8_t *scales, long scales_stride, int n_mats, int rows, int in, uint8_t *atoms,
+                          long atoms_stride, cudaStream_t s);
 int launch_mx_dequantize(const k3moe_mx_operand *op, void *y, int ydt, long ld, cudaStream_t s);
 int launch_mx_matmul(void *C, int cdt, long ldc, const k3moe_mx_operand *A, const k3moe_mx_operand *B, int accumulate,
                      int *err, cudaStream_t s);
@@ -20,6 +21,7 @@ int launch_swiglu_forward(void *h, long ldh, void *ckpt, const void *g, long ldg
                           int T, int f, cudaStream_t s);
 int launch_swiglu_backward(void *dg, long lddg, void *du, long lddu, const void *dh, long lddh, const void *ckpt,
                            int dtype, int T, int f, cudaStream_t s);
+int grouped_matmul_rows(int E, long slots, int N, int in);
 size_t balance_workspace_bytes(int E);
 int launch_balance_forward(float *loss, int32_t *counts, int32_t *n_valid, const void *logits, int dtype, long ld,
                            const int32_t *ids, const uint8_t *mask, int T, int E, int k, float alpha, int rule,
@@ -86,6 +88,14 @@ bool valid_groups(const k3moe_groups *g)
 }
 // Two row matrices of a call that may be one: the same rows then.
 bool apart_or_same(const void *p, int64_t ldp, const void *q, int64_t ldq, int32_t T) { return p != q || T == 1 || ldp == ldq; }
+bool valid_experts(const k3moe_mx_experts *W)
+{
+    return W && W->codes && W->atoms && aligned(W->codes, 32) && aligned(W->atoms, 16) && W->E >= 1 && W->E <= 1024 &&
+           W->rows >= 1 && W->rows <= kMaxDim && W->in >= 128 && W->in <= kMaxIn && W->in % 128 == 0 &&
+           W->codes_stride % 32 == 0 && W->codes_stride >= (int64_t)W->rows * (W->in / 2) &&
+           W->codes_stride < ((int64_t)1 << 40) && W->atoms_stride % 16 == 0 &&
+           W->atoms_stride >= k3moe_mx_operand_atoms_bytes(W->rows, W->in) && W->atoms_stride < ((int64_t)1 << 40);
+}
 // A launch that writes what a later call may read as weights.  The launches allocate
 // no memory of their own, but the library's table of raised shared-memory limits may
 // grow: no exception leaves an entry point.
@@ -131,7 +141,7 @@ int k3moe_mx_operand_from_matrix(const k3moe_mx_operand *op, const k3moe_mat *W,
     if (!valid_operand(op) || !W || !W->packed || !W->scales || op->codes != W->packed || op->rows != W->rows ||
         W->in % 32 || k3::op_in_padded(op->in) != W->in || !aligned(W->scales, 16))
         return K3MOE_EINVAL;
-    return writing(s, [&] { return k3::launch_mx_scale_atoms(W->scales, op->rows, op->in, op->atoms, cs(s)); });
+    return writing(s, [&] { return k3::launch_mx_scale_atoms(W->scales, 0, 1, op->rows, op->in, op->atoms, 0, cs(s)); });
 }
 
 int k3moe_mx_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx_operand *op, k3moe_stream s)
@@ -312,14 +322,30 @@ int k3moe_groups_plan(const k3moe_groups *g, const int32_t *ids, k3moe_stream s)
     return writing(s, [&] { return k3::launch_groups_plan(g, ids, cs(s)); });
 }
 
+int k3moe_mx_experts_from_matrices(const k3moe_mx_experts *W, const uint8_t *scales, int64_t scales_stride, k3moe_stream s)
+{
+    if (!valid_experts(W) || !scales || scales_stride < (int64_t)W->rows * (W->in / 32) ||
+        scales_stride > ((int64_t)1 << 40))
+        return K3MOE_EINVAL;
+    return writing(s, [&] {
+        return k3::launch_mx_scale_atoms(scales, (long)scales_stride, W->E, W->rows, W->in, W->atoms, (long)W->atoms_stride,
+                                         cs(s));
+    });
+}
+
+int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, int32_t *rows)
+{
+    if (E < 1 || E > 1024 || slots < 1 || slots > kMaxDim || N < 1 || N > kMaxDim || in < 128 || in > kMaxIn || in % 128 ||
+        !rows)
+        return K3MOE_EINVAL;
+    *rows = k3::grouped_matmul_rows(E, (long)slots, N, in);
+    return K3MOE_OK;
+}
+
 int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
                          const k3moe_groups *g, int32_t gather, int32_t accumulate, k3moe_stream s)
 {
-    if (!valid_groups(g) || !valid_mx8(A) || !W || !W->codes || !W->atoms || !aligned(W->codes, 32) || !aligned(W->atoms, 16) ||
-        W->E != g->E || W->rows < 1 || W->rows > kMaxDim || W->in != A->in || W->in % 128 ||
-        W->codes_stride % 32 || W->codes_stride < (int64_t)W->rows * (W->in / 2) || W->codes_stride >= ((int64_t)1 << 40) ||
-        W->atoms_stride % 16 || W->atoms_stride < k3moe_mx_operand_atoms_bytes(W->rows, W->in) ||
-        W->atoms_stride > ((int64_t)1 << 40) || A->rows < (gather ? g->tokens : g->tokens * g->top_k) ||
+    if (!valid_groups(g) || !valid_mx8(A) || !valid_experts(W) || W->E != g->E || W->in != A->in || A->rows < (gather ? g->tokens : g->tokens * g->top_k) ||
         !valid_dtype(c_dtype) || !valid_rows(C, c_dtype, ldc, W->rows) || (accumulate && c_dtype != K3MOE_F32))
         return K3MOE_EINVAL;
     return writing(s, [&] {

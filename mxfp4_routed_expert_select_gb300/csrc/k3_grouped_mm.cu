@@ -888,29 +888,35 @@ int launch_gp(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, GmArgs a, cuda
 //   7168 x 1536, 8 rows 82 80 83 101, 32 rows 175 113 98 103, 64 rows 317 187 145 109.
 // (Single tiles of 128 rows never won: 114, 203 and 164 us at the last three sizes but
 // one, and 16 to 35% behind pairs from 128 rows on.)
-template <typename CT>
-int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &a, cudaStream_t s)
+int tile_rows(int E, long slots, int N, int nks)
 {
-    const long hit = std::min(a.E, a.slots), sms = num_sms();
+    const long hit = std::min<long>(E, slots), sms = num_sms(), tiles_n = ((long)N + GM_M - 1) / GM_M;
     const struct {
         int rows, step, tile;  // of a tile; ns
         long columns, at_once;
-    } forms[4] = {{16, 236, 500, a.tiles_n, sms},
-                  {32, 240, 600, a.tiles_n, sms},
-                  {64, 255, 1300, a.tiles_n, sms},
-                  {GP_NT, 290, 1500, (a.N + 2L * GM_M - 1) / (2 * GM_M), std::max(1L, sms / 2)}};
+    } forms[4] = {{16, 236, 500, tiles_n, sms},
+                  {32, 240, 600, tiles_n, sms},
+                  {64, 255, 1300, tiles_n, sms},
+                  {GP_NT, 290, 1500, (tiles_n + 1) / 2, std::max(1L, sms / 2)}};
     int best = 0;
     long cost = 0;
-    for (int i = 0; i < 4; i++) {
-        const long half_tiles = std::max(2 * hit, 2 * (long)a.slots / forms[i].rows + hit);
-        const long waves = (half_tiles * forms[i].columns + 2 * forms[i].at_once - 1) / (2 * forms[i].at_once);
-        const long c = waves * ((long)forms[i].step * a.nks + forms[i].tile);
-        if (!cost || c < cost) cost = c, best = i;
+    for (const auto &f : forms) {
+        const long half_tiles = std::max(2 * hit, 2 * slots / f.rows + hit);
+        const long waves = (half_tiles * f.columns + 2 * f.at_once - 1) / (2 * f.at_once);
+        const long c = waves * ((long)f.step * nks + f.tile);
+        if (!cost || c < cost) cost = c, best = f.rows;
     }
-    return best == 0   ? launch_gm<16, CT>(A, W, a, s)
-           : best == 1 ? launch_gm<32, CT>(A, W, a, s)
-           : best == 2 ? launch_gm<64, CT>(A, W, a, s)
-                       : launch_gp<CT>(A, W, a, s);
+    return best;
+}
+template <typename CT>
+int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArgs &a, cudaStream_t s)
+{
+    switch (tile_rows(a.E, a.slots, a.N, a.nks)) {
+    case 16: return launch_gm<16, CT>(A, W, a, s);
+    case 32: return launch_gm<32, CT>(A, W, a, s);
+    case 64: return launch_gm<64, CT>(A, W, a, s);
+    default: return launch_gp<CT>(A, W, a, s);
+    }
 }
 
 }  // namespace
@@ -918,6 +924,8 @@ int launch_gm_ct(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, const GmArg
 // The workspace: a count for each tile that has parts (zero between calls), and the sums
 // of parts of tiles.
 size_t grouped_matmul_workspace_bytes() { return GM_CTAS * (sizeof(float) * GM_M * GM_MAX_NT + sizeof(int32_t)); }
+
+int grouped_matmul_rows(int E, long slots, int N, int in) { return tile_rows(E, slots, N, in / 128); }
 
 int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
                           const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s)

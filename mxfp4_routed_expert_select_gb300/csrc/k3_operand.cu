@@ -241,10 +241,13 @@ __global__ void __launch_bounds__(q_threads<XT>(), sizeof(XT) == 2 ? 4 : 2) k3_m
 
 // Scale atoms of a stored matrix (scales [rows][nb], nb blocks per row): byte
 // 255 (a dropped group) becomes 0, so that the group adds at most 6 * 2^-127
-// of the other operand's block.  One CTA per atom.
-__global__ void __launch_bounds__(128) k3_mx_scale_atoms(const uint8_t *scales, int rows, int nb, int nk, uint8_t *atoms)
+// of the other operand's block.  One CTA per atom; matrix blockIdx.y of several.
+__global__ void __launch_bounds__(128)
+    k3_mx_scale_atoms(const uint8_t *scales, long scales_stride, int rows, int nb, int nk, uint8_t *atoms, long atoms_stride)
 {
     griddep_wait();
+    scales += blockIdx.y * scales_stride;
+    atoms += blockIdx.y * atoms_stride;
     const int r = (int)(blockIdx.x / nk) * 128 + threadIdx.x, b0 = 4 * (int)(blockIdx.x % nk);
     uint32_t w = 0u;
     if (r < rows)
@@ -382,12 +385,13 @@ int launch_mx_quantize_operand(const void *x, int xdt, int rows, int cols, long 
                : (cudaGetLastError(), K3MOE_ECUDA);
 }
 
-int launch_mx_scale_atoms(const uint8_t *scales, int rows, int in, uint8_t *atoms, cudaStream_t s)
+int launch_mx_scale_atoms(const uint8_t *scales, long scales_stride, int n_mats, int rows, int in, uint8_t *atoms,
+                          long atoms_stride, cudaStream_t s)
 {
     const long n = (long)op_row_tiles(rows) * op_k_atoms(in);
     if (n > 0x7fffffffL) return K3MOE_EINVAL;
-    const cudaError_t e = launch_pdl(k3_mx_scale_atoms, dim3((unsigned)n), dim3(128), 0, s, scales, rows,
-                                     op_in_padded(in) / 32, op_k_atoms(in), atoms);
+    const cudaError_t e = launch_pdl(k3_mx_scale_atoms, dim3((unsigned)n, (unsigned)n_mats), dim3(128), 0, s, scales,
+                                     scales_stride, rows, op_in_padded(in) / 32, op_k_atoms(in), atoms, atoms_stride);
     return e == cudaSuccess ? K3MOE_OK : (cudaGetLastError(), K3MOE_ECUDA);
 }
 

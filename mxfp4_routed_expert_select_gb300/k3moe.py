@@ -182,6 +182,8 @@ SIGNATURES = {
                                            _P]),
     "k3moe_groups_workspace": (_SZ, [_I, _I64]),
     "k3moe_groups_plan": (ctypes.c_int, [_P, _P, _P]),
+    "k3moe_mx_experts_from_matrices": (ctypes.c_int, [_P, _P, _I64, _P]),
+    "k3moe_grouped_matmul_form": (ctypes.c_int, [_I, _I64, _I, _I, _P]),
     "k3moe_grouped_matmul": (ctypes.c_int, [_P, _I, _I64, _P, _P, _P, _I, _I, _P]),
     "k3moe_grouped_wgrad": (ctypes.c_int, [_P, _I, _P, _I64, _P, _I64, _I, _I, _I, _P, _I, _I, _P]),
     "k3moe_combine": (ctypes.c_int, [_P, _I64, _P, _I64, _I, _I, _P, _P, _I, _P]),
@@ -570,25 +572,30 @@ class RmsNorm:
         self.gpu = _gpu(self.workspace)
 
     def _rows(self, t, T, dtype):
+        """Pointer and row stride of a [T][n] tensor (or None): _dtype and _ld in one
+        call, 0.4 us less a tensor."""
         if t is None:
             return None, 0
-        if t.dtype is not dtype:
-            raise TypeError("tensors of one type expected, got %s and %s" % (dtype, t.dtype))
-        return t.data_ptr(), _ld(t, T, self.n)
+        n, (ld, cs) = self.n, t.stride()
+        if t.dtype is not dtype or t.shape != (T, n) or (cs != 1 and n > 1):
+            if t.dtype is not dtype:
+                raise TypeError("tensors of one type expected, got %s and %s" % (dtype, t.dtype))
+            _ld(t, T, n)
+        return t.data_ptr(), ld if T > 1 or ld > n else n
 
     def forward(self, y, x, delta=None, r=None, rstd=None, gain=None, y8=None, stream=None):
         """r = x + delta; y (rows' type) and / or y8 (Mx8Rows) = r / sqrt(mean r^2 +
         eps) * gain; rstd fp32 [T].  x, delta, r, y [T][n] of one type, gain fp32 [n]."""
-        T, dt, gpu = x.shape[0], x.dtype, self.gpu
+        T, dt, gpu, f32 = x.shape[0], x.dtype, self.gpu, self._f32
         if (x.get_device() != gpu or (y is not None and y.get_device() != gpu) or
                 (delta is not None and delta.get_device() != gpu) or (r is not None and r.get_device() != gpu) or
                 (rstd is not None and rstd.get_device() != gpu) or (gain is not None and gain.get_device() != gpu) or
                 (y8 is not None and y8.gpu != gpu)):
             _elsewhere(gpu, x, y, delta, r, rstd, gain, None if y8 is None else y8.codes)
         st = (_lib or lib()).k3moe_norm_forward(
-            *self._rows(y, T, dt), *self._rows(r, T, dt), _flat(rstd, self._f32, T), y8 and y8.ref,
-            *self._rows(x, T, dt), *self._rows(delta, T, dt), _flat(gain, self._f32, self.n), _dtype(x), T, self.n,
-            self.eps, _stream(stream))
+            *self._rows(y, T, dt), *self._rows(r, T, dt), rstd if rstd is None else _flat(rstd, f32, T),
+            y8 if y8 is None else y8.ref, *self._rows(x, T, dt), *self._rows(delta, T, dt),
+            gain if gain is None else _flat(gain, f32, self.n), _dtype(x), T, self.n, self.eps, _stream(stream))
         if st:
             check(st, "k3moe_norm_forward")
 
@@ -625,7 +632,7 @@ class ExpertGroups:
         self._order = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
         self._pos = torch.empty(max_tokens * top_k, dtype=torch.int32, device=device)
         self.workspace = torch.zeros(nb, dtype=torch.uint8, device=device)
-        self._i32 = torch.int32
+        self._i32, self._f32 = torch.int32, torch.float32
         self.gpu = _gpu(self.offsets)
         self.struct = GroupsStruct(self.offsets.data_ptr(), self._order.data_ptr(), self._pos.data_ptr(),
                                    self.workspace.data_ptr(), nb, E, top_k, 0)
@@ -697,17 +704,18 @@ class MxExperts:
         if _gpu(packed) is None or scales.get_device() != packed.get_device():
             _elsewhere(_gpu(packed), packed, scales)
         W = cls(E, rows, 2 * half, codes=packed)
-        if scales.data_ptr() % 16 or (E > 1 and scales.stride(0) % 16):  # the library reads aligned planes
-            n, handle = rows * half // 16, _stream(stream)
-            with torch.cuda.device(packed.device), torch.cuda.stream(torch.cuda.ExternalStream(handle)):
-                aligned = torch.empty(E, -(-n // 16) * 16, dtype=torch.uint8, device=packed.device)
-                aligned[:, :n].copy_(scales.reshape(E, n))
-            scales = W._planes = aligned
-        for e in range(E):
-            m = Mat(packed[e].data_ptr(), scales[e].data_ptr(), rows, 2 * half)
-            check(lib().k3moe_mx_operand_from_matrix(W.operand(e).ref, ctypes.byref(m), _stream(stream)),
-                  "k3moe_mx_operand_from_matrix")
+        check(lib().k3moe_mx_experts_from_matrices(W.ref, scales.data_ptr(),
+                                                   scales.stride(0) if E > 1 else rows * half // 16, _stream(stream)),
+              "k3moe_mx_experts_from_matrices")
         return W
+
+
+def grouped_matmul_form(E, slots, N, in_):
+    """How grouped_matmul runs `slots` rows with E matrices [N][in_] on the current
+    device: the most rows of a tile, 256 on CTA pairs, else 16, 32 or 64."""
+    rows = ctypes.c_int32()
+    check(lib().k3moe_grouped_matmul_form(E, slots, N, in_, ctypes.byref(rows)), "k3moe_grouped_matmul_form")
+    return rows.value
 
 
 def grouped_matmul(C, A, W, groups, gather=False, accumulate=False, stream=None):
@@ -746,13 +754,12 @@ def grouped_wgrad(dW, dY, X, groups, gather=False, accumulate=False, stream=None
 def combine(out, y, groups, w=None, accumulate=False, stream=None):
     """out [tokens][n] (+)= the sum of each token's rows of y [slots][n] (group order),
     weighted by w fp32 [tokens][top_k] (ones without)."""
-    import torch
     gpu = groups.gpu
     if out.get_device() != gpu or y.get_device() != gpu or (w is not None and w.get_device() != gpu):
         _elsewhere(gpu, out, y, w)
     n = out.shape[1]
     st = (_lib or lib()).k3moe_combine(out.data_ptr(), _ld(out, groups.tokens, n), y.data_ptr(), _ld(y, groups.slots, n),
-                                       _dtype(out, y), n, groups.ref, _flat(w, torch.float32, groups.tokens, groups.k),
+                                       _dtype(out, y), n, groups.ref, _flat(w, groups._f32, groups.tokens, groups.k),
                                        1 if accumulate else 0, _stream(stream))
     if st:
         check(st, "k3moe_combine")
@@ -766,7 +773,7 @@ def combine_backward(dy, dw, dout, y, groups, w=None, stream=None):
     if (dy.get_device() != gpu or dout.get_device() != gpu or (dw is not None and dw.get_device() != gpu) or
             (y is not None and y.get_device() != gpu) or (w is not None and w.get_device() != gpu)):
         _elsewhere(gpu, dy, dout, dw, y, w)
-    n, T, k, f32 = dout.shape[1], groups.tokens, groups.k, torch.float32
+    n, T, k, f32 = dout.shape[1], groups.tokens, groups.k, groups._f32
     st = (_lib or lib()).k3moe_combine_backward(
         dy.data_ptr(), _ld(dy, groups.slots, n), _flat(dw, f32, T, k), dout.data_ptr(), _ld(dout, T, n),
         None if y is None else y.data_ptr(), 0 if y is None else _ld(y, groups.slots, n),

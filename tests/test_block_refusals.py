@@ -101,6 +101,25 @@ def test_matmul():
                                             None) == EINVAL, b
 
 
+def test_stored_experts():
+    L = k.lib()
+    for W, sc, st in ((None, P, 160), (experts(), None, 160), (experts(), P, 159), (experts(), P, (1 << 40) + 1),
+                      (experts(n=96), P, 160), (experts(codes=P + 16), P, 160), (experts(as_=512), P, 160),
+                      (experts(E=0), P, 160), (experts(E=1025), P, 160)):
+        assert L.k3moe_mx_experts_from_matrices(W, sc, st, None) == EINVAL
+
+
+def test_form_query():
+    L, o = k.lib(), ctypes.byref(ctypes.c_int32())
+    assert L.k3moe_grouped_matmul_form(1, 1, 1, 128, o) == k.K3MOE_OK
+    for a in ((0, 1, 1, 128), (1025, 1, 1, 128), (1, 0, 1, 128), (1, (1 << 30) + 1, 1, 128), (1, 1, 0, 128), (1, 1, 1, 0),
+              (1, 1, 1, 64), (1, 1, 1, 192)):
+        assert L.k3moe_grouped_matmul_form(*a, o) == EINVAL
+    assert L.k3moe_grouped_matmul_form(1, 1, 1, 128, None) == EINVAL
+    for E, slots, N, n in ((1, 1, 1, 128), (1024, 1 << 30, 1 << 20, 1 << 20), (8, 1000, 7168, 1536)):
+        assert k.grouped_matmul_form(E, slots, N, n) in (16, 32, 64, 256)
+
+
 def test_wgrad():
     good = dict(dw=P, dt=0, dy=P, lddy=16, x=P, ldx=24, xr=10, N=16, K=24, g=groups(), gather=0, acc=0)
     bad = [dict(dw=None), dict(dw=P + 8), dict(dt=2), dict(dt=1, acc=1), dict(dy=None), dict(dy=P + 8), dict(lddy=8),

@@ -69,9 +69,10 @@ SIZES = {"one": [1], "few": [0, 1, 3, 16, 17, 0, 5, 2], "some": [33, 0, 1, 32, 3
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("gather", [False, True])
 @pytest.mark.parametrize("sizes", list(SIZES))
-@pytest.mark.parametrize("N,K,kk", [(128, 128, 1), (200, 384, 2), (1, 1152, 3), (129, 256, 4), (1000, 640, 5)])
-def test_matmul(N, K, kk, sizes, gather, out):
-    sizes = SIZES[sizes] or [0]
+@pytest.mark.parametrize("N,K,kk,pad", [(128, 128, 1, 2), (200, 384, 2, 0), (1, 1152, 3, 3), (129, 256, 4, 1),
+                                        (1000, 640, 5, 3)])
+def test_matmul(N, K, kk, pad, sizes, gather, out):
+    sizes = SIZES[sizes]
     if not sum(sizes):
         g, ids = k.ExpertGroups(len(sizes), kk, 4), np.full((4, kk), -1, np.int32)
         g.plan(torch.from_numpy(ids).cuda())
@@ -80,7 +81,7 @@ def test_matmul(N, K, kk, sizes, gather, out):
     E, slots = len(sizes), ids.size
     W, V = _weights(E, N, K, N + K)
     a, A = _rows(ids.shape[0] if gather else slots, K, 3)
-    C = torch.full((slots, N + 3), 9.0, dtype=DT[out], device="cuda")
+    C = torch.full((slots, N + pad), 9.0, dtype=DT[out], device="cuda")
     k.grouped_matmul(C[:, :N], a, W, g, gather=gather)
     off, src = _sources(ids, E, gather)
     want, mag = _want(off, src, A, V)
@@ -114,6 +115,86 @@ def test_matmul_many_experts(T, kk, E, N, K):
     off, src = _sources(ids, E, True)
     want, mag = _want(off, src, A, V)
     assert (np.abs(C.double().cpu().numpy() - want) <= mag * (K / 32 + 10) * 2.0 ** -22 + np.abs(want) * 2.0 ** -24).all()
+
+
+def _wide(E, N, K):
+    """Random stored matrices on the GPU and their fp64 values."""
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    packed = torch.randint(0, 256, (E, N, K // 2), generator=gen, device="cuda", dtype=torch.uint8)
+    scales = torch.randint(120, 131, (E, N, K // 32), generator=gen, device="cuda", dtype=torch.uint8)
+    lut = torch.tensor(np.concatenate([mx.MAG, -mx.MAG]), device="cuda")
+    V = torch.empty(E, N, K, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        V[e, :, 0::2], V[e, :, 1::2] = lut[(packed[e] & 15).long()], lut[(packed[e] >> 4).long()]
+        V[e] *= torch.exp2(scales[e].double() - 127).repeat_interleave(32, 1)
+    return k.MxExperts.from_matrices(packed, scales), V
+
+
+def _check_wide(W, V, sizes, kk, gather, out, accumulate=False):
+    E, N, K = V.shape
+    g, ids = _plan(sizes, kk, 5)
+    a, A = _rows(ids.shape[0] if gather else ids.size, K, 3)
+    off, src = _sources(ids, E, gather)
+    A = torch.from_numpy(A).cuda()[torch.from_numpy(src).cuda()]
+    C = torch.full((ids.size, N), 0.5, dtype=DT[out], device="cuda")
+    k.grouped_matmul(C, a, W, g, gather=gather, accumulate=accumulate)
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        want, mag = A[s] @ V[e].t(), A[s].abs() @ V[e].abs().t()
+        if accumulate:
+            want, mag = want + 0.5, mag + 0.5
+        tol = mag * (K / 32 + 10) * 2.0 ** -22 + want.abs() * HALF[out]
+        assert bool(((C[s].double() - want).abs() <= tol).all()), e
+    assert bool((C[off[E]:] == 0.5).all())
+    again = torch.full_like(C, 0.5)
+    k.grouped_matmul(again, a, W, g, gather=gather, accumulate=accumulate)
+    assert torch.equal(again, C) and k.device_error() == 0
+
+
+# by the form that runs: tiles of 16, 32 and 64 rows, and pairs of CTAs
+FORMS = {16: [0, 1, 16, 17, 5, 9], 32: [33, 0, 31, 1, 15, 16], 64: [64, 65, 0, 1, 50, 36], 256: [256, 0, 1, 40, 33, 31]}
+
+
+@pytest.fixture(scope="module")
+def wide():
+    return _wide(6, 9000, 1024)
+
+
+@pytest.mark.parametrize("out,acc", [("f32", False), ("bf16", False), ("f32", True)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("form", list(FORMS))
+def test_matmul_every_form(wide, form, gather, out, acc):
+    sizes = FORMS[form]
+    assert k.grouped_matmul_form(6, sum(sizes), 9000, 1024) == form
+    _check_wide(*wide, sizes, 1, gather, out, acc)
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sizes", [[300, 257, 31, 0, 513, 95], [1025, 255, 256, 512, 2, 480]])
+def test_matmul_pairs_of_several_tiles(wide, sizes, gather, out):
+    assert k.grouped_matmul_form(6, sum(sizes), 9000, 1024) == 256
+    _check_wide(*wide, sizes, 1, gather, out)
+
+
+# few tiles of a long K: those left over from full waves are shared by several CTAs
+@pytest.mark.parametrize("form,each", [(32, 40), (64, 60)])
+def test_matmul_tiles_in_parts(form, each):
+    W, V = _wide(80, 250, 4096)
+    rng = np.random.default_rng(each)
+    sizes = rng.integers(each - 12, each + 12, 80)
+    sizes[-1] += 80 * each - sizes.sum()
+    assert k.grouped_matmul_form(80, 80 * each, 250, 4096) == form
+    for gather, out, acc in ((True, "f32", False), (False, "bf16", False), (True, "f32", True)):
+        _check_wide(W, V, list(sizes), 4, gather, out, acc)
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 7, 1], [16, 3, 0, 12, 17]])
+@pytest.mark.parametrize("N,K", [(1, 4096), (200, 4096), (385, 7168)])
+def test_matmul_few_tiles_in_parts(N, K, sizes):
+    W, V = _wide(len(sizes), N, K)
+    for gather, out, acc in ((True, "f32", False), (False, "bf16", False), (True, "f32", True)):
+        _check_wide(W, V, sizes, 1, gather, out, acc)
 
 
 def test_matmul_whole_numbers_are_exact():
