@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     __syncthreads();
     cluster_sync();  // the other CTA's barriers are initialised
     tc_fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, *(volatile uint32_t *)tmem_slot);
     griddep_wait();
     gm_table(tab, a, GP_NT);
     const int n_tiles = tab.before[a.E] * a.tiles_n;
@@ -740,7 +740,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             bool ok = tile_in(ut);
             const GpTile *t = ring + ut % GP_RING;
             if (!ok || t->e < 0) break;
-            const uint32_t id = gm_idesc(2 * GM_M, 2 * t->half, 0);
+            const uint32_t id = __reduce_max_sync(0xffffffffu, gm_idesc(2 * GM_M, 2 * t->half, 0));
             tile_out(ut);
             // the epilogue frees the columns that a tile's accumulator shares with the next
             if (ut >= 1) {

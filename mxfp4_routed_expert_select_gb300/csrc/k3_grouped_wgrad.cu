@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)tmem_slot;
+    const uint32_t tmem = __reduce_max_sync(0xffffffffu, *(volatile uint32_t *)tmem_slot);
     griddep_wait();
     const int n_tiles = a.E * (int)a.tiles_e.d, first = (int)blockIdx.x, step = (int)gridDim.x;
 
