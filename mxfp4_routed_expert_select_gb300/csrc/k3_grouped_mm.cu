@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
         // -------------------------------------------------------------- MMA
         uint32_t ut = 0, phase = 0;
         int s = 0;
-        bool ok = true;
+        bool ok = true, ready = false;
         const uint32_t lo = sw128_lo(sbase);
         constexpr uint32_t SD = C::STAGE / 16;  // descriptor words between stages
         for (;; ut++) {
@@ -378,16 +378,22 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
                 break;
             tc_fence_after();
             for (int ks = part.k0; ks < part.k1; ks++) {
-                if (!__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
+                const int sn = s + 1 == NS ? 0 : s + 1;
+                const uint32_t pn = sn ? phase : phase ^ 1u;
+                // ask for the next stage before this one is issued, look at the answer after
+                const bool next = mbar_test(bar(B_FULL + sn), pn);
                 const uint32_t d = lo + (uint32_t)s * SD;
                 gm_step<NT>(tmem + (uint32_t)(buf * NT), d, d + C::OFF_X / 16, d + C::OFF_WA / 16,
                             tmem + (uint32_t)(C::SF0 + C::SF * s), ks > part.k0 ? 1u : 0u);
                 mma_commit(bar(B_EMPTY + s));
-                if (++s == NS) s = 0, phase ^= 1u;
+                ready = __all_sync(0xffffffffu, next);
+                s = sn;
+                phase = pn;
             }
             if (!ok) break;
             mma_commit(bar(B_ACCF + buf));

@@ -265,11 +265,12 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 tc_fence_after();
                 const int sn = s + 1 == NS ? 0 : s + 1;
                 const uint32_t pn = sn ? phase : phase ^ 1u;
-                // look at the next stage while this one is issued
-                ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
+                // ask for the next stage before this one is issued, look at the answer after
+                const bool next = mbar_test(bar(B_FULL + sn), pn);
                 const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
                 gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_Y / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
                 mma_commit(bar(B_EMPTY + s));
+                ready = __all_sync(0xffffffffu, next);
                 s = sn;
                 phase = pn;
             }
