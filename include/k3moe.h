@@ -771,12 +771,47 @@ int k3moe_mx8_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx8_rows 
  * strides, an eps that is negative or not finite.
  */
 size_t k3moe_norm_workspace(int32_t n);
-int k3moe_norm_forward(void *y, int64_t ldy, void *r, int64_t ldr, float *rstd, const k3moe_mx8_rows *host_y8,
-                       const void *x, int64_t ldx, const void *delta, int64_t ldd, const float *gain, int dtype, int32_t T,
-                       int32_t n, float eps, k3moe_stream s);
-int k3moe_norm_backward(void *dx, int64_t lddx, float *dgain, int32_t accumulate, const void *dy, int64_t lddy,
-                        const void *dr, int64_t lddr, const void *r, int64_t ldr, const float *rstd, const float *gain,
-                        int dtype, int32_t T, int32_t n, void *workspace, size_t workspace_bytes, k3moe_stream s);
+
+typedef struct {
+    void *y;
+    int64_t ldy;
+    void *r;
+    int64_t ldr;
+    float *rstd;
+    const k3moe_mx8_rows *host_y8;
+    const void *x;
+    int64_t ldx;
+    const void *delta;
+    int64_t ldd;
+    const float *gain;
+    int32_t dtype;
+    int32_t T;
+    int32_t n;
+    float eps;
+} k3moe_norm_forward_desc;
+
+typedef struct {
+    void *dx;
+    int64_t lddx;
+    float *dgain;
+    const void *dy;
+    int64_t lddy;
+    const void *dr;
+    int64_t lddr;
+    const void *r;
+    int64_t ldr;
+    const float *rstd;
+    const float *gain;
+    void *workspace;
+    size_t workspace_bytes;
+    int32_t dtype;
+    int32_t T;
+    int32_t n;
+    int32_t accumulate;
+} k3moe_norm_backward_desc;
+
+int k3moe_norm_forward(const k3moe_norm_forward_desc *host_desc, k3moe_stream s);
+int k3moe_norm_backward(const k3moe_norm_backward_desc *host_desc, k3moe_stream s);
 
 /* --------------------------------------------- products grouped by expert */
 
@@ -855,8 +890,18 @@ int k3moe_mx_experts_from_matrices(const k3moe_mx_experts *host_W, const uint8_t
  * Errors: K3MOE_EINVAL for null or misaligned pointers, E or `in` that differ, too few
  * rows, bad sizes or types.
  */
-int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *host_A, const k3moe_mx_experts *host_W,
-                         const k3moe_groups *host_g, int32_t gather, int32_t accumulate, k3moe_stream s);
+typedef struct {
+    void *C;
+    int64_t ldc;
+    const k3moe_mx8_rows *host_A;
+    const k3moe_mx_experts *host_W;
+    const k3moe_groups *host_groups;
+    int32_t c_dtype;
+    int32_t gather;
+    int32_t accumulate;
+} k3moe_grouped_matmul_desc;
+
+int k3moe_grouped_matmul(const k3moe_grouped_matmul_desc *host_desc, k3moe_stream s);
 
 /* How a grouped product of `slots` rows with E matrices [N][in] runs on the current device
  * (for profiles and tests): *host_rows is the most rows of a tile, 256 on CTA pairs, else
@@ -875,9 +920,22 @@ int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, i
  * N and K are multiples of 8; dY, X and dW 16-byte aligned, lddy and ldx multiples of 8.
  * The result does not depend on timing.  Errors: K3MOE_EINVAL.
  */
-int k3moe_grouped_wgrad(void *dW, int dw_dtype, const void *dY, int64_t lddy, const void *X, int64_t ldx, int32_t xrows,
-                        int32_t N, int32_t K, const k3moe_groups *host_g, int32_t gather, int32_t accumulate,
-                        k3moe_stream s);
+typedef struct {
+    void *dW;
+    const void *dY;
+    int64_t lddy;
+    const void *X;
+    int64_t ldx;
+    const k3moe_groups *host_groups;
+    int32_t dw_dtype;
+    int32_t xrows;
+    int32_t N;
+    int32_t K;
+    int32_t gather;
+    int32_t accumulate;
+} k3moe_grouped_wgrad_desc;
+
+int k3moe_grouped_wgrad(const k3moe_grouped_wgrad_desc *host_desc, k3moe_stream s);
 
 /*
  * The end of the layer, out[t] (+)= sum_j w[t][j] y[pos[t][j]], and its gradients
@@ -893,10 +951,34 @@ int k3moe_grouped_wgrad(void *dW, int dw_dtype, const void *dY, int64_t lddy, co
  * aligned to the element size; 1 <= n <= 2^20.  dy may be y with the same stride.
  * Sums are taken in rising j.  Errors: K3MOE_EINVAL.
  */
-int k3moe_combine(void *out, int64_t ldo, const void *y, int64_t ldy, int dtype, int32_t n, const k3moe_groups *host_g,
-                  const float *w, int32_t accumulate, k3moe_stream s);
-int k3moe_combine_backward(void *dy, int64_t lddy, float *dw, const void *dout, int64_t lddo, const void *y, int64_t ldy,
-                           int dtype, int32_t n, const k3moe_groups *host_g, const float *w, k3moe_stream s);
+typedef struct {
+    void *out;
+    int64_t ldo;
+    const void *y;
+    int64_t ldy;
+    const float *w;
+    const k3moe_groups *host_groups;
+    int32_t dtype;
+    int32_t n;
+    int32_t accumulate;
+} k3moe_combine_desc;
+
+typedef struct {
+    void *dy;
+    int64_t lddy;
+    float *dw;
+    const void *dout;
+    int64_t lddo;
+    const void *y;
+    int64_t ldy;
+    const float *w;
+    const k3moe_groups *host_groups;
+    int32_t dtype;
+    int32_t n;
+} k3moe_combine_backward_desc;
+
+int k3moe_combine(const k3moe_combine_desc *host_desc, k3moe_stream s);
+int k3moe_combine_backward(const k3moe_combine_backward_desc *host_desc, k3moe_stream s);
 
 /* ------------------------------- SwiGLU with an 8-bit activation checkpoint */
 

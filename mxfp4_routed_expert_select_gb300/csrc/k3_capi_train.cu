@@ -33,22 +33,14 @@ int launch_balance_backward(void *dlogits, long ldd, const void *logits, int dty
 int launch_mx8_quantize(const k3moe_mx8_rows *o, const void *x, int dtype, long ld, cudaStream_t s);
 int launch_mx8_dequantize(void *y, int dtype, long ld, const k3moe_mx8_rows *o, cudaStream_t s);
 size_t norm_workspace_bytes(int n);
-int launch_norm_forward(void *y, long ldy, void *r, long ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
-                        long ldx, const void *delta, long ldd, const float *gain, int dtype, int T, int n, float eps,
-                        cudaStream_t s);
-int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, const void *dy, long lddy, const void *dr,
-                         long lddr, const void *r, long ldr, const float *rstd, const float *gain, int dtype, int T,
-                         int n, void *ws, cudaStream_t s);
+int launch_norm_forward(const k3moe_norm_forward_desc &d, cudaStream_t s);
+int launch_norm_backward(const k3moe_norm_backward_desc &d, cudaStream_t s);
 size_t groups_workspace_bytes(int E, long slots);
 int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, cudaStream_t s);
-int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
-                          const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s);
-int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const void *X, long ldx, int xrows, int N, int K,
-                         const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s);
-int launch_combine(void *out, long ldo, const void *y, long ldy, int dtype, int n, const k3moe_groups *g, const float *w,
-                   int accumulate, cudaStream_t s);
-int launch_combine_backward(void *dy, long lddy, float *dw, const void *dout, long lddo, const void *y, long ldy, int dtype,
-                            int n, const k3moe_groups *g, const float *w, cudaStream_t s);
+int launch_grouped_matmul(const k3moe_grouped_matmul_desc &d, int *err, cudaStream_t s);
+int launch_grouped_wgrad(const k3moe_grouped_wgrad_desc &d, int *err, cudaStream_t s);
+int launch_combine(const k3moe_combine_desc &d, cudaStream_t s);
+int launch_combine_backward(const k3moe_combine_backward_desc &d, cudaStream_t s);
 }  // namespace k3
 
 namespace {
@@ -274,39 +266,32 @@ static bool valid_norm(int32_t T, int32_t n) { return T >= 1 && T <= kMaxDim && 
 
 size_t k3moe_norm_workspace(int32_t n) { return valid_norm(1, n) ? k3::norm_workspace_bytes(n) : 0; }
 
-int k3moe_norm_forward(void *y, int64_t ldy, void *r, int64_t ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
-                       int64_t ldx, const void *delta, int64_t ldd, const float *gain, int dtype, int32_t T, int32_t n,
-                       float eps, k3moe_stream s)
+int k3moe_norm_forward(const k3moe_norm_forward_desc *a, k3moe_stream s)
 {
-    if (!valid_norm(T, n) || !valid_dtype(dtype) || !valid_rows(x, dtype, ldx, n) ||
-        (delta && !valid_rows(delta, dtype, ldd, n)) || (y && !valid_rows(y, dtype, ldy, n)) ||
-        (r && (!delta || !valid_rows(r, dtype, ldr, n))) || (!y && !y8) ||
-        (y8 && (!valid_mx8(y8) || y8->rows != T || y8->in != n)) || !aligned(rstd, 4) || !aligned(gain, 4) ||
-        !(eps >= 0.f) || std::isinf(eps) || (y && y == r) || (y && !apart_or_same(y, ldy, x, ldx, T)) ||
-        (y && delta && !apart_or_same(y, ldy, delta, ldd, T)) || (r && !apart_or_same(r, ldr, x, ldx, T)) ||
-        (r && !apart_or_same(r, ldr, delta, ldd, T)))
+    if (!a || !valid_norm(a->T, a->n) || !valid_dtype(a->dtype) || !valid_rows(a->x, a->dtype, a->ldx, a->n) ||
+        (a->delta && !valid_rows(a->delta, a->dtype, a->ldd, a->n)) || (a->y && !valid_rows(a->y, a->dtype, a->ldy, a->n)) ||
+        (a->r && (!a->delta || !valid_rows(a->r, a->dtype, a->ldr, a->n))) || (!a->y && !a->host_y8) ||
+        (a->host_y8 && (!valid_mx8(a->host_y8) || a->host_y8->rows != a->T || a->host_y8->in != a->n)) ||
+        !aligned(a->rstd, 4) || !aligned(a->gain, 4) || !(a->eps >= 0.f) || std::isinf(a->eps) || (a->y && a->y == a->r) ||
+        (a->y && !apart_or_same(a->y, a->ldy, a->x, a->ldx, a->T)) ||
+        (a->y && a->delta && !apart_or_same(a->y, a->ldy, a->delta, a->ldd, a->T)) ||
+        (a->r && !apart_or_same(a->r, a->ldr, a->x, a->ldx, a->T)) ||
+        (a->r && !apart_or_same(a->r, a->ldr, a->delta, a->ldd, a->T)))
         return K3MOE_EINVAL;
-    return writing(s, [&] {
-        return k3::launch_norm_forward(y, (long)ldy, r, (long)ldr, rstd, y8, x, (long)ldx, delta, (long)ldd, gain, dtype, T,
-                                       n, eps, cs(s));
-    });
+    return writing(s, [&] { return k3::launch_norm_forward(*a, cs(s)); });
 }
 
-int k3moe_norm_backward(void *dx, int64_t lddx, float *dgain, int32_t accumulate, const void *dy, int64_t lddy,
-                        const void *dr, int64_t lddr, const void *r, int64_t ldr, const float *rstd, const float *gain,
-                        int dtype, int32_t T, int32_t n, void *ws, size_t ws_bytes, k3moe_stream s)
+int k3moe_norm_backward(const k3moe_norm_backward_desc *a, k3moe_stream s)
 {
-    if (!valid_norm(T, n) || !valid_dtype(dtype) || !valid_rows(dx, dtype, lddx, n) || !valid_rows(dy, dtype, lddy, n) ||
-        !valid_rows(r, dtype, ldr, n) || (dr && !valid_rows(dr, dtype, lddr, n)) || !rstd || !aligned(rstd, 4) ||
-        !aligned(gain, 4) || (dgain && (!gain || !aligned(dgain, 4) || !ws || !aligned(ws, 16) ||
-                                        ws_bytes < k3moe_norm_workspace(n))) ||
-        !apart_or_same(dx, lddx, dy, lddy, T) || !apart_or_same(dx, lddx, r, ldr, T) ||
-        (dr && !apart_or_same(dx, lddx, dr, lddr, T)))
+    if (!a || !valid_norm(a->T, a->n) || !valid_dtype(a->dtype) || !valid_rows(a->dx, a->dtype, a->lddx, a->n) ||
+        !valid_rows(a->dy, a->dtype, a->lddy, a->n) || !valid_rows(a->r, a->dtype, a->ldr, a->n) ||
+        (a->dr && !valid_rows(a->dr, a->dtype, a->lddr, a->n)) || !a->rstd || !aligned(a->rstd, 4) || !aligned(a->gain, 4) ||
+        (a->dgain && (!a->gain || !aligned(a->dgain, 4) || !a->workspace || !aligned(a->workspace, 16) ||
+                      a->workspace_bytes < k3moe_norm_workspace(a->n))) ||
+        !apart_or_same(a->dx, a->lddx, a->dy, a->lddy, a->T) || !apart_or_same(a->dx, a->lddx, a->r, a->ldr, a->T) ||
+        (a->dr && !apart_or_same(a->dx, a->lddx, a->dr, a->lddr, a->T)))
         return K3MOE_EINVAL;
-    return writing(s, [&] {
-        return k3::launch_norm_backward(dx, (long)lddx, dgain, accumulate ? 1 : 0, dy, (long)lddy, dr, (long)lddr, r,
-                                        (long)ldr, rstd, gain, dtype, T, n, ws, cs(s));
-    });
+    return writing(s, [&] { return k3::launch_norm_backward(*a, cs(s)); });
 }
 
 // ------------------------------------------------------------ grouped by expert
@@ -342,33 +327,38 @@ int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, i
     return K3MOE_OK;
 }
 
-int k3moe_grouped_matmul(void *C, int c_dtype, int64_t ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
-                         const k3moe_groups *g, int32_t gather, int32_t accumulate, k3moe_stream s)
+int k3moe_grouped_matmul(const k3moe_grouped_matmul_desc *a, k3moe_stream s)
 {
-    if (!valid_groups(g) || !valid_mx8(A) || !valid_experts(W) || W->E != g->E || W->in != A->in || A->rows < (gather ? g->tokens : g->tokens * g->top_k) ||
-        !valid_dtype(c_dtype) || !valid_rows(C, c_dtype, ldc, W->rows) || (accumulate && c_dtype != K3MOE_F32))
+    if (!a) return K3MOE_EINVAL;
+    const k3moe_mx8_rows *A = a->host_A;
+    const k3moe_mx_experts *W = a->host_W;
+    const k3moe_groups *g = a->host_groups;
+    if (!valid_groups(g) || !valid_mx8(A) || !valid_experts(W) || W->E != g->E || W->in != A->in ||
+        A->rows < (a->gather ? g->tokens : g->tokens * g->top_k) || !valid_dtype(a->c_dtype) ||
+        !valid_rows(a->C, a->c_dtype, a->ldc, W->rows) || (a->accumulate && a->c_dtype != K3MOE_F32))
         return K3MOE_EINVAL;
     return writing(s, [&] {
         int *err = k3::device_error_word();
         if (!err) return (int)K3MOE_ECUDA;
-        return k3::launch_grouped_matmul(C, c_dtype, (long)ldc, A, W, g, gather ? 1 : 0, accumulate ? 1 : 0, err, cs(s));
+        return k3::launch_grouped_matmul(*a, err, cs(s));
     });
 }
 
-int k3moe_grouped_wgrad(void *dW, int dw_dtype, const void *dY, int64_t lddy, const void *X, int64_t ldx, int32_t xrows,
-                        int32_t N, int32_t K, const k3moe_groups *g, int32_t gather, int32_t accumulate, k3moe_stream s)
+int k3moe_grouped_wgrad(const k3moe_grouped_wgrad_desc *a, k3moe_stream s)
 {
-    if (!valid_groups(g) || N < 8 || K < 8 || N > kMaxIn || K > kMaxIn || N % 8 || K % 8 || !valid_dtype(dw_dtype) || !dW ||
-        !aligned(dW, 16) || !valid_rows(dY, K3MOE_BF16, lddy, N) || !valid_rows(X, K3MOE_BF16, ldx, K) || !aligned(dY, 16) ||
-        !aligned(X, 16) || lddy % 8 || ldx % 8 || lddy >= ((int64_t)1 << 39) || ldx >= ((int64_t)1 << 39) ||
-        (int64_t)N * K >= ((int64_t)1 << 38) || xrows < (gather ? g->tokens : g->tokens * g->top_k) || xrows > kMaxDim ||
-        (accumulate && dw_dtype != K3MOE_F32))
+    if (!a) return K3MOE_EINVAL;
+    const k3moe_groups *g = a->host_groups;
+    if (!valid_groups(g) || a->N < 8 || a->K < 8 || a->N > kMaxIn || a->K > kMaxIn || a->N % 8 || a->K % 8 ||
+        !valid_dtype(a->dw_dtype) || !a->dW || !aligned(a->dW, 16) || !valid_rows(a->dY, K3MOE_BF16, a->lddy, a->N) ||
+        !valid_rows(a->X, K3MOE_BF16, a->ldx, a->K) || !aligned(a->dY, 16) || !aligned(a->X, 16) || a->lddy % 8 ||
+        a->ldx % 8 || a->lddy >= ((int64_t)1 << 39) || a->ldx >= ((int64_t)1 << 39) ||
+        (int64_t)a->N * a->K >= ((int64_t)1 << 38) || a->xrows < (a->gather ? g->tokens : g->tokens * g->top_k) ||
+        a->xrows > kMaxDim || (a->accumulate && a->dw_dtype != K3MOE_F32))
         return K3MOE_EINVAL;
     return writing(s, [&] {
         int *err = k3::device_error_word();
         if (!err) return (int)K3MOE_ECUDA;
-        return k3::launch_grouped_wgrad(dW, dw_dtype, dY, (long)lddy, X, (long)ldx, xrows, N, K, g, gather ? 1 : 0,
-                                        accumulate ? 1 : 0, err, cs(s));
+        return k3::launch_grouped_wgrad(*a, err, cs(s));
     });
 }
 
@@ -379,27 +369,22 @@ static bool valid_combine(const k3moe_groups *g, int dtype, int32_t n)
            (int64_t)g->tokens * ((n + 1023) / 1024) <= 0x7fffffff;
 }
 
-int k3moe_combine(void *out, int64_t ldo, const void *y, int64_t ldy, int dtype, int32_t n, const k3moe_groups *g,
-                  const float *w, int32_t accumulate, k3moe_stream s)
+int k3moe_combine(const k3moe_combine_desc *a, k3moe_stream s)
 {
-    if (!valid_combine(g, dtype, n) || !valid_rows(out, dtype, ldo, n) || !valid_rows(y, dtype, ldy, n) || !aligned(w, 4) ||
-        out == y)
+    if (!a || !valid_combine(a->host_groups, a->dtype, a->n) || !valid_rows(a->out, a->dtype, a->ldo, a->n) ||
+        !valid_rows(a->y, a->dtype, a->ldy, a->n) || !aligned(a->w, 4) || a->out == a->y)
         return K3MOE_EINVAL;
-    return writing(s, [&] {
-        return k3::launch_combine(out, (long)ldo, y, (long)ldy, dtype, n, g, w, accumulate ? 1 : 0, cs(s));
-    });
+    return writing(s, [&] { return k3::launch_combine(*a, cs(s)); });
 }
 
-int k3moe_combine_backward(void *dy, int64_t lddy, float *dw, const void *dout, int64_t lddo, const void *y, int64_t ldy,
-                           int dtype, int32_t n, const k3moe_groups *g, const float *w, k3moe_stream s)
+int k3moe_combine_backward(const k3moe_combine_backward_desc *a, k3moe_stream s)
 {
-    if (!valid_combine(g, dtype, n) || !valid_rows(dy, dtype, lddy, n) || !valid_rows(dout, dtype, lddo, n) || dy == dout ||
-        (dw && (!w || !valid_rows(y, dtype, ldy, n) || !aligned(dw, 4))) || !aligned(w, 4) ||
-        (dw && !apart_or_same(dy, lddy, y, ldy, 2)))
+    if (!a || !valid_combine(a->host_groups, a->dtype, a->n) || !valid_rows(a->dy, a->dtype, a->lddy, a->n) ||
+        !valid_rows(a->dout, a->dtype, a->lddo, a->n) || a->dy == a->dout ||
+        (a->dw && (!a->w || !valid_rows(a->y, a->dtype, a->ldy, a->n) || !aligned(a->dw, 4))) || !aligned(a->w, 4) ||
+        (a->dw && !apart_or_same(a->dy, a->lddy, a->y, a->ldy, 2)))
         return K3MOE_EINVAL;
-    return writing(s, [&] {
-        return k3::launch_combine_backward(dy, (long)lddy, dw, dout, (long)lddo, y, (long)ldy, dtype, n, g, w, cs(s));
-    });
+    return writing(s, [&] { return k3::launch_combine_backward(*a, cs(s)); });
 }
 
 }  // extern "C"

@@ -933,21 +933,23 @@ size_t grouped_matmul_workspace_bytes() { return GM_CTAS * (sizeof(float) * GM_M
 
 int grouped_matmul_rows(int E, long slots, int N, int in) { return tile_rows(E, slots, N, in / 128); }
 
-int launch_grouped_matmul(void *C, int cdt, long ldc, const k3moe_mx8_rows *A, const k3moe_mx_experts *W,
-                          const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s)
+int launch_grouped_matmul(const k3moe_grouped_matmul_desc &d, int *err, cudaStream_t s)
 {
+    const k3moe_mx8_rows *A = d.host_A;
+    const k3moe_mx_experts *W = d.host_W;
+    const k3moe_groups *g = d.host_groups;
     GmArgs a = {};
-    a.atoms = W->atoms, a.atoms_stride = W->atoms_stride;
+    a.atoms = W->atoms, a.atoms_stride = (long)W->atoms_stride;
     a.codes = A->codes, a.scales = A->scales, a.cstride = op_in_padded(A->in), a.sstride = mx8_scale_stride(A->in);
     a.offsets = g->offsets, a.order = g->order;
-    a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = A->rows;
+    a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = d.gather ? 1 : 0, a.xrows = A->rows;
     a.N = W->rows, a.nks = W->in / 128, a.nka = op_k_atoms(W->in), a.tiles_n = (W->rows + GM_M - 1) / GM_M;
     a.counts = (int32_t *)g->workspace;
     a.parts = (float *)(a.counts + GM_CTAS);
-    a.C = C, a.ldc = ldc, a.accumulate = accumulate, a.err = err;
-    a.pairs = cdt == K3MOE_BF16 && a.N % 2 == 0 && ldc % 2 == 0 && ((uintptr_t)C & 3u) == 0;
+    a.C = d.C, a.ldc = (long)d.ldc, a.accumulate = d.accumulate ? 1 : 0, a.err = err;
+    a.pairs = d.c_dtype == K3MOE_BF16 && a.N % 2 == 0 && d.ldc % 2 == 0 && ((uintptr_t)d.C & 3u) == 0;
     if (((long)a.E + a.slots) * a.tiles_n > 0x7fffffffL) return K3MOE_EINVAL;
-    return cdt == K3MOE_BF16 ? launch_gm_ct<__nv_bfloat16>(A, W, a, s) : launch_gm_ct<float>(A, W, a, s);
+    return d.c_dtype == K3MOE_BF16 ? launch_gm_ct<__nv_bfloat16>(A, W, a, s) : launch_gm_ct<float>(A, W, a, s);
 }
 
 }  // namespace k3

@@ -389,20 +389,20 @@ int launch_gw(const GwArgs &a, cudaStream_t s)
 
 }  // namespace
 
-int launch_grouped_wgrad(void *dW, int dwdt, const void *dY, long lddy, const void *X, long ldx, int xrows, int N, int K,
-                         const k3moe_groups *g, int gather, int accumulate, int *err, cudaStream_t s)
+int launch_grouped_wgrad(const k3moe_grouped_wgrad_desc &d, int *err, cudaStream_t s)
 {
+    const k3moe_groups *g = d.host_groups;
     GwArgs a = {};
     a.offsets = g->offsets, a.order = g->order;
-    a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = gather, a.xrows = xrows;
-    const int tiles_k = (K + GW_M - 1) / GW_M;
-    const long tiles = (long)tiles_k * ((N + GW_N - 1) / GW_N);
+    a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = d.gather ? 1 : 0, a.xrows = d.xrows;
+    const int tiles_k = (d.K + GW_M - 1) / GW_M;
+    const long tiles = (long)tiles_k * ((d.N + GW_N - 1) / GW_N);
     if (tiles * a.E > 0x7fffffffL) return K3MOE_EINVAL;
     a.tiles_k = FastDiv((uint32_t)tiles_k), a.tiles_e = FastDiv((uint32_t)tiles);
-    a.N = N, a.K = K, a.accumulate = accumulate, a.err = err;
-    a.dy = (const __nv_bfloat16 *)dY, a.x = (const __nv_bfloat16 *)X, a.dw = dW, a.lddy = lddy, a.ldx = ldx;
-    return dwdt == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(a, s)
-                              : launch_gw<float>(a, s);
+    a.N = d.N, a.K = d.K, a.accumulate = d.accumulate ? 1 : 0, a.err = err;
+    a.dy = (const __nv_bfloat16 *)d.dY, a.x = (const __nv_bfloat16 *)d.X, a.dw = d.dW;
+    a.lddy = (long)d.lddy, a.ldx = (long)d.ldx;
+    return d.dw_dtype == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(a, s) : launch_gw<float>(a, s);
 }
 
 }  // namespace k3

@@ -334,35 +334,36 @@ int launch_groups_plan(const k3moe_groups *g, const int32_t *ids, cudaStream_t s
     return st;
 }
 
-int launch_combine(void *out, long ldo, const void *y, long ldy, int dtype, int n, const k3moe_groups *g, const float *w,
-                   int accumulate, cudaStream_t s)
+int launch_combine(const k3moe_combine_desc &d, cudaStream_t s)
 {
     CombineArgs a = {};
-    a.y = y, a.out = out, a.ldy = ldy, a.ldo = ldo, a.w = w, a.pos = g->pos;
-    a.T = g->tokens, a.k = g->top_k, a.n = n, a.rows = a.T * a.k, a.accumulate = accumulate;
-    a.blocks = (n + 1023) / 1024;
-    const bool vec = n % 8 == 0 && rows16(y, ldy, dtype) && rows16(out, ldo, dtype);
-    void (*const kernel)(CombineArgs) = dtype == K3MOE_BF16 ? (vec ? k3_combine<uint16_t, true> : k3_combine<uint16_t, false>)
-                                                            : (vec ? k3_combine<uint32_t, true> : k3_combine<uint32_t, false>);
+    a.y = d.y, a.out = d.out, a.ldy = (long)d.ldy, a.ldo = (long)d.ldo, a.w = d.w, a.pos = d.host_groups->pos;
+    a.T = d.host_groups->tokens, a.k = d.host_groups->top_k, a.n = d.n, a.rows = a.T * a.k, a.accumulate = d.accumulate;
+    a.blocks = (a.n + 1023) / 1024;
+    const bool vec = a.n % 8 == 0 && rows16(a.y, a.ldy, d.dtype) && rows16(a.out, a.ldo, d.dtype);
+    void (*const kernel)(CombineArgs) = d.dtype == K3MOE_BF16
+                                            ? (vec ? k3_combine<uint16_t, true> : k3_combine<uint16_t, false>)
+                                            : (vec ? k3_combine<uint32_t, true> : k3_combine<uint32_t, false>);
     return launch(kernel, (long)a.T * a.blocks, 128, 0, s, a);
 }
 
-int launch_combine_backward(void *dy, long lddy, float *dw, const void *dout, long lddo, const void *y, long ldy, int dtype,
-                            int n, const k3moe_groups *g, const float *w, cudaStream_t s)
+int launch_combine_backward(const k3moe_combine_backward_desc &d, cudaStream_t s)
 {
     CombineArgs a = {};
-    a.y = y, a.dout = dout, a.dy = dy, a.dw = dw, a.ldy = ldy, a.ldo = lddo, a.lddy = lddy, a.w = w, a.pos = g->pos;
-    a.T = g->tokens, a.k = g->top_k, a.n = n, a.rows = a.T * a.k;
-    const bool vec = n % 8 == 0 && rows16(dout, lddo, dtype) && rows16(dy, lddy, dtype) && (!dw || rows16(y, ldy, dtype));
+    a.y = d.y, a.dout = d.dout, a.dy = d.dy, a.dw = d.dw, a.ldy = (long)d.ldy, a.ldo = (long)d.lddo, a.lddy = (long)d.lddy;
+    a.w = d.w, a.pos = d.host_groups->pos;
+    a.T = d.host_groups->tokens, a.k = d.host_groups->top_k, a.n = d.n, a.rows = a.T * a.k;
+    const bool vec = a.n % 8 == 0 && rows16(a.dout, a.ldo, d.dtype) && rows16(a.dy, a.lddy, d.dtype) &&
+                     (!a.dw || rows16(a.y, a.ldy, d.dtype));
     const bool few = (long)a.T * ((a.k + 7) / 8) <= 2 * num_sms();
     a.blocks = few ? (a.k + 3) / 4 : (a.k + 7) / 8;
     const auto pick = [&](auto small, auto large) { return few ? small : large; };
     void (*const kernel)(CombineArgs) =
-        dtype == K3MOE_BF16 ? (vec ? pick(k3_combine_backward<uint16_t, true, 4>, k3_combine_backward<uint16_t, true, 8>)
-                                   : pick(k3_combine_backward<uint16_t, false, 4>, k3_combine_backward<uint16_t, false, 8>))
-                            : (vec ? pick(k3_combine_backward<uint32_t, true, 4>, k3_combine_backward<uint32_t, true, 8>)
-                                   : pick(k3_combine_backward<uint32_t, false, 4>, k3_combine_backward<uint32_t, false, 8>));
-    return launch(kernel, (long)a.T * a.blocks, std::min(few ? 1024 : 256, (n + 255) / 256 * 32), 0, s, a);
+        d.dtype == K3MOE_BF16 ? (vec ? pick(k3_combine_backward<uint16_t, true, 4>, k3_combine_backward<uint16_t, true, 8>)
+                                     : pick(k3_combine_backward<uint16_t, false, 4>, k3_combine_backward<uint16_t, false, 8>))
+                              : (vec ? pick(k3_combine_backward<uint32_t, true, 4>, k3_combine_backward<uint32_t, true, 8>)
+                                     : pick(k3_combine_backward<uint32_t, false, 4>, k3_combine_backward<uint32_t, false, 8>));
+    return launch(kernel, (long)a.T * a.blocks, std::min(few ? 1024 : 256, (a.n + 255) / 256 * 32), 0, s, a);
 }
 
 }  // namespace k3

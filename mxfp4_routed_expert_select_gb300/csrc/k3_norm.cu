@@ -382,14 +382,14 @@ bool rows16(const void *p, long ld, int dtype)
 
 // Chunks a thread, by the row's length: few, so that the next row's chunks fit in
 // registers beside this one's.
-template <typename T, bool VEC>
+template <typename T, bool WIDE>
 auto pick(int c, bool backward) -> void (*)(NormArgs)
 {
     if (backward)
-        return c == 1 ? k3_norm_backward<T, VEC, 1> : c == 2 ? k3_norm_backward<T, VEC, 2>
-               : c == 4 ? k3_norm_backward<T, VEC, 4> : k3_norm_backward<T, VEC, 8>;
-    return c == 1 ? k3_norm_forward<T, VEC, 1> : c == 2 ? k3_norm_forward<T, VEC, 2>
-           : c == 4 ? k3_norm_forward<T, VEC, 4> : k3_norm_forward<T, VEC, 8>;
+        return c == 1 ? k3_norm_backward<T, WIDE, 1> : c == 2 ? k3_norm_backward<T, WIDE, 2>
+               : c == 4 ? k3_norm_backward<T, WIDE, 4> : k3_norm_backward<T, WIDE, 8>;
+    return c == 1 ? k3_norm_forward<T, WIDE, 1> : c == 2 ? k3_norm_forward<T, WIDE, 2>
+           : c == 4 ? k3_norm_forward<T, WIDE, 4> : k3_norm_forward<T, WIDE, 8>;
 }
 struct NormPlan {
     int c, warps, teams, grid;
@@ -405,14 +405,14 @@ NormPlan norm_plan(int T, int n)
     p.grid = (int)std::min<long>((T + p.teams - 1L) / p.teams, (long)num_sms() * std::max(1, 1024 / threads));
     return p;
 }
-int launch_norm(NormArgs a, int dtype, bool vec, bool backward, const NormPlan &p, cudaStream_t s)
+int launch_norm(NormArgs a, int dtype, bool wide, bool backward, const NormPlan &p, cudaStream_t s)
 {
     a.warps = p.warps;
     a.inv_n = 1.f / (float)a.n;
-    vec = vec && a.n % 8 == 0;
+    wide = wide && a.n % 8 == 0;
     void (*const kernel)(NormArgs) = dtype == K3MOE_BF16
-                                         ? (vec ? pick<uint16_t, true>(p.c, backward) : pick<uint16_t, false>(p.c, backward))
-                                         : (vec ? pick<uint32_t, true>(p.c, backward) : pick<uint32_t, false>(p.c, backward));
+                                         ? (wide ? pick<uint16_t, true>(p.c, backward) : pick<uint16_t, false>(p.c, backward))
+                                         : (wide ? pick<uint32_t, true>(p.c, backward) : pick<uint32_t, false>(p.c, backward));
     if (launch_pdl(kernel, dim3((unsigned)p.grid), dim3((unsigned)(p.warps * p.teams * 32)), 0, s, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
@@ -448,39 +448,35 @@ int launch_mx8(K pick_kernel, Mx8Args a, int dtype, int rows, bool vec, cudaStre
 
 size_t norm_workspace_bytes(int n) { return (size_t)NORM_PARTS * (size_t)n * sizeof(float); }
 
-int launch_norm_forward(void *y, long ldy, void *r, long ldr, float *rstd, const k3moe_mx8_rows *y8, const void *x,
-                        long ldx, const void *delta, long ldd, const float *gain, int dtype, int T, int n, float eps,
-                        cudaStream_t s)
+int launch_norm_forward(const k3moe_norm_forward_desc &d, cudaStream_t s)
 {
     NormArgs a = {};
-    a.x = x, a.delta = delta, a.y = y, a.r = r;
-    a.ldx = ldx, a.ldd = ldd, a.ldy = ldy, a.ldr = ldr;
-    a.gain = gain, a.rstd = rstd;
-    if (y8) a.codes = y8->codes, a.scales = y8->scales;
-    a.T = T, a.n = n, a.eps = eps;
-    const bool vec = rows16(x, ldx, dtype) && (!delta || rows16(delta, ldd, dtype)) && (!y || rows16(y, ldy, dtype)) &&
-                     (!r || rows16(r, ldr, dtype));
-    return launch_norm(a, dtype, vec, false, norm_plan(T, n), s);
+    a.x = d.x, a.delta = d.delta, a.y = d.y, a.r = d.r;
+    a.ldx = (long)d.ldx, a.ldd = (long)d.ldd, a.ldy = (long)d.ldy, a.ldr = (long)d.ldr;
+    a.gain = d.gain, a.rstd = d.rstd;
+    if (d.host_y8) a.codes = d.host_y8->codes, a.scales = d.host_y8->scales;
+    a.T = d.T, a.n = d.n, a.eps = d.eps;
+    const bool wide = rows16(d.x, a.ldx, d.dtype) && (!d.delta || rows16(d.delta, a.ldd, d.dtype)) &&
+                      (!d.y || rows16(d.y, a.ldy, d.dtype)) && (!d.r || rows16(d.r, a.ldr, d.dtype));
+    return launch_norm(a, d.dtype, wide, false, norm_plan(d.T, d.n), s);
 }
 
-int launch_norm_backward(void *dx, long lddx, float *dgain, int accumulate, const void *dy, long lddy, const void *dr,
-                         long lddr, const void *r, long ldr, const float *rstd, const float *gain, int dtype, int T,
-                         int n, void *ws, cudaStream_t s)
+int launch_norm_backward(const k3moe_norm_backward_desc &d, cudaStream_t s)
 {
     NormArgs a = {};
-    a.x = r, a.dy = dy, a.dr = dr, a.dx = dx;
-    a.ldx = ldr, a.lddy = lddy, a.lddr = lddr, a.lddx = lddx;
-    a.gain = gain, a.rstd = (float *)rstd;
-    a.parts = dgain ? (float *)ws : nullptr;
-    a.T = T, a.n = n;
-    const bool vec = rows16(r, ldr, dtype) && rows16(dy, lddy, dtype) && (!dr || rows16(dr, lddr, dtype)) &&
-                     rows16(dx, lddx, dtype);
-    NormPlan p = norm_plan(T, n);
+    a.x = d.r, a.dy = d.dy, a.dr = d.dr, a.dx = d.dx;
+    a.ldx = (long)d.ldr, a.lddy = (long)d.lddy, a.lddr = (long)d.lddr, a.lddx = (long)d.lddx;
+    a.gain = d.gain, a.rstd = (float *)d.rstd;
+    a.parts = d.dgain ? (float *)d.workspace : nullptr;
+    a.T = d.T, a.n = d.n;
+    const bool wide = rows16(d.r, a.ldx, d.dtype) && rows16(d.dy, a.lddy, d.dtype) &&
+                      (!d.dr || rows16(d.dr, a.lddr, d.dtype)) && rows16(d.dx, a.lddx, d.dtype);
+    NormPlan p = norm_plan(d.T, d.n);
     p.grid = std::min(p.grid, NORM_PARTS / p.teams);
-    const int st = launch_norm(a, dtype, vec, true, p, s);
-    if (st != K3MOE_OK || !dgain) return st;
-    if (launch_pdl(k3_norm_columns, dim3((unsigned)((n + 31) / 32)), dim3(NC_WARPS * 32), 0, s, dgain, (const float *)ws, n,
-                   p.grid * p.teams, accumulate) != cudaSuccess) {
+    const int st = launch_norm(a, d.dtype, wide, true, p, s);
+    if (st != K3MOE_OK || !d.dgain) return st;
+    if (launch_pdl(k3_norm_columns, dim3((unsigned)((d.n + 31) / 32)), dim3(NC_WARPS * 32), 0, s, d.dgain,
+                   (const float *)d.workspace, (int)d.n, p.grid * p.teams, d.accumulate ? 1 : 0) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }

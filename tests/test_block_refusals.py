@@ -12,6 +12,15 @@ EINVAL = k.K3MOE_EINVAL
 P, Q, R, S = 4096, 2 << 20, 4 << 20, 6 << 20  # pointers that are never followed
 
 
+def addr(ref):
+    """Address behind a byref (0 for None)."""
+    return 0 if ref is None else ctypes.cast(ref, ctypes.c_void_p).value
+
+
+def pack(S, *a):
+    return S.pack(*(0 if v is None else v for v in a))
+
+
 def rows8(rows=4, n=64, codes=P, scales=P):
     return ctypes.byref(k.Mx8RowsStruct(codes, scales, rows, n))
 
@@ -57,8 +66,10 @@ def test_norm_forward():
                 dict(eps=-1e-6), dict(eps=float("nan")), dict(eps=float("inf")), dict(y8=rows8(5)), dict(y8=rows8(4, 63)),
                 dict(y=P, ldy=72), dict(y=S, ldy=72), dict(r=P, ldr=72), dict(r=S, ldr=72), *(dict(y8=b) for b in BAD_ROWS[1:])):
         a = {**good, **bad}
-        assert k.lib().k3moe_norm_forward(a["y"], a["ldy"], a["r"], a["ldr"], a["rstd"], a["y8"], a["x"], a["ldx"], a["d"],
-                                          a["ldd"], a["gain"], a["dt"], a["T"], a["n"], a["eps"], None) == EINVAL, bad
+        d = pack(k.NORM_FORWARD, a["y"], a["ldy"], a["r"], a["ldr"], a["rstd"], addr(a["y8"]), a["x"], a["ldx"], a["d"],
+                 a["ldd"], a["gain"], a["dt"], a["T"], a["n"], a["eps"])
+        assert k.lib().k3moe_norm_forward(d, None) == EINVAL, bad
+    assert k.lib().k3moe_norm_forward(None, None) == EINVAL
 
 
 def test_norm_backward():
@@ -69,9 +80,10 @@ def test_norm_backward():
                 dict(dg=P + 2), dict(ws=None), dict(ws=P + 8), dict(nws=ws - 1), dict(dt=3), dict(T=0), dict(n=0),
                 dict(dx=R, lddx=72), dict(dx=S, lddx=72), dict(dx=P, lddx=72)):
         a = {**good, **bad}
-        assert k.lib().k3moe_norm_backward(a["dx"], a["lddx"], a["dg"], 0, a["dy"], a["lddy"], a["dr"], a["lddr"], a["r"],
-                                           a["ldr"], a["rstd"], a["gain"], a["dt"], a["T"], a["n"], a["ws"], a["nws"],
-                                           None) == EINVAL, bad
+        d = pack(k.NORM_BACKWARD, a["dx"], a["lddx"], a["dg"], a["dy"], a["lddy"], a["dr"], a["lddr"], a["r"], a["ldr"],
+                 a["rstd"], a["gain"], a["ws"], a["nws"], a["dt"], a["T"], a["n"], 0)
+        assert k.lib().k3moe_norm_backward(d, None) == EINVAL, bad
+    assert k.lib().k3moe_norm_backward(None, None) == EINVAL
 
 
 BAD_GROUPS = (None, groups(0), groups(1025), groups(kk=0), groups(kk=33), groups(T=0), groups(T=1 << 30), groups(offsets=None),
@@ -97,8 +109,9 @@ def test_matmul():
            *(dict(A=b) for b in BAD_ROWS), *(dict(g=b) for b in BAD_GROUPS)]
     for b in bad:
         a = {**good, **b}
-        assert k.lib().k3moe_grouped_matmul(a["C"], a["dt"], a["ldc"], a["A"], a["W"], a["g"], a["gather"], a["acc"],
-                                            None) == EINVAL, b
+        d = pack(k.GROUPED_MATMUL, a["C"], a["ldc"], addr(a["A"]), addr(a["W"]), addr(a["g"]), a["dt"], a["gather"], a["acc"])
+        assert k.lib().k3moe_grouped_matmul(d, None) == EINVAL, b
+    assert k.lib().k3moe_grouped_matmul(None, None) == EINVAL
 
 
 def test_stored_experts():
@@ -127,8 +140,10 @@ def test_wgrad():
            dict(N=0), dict(K=20), dict(K=0), dict(xr=(1 << 30) + 1), *(dict(g=b) for b in BAD_GROUPS)]
     for b in bad:
         a = {**good, **b}
-        assert k.lib().k3moe_grouped_wgrad(a["dw"], a["dt"], a["dy"], a["lddy"], a["x"], a["ldx"], a["xr"], a["N"], a["K"],
-                                           a["g"], a["gather"], a["acc"], None) == EINVAL, b
+        d = pack(k.GROUPED_WGRAD, a["dw"], a["dy"], a["lddy"], a["x"], a["ldx"], addr(a["g"]), a["dt"], a["xr"], a["N"], a["K"],
+                 a["gather"], a["acc"])
+        assert k.lib().k3moe_grouped_wgrad(d, None) == EINVAL, b
+    assert k.lib().k3moe_grouped_wgrad(None, None) == EINVAL
 
 
 def test_combine():
@@ -138,13 +153,47 @@ def test_combine():
             *(dict(g=b) for b in BAD_GROUPS)]
     for b in both + [dict(y=None), dict(o=Q)]:
         a = {**good, **b}
-        assert k.lib().k3moe_combine(a["o"], a["ldo"], a["y"], a["ldy"], a["dt"], a["n"], a["g"], a["w"], 0, None) == EINVAL, b
+        d = pack(k.COMBINE, a["o"], a["ldo"], a["y"], a["ldy"], a["w"], addr(a["g"]), a["dt"], a["n"], 0)
+        assert k.lib().k3moe_combine(d, None) == EINVAL, b
     good.update(dy=R, lddy=64, dw=P)
     for b in both + [dict(y=None), dict(dy=None), dict(dy=R + 2), dict(lddy=63), dict(dy=P), dict(w=None), dict(dw=P + 2),
                      dict(dy=Q, lddy=72)]:
         a = {**good, **b}
-        assert k.lib().k3moe_combine_backward(a["dy"], a["lddy"], a["dw"], a["o"], a["ldo"], a["y"], a["ldy"], a["dt"], a["n"],
-                                              a["g"], a["w"], None) == EINVAL, b
+        d = pack(k.COMBINE_BACKWARD, a["dy"], a["lddy"], a["dw"], a["o"], a["ldo"], a["y"], a["ldy"], a["w"], addr(a["g"]),
+                 a["dt"], a["n"])
+        assert k.lib().k3moe_combine_backward(d, None) == EINVAL, b
+    assert k.lib().k3moe_combine(None, None) == EINVAL and k.lib().k3moe_combine_backward(None, None) == EINVAL
+
+
+def test_packed_descriptions_have_the_header_s_layout():
+    """Sizes and the place of the last field, by the C compiler."""
+    import shutil
+    import subprocess
+    import tempfile
+    from conftest import ROOT
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no gcc")
+    last = {"norm_forward": ("NORM_FORWARD", "eps"), "norm_backward": ("NORM_BACKWARD", "accumulate"),
+            "grouped_matmul": ("GROUPED_MATMUL", "accumulate"), "grouped_wgrad": ("GROUPED_WGRAD", "accumulate"),
+            "combine": ("COMBINE", "accumulate"), "combine_backward": ("COMBINE_BACKWARD", "n")}
+    src = "#include <stdio.h>\n#include \"k3moe.h\"\nint main(void) {\n" + "".join(
+        'printf("%%d %%d\\n", (int)sizeof(k3moe_%s_desc), (int)offsetof(k3moe_%s_desc, %s));\n' % (n, n, f)
+        for n, (_, f) in last.items()) + "return 0; }\n"
+    with tempfile.TemporaryDirectory() as d:
+        r = subprocess.run([gcc, "-I", ROOT + "/include", "-x", "c", "-", "-o", d + "/a"], input=src, text=True,
+                           capture_output=True)
+        assert r.returncode == 0, r.stderr
+        out = subprocess.run([d + "/a"], capture_output=True, text=True).stdout.split()
+    for i, (S, f) in enumerate(last.values()):
+        S = getattr(k, S)
+        marks = S.unpack(S.pack(*range(1, 1 + len(S.unpack(bytes(S.size))))))
+        assert S.size == int(out[2 * i]), f
+        data = bytearray(S.size)
+        probe = S.pack(*([0] * (len(marks) - 1) + [1]))
+        data[:] = probe
+        first = next(j for j, v in enumerate(data) if v)
+        assert first // 4 * 4 == int(out[2 * i + 1]), f
 
 
 @pytest.fixture(params=["objects on the CPU too", "objects on GPU 0"])
