@@ -170,8 +170,8 @@ K3_DEV GmTile gm_tile(const GmTable &tab, const GmArgs &a, int u)
 }
 // What a CTA works on as its i-th piece: whole tiles in turn over the CTAs, as many as
 // make full waves, and of the tiles that are left a part along K, several CTAs to a tile
-// where there are enough (1 token x 16 experts x 1536 x 7168, 192 tiles on 152 SMs: %s
-// us against %s).  slot: where a part leaves its sums; u < 0: nothing more.
+// where there are enough (1 token x 16 experts x 1536 x 7168, 192 tiles on 152 SMs: 24.9
+// us against 29.8).  slot: where a part leaves its sums; u < 0: nothing more.
 struct GmPart {
     int u, k0, k1, of, slot;
 };

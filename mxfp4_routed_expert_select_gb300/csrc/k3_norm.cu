@@ -337,7 +337,7 @@ __global__ void __launch_bounds__(NC_WARPS * 32) k3_norm_columns(float *dgain, c
 
 // ------------------------------------------------------------- 8-bit rows
 
-constexpr int M8_THREADS = 256;
+constexpr int M8_THREADS = 256, M8_U = 2;
 
 struct Mx8Args {
     const void *x;
@@ -349,30 +349,50 @@ struct Mx8Args {
     FastDiv cpr;  // chunks per row, ceil128(in) / 8
 };
 
-template <typename T, bool VEC>
+// A thread has U chunks, a CTA's threads apart, all loaded before the first is used
+// (4096 x 7168 bf16: quantised in 16.3 us, with one in 18.5; the values in 12.6, 15.2).
+template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(M8_THREADS) k3_mx8_quantize(const Mx8Args a)
 {
     griddep_wait();
-    const uint32_t i = blockIdx.x * M8_THREADS + threadIdx.x;
-    const uint32_t t = a.cpr.div(i);
-    const int c = i < a.n ? (int)(i - t * a.cpr.d) * 8 : INT_MAX - 8;
-    const Raw<T> v = load8<T, VEC>(a.x, a.ld, (int)t, c, a.in);
-    store_mx8(a.codes, a.scales, a.in, (int)t, c, v);
+    const uint32_t i0 = blockIdx.x * (M8_THREADS * U) + threadIdx.x;
+    Raw<T> v[U];
+    int t[U], c[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const uint32_t i = i0 + u * M8_THREADS;
+        t[u] = (int)a.cpr.div(i);
+        c[u] = i < a.n ? (int)(i - (uint32_t)t[u] * a.cpr.d) * 8 : INT_MAX - 8;
+        v[u] = load8<T, VEC>(a.x, a.ld, t[u], c[u], a.in);
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) store_mx8(a.codes, a.scales, a.in, t[u], c[u], v[u]);
 }
-template <typename T, bool VEC>
+template <typename T, bool VEC, int U>
 __global__ void __launch_bounds__(M8_THREADS) k3_mx8_dequantize(const Mx8Args a)
 {
     griddep_wait();
-    const uint32_t i = blockIdx.x * M8_THREADS + threadIdx.x;
-    if (i >= a.n) return;
-    const uint32_t t = a.cpr.div(i);
-    const int c = (int)(i - t * a.cpr.d) * 8;
-    if (c >= a.in) return;
-    const uint2 q = *(const uint2 *)(a.codes + (long)t * op_in_padded(a.in) + c);
-    const uint32_t e = a.scales[(long)t * mx8_scale_stride(a.in) + c / 32];
-    float v[8];
-    from_e4m3x8(q, e, v);
-    store8<T, VEC>(a.y, a.ld, (int)t, c, a.in, v);
+    const uint32_t i0 = blockIdx.x * (M8_THREADS * U) + threadIdx.x;
+    uint2 q[U];
+    uint32_t e[U];
+    int t[U], c[U];
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        const uint32_t i = i0 + u * M8_THREADS;
+        t[u] = (int)a.cpr.div(i);
+        c[u] = i < a.n ? (int)(i - (uint32_t)t[u] * a.cpr.d) * 8 : a.in;
+        if (c[u] < a.in) {
+            q[u] = *(const uint2 *)(a.codes + (long)t[u] * op_in_padded(a.in) + c[u]);
+            e[u] = a.scales[(long)t[u] * mx8_scale_stride(a.in) + c[u] / 32];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < U; u++) {
+        if (c[u] >= a.in) continue;
+        float v[8];
+        from_e4m3x8(q[u], e[u], v);
+        store8<T, VEC>(a.y, a.ld, t[u], c[u], a.in, v);
+    }
 }
 
 bool rows16(const void *p, long ld, int dtype)
@@ -432,7 +452,8 @@ int launch_mx8(K pick_kernel, Mx8Args a, int dtype, int rows, bool vec, cudaStre
     for (int t = 0; t < rows; t += step) {
         const int r = std::min(step, rows - t);
         a.n = (uint32_t)r * cpr;
-        if (launch_pdl(kernel, dim3((a.n + M8_THREADS - 1) / M8_THREADS), dim3(M8_THREADS), 0, s, a) != cudaSuccess) {
+        const uint32_t each = M8_THREADS * M8_U;
+        if (launch_pdl(kernel, dim3((a.n + each - 1) / each), dim3(M8_THREADS), 0, s, a) != cudaSuccess) {
             cudaGetLastError();
             return K3MOE_ECUDA;
         }
@@ -489,8 +510,8 @@ int launch_mx8_quantize(const k3moe_mx8_rows *o, const void *x, int dtype, long 
     a.x = x, a.ld = ld, a.codes = o->codes, a.scales = o->scales, a.in = o->in;
     return launch_mx8(
         [](bool bf16, bool vec) {
-            return bf16 ? (vec ? k3_mx8_quantize<uint16_t, true> : k3_mx8_quantize<uint16_t, false>)
-                        : (vec ? k3_mx8_quantize<uint32_t, true> : k3_mx8_quantize<uint32_t, false>);
+            return bf16 ? (vec ? k3_mx8_quantize<uint16_t, true, M8_U> : k3_mx8_quantize<uint16_t, false, M8_U>)
+                        : (vec ? k3_mx8_quantize<uint32_t, true, M8_U> : k3_mx8_quantize<uint32_t, false, M8_U>);
         },
         a, dtype, o->rows, rows16(x, ld, dtype), s);
 }
@@ -500,8 +521,8 @@ int launch_mx8_dequantize(void *y, int dtype, long ld, const k3moe_mx8_rows *o, 
     a.y = y, a.ld = ld, a.codes = o->codes, a.scales = o->scales, a.in = o->in;
     return launch_mx8(
         [](bool bf16, bool vec) {
-            return bf16 ? (vec ? k3_mx8_dequantize<uint16_t, true> : k3_mx8_dequantize<uint16_t, false>)
-                        : (vec ? k3_mx8_dequantize<uint32_t, true> : k3_mx8_dequantize<uint32_t, false>);
+            return bf16 ? (vec ? k3_mx8_dequantize<uint16_t, true, M8_U> : k3_mx8_dequantize<uint16_t, false, M8_U>)
+                        : (vec ? k3_mx8_dequantize<uint32_t, true, M8_U> : k3_mx8_dequantize<uint32_t, false, M8_U>);
         },
         a, dtype, o->rows, rows16(y, ld, dtype), s);
 }
