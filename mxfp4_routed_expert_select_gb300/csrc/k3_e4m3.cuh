@@ -6,6 +6,12 @@
 
 namespace k3 {
 
+// Rows that are all 16-byte aligned.
+inline bool rows16(const void *p, long ld, int dtype)
+{
+    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
+}
+
 // Eight values of a row as loaded.
 template <typename T>
 struct Raw {

@@ -23,7 +23,7 @@ namespace {
 constexpr int GR_THREADS = 1024, GR_WARPS = GR_THREADS / 32;
 constexpr int GR_WHOLE = 4096;  // slots that one CTA sorts alone; a warp's run fits the 16-bit counts
 constexpr int GR_CHUNK = 2048;  // slots of a CTA where there are more
-constexpr int GR_FEW = 64;      // chunks whose counts each CTA sums itself
+constexpr int GR_FEW = 256;     // chunks whose counts each CTA sums itself
 
 struct GroupArgs {
     const int32_t *ids;
@@ -65,10 +65,11 @@ K3_DEV int expert_of(const GroupArgs &a, int slot, int end)
     return e >= 0 && e < a.E ? e : -1;
 }
 
-// WHOLE: one chunk is the batch.  Otherwise COUNT leaves the chunk's counts, and the
-// placing pass reads where each expert's slots of this chunk start: sums over the chunks'
-// counts, which each CTA forms itself where there are few (SCAN; one launch less, 65536
-// slots: 13 instead of 17 us), else a scan's results.
+// WHOLE: one chunk is the batch (4096 slots of 896 experts: 9.8 us, 10.7 in chunks; 2048:
+// 6.7 and 10.5).  Otherwise COUNT leaves the chunk's counts, and the placing pass reads
+// where each expert's slots of this chunk start: sums over the chunks' counts, which each
+// CTA forms itself where there are few (SCAN; one launch less: 65536 slots 12.2 us, with
+// a scan's results 15.0; 2^19 42 and 54, 2^20 122 and 104).
 template <bool WHOLE, bool COUNT, bool SCAN>
 __global__ void __launch_bounds__(GR_THREADS) k3_groups(const GroupArgs a)
 {
@@ -238,8 +239,10 @@ __global__ void __launch_bounds__(128) k3_combine(const CombineArgs a)
 
 // dy[pos[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[pos[t][j]]>.  A CTA takes
 // DEEP slots of a token, its threads eight columns at a time; the dot products are
-// joined together.  DEEP 4 and up to 1024 threads where a batch has few tokens (64
-// tokens x 16 x 7168 bf16: 9.9 us, 15.4 with a CTA of 256 for all 16), else 8 and 256.
+// joined together.  DEEP 4 and up to 1024 threads where a batch has no more tokens than
+// fill the SMs once, else 8 and 256 (7168 bf16, us: 16 tokens x 16 3.5 and 5.9, 64 x 16 6.3
+// and 6.6, 128 x 16 11.8 and 9.1, 1024 x 16 106 and 84; 152 x 8 6.6 and 6.8, 256 x 8 11.8
+// and 9.0).
 template <typename T, bool VEC, int DEEP>
 __global__ void __launch_bounds__(DEEP == 4 ? 1024 : 256) k3_combine_backward(const CombineArgs a)
 {
@@ -272,6 +275,7 @@ __global__ void __launch_bounds__(DEEP == 4 ? 1024 : 256) k3_combine_backward(co
                 if (p[j] >= 0)
 #pragma unroll
                     for (int i = 0; i < 8; i++) dot[j] += d[i] * value(r[j], i);
+        asm volatile("" ::: "memory");  // y is read before dy is written: they may be one
 #pragma unroll
         for (int j = 0; j < DEEP; j++)
             if (p[j] >= 0) {
@@ -296,10 +300,6 @@ __global__ void __launch_bounds__(DEEP == 4 ? 1024 : 256) k3_combine_backward(co
     }
 }
 
-bool rows16(const void *p, long ld, int dtype)
-{
-    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
-}
 template <typename... KArgs, typename... Args>
 int launch(void (*kernel)(KArgs...), long grid, int threads, size_t smem, cudaStream_t s, const Args &...args)
 {
@@ -355,7 +355,7 @@ int launch_combine_backward(const k3moe_combine_backward_desc &d, cudaStream_t s
     a.T = d.host_groups->tokens, a.k = d.host_groups->top_k, a.n = d.n, a.rows = a.T * a.k;
     const bool vec = a.n % 8 == 0 && rows16(a.dout, a.ldo, d.dtype) && rows16(a.dy, a.lddy, d.dtype) &&
                      (!a.dw || rows16(a.y, a.ldy, d.dtype));
-    const bool few = (long)a.T * ((a.k + 7) / 8) <= 2 * num_sms();
+    const bool few = (long)a.T * ((a.k + 7) / 8) <= num_sms();
     a.blocks = few ? (a.k + 3) / 4 : (a.k + 7) / 8;
     const auto pick = [&](auto small, auto large) { return few ? small : large; };
     void (*const kernel)(CombineArgs) =

@@ -9,7 +9,12 @@
 // values a thread, and takes one row after the other, so that its gains (and the
 // sums of dgain) stay in registers and the next row's loads are in flight while
 // this one's sum is joined.  The column sums of the teams meet in a second small
-// kernel, in an order that does not depend on timing.
+// kernel, in an order that does not depend on timing.  Rows too long for that are read
+// twice by a CTA, the second time from L2.
+//
+// bf16, x, delta, r and y or the backward call's four: 8192 x 4096 44 us (6.1 TB/s) and
+// 56, 8192 x 8192 85 (6.3) and 99, 8192 x 32768 385 (5.6) and 602; 4096 x 7168 to 8 bits
+// 39 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -92,23 +97,18 @@ K3_DEV float fine_rstd(float ss, float n, float inv_n, float eps)
 
 // 1 / sqrt(mean v^2 + eps) where the sum of squares left fp32's range or its normal
 // numbers while its root need not: the values scaled by a power of two.
-template <int C>
-K3_DEV float far_rstd(Team &team, const float (&v)[C][8], float ss, float inv_n, float eps)
+// each(f) calls f with this thread's values.
+template <typename F>
+K3_DEV float far_rstd(Team &team, F each, float ss, float inv_n, float eps)
 {
     float m = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) m = fmaxf(m, fabsf(v[c][i]));
+    each([&](float v) { m = fmaxf(m, fabsf(v)); });
     m = team.max(m);
     if (!(m > 0.f) || m > 3.4028235e38f || ss != ss) return rsqrtf(ss * inv_n + eps);
     const int e = max(-126, min(126, 126 - (int)(__float_as_uint(m) >> 23)));
     const float s = __uint_as_float((uint32_t)(127 + e) << 23);
     float t = 0.f;
-#pragma unroll
-    for (int c = 0; c < C; c++)
-#pragma unroll
-        for (int i = 0; i < 8; i++) t += v[c][i] * s * (v[c][i] * s);
+    each([&](float v) { t += v * s * (v * s); });
     t = team.sum(t);
     const float es = eps * s * s;
     return es > 1e37f ? rsqrtf(eps) : rsqrtf(t * inv_n + es) * s;
@@ -122,10 +122,11 @@ K3_DEV Team make_team(int warps, float (*slots)[64], int &first, int &step)
     step = (int)gridDim.x * teams;
     return Team{warps, w - id * warps, (int)threadIdx.x & 31, 1 + id, slots[id], 0};
 }
-// A thread's columns.  WIDE (every row 16-byte aligned, n a multiple of 8): C chunks of
-// eight, 16-byte accesses.  Otherwise 8 C single values, 32 neighbours to a warp, so
-// that rows of any alignment are read and written whole sectors at a time.
-template <bool WIDE, int C>
+// A thread's columns.  WIDE (every row 16-byte aligned, n a multiple of 8): chunks of
+// eight, 16-byte accesses.  Otherwise a chunk is eight single values, each the neighbour
+// of the next lane's, so that rows of any alignment are read and written whole sectors
+// at a time.
+template <bool WIDE>
 struct Cols {
     int first, step, n;  // of chunk 0 or value 0; to the next chunk or value
 
@@ -170,35 +171,29 @@ struct Cols {
                     p[at(c, i)] = __float_as_uint(v[i]);
             }
     }
-    K3_DEV void load_gain(float (&g)[C][8], const float *gain) const
+    K3_DEV void load_gain(float (&g)[8], const float *gain, int c) const
     {
+        if (WIDE && gain && ((uintptr_t)gain & 15u) == 0) {
+            const int col = min(first + c * step, n - 8);
+            const float4 a = *(const float4 *)(gain + col), b = *(const float4 *)(gain + col + 4);
+            g[0] = a.x, g[1] = a.y, g[2] = a.z, g[3] = a.w;
+            g[4] = b.x, g[5] = b.y, g[6] = b.z, g[7] = b.w;
+        } else {
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            if (WIDE && gain && ((uintptr_t)gain & 15u) == 0) {
-                const int col = min(first + c * step, n - 8);
-                const float4 a = *(const float4 *)(gain + col), b = *(const float4 *)(gain + col + 4);
-                g[c][0] = a.x, g[c][1] = a.y, g[c][2] = a.z, g[c][3] = a.w;
-                g[c][4] = b.x, g[c][5] = b.y, g[c][6] = b.z, g[c][7] = b.w;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) g[c][i] = gain && at(c, i) < n ? gain[at(c, i)] : 1.f;
-            }
+            for (int i = 0; i < 8; i++) g[i] = gain && at(c, i) < n ? gain[at(c, i)] : 1.f;
         }
     }
-    // Row t in 8 bits; called by whole warps.
-    K3_DEV void store_8bit(uint8_t *codes, uint8_t *scales, int t, const float (&v)[C][8]) const
+    // A chunk of row t in 8 bits; called by whole warps.
+    K3_DEV void store_8bit(uint8_t *codes, uint8_t *scales, int t, int c, const float (&v)[8]) const
     {
+        if constexpr (WIDE) {
+            Raw<uint32_t> q;
 #pragma unroll
-        for (int c = 0; c < C; c++) {
-            if constexpr (WIDE) {
-                Raw<uint32_t> q;
+            for (int i = 0; i < 8; i++) q.w[i] = first + c * step < n ? __float_as_uint(v[i]) : 0u;
+            store_mx8(codes, scales, n, t, first + c * step, q);
+        } else {
 #pragma unroll
-                for (int i = 0; i < 8; i++) q.w[i] = first + c * step < n ? __float_as_uint(v[c][i]) : 0u;
-                store_mx8(codes, scales, n, t, first + c * step, q);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; i++) store_mx8_block(codes, scales, n, t, at(c, i), at(c, i) < n ? v[c][i] : 0.f);
-            }
+            for (int i = 0; i < 8; i++) store_mx8_block(codes, scales, n, t, at(c, i), at(c, i) < n ? v[i] : 0.f);
         }
     }
 };
@@ -211,7 +206,7 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
     griddep_launch_dependents();
     int t, step;
     Team team = make_team(a.warps, slots, t, step);
-    const Cols<WIDE, C> cols(team, a.n);
+    const Cols<WIDE> cols(team, a.n);
     Raw<T> x[C], d[C];
     auto load = [&](int row) {
 #pragma unroll
@@ -222,7 +217,8 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
     };
     load(t);
     float gn[C][8];
-    cols.load_gain(gn, a.gain);
+#pragma unroll
+    for (int c = 0; c < C; c++) cols.load_gain(gn[c], a.gain, c);
     for (; t < a.T; t += step) {
         float v[C][8], ss = 0.f;
 #pragma unroll
@@ -241,7 +237,15 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
         // the sum is exact enough unless it left the normal range, or fell below
         // where eps outweighs what it lost
         float s = fine_rstd(ss, (float)a.n, a.inv_n, a.eps);
-        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f)) s = far_rstd<C>(team, v, ss, a.inv_n, a.eps);
+        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f)) 
+            s = far_rstd(
+                team, [&](auto &&take) {
+#pragma unroll
+                    for (int c = 0; c < C; c++)
+#pragma unroll
+                        for (int i = 0; i < 8; i++) take(v[c][i]);
+                },
+                ss, a.inv_n, a.eps);
         if (a.rstd && team.warp == 0 && team.lane == 0) a.rstd[t] = s;
 #pragma unroll
         for (int c = 0; c < C; c++)
@@ -250,7 +254,9 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
         if (a.y)
 #pragma unroll
             for (int c = 0; c < C; c++) cols.template store<T>(a.y, a.ldy, t, c, v[c]);
-        if (a.codes) cols.store_8bit(a.codes, a.scales, t, v);
+        if (a.codes)
+#pragma unroll
+            for (int c = 0; c < C; c++) cols.store_8bit(a.codes, a.scales, t, c, v[c]);
     }
 }
 
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
     int t, step;
     Team team = make_team(a.warps, slots, t, step);
     const int part = t;
-    const Cols<WIDE, C> cols(team, a.n);
+    const Cols<WIDE> cols(team, a.n);
     Raw<T> x[C], dy[C], dr[C];
     float s = 0.f;
     auto load = [&](int row) {
@@ -277,11 +283,12 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
     };
     load(t);
     float gn[C][8], sum[C][8];
-    cols.load_gain(gn, a.gain);
 #pragma unroll
-    for (int c = 0; c < C; c++)
+    for (int c = 0; c < C; c++) {
+        cols.load_gain(gn[c], a.gain, c);
 #pragma unroll
         for (int i = 0; i < 8; i++) sum[c][i] = 0.f;
+    }
     for (; t < a.T; t += step) {
         float xh[C][8], g[C][8], res[C][8], dot = 0.f;
         const float sc = s;
@@ -311,6 +318,161 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
 #pragma unroll
             for (int i = 0; i < 8; i++)
                 if (cols.at(c, i) < a.n) a.parts[(long)part * a.n + cols.at(c, i)] = sum[c][i];
+}
+
+// Rows that do not fit in registers: a CTA holds one after the other and reads each
+// twice, the second time from L2, U chunks a thread at a time (a load does not pass the
+// stores before it).
+constexpr int LONG_THREADS = 512, LONG_CTAS = 2;  // of an SM
+
+K3_DEV Team long_team(float *slots)
+{
+    return Team{LONG_THREADS / 32, (int)threadIdx.x >> 5, (int)threadIdx.x & 31, 1, slots, 0};
+}
+
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(const NormArgs a)
+{
+    constexpr int U = WIDE && sizeof(T) == 2 ? 2 : 1;
+    __shared__ float slots[64];
+    griddep_wait();
+    griddep_launch_dependents();
+    Team team = long_team(slots);
+    const Cols<WIDE> cols(team, a.n);
+    const int chunks = (a.n + LONG_THREADS * 8 - 1) / (LONG_THREADS * 8);
+    for (int t = (int)blockIdx.x; t < a.T; t += (int)gridDim.x) {
+        // f(c, v) with the values of r, read as such (stored) or made from x and delta
+        auto row = [&](bool stored, auto &&f) {
+#pragma unroll U == 2 || !WIDE ? 1 : 2
+            for (int c0 = 0; c0 < chunks; c0 += U) {
+                Raw<T> x[U], d[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    x[u] = cols.template load<T>(stored ? a.r : a.x, stored ? a.ldr : a.ldx, t, c0 + u, true);
+                    if (a.delta && !stored) d[u] = cols.template load<T>(a.delta, a.ldd, t, c0 + u, true);
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    float v[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        v[i] = value(x[u], i);
+                        if (a.delta && !stored) v[i] = rounded<T>(v[i] + value(d[u], i));
+                    }
+                    f(c0 + u, v);
+                }
+            }
+        };
+        float ss = 0.f;
+        row(false, [&](int c, float (&v)[8]) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) ss += v[i] * v[i];
+            if (a.r) cols.template store<T>(a.r, a.ldr, t, c, v);
+        });
+        asm volatile("" ::: "memory");  // r, which may lie over x, is stored before it is read again
+        const bool stored = a.r != nullptr;
+        ss = team.sum(ss);
+        float s = fine_rstd(ss, (float)a.n, a.inv_n, a.eps);
+        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f))
+            s = far_rstd(
+                team, [&](auto &&take) {
+                    row(stored, [&](int, float (&v)[8]) {
+#pragma unroll
+                        for (int i = 0; i < 8; i++) take(v[i]);
+                    });
+                },
+                ss, a.inv_n, a.eps);
+        if (a.rstd && threadIdx.x == 0) a.rstd[t] = s;
+        row(stored, [&](int c, float (&v)[8]) {
+            float g[8];
+            cols.load_gain(g, a.gain, c);
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = v[i] * s * g[i];
+            if (a.y) cols.template store<T>(a.y, a.ldy, t, c, v);
+            if (a.codes) cols.store_8bit(a.codes, a.scales, t, c, v);
+        });
+    }
+}
+
+// The sums of dgain stay in shared memory, [n].
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_backward(const NormArgs a)
+{
+    constexpr int U = WIDE ? 8 / sizeof(T) : 1, V = WIDE ? 4 / sizeof(T) : 1;
+    extern __shared__ __align__(16) float sums[];
+    __shared__ float slots[64];
+    griddep_wait();
+    griddep_launch_dependents();
+    Team team = long_team(slots);
+    const Cols<WIDE> cols(team, a.n);
+    const int chunks = (a.n + LONG_THREADS * 8 - 1) / (LONG_THREADS * 8);
+    if (a.parts)
+        for (int c = 0; c < chunks; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (cols.at(c, i) < a.n) sums[cols.at(c, i)] = 0.f;
+    for (int t = (int)blockIdx.x; t < a.T; t += (int)gridDim.x) {
+        const float s = a.rstd[t];
+        float dot = 0.f;
+#pragma unroll WIDE ? 1 : 4
+        for (int c0 = 0; c0 < chunks; c0 += U) {
+            Raw<T> x[U], dy[U];
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                x[u] = cols.template load<T>(a.x, a.ldx, t, c0 + u, true);
+                dy[u] = cols.template load<T>(a.dy, a.lddy, t, c0 + u, true);
+            }
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                float g[8];
+                cols.load_gain(g, a.gain, c0 + u);
+#pragma unroll
+                for (int i = 0; i < 8; i++) dot += value(dy[u], i) * g[i] * (value(x[u], i) * s);
+            }
+        }
+        dot = team.sum(dot) * a.inv_n;
+#pragma unroll WIDE ? 1 : 2
+        for (int c0 = 0; c0 < chunks; c0 += V) {
+            Raw<T> x[V], dy[V], dr[V];
+#pragma unroll
+            for (int u = 0; u < V; u++) {
+                x[u] = cols.template load<T>(a.x, a.ldx, t, c0 + u, true);
+                dy[u] = cols.template load<T>(a.dy, a.lddy, t, c0 + u, true);
+                dr[u] = Raw<T>{};
+                if (a.dr) dr[u] = cols.template load<T>(a.dr, a.lddr, t, c0 + u, true);
+            }
+#pragma unroll
+            for (int u = 0; u < V; u++) {
+                const int c = c0 + u;
+                float g[8], add[8];
+                cols.load_gain(g, a.gain, c);
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float xh = value(x[u], i) * s, dv = value(dy[u], i);
+                    g[i] = value(dr[u], i) + s * (dv * g[i] - xh * dot);
+                    add[i] = dv * xh;
+                }
+                cols.template store<T>(a.dx, a.lddx, t, c, g);
+                if (!a.parts) continue;
+                if constexpr (WIDE) {
+                    if (cols.at(c, 0) >= a.n) continue;
+                    float4 *const p = (float4 *)(sums + cols.at(c, 0));
+                    const float4 q = p[0], r = p[1];
+                    p[0] = make_float4(q.x + add[0], q.y + add[1], q.z + add[2], q.w + add[3]);
+                    p[1] = make_float4(r.x + add[4], r.y + add[5], r.z + add[6], r.w + add[7]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        if (cols.at(c, i) < a.n) sums[cols.at(c, i)] += add[i];
+                }
+            }
+        }
+    }
+    if (a.parts)
+        for (int c = 0; c < chunks; c++)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (cols.at(c, i) < a.n) a.parts[(long)blockIdx.x * a.n + cols.at(c, i)] = sums[cols.at(c, i)];
 }
 
 // dgain[c] (+)= the sum of its column over the parts.  A block takes 32 columns, its
@@ -395,45 +557,57 @@ __global__ void __launch_bounds__(M8_THREADS) k3_mx8_dequantize(const Mx8Args a)
     }
 }
 
-bool rows16(const void *p, long ld, int dtype)
-{
-    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
-}
-
-// Chunks a thread, by the row's length: few, so that the next row's chunks fit in
-// registers beside this one's.
-template <typename T, bool WIDE>
-auto pick(int c, bool backward) -> void (*)(NormArgs)
-{
-    if (backward)
-        return c == 1 ? k3_norm_backward<T, WIDE, 1> : c == 2 ? k3_norm_backward<T, WIDE, 2>
-               : c == 4 ? k3_norm_backward<T, WIDE, 4> : k3_norm_backward<T, WIDE, 8>;
-    return c == 1 ? k3_norm_forward<T, WIDE, 1> : c == 2 ? k3_norm_forward<T, WIDE, 2>
-           : c == 4 ? k3_norm_forward<T, WIDE, 4> : k3_norm_forward<T, WIDE, 8>;
-}
+// Chunks a thread: few, so that the next row's fit in registers beside this one's; of
+// unaligned rows, whose values come one by one, one.  Measured in us on 8192 rows, forward
+// and backward: bf16 4096 wide with one chunk a thread 44 and 61, two 47 and 55, four 44
+// and (with spills) 396; 8192 wide two 89 and 98, four 85, long 102 and 136; 16384 wide four
+// 166 and 2340, long 190 and 252.  fp32 1024 wide one 27 and 24, two 22 and 33; 8192 wide
+// two 176 and 253, long 183 and 235.  bf16 4093 wide, unaligned, one 154 and 220, long 88 and
+// 96; 2045 wide one 74 and 121, long 79 and 85, but on 256 rows one 4.0 and 6.5.
 struct NormPlan {
-    int c, warps, teams, grid;
+    int c, warps, teams, grid;  // c: chunks a thread, 0 for the kernels of long rows
 };
-NormPlan norm_plan(int T, int n)
+NormPlan norm_plan(int T, int n, int dtype, bool wide, bool backward)
 {
     NormPlan p;
     const int chunks = (n + 7) / 8;
-    p.c = chunks <= 128 ? 1 : chunks <= 1024 ? 2 : chunks <= 2048 ? 4 : 8;
+    if (!wide)
+        p.c = chunks <= 256 ? 1 : 0;
+    else if (dtype == K3MOE_BF16)
+        p.c = backward ? (chunks <= 128 ? 1 : chunks <= 1024 ? 2 : 0) : (chunks <= 512 ? 1 : chunks <= 2048 ? 4 : 0);
+    else
+        p.c = backward ? (chunks <= 512 ? 1 : 0) : (chunks <= 32 ? 1 : chunks <= 1024 ? 2 : 0);
+    if (!p.c) {
+        p.warps = LONG_THREADS / 32, p.teams = 1;
+        p.grid = std::min(T, num_sms() * LONG_CTAS);
+        return p;
+    }
     p.warps = (chunks + 32 * p.c - 1) / (32 * p.c);
     p.teams = std::max(1, 8 / p.warps);
     const int threads = p.warps * p.teams * 32;
     p.grid = (int)std::min<long>((T + p.teams - 1L) / p.teams, (long)num_sms() * std::max(1, 1024 / threads));
     return p;
 }
+template <typename T>
+auto pick(int c, bool wide, bool backward) -> void (*)(NormArgs)
+{
+    if (backward)
+        return c == 0 ? (wide ? k3_norm_long_backward<T, true> : k3_norm_long_backward<T, false>)
+               : !wide ? k3_norm_backward<T, false, 1>
+               : c == 1 ? k3_norm_backward<T, true, 1> : k3_norm_backward<T, true, sizeof(T) == 2 ? 2 : 1>;
+    if (c == 0) return wide ? k3_norm_long_forward<T, true> : k3_norm_long_forward<T, false>;
+    return !wide ? k3_norm_forward<T, false, 1> : c == 1 ? k3_norm_forward<T, true, 1>
+           : k3_norm_forward<T, true, sizeof(T) == 2 ? 4 : 2>;
+}
 int launch_norm(NormArgs a, int dtype, bool wide, bool backward, const NormPlan &p, cudaStream_t s)
 {
     a.warps = p.warps;
     a.inv_n = 1.f / (float)a.n;
-    wide = wide && a.n % 8 == 0;
-    void (*const kernel)(NormArgs) = dtype == K3MOE_BF16
-                                         ? (wide ? pick<uint16_t, true>(p.c, backward) : pick<uint16_t, false>(p.c, backward))
-                                         : (wide ? pick<uint32_t, true>(p.c, backward) : pick<uint32_t, false>(p.c, backward));
-    if (launch_pdl(kernel, dim3((unsigned)p.grid), dim3((unsigned)(p.warps * p.teams * 32)), 0, s, a) != cudaSuccess) {
+    void (*const kernel)(NormArgs) =
+        dtype == K3MOE_BF16 ? pick<uint16_t>(p.c, wide, backward) : pick<uint32_t>(p.c, wide, backward);
+    const size_t smem = p.c == 0 && a.parts ? (size_t)a.n * sizeof(float) : 0;
+    if (smem && ensure_smem((const void *)kernel, smem) != K3MOE_OK) return K3MOE_ECUDA;
+    if (launch_pdl(kernel, dim3((unsigned)p.grid), dim3((unsigned)(p.warps * p.teams * 32)), smem, s, a) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
@@ -477,9 +651,9 @@ int launch_norm_forward(const k3moe_norm_forward_desc &d, cudaStream_t s)
     a.gain = d.gain, a.rstd = d.rstd;
     if (d.host_y8) a.codes = d.host_y8->codes, a.scales = d.host_y8->scales;
     a.T = d.T, a.n = d.n, a.eps = d.eps;
-    const bool wide = rows16(d.x, a.ldx, d.dtype) && (!d.delta || rows16(d.delta, a.ldd, d.dtype)) &&
+    const bool wide = d.n % 8 == 0 && rows16(d.x, a.ldx, d.dtype) && (!d.delta || rows16(d.delta, a.ldd, d.dtype)) &&
                       (!d.y || rows16(d.y, a.ldy, d.dtype)) && (!d.r || rows16(d.r, a.ldr, d.dtype));
-    return launch_norm(a, d.dtype, wide, false, norm_plan(d.T, d.n), s);
+    return launch_norm(a, d.dtype, wide, false, norm_plan(d.T, d.n, d.dtype, wide, false), s);
 }
 
 int launch_norm_backward(const k3moe_norm_backward_desc &d, cudaStream_t s)
@@ -490,9 +664,9 @@ int launch_norm_backward(const k3moe_norm_backward_desc &d, cudaStream_t s)
     a.gain = d.gain, a.rstd = (float *)d.rstd;
     a.parts = d.dgain ? (float *)d.workspace : nullptr;
     a.T = d.T, a.n = d.n;
-    const bool wide = rows16(d.r, a.ldx, d.dtype) && rows16(d.dy, a.lddy, d.dtype) &&
+    const bool wide = d.n % 8 == 0 && rows16(d.r, a.ldx, d.dtype) && rows16(d.dy, a.lddy, d.dtype) &&
                       (!d.dr || rows16(d.dr, a.lddr, d.dtype)) && rows16(d.dx, a.lddx, d.dtype);
-    NormPlan p = norm_plan(d.T, d.n);
+    NormPlan p = norm_plan(d.T, d.n, d.dtype, wide, true);
     p.grid = std::min(p.grid, NORM_PARTS / p.teams);
     const int st = launch_norm(a, d.dtype, wide, true, p, s);
     if (st != K3MOE_OK || !d.dgain) return st;

@@ -215,11 +215,6 @@ int launch(SwigluArgs a, void *ckpt, int dtype, int T, bool vec, bool backward, 
     }
     return K3MOE_OK;
 }
-bool rows16(const void *p, long ld, int dtype)
-{
-    return ((uintptr_t)p & 15u) == 0 && ld % (dtype == K3MOE_BF16 ? 8 : 4) == 0;
-}
-
 }  // namespace
 
 int launch_swiglu_forward(void *h, long ldh, void *ckpt, const void *g, long ldg, const void *u, long ldu, int dtype,

@@ -183,6 +183,20 @@ def test_in_place(dt):
         assert torch.equal(v[which], dx)
 
 
+@pytest.mark.parametrize("n", [1024, 1001])
+def test_gains_of_any_alignment(n):
+    g = torch.Generator().manual_seed(n)
+    x, dy = _t(g, 9, n, "bf16"), _t(g, 9, n, "bf16")
+    gains = torch.rand(n + 1, generator=g).cuda()
+    norm, outs = k.RmsNorm(n, 1e-6), []
+    for gain in (gains[1:], gains[1:].clone()):
+        y, dx, rstd, dgain = torch.empty_like(x), torch.empty_like(x), torch.empty(9, device="cuda"), torch.empty(n + 1, device="cuda")
+        norm.forward(y, x, None, None, rstd, gain)
+        norm.backward(dx, dgain[1:], dy, x, rstd, gain)
+        outs.append((y, dx, dgain[1:].clone()))
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+
+
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
 def test_repeats_capture_and_other_stream(dt):
     T, n = 1500, 264
