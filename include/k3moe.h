@@ -887,6 +887,7 @@ int k3moe_mx_experts_from_matrices(const k3moe_mx_experts *host_W, const uint8_t
  * The result does not depend on timing.  After a device-side timeout
  * (k3moe_device_error() == K3MOE_ETIMEOUT) the plan's workspace is zeroed again before it
  * is used.
+ * (E + tokens * top_k) * ceil(W->rows / 128) <= 2^30.
  * Errors: K3MOE_EINVAL for null or misaligned pointers, E or `in` that differ, too few
  * rows, bad sizes or types.
  */
@@ -917,7 +918,8 @@ int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, i
  *              (xrows >= tokens); gather = 0: rows in group order (xrows >= tokens * top_k)
  *  dW          [E][N][K], dw_dtype K3MOE_F32 or K3MOE_BF16
  *  accumulate  != 0 adds into dW (K3MOE_F32 only)
- * N and K are multiples of 8; dY, X and dW 16-byte aligned, lddy and ldx multiples of 8.
+ * N and K are multiples of 8, at most 2^20, E * ceil(N / 256) * ceil(K / 128) <= 2^30 and
+ * N * K < 2^38; dY, X and dW 16-byte aligned, lddy and ldx multiples of 8.
  * The result does not depend on timing.  Errors: K3MOE_EINVAL.
  */
 typedef struct {
@@ -946,7 +948,8 @@ int k3moe_grouped_wgrad(const k3moe_grouped_wgrad_desc *host_desc, k3moe_stream 
  *  y, dy       [tokens * top_k][n] rows in group order; rows of dy from offsets[E] on are
  *              left as they are
  *  out, dout   [tokens][n]; accumulate != 0 adds into out
- *  w, dw       fp32 [tokens][top_k]; dw NULL where it is not wanted (y may then be NULL)
+ *  w, dw       fp32 [tokens][top_k]; dw NULL where it is not wanted (y may then be NULL),
+ *              and with w NULL
  * y, dy, out and dout of one type (K3MOE_F32 or K3MOE_BF16) in a call, row strides >= n,
  * aligned to the element size; 1 <= n <= 2^20.  dy may be y with the same stride.
  * Sums are taken in rising j.  Errors: K3MOE_EINVAL.

@@ -335,7 +335,8 @@ int k3moe_grouped_matmul(const k3moe_grouped_matmul_desc *a, k3moe_stream s)
     const k3moe_groups *g = a->host_groups;
     if (!valid_groups(g) || !valid_mx8(A) || !valid_experts(W) || W->E != g->E || W->in != A->in ||
         A->rows < (a->gather ? g->tokens : g->tokens * g->top_k) || !valid_dtype(a->c_dtype) ||
-        !valid_rows(a->C, a->c_dtype, a->ldc, W->rows) || (a->accumulate && a->c_dtype != K3MOE_F32))
+        !valid_rows(a->C, a->c_dtype, a->ldc, W->rows) || (a->accumulate && a->c_dtype != K3MOE_F32) ||
+        ((int64_t)g->E + (int64_t)g->tokens * g->top_k) * ((W->rows + 127) / 128) > kMaxDim)
         return K3MOE_EINVAL;
     return writing(s, [&] {
         int *err = k3::device_error_word();
@@ -353,7 +354,8 @@ int k3moe_grouped_wgrad(const k3moe_grouped_wgrad_desc *a, k3moe_stream s)
         !valid_rows(a->X, K3MOE_BF16, a->ldx, a->K) || !aligned(a->dY, 16) || !aligned(a->X, 16) || a->lddy % 8 ||
         a->ldx % 8 || a->lddy >= ((int64_t)1 << 39) || a->ldx >= ((int64_t)1 << 39) ||
         (int64_t)a->N * a->K >= ((int64_t)1 << 38) || a->xrows < (a->gather ? g->tokens : g->tokens * g->top_k) ||
-        a->xrows > kMaxDim || (a->accumulate && a->dw_dtype != K3MOE_F32))
+        a->xrows > kMaxDim || (a->accumulate && a->dw_dtype != K3MOE_F32) ||
+        (int64_t)g->E * ((a->N + 255) / 256) * ((a->K + 127) / 128) > kMaxDim)
         return K3MOE_EINVAL;
     return writing(s, [&] {
         int *err = k3::device_error_word();

@@ -98,11 +98,6 @@ K3_DEV void gm_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
                  "l"((uint64_t)map), "r"(adst), "l"(atom), "r"(x), "r"(row), "r"(e), "r"(bar)
                  : "memory");
 }
-// 16 bytes from global to shared memory, asynchronously.
-K3_DEV void copy16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 
 // The tiles of the batch, made by every CTA in shared memory: before[e] row tiles lie
 // before expert e's, off[e] is its first place.
@@ -170,8 +165,8 @@ K3_DEV GmTile gm_tile(const GmTable &tab, const GmArgs &a, int u)
 }
 // What a CTA works on as its i-th piece: whole tiles in turn over the CTAs, as many as
 // make full waves, and of the tiles that are left a part along K, several CTAs to a tile
-// where there are enough (1 token x 16 experts x 1536 x 7168, 192 tiles on 152 SMs: 24.9
-// us against 29.8).  slot: where a part leaves its sums; u < 0: nothing more.
+// where there are enough (1 token x 16 experts x 1536 x 7168, 192 tiles on 152 SMs: 21.2
+// us against 24.9).  slot: where a part leaves its sums; u < 0: nothing more.
 struct GmPart {
     int u, k0, k1, of, slot;
 };
@@ -886,31 +881,32 @@ int launch_gp(const k3moe_mx8_rows *A, const k3moe_mx_experts *W, GmArgs a, cuda
     }
     return K3MOE_OK;
 }
-// The form by the time it would take: for every wave of tiles over the SMs (or pairs of
-// them) a time per step and one per tile.  An expert with `avg` rows makes about avg /
-// height + 1/2 tiles.  Measured on 64 experts, in us, with 16, 32 and 64 rows and pairs:
-//   1536 x 7168, 8 rows an expert 80 82 86 104, 16 rows 104 83 86 105, 32 rows 163 107 90
-//   107, 64 rows 285 170 120 110, 192 rows 771 420 266 152;
-//   7168 x 1536, 8 rows 82 80 83 101, 32 rows 175 113 98 103, 64 rows 317 187 145 109.
-// (Single tiles of 128 rows never won: 114, 203 and 164 us at the last three sizes but
-// one, and 16 to 35% behind pairs from 128 rows on.)
+// The form by the time it would take: a time per step and one per tile, times the tiles of
+// an SM (or a pair of them), one at least.  An expert with `avg` rows makes about avg /
+// height + 1/2 tiles.  The times are fitted to 157 measured shapes of 8 to 384 experts with
+// 1 to 300 rows each; the form they choose is 0.5% behind the best one on average, 13% at
+// worst.  Measured on 64 experts, in us, with 16, 32 and 64 rows and pairs:
+//   1536 x 7168, 8 rows an expert 68 70 75 100, 16 rows 84 71 82 101, 32 rows 131 88 94
+//   106, 64 rows 230 140 116 109, 192 rows 626 351 233 138;
+//   7168 x 1536, 8 rows 71 72 82 98, 32 rows 158 114 102 100, 64 rows 282 185 151 105.
+// (Single tiles of 128 rows never won: 16 to 35% behind pairs from 128 rows on.)
 int tile_rows(int E, long slots, int N, int nks)
 {
     const long hit = std::min<long>(E, slots), sms = num_sms(), tiles_n = ((long)N + GM_M - 1) / GM_M;
     const struct {
         int rows, step, tile;  // of a tile; ns
         long columns, at_once;
-    } forms[4] = {{16, 236, 500, tiles_n, sms},
-                  {32, 240, 600, tiles_n, sms},
-                  {64, 255, 1300, tiles_n, sms},
-                  {GP_NT, 290, 1500, (tiles_n + 1) / 2, std::max(1L, sms / 2)}};
+    } forms[4] = {{16, 226, 600, tiles_n, sms},
+                  {32, 225, 700, tiles_n, sms},
+                  {64, 210, 1600, tiles_n, sms},
+                  {GP_NT, 255, 1500, (tiles_n + 1) / 2, std::max(1L, sms / 2)}};
     int best = 0;
-    long cost = 0;
+    double cost = 0;
     for (const auto &f : forms) {
         const long half_tiles = std::max(2 * hit, 2 * slots / f.rows + hit);
-        const long waves = (half_tiles * f.columns + 2 * f.at_once - 1) / (2 * f.at_once);
-        const long c = waves * ((long)f.step * nks + f.tile);
-        if (!cost || c < cost) cost = c, best = f.rows;
+        const double tiles = std::max(1.0, 0.5 * (double)half_tiles * (double)f.columns / (double)f.at_once);
+        const double c = tiles * ((double)f.step * nks + f.tile);
+        if (best == 0 || c < cost) cost = c, best = f.rows;
     }
     return best;
 }
@@ -948,7 +944,6 @@ int launch_grouped_matmul(const k3moe_grouped_matmul_desc &d, int *err, cudaStre
     a.parts = (float *)(a.counts + GM_CTAS);
     a.C = d.C, a.ldc = (long)d.ldc, a.accumulate = d.accumulate ? 1 : 0, a.err = err;
     a.pairs = d.c_dtype == K3MOE_BF16 && a.N % 2 == 0 && d.ldc % 2 == 0 && ((uintptr_t)d.C & 3u) == 0;
-    if (((long)a.E + a.slots) * a.tiles_n > 0x7fffffffL) return K3MOE_EINVAL;
     return d.c_dtype == K3MOE_BF16 ? launch_gm_ct<__nv_bfloat16>(A, W, a, s) : launch_gm_ct<float>(A, W, a, s);
 }
 

@@ -83,18 +83,13 @@ K3_DEV void gw_step(uint32_t tacc, uint32_t xlo, uint32_t ylo, uint32_t acc, int
 }
 K3_DEV uint32_t mn_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(GW_PANEL >> 4) << 16); }
 
-// 16 bytes from global to shared memory, asynchronously.
-K3_DEV void gw_copy16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 // Chunk c of row r of a panel: eight columns of a row, zeros where `on` is false or the
 // columns lie past the matrix.
 K3_DEV void gw_chunk(uint32_t panel, int r, int c, const __nv_bfloat16 *row, int col, int cols, bool on)
 {
     const uint32_t dst = panel + (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
     if (on && col < cols)
-        gw_copy16(dst, row + col);
+        copy16(dst, row + col);
     else
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0u) : "memory");
 }
@@ -397,7 +392,6 @@ int launch_grouped_wgrad(const k3moe_grouped_wgrad_desc &d, int *err, cudaStream
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = d.gather ? 1 : 0, a.xrows = d.xrows;
     const int tiles_k = (d.K + GW_M - 1) / GW_M;
     const long tiles = (long)tiles_k * ((d.N + GW_N - 1) / GW_N);
-    if (tiles * a.E > 0x7fffffffL) return K3MOE_EINVAL;
     a.tiles_k = FastDiv((uint32_t)tiles_k), a.tiles_e = FastDiv((uint32_t)tiles);
     a.N = d.N, a.K = d.K, a.accumulate = d.accumulate ? 1 : 0, a.err = err;
     a.dy = (const __nv_bfloat16 *)d.dY, a.x = (const __nv_bfloat16 *)d.X, a.dw = d.dW;

@@ -1,4 +1,4 @@
-// k3_tmem.cuh -- accumulator reads, the barriers of CTA pairs, and tensor-map making,
+// k3_tmem.cuh -- accumulator reads, asynchronous copies, the barriers of CTA pairs, and tensor-map making,
 // shared by the operand product and the grouped products.
 #pragma once
 #include "k3_tcgen05.cuh"
@@ -38,6 +38,12 @@ K3_DEV void tmem_ld_chunk(uint32_t taddr, uint32_t (&r)[32])
                    "+r"(r[30]), "+r"(r[31])
                  :
                  : "memory");
+}
+
+// 16 bytes from global to shared memory, asynchronously.
+K3_DEV void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 K3_DEV uint32_t cluster_rank()

@@ -685,6 +685,10 @@ class MxExperts:
         nc, na = lib().k3moe_mx_operand_codes_bytes(rows, in_), lib().k3moe_mx_operand_atoms_bytes(rows, in_)
         if nc < 0 or na < 0 or not 1 <= E <= 1024 or in_ % 128:
             raise K3Error(K3MOE_EINVAL, "MxExperts(%d, %d, %d)" % (E, rows, in_))
+        if codes is not None and (codes.dtype is not torch.uint8 or codes.shape != (E, rows, in_ // 2) or
+                                  not codes[0].is_contiguous()):
+            raise ValueError("expected byte planes [%d][%d][%d], got %s %s" % (E, rows, in_ // 2, codes.dtype,
+                                                                               tuple(codes.shape)))
         self.E, self.rows, self.in_ = E, rows, in_
         self.codes = torch.empty(E, rows, in_ // 2, dtype=torch.uint8, device=device) if codes is None else codes
         self.atoms = torch.empty(E, na, dtype=torch.uint8, device=self.codes.device)

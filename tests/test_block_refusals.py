@@ -106,6 +106,7 @@ def test_matmul():
            dict(W=experts(n=64), A=rows8(10, 64)), dict(W=experts(codes=P + 16)), dict(W=experts(codes=None)),
            dict(W=experts(atoms=P + 8)), dict(W=experts(atoms=None)), dict(W=experts(rows=0)), dict(W=experts(cs=40 * 64 - 32)),
            dict(W=experts(cs=40 * 64 + 16)), dict(W=experts(as_=512)), dict(W=experts(as_=2056)), dict(W=experts(cs=1 << 40)),
+           dict(W=experts(rows=1 << 14, cs=1 << 20, as_=1 << 20), g=groups(T=1 << 23), A=rows8(1 << 24, 128), ldc=1 << 14),
            *(dict(A=b) for b in BAD_ROWS), *(dict(g=b) for b in BAD_GROUPS)]
     for b in bad:
         a = {**good, **b}
@@ -137,7 +138,8 @@ def test_wgrad():
     good = dict(dw=P, dt=0, dy=P, lddy=16, x=P, ldx=24, xr=10, N=16, K=24, g=groups(), gather=0, acc=0)
     bad = [dict(dw=None), dict(dw=P + 8), dict(dt=2), dict(dt=1, acc=1), dict(dy=None), dict(dy=P + 8), dict(lddy=8),
            dict(lddy=20), dict(x=None), dict(x=P + 2), dict(ldx=16), dict(ldx=28), dict(xr=9), dict(xr=4, gather=1), dict(N=12),
-           dict(N=0), dict(K=20), dict(K=0), dict(xr=(1 << 30) + 1), *(dict(g=b) for b in BAD_GROUPS)]
+           dict(N=0), dict(K=20), dict(K=0), dict(xr=(1 << 30) + 1),
+           dict(N=1 << 18, K=1 << 19, lddy=1 << 18, ldx=1 << 19, g=groups(E=1000)), *(dict(g=b) for b in BAD_GROUPS)]
     for b in bad:
         a = {**good, **b}
         d = pack(k.GROUPED_WGRAD, a["dw"], a["dy"], a["lddy"], a["x"], a["ldx"], addr(a["g"]), a["dt"], a["xr"], a["N"], a["K"],
@@ -255,6 +257,7 @@ def test_binding_refuses_types_and_shapes():
                       (lambda: k.grouped_wgrad(o(torch.zeros(3, 8, 16).transpose(1, 2)), h, h, g), ValueError),
                       (lambda: k.grouped_wgrad(o(torch.zeros(3, 8, 8)), x, x, g), TypeError),
                       (lambda: k.combine(h, x, g), (TypeError, ValueError)),
+                      (lambda: k.MxExperts(3, 8, 128, codes=o(torch.zeros(3, 8, 32, dtype=torch.uint8))), ValueError),
                       (lambda: k.MxExperts(3, 8, 96, device="cpu"), k.K3Error), (lambda: k.MxExperts(1025, 8, 128), k.K3Error),
                       (lambda: k.ExpertGroups(3, 33, 4, device="cpu"), k.K3Error), (lambda: k.RmsNorm(0, 1e-6, device="cpu"), k.K3Error),
                       (lambda: k.Mx8Rows(0, 5, device="cpu"), k.K3Error)):

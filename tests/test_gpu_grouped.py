@@ -117,6 +117,12 @@ def test_matmul_many_experts(T, kk, E, N, K):
     assert (np.abs(C.double().cpu().numpy() - want) <= mag * (K / 32 + 10) * 2.0 ** -22 + np.abs(want) * 2.0 ** -24).all()
 
 
+def test_matmul_of_the_longest_rows():
+    for K, sizes in ((1 << 20, [1, 20]), (1 << 17, [70, 100])):
+        W, V = _wide(2, 8, K)
+        _check_wide(W, V, sizes, 1, True, "f32")
+
+
 def _wide(E, N, K):
     """Random stored matrices on the GPU and their fp64 values."""
     gen = torch.Generator(device="cuda").manual_seed(N + K)
@@ -178,7 +184,7 @@ def test_matmul_pairs_of_several_tiles(wide, sizes, gather, out):
 
 
 # few tiles of a long K: those left over from full waves are shared by several CTAs
-@pytest.mark.parametrize("form,each", [(32, 40), (64, 60)])
+@pytest.mark.parametrize("form,each", [(32, 16), (64, 40)])
 def test_matmul_tiles_in_parts(form, each):
     W, V = _wide(80, 250, 4096)
     rng = np.random.default_rng(each)
