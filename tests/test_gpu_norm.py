@@ -38,7 +38,8 @@ def _formula(r, gain, eps):
 
 
 CASES = [(1, 1, 0), (1, 7168, 0), (3, 31, 1), (5, 129, 0), (33, 1000, 8), (257, 1537, 0), (9, 1024, 0), (2, 8193, 0),
-         (3, 8192, 8), (2, 16390, 0), (1, 32768, 0), (2, 32767, 1), (700, 64, 0), (2000, 40, 0)]
+         (3, 8192, 8), (2, 16390, 0), (1, 32768, 0), (2, 32767, 1), (700, 64, 0), (2000, 40, 0),
+         (700, 4099, 0), (400, 16392, 0), (330, 32765, 3)]  # the last three: several rows to a CTA that reads them twice
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
@@ -132,7 +133,7 @@ def test_gradients_against_differences():
         assert abs((_f64(dgain) * w).sum() - num) <= 1e-7 + 1e-4 * np.abs(_f64(dgain) * w).sum() * 2 ** -7
 
 
-@pytest.mark.parametrize("n", [8, 100, 7168])
+@pytest.mark.parametrize("n", [8, 100, 7168, 4099, 20000])
 def test_rows_out_of_range(n):
     """Zeros, rows whose squares leave fp32 both ways, infinities and NaN; each row by
     itself, eps 0 and 1e-6."""
@@ -163,9 +164,9 @@ def test_rows_out_of_range(n):
         assert np.array_equal(v, e[0], equal_nan=True) and np.array_equal(sc, e[1])
 
 
+@pytest.mark.parametrize("T,n", [(50, 200), (400, 4100), (400, 16640)])
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-def test_in_place(dt):
-    T, n = 50, 200
+def test_in_place(dt, T, n):
     g = torch.Generator().manual_seed(4)
     x, d, dy, dr = (_t(g, T, n, dt) for _ in range(4))
     gain = torch.rand(n, generator=g).cuda()
