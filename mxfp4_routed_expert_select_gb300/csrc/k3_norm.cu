@@ -59,6 +59,14 @@ K3_DEV float warp_max(float v)
     return v;
 }
 
+// The sum of eight squares, in pairs.
+K3_DEV float squares(const float (&v)[8])
+{
+    const float a = fmaf(v[1], v[1], v[0] * v[0]), b = fmaf(v[3], v[3], v[2] * v[2]);
+    const float c = fmaf(v[5], v[5], v[4] * v[4]), d = fmaf(v[7], v[7], v[6] * v[6]);
+    return (a + b) + (c + d);
+}
+
 // A team's warps, its barrier and its slots for partial results.  Two sets of
 // slots in turn: a warp that has passed one barrier cannot reach the second next
 // one's writes before the others have read.
@@ -222,13 +230,14 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
     for (; t < a.T; t += step) {
         float v[C][8], ss = 0.f;
 #pragma unroll
-        for (int c = 0; c < C; c++)
+        for (int c = 0; c < C; c++) {
 #pragma unroll
             for (int i = 0; i < 8; i++) {
                 v[c][i] = value(x[c], i);
                 if (a.delta) v[c][i] = rounded<T>(v[c][i] + value(d[c], i));
-                ss += v[c][i] * v[c][i];
             }
+            ss += squares(v[c]);
+        }
         load(t + step);
         if (a.r)
 #pragma unroll
@@ -365,8 +374,7 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(
         };
         float ss = 0.f;
         row(false, [&](int c, float (&v)[8]) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) ss += v[i] * v[i];
+            ss += squares(v);
             if (a.r) cols.template store<T>(a.r, a.ldr, t, c, v);
         });
         asm volatile("" ::: "memory");  // r, which may lie over x, is stored before it is read again
