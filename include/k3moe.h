@@ -7,7 +7,8 @@
  * expert the gate/up products, SwiGLU, the down product and the weighted
  * combine.  The 4-bit codes feed block-scaled tensor-core products as stored
  * (batch 1) or are decoded on chip, in registers or shared memory; no weight
- * is ever expanded in device memory.
+ * is ever expanded in device memory.  Operators beside the layer make and train
+ * MXFP4 experts, one at a time or all experts of a routed batch in one call.
  *
  * Sources of the operations (page title, section):
  *  [EXPL]  "kimi-k3-in-c" explainer, ai.thesatyajit.com

@@ -151,7 +151,7 @@ const char *k3moe_strerror(int st)
     }
 }
 
-int k3moe_version(void) { return (1 << 16) | 2; }
+int k3moe_version(void) { return (1 << 16) | 3; }
 
 int k3moe_device_error(void)
 {

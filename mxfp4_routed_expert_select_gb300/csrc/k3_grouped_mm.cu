@@ -18,7 +18,12 @@
 // the form this kind of MMA reads, so HBM and L2 move packed bytes), the rows' codes by
 // TMA where they lie in group order, else row by row with asynchronous copies into the
 // same swizzled form, and the rows' scale bytes.  (Gathered by TMA, four rows a copy of
-// 72 clocks, 65536 rows x 1536 x 7168 took 2.94 ms; the same rows as tiles 0.76.)
+// 72 clocks, the first version took 2.94 ms for 65536 rows x 1536 x 7168, as tiles 0.76.)
+//
+// Bound: few rows stream the weights (1 token x 16 of 896 experts x 1536 x 7168, 94 MB, 21.2
+// us; 64 x 16 over 128 experts, 753 MB, 123, 6.1 TB/s), many the pairs' shared memory and
+// MMAs (65536 rows with 64 experts x 1536 x 7168 gathered 575 us, 2.5 PFLOP/s, in group
+// order 490).
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.

