@@ -8,12 +8,12 @@
 // Bound: HBM, one pass each way.  A team of warps holds a row, C chunks of eight
 // values a thread, and takes one row after the other, so that its gains (and the
 // sums of dgain) stay in registers and the next row's loads are in flight while
-// this one's sum is joined.  The column sums of the teams meet in a second small
+// this one's sum is joined.  The column sums of the CTAs meet in a second small
 // kernel, in an order that does not depend on timing.  Rows too long for that are read
 // twice by a CTA, the second time from L2.
 //
 // bf16, x, delta, r and y or the backward call's four: 8192 x 4096 44 us (6.1 TB/s) and
-// 56, 8192 x 8192 85 (6.3) and 99, 8192 x 32768 385 (5.6) and 602; 4096 x 7168 to 8 bits
+// 50, 8192 x 8192 85 (6.3) and 99, 8192 x 32768 385 (5.6) and 602; 4096 x 7168 to 8 bits
 // 39 us.
 #include <cuda_runtime.h>
 
@@ -272,12 +272,12 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
 template <typename T, bool WIDE, int C>
 __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs a)
 {
+    extern __shared__ __align__(16) float sums[];  // [teams][n] where there are several
     __shared__ float slots[8][64];
     griddep_wait();
     griddep_launch_dependents();
     int t, step;
     Team team = make_team(a.warps, slots, t, step);
-    const int part = t;
     const Cols<WIDE> cols(team, a.n);
     Raw<T> x[C], dy[C], dr[C];
     float s = 0.f;
@@ -321,12 +321,22 @@ __global__ void __launch_bounds__(NORM_THREADS) k3_norm_backward(const NormArgs 
             cols.template store<T>(a.dx, a.lddx, t, c, g[c]);
         }
     }
-    if (a.parts)
+    if (!a.parts) return;
+    // the CTA's sums: its teams', added in their order
+    const int teams = (int)(blockDim.x >> 5) / a.warps;
+    float *const part = a.parts + (long)blockIdx.x * a.n, *const mine = teams > 1 ? sums + (team.bar - 1) * a.n : part;
 #pragma unroll
-        for (int c = 0; c < C; c++)
+    for (int c = 0; c < C; c++)
 #pragma unroll
-            for (int i = 0; i < 8; i++)
-                if (cols.at(c, i) < a.n) a.parts[(long)part * a.n + cols.at(c, i)] = sum[c][i];
+        for (int i = 0; i < 8; i++)
+            if (cols.at(c, i) < a.n) mine[cols.at(c, i)] = sum[c][i];
+    if (teams == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x; c < a.n; c += blockDim.x) {
+        float v = sums[c];
+        for (int i = 1; i < teams; i++) v += sums[i * a.n + c];
+        part[c] = v;
+    }
 }
 
 // Rows that do not fit in registers: a CTA holds one after the other and reads each
@@ -579,9 +589,10 @@ NormPlan norm_plan(int T, int n, int dtype, bool wide, bool backward)
 {
     NormPlan p;
     const int chunks = (n + 7) / 8;
+    const bool two_bytes = dtype == K3MOE_BF16;
     if (!wide)
         p.c = chunks <= 256 ? 1 : 0;
-    else if (dtype == K3MOE_BF16)
+    else if (two_bytes)
         p.c = backward ? (chunks <= 128 ? 1 : chunks <= 1024 ? 2 : 0) : (chunks <= 512 ? 1 : chunks <= 2048 ? 4 : 0);
     else
         p.c = backward ? (chunks <= 512 ? 1 : 0) : (chunks <= 32 ? 1 : chunks <= 1024 ? 2 : 0);
@@ -593,7 +604,11 @@ NormPlan norm_plan(int T, int n, int dtype, bool wide, bool backward)
     p.warps = (chunks + 32 * p.c - 1) / (32 * p.c);
     p.teams = std::max(1, 8 / p.warps);
     const int threads = p.warps * p.teams * 32;
-    p.grid = (int)std::min<long>((T + p.teams - 1L) / p.teams, (long)num_sms() * std::max(1, 1024 / threads));
+    // backward no more CTAs than run at once, by registers (76 a thread, 93 to 128 the
+    // others): 8192 x 4096 bf16 50 us, with twice as many 56; 8192 x 1024 15.0 with 768
+    // threads an SM, 17.7 with 512, 18.0 with 1024
+    const int at_once = !backward ? 1024 : two_bytes && wide && p.c == 1 ? 768 : 512;
+    p.grid = (int)std::min<long>((T + p.teams - 1L) / p.teams, (long)num_sms() * std::max(1, at_once / threads));
     return p;
 }
 template <typename T>
@@ -613,7 +628,7 @@ int launch_norm(NormArgs a, int dtype, bool wide, bool backward, const NormPlan 
     a.inv_n = 1.f / (float)a.n;
     void (*const kernel)(NormArgs) =
         dtype == K3MOE_BF16 ? pick<uint16_t>(p.c, wide, backward) : pick<uint32_t>(p.c, wide, backward);
-    const size_t smem = p.c == 0 && a.parts ? (size_t)a.n * sizeof(float) : 0;
+    const size_t smem = a.parts && (p.c == 0 || p.teams > 1) ? (size_t)p.teams * a.n * sizeof(float) : 0;
     if (smem && ensure_smem((const void *)kernel, smem) != K3MOE_OK) return K3MOE_ECUDA;
     if (launch_pdl(kernel, dim3((unsigned)p.grid), dim3((unsigned)(p.warps * p.teams * 32)), smem, s, a) != cudaSuccess) {
         cudaGetLastError();
@@ -675,11 +690,11 @@ int launch_norm_backward(const k3moe_norm_backward_desc &d, cudaStream_t s)
     const bool wide = d.n % 8 == 0 && rows16(d.r, a.ldx, d.dtype) && rows16(d.dy, a.lddy, d.dtype) &&
                       (!d.dr || rows16(d.dr, a.lddr, d.dtype)) && rows16(d.dx, a.lddx, d.dtype);
     NormPlan p = norm_plan(d.T, d.n, d.dtype, wide, true);
-    p.grid = std::min(p.grid, NORM_PARTS / p.teams);
+    p.grid = std::min(p.grid, NORM_PARTS);
     const int st = launch_norm(a, d.dtype, wide, true, p, s);
     if (st != K3MOE_OK || !d.dgain) return st;
     if (launch_pdl(k3_norm_columns, dim3((unsigned)((d.n + 31) / 32)), dim3(NC_WARPS * 32), 0, s, d.dgain,
-                   (const float *)d.workspace, (int)d.n, p.grid * p.teams, d.accumulate ? 1 : 0) != cudaSuccess) {
+                   (const float *)d.workspace, (int)d.n, p.grid, d.accumulate ? 1 : 0) != cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
