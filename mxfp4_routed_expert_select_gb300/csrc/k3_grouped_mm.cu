@@ -542,24 +542,6 @@ K3_DEV void gp_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
                  "l"((uint64_t)map), "r"(adst), "l"((uint64_t)amap), "r"(x), "r"(row), "r"(e), "r"(ak), "r"(art), "r"(bar)
                  : "memory");
 }
-K3_DEV void gp_load_x(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar)
-{
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
-                 "[%1, {%2, %3}], [%4];" ::"r"(dst),
-                 "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
-                 : "memory");
-}
-// Arrival at the even CTA's barrier behind what this thread (and, after a warp barrier,
-// its warp) has written to its own CTA's shared memory.  Those bytes never leave that
-// shared memory: the tensor core beside it reads them, behind the proxy fence that each
-// writer has passed.  So no wider fence than the CTA's own goes with the arrival; one at
-// cluster scope takes 1000 clocks or more, and with it in each stage's path 65536 rows x
-// 1536 x 7168 took 648 us instead of 520.
-K3_DEV void gp_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
 // The waits are of the CTA's scope too, those for the other CTA's arrivals among them: what
 // they hand over is tensor memory and staged tiles, which only the tensor core and copies
 // touch.  (An acquire at cluster scope makes a warp wait for its own stores.)
@@ -716,14 +698,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                         copy16(st + GP_OFF_X + (uint32_t)(r * 128 + (((lane & 7) ^ (r & 7)) << 4)), base + (long)t->src[c] * a.cstride);
                 }
             } else if (f == 1 && lane < boxes) {
-                gp_load_x(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t->row + rank * half + lane * GP_BOX,
+                pair_load_2d(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t->row + rank * half + lane * GP_BOX,
                           full0);
             }
             *(uint4 *)(sm + s * GP_STAGE + GP_OFF_XA + f * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             if (a.gather) asm volatile("cp.async.wait_all;" ::: "memory");
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) gp_arrive(full0);
+            if (lane == 0) pair_arrive(full0);
         }
         // drain: the last turn's copies of both CTAs have landed before the even CTA
         // exits; the odd one waits in the closing cluster barrier

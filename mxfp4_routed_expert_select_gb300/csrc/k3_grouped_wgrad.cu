@@ -6,20 +6,24 @@
 // lie in memory (M- and N-major tiles, the 128-byte swizzle over 64 columns of a row)
 // and nothing is transposed.
 //
-// X's columns k take the MMA's 128 lanes and dY's columns n its 256 columns, so that the
-// matrix whose rows may have to be gathered is the smaller part of a step (with n in the
-// lanes 16 x 2048 x 2048 from 131072 gathered rows took 1029 us instead of 765).
+// X's columns k take the MMA's lanes and dY's columns n its columns.  A pair of CTAs
+// (cta_group::2) works on 256 k x 256 n: each loads 128 columns of X and 128 of dY and the
+// MMA reads both, so that a step of 64 rows brings 32 KB into an SM for its 512 clocks of
+// MMAs.  (Lone CTAs with 128 k x 256 n, 48 KB a step: 64 x 1536 x 7168 from 16384 gathered
+// rows 518 us, pairs 480; 16 x 2048 x 2048 from 131072 773 and 622, in group order 690 and
+// 600.)  Where 128 x 128 tiles make two waves at most, single CTAs take those.
 //
-// A persistent CTA walks (expert, 128 k, 256 n) tiles; a step is 64 rows of the group.
-// Roles: warp 0 issues MMAs, warps 4 to 11 read one accumulator out while the other one's
-// products run, and each further warp fills a share of a stage of 64 rows: dY's columns by
-// TMA, X's by TMA too where it lies in group order, else row by row with asynchronous
-// copies into the same swizzled form; in a group's last step rows past it are made zeros
-// in both.  (TMA gathers of four rows take 72 clocks each: 2.06 ms with them.)
+// Persistent CTAs or pairs walk (expert, k, n) tiles.  Roles: warp 0 (of the even CTA) issues
+// MMAs, warps 4 to 11 read one accumulator out while the other one's products run, and each
+// further warp fills a share of a stage of 64 rows: dY's columns by TMA, X's by TMA too
+// where it lies in group order, else row by row with asynchronous copies into the same
+// swizzled form; in a group's last step rows past it are made zeros in both.  Copies and
+// fillers of both CTAs are counted on the even one's barrier.  (TMA gathers of four rows
+// take 72 clocks each: 2.06 ms with them.)
 //
 // Bound: the stores of dW where groups are short (64 x 1536 x 7168 fp32 from 16384 rows, 2.8
-// GB, 526 us), the MMAs beside the copies where they are long (16 x 2048 x 2048 from 131072
-// rows 685 us in group order, 1.6 PFLOP/s; gathered 760).
+// GB, gathered 480 us, 5.9 TB/s), the MMAs beside the copies where they are long (16 x 2048
+// x 2048 from 131072 rows 600 us in group order, 1.8 PFLOP/s; gathered 622).
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -37,12 +41,12 @@
 namespace k3 {
 namespace {
 
-constexpr int GW_M = 128, GW_N = 256, GW_K = 64;  // k and n of a tile, rows of a step
-constexpr int GW_NS = 4;
+constexpr int GW_CTA = 128, GW_K = 64;  // k and n of a CTA in a tile, rows of a step
+constexpr int GW_NS = 6;
 constexpr int GW_W_MMA = 0, GW_W_EPI = 4;
 constexpr int GW_EPI = 8;  // epilogue warps: two per TMEM lane quadrant, on alternate pieces
 constexpr int GW_W_FILL = GW_W_EPI + GW_EPI;
-constexpr int GW_FILL = 4;  // warps that fill a stage, a quarter of its rows each
+constexpr int GW_FILL = 2;  // warps that fill a stage, half of its rows each
 constexpr int GW_THREADS = (GW_W_FILL + GW_FILL * GW_NS) * 32;
 
 struct GwArgs {
@@ -53,36 +57,46 @@ struct GwArgs {
     const __nv_bfloat16 *dy, *x;
     void *dw;
     long lddy, ldx;
+    int ns;  // stages in use, at most GW_NS
     int *err;
 };
 
 constexpr int GW_PANEL = GW_K * 128;  // 64 rows of 64 columns
-constexpr int GW_OFF_Y = GW_M / 64 * GW_PANEL, GW_STAGE = GW_OFF_Y + GW_N / 64 * GW_PANEL;
+constexpr int GW_PANELS = GW_CTA / 64, GW_OFF_Y = GW_PANELS * GW_PANEL, GW_STAGE = 2 * GW_OFF_Y;
 constexpr int GW_BOX = 16;  // rows n of a staged box of dW, 32 columns k wide; two boxes a warp
 constexpr int GW_OFF_C = GW_NS * GW_STAGE, GW_OFF_BAR = GW_OFF_C + GW_EPI * 2 * GW_BOX * 128;
 constexpr int GW_BARS = 2 * GW_NS + 2 * 2 + 1;
 constexpr int GW_SMEM = 1024 + GW_OFF_BAR + 256;
 static_assert(GW_SMEM <= 232448, "shared memory");
-static_assert(GW_K / GW_FILL == 16, "a share is the rows of an MMA");
+static_assert(GW_K / GW_FILL % 16 == 0, "a share is the rows of whole MMAs");
 
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, both M/N-major.
-constexpr uint32_t GW_IDESC = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(GW_N >> 3) << 17) |
-                              ((uint32_t)(GW_M >> 4) << 24);
+constexpr uint32_t gw_idesc(int m, int n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
 
 // A step: an MMA for each 16 rows, one to four.  Descriptors of M/N-major tiles: panels
 // of 64 columns GW_PANEL bytes apart (leading offset), groups of eight rows 1024 bytes
 // (stride).
+template <int CTAS>
 K3_DEV void gw_step(uint32_t tacc, uint32_t xlo, uint32_t ylo, uint32_t acc, int mmas)
 {
-#define GW_MMA(k2, pred, on)                                                                                 \
+#define GW_MMA(group, k2, pred, on)                                                                                 \
     "add.u32 x, %1, " #k2 ";\n\tadd.u32 y, %2, " #k2 ";\n\tmov.b64 da, {x, %4};\n\tmov.b64 db, {y, %4};\n\t" \
-    "@" on " tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, " pred ";\n\t"
-    asm volatile("{\n\t.reg .pred p, t, e, f, g, h;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\tsetp.gt.and.s32 f, %6, 1, e;\n\t"
-                 "setp.gt.and.s32 g, %6, 2, e;\n\tsetp.gt.and.s32 h, %6, 3, e;\n\t" GW_MMA(0, "p", "e") GW_MMA(128, "t", "f")
-                     GW_MMA(256, "t", "g") GW_MMA(384, "t", "h") "}" ::"r"(tacc),
-                 "r"(xlo), "r"(ylo), "r"(acc), "r"(SW128_HI), "r"(GW_IDESC), "r"(mmas)
-                 : "memory");
+    "@" on " tcgen05.mma.cta_group::" group ".kind::f16 [%0], da, db, %5, " pred ";\n\t"
+#define GW_STEP(group)                                                                                            \
+    asm volatile("{\n\t.reg .pred p, t, e, f, g, h;\n\t.reg .b64 da, db;\n\t.reg .b32 x, y;\n\telect.sync _|e, 0xffffffff;\n\t" \
+                 "setp.ne.b32 p, %3, 0;\n\tsetp.eq.b32 t, %5, %5;\n\tsetp.gt.and.s32 f, %6, 1, e;\n\t"             \
+                 "setp.gt.and.s32 g, %6, 2, e;\n\tsetp.gt.and.s32 h, %6, 3, e;\n\t" GW_MMA(group, 0, "p", "e")      \
+                     GW_MMA(group, 128, "t", "f") GW_MMA(group, 256, "t", "g") GW_MMA(group, 384, "t", "h") "}" ::"r"(tacc), \
+                 "r"(xlo), "r"(ylo), "r"(acc), "r"(SW128_HI), "r"(gw_idesc(CTAS * GW_CTA, CTAS * GW_CTA)), "r"(mmas)  \
+                 : "memory")
+    if constexpr (CTAS == 2)
+        GW_STEP("2");
+    else
+        GW_STEP("1");
+#undef GW_STEP
 #undef GW_MMA
 }
 K3_DEV uint32_t mn_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(GW_PANEL >> 4) << 16); }
@@ -106,13 +120,13 @@ K3_DEV void mbar_expect(uint32_t bar, uint32_t bytes)
 struct GwTile {
     int e, n0, k0, row, rows;
 };
-K3_DEV GwTile gw_tile(const GwArgs &a, int u)
+K3_DEV GwTile gw_tile(const GwArgs &a, int u, int size)  // size: k and n of a tile
 {
     GwTile t;
     t.e = (int)a.tiles_e.div((uint32_t)u);
     const int r = u - t.e * (int)a.tiles_e.d, rn = (int)a.tiles_k.div((uint32_t)r);
-    t.n0 = rn * GW_N;
-    t.k0 = (r - rn * (int)a.tiles_k.d) * GW_M;
+    t.n0 = rn * size;
+    t.k0 = (r - rn * (int)a.tiles_k.d) * size;
     t.row = max(a.offsets[t.e], 0);
     t.rows = max(min(a.offsets[t.e + 1], a.slots) - t.row, 0);
     return t;
@@ -135,7 +149,7 @@ K3_DEV void gw_store(const CUtensorMap *map, uint32_t src, int k, int n, int e, 
                      : "memory");
 }
 
-template <typename CT>
+template <int CTAS, typename CT>
 __global__ void __launch_bounds__(GW_THREADS, 1)
     k3_grouped_wgrad(const __grid_constant__ CUtensorMap ymap, const __grid_constant__ CUtensorMap xmap,
                      const __grid_constant__ CUtensorMap cmap, const GwArgs a)
@@ -144,58 +158,74 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
     uint8_t *sm = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const uint32_t sbase = smem_addr(sm);
     uint64_t *bars = (uint64_t *)(sm + GW_OFF_BAR);
-    constexpr int NS = GW_NS;
+    constexpr int NS = GW_NS, TILE = CTAS * GW_CTA;
     constexpr int B_FULL = 0, B_EMPTY = NS, B_ACCF = 2 * NS, B_ACCE = B_ACCF + 2, B_FIN = B_ACCE + 2;
     uint32_t *tmem_slot = (uint32_t *)(bars + GW_BARS);
     volatile int *abort_flag = (volatile int *)(tmem_slot + 1);
     auto bar = [&](int i) { return smem_addr(bars + i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CTAS == 2 ? (int)cluster_rank() : 0;  // 0: the CTA that issues
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < NS; i++) {
-            mbar_init(bar(B_FULL + i), GW_FILL);
+            mbar_init(bar(B_FULL + i), CTAS * GW_FILL);
             mbar_init(bar(B_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; i++) {
             mbar_init(bar(B_ACCF + i), 1);
-            mbar_init(bar(B_ACCE + i), GW_EPI);
+            mbar_init(bar(B_ACCE + i), CTAS * GW_EPI);  // the epilogue warps of both CTAs
         }
         mbar_init(bar(B_FIN), 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == GW_W_MMA) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
-                     "r"(512)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        if constexpr (CTAS == 2) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                         "r"(2 * TILE)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(tmem_slot)),
+                         "r"(2 * TILE)
+                         : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        }
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync();  // the other CTA's barriers are initialised
     tc_fence_after();
     const uint32_t tmem = __reduce_max_sync(0xffffffffu, *(volatile uint32_t *)tmem_slot);
     griddep_wait();
-    const int n_tiles = a.E * (int)a.tiles_e.d, first = (int)blockIdx.x, step = (int)gridDim.x;
+    const int n_tiles = a.E * (int)a.tiles_e.d, first = (int)blockIdx.x / CTAS, step = (int)gridDim.x / CTAS;
+    auto commit = [](uint32_t b) {
+        if constexpr (CTAS == 2)
+            pair_commit(b);
+        else
+            mma_commit(b);
+    };
 
     if (warp >= GW_W_FILL) {
         // -------------------------------------------------- a stage's fillers
-        // Every NS-th step of this CTA's tiles; the GW_FILL warps of a stage have a
+        // Every ns-th step of these tiles; the GW_FILL warps of a stage have a
         // share of its rows each, the first one issues the TMA copies.
         const int s = (warp - GW_W_FILL) / GW_FILL, share = (warp - GW_W_FILL) % GW_FILL;
         constexpr int ROWS = GW_K / GW_FILL;
-        const uint32_t st = sbase + (uint32_t)(s * GW_STAGE), full = bar(B_FULL + s);
+        const uint32_t st = sbase + (uint32_t)(s * GW_STAGE), full0 = CTAS == 2 ? addr_of_rank(bar(B_FULL + s), 0) : bar(B_FULL + s);
         uint32_t turn = 0;
         int u = first, r0 = s * GW_K, tile = -1;
         GwTile t = {};
-        for (;; r0 += NS * GW_K, turn++) {
+        for (; s < a.ns; r0 += a.ns * GW_K, turn++) {
             for (; u < n_tiles; u += step) {
-                if (u != tile) tile = u, t = gw_tile(a, u);
+                if (u != tile) tile = u, t = gw_tile(a, u, TILE);
                 if (r0 < t.rows) break;
                 r0 -= (t.rows + GW_K - 1) / GW_K * GW_K;
             }
             if (u >= n_tiles) break;
-            const int n = min(GW_K, t.rows - r0);  // rows of the group in this step
-            const int n16 = (n + 15) & ~15;        // rows that its MMAs read
+            const int k0 = t.k0 + rank * GW_CTA, n0 = t.n0 + rank * GW_CTA;  // this CTA's columns
+            const int n = min(GW_K, t.rows - r0);                            // rows of the group in this step
+            const int n16 = (n + 15) & ~15;                                  // rows that its MMAs read
             // lane l: X's row of the share's row l
             int src = 0;
             if (a.gather && lane < ROWS && share * ROWS + lane < n) {
@@ -207,41 +237,51 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
             const bool whole = n == n16;
             // where no row past the group is read: dY (and X in group order) by TMA
             if (share == 0 && whole) {
-                if (lane == 0) mbar_expect(full, (uint32_t)(a.gather ? GW_STAGE - GW_OFF_Y : GW_STAGE));
+                if (rank == 0 && lane == 0)
+                    mbar_expect(bar(B_FULL + s), (uint32_t)CTAS * (uint32_t)(a.gather ? GW_STAGE - GW_OFF_Y : GW_STAGE));
                 __syncwarp();
-                if (lane < GW_N / 64)
-                    tma_load_2d(st + (uint32_t)(GW_OFF_Y + lane * GW_PANEL), &ymap, t.n0 + 64 * lane, t.row + r0, full);
-                else if (!a.gather && lane < GW_N / 64 + GW_M / 64)
-                    tma_load_2d(st + (uint32_t)((lane - GW_N / 64) * GW_PANEL), &xmap, t.k0 + 64 * (lane - GW_N / 64), t.row + r0,
-                                full);
+                auto load = [&](uint32_t at, const CUtensorMap *map, int col) {
+                    if constexpr (CTAS == 2)
+                        pair_load_2d(st + at, map, col, t.row + r0, full0);
+                    else
+                        tma_load_2d(st + at, map, col, t.row + r0, full0);
+                };
+                if (lane < GW_PANELS)
+                    load((uint32_t)(GW_OFF_Y + lane * GW_PANEL), &ymap, n0 + 64 * lane);
+                else if (!a.gather && lane < 2 * GW_PANELS)
+                    load((uint32_t)((lane - GW_PANELS) * GW_PANEL), &xmap, k0 + 64 * (lane - GW_PANELS));
                 __syncwarp();
             }
             if ((a.gather || !whole) && share * ROWS < n16) {
-                // A row of 128 + 256 columns is 16 + 32 chunks of 16 bytes: X's by half a
-                // warp, two rows at a time, dY's by a warp
+                // 128 columns of a row are 16 chunks of 16 bytes, two rows a warp
 #pragma unroll
                 for (int i = 0; i < ROWS; i += 2) {
                     const int r = share * ROWS + i + (lane >> 4), c = lane & 15;
                     const int g = __shfl_sync(0xffffffffu, src, i + (lane >> 4));
                     const long x = a.gather ? g : t.row + r0 + min(r, n - 1);
-                    gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.x + x * a.ldx, t.k0 + 8 * c, a.K, r < n);
+                    gw_chunk(st + (uint32_t)((c >> 3) * GW_PANEL), r, c & 7, a.x + x * a.ldx, k0 + 8 * c, a.K, r < n);
                 }
                 if (!whole)
 #pragma unroll
-                    for (int i = 0; i < ROWS; i++) {
-                        const int r = share * ROWS + i;
-                        gw_chunk(st + (uint32_t)(GW_OFF_Y + (lane >> 3) * GW_PANEL), r, lane & 7,
-                                 a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy, t.n0 + 8 * lane, a.N, r < n);
+                    for (int i = 0; i < ROWS; i += 2) {
+                        const int r = share * ROWS + i + (lane >> 4), c = lane & 15;
+                        gw_chunk(st + (uint32_t)(GW_OFF_Y + (c >> 3) * GW_PANEL), r, c & 7,
+                                 a.dy + (long)(t.row + r0 + min(r, n - 1)) * a.lddy, n0 + 8 * c, a.N, r < n);
                     }
                 asm volatile("cp.async.wait_all;" ::: "memory");
                 fence_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) mbar_arrive(full);
+            if (lane == 0) pair_arrive(full0);
         }
-        // drain: every copy issued here has landed before the CTA exits (the last turn's;
-        // earlier ones were waited for before their stage's reuse)
-        if (turn) mbar_wait(full, (turn - 1) & 1, a.err);
+        // drain: the last turn's copies of both CTAs have landed before the even CTA
+        // exits; the odd one waits in the closing cluster barrier
+        if (rank == 0 && turn) mbar_wait(bar(B_FULL + s), (turn - 1) & 1, a.err);
+        __syncwarp();
+    } else if (warp == GW_W_MMA && rank == 1) {
+        // the even CTA's last commits have arrived here before this CTA may exit
+        volatile int ignore = 0;  // after an abort too
+        if (lane == 0) tc_wait(bar(B_FIN), 0, a.err, &ignore);
         __syncwarp();
     } else if (warp == GW_W_MMA) {
         // -------------------------------------------------------------- MMA
@@ -250,7 +290,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
         bool ok = true, ready = false;
         const uint32_t lo = mn_lo(sbase);
         for (int u = first; u < n_tiles && ok; u += step) {
-            const GwTile t = gw_tile(a, u);
+            const GwTile t = gw_tile(a, u, TILE);
             if (!t.rows) continue;
             const int buf = (int)(ut & 1);
             if (ut >= 2 && !__all_sync(0xffffffffu, tc_wait(bar(B_ACCE + buf), (ut / 2 - 1) & 1, a.err, abort_flag)))
@@ -262,23 +302,23 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                     break;
                 }
                 tc_fence_after();
-                const int sn = s + 1 == NS ? 0 : s + 1;
+                const int sn = s + 1 == a.ns ? 0 : s + 1;
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // ask for the next stage before this one is issued, look at the answer after
                 const bool next = mbar_test(bar(B_FULL + sn), pn);
                 const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
-                gw_step(tmem + (uint32_t)(buf * GW_N), d, d + GW_OFF_Y / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
-                mma_commit(bar(B_EMPTY + s));
+                gw_step<CTAS>(tmem + (uint32_t)(buf * TILE), d, d + GW_OFF_Y / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
+                commit(bar(B_EMPTY + s));
                 ready = __all_sync(0xffffffffu, next);
                 s = sn;
                 phase = pn;
             }
             if (!ok) break;
-            mma_commit(bar(B_ACCF + buf));
+            commit(bar(B_ACCF + buf));
             ut++;
         }
         // every MMA issued above has completed before TMEM is freed
-        mma_commit(bar(B_FIN));
+        commit(bar(B_FIN));
         mbar_wait(bar(B_FIN), 0, a.err);
         __syncwarp();
     } else if (warp >= GW_W_EPI) {
@@ -290,20 +330,20 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
         // 64 x 1536 x 7168 from 16384 gathered rows took 664 us; with one box of 32 rows,
         // waited for, 558.)
         const int q = warp & 3, half = (warp - GW_W_EPI) >> 2;
-        constexpr int NP = GW_N / 32;
+        constexpr int NP = TILE / 32;
         CT *const boxes = (CT *)(sm + GW_OFF_C + (warp - GW_W_EPI) * 2 * GW_BOX * 128);
         uint32_t box = 0;
         uint32_t ut = 0;
         for (int u = first; u < n_tiles; u += step) {
-            const GwTile t = gw_tile(a, u);
+            const GwTile t = gw_tile(a, u, TILE);
             if (!t.rows && a.accumulate) continue;
             const int buf = (int)(ut & 1);
             if (t.rows) {
                 if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
                 tc_fence_after();
             }
-            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * GW_N);
-            const int k = t.k0 + q * 32 + lane;
+            const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * TILE);
+            const int k = t.k0 + rank * GW_CTA + q * 32 + lane;
 #pragma unroll 1
             for (int j = half; j < NP; j += 2) {
                 uint32_t r[32];
@@ -312,7 +352,12 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                     if (j + 2 >= NP) {  // this warp's last piece
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(B_ACCE + buf));
+                        if (lane == 0) {
+                            if constexpr (CTAS == 2)
+                                mbar_arrive_rank(bar(B_ACCE + buf), 0);
+                            else
+                                mbar_arrive(bar(B_ACCE + buf));
+                        }
                     }
                 } else {
 #pragma unroll
@@ -347,9 +392,13 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if constexpr (CTAS == 2) cluster_sync();  // neither CTA leaves, or frees TMEM, while the other's work may reach it
     if (warp == GW_W_MMA) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+        if constexpr (CTAS == 2)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * TILE) : "memory");
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2 * TILE) : "memory");
     }
 }
 
@@ -363,7 +412,7 @@ int row_map(CUtensorMap *map, const void *p, int cols, int n_rows, long ld)
     return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, p, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-template <typename CT>
+template <int CTAS, typename CT>
 int launch_gw(const GwArgs &a, cudaStream_t s)
 {
     CUtensorMap ymap, xmap;
@@ -377,9 +426,10 @@ int launch_gw(const GwArgs &a, cudaStream_t s)
         st = encode_map(&cmap, sizeof(CT) == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, a.dw,
                         dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE);
     if (st != K3MOE_OK) return st;
-    if (ensure_smem((const void *)k3_grouped_wgrad<CT>, GW_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
-    const int grid = std::min(a.E * (int)a.tiles_e.d, num_sms());
-    if (launch_pdl(k3_grouped_wgrad<CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, xmap, cmap, a) != cudaSuccess) {
+    if (ensure_smem((const void *)k3_grouped_wgrad<CTAS, CT>, GW_SMEM) != K3MOE_OK) return K3MOE_ECUDA;
+    const int grid = CTAS * std::min(a.E * (int)a.tiles_e.d, num_sms() / CTAS);
+    if (launch_dependent(true, CTAS, k3_grouped_wgrad<CTAS, CT>, dim3((unsigned)grid), dim3(GW_THREADS), GW_SMEM, s, ymap, xmap, cmap, a) !=
+        cudaSuccess) {
         cudaGetLastError();
         return K3MOE_ECUDA;
     }
@@ -394,13 +444,21 @@ int launch_grouped_wgrad(const k3moe_grouped_wgrad_desc &d, int *err, cudaStream
     GwArgs a = {};
     a.offsets = g->offsets, a.order = g->order;
     a.E = g->E, a.top_k = g->top_k, a.slots = g->tokens * g->top_k, a.gather = d.gather ? 1 : 0, a.xrows = d.xrows;
-    const int tiles_k = (d.K + GW_M - 1) / GW_M;
-    const long tiles = (long)tiles_k * ((d.N + GW_N - 1) / GW_N);
+    // single CTAs or pairs, in us: 66 tiles of single CTAs from few rows 5.9 and 9.2, 128 from
+    // 512 rows a group 10.9 and 15.1, 256 from 2048 24.5 and 29.5, 512 from 128 10.6 and 11.0
+    const bool pair = (long)a.E * ((d.K + GW_CTA - 1) / GW_CTA) * ((d.N + GW_CTA - 1) / GW_CTA) > 2 * num_sms();
+    const int size = pair ? 2 * GW_CTA : GW_CTA, tiles_k = (d.K + size - 1) / size;
+    const long tiles = (long)tiles_k * ((d.N + size - 1) / size);
+    // In group order, where X comes from HBM, the rows of a short group's tile are read no
+    // further ahead than that tile's time (64 x 1536 x 7168, rows a group: 256 488 us with
+    // four stages, 553 with six; 320 531, 573; 384 573, 577; 448 618, 569).
+    a.ns = !d.gather && a.slots <= 352L * std::min(a.E, a.slots) ? 4 : GW_NS;
     a.tiles_k = FastDiv((uint32_t)tiles_k), a.tiles_e = FastDiv((uint32_t)tiles);
     a.N = d.N, a.K = d.K, a.accumulate = d.accumulate ? 1 : 0, a.err = err;
     a.dy = (const __nv_bfloat16 *)d.dY, a.x = (const __nv_bfloat16 *)d.X, a.dw = d.dW;
     a.lddy = (long)d.lddy, a.ldx = (long)d.ldx;
-    return d.dw_dtype == K3MOE_BF16 ? launch_gw<__nv_bfloat16>(a, s) : launch_gw<float>(a, s);
+    if (d.dw_dtype == K3MOE_BF16) return pair ? launch_gw<2, __nv_bfloat16>(a, s) : launch_gw<1, __nv_bfloat16>(a, s);
+    return pair ? launch_gw<2, float>(a, s) : launch_gw<1, float>(a, s);
 }
 
 }  // namespace k3

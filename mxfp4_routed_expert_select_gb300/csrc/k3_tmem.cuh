@@ -62,6 +62,25 @@ K3_DEV uint32_t addr_of_rank(uint32_t addr, uint32_t rank)
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
     return a;
 }
+// A tile of this CTA, its bytes counted on barrier `bar`, a shared::cluster address (the
+// even CTA's).
+K3_DEV void pair_load_2d(uint32_t dst, const CUtensorMap *map, int x, int row, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], "
+                 "[%1, {%2, %3}], [%4];" ::"r"(dst),
+                 "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
+                 : "memory");
+}
+// Arrival at the even CTA's barrier behind what this thread (and, after a warp barrier,
+// its warp) has written to its own CTA's shared memory.  Those bytes never leave that
+// shared memory: the tensor core beside it reads them, behind the proxy fence that each
+// writer has passed.  So no wider fence than the CTA's own goes with the arrival; one at
+// cluster scope takes 1000 clocks or more, and with it in each stage's path 65536 rows x
+// 1536 x 7168 took 648 us instead of 520.
+K3_DEV void pair_arrive(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // Arrival at the barrier of the same offset in the pair's CTA `rank`, for a
 // hand-over of tensor memory alone: the accumulator's loads are ordered by their
 // wait and the tcgen05 fence before this, and no ordinary memory is handed over, so

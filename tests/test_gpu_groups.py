@@ -34,7 +34,7 @@ def _check_plan(g, ids):
 @pytest.mark.parametrize("kind", ["any", "one", "none", "dropped"])
 @pytest.mark.parametrize("T,kk,E", [(1, 1, 1), (1, 16, 896), (7, 3, 5), (64, 16, 128), (31, 32, 1024), (256, 32, 1000),
                                     (4096, 1, 33), (8192, 1, 1024), (2049, 2, 40), (4097, 1, 7), (4096, 16, 896), (20001, 5, 64),
-                                    (8192, 16, 300), (8193, 16, 1024)])
+                                    (8192, 16, 300), (8193, 16, 1024), (40001, 16, 300)])
 def test_plan(T, kk, E, kind):
     ids = _ids(T, kk, E, T + E, kind)
     g = k.ExpertGroups(E, kk, T + 3)
