@@ -185,7 +185,7 @@ __global__ void __launch_bounds__(GR_THREADS) k3_groups_scan(const GroupArgs a)
 // out[t] (+)= sum_j w[t][j] y[pos[t][j]] over a token's slots, in rising j.
 // Bound: HBM, each row of y read once.  A thread takes eight columns of a token and
 // has up to CB_DEEP slots' loads in flight (4096 tokens x 16 x 7168 bf16, 1 GB: 135 us;
-// backward, 1.9 GB: 312).
+// backward, 1.9 GB: 296).
 
 constexpr int CB_DEEP = 8;
 
@@ -240,13 +240,17 @@ __global__ void __launch_bounds__(128) k3_combine(const CombineArgs a)
 
 // dy[pos[t][j]] = w[t][j] dout[t],  dw[t][j] = <dout[t], y[pos[t][j]]>.  A CTA takes
 // DEEP slots of a token, its threads eight columns at a time; the dot products are
-// joined together.  DEEP 4 and up to 1024 threads where a batch has no more tokens than
-// fill the SMs once, else 8 and 256 (7168 bf16, us: 16 tokens x 16 3.5 and 5.9, 64 x 16 6.3
-// and 6.6, 128 x 16 11.8 and 9.1, 1024 x 16 106 and 84; 152 x 8 6.6 and 6.8, 256 x 8 11.8
-// and 9.0).
-template <typename T, bool VEC, int DEEP>
-__global__ void __launch_bounds__(DEEP == 4 ? 1024 : 256) k3_combine_backward(const CombineArgs a)
+// joined together.  Its threads are the fewer the more CTAs there are: 512 where they
+// all run at once, 256, and 128 from three CTAs an SM on (7168 bf16, us, 512, 256 and 128:
+// 64 tokens x 4 3.4 3.8 4.7, 64 x 16 5.1 5.0 5.9, 256 x 16 19.9 17.7 16.6, 4096 x 16 325 293
+// 296; 2048 bf16, 4096 x 16 101 101 85).  Eight slots to a CTA of 256: 64 x 16 6.4,
+// 256 x 16 20.7, 4096 x 16 318.
+constexpr int CBB_DEEP = 4;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(512) k3_combine_backward(const CombineArgs a)
 {
+    constexpr int DEEP = CBB_DEEP;
     __shared__ float sh[DEEP][32];
     griddep_wait();
     griddep_launch_dependents();
@@ -356,15 +360,13 @@ int launch_combine_backward(const k3moe_combine_backward_desc &d, cudaStream_t s
     a.T = d.host_groups->tokens, a.k = d.host_groups->top_k, a.n = d.n, a.rows = a.T * a.k;
     const bool vec = a.n % 8 == 0 && rows16(a.dout, a.ldo, d.dtype) && rows16(a.dy, a.lddy, d.dtype) &&
                      (!a.dw || rows16(a.y, a.ldy, d.dtype));
-    const bool few = (long)a.T * ((a.k + 7) / 8) <= num_sms();
-    a.blocks = few ? (a.k + 3) / 4 : (a.k + 7) / 8;
-    const auto pick = [&](auto small, auto large) { return few ? small : large; };
-    void (*const kernel)(CombineArgs) =
-        d.dtype == K3MOE_BF16 ? (vec ? pick(k3_combine_backward<uint16_t, true, 4>, k3_combine_backward<uint16_t, true, 8>)
-                                     : pick(k3_combine_backward<uint16_t, false, 4>, k3_combine_backward<uint16_t, false, 8>))
-                              : (vec ? pick(k3_combine_backward<uint32_t, true, 4>, k3_combine_backward<uint32_t, true, 8>)
-                                     : pick(k3_combine_backward<uint32_t, false, 4>, k3_combine_backward<uint32_t, false, 8>));
-    return launch(kernel, (long)a.T * a.blocks, std::min(few ? 1024 : 256, (a.n + 255) / 256 * 32), 0, s, a);
+    a.blocks = (a.k + CBB_DEEP - 1) / CBB_DEEP;
+    const long ctas = (long)a.T * a.blocks;
+    const int threads = ctas <= num_sms() ? 512 : ctas <= 3 * num_sms() ? 256 : 128;
+    void (*const kernel)(CombineArgs) = d.dtype == K3MOE_BF16
+                                            ? (vec ? k3_combine_backward<uint16_t, true> : k3_combine_backward<uint16_t, false>)
+                                            : (vec ? k3_combine_backward<uint32_t, true> : k3_combine_backward<uint32_t, false>);
+    return launch(kernel, ctas, std::min(threads, (a.n + 255) / 256 * 32), 0, s, a);
 }
 
 }  // namespace k3
