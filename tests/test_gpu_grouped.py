@@ -315,6 +315,42 @@ def test_wgrad(N, K, kk, pad, sizes, gather, out):
     assert k.device_error() == 0
 
 
+# more tiles than two waves of single CTAs: pairs; groups of few rows and of many (in group
+# order they keep four and six stages), columns that leave the odd CTA little or nothing
+MANY = {"short": [200, 128, 129, 1, 0, 257], "long": [900, 400, 0, 513, 64, 463]}
+
+
+@pytest.mark.parametrize("out", ["f32", "bf16"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("N,K,sizes", [(1032, 2056, "short"), (1032, 2056, "long"), (136, 264, "experts"), (72, 520, "experts")])
+def test_wgrad_pairs(N, K, sizes, gather, out):
+    kk = 2
+    sizes = [int(n) for n in np.random.default_rng(N).integers(0, 70, 128)] if sizes == "experts" else MANY[sizes]
+    g, ids = _plan(sizes, kk, 9)
+    E, slots = len(sizes), ids.size
+    off, src = _sources(ids, E, gather)
+    gen = torch.Generator(device="cuda").manual_seed(N + K)
+    dy = torch.randn(slots, N + 8, generator=gen, device="cuda").bfloat16()[:, :N]
+    x = torch.randn(ids.shape[0] if gather else slots, K, generator=gen, device="cuda").bfloat16()
+    dy[off[E]:] = float("nan")
+    dw = torch.full((E, N, K), 7.0, dtype=DT[out], device="cuda")
+    k.grouped_wgrad(dw, dy, x, g, gather=gather)
+    rows = torch.from_numpy(np.ascontiguousarray(src)).cuda().long()
+    for e in range(E):
+        s = slice(int(off[e]), int(off[e + 1]))
+        DY, X = dy[s].double(), x[rows[s]].double()
+        want, mag = DY.t() @ X, DY.abs().t() @ X.abs()
+        tol = mag * ((off[e + 1] - off[e]) / 16 + 10) * 2.0 ** -22 + want.abs() * HALF[out]
+        assert bool(((dw[e].double() - want).abs() <= tol).all()), e
+    again = torch.empty_like(dw)
+    k.grouped_wgrad(again, dy, x, g, gather=gather)
+    assert torch.equal(again, dw)
+    if out == "f32":
+        k.grouped_wgrad(dw, dy, x, g, gather=gather, accumulate=True)
+        assert torch.equal(dw, again + again)
+    assert k.device_error() == 0
+
+
 def test_wgrad_bad_values_stay_in_their_expert():
     sizes, kk, N, K = [30, 64, 5], 1, 136, 264
     g, ids = _plan(sizes, kk)
