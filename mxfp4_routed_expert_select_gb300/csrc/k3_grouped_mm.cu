@@ -22,8 +22,8 @@
 //
 // Bound: few rows stream the weights (1 token x 16 of 896 experts x 1536 x 7168, 94 MB, 21.2
 // us; 64 x 16 over 128 experts, 753 MB, 123, 6.1 TB/s), many the pairs' shared memory and
-// MMAs (65536 rows with 64 experts x 1536 x 7168 gathered 575 us, 2.5 PFLOP/s, in group
-// order 490).
+// MMAs (65536 rows with 64 experts x 1536 x 7168 gathered 528 us, 2.7 PFLOP/s, in group
+// order 440).
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -479,14 +479,18 @@ __global__ void __launch_bounds__(GmCfg<NT>::THREADS, 1)
 // The MMA's columns are the rows of the group, so their number follows the tile: a
 // group is cut into equal tiles of whole 32 rows, and a short tile costs a short MMA.
 //
-// The even CTA issues for both.  Every stage has two filling warps in each CTA; the
-// copies of both CTAs are counted on the even CTA's barrier, and each warp arrives there
-// when its rows' codes and scale bytes are in place.  Warp 1 finds out each tile (its
+// The even CTA issues for both.  Every stage has two filling warps in each CTA, and two
+// further warps bring the rows' scale bytes of all stages; the copies of both CTAs are
+// counted on the even CTA's barrier, and each warp arrives there when its part is in place.
+// (A lane reads 16 scale bytes of a row, four steps' worth; a word for each step, by the
+// stage's own warps, was a line of L1 a lane: 65536 rows x 1536 x 7168 with 64 experts 547
+// us gathered and 457 in group order, so 528 and 440.)  Warp 1 finds out each tile (its
 // expert, its rows, which rows of the 8-bit matrix they are) ahead of the others and
 // leaves it in a ring: a search takes 1000 clocks, a sixth of a tile with K = 1536.
 
 constexpr int GP_EPI = 8, GP_FILL = 2, GP_NT = 256, GP_RING = 4;
-constexpr int GP_W_PLAN = 1, GP_W_FILL = GM_W_EPI + GP_EPI;
+constexpr int GP_SC = 2;  // warps of scale bytes, 128 rows each
+constexpr int GP_W_PLAN = 1, GP_W_SCALE = 2, GP_W_FILL = GM_W_EPI + GP_EPI;
 constexpr int GP_OFF_X = GM_M * 128, GP_OFF_WA = 2 * GM_M * 128, GP_OFF_XA = GP_OFF_WA + 512;
 constexpr int GP_STAGE = GP_OFF_XA + 1024 + 512, GP_NS = 6;
 constexpr int GP_THREADS = 32 * (GP_W_FILL + GP_FILL * GP_NS);
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&amap) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)&xmap) : "memory");
         for (int i = 0; i < NS; i++) {
-            mbar_init(bar(B_FULL + i), 1 + 2 * GP_FILL);  // the bytes announced; each filler's part done
+            mbar_init(bar(B_FULL + i), 1 + 2 * (GP_FILL + GP_SC));  // the bytes announced; each warp's part done
             mbar_init(bar(B_EMPTY + i), 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -606,7 +610,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         }
         for (int i = 0; i < GP_RING; i++) {
             mbar_init(bar(B_TILEF + i), 1);
-            mbar_init(bar(B_TILEE + i), GP_FILL * NS + GP_EPI + (rank == 0));  // the warps that read it
+            mbar_init(bar(B_TILEE + i), GP_FILL * NS + GP_SC + GP_EPI + (rank == 0));  // the warps that read it
         }
         mbar_init(bar(B_FIN), 1);
         *abort_flag = 0;
@@ -654,11 +658,70 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             if (lane == 0) mbar_arrive(bar(B_TILEF + (int)(i % GP_RING)));
             if (u >= n_tiles) break;
         }
+    } else if (warp >= GP_W_SCALE && warp < GM_W_EPI) {
+        // ------------------------------------------------------- scale bytes
+        // Of each tile's 256 rows a warp has 128, a lane every 32nd, four steps at a time,
+        // the next four on their way while these are handed out.
+        const int f = warp - GP_W_SCALE;
+        const bool wide = a.nks % 4 == 0 && ((uintptr_t)a.scales & 15u) == 0;
+        uint32_t phase = 1;  // before its first completion a barrier's odd phase counts as passed
+        int s = 0;
+        for (uint32_t i = 0;; i++) {
+            if (!tile_in(i)) break;
+            const GpTile *t = ring + i % GP_RING;
+            if (t->e < 0) break;
+            const uint32_t *row[4];
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const int r = 128 * f + 32 * j + lane;
+                row[j] = r < t->rows ? (const uint32_t *)(a.scales + (long)t->src[r] * a.sstride) : nullptr;
+            }
+            tile_out(i);
+            uint4 now[4], next[4];
+            auto load = [&](int ks) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    next[j] = make_uint4(0u, 0u, 0u, 0u);
+                    if (!row[j] || ks >= a.nks) continue;
+                    if (wide) {
+                        next[j] = *(const uint4 *)(row[j] + ks);
+                    } else {
+                        next[j].x = row[j][ks];
+                        if (ks + 1 < a.nks) next[j].y = row[j][ks + 1];
+                        if (ks + 2 < a.nks) next[j].z = row[j][ks + 2];
+                        if (ks + 3 < a.nks) next[j].w = row[j][ks + 3];
+                    }
+                }
+            };
+            load(0);
+            bool ok = true;
+            for (int ks = 0; ks < a.nks && ok; ks += 4) {
+#pragma unroll
+                for (int j = 0; j < 4; j++) now[j] = next[j];
+                load(ks + 4);
+#pragma unroll
+                for (int q = 0; q < 4; q++) {
+                    if (ks + q >= a.nks) break;
+                    if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), phase, a.err, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    auto word = [&](const uint4 &v) { return q == 0 ? v.x : q == 1 ? v.y : q == 2 ? v.z : v.w; };
+                    *(uint4 *)(sm + s * GP_STAGE + GP_OFF_XA + f * 512 + lane * 16) =
+                        make_uint4(word(now[0]), word(now[1]), word(now[2]), word(now[3]));
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) pair_arrive(addr_of_rank(bar(B_FULL + s), 0));
+                    if (++s == NS) s = 0, phase ^= 1u;
+                }
+            }
+            if (!ok) break;
+        }
     } else if (warp >= GP_W_FILL) {
         // -------------------------------------------------- a stage's fillers
         // Every NS-th step of this pair's tiles.  Of this CTA's rows (half the tile's)
         // each warp copies 64, lanes 8 q .. 8 q + 7 the 16-byte chunks of rows q, q + 4,
-        // ..; of all the tile's rows it brings the scale words of 128, a lane every 32nd.
+        // ...
         constexpr int R = 64 / 4;
         const int s = (warp - GP_W_FILL) / GP_FILL, f = (warp - GP_W_FILL) % GP_FILL;
         const uint32_t st = sbase + (uint32_t)(s * GP_STAGE), full0 = addr_of_rank(bar(B_FULL + s), 0);
@@ -675,12 +738,6 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             }
             if (!ok || t->e < 0) break;
             const int rows = t->rows, half = t->half;
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const int r = 128 * f + 32 * j + lane;
-                w[j] = r < rows ? *(const uint32_t *)(a.scales + (long)t->src[r] * a.sstride + 4 * ks) : 0u;
-            }
             if (!__all_sync(0xffffffffu, tc_wait(bar(B_EMPTY + s), (turn & 1) ^ 1u, a.err, abort_flag))) break;
             const int boxes = (half + GP_BOX - 1) / GP_BOX;
             if (f == 0) {
@@ -701,9 +758,10 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                 pair_load_2d(st + GP_OFF_X + (uint32_t)(lane * GP_BOX * 128), &xmap, ks * 128, t->row + rank * half + lane * GP_BOX,
                           full0);
             }
-            *(uint4 *)(sm + s * GP_STAGE + GP_OFF_XA + f * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            if (a.gather) asm volatile("cp.async.wait_all;" ::: "memory");
-            fence_async_smem();
+            if (a.gather) {
+                asm volatile("cp.async.wait_all;" ::: "memory");
+                fence_async_smem();
+            }
             __syncwarp();
             if (lane == 0) pair_arrive(full0);
         }
