@@ -12,9 +12,10 @@
 // kernel, in an order that does not depend on timing.  Rows too long for that are read
 // twice by a CTA, the second time from L2.
 //
-// bf16, x, delta, r and y or the backward call's four: 8192 x 4096 44 us (6.1 TB/s) and
+// bf16, x, delta, r and y or the backward call's four: 8192 x 4096 43 us (6.2 TB/s) and
 // 50, 8192 x 8192 85 (6.3) and 99, 8192 x 32768 385 (5.6) and 602; 4096 x 7168 to 8 bits
-// 39 us.
+// 36 us (each value takes 25 instructions; with the sums of bf16 rows value by value 29, and
+// 40 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,11 +41,21 @@ struct NormArgs {
     float eps, inv_n;
 };
 
-// v rounded to the rows' type.
+// a + b, each sum rounded once to the rows' type.
 template <typename T>
-K3_DEV float rounded(float v)
+K3_DEV Raw<T> sum8(const Raw<T> &a, const Raw<T> &b)
 {
-    return sizeof(T) == 2 ? __bfloat162float(__float2bfloat16_rn(v)) : v;
+    Raw<T> r;
+#pragma unroll
+    for (int i = 0; i < (int)(2 * sizeof(T)); i++) {
+        if constexpr (sizeof(T) == 2) {
+            const __nv_bfloat162 v = __hadd2(*(const __nv_bfloat162 *)&a.w[i], *(const __nv_bfloat162 *)&b.w[i]);
+            r.w[i] = *(const uint32_t *)&v;
+        } else {
+            r.w[i] = __float_as_uint(__uint_as_float(a.w[i]) + __uint_as_float(b.w[i]));
+        }
+    }
+    return r;
 }
 K3_DEV float warp_sum(float v)
 {
@@ -163,6 +174,26 @@ struct Cols {
         return r;
     }
     template <typename T>
+    K3_DEV void store(void *base, long ld, int t, int c, const Raw<T> &v) const
+    {
+        T *p = (T *)base + (long)t * ld;
+        if constexpr (WIDE) {
+            if (first + c * step < n)
+#pragma unroll
+                for (int i = 0; i < (int)sizeof(T) / 2; i++)
+                    ((uint4 *)(p + first + c * step))[i] = make_uint4(v.w[4 * i], v.w[4 * i + 1], v.w[4 * i + 2], v.w[4 * i + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                if (at(c, i) < n) {
+                    if constexpr (sizeof(T) == 2)
+                        p[at(c, i)] = (T)(v.w[i >> 1] >> (16 * (i & 1)));
+                    else
+                        p[at(c, i)] = v.w[i];
+                }
+        }
+    }
+    template <typename T>
     K3_DEV void store(void *base, long ld, int t, int c, const float (&v)[8]) const
     {
         if constexpr (WIDE) {
@@ -231,17 +262,13 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
         float v[C][8], ss = 0.f;
 #pragma unroll
         for (int c = 0; c < C; c++) {
+            if (a.delta) x[c] = sum8(x[c], d[c]);
+            if (a.r) cols.template store<T>(a.r, a.ldr, t, c, x[c]);
 #pragma unroll
-            for (int i = 0; i < 8; i++) {
-                v[c][i] = value(x[c], i);
-                if (a.delta) v[c][i] = rounded<T>(v[c][i] + value(d[c], i));
-            }
+            for (int i = 0; i < 8; i++) v[c][i] = value(x[c], i);
             ss += squares(v[c]);
         }
         load(t + step);
-        if (a.r)
-#pragma unroll
-            for (int c = 0; c < C; c++) cols.template store<T>(a.r, a.ldr, t, c, v[c]);
         ss = team.sum(ss);
         // the sum is exact enough unless it left the normal range, or fell below
         // where eps outweighs what it lost
@@ -360,7 +387,7 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(
     const Cols<WIDE> cols(team, a.n);
     const int chunks = (a.n + LONG_THREADS * 8 - 1) / (LONG_THREADS * 8);
     for (int t = (int)blockIdx.x; t < a.T; t += (int)gridDim.x) {
-        // f(c, v) with the values of r, read as such (stored) or made from x and delta
+        // f(c, r) with the chunks of r, read as such (stored) or made from x and delta
         auto row = [&](bool stored, auto &&f) {
 #pragma unroll U == 2 || !WIDE ? 1 : 2
             for (int c0 = 0; c0 < chunks; c0 += U) {
@@ -372,20 +399,18 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(
                 }
 #pragma unroll
                 for (int u = 0; u < U; u++) {
-                    float v[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        v[i] = value(x[u], i);
-                        if (a.delta && !stored) v[i] = rounded<T>(v[i] + value(d[u], i));
-                    }
-                    f(c0 + u, v);
+                    if (a.delta && !stored) x[u] = sum8(x[u], d[u]);
+                    f(c0 + u, x[u]);
                 }
             }
         };
         float ss = 0.f;
-        row(false, [&](int c, float (&v)[8]) {
+        row(false, [&](int c, const Raw<T> &r) {
+            float v[8];
+#pragma unroll
+            for (int i = 0; i < 8; i++) v[i] = value(r, i);
             ss += squares(v);
-            if (a.r) cols.template store<T>(a.r, a.ldr, t, c, v);
+            if (a.r) cols.template store<T>(a.r, a.ldr, t, c, r);
         });
         asm volatile("" ::: "memory");  // r, which may lie over x, is stored before it is read again
         const bool stored = a.r != nullptr;
@@ -394,18 +419,18 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(
         if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f))
             s = far_rstd(
                 team, [&](auto &&take) {
-                    row(stored, [&](int, float (&v)[8]) {
+                    row(stored, [&](int, const Raw<T> &r) {
 #pragma unroll
-                        for (int i = 0; i < 8; i++) take(v[i]);
+                        for (int i = 0; i < 8; i++) take(value(r, i));
                     });
                 },
                 ss, a.inv_n, a.eps);
         if (a.rstd && threadIdx.x == 0) a.rstd[t] = s;
-        row(stored, [&](int c, float (&v)[8]) {
-            float g[8];
+        row(stored, [&](int c, const Raw<T> &r) {
+            float g[8], v[8];
             cols.load_gain(g, a.gain, c);
 #pragma unroll
-            for (int i = 0; i < 8; i++) v[i] = v[i] * s * g[i];
+            for (int i = 0; i < 8; i++) v[i] = value(r, i) * s * g[i];
             if (a.y) cols.template store<T>(a.y, a.ldy, t, c, v);
             if (a.codes) cols.store_8bit(a.codes, a.scales, t, c, v);
         });
