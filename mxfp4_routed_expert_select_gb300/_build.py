@@ -26,14 +26,15 @@ def _stale(outputs_mtime):
     return any(os.path.getmtime(d) > outputs_mtime for d in deps)
 
 
-def build(force=False, verbose=False, extra=()):
-    if not force and os.path.exists(SO) and not _stale(os.path.getmtime(SO)):
-        return SO
-    os.makedirs(BUILD, exist_ok=True)
+def build(force=False, verbose=False, extra=(), so=SO):
+    build_dir = BUILD if so == SO else so + ".objects"
+    if not force and os.path.exists(so) and not _stale(os.path.getmtime(so)):
+        return so
+    os.makedirs(build_dir, exist_ok=True)
     procs = []
     objs = []
     for src in sources():
-        obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
+        obj = os.path.join(build_dir, os.path.splitext(os.path.basename(src))[0] + ".o")
         objs.append(obj)
         cmd = [NVCC] + ARCH + FLAGS + list(extra) + ["-c", src, "-o", obj]
         if verbose:
@@ -48,10 +49,10 @@ def build(force=False, verbose=False, extra=()):
             failed.append(src)
     if failed:
         raise RuntimeError("nvcc failed for: " + ", ".join(failed))
-    tmp = SO + ".%d.tmp" % os.getpid()
+    tmp = so + ".%d.tmp" % os.getpid()
     subprocess.check_call([NVCC] + ARCH + ["-shared", "-o", tmp] + objs)
-    os.replace(tmp, SO)
-    return SO
+    os.replace(tmp, so)
+    return so
 
 
 if __name__ == "__main__":

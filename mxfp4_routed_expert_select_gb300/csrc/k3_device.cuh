@@ -282,7 +282,10 @@ K3_DEV uint64_t global_ns()
     asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
     return t;
 }
-constexpr uint64_t kWaitLimitNs = 2000000000ull;  // 2 s: far beyond any legal wait
+#ifndef K3_WAIT_LIMIT_NS
+#define K3_WAIT_LIMIT_NS 2000000000ull  // 2 s: far beyond any legal wait for one step
+#endif
+constexpr uint64_t kWaitLimitNs = K3_WAIT_LIMIT_NS;
 // try_wait with a suspend-time hint: a warp whose barrier phase has not
 // completed is parked by the hardware (up to the hint) instead of spinning,
 // so waiting warps do not take issue slots from working ones.

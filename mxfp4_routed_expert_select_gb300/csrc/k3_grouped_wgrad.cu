@@ -25,8 +25,9 @@
 // GB, gathered 480 us, 5.9 TB/s), the MMAs beside the copies where they are long (16 x 2048
 // x 2048 from 131072 rows 600 us in group order, 1.8 PFLOP/s; gathered 622).
 //
-// Every wait is bounded (2 s); a timeout sets the device error word and the CTA
-// drains its copies and MMAs, frees TMEM and exits.
+// Every wait is bounded (2 s, and 16 us a step where a whole tile is waited for); a
+// timeout sets the device error word and the CTA drains its copies and MMAs, frees TMEM
+// and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -339,7 +340,9 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
             if (!t.rows && a.accumulate) continue;
             const int buf = (int)(ut & 1);
             if (t.rows) {
-                if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
+                if (!__all_sync(0xffffffffu, tc_wait_tile(bar(B_ACCF + buf), (ut / 2) & 1, (uint32_t)(t.rows / GW_K), a.err,
+                                                          abort_flag)))
+                    break;
                 tc_fence_after();
             }
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * TILE);

@@ -25,8 +25,9 @@
 // warps 4 and up read the accumulators.  Rows, columns and K past the matrices are
 // zero-filled by the copies or not stored.
 //
-// Every wait is bounded (2 s); a timeout sets the device error word and the CTA
-// drains its copies and MMAs, frees TMEM and exits.
+// Every wait is bounded (2 s, and 16 us a step where a whole tile is waited for); a
+// timeout sets the device error word and the CTA drains its copies and MMAs, frees TMEM
+// and exits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
@@ -387,7 +388,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         uint32_t ut = 0;
         for (int u = first; u < a.n_tiles; u += step, ut++) {
             const int buf = (int)(ut & 1);
-            if (!__all_sync(0xffffffffu, tc_wait(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
+            if (!__all_sync(0xffffffffu, tc_wait_tile(bar(B_ACCF + buf), (ut / 2) & 1, (uint32_t)(k1 - k0), a.err, abort_flag)))
+                break;
             tc_fence_after();
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf * NT);
             const int n = (u / a.tiles_t) * MG_M + q * 32 + lane, m0 = (u % a.tiles_t) * NT;
@@ -670,7 +672,9 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
         uint32_t ut = 0;
         for (int u = first; u < a.n_tiles; u += step, ut++) {
             const int buf = (int)(ut & 1);
-            if (!__all_sync(0xffffffffu, tc_wait_cluster(bar(B_ACCF + buf), (ut / 2) & 1, a.err, abort_flag))) break;
+            if (!__all_sync(0xffffffffu, tc_wait_tile<mbar_try_wait_cluster>(bar(B_ACCF + buf), (ut / 2) & 1, (uint32_t)a.nks, a.err,
+                                                                             abort_flag)))
+                break;
             tc_fence_after();
             const uint32_t tacc = tmem + ((uint32_t)(q * 32) << 16) + (uint32_t)(buf ? C::OVER : 0);
             const int m0 = (u / a.tiles_t) * 2 * MG_M + rank * MG_M + q * 32, n0 = (u % a.tiles_t) * NT;

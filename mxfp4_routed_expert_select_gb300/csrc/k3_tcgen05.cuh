@@ -99,6 +99,29 @@ K3_DEV bool tc_wait(uint32_t bar, uint32_t parity, int *err, volatile int *abort
     }
     return true;
 }
-
+// A wait for a tile of `steps` steps, each of which other warps of the CTA wait for on
+// their own: the limit of a wait and 16 us a step (one takes under 1 us), left sooner
+// when one of the others has given up.  TRY: mbar_try_wait or one of another scope.
+template <uint32_t (*TRY)(uint32_t, uint32_t)>
+static __device__ __noinline__ bool mbar_wait_tile_slow(uint32_t bar, uint32_t parity, uint32_t steps, int *err,
+                                                        volatile int *abort_flag)
+{
+    const uint64_t t0 = global_ns(), limit = kWaitLimitNs + (uint64_t)steps * 16000u;
+    for (uint32_t n = 1;; n++) {
+        if (TRY(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if ((n & 63u) == 0 && global_ns() - t0 > limit) {
+            set_device_error(err, K3MOE_ETIMEOUT);
+            *abort_flag = 1;
+            return false;
+        }
+    }
+}
+template <uint32_t (*TRY)(uint32_t, uint32_t) = mbar_try_wait>
+K3_DEV bool tc_wait_tile(uint32_t bar, uint32_t parity, uint32_t steps, int *err, volatile int *abort_flag)
+{
+    if (*abort_flag) return false;
+    return TRY(bar, parity) || mbar_wait_tile_slow<TRY>(bar, parity, steps, err, abort_flag);
+}
 
 }  // namespace k3
