@@ -770,10 +770,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
         if (rank == 0 && turn) mbar_wait(bar(B_FULL + s), (turn - 1) & 1, a.err);
         __syncwarp();
     } else if (warp == GM_W_MMA && rank == 1) {
-        // the even CTA's last commits have arrived here before this CTA may exit
-        volatile int ignore = 0;  // after an abort too
-        if (lane == 0) tc_wait(bar(B_FIN), 0, a.err, &ignore);
-        __syncwarp();
+        // the even CTA issues for both
     } else if (warp == GM_W_MMA) {
         // -------------------------------------------------------------- MMA
         uint32_t phase = 0, slot = 0, it = 0;
@@ -862,6 +859,14 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
     }
     tc_fence_before();
     __syncthreads();
+    // The even CTA's last commits have arrived here before this CTA may exit.  The
+    // last tile has been read, so they are on their way: a short wait after a call of any
+    // length.
+    if (rank == 1 && warp == GM_W_MMA) {
+        volatile int ignore = 0;  // after an abort too
+        if (lane == 0) tc_wait(bar(B_FIN), 0, a.err, &ignore);
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA leaves, or frees TMEM, while the other's work may reach it
     if (warp == GM_W_MMA) {
         tc_fence_after();

@@ -610,10 +610,7 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
                 mbar_wait(bar(B_FULL + (int)(i % NS)), (i / NS) & 1, a.err);
         __syncwarp();
     } else if (warp == MG_W_MMA && rank == 1) {
-        // the even CTA's last commits have arrived here before this CTA may exit
-        volatile int ignore = 0;  // after an abort too
-        if (lane == 0) tc_wait_cluster(bar(B_FIN), 0, a.err, &ignore);
-        __syncwarp();
+        // the even CTA issues for both
     } else if (warp == MG_W_MMA) {
         // -------------------------------------------------------------- MMA
         uint32_t ut = 0, phase = 0;
@@ -745,6 +742,14 @@ __global__ void __launch_bounds__(MP_THREADS, 1)
 
     tc_fence_before();
     __syncthreads();
+    // The even CTA's last commits have arrived here before this CTA may exit.  The
+    // last tile has been read, so they are on their way: a short wait after a call of any
+    // length.
+    if (rank == 1 && warp == MG_W_MMA) {
+        volatile int ignore = 0;  // after an abort too
+        if (lane == 0) tc_wait_cluster(bar(B_FIN), 0, a.err, &ignore);
+        __syncwarp();
+    }
     cluster_sync();  // neither CTA leaves, or frees TMEM, while the other's work may reach it
     if (warp == MG_W_MMA) {
         tc_fence_after();
