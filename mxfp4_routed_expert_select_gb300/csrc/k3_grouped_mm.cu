@@ -546,9 +546,11 @@ K3_DEV void gp_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
                  "l"((uint64_t)map), "r"(adst), "l"((uint64_t)amap), "r"(x), "r"(row), "r"(e), "r"(ak), "r"(art), "r"(bar)
                  : "memory");
 }
-// The waits are of the CTA's scope too, those for the other CTA's arrivals among them: what
-// they hand over is tensor memory and staged tiles, which only the tensor core and copies
-// touch.  (An acquire at cluster scope makes a warp wait for its own stores.)
+// What the CTAs' threads have staged is acquired from both (pair_acquire).  The waits for
+// the other CTA's commits and for read accumulators are of the CTA's scope: behind them lie
+// MMAs that have completed and tensor memory, ordered by the tcgen05 fences, and no memory
+// that a thread has written.  (An acquire at cluster scope makes a warp wait for its own
+// stores; with the fence behind every EMPTY wait 443 us in group order became 462.)
 
 // Tile u into the ring, by a whole warp.
 K3_DEV void gp_plan(GpTile &t, const GmTable &tab, const GmArgs &a, int u)
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                         make_uint4(word(now[0]), word(now[1]), word(now[2]), word(now[3]));
                     fence_async_smem();
                     __syncwarp();
-                    if (lane == 0) pair_arrive(addr_of_rank(bar(B_FULL + s), 0));
+                    if (lane == 0) pair_arrive(bar(B_FULL + s), addr_of_rank(bar(B_FULL + s), 0), rank);
                     if (++s == NS) s = 0, phase ^= 1u;
                 }
             }
@@ -763,7 +765,7 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
                 fence_async_smem();
             }
             __syncwarp();
-            if (lane == 0) pair_arrive(full0);
+            if (lane == 0) pair_arrive(bar(B_FULL + s), full0, rank);
         }
         // drain: the last turn's copies of both CTAs have landed before the even CTA
         // exits; the odd one waits in the closing cluster barrier
@@ -793,15 +795,16 @@ __global__ void __launch_bounds__(GP_THREADS, 1)
             }
             tc_fence_after();
             for (int ks = 0; ks < a.nks; ks++, it++) {
-                if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                if (!ready && !__all_sync(0xffffffffu, tc_wait_pair(bar(B_FULL + s), phase, a.err, abort_flag))) {
                     ok = false;
                     break;
                 }
+                pair_acquire();
                 tc_fence_after();
                 const int sn = s + 1 == NS ? 0 : s + 1;
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // look at the next stage while this one is issued
-                ready = __all_sync(0xffffffffu, mbar_test(bar(B_FULL + sn), pn));
+                ready = __all_sync(0xffffffffu, mbar_test_pair(bar(B_FULL + sn), pn));
                 // The products that read this slot of scales before have completed: the
                 // next stage could only be filled behind them.  Where it is not yet, wait.
                 if (!ready && it >= (uint32_t)GP_SLOTS &&

@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 fence_async_smem();
                 __syncwarp();
             }
-            if (lane == 0) pair_arrive(full0);
+            if (lane == 0) pair_arrive(bar(B_FULL + s), full0, rank);
         }
         // drain: the last turn's copies of both CTAs have landed before the even CTA
         // exits; the odd one waits in the closing cluster barrier
@@ -287,6 +287,9 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
         int s = 0;
         bool ok = true, ready = false;
         const uint32_t lo = mn_lo(sbase);
+        auto full = [&](uint32_t b, uint32_t parity) {
+            return CTAS == 2 ? tc_wait_pair(b, parity, a.err, abort_flag) : tc_wait(b, parity, a.err, abort_flag);
+        };
         for (int u = first; u < n_tiles && ok; u += step) {
             const GwTile t = gw_tile(a, u, TILE);
             if (!t.rows) continue;
@@ -295,15 +298,16 @@ __global__ void __launch_bounds__(GW_THREADS, 1)
                 break;
             tc_fence_after();
             for (int r0 = 0; r0 < t.rows; r0 += GW_K) {
-                if (!ready && !__all_sync(0xffffffffu, tc_wait(bar(B_FULL + s), phase, a.err, abort_flag))) {
+                if (!ready && !__all_sync(0xffffffffu, full(bar(B_FULL + s), phase))) {
                     ok = false;
                     break;
                 }
+                if constexpr (CTAS == 2) pair_acquire();
                 tc_fence_after();
                 const int sn = s + 1 == a.ns ? 0 : s + 1;
                 const uint32_t pn = sn ? phase : phase ^ 1u;
                 // ask for the next stage before this one is issued, look at the answer after
-                const bool next = mbar_test(bar(B_FULL + sn), pn);
+                const bool next = CTAS == 2 ? mbar_test_pair(bar(B_FULL + sn), pn) : mbar_test(bar(B_FULL + sn), pn);
                 const uint32_t d = lo + (uint32_t)(s * (GW_STAGE / 16));
                 gw_step<CTAS>(tmem + (uint32_t)(buf * TILE), d, d + GW_OFF_Y / 16, r0 ? 1u : 0u, (t.rows - r0 + 15) / 16);
                 commit(bar(B_EMPTY + s));

@@ -71,16 +71,51 @@ K3_DEV void pair_load_2d(uint32_t dst, const CUtensorMap *map, int x, int row, u
                  "l"((uint64_t)map), "r"(x), "r"(row), "r"(bar)
                  : "memory");
 }
-// Arrival at the even CTA's barrier behind what this thread (and, after a warp barrier,
-// its warp) has written to its own CTA's shared memory.  Those bytes never leave that
-// shared memory: the tensor core beside it reads them, behind the proxy fence that each
-// writer has passed.  So no wider fence than the CTA's own goes with the arrival; one at
-// cluster scope takes 1000 clocks or more, and with it in each stage's path 65536 rows x
-// 1536 x 7168 took 648 us instead of 520.
-K3_DEV void pair_arrive(uint32_t bar)
+// Arrival at a pair's barrier in the even CTA (bar: there; full0: its shared::cluster
+// address) behind what this thread, and after a warp barrier its warp, has written to its
+// own CTA's shared memory and shown to the tensor core by the proxy fence.  The thread that
+// issues the MMAs is in the even CTA, so the odd one's release has cluster scope; its fence
+// covers the CTA's shared memory alone, which is all that is handed over (65536 rows x 1536
+// x 7168 with 64 experts, gathered and in group order: 540 and 443 us; 532 and 443 with the
+// CTA's scope, which gives no order between two CTAs; 1150 and 1025 with the arrive's own
+// release at cluster scope, which waits for all memory).
+K3_DEV void pair_arrive(uint32_t bar, uint32_t full0, int rank)
 {
-    asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+    if (rank)
+        asm volatile("fence.release.sync_restrict::shared::cta.cluster;\n\t"
+                     "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(full0)
+                     : "memory");
+    else
+        mbar_arrive(bar);
 }
+// The other side: a relaxed wait or test of the even CTA's barrier, then the acquire of what
+// both CTAs' shared memory holds.
+K3_DEV uint32_t mbar_try_wait_pair(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.try_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity), "r"(20000u)
+                 : "memory");
+    return ok;
+}
+K3_DEV bool mbar_test_pair(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.relaxed.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
+K3_DEV bool tc_wait_pair(uint32_t bar, uint32_t parity, int *err, volatile int *abort_flag)
+{
+    return tc_wait_tile<mbar_try_wait_pair>(bar, parity, 0, err, abort_flag);
+}
+K3_DEV void pair_acquire() { asm volatile("fence.acquire.sync_restrict::shared::cluster.cluster;" ::: "memory"); }
 // Arrival at the barrier of the same offset in the pair's CTA `rank`, for a
 // hand-over of tensor memory alone: the accumulator's loads are ordered by their
 // wait and the tcgen05 fence before this, and no ordinary memory is handed over, so
