@@ -518,11 +518,11 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_backward
 }
 
 // dgain[c] (+)= the sum of its column over the parts.  A block takes 32 columns, its
-// warps a share of the parts each.
+// warps a share of the parts each; the shares are joined pair by pair.
 constexpr int NC_WARPS = 32;
 __global__ void __launch_bounds__(NC_WARPS * 32) k3_norm_columns(float *dgain, const float *parts, int n, int n_parts, int accumulate)
 {
-    __shared__ float sh[NC_WARPS][32];
+    __shared__ float sh[NC_WARPS][33];
     griddep_wait();
     griddep_launch_dependents();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = (int)blockIdx.x * 32 + lane;
@@ -532,11 +532,9 @@ __global__ void __launch_bounds__(NC_WARPS * 32) k3_norm_columns(float *dgain, c
         for (int p = w; p < n_parts; p += NC_WARPS) v += parts[(long)p * n + col];
     sh[w][lane] = v;
     __syncthreads();
-    if (w == 0 && col < n) {
-#pragma unroll
-        for (int i = 1; i < NC_WARPS; i++) v += sh[i][lane];
-        dgain[col] = accumulate ? dgain[col] + v : v;
-    }
+    const int mine = (int)blockIdx.x * 32 + w;  // the column that this warp joins
+    v = warp_sum(sh[lane][w]);
+    if (lane == 0 && mine < n) dgain[mine] = accumulate ? dgain[mine] + v : v;
 }
 
 // ------------------------------------------------------------- 8-bit rows
