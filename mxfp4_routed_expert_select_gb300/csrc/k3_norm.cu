@@ -113,6 +113,13 @@ K3_DEV float fine_rstd(float ss, float n, float inv_n, float eps)
     return fmaf(0.5f * s, fmaf(-fmaf(m, s, -t) - left * s, s, fmaf(-t, s, 1.f)), s);
 }
 
+// The sum of squares is exact enough unless it, or its mean with eps, left the normal range,
+// or fell below where eps outweighs what it lost.
+K3_DEV bool sum_out_of_range(float ss, float eps)
+{
+    return !(ss < 1e37f && eps < 1e37f) || (ss < 1e-30f && eps < 1e-12f);
+}
+
 // 1 / sqrt(mean v^2 + eps) where the sum of squares left fp32's range or its normal
 // numbers while its root need not: the values scaled by a power of two.
 // each(f) calls f with this thread's values.
@@ -269,10 +276,8 @@ __global__ void __launch_bounds__(NORM_THREADS, C <= 2 && sizeof(T) == 2 ? 2 : 1
         }
         load(t + step);
         ss = team.sum(ss);
-        // the sum is exact enough unless it left the normal range, or fell below
-        // where eps outweighs what it lost
         float s = fine_rstd(ss, (float)a.n, a.inv_n, a.eps);
-        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f)) 
+        if (sum_out_of_range(ss, a.eps))
             s = far_rstd(
                 team, [&](auto &&take) {
 #pragma unroll
@@ -415,7 +420,7 @@ __global__ void __launch_bounds__(LONG_THREADS, LONG_CTAS) k3_norm_long_forward(
         const bool stored = a.r != nullptr;
         ss = team.sum(ss);
         float s = fine_rstd(ss, (float)a.n, a.inv_n, a.eps);
-        if (!(ss < 1e37f) || (ss < 1e-30f && a.eps < 1e-12f))
+        if (sum_out_of_range(ss, a.eps))
             s = far_rstd(
                 team, [&](auto &&take) {
                     row(stored, [&](int, const Raw<T> &r) {
