@@ -668,9 +668,13 @@ class ExpertGroups:
             raise ValueError("expected 1 to %d tokens, got %d" % (self.max_tokens, T))
         p = _flat(ids, self._i32, T, self.k)
         self.struct.tokens = T
-        st = (_lib or lib()).k3moe_groups_plan(self.ref, p, _stream(stream))
+        st = None
+        try:
+            st = (_lib or lib()).k3moe_groups_plan(self.ref, p, _stream(stream))
+        finally:
+            if st != K3MOE_OK:
+                self.struct.tokens = self.tokens
         if st:
-            self.struct.tokens = self.tokens
             check(st, "k3moe_groups_plan")
         self.tokens, self.slots = T, T * self.k
 
