@@ -4,7 +4,9 @@ r = x + delta; u = norm(r); the router's choice of u; every expert's SwiGLU over
 tokens with MXFP4 matrices and 8-bit rows; the weighted sum of each token's experts.
 Backward: the same matrices transposed for the input gradients (8-bit rows again),
 bf16 rows for the weight gradients, the balance loss and the combine weights for the
-router, the norm for the stream.  All experts in one call each.
+router, the norm for the stream.  The products, weight gradients and combines are one
+call each for all experts; the weights' operands are made anew in every step, a call for
+each expert's matrix.
 
     python examples/train_moe.py [--steps N]
 """

@@ -693,6 +693,9 @@ int k3moe_mx_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx_operand
  * C [M][N] = A B^T for operands A (M rows) and B (N rows) with the same `in`,
  * on the block-scaled tensor cores, fp32 accumulation, rounded once to c_dtype.
  * Any M >= 1: a single token's projection is M = 1 with the weights as B.
+ * The products of codes are exact, but the tensor cores' additions keep fewer bits than an
+ * fp32 addition: each step of 64 columns loses up to 2^-22 of the sum of the magnitudes
+ * (the bound that the tests hold them to; an fp32 addition loses 2^-24).
  *  C           c_dtype K3MOE_F32 or K3MOE_BF16, aligned to its element size, row
  *              stride ldc >= N elements; must not overlap the operands
  *  accumulate  != 0 adds into C (K3MOE_F32 only), e.g. for weight gradients
@@ -753,6 +756,8 @@ int k3moe_mx8_dequantize(void *y, int y_dtype, int64_t ld, const k3moe_mx8_rows 
  *   dx = dr + s (g - xhat mean(g xhat)),   dgain = sum over rows of dy xhat
  * dx is the gradient of x and of delta.  fp32 arithmetic; a mean of squares beyond
  * fp32 (values above 10^19) or below its normal numbers is formed in a scaled range.
+ * s itself is an fp32 number: infinite where the root is below 2^-128 (eps 0 and a row of
+ * subnormal values, or of zeros, whose y is then infinite or NaN).
  *  x, delta, r, y, dy, dr, dx  [T][n], all of one type (K3MOE_F32 or K3MOE_BF16) in a
  *              call, each with its own row stride >= n elements, aligned to the
  *              element size.  1 <= T <= 2^30, 1 <= n <= 32768
@@ -875,8 +880,9 @@ int k3moe_mx_experts_from_matrices(const k3moe_mx_experts *host_W, const uint8_t
 
 /*
  * C[i] = W_e a(i) for every place i of a plan, e the expert it belongs to: 8-bit rows
- * times MXFP4 matrices on the block-scaled tensor cores, fp32 accumulation, rounded
- * once to c_dtype.  One call for all experts, from a single token to whole batches;
+ * times MXFP4 matrices on the block-scaled tensor cores, fp32 accumulation (each step of
+ * 32 columns loses up to 2^-22 of the sum of the magnitudes), rounded once to c_dtype.
+ * One call for all experts, from a single token to whole batches;
  * with the transposed matrices and the 8-bit rows of dC it is the input gradient.
  *  A           the rows, `in` = W's.  gather != 0: a row per token, a(i) is that of the
  *              token of slot order[i] (A->rows >= tokens).  gather = 0: rows in group
@@ -912,7 +918,8 @@ int k3moe_grouped_matmul_form(int32_t E, int64_t slots, int32_t N, int32_t in, i
 
 /*
  * The gradients of the experts' matrices, dW_e = sum over e's places i of dY[i] x(i)^T,
- * from bf16 rows on the tensor cores, fp32 accumulation, rounded once to dw_dtype.  An
+ * from bf16 rows on the tensor cores, fp32 accumulation (products exact; each step of 16
+ * rows loses up to 2^-22 of the sum of the magnitudes), rounded once to dw_dtype.  An
  * expert without places gets zeros (nothing is added to it with accumulate).
  *  dY          bf16 [tokens * top_k][N] in group order, row stride lddy >= N
  *  X           bf16 [xrows][K], row stride ldx >= K.  gather != 0: a row per token
