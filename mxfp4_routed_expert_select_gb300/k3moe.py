@@ -285,8 +285,9 @@ def _first_stream():
     import torch
     handle = torch.cuda.current_stream().cuda_stream
     get, dev = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
-    if get is not None and dev is not None:
-        _raw_stream, _raw_device = get, dev
+    if get is None or dev is None:
+        get, dev = lambda device: torch.cuda.current_stream(device).cuda_stream, torch.cuda.current_device
+    _raw_stream, _raw_device = get, dev
     return handle
 
 
@@ -294,6 +295,21 @@ def _stream(s=None):
     if s is None:
         return _raw_stream(_raw_device()) if _raw_stream is not None else _first_stream()
     return s.cuda_stream if hasattr(s, "cuda_stream") else s
+
+
+def _stream_on(gpu, s=None):
+    """The stream of a call on GPU number `gpu`.  Kernels run on the current device, so it
+    has to be that one."""
+    if s is None and _raw_device is not None and _raw_device() == gpu:
+        return _raw_stream(gpu)
+    if _raw_device is None:
+        import torch
+        if s is not None and not torch.cuda.is_initialized():  # no tensor is on a GPU yet
+            return _stream(s)
+        _first_stream()
+    if _raw_device() != gpu:
+        raise ValueError("expected GPU %s to be the current device, which is GPU %d" % (gpu, _raw_device()))
+    return _stream(s)
 
 
 def matrix_bytes(rows, cols):
@@ -439,7 +455,7 @@ class MxOperand:
         if _gpu(packed) is None or scales.get_device() != packed.get_device():
             _elsewhere(_gpu(packed), packed, scales)
         op = cls(rows, in_, codes=packed)
-        check(lib().k3moe_mx_operand_from_matrix(op.ref, ctypes.byref(m), _stream(stream)),
+        check(lib().k3moe_mx_operand_from_matrix(op.ref, ctypes.byref(m), _stream_on(_gpu(packed), stream)),
               "k3moe_mx_operand_from_matrix")
         return op
 
@@ -452,7 +468,7 @@ def mx_quantize_operand(x, row=None, col=None, stream=None):
     if (row is not None and row.gpu != gpu) or (col is not None and col.gpu != gpu):
         _elsewhere(row.gpu if row is not None else col.gpu, x)
     st = (_lib or lib()).k3moe_mx_quantize_operand(row and row.ref, col and col.ref, x.data_ptr(), _dtype(x), rows,
-                                                   cols, _ld(x, rows, cols), _stream(stream))
+                                                   cols, _ld(x, rows, cols), _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_mx_quantize_operand")
 
@@ -462,7 +478,7 @@ def mx_dequantize(y, op, stream=None):
     if y.get_device() != op.gpu:
         _elsewhere(op.gpu, y)
     st = (_lib or lib()).k3moe_mx_dequantize(y.data_ptr(), _dtype(y), _ld(y, op.rows, op.in_), op.ref,
-                                             _stream(stream))
+                                             _stream_on(op.gpu, stream))
     if st:
         check(st, "k3moe_mx_dequantize")
 
@@ -472,7 +488,7 @@ def mx_matmul(C, A, B, accumulate=False, stream=None):
     if C.get_device() != A.gpu or B.gpu != A.gpu:
         _elsewhere(A.gpu, C, B.codes)
     st = (_lib or lib()).k3moe_mx_matmul(C.data_ptr(), _dtype(C), _ld(C, A.rows, B.rows), A.ref, B.ref,
-                                         1 if accumulate else 0, _stream(stream))
+                                         1 if accumulate else 0, _stream_on(A.gpu, stream))
     if st:
         check(st, "k3moe_mx_matmul")
 
@@ -509,7 +525,7 @@ def swiglu_forward(h, ckpt, g, u, stream=None):
     T, f = ckpt.T, ckpt.f
     st = (_lib or lib()).k3moe_swiglu_forward(h.data_ptr(), _ld(h, T, f), ckpt.ptr, ckpt.nbytes, g.data_ptr(),
                                               _ld(g, T, f), u.data_ptr(), _ld(u, T, f), _dtype(h, g, u), T, f,
-                                              _stream(stream))
+                                              _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_swiglu_forward")
 
@@ -522,7 +538,7 @@ def swiglu_backward(dg, du, dh, ckpt, stream=None):
     T, f = ckpt.T, ckpt.f
     st = (_lib or lib()).k3moe_swiglu_backward(dg.data_ptr(), _ld(dg, T, f), du.data_ptr(), _ld(du, T, f),
                                                dh.data_ptr(), _ld(dh, T, f), ckpt.ptr, ckpt.nbytes,
-                                               _dtype(dg, du, dh), T, f, _stream(stream))
+                                               _dtype(dg, du, dh), T, f, _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_swiglu_backward")
 
@@ -562,7 +578,7 @@ def mx8_quantize(rows8, x, stream=None):
     if x.get_device() != rows8.gpu:
         _elsewhere(rows8.gpu, x)
     st = (_lib or lib()).k3moe_mx8_quantize(rows8.ref, x.data_ptr(), _dtype(x), _ld(x, rows8.rows, rows8.in_),
-                                            _stream(stream))
+                                            _stream_on(rows8.gpu, stream))
     if st:
         check(st, "k3moe_mx8_quantize")
 
@@ -572,7 +588,7 @@ def mx8_dequantize(y, rows8, stream=None):
     if y.get_device() != rows8.gpu:
         _elsewhere(rows8.gpu, y)
     st = (_lib or lib()).k3moe_mx8_dequantize(y.data_ptr(), _dtype(y), _ld(y, rows8.rows, rows8.in_), rows8.ref,
-                                              _stream(stream))
+                                              _stream_on(rows8.gpu, stream))
     if st:
         check(st, "k3moe_mx8_dequantize")
 
@@ -606,7 +622,7 @@ class RmsNorm:
         st = (_lib or lib()).k3moe_norm_forward(NORM_FORWARD.pack(
             *_mat(y, T, n, dt), *_mat(r, T, n, dt), 0 if rstd is None else _flat(rstd, f32, T),
             0 if y8 is None else y8.addr, *_mat(x, T, n, dt), *_mat(delta, T, n, dt),
-            0 if gain is None else _flat(gain, f32, n), _dtype(x), T, n, self.eps), _stream(stream))
+            0 if gain is None else _flat(gain, f32, n), _dtype(x), T, n, self.eps), _stream_on(gpu, stream))
         if st:
             check(st, "k3moe_norm_forward")
 
@@ -623,7 +639,7 @@ class RmsNorm:
         st = (_lib or lib()).k3moe_norm_backward(NORM_BACKWARD.pack(
             *_mat(dx, T, n, dt), 0 if dgain is None else _flat(dgain, f32, n), *_mat(dy, T, n, dt), *_mat(dr, T, n, dt),
             *_mat(r, T, n, dt), _flat(rstd, f32, T), 0 if gain is None else _flat(gain, f32, n), *self._ws, _dtype(dy), T, n,
-            1 if accumulate else 0), _stream(stream))
+            1 if accumulate else 0), _stream_on(gpu, stream))
         if st:
             check(st, "k3moe_norm_backward")
 
@@ -670,7 +686,7 @@ class ExpertGroups:
         self.struct.tokens = T
         st = None
         try:
-            st = (_lib or lib()).k3moe_groups_plan(self.ref, p, _stream(stream))
+            st = (_lib or lib()).k3moe_groups_plan(self.ref, p, _stream_on(self.gpu, stream))
         finally:
             if st != K3MOE_OK:
                 self.struct.tokens = self.tokens
@@ -725,7 +741,7 @@ class MxExperts:
             _elsewhere(_gpu(packed), packed, scales)
         W = cls(E, rows, 2 * half, codes=packed)
         check(lib().k3moe_mx_experts_from_matrices(W.ref, scales.data_ptr(),
-                                                   scales.stride(0) if E > 1 else rows * half // 16, _stream(stream)),
+                                                   scales.stride(0) if E > 1 else rows * half // 16, _stream_on(W.gpu, stream)),
               "k3moe_mx_experts_from_matrices")
         return W
 
@@ -748,7 +764,7 @@ def grouped_matmul(C, A, W, groups, gather=False, accumulate=False, stream=None)
     dt = _dtype(C)
     st = (_lib or lib()).k3moe_grouped_matmul(GROUPED_MATMUL.pack(
         *_mat(C, groups.slots, W.rows, C.dtype), A.addr, W.addr, groups.addr, dt, 1 if gather else 0,
-        1 if accumulate else 0), _stream(stream))
+        1 if accumulate else 0), _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_grouped_matmul")
 
@@ -768,7 +784,7 @@ def grouped_wgrad(dW, dY, X, groups, gather=False, accumulate=False, stream=None
     xrows, bf16 = X.shape[0], X.dtype
     st = (_lib or lib()).k3moe_grouped_wgrad(GROUPED_WGRAD.pack(
         dW.data_ptr(), *_mat(dY, groups.slots, N, bf16), *_mat(X, xrows, K, bf16), groups.addr, _dtype(dW), xrows, N, K,
-        1 if gather else 0, 1 if accumulate else 0), _stream(stream))
+        1 if gather else 0, 1 if accumulate else 0), _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_grouped_wgrad")
 
@@ -782,7 +798,7 @@ def combine(out, y, groups, w=None, accumulate=False, stream=None):
     n, dt, T = out.shape[1], out.dtype, groups.tokens
     st = (_lib or lib()).k3moe_combine(COMBINE.pack(
         *_mat(out, T, n, dt), *_mat(y, groups.slots, n, dt), 0 if w is None else _flat(w, groups._f32, T, groups.k),
-        groups.addr, _dtype(out), n, 1 if accumulate else 0), _stream(stream))
+        groups.addr, _dtype(out), n, 1 if accumulate else 0), _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_combine")
 
@@ -799,7 +815,7 @@ def combine_backward(dy, dw, dout, y, groups, w=None, stream=None):
     st = (_lib or lib()).k3moe_combine_backward(COMBINE_BACKWARD.pack(
         *_mat(dy, groups.slots, n, dt), 0 if dw is None else _flat(dw, f32, T, k), *_mat(dout, T, n, dt),
         *_mat(y, groups.slots, n, dt), 0 if w is None else _flat(w, f32, T, k), groups.addr, _dtype(dout), n),
-        _stream(stream))
+        _stream_on(gpu, stream))
     if st:
         check(st, "k3moe_combine_backward")
 
@@ -840,7 +856,7 @@ class BalanceLoss:
         st = (_lib or lib()).k3moe_balance_forward(
             _flat(loss, self._f32, 1), _flat(counts, i32, E), _flat(n_valid, i32, 1), logits.data_ptr(),
             _dtype(logits), _ld(logits, T, E), _flat(ids, i32, T, k), self._mask(mask, T), T, E, k, self.alpha,
-            self.rule, *self._ws, _stream(stream))
+            self.rule, *self._ws, _stream_on(gpu, stream))
         if st:
             check(st, "k3moe_balance_forward")
 
@@ -858,7 +874,7 @@ class BalanceLoss:
             dlogits.data_ptr(), _ld(dlogits, T, E), logits.data_ptr(), _dtype(logits, dlogits), _ld(logits, T, E),
             _flat(ids, i32, T, k), self._mask(mask, T), _flat(counts, i32, E), _flat(n_valid, i32, 1),
             _flat(dloss, f32, 1), _flat(w, f32, T, k), _flat(dw, f32, T, k), T, E, k, self.alpha, self.rule,
-            _stream(stream))
+            _stream_on(gpu, stream))
         if st:
             check(st, "k3moe_balance_backward")
 

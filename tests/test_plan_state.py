@@ -28,6 +28,7 @@ class Library:
 def test_a_plan_that_was_not_made(monkeypatch, result):
     g = k.ExpertGroups(3, 2, 8, device="cpu")
     g.gpu = -1  # as the CPU's tensors say
+    monkeypatch.setattr(k, "_raw_device", lambda: -1)
     monkeypatch.setattr(k, "_lib", Library(0))
     g.plan(torch.zeros(3, 2, dtype=torch.int32), stream=0)
     assert (g.tokens, g.slots, g.struct.tokens) == (3, 6, 3)
