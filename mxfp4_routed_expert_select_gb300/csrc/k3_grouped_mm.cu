@@ -22,8 +22,8 @@
 //
 // Bound: few rows stream the weights (1 token x 16 of 896 experts x 1536 x 7168, 94 MB, 21.2
 // us; 64 x 16 over 128 experts, 753 MB, 123, 6.1 TB/s), many the pairs' shared memory and
-// MMAs (65536 rows with 64 experts x 1536 x 7168 gathered 528 us, 2.7 PFLOP/s, in group
-// order 440).
+// MMAs (65536 rows with 64 experts x 1536 x 7168 gathered 533 us, 2.7 PFLOP/s, in group
+// order 451).
 //
 // Every wait is bounded (2 s); a timeout sets the device error word and the CTA
 // drains its copies and MMAs, frees TMEM and exits.
@@ -550,7 +550,7 @@ K3_DEV void gp_load_w(uint32_t dst, const CUtensorMap *map, int x, int row, int 
 // the other CTA's commits and for read accumulators are of the CTA's scope: behind them lie
 // MMAs that have completed and tensor memory, ordered by the tcgen05 fences, and no memory
 // that a thread has written.  (An acquire at cluster scope makes a warp wait for its own
-// stores; with the fence behind every EMPTY wait 443 us in group order became 462.)
+// stores; with the fence behind every EMPTY wait 443 us in group order were 462.)
 
 // Tile u into the ring, by a whole warp.
 K3_DEV void gp_plan(GpTile &t, const GmTable &tab, const GmArgs &a, int u)

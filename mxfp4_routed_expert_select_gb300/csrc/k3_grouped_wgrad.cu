@@ -23,7 +23,7 @@
 //
 // Bound: the stores of dW where groups are short (64 x 1536 x 7168 fp32 from 16384 rows, 2.8
 // GB, gathered 480 us, 5.9 TB/s), the MMAs beside the copies where they are long (16 x 2048
-// x 2048 from 131072 rows 600 us in group order, 1.8 PFLOP/s; gathered 622).
+// x 2048 from 131072 rows 604 us in group order, 1.8 PFLOP/s; gathered 650).
 //
 // Every wait is bounded (2 s, and 16 us a step where a whole tile is waited for); a
 // timeout sets the device error word and the CTA drains its copies and MMAs, frees TMEM

@@ -76,7 +76,7 @@ K3_DEV void pair_load_2d(uint32_t dst, const CUtensorMap *map, int x, int row, u
 // own CTA's shared memory and shown to the tensor core by the proxy fence.  The thread that
 // issues the MMAs is in the even CTA, so the odd one's release has cluster scope; its fence
 // covers the CTA's shared memory alone, which is all that is handed over (65536 rows x 1536
-// x 7168 with 64 experts, gathered and in group order: 540 and 443 us; 532 and 443 with the
+// x 7168 with 64 experts, gathered and in group order: 533 and 451 us; 528 and 448 with the
 // CTA's scope, which gives no order between two CTAs; 1150 and 1025 with the arrive's own
 // release at cluster scope, which waits for all memory).
 K3_DEV void pair_arrive(uint32_t bar, uint32_t full0, int rank)
